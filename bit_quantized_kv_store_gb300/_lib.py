@@ -35,6 +35,20 @@ class CacheDesc(ctypes.Structure):
                 ("signs", _P)]
 
 
+class RowsDesc(ctypes.Structure):
+    _fields_ = [("data", _P), ("dtype", _I32), ("heads", _I32), ("tok_stride", _I64), ("head_stride", _I64)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("weight", _P), ("dtype", _I32), ("eps", _F), ("offset", _F)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rot_dim", _I32), ("interleaved", _I32), ("num_axes", _I32), ("reserved", _I32), ("table", _P)]
+
+
+_ROWS, _NORM, _ROPE, _CACHE = (ctypes.POINTER(c) for c in (RowsDesc, NormDesc, RopeDesc, CacheDesc))
+
 # name -> (restype, argtypes); mirrors include/kvq.h
 SIGNATURES = {
     "kvq_version": (_I32, []),
@@ -64,6 +78,14 @@ SIGNATURES = {
     "kvq_noalloc_scratch_bytes": (_SZ, []),
     "kvq_decode_noalloc": (_I32, [ctypes.POINTER(CacheDesc), _P, _I32, _I32, _P, _P, _I32, _I32, _P, _I32, _F, _I32,
                                   _P, _P, _P]),
+    "kvq_rope_table": (_I32, [_P, _P, _I32, _P]),
+    "kvq_norm_rope": (_I32, [_ROWS, _ROWS, _I64, _I32, _NORM, _ROPE, _P, _I64, _P, _P]),
+    "kvq_norm_rope_store": (_I32, [_CACHE, _ROWS, _ROWS, _ROWS, _I64, _NORM, _NORM, _ROPE, _P, _I64, _P, _ROWS, _I32,
+                                   _P, _P]),
+    "kvq_load": (_I32, [_CACHE, _P, _I64, _I32, _ROWS, _ROWS, _P, _P]),
+    "kvq_load_seqs": (_I32, [_CACHE, _P, _I32, _I32, _P, _P, _I64, _I32, _ROWS, _ROWS, _P, _P]),
+    "kvq_merge_diff": (_I32, [_CACHE, _P, _SZ, _I32, _I32, _P, _I32, _I32, _I32, _P, _I64, _NORM, _F, _P, _I32, _P]),
+    "kvq_diff_heads": (_I32, [_P, _I64, _I32, _I32, _P, _I64, _NORM, _F, _P, _I32, _P]),
 }
 
 _lib = None
@@ -378,6 +400,269 @@ def prefill_attn_fp8(cache: Cache, q, q_start, block_table, sm_scale, workspace=
                                       float(sm_scale), _ptr(workspace), workspace.numel(), _ptr(out),
                                       _stream(stream)), "kvq_prefill_attn_fp8")
     return out
+
+
+def _on_device(t, what, dtype=None, device=None):
+    """A tensor the calls below hand to the library by address: on the current
+    device (the kernels are launched there), of the type the call reads."""
+    if not t.is_cuda:
+        raise ValueError(f"kvq: expected a CUDA tensor, got one on {t.device}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"kvq: {what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"kvq: {what} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def _ints(t, what, shape):
+    """Address of contiguous int32 metadata of a given shape."""
+    _on_device(t, what, torch.int32)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"kvq: {what} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _status_ptr(t):
+    if t is None:
+        return None
+    _on_device(t, "status", torch.int32)
+    return t.data_ptr()
+
+
+def _rows(t, what, tokens=None, heads=None, width=None):
+    """kvq_rows of a tensor [tokens, heads, width] whose last dimension is contiguous."""
+    _on_device(t, what)
+    n, h, w = t.shape if t.dim() == 3 else (None, None, None)
+    if n is None or (tokens is not None and n != tokens) or (heads is not None and h != heads) or \
+            (width is not None and w != width):
+        raise ValueError(f"kvq: {what} must be [{'tokens' if tokens is None else tokens}, "
+                         f"{'heads' if heads is None else heads}, {'width' if width is None else width}], "
+                         f"got {tuple(t.shape)}")
+    ts, hs, es = t.stride()
+    if es != 1 and w > 1:
+        raise ValueError(f"kvq: the last dimension of {what} must be contiguous")
+    return RowsDesc(t.data_ptr(), _dtype_code(t), h, ts, hs)
+
+
+def _new(shape, dtype, like, stream):
+    """An output tensor that belongs to the stream it is written on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+class Norm:
+    """Root-mean-square norm of a head's row: x / sqrt(mean(x^2) + eps) * (weight +
+    offset).  weight: [width] fp32 or bf16 on the device (kept, not copied)."""
+
+    def __init__(self, weight, eps=1e-6, offset=0.0):
+        self.weight, self.eps, self.offset, self.width = weight, eps, offset, weight.numel()
+        self.desc = NormDesc(_ptr(weight), _dtype_code(weight), eps, offset)
+        self.ref = ctypes.byref(self.desc)
+
+
+class Rope:
+    """Rotary positions of the first 2 * len(inv_freq) elements of a row: pair i is
+    turned by position * inv_freq[i] radians.  inv_freq: floats (theta ** (-2 i /
+    rot_dim), or a model's scaled ones).  axes: the position axis of every pair
+    (default 0: one axis).  interleaved: pairs (2i, 2i + 1) instead of
+    (i, i + rot_dim / 2)."""
+
+    def __init__(self, inv_freq, axes=None, interleaved=False, device="cuda"):
+        n = len(inv_freq)
+        if axes is not None and len(axes) != n:
+            raise ValueError("kvq: one axis for every pair")
+        words = (ctypes.c_uint64 * max(n, 1))()
+        _check(lib().kvq_rope_table((ctypes.c_double * max(n, 1))(*inv_freq),
+                                    None if axes is None else (_I32 * max(n, 1))(*axes), n, words), "kvq_rope_table")
+        self.num_axes = 1 if axes is None else max(axes) + 1
+        self.rot_dim, self.interleaved = 2 * n, bool(interleaved)
+        signed = [w - (1 << 64) if w >= 1 << 63 else w for w in words]
+        self.table = torch.tensor(signed, dtype=torch.int64).to(device)
+        self.desc = RopeDesc(2 * n, int(self.interleaved), self.num_axes, 0, _ptr(self.table))
+        self.ref = ctypes.byref(self.desc)
+
+
+def _norm_ref(norm, what, width):
+    if norm is None:
+        return None
+    if norm.width != width:
+        raise ValueError(f"kvq: {what} is for rows of {norm.width}, not {width}")
+    _on_device(norm.weight, what)
+    return norm.ref
+
+
+def _rope_args(rope, positions, n):
+    """(kvq_rope, positions, axis stride) of a call over n tokens; positions int32
+    [n] (one axis) or [axes, n]."""
+    if rope is None:
+        return None, None, 0
+    if positions is None:
+        raise ValueError("kvq: rotary positions need positions")
+    _on_device(positions, "positions", torch.int32)
+    _on_device(rope.table, "the rope's table")
+    shape = tuple(positions.shape)
+    if not (shape == (rope.num_axes, n) or (rope.num_axes == 1 and shape == (n,))):
+        raise ValueError(f"kvq: positions must be [{rope.num_axes}, {n}], got {shape}")
+    st = positions.stride()
+    if n > 1 and st[-1] != 1:
+        raise ValueError("kvq: positions of an axis must be contiguous")
+    return rope.ref, positions.data_ptr(), (st[0] if rope.num_axes > 1 else n)
+
+
+def norm_rope(x, positions=None, rope=None, norm=None, out=None, dtype=None, status=None, stream=None):
+    """Norm and rotary positions of rows x [tokens, heads, width] (any strides with a
+    contiguous last dimension) in one pass; returns out (default: a new tensor of
+    `dtype`, x's own if None).  out may be x."""
+    n, heads, width = x.shape
+    if out is None:
+        out = _new((n, heads, width), dtype or x.dtype, x, stream)
+    rx, ry = _rows(x, "x"), _rows(out, "out", n, heads, width)
+    ref, pos, ps = _rope_args(rope, positions, n)
+    _check(lib().kvq_norm_rope(rx, ry, n, width, _norm_ref(norm, "norm", width), ref, pos, ps, _status_ptr(status),
+                               _stream(stream)), "kvq_norm_rope")
+    return out
+
+
+def norm_rope_store(cache: Cache, q, k, v, slot_mapping, positions=None, rope=None, q_norm=None, k_norm=None,
+                    q_out=None, rotate=True, status=None, stream=None):
+    """One launch from a layer's projections to the cache: the queries q [tokens, Hq,
+    D] normed, position-rotated and (rotate) turned into the cache's space, the
+    keys normed, position-rotated and stored, the values stored.  Returns q_out
+    (default: a new fp32 tensor) for decode_attn, or with rotate=False for the
+    calls that take unrotated queries.  q None: keys and values only."""
+    n = k.shape[0]
+    rk, rv = _rows(k, "k", None, cache.Hk, cache.D), _rows(v, "v", n, cache.Hk, cache.D)
+    rq = ro = None
+    if q is not None:
+        rq = _rows(q, "q", n, None, cache.D)
+        if q_out is None:
+            q_out = _new(tuple(q.shape), torch.float32, q, stream)
+        ro = _rows(q_out, "q_out", n, q.shape[1], cache.D)
+    elif q_out is not None:
+        raise ValueError("kvq: q_out without q")
+    ref, pos, ps = _rope_args(rope, positions, n)
+    _check(lib().kvq_norm_rope_store(cache.ref, rq, rk, rv, n, _norm_ref(q_norm, "q_norm", cache.D),
+                                     _norm_ref(k_norm, "k_norm", cache.D), ref, pos, ps,
+                                     _ints(slot_mapping, "slot_mapping", (n,)), ro, int(rotate), _status_ptr(status),
+                                     _stream(stream)), "kvq_norm_rope_store")
+    return q_out
+
+
+def _load_outputs(cache, n, k, v, dtype, like, stream):
+    """The outputs of a load and their kvq_rows: new ones where both are None."""
+    fp8 = cache.fmt == FMT_FP8_ROW
+    width = cache.D + cache.rope if fp8 else cache.D
+    if k is None and v is None:
+        k = _new((n, cache.Hk, width), dtype, like, stream)
+        v = None if fp8 else _new((n, cache.Hk, width), dtype, like, stream)
+    return (k, v, None if k is None else _rows(k, "k", n, cache.Hk, width),
+            None if v is None else _rows(v, "v", n, cache.Hk, width))
+
+
+def _rotates(cache, rotate_back):
+    return int(cache.fmt in (FMT_Q4_HAD32, FMT_TQ4) if rotate_back is None else rotate_back)
+
+
+def load(cache: Cache, slots, k=None, v=None, dtype=torch.bfloat16, rotate_back=None, status=None, stream=None):
+    """The rows at slots (int32 [n]) as the values they stand for: (k, v), each [n,
+    Hk, D] (fp8: k [n, 1, 576], v None).  Given k and / or v are written instead of
+    new ones (one alone: only that plane); a negative slot leaves its rows as they were."""
+    n = slots.shape[0]
+    k, v, rk, rv = _load_outputs(cache, n, k, v, dtype, slots, stream)
+    _check(lib().kvq_load(cache.ref, _ints(slots, "slots", (n,)), n, _rotates(cache, rotate_back), rk, rv,
+                          _status_ptr(status), _stream(stream)), "kvq_load")
+    return k, v
+
+
+def load_seqs(cache: Cache, block_tables, cu_lens, n_tok, starts=None, k=None, v=None, dtype=torch.bfloat16,
+              rotate_back=None, status=None, stream=None):
+    """Runs of positions of several sequences, packed: output rows cu_lens[b] ..
+    cu_lens[b + 1] - 1 are positions starts[b] (default 0) onwards of the sequence
+    whose pages block_tables[b] lists.  n_tok: rows of the outputs; those past
+    cu_lens[-1] are left as they were.  Outputs as for load()."""
+    B = cu_lens.shape[0] - 1
+    k, v, rk, rv = _load_outputs(cache, n_tok, k, v, dtype, cu_lens, stream)
+    _check(lib().kvq_load_seqs(cache.ref, _ints(block_tables, "block_tables", (B, block_tables.shape[-1])),
+                               block_tables.shape[-1], B, None if starts is None else _ints(starts, "starts", (B,)),
+                               _ints(cu_lens, "cu_lens", (B + 1,)), n_tok, _rotates(cache, rotate_back), rk, rv,
+                               _status_ptr(status), _stream(stream)), "kvq_load_seqs")
+    return k, v
+
+
+def _lambda(lam, rows, heads):
+    """Address and row stride of lambda: fp32 [heads] (one set) or [rows, heads]."""
+    _on_device(lam, "lam", torch.float32)
+    if tuple(lam.shape) not in ((heads,), (rows, heads)) or (heads > 1 and lam.stride(-1) != 1):
+        raise ValueError(f"kvq: lam must be [{heads}] or [{rows}, {heads}] with contiguous rows, got {tuple(lam.shape)}")
+    return lam.data_ptr(), (lam.stride(0) if lam.dim() == 2 else 0)
+
+
+def _diff_out(out, rows, heads, width, dtype, like, stream):
+    if out is None:
+        return _new((rows, heads, width), dtype, like, stream)
+    _on_device(out, "out")
+    if tuple(out.shape) != (rows, heads, width) or not out.is_contiguous():
+        raise ValueError(f"kvq: out must be contiguous [{rows}, {heads}, {width}], got {tuple(out.shape)}")
+    return out
+
+
+def merge_diff(cache: Cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq_len, lam, norm=None, out_scale=1.0,
+               out=None, dtype=torch.float32, n_sel=0, rotate_back=None, stream=None):
+    """merge() for differential attention: output head h is query head 2h's merged
+    output minus lam[.., h] times head 2h + 1's, rotated back, normed (norm) and
+    scaled.  lam: fp32 [num_q_heads / 2] or [num_seqs, num_q_heads / 2].  Returns
+    out [num_seqs, num_q_heads / 2, D]."""
+    out = _diff_out(out, num_seqs, num_q_heads // 2, cache.D, dtype, seq_lens, stream)
+    lp, ls = _lambda(lam, num_seqs, num_q_heads // 2)
+    _check(lib().kvq_merge_diff(cache.ref, _ptr(workspace), workspace.numel(), num_seqs, num_q_heads,
+                                _ints(seq_lens, "seq_lens", (num_seqs,)), max_seq_len, n_sel,
+                                _rotates(cache, rotate_back), lp, ls, _norm_ref(norm, "norm", cache.D),
+                                float(out_scale), out.data_ptr(), _dtype_code(out), _stream(stream)), "kvq_merge_diff")
+    return out
+
+
+def diff_heads(x, lam, norm=None, out_scale=1.0, out=None, dtype=torch.float32, stream=None):
+    """The same difference of heads already merged: x fp32 [rows, Hq, width]
+    (prefill_attn's output) to [rows, Hq / 2, width]."""
+    rows, Hq, width = x.shape
+    _on_device(x, "x", torch.float32)
+    out = _diff_out(out, rows, Hq // 2, width, dtype, x, stream)
+    lp, ls = _lambda(lam, rows, Hq // 2)
+    _check(lib().kvq_diff_heads(_ptr(x), rows, Hq, width, lp, ls, _norm_ref(norm, "norm", width), float(out_scale),
+                                out.data_ptr(), _dtype_code(out), _stream(stream)), "kvq_diff_heads")
+    return out
+
+
+def decode_diff(cache: Cache, q, seq_lens, block_tables, max_seq_len, sm_scale, workspace, lam, norm=None,
+                out_scale=1.0, out=None, dtype=torch.float32, sel=None, stream=None):
+    """One differential decode step: decode() of the Hq query heads with merge_diff();
+    returns [B, Hq / 2, D]."""
+    B, Hq = q.shape[0], q.shape[1]
+    if cache.fmt in (FMT_Q4_HAD32, FMT_Q4_0):
+        decode_attn_unrotated(cache, q, seq_lens, block_tables, max_seq_len, sm_scale, workspace, sel=sel,
+                              stream=stream)
+    else:
+        qq = q
+        if cache.fmt == FMT_TQ4:
+            qq = tq4_rotate(cache, q, out=_new(tuple(q.shape), torch.float32, q, stream), stream=stream)
+        elif q.dtype != torch.float32:
+            qq = _new(tuple(q.shape), torch.float32, q, stream)
+            with torch.cuda.stream(stream):
+                qq.copy_(q)
+        decode_attn(cache, qq, seq_lens, block_tables, max_seq_len, sm_scale, workspace, sel=sel, stream=stream)
+    return merge_diff(cache, workspace, B, Hq, seq_lens, max_seq_len, lam, norm=norm, out_scale=out_scale, out=out,
+                      dtype=dtype, n_sel=0 if sel is None else sel.shape[1], stream=stream)
+
+
+def prefill_diff(cache: Cache, q, q_start, block_table, sm_scale, lam, norm=None, out_scale=1.0, out=None,
+                 dtype=torch.float32, status=None, stream=None):
+    """Differential prefill of a prompt chunk: prefill_attn() of the Hq query heads,
+    then diff_heads(); returns [n, Hq / 2, D]."""
+    o = prefill_attn(cache, q, q_start, block_table, sm_scale, out=_new(tuple(q.shape), torch.float32, q, stream),
+                     status=status, stream=stream)
+    return diff_heads(o, lam, norm=norm, out_scale=out_scale, out=out, dtype=dtype, stream=stream)
 
 
 def selftest_wait_timeout(d_status, stream=None):

@@ -2,6 +2,7 @@
 // validation, workspace geometry and kernel launches.  Nothing here allocates.
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstdio>
 
 #include <mutex>
@@ -215,7 +216,7 @@ using namespace kvq;
 
 extern "C" {
 
-int32_t kvq_version(void) { return 100; }
+int32_t kvq_version(void) { return 200; }
 
 const char* kvq_status_string(int32_t s) {
   switch (s) {
@@ -612,6 +613,258 @@ int32_t kvq_read_status(const void* d_status, int32_t* host_code, void* stream) 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaMemcpyAsync(host_code, d_status, sizeof(int32_t), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+// ---------------------------------------------------------------- around the cache
+
+static bool dtype_ok(int32_t d) { return d == KVQ_DT_F32 || d == KVQ_DT_BF16; }
+
+// Checks of a strided activation tensor of `heads` heads of `width` values and its
+// view; `align`: the boundary its rows must start on for whole-vector access.
+static int32_t check_rows(const kvq_rows* r, int32_t heads, int32_t width, uint32_t align, RowsView* v) {
+  if (!r->data || !dtype_ok(r->dtype) || r->heads != heads) return KVQ_ERR_INVALID_ARG;
+  if (r->tok_stride < 0 || r->head_stride < 0) return KVQ_ERR_INVALID_ARG;
+  const uint64_t esz = r->dtype == KVQ_DT_F32 ? 4 : 2;
+  const uintptr_t base = reinterpret_cast<uintptr_t>(r->data);
+  if (base % esz != 0) return KVQ_ERR_INVALID_ARG;
+  // offsets are products in 64 bits
+  if (r->tok_stride > (int64_t(1) << 31) || r->head_stride > (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  const uint64_t off = base | static_cast<uint64_t>(r->tok_stride) * esz | static_cast<uint64_t>(r->head_stride) * esz |
+                       static_cast<uint64_t>(width) * esz;
+  *v = RowsView{r->data, r->tok_stride, r->head_stride, r->dtype, off % align == 0 ? 1 : 0};
+  return KVQ_OK;
+}
+
+// Rows that are written must not overlap each other.
+static bool rows_distinct(const kvq_rows* r, int64_t n_tok, int32_t width) {
+  const int64_t hs = r->heads > 1 ? r->head_stride : 0, ts = n_tok > 1 ? r->tok_stride : 0;
+  if ((r->heads > 1 && hs < width) || (n_tok > 1 && ts < width)) return false;
+  if (r->heads == 1 || n_tok == 1) return true;
+  // tokens outside heads, or heads outside tokens
+  return ts >= (r->heads - 1) * hs + width || hs >= (n_tok - 1) * ts + width;
+}
+
+static int32_t check_norm(const kvq_norm* n, NormView* v) {
+  *v = NormView{nullptr, 0, 0.f, 0.f};
+  if (!n) return KVQ_OK;
+  if (!n->weight || !dtype_ok(n->dtype) || !(n->eps > 0.f) || !(n->eps < INFINITY) || !(fabsf(n->offset) < INFINITY))
+    return KVQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(n->weight) % (n->dtype == KVQ_DT_F32 ? 4 : 2) != 0) return KVQ_ERR_INVALID_ARG;
+  *v = NormView{n->weight, n->dtype, n->eps, n->offset};
+  return KVQ_OK;
+}
+
+static int32_t check_rope(const kvq_rope* r, int32_t width, const int32_t* pos, int64_t pos_stride, int64_t n_tok,
+                          RopeView* v) {
+  *v = RopeView{nullptr, nullptr, 0, 0, 0, 0};
+  if (!r) return KVQ_OK;
+  if (r->interleaved != 0 && r->interleaved != 1) return KVQ_ERR_INVALID_ARG;
+  if (r->rot_dim < 2 || r->rot_dim % 2 != 0 || r->rot_dim > width || r->num_axes < 1 || r->num_axes > 4 ||
+      r->reserved != 0 || !r->table || reinterpret_cast<uintptr_t>(r->table) % 8 != 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (r->rot_dim > 256 || (!r->interleaved && r->rot_dim % (width / 16) != 0)) return KVQ_ERR_UNSUPPORTED;
+  if (!pos || reinterpret_cast<uintptr_t>(pos) % 4 != 0 || (r->num_axes > 1 && pos_stride < n_tok))
+    return KVQ_ERR_INVALID_ARG;
+  *v = RopeView{r->table, pos, pos_stride, r->rot_dim, r->interleaved, r->num_axes};
+  return KVQ_OK;
+}
+
+static bool norm_rope_width(int32_t w) { return w == 64 || w == 128 || w == 256 || w == 512; }
+
+constexpr int32_t kMaxHeads = 16384;  // (a grid dimension of the norm and rope kernel)
+
+int32_t kvq_rope_table(const double* inv_freq, const int32_t* axis, int32_t pairs, uint64_t* table) {
+  if (!inv_freq || !table || pairs < 1) return KVQ_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < pairs; ++i)
+    if (!(fabs(inv_freq[i]) < INFINITY) || (axis && (axis[i] < 0 || axis[i] > 3))) return KVQ_ERR_INVALID_ARG;
+  for (int32_t i = 0; i < pairs; ++i) {
+    const double t = fmod(fabs(inv_freq[i]) * 0.15915494309189534561, 1.0);  // turns: radians / (2 pi)
+    // units of 2^-62 of a turn, modulo a turn (the shift drops what is above it)
+    uint64_t q = static_cast<uint64_t>(rint(t * 4611686018427387904.0));
+    if (inv_freq[i] < 0) q = 0 - q;
+    table[i] = (q << 2) | static_cast<uint64_t>(axis ? axis[i] : 0);
+  }
+  return KVQ_OK;
+}
+
+int32_t kvq_norm_rope(const kvq_rows* x, const kvq_rows* y, int64_t n_tok, int32_t width, const kvq_norm* norm,
+                      const kvq_rope* rope, const int32_t* d_pos, int64_t pos_stride, int32_t* d_status,
+                      void* stream) {
+  if (n_tok < 0 || width <= 0) return KVQ_ERR_INVALID_ARG;
+  if (!norm_rope_width(width)) return KVQ_ERR_UNSUPPORTED;
+  if (n_tok == 0) return KVQ_OK;
+  if (!x || !y || x->heads < 1) return KVQ_ERR_INVALID_ARG;
+  if (x->heads > kMaxHeads || n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  NormRopeArgs a{};
+  int32_t st = check_rows(x, x->heads, width, 16, &a.q);
+  if (st == KVQ_OK) st = check_rows(y, x->heads, width, 16, &a.qo);
+  if (st == KVQ_OK) st = check_norm(norm, &a.qn);
+  if (st == KVQ_OK) st = check_rope(rope, width, d_pos, pos_stride, n_tok, &a.rope);
+  if (st != KVQ_OK) return st;
+  if (!rows_distinct(y, n_tok, width)) return KVQ_ERR_INVALID_ARG;
+  if (x->data == y->data &&
+      (x->dtype != y->dtype || x->tok_stride != y->tok_stride || x->head_stride != y->head_stride))
+    return KVQ_ERR_INVALID_ARG;
+  a.status = d_status;
+  a.n_tok = n_tok;
+  a.Hq = x->heads;
+  a.ps = make_fastdiv(1);
+  cudaError_t e = launch_norm_rope(a, width, -1, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq_rows* k, const kvq_rows* v,
+                            int64_t n_tok, const kvq_norm* q_norm, const kvq_norm* k_norm, const kvq_rope* rope,
+                            const int32_t* d_pos, int64_t pos_stride, const int32_t* d_slot_mapping,
+                            const kvq_rows* q_out, int32_t rotate, int32_t* d_status, void* stream) {
+  int32_t st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (n_tok < 0 || (rotate != 0 && rotate != 1) || !q != !q_out) return KVQ_ERR_INVALID_ARG;
+  const int D = cache->head_dim, Hk = cache->num_kv_heads;
+  if (cache->format == KVQ_FMT_FP8_ROW || !norm_rope_width(D)) return KVQ_ERR_UNSUPPORTED;
+  if (n_tok == 0) return KVQ_OK;
+  if (!k || !v || !d_slot_mapping || (q && q->heads < 1)) return KVQ_ERR_INVALID_ARG;
+  if ((q && q->heads > kMaxHeads) || Hk > kMaxHeads || n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  NormRopeArgs a{};
+  st = check_rows(k, Hk, D, 16, &a.k);
+  if (st == KVQ_OK) st = check_rows(v, Hk, D, 16, &a.v);
+  if (st == KVQ_OK) st = check_norm(k_norm, &a.kn);
+  if (st == KVQ_OK) st = check_rope(rope, D, d_pos, pos_stride, n_tok, &a.rope);
+  if (q) {
+    if (st == KVQ_OK) st = check_rows(q, q->heads, D, 16, &a.q);
+    if (st == KVQ_OK) st = check_rows(q_out, q->heads, D, 16, &a.qo);
+    if (st == KVQ_OK) st = check_norm(q_norm, &a.qn);
+    if (st != KVQ_OK) return st;
+    if (rotate && q_out->dtype != KVQ_DT_F32) return KVQ_ERR_INVALID_ARG;
+    if (!rows_distinct(q_out, n_tok, D)) return KVQ_ERR_INVALID_ARG;
+    if (q->data == q_out->data && (q->dtype != q_out->dtype || q->tok_stride != q_out->tok_stride ||
+                                   q->head_stride != q_out->head_stride))
+      return KVQ_ERR_INVALID_ARG;
+  }
+  if (st != KVQ_OK) return st;
+  a.c = *cache;
+  a.slots = d_slot_mapping;
+  a.status = d_status;
+  a.n_tok = n_tok;
+  a.Hq = q ? q->heads : 0;
+  a.Hk = Hk;
+  a.rotate = rotate;
+  a.ps = make_fastdiv(static_cast<uint32_t>(cache->page_size));
+  cudaError_t e = launch_norm_rope(a, D, cache->format, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+// The checks that both loads share, and their launch.
+static int32_t load_impl(const kvq_cache* cache, LoadArgs& a, int32_t rotate_back, const kvq_rows* k,
+                         const kvq_rows* v, void* stream) {
+  const bool fp8 = cache->format == KVQ_FMT_FP8_ROW;
+  const int width = fp8 ? cache->head_dim + cache->rope_dim : cache->head_dim;
+  if (rotate_back != 0 && rotate_back != 1) return KVQ_ERR_INVALID_ARG;
+  if (rotate_back && cache->format != KVQ_FMT_Q4_HAD32 && cache->format != KVQ_FMT_TQ4) return KVQ_ERR_INVALID_ARG;
+  if (a.n_tok < 0 || (fp8 && v) || (!k && !v)) return KVQ_ERR_INVALID_ARG;
+  if (a.n_tok == 0) return KVQ_OK;
+  if (a.n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  int32_t st = KVQ_OK;
+  if (k) {
+    st = check_rows(k, cache->num_kv_heads, width, 32, &a.k);
+    if (st == KVQ_OK && !rows_distinct(k, a.n_tok, width)) st = KVQ_ERR_INVALID_ARG;
+  }
+  if (st == KVQ_OK && v) {
+    st = check_rows(v, cache->num_kv_heads, width, 32, &a.v);
+    if (st == KVQ_OK && !rows_distinct(v, a.n_tok, width)) st = KVQ_ERR_INVALID_ARG;
+  }
+  if (st != KVQ_OK) return st;
+  a.c = *cache;
+  a.rotate_back = rotate_back;
+  a.ps = make_fastdiv(static_cast<uint32_t>(cache->page_size));
+  a.hk = make_fastdiv(static_cast<uint32_t>(cache->num_kv_heads));
+  cudaError_t e = launch_load(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+int32_t kvq_load(const kvq_cache* cache, const int32_t* d_slots, int64_t n_tok, int32_t rotate_back,
+                 const kvq_rows* k, const kvq_rows* v, int32_t* d_status, void* stream) {
+  int32_t st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (n_tok > 0 && !d_slots) return KVQ_ERR_INVALID_ARG;
+  LoadArgs a{};
+  a.slots = d_slots;
+  a.n_tok = n_tok;
+  a.status = d_status;
+  return load_impl(cache, a, rotate_back, k, v, stream);
+}
+
+int32_t kvq_load_seqs(const kvq_cache* cache, const int32_t* d_block_tables, int32_t max_pages, int32_t num_seqs,
+                      const int32_t* d_starts, const int32_t* d_cu_lens, int64_t n_tok, int32_t rotate_back,
+                      const kvq_rows* k, const kvq_rows* v, int32_t* d_status, void* stream) {
+  int32_t st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (num_seqs < 0) return KVQ_ERR_INVALID_ARG;
+  if (num_seqs > 0 && n_tok > 0 && (!d_block_tables || max_pages < 1 || !d_cu_lens)) return KVQ_ERR_INVALID_ARG;
+  LoadArgs a{};
+  a.block_tables = d_block_tables;
+  a.starts = d_starts;
+  a.cu_lens = d_cu_lens;
+  a.max_pages = max_pages;
+  a.num_seqs = num_seqs;
+  a.n_tok = num_seqs > 0 ? n_tok : (n_tok < 0 ? n_tok : 0);
+  a.status = d_status;
+  return load_impl(cache, a, rotate_back, k, v, stream);
+}
+
+// The checks of an output of differential heads, and its view.
+static int32_t check_diff(const float* d_lambda, int64_t lambda_stride, int64_t rows, int32_t heads,
+                          const kvq_norm* norm, float out_scale, void* out, int32_t out_dtype, DiffView* d) {
+  if (!d_lambda || reinterpret_cast<uintptr_t>(d_lambda) % 4 != 0 || !out || !dtype_ok(out_dtype) ||
+      !(fabsf(out_scale) < INFINITY))
+    return KVQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(out) % (out_dtype == KVQ_DT_F32 ? 4 : 2) != 0) return KVQ_ERR_INVALID_ARG;
+  if (lambda_stride < 0 || (lambda_stride > 0 && rows > 1 && lambda_stride < heads)) return KVQ_ERR_INVALID_ARG;
+  *d = DiffView{d_lambda, lambda_stride, {}, out_scale, out, out_dtype};
+  return check_norm(norm, &d->norm);
+}
+
+int32_t kvq_merge_diff(const kvq_cache* cache, const void* workspace, size_t ws_bytes, int32_t num_seqs,
+                       int32_t num_q_heads, const int32_t* d_seq_lens, int32_t max_seq_len, int32_t n_sel,
+                       int32_t rotate_back, const float* d_lambda, int64_t lambda_stride, const kvq_norm* norm,
+                       float out_scale, void* out, int32_t out_dtype, void* stream) {
+  int32_t st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (n_sel < 0 || n_sel > 4096) return KVQ_ERR_INVALID_ARG;
+  if (cache->format == KVQ_FMT_FP8_ROW) return KVQ_ERR_UNSUPPORTED;
+  st = check_decode_shape(cache, num_seqs, num_q_heads, d_seq_lens, max_seq_len, n_sel > 0, n_sel);
+  if (st != KVQ_OK) return st;
+  if (num_q_heads / cache->num_kv_heads % 2 != 0 || num_seqs > 65535 || num_q_heads / 2 > 65535)
+    return KVQ_ERR_UNSUPPORTED;
+  if (rotate_back && cache->format != KVQ_FMT_Q4_HAD32 && cache->format != KVQ_FMT_TQ4) return KVQ_ERR_INVALID_ARG;
+  if (num_seqs == 0) return KVQ_OK;
+  if (!workspace || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+  DiffView d;
+  st = check_diff(d_lambda, lambda_stride, num_seqs, num_q_heads / 2, norm, out_scale, out, out_dtype, &d);
+  if (st != KVQ_OK) return st;
+  const WsLayout w = ws_layout(cache, num_seqs, num_q_heads, max_seq_len, n_sel);
+  if (ws_bytes < w.total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  const uint8_t* ws = static_cast<const uint8_t*>(workspace);
+  // rotate_back: 1 the groups' rotation, 2 the TQ4 rows'
+  MergeArgs a{reinterpret_cast<const float*>(ws + w.m_off), reinterpret_cast<const float*>(ws + w.z_off),
+              reinterpret_cast<const float*>(ws + w.acc_off), w.P, num_q_heads, value_width(cache), d_seq_lens,
+              max_seq_len, n_sel, !rotate_back ? 0 : cache->format == KVQ_FMT_TQ4 ? 2 : 1, nullptr, w.part};
+  cudaError_t e = launch_merge_diff(a, d, *cache, num_seqs, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_t width, const float* d_lambda,
+                       int64_t lambda_stride, const kvq_norm* norm, float out_scale, void* out, int32_t out_dtype,
+                       void* stream) {
+  if (rows < 0 || num_q_heads < 2 || num_q_heads % 2 != 0 || width <= 0) return KVQ_ERR_INVALID_ARG;
+  if (!norm_rope_width(width)) return KVQ_ERR_UNSUPPORTED;
+  if (rows == 0) return KVQ_OK;
+  if (!x || reinterpret_cast<uintptr_t>(x) % 4 != 0) return KVQ_ERR_INVALID_ARG;
+  DiffView d;
+  int32_t st = check_diff(d_lambda, lambda_stride, rows, num_q_heads / 2, norm, out_scale, out, out_dtype, &d);
+  if (st != KVQ_OK) return st;
+  cudaError_t e = launch_diff_heads(x, rows, num_q_heads, width, d, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
 }
 

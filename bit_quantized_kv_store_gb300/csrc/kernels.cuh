@@ -108,6 +108,70 @@ struct PrefillArgs {
   int rotate;  // 1: Hadamard format (rotate q, rotate the output back); 0: Q4_0
 };
 
+// Strided activation rows (a kvq_rows as the kernels take it).
+struct RowsView {
+  void* data;
+  int64_t ts, hs;  // elements from a token, a head to the next
+  int dtype;
+  int wide;  // 1: every row starts on a 16-byte boundary, so lanes move whole vectors
+};
+
+// A kvq_norm; weight NULL: no norm.
+struct NormView {
+  const void* weight;
+  int dtype;
+  float eps, offset;
+};
+
+// A kvq_rope with its positions; rot 0: no rotation.
+struct RopeView {
+  const uint64_t* table;
+  const int32_t* pos;
+  int64_t pos_stride;
+  int rot, interleaved, axes;
+};
+
+// Norm and rotary positions, alone (Hk = 0) or on the way into the cache (norm_rope.cu).
+struct NormRopeArgs {
+  RowsView q, qo, k, v;
+  NormView qn, kn;
+  RopeView rope;
+  kvq_cache c;
+  const int32_t* slots;
+  int32_t* status;
+  int64_t n_tok;
+  int Hq, Hk;
+  int rotate;  // 1: queries into the cache's space
+  int hpw;     // heads a warp takes (set by the launch)
+  FastDiv ps;  // page_size
+};
+
+// Rows read back (load.cu).
+struct LoadArgs {
+  kvq_cache c;
+  RowsView k, v;         // data NULL: not wanted
+  const int32_t* slots;  // row t's slot; NULL: by block tables
+  const int32_t* block_tables;
+  const int32_t* starts;  // NULL: 0
+  const int32_t* cu_lens;
+  int max_pages, num_seqs;
+  int64_t t0, n_tok;  // output tokens [t0, n_tok)
+  int rotate_back;
+  int32_t* status;
+  FastDiv ps, hk;
+};
+
+// Differential heads (diff.cu): the difference of the two maps of an output head,
+// its norm and its scale.
+struct DiffView {
+  const float* lambda;
+  int64_t stride;
+  NormView norm;
+  float scale;
+  void* out;
+  int out_dtype;
+};
+
 // The host-side checks of kvq_decode_attn + kvq_merge on a workspace of ws_bytes
 // bytes (api.cu); enqueues nothing.
 int32_t check_decode_and_merge(const kvq_cache* cache, const float* q, int32_t num_seqs, int32_t num_q_heads,
@@ -165,5 +229,14 @@ cudaError_t launch_merge(const MergeArgs& a, int B, cudaStream_t s);
 // A barrier wait that nothing completes, bounded like every copy wait (api.cu).
 cudaError_t launch_wait_timeout_probe(int32_t* status, cudaStream_t s);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t s);
+// Norm and rotary positions of rows of `width`; fmt: the cache's format, or -1
+// for rows that are only normed and rotated (norm_rope.cu).
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int width, int fmt, cudaStream_t s);
+// Rows of the cache as the values they stand for (load.cu).
+cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);
+// The merge of two maps' partials with their difference (tq: TQ4 rows), and the
+// difference of merged heads (diff.cu).
+cudaError_t launch_merge_diff(const MergeArgs& a, const DiffView& d, const kvq_cache& c, int B, cudaStream_t s);
+cudaError_t launch_diff_heads(const float* x, int64_t rows, int Hq, int width, const DiffView& d, cudaStream_t s);
 
 }  // namespace kvq

@@ -17,16 +17,10 @@
 // spans the whole row, so their rotation back is a second launch, tq4.cu.)
 // The number of keys per partition comes with the arguments: 512, or for the
 // fp8 streaming prefill one partition per row, whose length is q_start + row + 1.
-#include "kernels.cuh"
+#include "merge_fold.cuh"
 
 namespace kvq {
 
-// kBatch: partitions a row-thread loads before using them (4; for a grid of few
-// CTAs over many partitions 8, or 17 past 256 partitions, so that a 262K-key
-// sequence's 513 take one round trip, still at two CTAs per SM: fewer round
-// trips, more registers; for a grid of many waves 2, at six CTAs per SM: more
-// CTAs resident, more round trips); the updates run in ascending partition
-// order either way, so the bits are the same.
 template <int kBatch>
 __global__ void __launch_bounds__(256, kBatch > 8 ? 2 : kBatch == 2 ? 6 : 1) merge_kernel(const MergeArgs a) {
   pdl_wait();
@@ -52,80 +46,9 @@ __global__ void __launch_bounds__(256, kBatch > 8 ? 2 : kBatch == 2 ? 6 : 1) mer
     return;
   }
   const int64_t base = ((int64_t)b * a.Hq + h) * a.P;
-  const float* m = a.ws_m + base;
-  const float* z = a.ws_z + base;
-  const int chunk = tid & 7, row = tid >> 3;
-  const float* accp = a.ws_acc + base * a.Dv + 32 * grp + 4 * chunk;
-
-  __shared__ float s_m[32], s_z[32];  // per row: its maximum, then its z rescaled to the CTA's
-  __shared__ float red_acc[32][33];
-  __shared__ int s_nan;
-  if (tid == 0) s_nan = 0;
-
-  // per-thread running partial over partitions row, row + 32, ...
-  float Mt = -INFINITY, Zt = 0.f;
-  float4 At = make_float4(0.f, 0.f, 0.f, 0.f);
-  int nan_seen = 0;
-  for (int i0 = row; i0 < np; i0 += kBatch * 32) {
-    float mv[kBatch], zv[kBatch];
-    float4 av[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {  // all loads of the batch first
-      const int i = i0 + 32 * k;
-      mv[k] = -INFINITY;
-      zv[k] = 0.f;
-      av[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < np) {
-        mv[k] = m[i];
-        if (chunk == 0) zv[k] = z[i];
-        av[k] = *reinterpret_cast<const float4*>(accp + (int64_t)i * a.Dv);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (i0 + 32 * k >= np) break;
-      nan_seen |= isnan(mv[k]);
-      const float Mn = fmaxf(Mt, mv[k]);
-      if (Mn == -INFINITY) continue;  // nothing attended so far
-      const float wo = exp2f(Mt - Mn), wn = exp2f(mv[k] - Mn);
-      Zt = fmaf(Zt, wo, zv[k] * wn);
-      At.x = fmaf(At.x, wo, av[k].x * wn);
-      At.y = fmaf(At.y, wo, av[k].y * wn);
-      At.z = fmaf(At.z, wo, av[k].z * wn);
-      At.w = fmaf(At.w, wo, av[k].w * wn);
-      Mt = Mn;
-    }
-  }
-  nan_seen = __any_sync(0xffffffffu, nan_seen);
-  __syncthreads();  // s_nan initialised
-  if (nan_seen && lane == 0) s_nan = 1;
-  if (chunk == 0) {
-    s_m[row] = Mt;
-    s_z[row] = Zt;
-  }
-  __syncthreads();
-  // M = max over the 32 rows; each row's partial rescaled to M
-  float M = s_m[0];
-#pragma unroll
-  for (int r = 1; r < 32; ++r) M = fmaxf(M, s_m[r]);
-  const bool empty = (M == -INFINITY);
-  const float wr = (empty || Mt == -INFINITY) ? 0.f : exp2f(Mt - M);
-  red_acc[row][4 * chunk + 0] = At.x * wr;
-  red_acc[row][4 * chunk + 1] = At.y * wr;
-  red_acc[row][4 * chunk + 2] = At.z * wr;
-  red_acc[row][4 * chunk + 3] = At.w * wr;
-  __syncthreads();  // every thread has read s_m
-  if (chunk == 0) s_z[row] = Zt * wr;
-  __syncthreads();
+  __shared__ FoldSmem sm;
+  float o = merge_fold<kBatch>(a.ws_m + base, a.ws_z + base, a.ws_acc + base * a.Dv + 32 * grp, a.Dv, np, tid, sm);
   if (tid < 32) {
-    float o = 0.f, Z = 0.f;
-#pragma unroll
-    for (int r = 0; r < 32; ++r) {  // ascending rows, a fixed order (unrolled: the loads go ahead of the adds)
-      o += red_acc[r][lane];
-      Z += s_z[r];
-    }
-    o = (empty || Z == 0.f) ? 0.f : o / Z;
-    if (s_nan) o = NAN;
     if (a.rotate_back) o = __fmul_rn(warp_fwht32(o, lane), kHadamardScale);
     outp[lane] = o;
   }

@@ -1,0 +1,115 @@
+// tq4_code.cuh -- the TQ4 rows' signed row transform and the codes and scale of one
+// transformed row across a warp, shared by the kernels that store such rows.  Lane
+// l holds elements E l .. E l + E - 1 (E = D / 32), so the butterfly's first
+// log2(E) stages run in registers and the other five across lanes, and the
+// pairwise tree of the sum of squares is the warp's xor reduction.  Every
+// floating-point operation is an explicit IEEE-rounded intrinsic.
+#pragma once
+#include "common.cuh"
+
+namespace kvq {
+
+// Lloyd-Max magnitudes for 16 levels of N(0,1), rounded to fp16 (exact values).
+__host__ __device__ constexpr float tq4_mag(int m) {
+  return m == 0 ? 0.12841796875f : m == 1 ? 0.387939453125f : m == 2 ? 0.65673828125f : m == 3 ? 0.9423828125f
+       : m == 4 ? 1.255859375f : m == 5 ? 1.6181640625f : m == 6 ? 2.068359375f : 2.732421875f;
+}
+// Midpoint between magnitudes m and m + 1 (exact: fp16 values summed in fp32).
+__host__ __device__ constexpr float tq4_mid(int m) { return (tq4_mag(m) + tq4_mag(m + 1)) * 0.5f; }
+
+template <int E>
+__host__ __device__ constexpr float tq4_row_scale() {  // fp32(1 / sqrt(32 E))
+  return E == 8 ? 0.0625f : E == 4 ? 0.0883883476483184405501f : 0.125f;
+}
+
+// In-place signed transform of the warp's row (forward: signs, butterfly, scale;
+// inverse: butterfly, scale, signs).  `sw` holds this lane's E sign bits.
+template <int E>
+__device__ __forceinline__ void tq4_transform(float (&y)[E], uint32_t sw, int lane, bool inverse) {
+  if (!inverse) {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if ((sw >> i) & 1u) y[i] = -y[i];
+  }
+#pragma unroll
+  for (int h = 1; h < E; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (!(i & h)) {
+        const float a = y[i], b = y[i + h];
+        y[i] = __fadd_rn(a, b);
+        y[i + h] = __fsub_rn(a, b);
+      }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float p = __shfl_xor_sync(0xffffffffu, y[i], o);
+      y[i] = (lane & o) ? __fsub_rn(p, y[i]) : __fadd_rn(y[i], p);
+    }
+#pragma unroll
+  for (int i = 0; i < E; ++i) y[i] = __fmul_rn(y[i], tq4_row_scale<E>());
+  if (inverse) {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if ((sw >> i) & 1u) y[i] = -y[i];
+  }
+}
+
+template <int E>
+__device__ __forceinline__ uint32_t lane_signs(const void* signs, int lane) {
+  const uint32_t w = static_cast<const uint32_t*>(signs)[(E * lane) >> 5];
+  return w >> ((E * lane) & 31);
+}
+
+// The codes (element i of the lane in nibble i) and the fp16 scale of the warp's
+// transformed row y.
+template <int E>
+__device__ __forceinline__ uint32_t tq4_row_codes(const float (&y)[E], __half& s16_out) {
+  constexpr int D = 32 * E;
+  // sum of squares by the pairwise tree: in-lane stages, then the xor reduction
+  float q2[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) q2[i] = __fmul_rn(y[i], y[i]);
+#pragma unroll
+  for (int h = 1; h < E; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < E; i += 2 * h) q2[i] = __fadd_rn(q2[i], q2[i + h]);
+  float ss = q2[0];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+  __half s16 = __float2half_rn(__fsqrt_rn(__fmul_rn(ss, 1.0f / D)));
+  if (__hisinf(s16)) s16 = __ushort_as_half(0x7BFFu);  // saturate to 65504
+  const float s = __half2float(s16);
+
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i) {
+    uint32_t code = 0;
+    if (s > 0.0f) {
+      const float q = __fdiv_rn(y[i], s);
+      const float a = fabsf(q);
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 7; ++j) m += a > tq4_mid(j) ? 1u : 0u;
+      code = (q < 0.0f ? 8u : 0u) | m;
+    }
+    word |= code << (4 * i);
+  }
+  s16_out = s16;
+  return word;
+}
+
+// Write the lane's E codes into its row of the codes plane.
+template <int E>
+__device__ __forceinline__ void tq4_write_codes(uint8_t* codes, uint32_t word) {
+  if constexpr (E == 8) {
+    *reinterpret_cast<uint32_t*>(codes) = word;
+  } else if constexpr (E == 4) {
+    *reinterpret_cast<uint16_t*>(codes) = static_cast<uint16_t>(word);
+  } else {
+    *codes = static_cast<uint8_t>(word);
+  }
+}
+
+}  // namespace kvq

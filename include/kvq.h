@@ -414,6 +414,146 @@ int32_t kvq_decode_noalloc(const kvq_cache* cache, const float* q, int32_t num_s
                            int32_t max_seq_len, const int32_t* d_sel, int32_t n_sel, float sm_scale,
                            int32_t rotate_back, float* out, int32_t* d_status_out, void* stream);
 
+/* ------------------------------------------------------------------ around the cache
+ * What a model does to its queries, keys and values just before the cache (norms
+ * per head, rotary positions), and the rows read back out of it.  The pages'
+ * producers do the first ([P3] KV8 base commit: the fresh normed and roped row is
+ * quantised) in kernels of their own; here they are one pass with the store. */
+
+/* Activations [tokens][heads][width], the last dimension contiguous, the other
+ * two with strides in elements: a slice of a fused projection, a head beside its
+ * gate, or a plain contiguous tensor. */
+typedef struct kvq_rows {
+  void* data;          /* device; read or written, as the call says */
+  int32_t dtype;       /* KVQ_DT_F32 or KVQ_DT_BF16 */
+  int32_t heads;
+  int64_t tok_stride;  /* elements from a token to the next */
+  int64_t head_stride; /* elements from a head to the next */
+} kvq_rows;
+
+/* Root-mean-square norm of each row:  y = x * r * (weight + offset),
+ * r = 1 / sqrt(mean(x^2) + eps), in fp32.  (offset 1: weights kept around zero.) */
+typedef struct kvq_norm {
+  const void* weight; /* device [width] */
+  int32_t dtype;      /* KVQ_DT_F32 or KVQ_DT_BF16 */
+  float eps;          /* finite, > 0 */
+  float offset;
+} kvq_norm;
+
+/* Rotary positions: pair i < rot_dim / 2 of a row is turned by
+ * 2 pi * pos[axis(i)] * turns(i).  Pairs are elements (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) when interleaved; elements past rot_dim stay as they are.
+ * Word i of the table holds the turns for one position step as a fraction of a
+ * turn in units of 2^-64 (its low two bits read as zero), and the axis in those
+ * two bits, so that the angle of any int32 position, also a negative one, is one
+ * 64-bit multiply that wraps exactly (kvq_rope_table makes the words). */
+typedef struct kvq_rope {
+  int32_t rot_dim;       /* even, 2 .. min(256, width); a multiple of width / 16 unless interleaved */
+  int32_t interleaved;   /* 0 or 1 */
+  int32_t num_axes;      /* 1 .. 4 (time, height, width, ...) */
+  int32_t reserved;      /* 0 */
+  const uint64_t* table; /* device [rot_dim / 2] */
+} kvq_rope;
+
+/* kvq_rope_table -- words of a kvq_rope's table (host memory) from the pairs'
+ * angles per position step, inv_freq [pairs] in radians (finite), and their axes
+ * (NULL: all 0; each 0 .. 3).  Turns are rounded to 2^-62 of a turn from the
+ * doubles given. */
+int32_t kvq_rope_table(const double* inv_freq, const int32_t* axis, int32_t pairs, uint64_t* table);
+
+/* kvq_norm_rope -- norm and rotary positions of `n_tok` tokens' rows in one pass
+ * (either may be NULL: not done).  x, y: [n_tok][heads][width] with equal heads;
+ * y may be x itself (same data, dtype and strides); other overlaps of x and y
+ * are not allowed.  width 64, 128, 256 or 512.  Arithmetic in fp32, rounded once
+ * into y's type.
+ *   d_pos: device int32 [num_axes][n_tok], axis a's at a * pos_stride (elements;
+ *       may be NULL without rope).
+ *   d_status: optional; a table word whose axis is >= num_axes turns its pair to
+ *       NaN and sets KVQ_DEV_BAD_INDEX. */
+int32_t kvq_norm_rope(const kvq_rows* x, const kvq_rows* y, int64_t n_tok, int32_t width, const kvq_norm* norm,
+                      const kvq_rope* rope, const int32_t* d_pos, int64_t pos_stride, int32_t* d_status,
+                      void* stream);
+
+/* kvq_norm_rope_store -- one launch from a layer's projections to the cache:
+ * queries: q_norm, rope, and the rotation into the cache's space (rotate != 0;
+ * as kvq_rotate_query or kvq_tq4_rotate; formats without a rotation: none) into
+ * q_out; keys: k_norm, rope, stored; values: stored.  Same bytes in the cache
+ * and the same q_out as kvq_norm_rope into fp32 followed by kvq_store and
+ * kvq_rotate_query / kvq_tq4_rotate.
+ *   q, q_out: [n_tok][num_q_heads][head_dim], both NULL: keys and values only.
+ *       q_out may be q itself.  With rotate, q_out is fp32 (for the decode
+ *       calls); without, either type (kvq_prefill_attn, kvq_decode_step and
+ *       kvq_decode_attn_unrotated take their queries unrotated, contiguous).
+ *   k, v: [n_tok][num_kv_heads][head_dim].
+ *   q_norm, k_norm, rope: NULL where the model has none.
+ *   d_pos, pos_stride as for kvq_norm_rope; d_slot_mapping and d_status as for
+ *       kvq_store (a token whose slot is negative or out of range is not stored;
+ *       its queries are still written).
+ * Formats Q4_HAD32, Q4_0, TQ4 and BF16 with head_dim 64, 128 or 256 (BF16 also
+ * 512); FP8_ROW: KVQ_ERR_UNSUPPORTED (its parts: kvq_norm_rope of the latent and
+ * of the rope columns, then kvq_store). */
+int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq_rows* k, const kvq_rows* v,
+                            int64_t n_tok, const kvq_norm* q_norm, const kvq_norm* k_norm, const kvq_rope* rope,
+                            const int32_t* d_pos, int64_t pos_stride, const int32_t* d_slot_mapping,
+                            const kvq_rows* q_out, int32_t rotate, int32_t* d_status, void* stream);
+
+/* kvq_load -- rows read back as the values they stand for: token t's K and V rows
+ * at slot d_slots[t] (device int32 [n_tok]) into k and v, [n_tok][num_kv_heads]
+ * [head_dim]; either may be NULL.  FP8_ROW: k is [n_tok][1][head_dim + rope_dim]
+ * (as kvq_store takes it) and v must be NULL.
+ *   rotate_back: 1: in the original space (Q4_HAD32 and TQ4; the other formats
+ *       take 0, as in kvq_merge); 0: in the cache's space.
+ * The value is the code's times its scale, rotated back from exact sums of the
+ * codes (the 4-bit formats), in fp32, rounded once into the output's type.
+ * A negative slot leaves its token's rows as they were; a slot >= num_pages *
+ * page_size writes NaN there and sets KVQ_DEV_BAD_SLOT in the optional status. */
+int32_t kvq_load(const kvq_cache* cache, const int32_t* d_slots, int64_t n_tok, int32_t rotate_back,
+                 const kvq_rows* k, const kvq_rows* v, int32_t* d_status, void* stream);
+
+/* kvq_load_seqs -- kvq_load of ragged runs of positions of several sequences,
+ * packed one after another: output token t, d_cu_lens[b] <= t < d_cu_lens[b + 1],
+ * is position (d_starts ? d_starts[b] : 0) + t - d_cu_lens[b] of the sequence
+ * whose pages d_block_tables[b] lists.
+ *   d_block_tables: device int32 [num_seqs][max_pages]; d_cu_lens: device int32
+ *   [num_seqs + 1], ascending; d_starts: device int32 [num_seqs] or NULL.
+ *   n_tok: the outputs' tokens; those outside [d_cu_lens[0], d_cu_lens[num_seqs])
+ *   are left as they were.
+ * A position outside [0, max_pages * page_size) writes NaN and sets
+ * KVQ_DEV_BAD_LENGTH; a page outside the pool writes NaN and sets
+ * KVQ_DEV_BAD_PAGE. */
+int32_t kvq_load_seqs(const kvq_cache* cache, const int32_t* d_block_tables, int32_t max_pages, int32_t num_seqs,
+                      const int32_t* d_starts, const int32_t* d_cu_lens, int64_t n_tok, int32_t rotate_back,
+                      const kvq_rows* k, const kvq_rows* v, int32_t* d_status, void* stream);
+
+/* Differential attention: query heads 2h and 2h + 1 read the same KV head with two
+ * softmax maps, and output head h is the first minus lambda times the second,
+ *   y[h] = o[2h] - lambda[h] * o[2h + 1],
+ * then, with a norm, y * r * (weight + offset) over the head's width, and at last
+ * times out_scale, rounded once into the output's type.
+ *   d_lambda: device fp32, row b's at b * lambda_stride, one per output head
+ *       (lambda_stride 0: one set of num_q_heads / 2 for every row).
+ *   out: device [rows][num_q_heads / 2][width] of out_dtype, contiguous. */
+
+/* kvq_merge_diff -- kvq_merge of a decode (kvq_decode_attn, _unrotated, _window or
+ * _step) with the difference in the merge: the partials of both maps are folded,
+ * subtracted and rotated back once.  The head_dim 256 formats (FP8_ROW:
+ * KVQ_ERR_UNSUPPORTED); num_q_heads / num_kv_heads even, so that the two maps of
+ * an output head share their KV head, else KVQ_ERR_UNSUPPORTED.  A sequence with
+ * no keys gives zeros, one whose length is out of range NaN; other arguments as
+ * for kvq_merge. */
+int32_t kvq_merge_diff(const kvq_cache* cache, const void* workspace, size_t ws_bytes, int32_t num_seqs,
+                       int32_t num_q_heads, const int32_t* d_seq_lens, int32_t max_seq_len, int32_t n_sel,
+                       int32_t rotate_back, const float* d_lambda, int64_t lambda_stride, const kvq_norm* norm,
+                       float out_scale, void* out, int32_t out_dtype, void* stream);
+
+/* kvq_diff_heads -- the same difference of heads already merged and rotated back
+ * (kvq_prefill_attn's output): x: device fp32 [rows][num_q_heads][width],
+ * contiguous, num_q_heads even, width 64, 128, 256 or 512.  out must not overlap
+ * x. */
+int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_t width, const float* d_lambda,
+                       int64_t lambda_stride, const kvq_norm* norm, float out_scale, void* out, int32_t out_dtype,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif
