@@ -402,54 +402,81 @@ def prefill_attn_fp8(cache: Cache, q, q_start, block_table, sm_scale, workspace=
     return out
 
 
-def _on_device(t, what, dtype=None, device=None):
-    """A tensor the calls below hand to the library by address: on the current
-    device (the kernels are launched there), of the type the call reads."""
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+
+
+def _device(t):
+    """The current device, on which a call's first tensor has to be."""
+    dev = t.get_device()
+    if dev < 0 or dev != _current_device():
+        _refuse_device(t, "a tensor", _current_device() if dev >= 0 else 0)
+    return dev
+
+
+def _refuse_device(t, what, dev):
     if not t.is_cuda:
         raise ValueError(f"kvq: expected a CUDA tensor, got one on {t.device}")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"kvq: {what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    if dtype is not None and t.dtype != dtype:
+    raise ValueError(f"kvq: {what} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _at(t, what, dev, dtype=None):
+    """Address of a tensor the calls below hand to the library: on the call's
+    device (the kernels are launched there), of the type the call reads."""
+    if t.get_device() != dev:
+        _refuse_device(t, what, dev)
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"kvq: {what} must be {dtype}, got {t.dtype}")
-    return t
+    return t.data_ptr()
 
 
-def _ints(t, what, shape):
+def _ints(t, what, dev, shape):
     """Address of contiguous int32 metadata of a given shape."""
-    _on_device(t, what, torch.int32)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"kvq: {what} must be contiguous {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
+    at = _at(t, what, dev, torch.int32)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"kvq: {what} must be contiguous {shape}, got {tuple(t.shape)}")
+    return at
 
 
-def _status_ptr(t):
-    if t is None:
-        return None
-    _on_device(t, "status", torch.int32)
-    return t.data_ptr()
+def _status_at(t, dev):
+    return None if t is None else _at(t, "status", dev, torch.int32)
 
 
-def _rows(t, what, tokens=None, heads=None, width=None):
+def _code(t, what):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"kvq: {what} must be fp32 or bf16, got {t.dtype}")
+    return code
+
+
+def _rows(t, what, dev, tokens, heads, width):
     """kvq_rows of a tensor [tokens, heads, width] whose last dimension is contiguous."""
-    _on_device(t, what)
-    n, h, w = t.shape if t.dim() == 3 else (None, None, None)
-    if n is None or (tokens is not None and n != tokens) or (heads is not None and h != heads) or \
-            (width is not None and w != width):
-        raise ValueError(f"kvq: {what} must be [{'tokens' if tokens is None else tokens}, "
-                         f"{'heads' if heads is None else heads}, {'width' if width is None else width}], "
-                         f"got {tuple(t.shape)}")
+    if t.shape != (tokens, heads, width):
+        raise ValueError(f"kvq: {what} must be [{tokens}, {heads}, {width}], got {tuple(t.shape)}")
     ts, hs, es = t.stride()
-    if es != 1 and w > 1:
+    if es != 1:
         raise ValueError(f"kvq: the last dimension of {what} must be contiguous")
-    return RowsDesc(t.data_ptr(), _dtype_code(t), h, ts, hs)
+    return RowsDesc(_at(t, what, dev), _code(t, what), heads, ts, hs)
+
+
+def _three(t, what):
+    if t.dim() != 3:
+        raise ValueError(f"kvq: {what} must be [tokens, heads, width], got {tuple(t.shape)}")
+    return t.shape
 
 
 def _new(shape, dtype, like, stream):
     """An output tensor that belongs to the stream it is written on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _launch_stream(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 class Norm:
@@ -484,44 +511,47 @@ class Rope:
         self.ref = ctypes.byref(self.desc)
 
 
-def _norm_ref(norm, what, width):
+def _norm_ref(norm, what, dev, width):
     if norm is None:
         return None
     if norm.width != width:
         raise ValueError(f"kvq: {what} is for rows of {norm.width}, not {width}")
-    _on_device(norm.weight, what)
+    if norm.weight.get_device() != dev:
+        _refuse_device(norm.weight, what, dev)
     return norm.ref
 
 
-def _rope_args(rope, positions, n):
+def _rope_args(rope, positions, dev, n):
     """(kvq_rope, positions, axis stride) of a call over n tokens; positions int32
     [n] (one axis) or [axes, n]."""
     if rope is None:
         return None, None, 0
     if positions is None:
         raise ValueError("kvq: rotary positions need positions")
-    _on_device(positions, "positions", torch.int32)
-    _on_device(rope.table, "the rope's table")
-    shape = tuple(positions.shape)
-    if not (shape == (rope.num_axes, n) or (rope.num_axes == 1 and shape == (n,))):
-        raise ValueError(f"kvq: positions must be [{rope.num_axes}, {n}], got {shape}")
+    at = _at(positions, "positions", dev, torch.int32)
+    if rope.table.get_device() != dev:
+        _refuse_device(rope.table, "the rope's table", dev)
+    axes, shape = rope.num_axes, positions.shape
+    if shape != (axes, n) and (axes != 1 or shape != (n,)):
+        raise ValueError(f"kvq: positions must be [{axes}, {n}], got {tuple(shape)}")
     st = positions.stride()
     if n > 1 and st[-1] != 1:
         raise ValueError("kvq: positions of an axis must be contiguous")
-    return rope.ref, positions.data_ptr(), (st[0] if rope.num_axes > 1 else n)
+    return rope.ref, at, (st[0] if axes > 1 else n)
 
 
 def norm_rope(x, positions=None, rope=None, norm=None, out=None, dtype=None, status=None, stream=None):
     """Norm and rotary positions of rows x [tokens, heads, width] (any strides with a
     contiguous last dimension) in one pass; returns out (default: a new tensor of
     `dtype`, x's own if None).  out may be x."""
-    n, heads, width = x.shape
+    n, heads, width = shape = _three(x, "x")
+    dev = _device(x)
     if out is None:
-        out = _new((n, heads, width), dtype or x.dtype, x, stream)
-    rx, ry = _rows(x, "x"), _rows(out, "out", n, heads, width)
-    ref, pos, ps = _rope_args(rope, positions, n)
-    _check(lib().kvq_norm_rope(rx, ry, n, width, _norm_ref(norm, "norm", width), ref, pos, ps, _status_ptr(status),
-                               _stream(stream)), "kvq_norm_rope")
+        out = _new(shape, dtype or x.dtype, x, stream)
+    ref, pos, ps = _rope_args(rope, positions, dev, n)
+    _check(lib().kvq_norm_rope(_rows(x, "x", dev, n, heads, width), _rows(out, "out", dev, n, heads, width), n, width,
+                               _norm_ref(norm, "norm", dev, width), ref, pos, ps, _status_at(status, dev),
+                               _launch_stream(stream, dev)), "kvq_norm_rope")
     return out
 
 
@@ -533,32 +563,34 @@ def norm_rope_store(cache: Cache, q, k, v, slot_mapping, positions=None, rope=No
     (default: a new fp32 tensor) for decode_attn, or with rotate=False for the
     calls that take unrotated queries.  q None: keys and values only."""
     n = k.shape[0]
-    rk, rv = _rows(k, "k", None, cache.Hk, cache.D), _rows(v, "v", n, cache.Hk, cache.D)
+    D, Hk, dev = cache.D, cache.Hk, _device(k)
+    rk, rv = _rows(k, "k", dev, n, Hk, D), _rows(v, "v", dev, n, Hk, D)
     rq = ro = None
     if q is not None:
-        rq = _rows(q, "q", n, None, cache.D)
+        Hq = _three(q, "q")[1]
+        rq = _rows(q, "q", dev, n, Hq, D)
         if q_out is None:
-            q_out = _new(tuple(q.shape), torch.float32, q, stream)
-        ro = _rows(q_out, "q_out", n, q.shape[1], cache.D)
+            q_out = _new((n, Hq, D), torch.float32, q, stream)
+        ro = _rows(q_out, "q_out", dev, n, Hq, D)
     elif q_out is not None:
         raise ValueError("kvq: q_out without q")
-    ref, pos, ps = _rope_args(rope, positions, n)
-    _check(lib().kvq_norm_rope_store(cache.ref, rq, rk, rv, n, _norm_ref(q_norm, "q_norm", cache.D),
-                                     _norm_ref(k_norm, "k_norm", cache.D), ref, pos, ps,
-                                     _ints(slot_mapping, "slot_mapping", (n,)), ro, int(rotate), _status_ptr(status),
-                                     _stream(stream)), "kvq_norm_rope_store")
+    ref, pos, ps = _rope_args(rope, positions, dev, n)
+    _check(lib().kvq_norm_rope_store(cache.ref, rq, rk, rv, n, _norm_ref(q_norm, "q_norm", dev, D),
+                                     _norm_ref(k_norm, "k_norm", dev, D), ref, pos, ps,
+                                     _ints(slot_mapping, "slot_mapping", dev, (n,)), ro, int(rotate),
+                                     _status_at(status, dev), _launch_stream(stream, dev)), "kvq_norm_rope_store")
     return q_out
 
 
-def _load_outputs(cache, n, k, v, dtype, like, stream):
+def _load_outputs(cache, n, k, v, dtype, like, dev, stream):
     """The outputs of a load and their kvq_rows: new ones where both are None."""
     fp8 = cache.fmt == FMT_FP8_ROW
-    width = cache.D + cache.rope if fp8 else cache.D
+    Hk, width = cache.Hk, cache.D + cache.rope if fp8 else cache.D
     if k is None and v is None:
-        k = _new((n, cache.Hk, width), dtype, like, stream)
-        v = None if fp8 else _new((n, cache.Hk, width), dtype, like, stream)
-    return (k, v, None if k is None else _rows(k, "k", n, cache.Hk, width),
-            None if v is None else _rows(v, "v", n, cache.Hk, width))
+        k = _new((n, Hk, width), dtype, like, stream)
+        v = None if fp8 else _new((n, Hk, width), dtype, like, stream)
+    return (k, v, None if k is None else _rows(k, "k", dev, n, Hk, width),
+            None if v is None else _rows(v, "v", dev, n, Hk, width))
 
 
 def _rotates(cache, rotate_back):
@@ -569,10 +601,10 @@ def load(cache: Cache, slots, k=None, v=None, dtype=torch.bfloat16, rotate_back=
     """The rows at slots (int32 [n]) as the values they stand for: (k, v), each [n,
     Hk, D] (fp8: k [n, 1, 576], v None).  Given k and / or v are written instead of
     new ones (one alone: only that plane); a negative slot leaves its rows as they were."""
-    n = slots.shape[0]
-    k, v, rk, rv = _load_outputs(cache, n, k, v, dtype, slots, stream)
-    _check(lib().kvq_load(cache.ref, _ints(slots, "slots", (n,)), n, _rotates(cache, rotate_back), rk, rv,
-                          _status_ptr(status), _stream(stream)), "kvq_load")
+    n, dev = slots.shape[0], _device(slots)
+    k, v, rk, rv = _load_outputs(cache, n, k, v, dtype, slots, dev, stream)
+    _check(lib().kvq_load(cache.ref, _ints(slots, "slots", dev, (n,)), n, _rotates(cache, rotate_back), rk, rv,
+                          _status_at(status, dev), _launch_stream(stream, dev)), "kvq_load")
     return k, v
 
 
@@ -582,29 +614,29 @@ def load_seqs(cache: Cache, block_tables, cu_lens, n_tok, starts=None, k=None, v
     cu_lens[b + 1] - 1 are positions starts[b] (default 0) onwards of the sequence
     whose pages block_tables[b] lists.  n_tok: rows of the outputs; those past
     cu_lens[-1] are left as they were.  Outputs as for load()."""
-    B = cu_lens.shape[0] - 1
-    k, v, rk, rv = _load_outputs(cache, n_tok, k, v, dtype, cu_lens, stream)
-    _check(lib().kvq_load_seqs(cache.ref, _ints(block_tables, "block_tables", (B, block_tables.shape[-1])),
-                               block_tables.shape[-1], B, None if starts is None else _ints(starts, "starts", (B,)),
-                               _ints(cu_lens, "cu_lens", (B + 1,)), n_tok, _rotates(cache, rotate_back), rk, rv,
-                               _status_ptr(status), _stream(stream)), "kvq_load_seqs")
+    B, pages, dev = cu_lens.shape[0] - 1, block_tables.shape[-1], _device(cu_lens)
+    k, v, rk, rv = _load_outputs(cache, n_tok, k, v, dtype, cu_lens, dev, stream)
+    _check(lib().kvq_load_seqs(cache.ref, _ints(block_tables, "block_tables", dev, (B, pages)), pages, B,
+                               None if starts is None else _ints(starts, "starts", dev, (B,)),
+                               _ints(cu_lens, "cu_lens", dev, (B + 1,)), n_tok, _rotates(cache, rotate_back), rk, rv,
+                               _status_at(status, dev), _launch_stream(stream, dev)), "kvq_load_seqs")
     return k, v
 
 
-def _lambda(lam, rows, heads):
+def _lambda(lam, dev, rows, heads):
     """Address and row stride of lambda: fp32 [heads] (one set) or [rows, heads]."""
-    _on_device(lam, "lam", torch.float32)
-    if tuple(lam.shape) not in ((heads,), (rows, heads)) or (heads > 1 and lam.stride(-1) != 1):
-        raise ValueError(f"kvq: lam must be [{heads}] or [{rows}, {heads}] with contiguous rows, got {tuple(lam.shape)}")
-    return lam.data_ptr(), (lam.stride(0) if lam.dim() == 2 else 0)
+    at, shape = _at(lam, "lam", dev, torch.float32), lam.shape
+    if (shape != (rows, heads) and shape != (heads,)) or (heads > 1 and lam.stride(-1) != 1):
+        raise ValueError(f"kvq: lam must be [{heads}] or [{rows}, {heads}] with contiguous rows, got {tuple(shape)}")
+    return at, (lam.stride(0) if len(shape) == 2 else 0)
 
 
-def _diff_out(out, rows, heads, width, dtype, like, stream):
+def _diff_out(out, rows, heads, width, dtype, like, dev, stream):
     if out is None:
         return _new((rows, heads, width), dtype, like, stream)
-    _on_device(out, "out")
-    if tuple(out.shape) != (rows, heads, width) or not out.is_contiguous():
+    if out.shape != (rows, heads, width) or not out.is_contiguous():
         raise ValueError(f"kvq: out must be contiguous [{rows}, {heads}, {width}], got {tuple(out.shape)}")
+    _at(out, "out", dev)
     return out
 
 
@@ -614,24 +646,27 @@ def merge_diff(cache: Cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq
     output minus lam[.., h] times head 2h + 1's, rotated back, normed (norm) and
     scaled.  lam: fp32 [num_q_heads / 2] or [num_seqs, num_q_heads / 2].  Returns
     out [num_seqs, num_q_heads / 2, D]."""
-    out = _diff_out(out, num_seqs, num_q_heads // 2, cache.D, dtype, seq_lens, stream)
-    lp, ls = _lambda(lam, num_seqs, num_q_heads // 2)
+    dev, heads = _device(seq_lens), num_q_heads // 2
+    out = _diff_out(out, num_seqs, heads, cache.D, dtype, seq_lens, dev, stream)
+    lp, ls = _lambda(lam, dev, num_seqs, heads)
     _check(lib().kvq_merge_diff(cache.ref, _ptr(workspace), workspace.numel(), num_seqs, num_q_heads,
-                                _ints(seq_lens, "seq_lens", (num_seqs,)), max_seq_len, n_sel,
-                                _rotates(cache, rotate_back), lp, ls, _norm_ref(norm, "norm", cache.D),
-                                float(out_scale), out.data_ptr(), _dtype_code(out), _stream(stream)), "kvq_merge_diff")
+                                _ints(seq_lens, "seq_lens", dev, (num_seqs,)), max_seq_len, n_sel,
+                                _rotates(cache, rotate_back), lp, ls, _norm_ref(norm, "norm", dev, cache.D),
+                                out_scale, out.data_ptr(), _code(out, "out"), _launch_stream(stream, dev)),
+           "kvq_merge_diff")
     return out
 
 
 def diff_heads(x, lam, norm=None, out_scale=1.0, out=None, dtype=torch.float32, stream=None):
     """The same difference of heads already merged: x fp32 [rows, Hq, width]
     (prefill_attn's output) to [rows, Hq / 2, width]."""
-    rows, Hq, width = x.shape
-    _on_device(x, "x", torch.float32)
-    out = _diff_out(out, rows, Hq // 2, width, dtype, x, stream)
-    lp, ls = _lambda(lam, rows, Hq // 2)
-    _check(lib().kvq_diff_heads(_ptr(x), rows, Hq, width, lp, ls, _norm_ref(norm, "norm", width), float(out_scale),
-                                out.data_ptr(), _dtype_code(out), _stream(stream)), "kvq_diff_heads")
+    rows, Hq, width = _three(x, "x")
+    dev = _device(x)
+    _at(x, "x", dev, torch.float32)
+    out = _diff_out(out, rows, Hq // 2, width, dtype, x, dev, stream)
+    lp, ls = _lambda(lam, dev, rows, Hq // 2)
+    _check(lib().kvq_diff_heads(_ptr(x), rows, Hq, width, lp, ls, _norm_ref(norm, "norm", dev, width), out_scale,
+                                out.data_ptr(), _code(out, "out"), _launch_stream(stream, dev)), "kvq_diff_heads")
     return out
 
 
@@ -639,16 +674,16 @@ def decode_diff(cache: Cache, q, seq_lens, block_tables, max_seq_len, sm_scale, 
                 out_scale=1.0, out=None, dtype=torch.float32, sel=None, stream=None):
     """One differential decode step: decode() of the Hq query heads with merge_diff();
     returns [B, Hq / 2, D]."""
-    B, Hq = q.shape[0], q.shape[1]
+    B, Hq, D = _three(q, "q")
     if cache.fmt in (FMT_Q4_HAD32, FMT_Q4_0):
         decode_attn_unrotated(cache, q, seq_lens, block_tables, max_seq_len, sm_scale, workspace, sel=sel,
                               stream=stream)
     else:
         qq = q
         if cache.fmt == FMT_TQ4:
-            qq = tq4_rotate(cache, q, out=_new(tuple(q.shape), torch.float32, q, stream), stream=stream)
+            qq = tq4_rotate(cache, q, out=_new((B, Hq, D), torch.float32, q, stream), stream=stream)
         elif q.dtype != torch.float32:
-            qq = _new(tuple(q.shape), torch.float32, q, stream)
+            qq = _new((B, Hq, D), torch.float32, q, stream)
             with torch.cuda.stream(stream):
                 qq.copy_(q)
         decode_attn(cache, qq, seq_lens, block_tables, max_seq_len, sm_scale, workspace, sel=sel, stream=stream)
@@ -660,7 +695,7 @@ def prefill_diff(cache: Cache, q, q_start, block_table, sm_scale, lam, norm=None
                  dtype=torch.float32, status=None, stream=None):
     """Differential prefill of a prompt chunk: prefill_attn() of the Hq query heads,
     then diff_heads(); returns [n, Hq / 2, D]."""
-    o = prefill_attn(cache, q, q_start, block_table, sm_scale, out=_new(tuple(q.shape), torch.float32, q, stream),
+    o = prefill_attn(cache, q, q_start, block_table, sm_scale, out=_new(_three(q, "q"), torch.float32, q, stream),
                      status=status, stream=stream)
     return diff_heads(o, lam, norm=norm, out_scale=out_scale, out=out, dtype=dtype, stream=stream)
 

@@ -621,8 +621,9 @@ int32_t kvq_read_status(const void* d_status, int32_t* host_code, void* stream) 
 static bool dtype_ok(int32_t d) { return d == KVQ_DT_F32 || d == KVQ_DT_BF16; }
 
 // Checks of a strided activation tensor of `heads` heads of `width` values and its
-// view; `align`: the boundary its rows must start on for whole-vector access.
-static int32_t check_rows(const kvq_rows* r, int32_t heads, int32_t width, uint32_t align, RowsView* v) {
+// view (whole-vector access where every row starts on a 32-byte boundary).
+static int32_t check_rows(const kvq_rows* r, int32_t heads, int32_t width, RowsView* v) {
+  if (!r) return KVQ_ERR_INVALID_ARG;
   if (!r->data || !dtype_ok(r->dtype) || r->heads != heads) return KVQ_ERR_INVALID_ARG;
   if (r->tok_stride < 0 || r->head_stride < 0) return KVQ_ERR_INVALID_ARG;
   const uint64_t esz = r->dtype == KVQ_DT_F32 ? 4 : 2;
@@ -632,7 +633,7 @@ static int32_t check_rows(const kvq_rows* r, int32_t heads, int32_t width, uint3
   if (r->tok_stride > (int64_t(1) << 31) || r->head_stride > (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   const uint64_t off = base | static_cast<uint64_t>(r->tok_stride) * esz | static_cast<uint64_t>(r->head_stride) * esz |
                        static_cast<uint64_t>(width) * esz;
-  *v = RowsView{r->data, r->tok_stride, r->head_stride, r->dtype, off % align == 0 ? 1 : 0};
+  *v = RowsView{r->data, r->tok_stride, r->head_stride, r->dtype, off % 32 == 0 ? 1 : 0};
   return KVQ_OK;
 }
 
@@ -697,8 +698,8 @@ int32_t kvq_norm_rope(const kvq_rows* x, const kvq_rows* y, int64_t n_tok, int32
   if (!x || !y || x->heads < 1) return KVQ_ERR_INVALID_ARG;
   if (x->heads > kMaxHeads || n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   NormRopeArgs a{};
-  int32_t st = check_rows(x, x->heads, width, 16, &a.q);
-  if (st == KVQ_OK) st = check_rows(y, x->heads, width, 16, &a.qo);
+  int32_t st = check_rows(x, x->heads, width, &a.q);
+  if (st == KVQ_OK) st = check_rows(y, x->heads, width, &a.qo);
   if (st == KVQ_OK) st = check_norm(norm, &a.qn);
   if (st == KVQ_OK) st = check_rope(rope, width, d_pos, pos_stride, n_tok, &a.rope);
   if (st != KVQ_OK) return st;
@@ -727,13 +728,13 @@ int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq
   if (!k || !v || !d_slot_mapping || (q && q->heads < 1)) return KVQ_ERR_INVALID_ARG;
   if ((q && q->heads > kMaxHeads) || Hk > kMaxHeads || n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   NormRopeArgs a{};
-  st = check_rows(k, Hk, D, 16, &a.k);
-  if (st == KVQ_OK) st = check_rows(v, Hk, D, 16, &a.v);
+  st = check_rows(k, Hk, D, &a.k);
+  if (st == KVQ_OK) st = check_rows(v, Hk, D, &a.v);
   if (st == KVQ_OK) st = check_norm(k_norm, &a.kn);
   if (st == KVQ_OK) st = check_rope(rope, D, d_pos, pos_stride, n_tok, &a.rope);
   if (q) {
-    if (st == KVQ_OK) st = check_rows(q, q->heads, D, 16, &a.q);
-    if (st == KVQ_OK) st = check_rows(q_out, q->heads, D, 16, &a.qo);
+    if (st == KVQ_OK) st = check_rows(q, q->heads, D, &a.q);
+    if (st == KVQ_OK) st = check_rows(q_out, q->heads, D, &a.qo);
     if (st == KVQ_OK) st = check_norm(q_norm, &a.qn);
     if (st != KVQ_OK) return st;
     if (rotate && q_out->dtype != KVQ_DT_F32) return KVQ_ERR_INVALID_ARG;
@@ -750,6 +751,7 @@ int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq
   a.Hq = q ? q->heads : 0;
   a.Hk = Hk;
   a.rotate = rotate;
+  a.plane_wide = (reinterpret_cast<uintptr_t>(cache->k) | reinterpret_cast<uintptr_t>(cache->v)) % 32 == 0 ? 1 : 0;
   a.ps = make_fastdiv(static_cast<uint32_t>(cache->page_size));
   cudaError_t e = launch_norm_rope(a, D, cache->format, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
@@ -767,11 +769,11 @@ static int32_t load_impl(const kvq_cache* cache, LoadArgs& a, int32_t rotate_bac
   if (a.n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   int32_t st = KVQ_OK;
   if (k) {
-    st = check_rows(k, cache->num_kv_heads, width, 32, &a.k);
+    st = check_rows(k, cache->num_kv_heads, width, &a.k);
     if (st == KVQ_OK && !rows_distinct(k, a.n_tok, width)) st = KVQ_ERR_INVALID_ARG;
   }
   if (st == KVQ_OK && v) {
-    st = check_rows(v, cache->num_kv_heads, width, 32, &a.v);
+    st = check_rows(v, cache->num_kv_heads, width, &a.v);
     if (st == KVQ_OK && !rows_distinct(v, a.n_tok, width)) st = KVQ_ERR_INVALID_ARG;
   }
   if (st != KVQ_OK) return st;

@@ -38,31 +38,55 @@ __device__ __forceinline__ void put_out(void* out, int dtype, int64_t i, float v
 
 constexpr int kDiffGroups = 8;  // CTAs of an output head: 32 of its 256 values each
 
-// One CTA of 512 threads per (32 output values, output head, sequence): two folds
-// side by side, one for each map, then the difference in the first warp.  What
-// needs the whole head -- the norm, and the TQ4 rows' transform -- is done after
-// the 8 CTAs of the head, one cluster, have put their values into each other's
-// shared memory (`whole`); each then works on all 256 and writes its own 32.
+// The keys of sequence b, or -1 for a length out of range.
+__device__ __forceinline__ int32_t keys_of(const MergeArgs& a, int b) {
+  if (a.n_sel > 0) return a.n_sel;
+  const int32_t T = a.seq_lens[b];
+  return T < 0 || T > a.max_seq_len ? -1 : T;
+}
+
+// What needs the whole head, by one warp on its 256 differences: the TQ4 rows'
+// transform, the norm, the scale.  Lane l ends with values 8 l .. 8 l + 7.
+constexpr int kDiffE = 8;
+__device__ __forceinline__ void finish_head(const MergeArgs& a, const DiffView& d, const void* signs, const float* all,
+                                            int lane, float (&x)[kDiffE]) {
+  constexpr int E = kDiffE;
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] = all[E * lane + i];
+  if (a.rotate_back == 2) tq4_transform<E>(x, lane_signs<E>(signs, lane), lane, true);
+  if (d.norm.weight) {
+    uint64_t p[E / 2], w[E / 2];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) p[i] = pk2(x[2 * i], x[2 * i + 1]);
+    load_weight<E>(d.norm, lane, w);
+    norm_row<E>(p, w, d.norm.eps);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) upk2(p[i], x[2 * i], x[2 * i + 1]);
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[i] *= d.scale;
+}
+
+// A long sequence's few heads: one CTA of 512 threads per (32 output values, output
+// head, sequence), two folds side by side, one for each map, then the difference
+// in the first warp.  For what needs the whole head (`whole`) the 8 CTAs of the
+// head are a cluster that put their values into each other's shared memory; each
+// then works on all 256 and writes its own 32.
 template <int kBatch>
-__global__ void __launch_bounds__(512, kBatch > 4 ? 1 : kBatch == 2 ? 3 : 1)
-    merge_diff_kernel(const MergeArgs a, const DiffView d, const void* signs, int whole) {
+__global__ void __launch_bounds__(512) merge_diff_kernel(const MergeArgs a, const DiffView d, const void* signs,
+                                                         int whole) {
   pdl_wait();
   pdl_trigger();
   constexpr int D = 32 * kDiffGroups;
   const int grp = blockIdx.x, ho = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, map = tid >> 8;
   const int64_t out0 = ((int64_t)b * (a.Hq >> 1) + ho) * D;
-  int32_t T = a.n_sel;
-  bool bad = false;
-  if (a.n_sel == 0) {
-    T = a.seq_lens[b];
-    bad = T < 0 || T > a.max_seq_len;
-  }
-  const int np = bad ? 0 : static_cast<int>(((int64_t)T + a.part - 1) / a.part);
-  if (np == 0) {  // (the whole cluster: T is the sequence's)
-    if (tid < 32) put_out(d.out, d.out_dtype, out0 + 32 * grp + lane, bad ? NAN : 0.f);
+  const int32_t T = keys_of(a, b);
+  if (T <= 0) {  // (the whole cluster: T is the sequence's)
+    if (tid < 32) put_out(d.out, d.out_dtype, out0 + 32 * grp + lane, T < 0 ? NAN : 0.f);
     return;
   }
+  const int np = static_cast<int>(((int64_t)T + a.part - 1) / a.part);
   if (whole) cluster_arrive();  // this CTA runs: its shared memory may be written
   __shared__ FoldSmem sm[2];
   __shared__ float second[32], all[D];
@@ -88,20 +112,170 @@ __global__ void __launch_bounds__(512, kBatch > 4 ? 1 : kBatch == 2 ? 3 : 1)
   cluster_arrive();
   cluster_wait();
   if (tid >= 32) return;
-  constexpr int E = D / 32;
-  float x[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = all[E * lane + i];
-  if (a.rotate_back == 2) tq4_transform<E>(x, lane_signs<E>(signs, lane), lane, true);
-  if (d.norm.weight) {
-    float w[E];
-    load_weight<E>(d.norm, lane, w);
-    norm_row<E>(x, w, d.norm.eps);
-  }
+  float x[kDiffE];
+  finish_head(a, d, signs, all, lane, x);
   if (lane / (32 / kDiffGroups) == grp) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) put_out(d.out, d.out_dtype, out0 + E * lane + i, x[i] * d.scale);
+    for (int i = 0; i < kDiffE; ++i) put_out(d.out, d.out_dtype, out0 + kDiffE * lane + i, x[i]);
   }
+}
+
+// Many heads, or few partitions: one CTA of 512 threads per (output head,
+// sequence).  The fold's arithmetic (merge_fold.cuh) in another arrangement, with
+// the same bits: the running maximum of row r of 32 (partitions r, r + 32, ...)
+// does not depend on the values, so one warp per map works out the rescaling
+// weights of every partition once; the other dimension, 64 chunks of 4 values in
+// 8 groups of 4 rows, is then plain multiply-adds over coalesced loads, the first
+// of which are in flight meanwhile.  (A cluster of 8 CTAs for each head of a batch
+// of 32 sequences of up to 8000 keys took 30 us of a 99 us decode: 3072 CTAs, each
+// with its own barriers for 32 KB of partials.)
+constexpr int kRowThreads = 512;
+constexpr int kRowMaxP = 1024;  // partitions whose weights fit in shared memory
+
+struct RowMergeSmem {
+  float acc[2][32][256];
+  float wr[2][32], z[2][32];
+  float all[256], second[256];
+  int nan[2], empty[2];
+};
+
+template <int kBatch>
+__global__ void __launch_bounds__(kRowThreads) merge_diff_row_kernel(const MergeArgs a, const DiffView d,
+                                                                     const void* signs) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  RowMergeSmem& sm = *reinterpret_cast<RowMergeSmem*>(smem_raw);
+  float2* wts = reinterpret_cast<float2*>(smem_raw + sizeof(RowMergeSmem));  // [2][np] (old, new) weights
+  pdl_wait();
+  pdl_trigger();
+  constexpr int D = 32 * kDiffGroups;
+  const int ho = blockIdx.x, b = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t out0 = ((int64_t)b * (a.Hq >> 1) + ho) * D;
+  const int32_t T = keys_of(a, b);
+  if (T <= 0) {
+    if (tid < D) put_out(d.out, d.out_dtype, out0 + tid, T < 0 ? NAN : 0.f);
+    return;
+  }
+  const int np = static_cast<int>(((int64_t)T + a.part - 1) / a.part);
+  const int64_t base = ((int64_t)b * a.Hq + 2 * ho) * a.P;  // map 1's partials follow map 0's
+  const int chunk = tid & 63, rg = tid >> 6;
+  const float* accp = a.ws_acc + base * D + 4 * chunk;
+  auto load = [&](int i0, float4 (&v)[kBatch][2][4]) {  // partitions i0 + 32 k + rg + 8 j of both maps
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + 32 * k + rg + 8 * j;
+          v[k][m][j] = i < np ? *reinterpret_cast<const float4*>(accp + ((int64_t)m * a.P + i) * D)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+  };
+  float4 v[kBatch][2][4];
+  load(0, v);
+  if (warp < 2) {  // map `warp`, row `lane`: the weights of its partitions
+    const float* m = a.ws_m + base + (int64_t)warp * a.P;
+    const float* z = a.ws_z + base + (int64_t)warp * a.P;
+    float Mt = -INFINITY, Zt = 0.f;
+    bool nan_seen = false;
+    for (int i = lane; i < np; i += 32) {
+      const float mi = m[i], zi = z[i];
+      nan_seen |= isnan(mi);
+      const float Mn = fmaxf(Mt, mi);
+      float2 w = make_float2(1.f, 0.f);
+      if (Mn != -INFINITY) {
+        w = make_float2(exp2f(Mt - Mn), exp2f(mi - Mn));
+        Zt = fmaf(Zt, w.x, zi * w.y);
+        Mt = Mn;
+      }
+      wts[warp * np + i] = w;
+    }
+    float M = Mt;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float wr = Mt == -INFINITY ? 0.f : exp2f(Mt - M);
+    sm.wr[warp][lane] = wr;
+    sm.z[warp][lane] = Zt * wr;
+    const int any_nan = __any_sync(0xffffffffu, nan_seen);
+    if (lane == 0) {
+      sm.nan[warp] = any_nan;
+      sm.empty[warp] = M == -INFINITY;
+    }
+  }
+  __syncthreads();
+  float4 A[2][4];
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) A[m][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0;;) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + 32 * k + rg + 8 * j;
+          if (i >= np) continue;
+          const float2 w = wts[m * np + i];
+          const float4 u = v[k][m][j];
+          A[m][j].x = fmaf(A[m][j].x, w.x, u.x * w.y);
+          A[m][j].y = fmaf(A[m][j].y, w.x, u.y * w.y);
+          A[m][j].z = fmaf(A[m][j].z, w.x, u.z * w.y);
+          A[m][j].w = fmaf(A[m][j].w, w.x, u.w * w.y);
+        }
+    i0 += 32 * kBatch;
+    if (i0 >= np) break;
+    load(i0, v);
+  }
+#pragma unroll
+  for (int m = 0; m < 2; ++m)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = rg + 8 * j;
+      if (r >= np) continue;
+      const float wr = sm.wr[m][r];
+      *reinterpret_cast<float4*>(&sm.acc[m][r][4 * chunk]) =
+          make_float4(A[m][j].x * wr, A[m][j].y * wr, A[m][j].z * wr, A[m][j].w * wr);
+    }
+  __syncthreads();
+  const int map = tid >> 8, col = tid & 255;
+  float o = 0.f, Z = 0.f;
+  const int rows = min(np, 32);
+#pragma unroll 8
+  for (int r = 0; r < rows; ++r) {  // ascending rows, as in the fold
+    o += sm.acc[map][r][col];
+    Z += sm.z[map][r];
+  }
+  o = (sm.empty[map] || Z == 0.f) ? 0.f : o / Z;
+  if (sm.nan[map]) o = NAN;
+  if (map == 1) sm.second[col] = o;
+  __syncthreads();
+  const bool whole = d.norm.weight != nullptr || a.rotate_back == 2;
+  if (map == 0) {
+    float y = fmaf(-d.lambda[b * d.stride + ho], sm.second[col], o);
+    if (a.rotate_back == 1) y = __fmul_rn(warp_fwht32(y, lane), kHadamardScale);
+    if (!whole) put_out(d.out, d.out_dtype, out0 + col, y * d.scale);
+    else sm.all[col] = y;
+  }
+  if (!whole) return;
+  __syncthreads();
+  if (warp != 0) return;
+  float x[kDiffE];
+  finish_head(a, d, signs, sm.all, lane, x);
+#pragma unroll
+  for (int i = 0; i < kDiffE; ++i) put_out(d.out, d.out_dtype, out0 + kDiffE * lane + i, x[i]);
+}
+
+template <int kBatch>
+cudaError_t launch_row(const MergeArgs& a, const DiffView& d, const void* signs, int B, cudaStream_t s) {
+  constexpr auto kern = merge_diff_row_kernel<kBatch>;
+  const int most = static_cast<int>(sizeof(RowMergeSmem)) + 2 * kRowMaxP * 8;
+  cudaError_t e = set_max_smem_once<kern>(most);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(a.Hq / 2, B), dim3(kRowThreads), sizeof(RowMergeSmem) + static_cast<size_t>(2) * a.P * 8,
+                    s, a, d, signs);
 }
 
 // One warp per (row, output head); lane l holds elements E l .. E l + E - 1.
@@ -116,18 +290,21 @@ __global__ void __launch_bounds__(256) diff_heads_kernel(const float* __restrict
   if (i >= n) return;
   const uint32_t row = fast_div(static_cast<uint32_t>(i), hd), h = static_cast<uint32_t>(i) - row * hd.d;
   const RowsView in{const_cast<float*>(x), 0, 0, KVQ_DT_F32, wide};
-  float p[E], q[E];
-  load_row<E>(in, 2 * i * W, lane, p);
-  load_row<E>(in, (2 * i + 1) * W, lane, q);
+  RawRow<E, false> r1, r2;
+  load_raw<E, false>(in, 2 * i * W, lane, r1);
+  load_raw<E, false>(in, (2 * i + 1) * W, lane, r2);
   const float lam = d.lambda[row * d.stride + h];
+  uint64_t p[E / 2], q[E / 2];
+  unpack_row<E, false>(r1, p);
+  unpack_row<E, false>(r2, q);
 #pragma unroll
-  for (int j = 0; j < E; ++j) p[j] = fmaf(-lam, q[j], p[j]);
+  for (int j = 0; j < E / 2; ++j) p[j] = fma2(pk2(-lam, -lam), q[j], p[j]);
   if (d.norm.weight) {
     load_weight<E>(d.norm, lane, q);
     norm_row<E>(p, q, d.norm.eps);
   }
 #pragma unroll
-  for (int j = 0; j < E; ++j) p[j] *= d.scale;
+  for (int j = 0; j < E / 2; ++j) p[j] = mul2(p[j], pk2(d.scale, d.scale));
   const RowsView out{d.out, 0, 0, d.out_dtype, wide};
   write_row<E>(out, i * W, lane, p);
 }
@@ -135,6 +312,15 @@ __global__ void __launch_bounds__(256) diff_heads_kernel(const float* __restrict
 }  // namespace
 
 cudaError_t launch_merge_diff(const MergeArgs& a, const DiffView& d, const kvq_cache& c, int B, cudaStream_t s) {
+  // A CTA for each head where that fills half the GPU, or where a head has few
+  // partitions; 8 CTAs for each head of a long sequence.
+  const int64_t heads = (int64_t)(a.Hq / 2) * B, n_sm = device_sm_count();
+  cudaError_t e;
+  if (a.P <= kRowMaxP && (a.P <= 96 || 2 * heads >= n_sm)) {
+    e = a.P <= 32 ? launch_row<1>(a, d, c.signs, B, s) : launch_row<2>(a, d, c.signs, B, s);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+  }
   const int whole = (d.norm.weight != nullptr || a.rotate_back == 2) ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kDiffGroups, a.Hq / 2, B);
@@ -148,15 +334,12 @@ cudaError_t launch_merge_diff(const MergeArgs& a, const DiffView& d, const kvq_c
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = whole ? 2 : 1;
-  // the merge's rule on CTAs of twice the threads
-  const int64_t ctas = (int64_t)kDiffGroups * (a.Hq / 2) * B, n_sm = device_sm_count();
-  cudaError_t e;
-  if (a.P > 128 && ctas <= n_sm)
+  // (as the merge: more of a thread's partitions loaded at once where there are more)
+  if (a.P > 128 && heads * kDiffGroups <= n_sm)
     e = a.P > 256 ? cudaLaunchKernelEx(&cfg, merge_diff_kernel<17>, a, d, c.signs, whole)
                   : cudaLaunchKernelEx(&cfg, merge_diff_kernel<8>, a, d, c.signs, whole);
   else
-    e = ctas > 4 * n_sm ? cudaLaunchKernelEx(&cfg, merge_diff_kernel<2>, a, d, c.signs, whole)
-                        : cudaLaunchKernelEx(&cfg, merge_diff_kernel<4>, a, d, c.signs, whole);
+    e = cudaLaunchKernelEx(&cfg, merge_diff_kernel<4>, a, d, c.signs, whole);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -167,7 +350,7 @@ cudaError_t launch_diff_heads(const float* x, int64_t rows, int Hq, int width, c
   const size_t esz = d.out_dtype == KVQ_DT_BF16 ? 2 : 4;
   const FastDiv hd = make_fastdiv(static_cast<uint32_t>(heads));
   const int wide =
-      (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (reinterpret_cast<uintptr_t>(d.out) & 15u) == 0 ? 1 : 0;
+      (reinterpret_cast<uintptr_t>(x) & 31u) == 0 && (reinterpret_cast<uintptr_t>(d.out) & 31u) == 0 ? 1 : 0;
   for (int64_t r0 = 0; r0 < rows; r0 += max_rows) {
     const int64_t n = (rows - r0 < max_rows ? rows - r0 : max_rows) * heads;
     DiffView p = d;

@@ -113,7 +113,7 @@ struct RowsView {
   void* data;
   int64_t ts, hs;  // elements from a token, a head to the next
   int dtype;
-  int wide;  // 1: every row starts on a 16-byte boundary, so lanes move whole vectors
+  int wide;  // 1: every row starts on a 32-byte boundary, so lanes move whole vectors
 };
 
 // A kvq_norm; weight NULL: no norm.
@@ -143,6 +143,7 @@ struct NormRopeArgs {
   int Hq, Hk;
   int rotate;  // 1: queries into the cache's space
   int hpw;     // heads a warp takes (set by the launch)
+  int plane_wide;  // BF16: the planes start on 32-byte boundaries
   FastDiv ps;  // page_size
 };
 

@@ -6,22 +6,25 @@
 // as 4-bit codes with an fp16 scale; "KV cache quantization: fp8 (KV8) + 4-bit
 // TurboQuant": e4m3 rows with fp32 scales, and randomized-Hadamard rows with a
 // 16-level codebook).  Rotating back takes the sums of the codes first and the
-// scale after, so that the sums are exact:
-//   Q4_HAD32: sums of 32 integers -8 .. 7 are at most 256 in magnitude, exact in
-//     fp16, so the butterfly runs on packed fp16 pairs;
-//   TQ4: the levels are multiples of 2^-13 below 4 and a sum of 256 of them is
-//     below 2^10, 23 bits: exact in fp32.
+// scale after, so that the sums are exact in fp32:
+//   Q4_HAD32: 32 integers -8 .. 7;
+//   TQ4: the levels are multiples of 2^-13 below 4, and a sum of 256 of them is
+//     below 2^10: 23 bits.
 // What is left is fl(sum * fl(scale / sqrt(n))) and the rounding into the output's
 // type.
 //
-// One lane takes one group of 32 values: one 16-byte load of codes, the butterfly
-// in registers (TQ4: its last stages across the row's lanes), and the 32 results
-// as whole 32-byte sectors (256-bit stores), so no shared memory is needed to
-// write full sectors.  Bound: memory (in bf16 the outputs are 3.6 times the
-// codes' bytes).
+// The 32-point transform of a group is a product with a matrix of +-1, so it runs
+// on the tensor cores (m16n8k16, fp16 operands that hold the codes exactly): as a
+// butterfly in registers it took 230 instructions a group and the whole kernel was
+// bound by issuing them (262144 tokens of 4 heads: 272 us, floor 203 us).  One
+// warp tile is 8 groups of K and the same 8 of V (the 16 rows of the operand); the
+// columns of the matrix are ordered so that a thread's results are 8 consecutive
+// values, and the terms so that it loads 8 consecutive codes as one word.  The TQ4
+// rows' remaining stages, between the groups of a row, are stages across lanes.
+// Bound: memory (in bf16 the outputs are 3.6 times the codes' bytes).
 #include <cuda_fp8.h>
 
-#include "kernels.cuh"
+#include "rows.cuh"
 #include "tq4_code.cuh"
 
 namespace kvq {
@@ -30,32 +33,17 @@ namespace {
 
 constexpr int kLoadBlock = 256;
 
-// 32 bytes at once (address a multiple of 32).
-__device__ __forceinline__ void st256(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// N (a multiple of 16) consecutive values into the view at element e (view.wide:
+// N (8, or a multiple of 16) consecutive values into the view at element e (view.wide:
 // the address is a multiple of 32 bytes).
 template <int N>
 __device__ __forceinline__ void put_values(const RowsView& v, int64_t e, const float (&x)[N]) {
   if (v.dtype == KVQ_DT_BF16) {
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(v.data) + e;
     if (v.wide) {
+      uint32_t w[N / 2];
 #pragma unroll
-      for (int i = 0; i < N; i += 16) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = bf16_pair(x[i + 2 * j], x[i + 2 * j + 1]);
-        st256(p + i, w);
-      }
+      for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+      st_words<N / 2>(p, w);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) p[i] = __float2bfloat16_rn(x[i]);
@@ -63,13 +51,10 @@ __device__ __forceinline__ void put_values(const RowsView& v, int64_t e, const f
   } else {
     float* p = static_cast<float*>(v.data) + e;
     if (v.wide) {
+      uint32_t w[N];
 #pragma unroll
-      for (int i = 0; i < N; i += 8) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[i + j]);
-        st256(p + i, w);
-      }
+      for (int i = 0; i < N; ++i) w[i] = __float_as_uint(x[i]);
+      st_words<N>(p, w);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) p[i] = x[i];
@@ -121,36 +106,6 @@ __device__ __forceinline__ Where locate(const LoadArgs& a, int64_t t, int32_t& p
   return kRow;
 }
 
-// The 32 codes of a group (16 bytes) as exact fp16 pairs (code - 8): register
-// 4q + j holds elements 8q + j and 8q + j + 4.
-__device__ __forceinline__ void q4_pairs(const uint4& u, __half2 (&p)[16]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    p[4 * q + 0] = u32_as_h2(nib_lo_pair(w[q]));
-    p[4 * q + 1] = u32_as_h2(nib_hi_pair(w[q]));
-    p[4 * q + 2] = u32_as_h2(nib_lo_pair(w[q] >> 8));
-    p[4 * q + 3] = u32_as_h2(nib_hi_pair(w[q] >> 8));
-  }
-}
-
-// The 32-point butterfly (unscaled) on those pairs; every sum is exact.
-__device__ __forceinline__ void h2_butterfly(__half2 (&p)[16]) {
-#pragma unroll
-  for (int h = 1; h < 16; h <<= 1)  // element distances 1, 2, 8, 16
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (!(i & h)) {
-        const __half2 s = __hadd2(p[i], p[i + h]), d = __hsub2(p[i], p[i + h]);
-        p[i] = s;
-        p[i + h] = d;
-      }
-  const __half2 pm = u32_as_h2(0xBC003C00u);  // (1, -1)
-#pragma unroll
-  for (int i = 0; i < 16; ++i)  // element distance 4: the halves of a register
-    p[i] = __hfma2(p[i], pm, __lowhigh2highlow(p[i]));
-}
-
 // Byte `hi` (1) or 0 of the fp16 levels m .. m + 3, as a byte-permute table word.
 __host__ __device__ constexpr uint32_t tq4_table(int m, int hi) {
   // the levels in fp16: 0.128.., 0.387.., 0.656.., 0.942.., 1.255.., 1.618.., 2.068.., 2.732..
@@ -160,111 +115,165 @@ __host__ __device__ constexpr uint32_t tq4_table(int m, int hi) {
   return w;
 }
 
-// The 8 levels (with sign) of a word of 8 TQ4 codes.
-__device__ __forceinline__ void tq4_levels8(uint32_t w, float (&x)[8]) {
-  const uint32_t m = w & 0x77777777u;
+// The 8 codes of a word as four exact fp16 pairs, and which codes a pair holds:
+// pair 2s + u is (element 2s + u, element 2s + u + 4) for the 4-bit formats (code -
+// 8), (element 4s + 2u, the next) for TQ4 (the levels, by byte permutes).
+template <int FMT>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&p)[4]) {
+  if constexpr (FMT == KVQ_FMT_TQ4) {
+    const uint32_t m = w & 0x77777777u;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {  // codes 4h .. 4h + 3
-    const uint32_t sel = h ? m >> 16 : m;
-    const uint32_t lo = prmt(tq4_table(0, 0), tq4_table(4, 0), sel), hi = prmt(tq4_table(0, 1), tq4_table(4, 1), sel);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = 4 * h + 2 * j;
-      const uint32_t pair = prmt(lo, hi, j ? 0x7362u : 0x5140u);
-      const float2 f = __half22float2(u32_as_h2(pair));
-      x[c] = __uint_as_float(__float_as_uint(f.x) | ((w << (28 - 4 * c)) & 0x80000000u));
-      x[c + 1] = __uint_as_float(__float_as_uint(f.y) | ((w << (24 - 4 * c)) & 0x80000000u));
+    for (int s = 0; s < 2; ++s) {  // codes 4s .. 4s + 3
+      const uint32_t sel = s ? m >> 16 : m;
+      const uint32_t lo = prmt(tq4_table(0, 0), tq4_table(4, 0), sel);
+      uint32_t hi = prmt(tq4_table(0, 1), tq4_table(4, 1), sel);
+      uint32_t sg = s ? w >> 16 : w & 0xFFFFu;  // their signs into the levels' high bytes
+      sg = (sg | sg << 8) & 0x00FF00FFu;
+      sg = (sg | sg << 4) & 0x08080808u;
+      hi |= sg << 4;
+      p[2 * s] = prmt(lo, hi, 0x5140u);
+      p[2 * s + 1] = prmt(lo, hi, 0x7362u);
     }
+  } else {
+    p[0] = nib_lo_pair(w);
+    p[1] = nib_hi_pair(w);
+    p[2] = nib_lo_pair(w >> 8);
+    p[3] = nib_hi_pair(w >> 8);
   }
 }
 
-// FMT: KVQ_FMT_Q4_HAD32, KVQ_FMT_Q4_0 or KVQ_FMT_TQ4; NG groups of 32 in a row.
-// A thread takes one group of one row; groups, heads, K / V and tokens in this
-// order.  rpt divides by a token's rows (its heads in the planes wanted, the
-// first of which is K when kv0 == 0), so a launch keeps tokens * rows * NG < 2^31.
-template <int FMT, int NG>
-__global__ void __launch_bounds__(kLoadBlock) load_q4_kernel(const __grid_constant__ LoadArgs a, int kv0, FastDiv rpt) {
+// The same pairs' codes in element order, as fp32.
+template <int FMT>
+__device__ __forceinline__ void code_values(uint32_t w, float (&x)[8]) {
+  uint32_t p[4];
+  code_pairs<FMT>(w, p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(u32_as_h2(p[i]));
+    x[FMT == KVQ_FMT_TQ4 ? 2 * i : i] = f.x;
+    x[FMT == KVQ_FMT_TQ4 ? 2 * i + 1 : i + 4] = f.y;
+  }
+}
+
+// The +-1 matrix's fragments of this lane (t = lane & 3, g = lane >> 2): step s of
+// the two of 16 terms, half u, result columns 8 nt + g, which stand for output
+// 8 (g >> 1) + 2 nt + (g & 1).  The sign of (element, output) is the parity of
+// their common bits: bits 3 and 4 give the lane's base sign, the bits of the pair's
+// place and of s, u, nt flip it.
+template <int FMT>
+struct SignMatrix {
+  uint32_t base;  // s = u = nt = 0
+  uint32_t flip;  // u = 1 (4-bit formats: where g is odd)
+  __device__ __forceinline__ explicit SignMatrix(int lane) {
+    const int t = lane & 3, g = lane >> 2;
+    const uint32_t b = (__popc(t & (g >> 1)) & 1) ? 0xBC00BC00u : 0x3C003C00u;
+    if constexpr (FMT == KVQ_FMT_TQ4) {  // pair place: element bit 0; u: bit 1; s: bit 2
+      base = b ^ ((g & 1) ? 0x80000000u : 0u);
+      flip = 0;
+    } else {  // u: element bit 0; s: bit 1; pair place: bit 2
+      base = b;
+      flip = (g & 1) ? 0x80008000u : 0u;
+    }
+  }
+  __device__ __forceinline__ uint32_t at(int s, int u, int nt) const {
+    if constexpr (FMT == KVQ_FMT_TQ4)
+      return base ^ ((((u & nt) ^ (s & (nt >> 1))) & 1) ? 0x80008000u : 0u);
+    else
+      return (base ^ (u ? flip : 0u)) ^ ((nt & 2) ? 0x80000000u : 0u) ^ ((s & nt & 1) ? 0x80008000u : 0u);
+  }
+};
+
+// FMT: KVQ_FMT_Q4_HAD32, KVQ_FMT_Q4_0 or KVQ_FMT_TQ4; NG groups of 32 in a row; ROT:
+// rotate back.  A warp takes 8 / NG tokens at once and hpw heads one after another
+// (kUnroll heads' loads in flight): lane 4g + t the codes 8t .. 8t + 7 of group g of
+// the 8 (group g % NG of token g / NG's row), in K and in V.
+constexpr int kUnroll = 4;
+
+template <int FMT, int NG, bool ROT>
+__global__ void __launch_bounds__(kLoadBlock) load_q4_kernel(const __grid_constant__ LoadArgs a, int hpw) {
   pdl_wait();
   pdl_trigger();
   constexpr int D = 32 * NG;
+  const int lane = threadIdx.x & 31, t4 = lane & 3, g = lane >> 2, G = g % NG;
+  const int64_t t = a.t0 + ((int64_t)blockIdx.x * (kLoadBlock / 32) + (threadIdx.x >> 5)) * (8 / NG) + g / NG;
   const int Hk = a.c.num_kv_heads;
-  const uint32_t idx = blockIdx.x * kLoadBlock + threadIdx.x;
-  const int G = static_cast<int>(idx % NG);
-  const uint32_t row = idx / NG;
-  const uint32_t dt = fast_div(row, rpt);
-  const uint32_t rt = row - dt * rpt.d;
-  const uint32_t plane = fast_div(rt, a.hk);
-  const int head = static_cast<int>(rt - plane * a.hk.d);
-  const bool is_v = kv0 + static_cast<int>(plane) != 0;
-  const int64_t t = a.t0 + dt;
+  const int h0 = blockIdx.y * hpw, h1 = min(h0 + hpw, Hk);
   int32_t page = 0, why = 0;
   uint32_t off = 0;
   const Where at = t < a.n_tok ? locate(a, t, page, off, why) : kSkip;
-  const int64_t r = ((int64_t)page * Hk + head) * a.c.page_size + off;
-  const uint8_t* codes = static_cast<const uint8_t*>(is_v ? a.c.v : a.c.k);
-  const __half* scales = static_cast<const __half*>(is_v ? a.c.v_scale : a.c.k_scale);
-  float x[32];
-  if constexpr (FMT == KVQ_FMT_TQ4) {
-    float f = 0.f;
-    uint4 u = make_uint4(0, 0, 0, 0);  // rows that are not read still take part in the exchanges
-    if (at == kRow) {
-      u = reinterpret_cast<const uint4*>(codes + r * (D / 2))[G];
-      f = __half2float(scales[r]);
-    }
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if (at == kBad && G == 0 && t4 == 0) set_status(a.status, why);
+  const bool with_k = a.k.data != nullptr, with_v = a.v.data != nullptr;
+  const SignMatrix<FMT> H(lane);
+  uint32_t sw = 0;
+  if constexpr (FMT == KVQ_FMT_TQ4 && ROT) sw = static_cast<const uint32_t*>(a.c.signs)[G] >> (8 * t4);
+  constexpr float kBack = !ROT ? 1.0f : FMT == KVQ_FMT_TQ4 ? tq4_row_scale<NG>() : kHadamardScale;
+
+  for (int hb = h0; hb < h1; hb += kUnroll) {
+    uint32_t word[kUnroll][2];
+    __half scale[kUnroll][2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) tq4_levels8(w[q], *reinterpret_cast<float(*)[8]>(&x[8 * q]));
-    if (a.rotate_back) {
+    for (int i = 0; i < kUnroll; ++i)
 #pragma unroll
-      for (int h = 1; h < 32; h <<= 1)
+      for (int kv = 0; kv < 2; ++kv) {
+        word[i][kv] = 0;
+        scale[i][kv] = __ushort_as_half(0);
+        if (at == kRow && hb + i < h1 && (kv ? with_v : with_k)) {
+          const int64_t r = ((int64_t)page * Hk + hb + i) * a.c.page_size + off;
+          word[i][kv] = static_cast<const uint32_t*>(kv ? a.c.v : a.c.k)[r * (D / 8) + 4 * G + t4];
+          scale[i][kv] = static_cast<const __half*>(
+              kv ? a.c.v_scale : a.c.k_scale)[FMT == KVQ_FMT_TQ4 ? r : r * NG + G];
+        }
+      }
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (!(i & h)) {
-            const float p = x[i], q = x[i + h];
-            x[i] = p + q;
-            x[i + h] = p - q;
+    for (int i = 0; i < kUnroll; ++i) {
+      if (hb + i >= h1) break;
+      float x[2][8];
+      if constexpr (ROT) {
+        uint32_t pk[4], pv[4];
+        code_pairs<FMT>(word[i][0], pk);
+        code_pairs<FMT>(word[i][1], pv);
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            mma_f16(c, pk[2 * s], pv[2 * s], pk[2 * s + 1], pv[2 * s + 1], H.at(s, 0, nt), H.at(s, 1, nt));
+          x[0][2 * nt] = c[0];
+          x[0][2 * nt + 1] = c[1];
+          x[1][2 * nt] = c[2];
+          x[1][2 * nt + 1] = c[3];
+        }
+        if constexpr (FMT == KVQ_FMT_TQ4) {
+#pragma unroll
+          for (int o = 1; o < NG; o <<= 1) {  // the stages between the row's groups
+            const float sgn = (G & o) ? -1.f : 1.f;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                x[kv][j] = __fmaf_rn(x[kv][j], sgn, __shfl_xor_sync(0xffffffffu, x[kv][j], 4 * o));
           }
-#pragma unroll
-      for (int o = 1; o < NG; o <<= 1) {  // the stages between the row's groups, its NG lanes
-        const float sgn = (G & o) ? -1.f : 1.f;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __fmaf_rn(x[i], sgn, __shfl_xor_sync(0xffffffffu, x[i], o));
+        }
+      } else {
+        code_values<FMT>(word[i][0], x[0]);
+        code_values<FMT>(word[i][1], x[1]);
       }
-      f *= tq4_row_scale<NG>();
-      const uint32_t sw = static_cast<const uint32_t*>(a.c.signs)[G];
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        x[i] = __uint_as_float(__float_as_uint(x[i] * f) ^ ((sw << (31 - i)) & 0x80000000u));
-    } else {
+      for (int kv = 0; kv < 2; ++kv) {
+        const float f = __half2float(scale[i][kv]) * kBack;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] *= f;
-    }
-  } else if (at == kRow) {
-    const uint4 u = reinterpret_cast<const uint4*>(codes + r * (D / 2))[G];
-    float f = __half2float(scales[r * NG + G]);
-    __half2 p[16];
-    q4_pairs(u, p);
-    if (FMT == KVQ_FMT_Q4_HAD32 && a.rotate_back) {
-      h2_butterfly(p);
-      f *= kHadamardScale;
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 v = __half22float2(p[4 * q + j]);
-        x[8 * q + j] = v.x * f;
-        x[8 * q + j + 4] = v.y * f;
+        for (int j = 0; j < 8; ++j) {
+          x[kv][j] *= f;
+          if constexpr (FMT == KVQ_FMT_TQ4 && ROT)
+            x[kv][j] = __uint_as_float(__float_as_uint(x[kv][j]) ^ ((sw << (31 - j)) & 0x80000000u));
+          if (at == kBad) x[kv][j] = NAN;
+        }
+        const RowsView& out = kv ? a.v : a.k;
+        if (at != kSkip && (kv ? with_v : with_k))
+          put_values<8>(out, t * out.ts + (hb + i) * out.hs + 32 * G + 8 * t4, x[kv]);
       }
+    }
   }
-  if (at == kSkip) return;
-  if (at == kBad) {
-    if (G == 0) set_status(a.status, why);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = NAN;
-  }
-  const RowsView& out = is_v ? a.v : a.k;
-  put_values<32>(out, t * out.ts + head * out.hs + 32 * G, x);
 }
 
 // BF16 and fp8 latent rows: a thread takes 16 consecutive values of a row.  cpt
@@ -344,47 +353,62 @@ cudaError_t launch_load(const LoadArgs& args, cudaStream_t s) {
   const int Hk = a.c.num_kv_heads, D = a.c.head_dim;
   const bool fp8 = a.c.format == KVQ_FMT_FP8_ROW, wide = fp8 || a.c.format == KVQ_FMT_BF16;
   const int NG = D / 32, cpr = (fp8 ? D + a.c.rope_dim : D) / 16;
-  const int64_t rows = fp8 ? 1 : (int64_t)Hk * kvs;      // of a token
-  const int64_t per_tok = rows * (wide ? cpr : NG);      // threads of a token
+  const int64_t n_tok = a.n_tok;
+  if (!wide) {
+    // enough warps to fill the GPU a few times over, several heads in each
+    const int64_t warps = (n_tok * NG + 7) / 8, target = (int64_t)device_sm_count() * 192;
+    int64_t hpw = 1;
+    if (warps * Hk > target) hpw = ((warps * Hk + target - 1) / target + kUnroll - 1) / kUnroll * kUnroll;
+    if (hpw > Hk) hpw = Hk;
+    const int64_t chunks = (Hk + hpw - 1) / hpw;
+    if (chunks > 65535) return cudaErrorInvalidValue;
+    const dim3 grid(static_cast<unsigned>((warps + kLoadBlock / 32 - 1) / (kLoadBlock / 32)),
+                    static_cast<unsigned>(chunks)),
+        block(kLoadBlock);
+    cudaError_t e = cudaErrorInvalidValue;
+#define KVQ_LOAD(F, N, R) e = launch_pdl(load_q4_kernel<F, N, R>, grid, block, 0, s, a, static_cast<int>(hpw)); break
+#define KVQ_LOAD_NG(F, R)       \
+  switch (NG) {                 \
+    case 1: KVQ_LOAD(F, 1, R);  \
+    case 2: KVQ_LOAD(F, 2, R);  \
+    case 4: KVQ_LOAD(F, 4, R);  \
+    case 8: KVQ_LOAD(F, 8, R);  \
+    default: break;             \
+  }
+#define KVQ_LOAD_TQ(R)                      \
+  switch (NG) {                             \
+    case 2: KVQ_LOAD(KVQ_FMT_TQ4, 2, R);    \
+    case 4: KVQ_LOAD(KVQ_FMT_TQ4, 4, R);    \
+    case 8: KVQ_LOAD(KVQ_FMT_TQ4, 8, R);    \
+    default: break;                         \
+  }
+    if (a.c.format == KVQ_FMT_TQ4) {
+      if (a.rotate_back) {
+        KVQ_LOAD_TQ(true)
+      } else {
+        KVQ_LOAD_TQ(false)
+      }
+    } else if (a.rotate_back) {  // Q4_HAD32
+      KVQ_LOAD_NG(KVQ_FMT_Q4_HAD32, true)
+    } else {  // the two 4-bit formats' codes have the same values
+      KVQ_LOAD_NG(KVQ_FMT_Q4_0, false)
+    }
+#undef KVQ_LOAD_TQ
+#undef KVQ_LOAD_NG
+#undef KVQ_LOAD
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+  }
+  const int64_t per_tok = fp8 ? cpr : (int64_t)cpr * Hk * kvs;  // threads of a token
   if (per_tok >= (int64_t(1) << 30)) return cudaErrorInvalidValue;
-  const FastDiv fr = make_fastdiv(static_cast<uint32_t>(rows)), ft = make_fastdiv(static_cast<uint32_t>(per_tok)),
-                fc = make_fastdiv(static_cast<uint32_t>(cpr));
-  // launches of at most 2^30 threads, so that the kernels' indices stay 32-bit
-  const int64_t max_tok = (int64_t(1) << 30) / per_tok, n_tok = a.n_tok;
+  const FastDiv ft = make_fastdiv(static_cast<uint32_t>(per_tok)), fc = make_fastdiv(static_cast<uint32_t>(cpr));
+  // launches of at most 2^30 threads, so that the kernel's indices stay 32-bit
+  const int64_t max_tok = (int64_t(1) << 30) / per_tok;
   for (a.t0 = 0; a.t0 < n_tok; a.t0 += max_tok) {
     a.n_tok = n_tok - a.t0 < max_tok ? n_tok : a.t0 + max_tok;  // tokens [t0, n_tok) in this launch
     const dim3 grid(static_cast<unsigned>(((a.n_tok - a.t0) * per_tok + kLoadBlock - 1) / kLoadBlock)), block(kLoadBlock);
-    cudaError_t e = cudaErrorInvalidValue;
-#define KVQ_LOAD(F, N) e = launch_pdl(load_q4_kernel<F, N>, grid, block, 0, s, a, kv0, fr); break
-    if (fp8) {
-      e = launch_pdl(load_wide_kernel<true>, grid, block, 0, s, a, kv0, ft, fc);
-    } else if (wide) {
-      e = launch_pdl(load_wide_kernel<false>, grid, block, 0, s, a, kv0, ft, fc);
-    } else if (a.c.format == KVQ_FMT_Q4_HAD32) {
-      switch (NG) {
-        case 1: KVQ_LOAD(KVQ_FMT_Q4_HAD32, 1);
-        case 2: KVQ_LOAD(KVQ_FMT_Q4_HAD32, 2);
-        case 4: KVQ_LOAD(KVQ_FMT_Q4_HAD32, 4);
-        case 8: KVQ_LOAD(KVQ_FMT_Q4_HAD32, 8);
-        default: break;
-      }
-    } else if (a.c.format == KVQ_FMT_Q4_0) {
-      switch (NG) {
-        case 1: KVQ_LOAD(KVQ_FMT_Q4_0, 1);
-        case 2: KVQ_LOAD(KVQ_FMT_Q4_0, 2);
-        case 4: KVQ_LOAD(KVQ_FMT_Q4_0, 4);
-        case 8: KVQ_LOAD(KVQ_FMT_Q4_0, 8);
-        default: break;
-      }
-    } else {
-      switch (NG) {
-        case 2: KVQ_LOAD(KVQ_FMT_TQ4, 2);
-        case 4: KVQ_LOAD(KVQ_FMT_TQ4, 4);
-        case 8: KVQ_LOAD(KVQ_FMT_TQ4, 8);
-        default: break;
-      }
-    }
-#undef KVQ_LOAD
+    cudaError_t e = fp8 ? launch_pdl(load_wide_kernel<true>, grid, block, 0, s, a, kv0, ft, fc)
+                        : launch_pdl(load_wide_kernel<false>, grid, block, 0, s, a, kv0, ft, fc);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();

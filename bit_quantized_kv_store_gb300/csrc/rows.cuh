@@ -1,61 +1,58 @@
 // rows.cuh -- strided activation rows in a warp's registers: lane l holds elements
-// E l .. E l + E - 1 of a row of 32 E values.  Loads and stores of bf16 and fp32
-// rows, the per-row norm, and the 4-bit groups of a row in this layout (a group
-// of 32 values spans 32 / E lanes).  Every floating-point operation that decides
-// bits is an explicit IEEE-rounded intrinsic, so kernels of different
-// translation units agree bit for bit.
+// E l .. E l + E - 1 of a row of 32 E values, as E / 2 packed fp32 pairs (element
+// 2i in the low half of pair i).  Loads and stores of bf16 and fp32 rows, the
+// per-row norm, the caches' row transforms and the 4-bit codes in this layout (a
+// group of 32 values spans 32 / E lanes).  The transforms perform the operations
+// of the store's butterflies on the same operands (two per packed instruction;
+// across lanes p + x * (+-1), one rounding), so the stored bytes are the same.
 #pragma once
+#include "f32x2.cuh"
 #include "kernels.cuh"
 #include "q4_code.cuh"
 
 namespace kvq {
 
-// The lane's E values of the row at element `e0` of the view (the row's start).
-template <int E>
-__device__ __forceinline__ void load_row(const RowsView& v, int64_t e0, int lane, float (&x)[E]) {
-  const int64_t e = e0 + E * lane;
-  if (v.dtype == KVQ_DT_BF16) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(v.data) + e;
-    if (v.wide) {
-      uint32_t w[(E + 1) / 2];
-      if constexpr (E >= 8) {
+// ---------------------------------------------------------------- loads and stores
+// 32 bytes at once (address a multiple of 32).
+__device__ __forceinline__ void ld256(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st256(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// N words (1, 2, 4, 8 or 16) at an address aligned to them (to 32 bytes past 8).
+template <int N>
+__device__ __forceinline__ void ld_words(const void* p, uint32_t* w) {
+  if constexpr (N >= 8) {
 #pragma unroll
-        for (int i = 0; i < E / 8; ++i) {
-          const uint4 u = reinterpret_cast<const uint4*>(p)[i];
-          w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
-        }
-      } else if constexpr (E == 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
-        w[0] = u.x; w[1] = u.y;
-      } else {
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
-      }
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = __bfloat162float(p[i]);
-    }
+    for (int i = 0; i < N; i += 8) ld256(static_cast<const uint32_t*>(p) + i, w + i);
+  } else if constexpr (N == 4) {
+    const uint4 u = *static_cast<const uint4*>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = *static_cast<const uint2*>(p);
+    w[0] = u.x; w[1] = u.y;
   } else {
-    const float* p = static_cast<const float*>(v.data) + e;
-    if (v.wide) {
-      if constexpr (E >= 4) {
+    w[0] = *static_cast<const uint32_t*>(p);
+  }
+}
+template <int N>
+__device__ __forceinline__ void st_words(void* p, const uint32_t* w) {
+  if constexpr (N >= 8) {
 #pragma unroll
-        for (int i = 0; i < E / 4; ++i) {
-          const float4 u = reinterpret_cast<const float4*>(p)[i];
-          x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
-        }
-      } else {
-        const float2 u = *reinterpret_cast<const float2*>(p);
-        x[0] = u.x; x[1] = u.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = p[i];
-    }
+    for (int i = 0; i < N; i += 8) st256(static_cast<uint32_t*>(p) + i, w + i);
+  } else if constexpr (N == 4) {
+    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if constexpr (N == 2) {
+    *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  } else {
+    *static_cast<uint32_t*>(p) = w[0];
   }
 }
 
@@ -64,101 +61,178 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The lane's E values into the row at element `e0`, rounded once (bf16) or as they are.
-template <int E>
-__device__ __forceinline__ void write_row(const RowsView& v, int64_t e0, int lane, const float (&x)[E]) {
+// The lane's part of a row as it lies in memory: E / 2 words of bf16 pairs (BF) or
+// E fp32 words, kept like this while the row before it is worked on.  Without BF
+// a bf16 row is converted as it is loaded.
+template <int E, bool BF>
+struct RawRow {
+  uint32_t w[BF ? E / 2 : E];
+};
+
+// The lane's part of the row at element e0 of the view.
+template <int E, bool BF>
+__device__ __forceinline__ void load_raw(const RowsView& v, int64_t e0, int lane, RawRow<E, BF>& r) {
   const int64_t e = e0 + E * lane;
-  if (v.dtype == KVQ_DT_BF16) {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(v.data) + e;
+  if (BF || v.dtype == KVQ_DT_BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(v.data) + e;
+    uint32_t w[E / 2];
     if (v.wide) {
-      uint32_t w[(E + 1) / 2];
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-      if constexpr (E >= 8) {
-#pragma unroll
-        for (int i = 0; i < E / 8; ++i)
-          reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      } else if constexpr (E == 4) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-      } else {
-        *reinterpret_cast<uint32_t*>(p) = w[0];
-      }
+      ld_words<E / 2>(p, w);
     } else {
 #pragma unroll
-      for (int i = 0; i < E; ++i) p[i] = __float2bfloat16_rn(x[i]);
+      for (int i = 0; i < E / 2; ++i) w[i] = p[2 * i] | static_cast<uint32_t>(p[2 * i + 1]) << 16;
     }
-  } else {
-    float* p = static_cast<float*>(v.data) + e;
-    if (v.wide) {
-      if constexpr (E >= 4) {
 #pragma unroll
-        for (int i = 0; i < E / 4; ++i)
-          reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    for (int i = 0; i < E / 2; ++i) {
+      if constexpr (BF) {
+        r.w[i] = w[i];
       } else {
-        *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+        r.w[2 * i] = w[i] << 16;
+        r.w[2 * i + 1] = w[i] & 0xFFFF0000u;
       }
+    }
+  } else if constexpr (!BF) {
+    const uint32_t* p = static_cast<const uint32_t*>(v.data) + e;
+    if (v.wide) {
+      ld_words<E>(p, r.w);
     } else {
 #pragma unroll
-      for (int i = 0; i < E; ++i) p[i] = x[i];
+      for (int i = 0; i < E; ++i) r.w[i] = p[i];
     }
   }
 }
 
+template <int E, bool BF>
+__device__ __forceinline__ void unpack_row(const RawRow<E, BF>& r, uint64_t (&x)[E / 2]) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i)
+    x[i] = BF ? pk2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u))
+              : pk2(__uint_as_float(r.w[BF ? 0 : 2 * i]), __uint_as_float(r.w[BF ? 0 : 2 * i + 1]));
+}
+
+// The lane's part of the row at element e0, rounded once (bf16) or as it is.
+template <int E>
+__device__ __forceinline__ void write_row(const RowsView& v, int64_t e0, int lane, const uint64_t (&x)[E / 2]) {
+  const int64_t e = e0 + E * lane;
+  float f[E];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) upk2(x[i], f[2 * i], f[2 * i + 1]);
+  if (v.dtype == KVQ_DT_BF16) {
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
+    uint16_t* p = static_cast<uint16_t*>(v.data) + e;
+    if (v.wide) {
+      st_words<E / 2>(p, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        p[2 * i] = static_cast<uint16_t>(w[i]);
+        p[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+      }
+    }
+  } else {
+    float* p = static_cast<float*>(v.data) + e;
+    if (v.wide) {
+      uint32_t w[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) w[i] = __float_as_uint(f[i]);
+      st_words<E>(p, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) p[i] = f[i];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- norm
 // weight + offset of the lane's elements.
 template <int E>
-__device__ __forceinline__ void load_weight(const NormView& n, int lane, float (&w)[E]) {
+__device__ __forceinline__ void load_weight(const NormView& n, int lane, uint64_t (&w)[E / 2]) {
 #pragma unroll
-  for (int i = 0; i < E; ++i) w[i] = __fadd_rn(load_act(n.weight, n.dtype, E * lane + i), n.offset);
+  for (int i = 0; i < E / 2; ++i)
+    w[i] = pk2(__fadd_rn(load_act(n.weight, n.dtype, E * lane + 2 * i), n.offset),
+               __fadd_rn(load_act(n.weight, n.dtype, E * lane + 2 * i + 1), n.offset));
 }
 
 // x * r * w over the warp's row, r = 1 / sqrt(mean(x^2) + eps).  The squares are
-// summed by a pairwise tree (in the lane, then across lanes) in fp32.
+// summed in fp32: a chain of fused adds over the lane's pairs, then across lanes.
 template <int E>
-__device__ __forceinline__ void norm_row(float (&x)[E], const float (&w)[E], float eps) {
-  float s[E];
+__device__ __forceinline__ void norm_row(uint64_t (&x)[E / 2], const uint64_t (&w)[E / 2], float eps) {
+  uint64_t s = mul2(x[0], x[0]);
 #pragma unroll
-  for (int i = 0; i < E; ++i) s[i] = __fmul_rn(x[i], x[i]);
-#pragma unroll
-  for (int h = 1; h < E; h <<= 1)
-#pragma unroll
-    for (int i = 0; i < E; i += 2 * h) s[i] = __fadd_rn(s[i], s[i + h]);
-  float ss = s[0];
+  for (int i = 1; i < E / 2; ++i) s = fma2(x[i], x[i], s);
+  float a, b;
+  upk2(s, a, b);
+  float ss = __fadd_rn(a, b);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
   const float r = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / (32 * E)), eps));
+  const uint64_t r2 = pk2(r, r);
 #pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
+  for (int i = 0; i < E / 2; ++i) x[i] = mul2(mul2(x[i], r2), w[i]);
 }
 
-// blockdiag(H32) over the warp's row: the butterfly's stages h < E pair registers,
-// the others pair lanes; the same operations on the same operands, in the same
-// stage order, as warp_fwht32 (lane i's value x[i]).
+// ---------------------------------------------------------------- row transforms
+// Butterfly stages at element distances 1 .. E / 2, in the lane.
 template <int E>
-__device__ __forceinline__ void rotate_row_had32(float (&x)[E], int lane) {
+__device__ __forceinline__ void lane_butterfly(uint64_t (&x)[E / 2]) {
 #pragma unroll
-  for (int h = 1; h < E; h <<= 1)
+  for (int i = 0; i < E / 2; ++i) {  // distance 1: the halves of a pair
+    float a, b;
+    upk2(x[i], a, b);
+    x[i] = pk2(__fadd_rn(a, b), __fsub_rn(a, b));
+  }
 #pragma unroll
-    for (int i = 0; i < E; ++i)
+  for (int h = 1; h < E / 2; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
       if (!(i & h)) {
-        const float a = x[i], b = x[i + h];
-        x[i] = __fadd_rn(a, b);
-        x[i + h] = __fsub_rn(a, b);
+        const uint64_t a = x[i], b = x[i + h];
+        x[i] = add2(a, b);
+        x[i + h] = sub2(a, b);
       }
+}
+
+// Stages across lanes: partners o = 1 .. LANES / 2 lanes apart.
+template <int E, int LANES>
+__device__ __forceinline__ void cross_butterfly(uint64_t (&x)[E / 2], int lane) {
 #pragma unroll
-  for (int o = 1; o < 32 / E; o <<= 1)
+  for (int o = 1; o < LANES; o <<= 1) {
+    const float sgn = (lane & o) ? -1.0f : 1.0f;
+    const uint64_t s2 = pk2(sgn, sgn);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float p = __shfl_xor_sync(0xffffffffu, x[i], o);
-      x[i] = (lane & o) ? __fsub_rn(p, x[i]) : __fadd_rn(x[i], p);
+    for (int i = 0; i < E / 2; ++i) {
+      float a, b;
+      upk2(x[i], a, b);
+      const uint64_t p = pk2(__shfl_xor_sync(0xffffffffu, a, o), __shfl_xor_sync(0xffffffffu, b, o));
+      x[i] = fma2(x[i], s2, p);
     }
+  }
+}
+
+// blockdiag(H32) over the warp's row (warp_fwht32's stages and scale).
+template <int E>
+__device__ __forceinline__ void rotate_row_had32(uint64_t (&x)[E / 2], int lane) {
+  lane_butterfly<E>(x);
+  cross_butterfly<E, 32 / E>(x, lane);
+  const uint64_t c2 = pk2(kHadamardScale, kHadamardScale);
 #pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = __fmul_rn(x[i], kHadamardScale);
+  for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c2);
 }
 
 // The 4-bit codes (element i of the lane in nibble i) of the lane's part of its
-// group, and the group's fp16 scale: q4_group_code_warp's arithmetic in this layout.
-template <int E>
-__device__ __forceinline__ uint32_t q4_row_codes(const float (&y)[E], __half& s16) {
+// group, and the group's fp16 scale: q4_group_code_warp's arithmetic in this
+// layout.  ROT: rotated values, whose groups hold no NaN beside finite values; all
+// of a lane's codes then come from one packed estimate
+//   t = min(fl(y * rcp(s) + 8), 15), u = fl(t + 1.5 * 2^23)
+// (u's low mantissa bits hold rint_even(t)), taken when every t lies farther than
+// the screen from a half-integer; t >= -1/2 for an fp16-normal, unsaturated scale.
+template <int E, bool ROT>
+__device__ __forceinline__ uint32_t q4_row_codes(const uint64_t (&x)[E / 2], __half& s16) {
+  float y[E];
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) upk2(x[i], y[2 * i], y[2 * i + 1]);
   float amax = fabsf(y[0]);
 #pragma unroll
   for (int i = 1; i < E; ++i) amax = fmaxf(amax, fabsf(y[i]));
@@ -167,12 +241,31 @@ __device__ __forceinline__ uint32_t q4_row_codes(const float (&y)[E], __half& s1
   s16 = __float2half_rn(__fmul_rn(amax, 0.125f));
   if (__hisinf(s16)) s16 = __ushort_as_half(0x7BFFu);  // saturate to 65504
   const float s = __half2float(s16);
+  if (s == 0.0f) return 0x88888888u >> (32 - 4 * E);  // every code 8
   uint32_t word = 0;
   const float r = rcp_approx(s);
+  if (ROT && s >= 6.103515625e-05f && s < 65504.0f) {  // (false for NaN)
+    const uint64_t r2 = pk2(r, r), e2 = pk2(8.0f, 8.0f), m2 = pk2(12582912.0f, 12582912.0f);
+    float dmax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+      float ta, tb, da, db, ua, ub;
+      upk2(fma2(x[i], r2, e2), ta, tb);
+      const uint64_t t2 = pk2(fminf(ta, 15.0f), fminf(tb, 15.0f));
+      const uint64_t u2 = add2(t2, m2);
+      upk2(sub2(t2, sub2(u2, m2)), da, db);
+      dmax = fmaxf(dmax, fmaxf(fabsf(da), fabsf(db)));
+      upk2(u2, ua, ub);
+      word = put_nibble(word, __float_as_uint(ua), 2 * i);
+      word = put_nibble(word, __float_as_uint(ub), 2 * i + 1);
+    }
+    if (dmax < kQ4Screen) return word;
+    word = 0;
+  }
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    uint32_t code = 8;
-    if (s != 0.0f && !q4_code_screened(y[i], r, code)) code = q4_code_exact(y[i], s);
+    uint32_t code;
+    if (!q4_code_screened(y[i], r, code)) code = q4_code_exact(y[i], s);
     word = put_nibble(word, code, i);
   }
   return word;

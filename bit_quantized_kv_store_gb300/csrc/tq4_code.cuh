@@ -6,6 +6,7 @@
 // floating-point operation is an explicit IEEE-rounded intrinsic.
 #pragma once
 #include "common.cuh"
+#include "rows.cuh"
 
 namespace kvq {
 
@@ -60,6 +61,22 @@ template <int E>
 __device__ __forceinline__ uint32_t lane_signs(const void* signs, int lane) {
   const uint32_t w = static_cast<const uint32_t*>(signs)[(E * lane) >> 5];
   return w >> ((E * lane) & 31);
+}
+
+// tq4_transform (forward) on a row in packed pairs: the same operations.
+template <int E>
+__device__ __forceinline__ void rotate_row_tq4(uint64_t (&x)[E / 2], uint32_t sw, int lane) {
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) {
+    float a, b;
+    upk2(x[i], a, b);
+    x[i] = pk2((sw >> (2 * i)) & 1u ? -a : a, (sw >> (2 * i + 1)) & 1u ? -b : b);
+  }
+  lane_butterfly<E>(x);
+  cross_butterfly<E, 32>(x, lane);
+  const uint64_t c2 = pk2(tq4_row_scale<E>(), tq4_row_scale<E>());
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c2);
 }
 
 // The codes (element i of the lane in nibble i) and the fp16 scale of the warp's

@@ -600,10 +600,26 @@ def test_decode_diff_head_layouts_and_batches(K, Hk, group):
         assert torch.isnan(out[[3, 50]]).all()
         keep = [i for i in range(100) if i not in (3, 50)]
         assert torch.equal(out[keep], want[keep])
-    # alone or in the batch: the same bits
+    # alone or in the batch: the same bits (in the batch one CTA takes a head; alone with a long table, eight)
     one = K.decode_diff(cache, q[7:8].contiguous(), sl[7:8].contiguous(), bt[7:8].contiguous(), T, 1 / 16,
                         K.alloc_workspace(cache, 1, Hk * group, T), lam[7:8])
     assert torch.equal(one[0], good[7])
+
+
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "TQ4"])
+@pytest.mark.parametrize("longest", [60000, 140000, 600000])
+def test_both_arrangements_of_the_merge_agree(K, fmt, longest):
+    """One CTA for a head (many heads, or few partitions) and eight (a long
+    sequence's few heads) give the same bits, with and without the norm."""
+    lens = [longest, 3, 513, longest - 700] + [900] * 9
+    cache, q, sl, bt, T, ws = diff_problem(K, getattr(K, "FMT_" + fmt), lens)
+    lam = torch.rand(len(lens), 12, device=DEV)
+    for norm in (None, K.Norm(torch.rand(256, device=DEV), 1e-5)):
+        many = K.decode_diff(cache, q, sl, bt, T, 1 / 16, ws, lam, norm=norm)
+        for b in (0, 1, 2, 3):
+            few = K.decode_diff(cache, q[b:b + 1].contiguous(), sl[b:b + 1].contiguous(), bt[b:b + 1].contiguous(), T,
+                                1 / 16, K.alloc_workspace(cache, 1, 24, T), lam[b:b + 1], norm=norm)
+            assert torch.equal(few[0], many[b])
 
 
 def test_merge_diff_of_a_window_and_a_gather(K):
