@@ -468,9 +468,18 @@ def _three(t, what):
 def _new(shape, dtype, like, stream):
     """An output tensor that belongs to the stream it is written on."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _new_rows(n, heads, width, dtype, like, stream):
+    """A new contiguous tensor [n, heads, width] and its kvq_rows."""
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"kvq: an output must be fp32 or bf16, got {dtype}")
+    t = _new((n, heads, width), dtype, like, stream)
+    return t, RowsDesc(t.data_ptr(), code, heads, heads * width, width)
 
 
 def _launch_stream(stream, dev):
@@ -544,14 +553,16 @@ def norm_rope(x, positions=None, rope=None, norm=None, out=None, dtype=None, sta
     """Norm and rotary positions of rows x [tokens, heads, width] (any strides with a
     contiguous last dimension) in one pass; returns out (default: a new tensor of
     `dtype`, x's own if None).  out may be x."""
-    n, heads, width = shape = _three(x, "x")
+    n, heads, width = _three(x, "x")
     dev = _device(x)
+    rx = _rows(x, "x", dev, n, heads, width)
     if out is None:
-        out = _new(shape, dtype or x.dtype, x, stream)
+        out, ry = _new_rows(n, heads, width, dtype or x.dtype, x, stream)
+    else:
+        ry = _rows(out, "out", dev, n, heads, width)
     ref, pos, ps = _rope_args(rope, positions, dev, n)
-    _check(lib().kvq_norm_rope(_rows(x, "x", dev, n, heads, width), _rows(out, "out", dev, n, heads, width), n, width,
-                               _norm_ref(norm, "norm", dev, width), ref, pos, ps, _status_at(status, dev),
-                               _launch_stream(stream, dev)), "kvq_norm_rope")
+    _check(lib().kvq_norm_rope(rx, ry, n, width, _norm_ref(norm, "norm", dev, width), ref, pos, ps,
+                               _status_at(status, dev), _launch_stream(stream, dev)), "kvq_norm_rope")
     return out
 
 
@@ -570,8 +581,9 @@ def norm_rope_store(cache: Cache, q, k, v, slot_mapping, positions=None, rope=No
         Hq = _three(q, "q")[1]
         rq = _rows(q, "q", dev, n, Hq, D)
         if q_out is None:
-            q_out = _new((n, Hq, D), torch.float32, q, stream)
-        ro = _rows(q_out, "q_out", dev, n, Hq, D)
+            q_out, ro = _new_rows(n, Hq, D, torch.float32, q, stream)
+        else:
+            ro = _rows(q_out, "q_out", dev, n, Hq, D)
     elif q_out is not None:
         raise ValueError("kvq: q_out without q")
     ref, pos, ps = _rope_args(rope, positions, dev, n)
@@ -587,8 +599,9 @@ def _load_outputs(cache, n, k, v, dtype, like, dev, stream):
     fp8 = cache.fmt == FMT_FP8_ROW
     Hk, width = cache.Hk, cache.D + cache.rope if fp8 else cache.D
     if k is None and v is None:
-        k = _new((n, Hk, width), dtype, like, stream)
-        v = None if fp8 else _new((n, Hk, width), dtype, like, stream)
+        k, rk = _new_rows(n, Hk, width, dtype, like, stream)
+        v, rv = (None, None) if fp8 else _new_rows(n, Hk, width, dtype, like, stream)
+        return k, v, rk, rv
     return (k, v, None if k is None else _rows(k, "k", dev, n, Hk, width),
             None if v is None else _rows(v, "v", dev, n, Hk, width))
 

@@ -647,12 +647,12 @@ static bool rows_distinct(const kvq_rows* r, int64_t n_tok, int32_t width) {
 }
 
 static int32_t check_norm(const kvq_norm* n, NormView* v) {
-  *v = NormView{nullptr, 0, 0.f, 0.f};
+  *v = NormView{nullptr, 0, 0.f, 0.f, 0};
   if (!n) return KVQ_OK;
   if (!n->weight || !dtype_ok(n->dtype) || !(n->eps > 0.f) || !(n->eps < INFINITY) || !(fabsf(n->offset) < INFINITY))
     return KVQ_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(n->weight) % (n->dtype == KVQ_DT_F32 ? 4 : 2) != 0) return KVQ_ERR_INVALID_ARG;
-  *v = NormView{n->weight, n->dtype, n->eps, n->offset};
+  *v = NormView{n->weight, n->dtype, n->eps, n->offset, reinterpret_cast<uintptr_t>(n->weight) % 32 == 0 ? 1 : 0};
   return KVQ_OK;
 }
 
@@ -664,7 +664,7 @@ static int32_t check_rope(const kvq_rope* r, int32_t width, const int32_t* pos, 
   if (r->rot_dim < 2 || r->rot_dim % 2 != 0 || r->rot_dim > width || r->num_axes < 1 || r->num_axes > 4 ||
       r->reserved != 0 || !r->table || reinterpret_cast<uintptr_t>(r->table) % 8 != 0)
     return KVQ_ERR_INVALID_ARG;
-  if (r->rot_dim > 256 || (!r->interleaved && r->rot_dim % (width / 16) != 0)) return KVQ_ERR_UNSUPPORTED;
+  if (r->rot_dim > 256 || (!r->interleaved && r->rot_dim % 16 != 0)) return KVQ_ERR_UNSUPPORTED;
   if (!pos || reinterpret_cast<uintptr_t>(pos) % 4 != 0 || (r->num_axes > 1 && pos_stride < n_tok))
     return KVQ_ERR_INVALID_ARG;
   *v = RopeView{r->table, pos, pos_stride, r->rot_dim, r->interleaved, r->num_axes};

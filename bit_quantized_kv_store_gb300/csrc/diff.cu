@@ -55,13 +55,13 @@ __device__ __forceinline__ void finish_head(const MergeArgs& a, const DiffView& 
   for (int i = 0; i < E; ++i) x[i] = all[E * lane + i];
   if (a.rotate_back == 2) tq4_transform<E>(x, lane_signs<E>(signs, lane), lane, true);
   if (d.norm.weight) {
-    uint64_t p[E / 2], w[E / 2];
+    uint64_t p[1][E / 2], w[E / 2];
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) p[i] = pk2(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < E / 2; ++i) p[0][i] = pk2(x[2 * i], x[2 * i + 1]);
     load_weight<E>(d.norm, lane, w);
-    norm_row<E>(p, w, d.norm.eps);
+    norm_rows<E, 32, 1>(p, w, d.norm.eps);
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) upk2(p[i], x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < E / 2; ++i) upk2(p[0][i], x[2 * i], x[2 * i + 1]);
   }
 #pragma unroll
   for (int i = 0; i < E; ++i) x[i] *= d.scale;
@@ -294,14 +294,15 @@ __global__ void __launch_bounds__(256) diff_heads_kernel(const float* __restrict
   load_raw<E, false>(in, 2 * i * W, lane, r1);
   load_raw<E, false>(in, (2 * i + 1) * W, lane, r2);
   const float lam = d.lambda[row * d.stride + h];
-  uint64_t p[E / 2], q[E / 2];
+  uint64_t p1[1][E / 2], q[E / 2];
+  uint64_t(&p)[E / 2] = p1[0];
   unpack_row<E, false>(r1, p);
   unpack_row<E, false>(r2, q);
 #pragma unroll
   for (int j = 0; j < E / 2; ++j) p[j] = fma2(pk2(-lam, -lam), q[j], p[j]);
   if (d.norm.weight) {
     load_weight<E>(d.norm, lane, q);
-    norm_row<E>(p, q, d.norm.eps);
+    norm_rows<E, 32, 1>(p1, q, d.norm.eps);
   }
 #pragma unroll
   for (int j = 0; j < E / 2; ++j) p[j] = mul2(p[j], pk2(d.scale, d.scale));
@@ -316,7 +317,7 @@ cudaError_t launch_merge_diff(const MergeArgs& a, const DiffView& d, const kvq_c
   // partitions; 8 CTAs for each head of a long sequence.
   const int64_t heads = (int64_t)(a.Hq / 2) * B, n_sm = device_sm_count();
   cudaError_t e;
-  if (a.P <= kRowMaxP && (a.P <= 96 || 2 * heads >= n_sm)) {
+  if (a.P <= kRowMaxP && (a.P <= 32 || 2 * heads >= n_sm)) {
     e = a.P <= 32 ? launch_row<1>(a, d, c.signs, B, s) : launch_row<2>(a, d, c.signs, B, s);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();

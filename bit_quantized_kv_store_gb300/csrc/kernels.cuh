@@ -121,6 +121,7 @@ struct NormView {
   const void* weight;
   int dtype;
   float eps, offset;
+  int wide;  // 1: the weight starts on a 32-byte boundary
 };
 
 // A kvq_rope with its positions; rot 0: no rotation.
@@ -142,7 +143,7 @@ struct NormRopeArgs {
   int64_t n_tok;
   int Hq, Hk;
   int rotate;  // 1: queries into the cache's space
-  int hpw;     // heads a warp takes (set by the launch)
+  int hpw;     // batches of heads a warp takes (set by the launch)
   int plane_wide;  // BF16: the planes start on 32-byte boundaries
   FastDiv ps;  // page_size
 };

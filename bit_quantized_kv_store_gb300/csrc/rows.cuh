@@ -1,8 +1,9 @@
-// rows.cuh -- strided activation rows in a warp's registers: lane l holds elements
-// E l .. E l + E - 1 of a row of 32 E values, as E / 2 packed fp32 pairs (element
-// 2i in the low half of pair i).  Loads and stores of bf16 and fp32 rows, the
-// per-row norm, the caches' row transforms and the 4-bit codes in this layout (a
-// group of 32 values spans 32 / E lanes).  The transforms perform the operations
+// rows.cuh -- strided activation rows in a warp's registers: a row of E LPR values
+// lies over LPR lanes (a warp, or an aligned part of one), its lane l holding
+// elements E l .. E l + E - 1 as E / 2 packed fp32 pairs (element 2i in the low
+// half of pair i).  Loads and stores of bf16 and fp32 rows, the per-row norm, the
+// caches' row transforms and the 4-bit codes in this layout (a group of 32 values
+// spans 32 / E lanes).  The transforms perform the operations
 // of the store's butterflies on the same operands (two per packed instruction;
 // across lanes p + x * (+-1), one rounding), so the stored bytes are the same.
 #pragma once
@@ -69,14 +70,13 @@ struct RawRow {
   uint32_t w[BF ? E / 2 : E];
 };
 
-// The lane's part of the row at element e0 of the view.
+// The lane's part of a row from its address there (`wide`, `dtype`: the row's view's).
 template <int E, bool BF>
-__device__ __forceinline__ void load_raw(const RowsView& v, int64_t e0, int lane, RawRow<E, BF>& r) {
-  const int64_t e = e0 + E * lane;
-  if (BF || v.dtype == KVQ_DT_BF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(v.data) + e;
+__device__ __forceinline__ void load_raw_at(const void* at, int dtype, int wide, RawRow<E, BF>& r) {
+  if (BF || dtype == KVQ_DT_BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(at);
     uint32_t w[E / 2];
-    if (v.wide) {
+    if (wide) {
       ld_words<E / 2>(p, w);
     } else {
 #pragma unroll
@@ -92,14 +92,25 @@ __device__ __forceinline__ void load_raw(const RowsView& v, int64_t e0, int lane
       }
     }
   } else if constexpr (!BF) {
-    const uint32_t* p = static_cast<const uint32_t*>(v.data) + e;
-    if (v.wide) {
+    const uint32_t* p = static_cast<const uint32_t*>(at);
+    if (wide) {
       ld_words<E>(p, r.w);
     } else {
 #pragma unroll
       for (int i = 0; i < E; ++i) r.w[i] = p[i];
     }
   }
+}
+
+// Address of element e of a view's data.
+__device__ __forceinline__ uint8_t* element_at(const RowsView& v, int64_t e) {
+  return static_cast<uint8_t*>(v.data) + (e << (v.dtype == KVQ_DT_BF16 ? 1 : 2));
+}
+
+// The lane's part of the row at element e0 of the view.
+template <int E, bool BF>
+__device__ __forceinline__ void load_raw(const RowsView& v, int64_t e0, int lane, RawRow<E, BF>& r) {
+  load_raw_at<E, BF>(element_at(v, e0 + E * lane), v.dtype, v.wide, r);
 }
 
 template <int E, bool BF>
@@ -110,67 +121,89 @@ __device__ __forceinline__ void unpack_row(const RawRow<E, BF>& r, uint64_t (&x)
               : pk2(__uint_as_float(r.w[BF ? 0 : 2 * i]), __uint_as_float(r.w[BF ? 0 : 2 * i + 1]));
 }
 
-// The lane's part of the row at element e0, rounded once (bf16) or as it is.
+// The lane's part of a row to its address there, rounded once (bf16) or as it is.
 template <int E>
-__device__ __forceinline__ void write_row(const RowsView& v, int64_t e0, int lane, const uint64_t (&x)[E / 2]) {
-  const int64_t e = e0 + E * lane;
+__device__ __forceinline__ void write_row_at(void* at, int dtype, int wide, const uint64_t (&x)[E / 2]) {
   float f[E];
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) upk2(x[i], f[2 * i], f[2 * i + 1]);
-  if (v.dtype == KVQ_DT_BF16) {
+  if (dtype == KVQ_DT_BF16) {
     uint32_t w[E / 2];
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) w[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-    uint16_t* p = static_cast<uint16_t*>(v.data) + e;
-    if (v.wide) {
-      st_words<E / 2>(p, w);
+    if (wide) {
+      st_words<E / 2>(at, w);
     } else {
+      uint16_t* p = static_cast<uint16_t*>(at);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
         p[2 * i] = static_cast<uint16_t>(w[i]);
         p[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
       }
     }
+  } else if (wide) {
+    uint32_t w[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) w[i] = __float_as_uint(f[i]);
+    st_words<E>(at, w);
   } else {
-    float* p = static_cast<float*>(v.data) + e;
-    if (v.wide) {
-      uint32_t w[E];
 #pragma unroll
-      for (int i = 0; i < E; ++i) w[i] = __float_as_uint(f[i]);
-      st_words<E>(p, w);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) p[i] = f[i];
-    }
+    for (int i = 0; i < E; ++i) static_cast<float*>(at)[i] = f[i];
   }
 }
 
-// ---------------------------------------------------------------- norm
-// weight + offset of the lane's elements.
+// The lane's part of the row at element e0 of the view.
 template <int E>
-__device__ __forceinline__ void load_weight(const NormView& n, int lane, uint64_t (&w)[E / 2]) {
-#pragma unroll
-  for (int i = 0; i < E / 2; ++i)
-    w[i] = pk2(__fadd_rn(load_act(n.weight, n.dtype, E * lane + 2 * i), n.offset),
-               __fadd_rn(load_act(n.weight, n.dtype, E * lane + 2 * i + 1), n.offset));
+__device__ __forceinline__ void write_row(const RowsView& v, int64_t e0, int lane, const uint64_t (&x)[E / 2]) {
+  write_row_at<E>(element_at(v, e0 + E * lane), v.dtype, v.wide, x);
 }
 
-// x * r * w over the warp's row, r = 1 / sqrt(mean(x^2) + eps).  The squares are
-// summed in fp32: a chain of fused adds over the lane's pairs, then across lanes.
+// ---------------------------------------------------------------- norm
+// weight + offset of the lane's elements (n.wide: on a 32-byte boundary).
 template <int E>
-__device__ __forceinline__ void norm_row(uint64_t (&x)[E / 2], const uint64_t (&w)[E / 2], float eps) {
-  uint64_t s = mul2(x[0], x[0]);
+__device__ __forceinline__ void load_weight(const NormView& n, int lane, uint64_t (&w)[E / 2]) {
+  const RowsView v{const_cast<void*>(n.weight), 0, 0, n.dtype, n.wide};
+  RawRow<E, false> r;
+  load_raw<E, false>(v, 0, lane, r);
+  unpack_row<E, false>(r, w);
+  const uint64_t o2 = pk2(n.offset, n.offset);
 #pragma unroll
-  for (int i = 1; i < E / 2; ++i) s = fma2(x[i], x[i], s);
-  float a, b;
-  upk2(s, a, b);
-  float ss = __fadd_rn(a, b);
+  for (int i = 0; i < E / 2; ++i) w[i] = add2(w[i], o2);
+}
+
+// x * r * w over the row's LPR lanes, r = 1 / sqrt(mean(x^2) + eps), for U rows side
+// by side.  The squares are summed in fp32: two chains of fused adds over the
+// lane's pairs, then across lanes.
+template <int E, int LPR, int U>
+__device__ __forceinline__ void norm_rows(uint64_t (&x)[U][E / 2], const uint64_t (&w)[E / 2], float eps) {
+  float ss[U];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
-  const float r = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / (32 * E)), eps));
-  const uint64_t r2 = pk2(r, r);
+  for (int u = 0; u < U; ++u) {
+    uint64_t s = mul2(x[u][0], x[u][0]);
+    if constexpr (E >= 4) {
+      uint64_t t = mul2(x[u][1], x[u][1]);
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) x[i] = mul2(mul2(x[i], r2), w[i]);
+      for (int i = 2; i < E / 2; i += 2) {
+        s = fma2(x[u][i], x[u][i], s);
+        t = fma2(x[u][i + 1], x[u][i + 1], t);
+      }
+      s = add2(s, t);
+    }
+    float a, b;
+    upk2(s, a, b);
+    ss[u] = __fadd_rn(a, b);
+  }
+#pragma unroll
+  for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+    for (int u = 0; u < U; ++u) ss[u] = __fadd_rn(ss[u], __shfl_xor_sync(0xffffffffu, ss[u], o));
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float r = rsqrtf(__fadd_rn(__fmul_rn(ss[u], 1.0f / (LPR * E)), eps));
+    const uint64_t r2 = pk2(r, r);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) x[u][i] = mul2(mul2(x[u][i], r2), w[i]);
+  }
 }
 
 // ---------------------------------------------------------------- row transforms
@@ -221,15 +254,15 @@ __device__ __forceinline__ void rotate_row_had32(uint64_t (&x)[E / 2], int lane)
   for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c2);
 }
 
-// The 4-bit codes (element i of the lane in nibble i) of the lane's part of its
-// group, and the group's fp16 scale: q4_group_code_warp's arithmetic in this
+// The 4-bit codes (element 8q + i of the lane in nibble i of word[q]; E <= 8: all in
+// word[0]) of the lane's part of its group, and the group's fp16 scale: q4_group_code_warp's arithmetic in this
 // layout.  ROT: rotated values, whose groups hold no NaN beside finite values; all
 // of a lane's codes then come from one packed estimate
 //   t = min(fl(y * rcp(s) + 8), 15), u = fl(t + 1.5 * 2^23)
 // (u's low mantissa bits hold rint_even(t)), taken when every t lies farther than
 // the screen from a half-integer; t >= -1/2 for an fp16-normal, unsaturated scale.
 template <int E, bool ROT>
-__device__ __forceinline__ uint32_t q4_row_codes(const uint64_t (&x)[E / 2], __half& s16) {
+__device__ __forceinline__ void q4_row_codes(const uint64_t (&x)[E / 2], uint32_t (&word)[(E + 7) / 8], __half& s16) {
   float y[E];
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) upk2(x[i], y[2 * i], y[2 * i + 1]);
@@ -241,8 +274,9 @@ __device__ __forceinline__ uint32_t q4_row_codes(const uint64_t (&x)[E / 2], __h
   s16 = __float2half_rn(__fmul_rn(amax, 0.125f));
   if (__hisinf(s16)) s16 = __ushort_as_half(0x7BFFu);  // saturate to 65504
   const float s = __half2float(s16);
-  if (s == 0.0f) return 0x88888888u >> (32 - 4 * E);  // every code 8
-  uint32_t word = 0;
+#pragma unroll
+  for (int q = 0; q < (E + 7) / 8; ++q) word[q] = 0x88888888u;  // scale 0: every code 8
+  if (s == 0.0f) return;
   const float r = rcp_approx(s);
   if (ROT && s >= 6.103515625e-05f && s < 65504.0f) {  // (false for NaN)
     const uint64_t r2 = pk2(r, r), e2 = pk2(8.0f, 8.0f), m2 = pk2(12582912.0f, 12582912.0f);
@@ -256,19 +290,33 @@ __device__ __forceinline__ uint32_t q4_row_codes(const uint64_t (&x)[E / 2], __h
       upk2(sub2(t2, sub2(u2, m2)), da, db);
       dmax = fmaxf(dmax, fmaxf(fabsf(da), fabsf(db)));
       upk2(u2, ua, ub);
-      word = put_nibble(word, __float_as_uint(ua), 2 * i);
-      word = put_nibble(word, __float_as_uint(ub), 2 * i + 1);
+      word[i >> 2] = put_nibble(word[i >> 2], __float_as_uint(ua), 2 * (i & 3));
+      word[i >> 2] = put_nibble(word[i >> 2], __float_as_uint(ub), 2 * (i & 3) + 1);
     }
-    if (dmax < kQ4Screen) return word;
-    word = 0;
+    if (dmax < kQ4Screen) return;
   }
+  // value by value: the screened estimate, and the IEEE division for those it leaves
+  // open, in a loop (rare, and sixteen divisions in a row would take registers from
+  // the rest of the kernel)
+  uint32_t open = 0;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     uint32_t code;
-    if (!q4_code_screened(y[i], r, code)) code = q4_code_exact(y[i], s);
-    word = put_nibble(word, code, i);
+    if (!q4_code_screened(y[i], r, code)) open |= 1u << i;
+    word[i >> 3] = put_nibble(word[i >> 3], code, i & 7);
   }
-  return word;
+  while (open) {
+    const int i = __ffs(open) - 1;
+    open &= open - 1;
+    float v = y[0];
+#pragma unroll
+    for (int j = 1; j < E; ++j)
+      if (j == i) v = y[j];
+    const uint32_t code = q4_code_exact(v, s);
+#pragma unroll
+    for (int q = 0; q < (E + 7) / 8; ++q)
+      if (i >> 3 == q) word[q] = put_nibble(word[q], code, i & 7);
+  }
 }
 
 }  // namespace kvq

@@ -50,9 +50,10 @@ __global__ void __launch_bounds__(256) store_tq4_kernel(kvq_cache c, const void*
   tq4_transform<E>(y, lane_signs<E>(c.signs, lane), lane, false);
 
   __half s16;
-  const uint32_t word = tq4_row_codes<E>(y, s16);
+  uint32_t word[1];
+  tq4_row_codes<E, 32>(y, word, s16);
   uint8_t* codes = static_cast<uint8_t*>(kv ? c.v : c.k) + r * (D / 2) + lane * (E / 2);
-  tq4_write_codes<E>(codes, word);
+  write_codes<E>(codes, word);
   if (lane == 0) static_cast<__half*>(kv ? c.v_scale : c.k_scale)[r] = s16;
 }
 

@@ -1,8 +1,8 @@
 // tq4_code.cuh -- the TQ4 rows' signed row transform and the codes and scale of one
-// transformed row across a warp, shared by the kernels that store such rows.  Lane
-// l holds elements E l .. E l + E - 1 (E = D / 32), so the butterfly's first
-// log2(E) stages run in registers and the other five across lanes, and the
-// pairwise tree of the sum of squares is the warp's xor reduction.  Every
+// transformed row across a warp (or an aligned part of one), shared by the kernels
+// that store such rows.  Lane l of the row holds elements E l .. E l + E - 1, so
+// the butterfly's first log2(E) stages run in registers and the others across
+// lanes, and the pairwise tree of the sum of squares is the lanes' xor reduction.  Every
 // floating-point operation is an explicit IEEE-rounded intrinsic.
 #pragma once
 #include "common.cuh"
@@ -63,8 +63,8 @@ __device__ __forceinline__ uint32_t lane_signs(const void* signs, int lane) {
   return w >> ((E * lane) & 31);
 }
 
-// tq4_transform (forward) on a row in packed pairs: the same operations.
-template <int E>
+// tq4_transform (forward) on a row of LPR lanes in packed pairs: the same operations.
+template <int E, int LPR>
 __device__ __forceinline__ void rotate_row_tq4(uint64_t (&x)[E / 2], uint32_t sw, int lane) {
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) {
@@ -73,17 +73,18 @@ __device__ __forceinline__ void rotate_row_tq4(uint64_t (&x)[E / 2], uint32_t sw
     x[i] = pk2((sw >> (2 * i)) & 1u ? -a : a, (sw >> (2 * i + 1)) & 1u ? -b : b);
   }
   lane_butterfly<E>(x);
-  cross_butterfly<E, 32>(x, lane);
-  const uint64_t c2 = pk2(tq4_row_scale<E>(), tq4_row_scale<E>());
+  cross_butterfly<E, LPR>(x, lane);
+  constexpr float c = tq4_row_scale<E * LPR / 32>();
+  const uint64_t c2 = pk2(c, c);
 #pragma unroll
   for (int i = 0; i < E / 2; ++i) x[i] = mul2(x[i], c2);
 }
 
-// The codes (element i of the lane in nibble i) and the fp16 scale of the warp's
-// transformed row y.
-template <int E>
-__device__ __forceinline__ uint32_t tq4_row_codes(const float (&y)[E], __half& s16_out) {
-  constexpr int D = 32 * E;
+// The codes (element 8q + i of the lane in nibble i of word[q]) and the fp16 scale of
+// the transformed row y of LPR lanes.
+template <int E, int LPR>
+__device__ __forceinline__ void tq4_row_codes(const float (&y)[E], uint32_t (&word)[(E + 7) / 8], __half& s16_out) {
+  constexpr int D = LPR * E;
   // sum of squares by the pairwise tree: in-lane stages, then the xor reduction
   float q2[E];
 #pragma unroll
@@ -94,12 +95,13 @@ __device__ __forceinline__ uint32_t tq4_row_codes(const float (&y)[E], __half& s
     for (int i = 0; i < E; i += 2 * h) q2[i] = __fadd_rn(q2[i], q2[i + h]);
   float ss = q2[0];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
+  for (int o = 1; o < LPR; o <<= 1) ss = __fadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, o));
   __half s16 = __float2half_rn(__fsqrt_rn(__fmul_rn(ss, 1.0f / D)));
   if (__hisinf(s16)) s16 = __ushort_as_half(0x7BFFu);  // saturate to 65504
   const float s = __half2float(s16);
 
-  uint32_t word = 0;
+#pragma unroll
+  for (int q = 0; q < (E + 7) / 8; ++q) word[q] = 0;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     uint32_t code = 0;
@@ -111,21 +113,22 @@ __device__ __forceinline__ uint32_t tq4_row_codes(const float (&y)[E], __half& s
       for (int j = 0; j < 7; ++j) m += a > tq4_mid(j) ? 1u : 0u;
       code = (q < 0.0f ? 8u : 0u) | m;
     }
-    word |= code << (4 * i);
+    word[i >> 3] |= code << (4 * (i & 7));
   }
   s16_out = s16;
-  return word;
 }
 
 // Write the lane's E codes into its row of the codes plane.
 template <int E>
-__device__ __forceinline__ void tq4_write_codes(uint8_t* codes, uint32_t word) {
-  if constexpr (E == 8) {
-    *reinterpret_cast<uint32_t*>(codes) = word;
+__device__ __forceinline__ void write_codes(uint8_t* codes, const uint32_t (&word)[(E + 7) / 8]) {
+  if constexpr (E == 16) {
+    *reinterpret_cast<uint2*>(codes) = make_uint2(word[0], word[1]);
+  } else if constexpr (E == 8) {
+    *reinterpret_cast<uint32_t*>(codes) = word[0];
   } else if constexpr (E == 4) {
-    *reinterpret_cast<uint16_t*>(codes) = static_cast<uint16_t>(word);
+    *reinterpret_cast<uint16_t*>(codes) = static_cast<uint16_t>(word[0]);
   } else {
-    *codes = static_cast<uint8_t>(word);
+    *codes = static_cast<uint8_t>(word[0]);
   }
 }
 

@@ -448,7 +448,7 @@ typedef struct kvq_norm {
  * two bits, so that the angle of any int32 position, also a negative one, is one
  * 64-bit multiply that wraps exactly (kvq_rope_table makes the words). */
 typedef struct kvq_rope {
-  int32_t rot_dim;       /* even, 2 .. min(256, width); a multiple of width / 16 unless interleaved */
+  int32_t rot_dim;       /* even, 2 .. min(256, width); a multiple of 16 unless interleaved */
   int32_t interleaved;   /* 0 or 1 */
   int32_t num_axes;      /* 1 .. 4 (time, height, width, ...) */
   int32_t reserved;      /* 0 */

@@ -97,7 +97,7 @@ def test_norm_rope_refusals(K):
     for bad in (rope(K, rot=0), rope(K, rot=63), rope(K, rot=258), rope(K, axes=0), rope(K, axes=5), rope(K, inter=2),
                 rope(K, ptr=0), rope(K, ptr=DUMMY + 4), rope(K, reserved=1)):
         assert call(rp=bad) == K.ERR_INVALID_ARG
-    assert call(rp=rope(K, rot=40)) == K.ERR_UNSUPPORTED                 # half-split: a multiple of width / 16
+    assert call(rp=rope(K, rot=40)) == K.ERR_UNSUPPORTED                 # half-split: a multiple of 16
     assert call(rp=rope(K, rot=288), w=512) == K.ERR_UNSUPPORTED
     assert call(rp=rope(K), pos=None) == K.ERR_INVALID_ARG
     assert call(rp=rope(K), pos=DUMMY + 2) == K.ERR_INVALID_ARG

@@ -150,7 +150,7 @@ def positions(axes, n, seed):
 NORM_ROPE_U = 26
 
 
-@pytest.mark.parametrize("width,rot,interleaved", [(64, 64, 0), (64, 32, 0), (64, 6, 1), (128, 128, 1), (128, 96, 0),
+@pytest.mark.parametrize("width,rot,interleaved", [(64, 64, 0), (64, 32, 0), (64, 16, 0), (64, 6, 1), (128, 48, 0), (256, 240, 0), (128, 128, 1), (128, 96, 0),
                                                    (256, 64, 0), (256, 256, 0), (256, 96, 0), (256, 250, 1),
                                                    (512, 256, 0), (512, 64, 1)])
 @pytest.mark.parametrize("n,heads,axes", [(1, 1, 1), (1, 24, 3), (7, 3, 4), (300, 5, 2)])
