@@ -1,4 +1,5 @@
-"""ctypes binding of libkvq (include/kvq.h).
+"""Binding of libkvq (include/kvq.h): ctypes, and for the calls around the cache a
+compiled module of the same marshalling (csrc/binding.cpp).
 
 Argument marshalling only: every step of the path runs in the CUDA kernels of
 libkvq.so.  Tensors are torch tensors on a CUDA device; their ``data_ptr()`` and
@@ -8,13 +9,17 @@ library has not been built, loading raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # KVQ_SANITIZE=1: the host-sanitizer build (argument validation checked on the CPU)
-LIB_PATH = os.path.join(_PKG, "_build_san" if os.environ.get("KVQ_SANITIZE") == "1" else "_build", "libkvq.so")
+_BUILD = os.path.join(_PKG, "_build_san" if os.environ.get("KVQ_SANITIZE") == "1" else "_build")
+LIB_PATH = os.path.join(_BUILD, "libkvq.so")
+CALLS_PATH = os.path.join(_BUILD, "_kvq_calls.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE_TOO_SMALL = 0, -1, -2, -3, -4
 DEV_BAD_SLOT, DEV_BAD_PAGE, DEV_BAD_LENGTH, DEV_BAD_INDEX, DEV_TIMEOUT = 1, 2, 4, 8, 16
@@ -216,6 +221,10 @@ class Cache:
     def ref(self):
         return ctypes.byref(self.desc)
 
+    @property
+    def address(self):
+        return ctypes.addressof(self.desc)
+
     def nbytes(self):
         return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale) if t is not None)
 
@@ -402,90 +411,24 @@ def prefill_attn_fp8(cache: Cache, q, q_start, block_table, sm_scale, workspace=
     return out
 
 
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_DTYPES = {torch.float32: DT_F32, torch.bfloat16: DT_BF16}
+_calls = None
 
 
-def _device(t):
-    """The current device, on which a call's first tensor has to be."""
-    dev = t.get_device()
-    if dev < 0 or dev != _current_device():
-        _refuse_device(t, "a tensor", _current_device() if dev >= 0 else 0)
-    return dev
-
-
-def _refuse_device(t, what, dev):
-    if not t.is_cuda:
-        raise ValueError(f"kvq: expected a CUDA tensor, got one on {t.device}")
-    raise ValueError(f"kvq: {what} is on {t.device}, the current device is cuda:{dev}")
-
-
-def _at(t, what, dev, dtype=None):
-    """Address of a tensor the calls below hand to the library: on the call's
-    device (the kernels are launched there), of the type the call reads."""
-    if t.get_device() != dev:
-        _refuse_device(t, what, dev)
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"kvq: {what} must be {dtype}, got {t.dtype}")
-    return t.data_ptr()
-
-
-def _ints(t, what, dev, shape):
-    """Address of contiguous int32 metadata of a given shape."""
-    at = _at(t, what, dev, torch.int32)
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"kvq: {what} must be contiguous {shape}, got {tuple(t.shape)}")
-    return at
-
-
-def _status_at(t, dev):
-    return None if t is None else _at(t, "status", dev, torch.int32)
-
-
-def _code(t, what):
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"kvq: {what} must be fp32 or bf16, got {t.dtype}")
-    return code
-
-
-def _rows(t, what, dev, tokens, heads, width):
-    """kvq_rows of a tensor [tokens, heads, width] whose last dimension is contiguous."""
-    if t.shape != (tokens, heads, width):
-        raise ValueError(f"kvq: {what} must be [{tokens}, {heads}, {width}], got {tuple(t.shape)}")
-    ts, hs, es = t.stride()
-    if es != 1:
-        raise ValueError(f"kvq: the last dimension of {what} must be contiguous")
-    return RowsDesc(_at(t, what, dev), _code(t, what), heads, ts, hs)
-
-
-def _three(t, what):
-    if t.dim() != 3:
-        raise ValueError(f"kvq: {what} must be [tokens, heads, width], got {tuple(t.shape)}")
-    return t.shape
-
-
-def _new(shape, dtype, like, stream):
-    """An output tensor that belongs to the stream it is written on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _new_rows(n, heads, width, dtype, like, stream):
-    """A new contiguous tensor [n, heads, width] and its kvq_rows."""
-    code = _DTYPES.get(dtype)
-    if code is None:
-        raise TypeError(f"kvq: an output must be fp32 or bf16, got {dtype}")
-    t = _new((n, heads, width), dtype, like, stream)
-    return t, RowsDesc(t.data_ptr(), code, heads, heads * width, width)
-
-
-def _launch_stream(stream, dev):
-    if stream is not None:
-        return stream.cuda_stream
-    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+def calls():
+    """The compiled form of the calls below (csrc/binding.cpp: their checks, outputs
+    and marshalling), bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        if not os.path.exists(CALLS_PATH):
+            raise RuntimeError(f"the binding is not built ({CALLS_PATH}); run bit_quantized_kv_store_gb300.build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_kvq_calls", CALLS_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kvq_calls", loader))
+        loader.exec_module(module)
+        module.init(tuple(ctypes.cast(getattr(L, "kvq_" + n), _P).value for n in
+                          ("norm_rope", "norm_rope_store", "load", "load_seqs", "merge_diff", "diff_heads")), _check)
+        _calls = module
+    return _calls
 
 
 class Norm:
@@ -495,7 +438,7 @@ class Norm:
     def __init__(self, weight, eps=1e-6, offset=0.0):
         self.weight, self.eps, self.offset, self.width = weight, eps, offset, weight.numel()
         self.desc = NormDesc(_ptr(weight), _dtype_code(weight), eps, offset)
-        self.ref = ctypes.byref(self.desc)
+        self.handle = (ctypes.addressof(self.desc), self.width, weight.get_device())
 
 
 class Rope:
@@ -517,53 +460,22 @@ class Rope:
         signed = [w - (1 << 64) if w >= 1 << 63 else w for w in words]
         self.table = torch.tensor(signed, dtype=torch.int64).to(device)
         self.desc = RopeDesc(2 * n, int(self.interleaved), self.num_axes, 0, _ptr(self.table))
-        self.ref = ctypes.byref(self.desc)
+        self.handle = (ctypes.addressof(self.desc), self.num_axes, self.table.get_device())
 
 
-def _norm_ref(norm, what, dev, width):
-    if norm is None:
-        return None
-    if norm.width != width:
-        raise ValueError(f"kvq: {what} is for rows of {norm.width}, not {width}")
-    if norm.weight.get_device() != dev:
-        _refuse_device(norm.weight, what, dev)
-    return norm.ref
-
-
-def _rope_args(rope, positions, dev, n):
-    """(kvq_rope, positions, axis stride) of a call over n tokens; positions int32
-    [n] (one axis) or [axes, n]."""
-    if rope is None:
-        return None, None, 0
-    if positions is None:
-        raise ValueError("kvq: rotary positions need positions")
-    at = _at(positions, "positions", dev, torch.int32)
-    if rope.table.get_device() != dev:
-        _refuse_device(rope.table, "the rope's table", dev)
-    axes, shape = rope.num_axes, positions.shape
-    if shape != (axes, n) and (axes != 1 or shape != (n,)):
-        raise ValueError(f"kvq: positions must be [{axes}, {n}], got {tuple(shape)}")
-    st = positions.stride()
-    if n > 1 and st[-1] != 1:
-        raise ValueError("kvq: positions of an axis must be contiguous")
-    return rope.ref, at, (st[0] if axes > 1 else n)
+def _handle(x):
+    return None if x is None else x.handle
 
 
 def norm_rope(x, positions=None, rope=None, norm=None, out=None, dtype=None, status=None, stream=None):
     """Norm and rotary positions of rows x [tokens, heads, width] (any strides with a
-    contiguous last dimension) in one pass; returns out (default: a new tensor of
+    contiguous last dimension) in one pass; positions int32 [tokens], or [axes,
+    tokens] for a rope of several axes.  Returns out (default: a new tensor of
     `dtype`, x's own if None).  out may be x."""
-    n, heads, width = _three(x, "x")
-    dev = _device(x)
-    rx = _rows(x, "x", dev, n, heads, width)
-    if out is None:
-        out, ry = _new_rows(n, heads, width, dtype or x.dtype, x, stream)
-    else:
-        ry = _rows(out, "out", dev, n, heads, width)
-    ref, pos, ps = _rope_args(rope, positions, dev, n)
-    _check(lib().kvq_norm_rope(rx, ry, n, width, _norm_ref(norm, "norm", dev, width), ref, pos, ps,
-                               _status_at(status, dev), _launch_stream(stream, dev)), "kvq_norm_rope")
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_rope(x, positions, rope, norm, out, dtype, status)
+    return (_calls or calls()).norm_rope(x, positions, _handle(rope), _handle(norm), out, dtype, status)
 
 
 def norm_rope_store(cache: Cache, q, k, v, slot_mapping, positions=None, rope=None, q_norm=None, k_norm=None,
@@ -573,52 +485,21 @@ def norm_rope_store(cache: Cache, q, k, v, slot_mapping, positions=None, rope=No
     keys normed, position-rotated and stored, the values stored.  Returns q_out
     (default: a new fp32 tensor) for decode_attn, or with rotate=False for the
     calls that take unrotated queries.  q None: keys and values only."""
-    n = k.shape[0]
-    D, Hk, dev = cache.D, cache.Hk, _device(k)
-    rk, rv = _rows(k, "k", dev, n, Hk, D), _rows(v, "v", dev, n, Hk, D)
-    rq = ro = None
-    if q is not None:
-        Hq = _three(q, "q")[1]
-        rq = _rows(q, "q", dev, n, Hq, D)
-        if q_out is None:
-            q_out, ro = _new_rows(n, Hq, D, torch.float32, q, stream)
-        else:
-            ro = _rows(q_out, "q_out", dev, n, Hq, D)
-    elif q_out is not None:
-        raise ValueError("kvq: q_out without q")
-    ref, pos, ps = _rope_args(rope, positions, dev, n)
-    _check(lib().kvq_norm_rope_store(cache.ref, rq, rk, rv, n, _norm_ref(q_norm, "q_norm", dev, D),
-                                     _norm_ref(k_norm, "k_norm", dev, D), ref, pos, ps,
-                                     _ints(slot_mapping, "slot_mapping", dev, (n,)), ro, int(rotate),
-                                     _status_at(status, dev), _launch_stream(stream, dev)), "kvq_norm_rope_store")
-    return q_out
-
-
-def _load_outputs(cache, n, k, v, dtype, like, dev, stream):
-    """The outputs of a load and their kvq_rows: new ones where both are None."""
-    fp8 = cache.fmt == FMT_FP8_ROW
-    Hk, width = cache.Hk, cache.D + cache.rope if fp8 else cache.D
-    if k is None and v is None:
-        k, rk = _new_rows(n, Hk, width, dtype, like, stream)
-        v, rv = (None, None) if fp8 else _new_rows(n, Hk, width, dtype, like, stream)
-        return k, v, rk, rv
-    return (k, v, None if k is None else _rows(k, "k", dev, n, Hk, width),
-            None if v is None else _rows(v, "v", dev, n, Hk, width))
-
-
-def _rotates(cache, rotate_back):
-    return int(cache.fmt in (FMT_Q4_HAD32, FMT_TQ4) if rotate_back is None else rotate_back)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_rope_store(cache, q, k, v, slot_mapping, positions, rope, q_norm, k_norm, q_out, rotate, status)
+    return (_calls or calls()).norm_rope_store(cache.address, q, k, v, slot_mapping, positions, _handle(rope),
+                                               _handle(q_norm), _handle(k_norm), q_out, rotate, status)
 
 
 def load(cache: Cache, slots, k=None, v=None, dtype=torch.bfloat16, rotate_back=None, status=None, stream=None):
     """The rows at slots (int32 [n]) as the values they stand for: (k, v), each [n,
     Hk, D] (fp8: k [n, 1, 576], v None).  Given k and / or v are written instead of
     new ones (one alone: only that plane); a negative slot leaves its rows as they were."""
-    n, dev = slots.shape[0], _device(slots)
-    k, v, rk, rv = _load_outputs(cache, n, k, v, dtype, slots, dev, stream)
-    _check(lib().kvq_load(cache.ref, _ints(slots, "slots", dev, (n,)), n, _rotates(cache, rotate_back), rk, rv,
-                          _status_at(status, dev), _launch_stream(stream, dev)), "kvq_load")
-    return k, v
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return load(cache, slots, k, v, dtype, rotate_back, status)
+    return (_calls or calls()).load(cache.address, slots, k, v, dtype, rotate_back, status)
 
 
 def load_seqs(cache: Cache, block_tables, cu_lens, n_tok, starts=None, k=None, v=None, dtype=torch.bfloat16,
@@ -627,30 +508,11 @@ def load_seqs(cache: Cache, block_tables, cu_lens, n_tok, starts=None, k=None, v
     cu_lens[b + 1] - 1 are positions starts[b] (default 0) onwards of the sequence
     whose pages block_tables[b] lists.  n_tok: rows of the outputs; those past
     cu_lens[-1] are left as they were.  Outputs as for load()."""
-    B, pages, dev = cu_lens.shape[0] - 1, block_tables.shape[-1], _device(cu_lens)
-    k, v, rk, rv = _load_outputs(cache, n_tok, k, v, dtype, cu_lens, dev, stream)
-    _check(lib().kvq_load_seqs(cache.ref, _ints(block_tables, "block_tables", dev, (B, pages)), pages, B,
-                               None if starts is None else _ints(starts, "starts", dev, (B,)),
-                               _ints(cu_lens, "cu_lens", dev, (B + 1,)), n_tok, _rotates(cache, rotate_back), rk, rv,
-                               _status_at(status, dev), _launch_stream(stream, dev)), "kvq_load_seqs")
-    return k, v
-
-
-def _lambda(lam, dev, rows, heads):
-    """Address and row stride of lambda: fp32 [heads] (one set) or [rows, heads]."""
-    at, shape = _at(lam, "lam", dev, torch.float32), lam.shape
-    if (shape != (rows, heads) and shape != (heads,)) or (heads > 1 and lam.stride(-1) != 1):
-        raise ValueError(f"kvq: lam must be [{heads}] or [{rows}, {heads}] with contiguous rows, got {tuple(shape)}")
-    return at, (lam.stride(0) if len(shape) == 2 else 0)
-
-
-def _diff_out(out, rows, heads, width, dtype, like, dev, stream):
-    if out is None:
-        return _new((rows, heads, width), dtype, like, stream)
-    if out.shape != (rows, heads, width) or not out.is_contiguous():
-        raise ValueError(f"kvq: out must be contiguous [{rows}, {heads}, {width}], got {tuple(out.shape)}")
-    _at(out, "out", dev)
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return load_seqs(cache, block_tables, cu_lens, n_tok, starts, k, v, dtype, rotate_back, status)
+    return (_calls or calls()).load_seqs(cache.address, block_tables, cu_lens, n_tok, starts, k, v, dtype, rotate_back,
+                                         status)
 
 
 def merge_diff(cache: Cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq_len, lam, norm=None, out_scale=1.0,
@@ -659,58 +521,50 @@ def merge_diff(cache: Cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq
     output minus lam[.., h] times head 2h + 1's, rotated back, normed (norm) and
     scaled.  lam: fp32 [num_q_heads / 2] or [num_seqs, num_q_heads / 2].  Returns
     out [num_seqs, num_q_heads / 2, D]."""
-    dev, heads = _device(seq_lens), num_q_heads // 2
-    out = _diff_out(out, num_seqs, heads, cache.D, dtype, seq_lens, dev, stream)
-    lp, ls = _lambda(lam, dev, num_seqs, heads)
-    _check(lib().kvq_merge_diff(cache.ref, _ptr(workspace), workspace.numel(), num_seqs, num_q_heads,
-                                _ints(seq_lens, "seq_lens", dev, (num_seqs,)), max_seq_len, n_sel,
-                                _rotates(cache, rotate_back), lp, ls, _norm_ref(norm, "norm", dev, cache.D),
-                                out_scale, out.data_ptr(), _code(out, "out"), _launch_stream(stream, dev)),
-           "kvq_merge_diff")
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return merge_diff(cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq_len, lam, norm, out_scale, out,
+                              dtype, n_sel, rotate_back)
+    return (_calls or calls()).merge_diff(cache.address, workspace, num_seqs, num_q_heads, seq_lens, max_seq_len, lam,
+                                          _handle(norm), out_scale, out, dtype, n_sel, rotate_back)
 
 
 def diff_heads(x, lam, norm=None, out_scale=1.0, out=None, dtype=torch.float32, stream=None):
     """The same difference of heads already merged: x fp32 [rows, Hq, width]
     (prefill_attn's output) to [rows, Hq / 2, width]."""
-    rows, Hq, width = _three(x, "x")
-    dev = _device(x)
-    _at(x, "x", dev, torch.float32)
-    out = _diff_out(out, rows, Hq // 2, width, dtype, x, dev, stream)
-    lp, ls = _lambda(lam, dev, rows, Hq // 2)
-    _check(lib().kvq_diff_heads(_ptr(x), rows, Hq, width, lp, ls, _norm_ref(norm, "norm", dev, width), out_scale,
-                                out.data_ptr(), _code(out, "out"), _launch_stream(stream, dev)), "kvq_diff_heads")
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return diff_heads(x, lam, norm, out_scale, out, dtype)
+    return (_calls or calls()).diff_heads(x, lam, _handle(norm), out_scale, out, dtype)
 
 
 def decode_diff(cache: Cache, q, seq_lens, block_tables, max_seq_len, sm_scale, workspace, lam, norm=None,
                 out_scale=1.0, out=None, dtype=torch.float32, sel=None, stream=None):
     """One differential decode step: decode() of the Hq query heads with merge_diff();
     returns [B, Hq / 2, D]."""
-    B, Hq, D = _three(q, "q")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return decode_diff(cache, q, seq_lens, block_tables, max_seq_len, sm_scale, workspace, lam, norm, out_scale,
+                               out, dtype, sel)
+    B, Hq, _ = q.shape
     if cache.fmt in (FMT_Q4_HAD32, FMT_Q4_0):
-        decode_attn_unrotated(cache, q, seq_lens, block_tables, max_seq_len, sm_scale, workspace, sel=sel,
-                              stream=stream)
+        decode_attn_unrotated(cache, q, seq_lens, block_tables, max_seq_len, sm_scale, workspace, sel=sel)
     else:
-        qq = q
-        if cache.fmt == FMT_TQ4:
-            qq = tq4_rotate(cache, q, out=_new((B, Hq, D), torch.float32, q, stream), stream=stream)
-        elif q.dtype != torch.float32:
-            qq = _new((B, Hq, D), torch.float32, q, stream)
-            with torch.cuda.stream(stream):
-                qq.copy_(q)
-        decode_attn(cache, qq, seq_lens, block_tables, max_seq_len, sm_scale, workspace, sel=sel, stream=stream)
-    return merge_diff(cache, workspace, B, Hq, seq_lens, max_seq_len, lam, norm=norm, out_scale=out_scale, out=out,
-                      dtype=dtype, n_sel=0 if sel is None else sel.shape[1], stream=stream)
+        qq = tq4_rotate(cache, q) if cache.fmt == FMT_TQ4 else q.float()
+        decode_attn(cache, qq, seq_lens, block_tables, max_seq_len, sm_scale, workspace, sel=sel)
+    return merge_diff(cache, workspace, B, Hq, seq_lens, max_seq_len, lam, norm, out_scale, out, dtype,
+                      0 if sel is None else sel.shape[1])
 
 
 def prefill_diff(cache: Cache, q, q_start, block_table, sm_scale, lam, norm=None, out_scale=1.0, out=None,
                  dtype=torch.float32, status=None, stream=None):
     """Differential prefill of a prompt chunk: prefill_attn() of the Hq query heads,
     then diff_heads(); returns [n, Hq / 2, D]."""
-    o = prefill_attn(cache, q, q_start, block_table, sm_scale, out=_new(_three(q, "q"), torch.float32, q, stream),
-                     status=status, stream=stream)
-    return diff_heads(o, lam, norm=norm, out_scale=out_scale, out=out, dtype=dtype, stream=stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return prefill_diff(cache, q, q_start, block_table, sm_scale, lam, norm, out_scale, out, dtype, status)
+    return diff_heads(prefill_attn(cache, q, q_start, block_table, sm_scale, status=status), lam, norm, out_scale, out,
+                      dtype)
 
 
 def selftest_wait_timeout(d_status, stream=None):

@@ -1,7 +1,8 @@
 """Build libkvq.so (the CUDA kernels + C ABI) in-tree for sm_103a.
 
 Each translation unit is compiled by nvcc in parallel, then linked into
-``bit_quantized_kv_store_gb300/_build/libkvq.so``.  A unit is rebuilt only when
+``bit_quantized_kv_store_gb300/_build/libkvq.so``; the compiled part of the Python
+binding becomes ``_kvq_calls.so`` beside it.  A unit is rebuilt only when
 its source or a header is newer than its object file.
 """
 from __future__ import annotations
@@ -10,6 +11,7 @@ import concurrent.futures as cf
 import glob
 import os
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 SANITIZE = os.environ.get("KVQ_SANITIZE") == "1"
 BUILD = os.path.join(PKG, "_build_san" if SANITIZE else "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
+CALLS = os.path.join(BUILD, "_kvq_calls.so")  # csrc/binding.cpp
 
 ARCH = ["-gencode", "arch=compute_103a,code=compute_103a" if SANITIZE else "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{os.path.join(ROOT, 'include')}"]
@@ -67,11 +70,33 @@ def _compile(src, verbose_ptxas=False):
     return obj, r.stderr
 
 
+def _build_calls():
+    """The compiled part of the Python binding, against the installed torch."""
+    import torch
+    src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "kvq.h")
+    tdir = os.path.dirname(os.path.abspath(torch.__file__))
+    newest = max(os.path.getmtime(f) for f in (src, header, os.path.join(tdir, "version.py")))
+    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
+        return
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-o", tmp, src,
+           f"-I{sysconfig.get_paths()['include']}", f"-I{tdir}/include", f"-I{tdir}/include/torch/csrc/api/include",
+           f"-I{cuda}/include", f"-L{tdir}/lib", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10",
+           f"-Wl,-rpath,{tdir}/lib"]
+    r = subprocess.run(cmd, capture_output=True, text=True, env=_tool_env())
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(verbose_ptxas=False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        calls = ex.submit(_build_calls)
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        calls.result()
     objs = [o for o, _ in results]
     if verbose_ptxas:
         for _, log in results:

@@ -5,8 +5,6 @@ import ctypes
 import math
 from fractions import Fraction
 
-import pytest
-
 from tests.test_abi import _desc, _tq4_desc, K  # noqa: F401
 
 DUMMY = 4096
@@ -224,18 +222,3 @@ def test_differential_refusals(K):
         assert f(out=None) == K.ERR_INVALID_ARG
         assert f(out=DUMMY + 2) == K.ERR_INVALID_ARG
         assert f(od=2) == K.ERR_INVALID_ARG
-
-
-def test_binding_refuses_host_tensors(K):
-    import torch
-    x = torch.zeros(4, 2, 64)
-    with pytest.raises(ValueError):
-        K.norm_rope(x)
-    with pytest.raises(ValueError):
-        K.Norm(torch.ones(64))
-    with pytest.raises(ValueError):
-        K.Rope([1.0, 0.5], axes=[0])
-    with pytest.raises(K.KvqError):
-        K.Rope([math.nan])
-    with pytest.raises(ValueError):
-        K.diff_heads(x, torch.zeros(1))

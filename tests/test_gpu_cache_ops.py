@@ -238,7 +238,8 @@ def test_norm_rope_values_that_are_not_numbers(K):
 
 def test_norm_rope_axis_out_of_range_is_flagged(K):
     rope = K.Rope([1.0] * 32, axes=[0] * 31 + [2])
-    rope.num_axes = rope.desc.num_axes = 2            # the last pair names a third axis
+    rope.desc.num_axes = 2                            # the last pair names a third axis
+    rope.handle = (rope.handle[0], 2, rope.handle[2])
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
     x = rnd((3, 2, 64), "axis")
     pos = torch.ones(2, 3, dtype=torch.int32, device=DEV)
