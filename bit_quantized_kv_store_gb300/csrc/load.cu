@@ -33,13 +33,13 @@ namespace {
 
 constexpr int kLoadBlock = 256;
 
-// N (8, or a multiple of 16) consecutive values into the view at element e (view.wide:
-// the address is a multiple of 32 bytes).
+// N (8, or a multiple of 16) consecutive values to an address (`wide`: a multiple of
+// their bytes, up to 32).
 template <int N>
-__device__ __forceinline__ void put_values(const RowsView& v, int64_t e, const float (&x)[N]) {
-  if (v.dtype == KVQ_DT_BF16) {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(v.data) + e;
-    if (v.wide) {
+__device__ __forceinline__ void put_values(void* at, int dtype, int wide, const float (&x)[N]) {
+  if (dtype == KVQ_DT_BF16) {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(at);
+    if (wide) {
       uint32_t w[N / 2];
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
@@ -49,8 +49,8 @@ __device__ __forceinline__ void put_values(const RowsView& v, int64_t e, const f
       for (int i = 0; i < N; ++i) p[i] = __float2bfloat16_rn(x[i]);
     }
   } else {
-    float* p = static_cast<float*>(v.data) + e;
-    if (v.wide) {
+    float* p = static_cast<float*>(at);
+    if (wide) {
       uint32_t w[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) w[i] = __float_as_uint(x[i]);
@@ -162,82 +162,164 @@ __device__ __forceinline__ void code_values(uint32_t w, float (&x)[8]) {
 // place and of s, u, nt flip it.
 template <int FMT>
 struct SignMatrix {
-  uint32_t base;  // s = u = nt = 0
-  uint32_t flip;  // u = 1 (4-bit formats: where g is odd)
+  // the few distinct fragments, kept in registers: TQ4 [parity], 4-bit [u][nt >> 1][s & nt & 1]
+  uint32_t m[FMT == KVQ_FMT_TQ4 ? 2 : 8];
   __device__ __forceinline__ explicit SignMatrix(int lane) {
     const int t = lane & 3, g = lane >> 2;
-    const uint32_t b = (__popc(t & (g >> 1)) & 1) ? 0xBC00BC00u : 0x3C003C00u;
+    const uint32_t b = (__popc(t & (g >> 1)) & 1) ? 0xBC00BC00u : 0x3C003C00u;  // -1, 1
     if constexpr (FMT == KVQ_FMT_TQ4) {  // pair place: element bit 0; u: bit 1; s: bit 2
-      base = b ^ ((g & 1) ? 0x80000000u : 0u);
-      flip = 0;
-    } else {  // u: element bit 0; s: bit 1; pair place: bit 2
-      base = b;
-      flip = (g & 1) ? 0x80008000u : 0u;
+      m[0] = b ^ ((g & 1) ? 0x80000000u : 0u);
+      m[1] = m[0] ^ 0x80008000u;
+    } else {  // u: element bit 0 (odd elements' entries are +-1/16); s: bit 1; pair place: bit 2
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        m[i] = b ^ ((i & 4) ? ((g & 1) ? 0x80008000u : 0u) ^ (0x3C003C00u ^ 0x2C002C00u) : 0u) ^
+               ((i & 2) ? 0x80000000u : 0u) ^ ((i & 1) ? 0x80008000u : 0u);
     }
+#pragma unroll
+    for (uint32_t& r : m) asm volatile("" : "+r"(r));  // (not to be worked out again for every tile)
   }
   __device__ __forceinline__ uint32_t at(int s, int u, int nt) const {
-    if constexpr (FMT == KVQ_FMT_TQ4)
-      return base ^ ((((u & nt) ^ (s & (nt >> 1))) & 1) ? 0x80008000u : 0u);
-    else
-      return (base ^ (u ? flip : 0u)) ^ ((nt & 2) ? 0x80000000u : 0u) ^ ((s & nt & 1) ? 0x80008000u : 0u);
+    if constexpr (FMT == KVQ_FMT_TQ4) return m[((u & nt) ^ (s & (nt >> 1))) & 1];
+    else return m[4 * u + (nt & 2) + (s & nt & 1)];
   }
 };
 
-// FMT: KVQ_FMT_Q4_HAD32, KVQ_FMT_Q4_0 or KVQ_FMT_TQ4; NG groups of 32 in a row; ROT:
-// rotate back.  A warp takes 8 / NG tokens at once and hpw heads one after another
-// (kUnroll heads' loads in flight): lane 4g + t the codes 8t .. 8t + 7 of group g of
-// the 8 (group g % NG of token g / NG's row), in K and in V.
-constexpr int kUnroll = 4;
+// The codes of a word as mma operands.  4-bit formats: left biased, 1024 + c in the
+// pairs of even elements and 1024 + 16 c in those of odd ones, whose matrix entries
+// are +-1/16: the biases, 1024 and 64, cancel in every sum but outputs 0 and 1,
+// whose accumulators start from minus theirs (kBias0, with the 8 of every code; kBias1).
+constexpr float kBias0 = -(16.f * 1024.f + 16.f * 64.f + 32.f * 8.f), kBias1 = -(16.f * 1024.f - 16.f * 64.f);
+template <int FMT>
+__device__ __forceinline__ void code_operands(uint32_t w, uint32_t (&p)[4]) {
+  if constexpr (FMT == KVQ_FMT_TQ4) {
+    code_pairs<FMT>(w, p);
+  } else {
+    p[0] = nib_lo_pair_biased(w);
+    p[1] = nib_hi_pair_biased(w);
+    p[2] = nib_lo_pair_biased(w >> 8);
+    p[3] = nib_hi_pair_biased(w >> 8);
+  }
+}
 
-template <int FMT, int NG, bool ROT>
-__global__ void __launch_bounds__(kLoadBlock) load_q4_kernel(const __grid_constant__ LoadArgs a, int hpw) {
+// FMT: KVQ_FMT_Q4_HAD32, KVQ_FMT_Q4_0 or KVQ_FMT_TQ4; NG groups of 32 in a row; ROT:
+// rotate back.  A unit of work is 8 / NG tokens and hpu <= kHeads heads of them: lane
+// 4g + t of its warp has the codes 8t .. 8t + 7 of group g of the 8 (group g % NG of
+// token g / NG's row), in K and in V.  Every warp walks the units with the grid's
+// stride, in three steps that overlap: where a unit's rows lie (a search and a
+// block-table entry, two dependent loads) two units ahead, its codes and scales one
+// ahead, the transform and the stores.  (One unit to a warp, each paying the chain
+// of loads by itself: 262 us for 262144 tokens.)
+// nb divides by a token's units; a launch has fewer than 2^31.  OUT: what is written,
+// kBf16 or kF32 (K and V both, whole vectors), or kAny (as the views say).
+constexpr int kHeads = 4;
+// CTAs of an SM: three (80 registers), two for the TQ4 rows (their exchange of 16
+// values spills at 80: 20011 tokens in fp32 45 us, against 37 us).
+__host__ __device__ constexpr int load_ctas(int fmt) { return fmt == KVQ_FMT_TQ4 ? 2 : 3; }
+enum Out { kAny, kBf16, kF32 };
+
+template <int FMT, int NG, bool ROT, int OUT>
+__global__ void __launch_bounds__(kLoadBlock, load_ctas(FMT)) load_q4_kernel(const __grid_constant__ LoadArgs a,
+                                                                             FastDiv nb, int hpu, uint32_t units) {
   pdl_wait();
   pdl_trigger();
   constexpr int D = 32 * NG;
   const int lane = threadIdx.x & 31, t4 = lane & 3, g = lane >> 2, G = g % NG;
-  const int64_t t = a.t0 + ((int64_t)blockIdx.x * (kLoadBlock / 32) + (threadIdx.x >> 5)) * (8 / NG) + g / NG;
   const int Hk = a.c.num_kv_heads;
-  const int h0 = blockIdx.y * hpw, h1 = min(h0 + hpw, Hk);
-  int32_t page = 0, why = 0;
-  uint32_t off = 0;
-  const Where at = t < a.n_tok ? locate(a, t, page, off, why) : kSkip;
-  if (at == kBad && G == 0 && t4 == 0) set_status(a.status, why);
-  const bool with_k = a.k.data != nullptr, with_v = a.v.data != nullptr;
+  const bool with_k = OUT != kAny || a.k.data != nullptr, with_v = OUT != kAny || a.v.data != nullptr;
+  const int k_dtype = OUT == kAny ? a.k.dtype : OUT == kBf16 ? KVQ_DT_BF16 : KVQ_DT_F32;
+  const int v_dtype = OUT == kAny ? a.v.dtype : k_dtype;
+  const int k_wide = OUT == kAny ? a.k.wide : 1, v_wide = OUT == kAny ? a.v.wide : 1;
   const SignMatrix<FMT> H(lane);
   uint32_t sw = 0;
   if constexpr (FMT == KVQ_FMT_TQ4 && ROT) sw = static_cast<const uint32_t*>(a.c.signs)[G] >> (8 * t4);
   constexpr float kBack = !ROT ? 1.0f : FMT == KVQ_FMT_TQ4 ? tq4_row_scale<NG>() : kHadamardScale;
+  const float c0 = FMT != KVQ_FMT_TQ4 && t4 == 0 ? kBias0 : 0.f, c1 = FMT != KVQ_FMT_TQ4 && t4 == 0 ? kBias1 : 0.f;
+  // bytes between the heads of a token's rows
+  const int64_t code_step = (int64_t)a.c.page_size * (D / 2);
+  const int64_t scale_step = (int64_t)a.c.page_size * (FMT == KVQ_FMT_TQ4 ? 2 : 2 * NG);
+  const int64_t ok_step = a.k.hs << (k_dtype == KVQ_DT_BF16 ? 1 : 2), ov_step = a.v.hs << (v_dtype == KVQ_DT_BF16 ? 1 : 2);
 
-  for (int hb = h0; hb < h1; hb += kUnroll) {
-    uint32_t word[kUnroll][2];
-    __half scale[kUnroll][2];
+  struct Unit {
+    int64_t t, row;  // the lane's token; its row in the planes at the unit's first head
+    int h, why;
+    Where at;
+  };
+  auto place = [&](uint32_t u, Unit& x) {
+    const uint32_t tb = fast_div(u, nb);
+    x.h = static_cast<int>(u - tb * nb.d) * hpu;
+    x.t = a.t0 + (int64_t)tb * (8 / NG) + g / NG;
+    int32_t page = 0, why = 0;
+    uint32_t off = 0;
+    x.at = x.t < a.n_tok ? locate(a, x.t, page, off, why) : kSkip;
+    x.why = why;
+    x.row = ((int64_t)page * Hk + x.h) * a.c.page_size + off;
+  };
+  uint32_t word[kHeads][2];
+  uint16_t scale[kHeads][2];
+  auto fetch = [&](const Unit& x, uint32_t (&w)[kHeads][2], uint16_t (&sc)[kHeads][2]) {
+    const int64_t code0 = x.row * (D / 2) + 16 * G + 4 * t4;
+    const int64_t scale0 = FMT == KVQ_FMT_TQ4 ? 2 * x.row : (x.row * NG + G) * 2;
+    const uint8_t *ck = static_cast<const uint8_t*>(a.c.k) + code0, *cv = static_cast<const uint8_t*>(a.c.v) + code0;
+    const uint8_t *sk = static_cast<const uint8_t*>(a.c.k_scale) + scale0,
+                  *sv = static_cast<const uint8_t*>(a.c.v_scale) + scale0;
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i)
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        word[i][kv] = 0;
-        scale[i][kv] = __ushort_as_half(0);
-        if (at == kRow && hb + i < h1 && (kv ? with_v : with_k)) {
-          const int64_t r = ((int64_t)page * Hk + hb + i) * a.c.page_size + off;
-          word[i][kv] = static_cast<const uint32_t*>(kv ? a.c.v : a.c.k)[r * (D / 8) + 4 * G + t4];
-          scale[i][kv] = static_cast<const __half*>(
-              kv ? a.c.v_scale : a.c.k_scale)[FMT == KVQ_FMT_TQ4 ? r : r * NG + G];
+    for (int i = 0; i < kHeads; ++i) {
+      w[i][0] = w[i][1] = 0;
+      sc[i][0] = sc[i][1] = 0x7E00;  // a position without a row stands for NaN
+      if (x.at == kRow && i < hpu && x.h + i < Hk) {
+        if (with_k) {
+          w[i][0] = *reinterpret_cast<const uint32_t*>(ck + i * code_step);
+          sc[i][0] = *reinterpret_cast<const uint16_t*>(sk + i * scale_step);
+        }
+        if (with_v) {
+          w[i][1] = *reinterpret_cast<const uint32_t*>(cv + i * code_step);
+          sc[i][1] = *reinterpret_cast<const uint16_t*>(sv + i * scale_step);
         }
       }
+    }
+  };
+
+  const uint32_t stride = gridDim.x * (kLoadBlock / 32);
+  uint32_t u = blockIdx.x * (kLoadBlock / 32) + (threadIdx.x >> 5);
+  if (u >= units) return;
+  Unit cur, nxt = {};
+  place(u, cur);
+  fetch(cur, word, scale);
+  bool more = units - u > stride;
+  if (more) place(u + stride, nxt);
+  for (;;) {
+    // the next unit's rows, and where the one after it lies
+    uint32_t nword[kHeads][2];
+    uint16_t nscale[kHeads][2];
+    Unit after = nxt;
+    bool more2 = false;
+    if (more) {
+      fetch(nxt, nword, nscale);
+      u += stride;
+      more2 = units - u > stride;
+      if (more2) place(u + stride, after);
+    }
+    if (cur.at == kBad && cur.h == 0 && G == 0 && t4 == 0) set_status(a.status, cur.why);
+    const bool stk = cur.at != kSkip && with_k, stv = cur.at != kSkip && with_v;
+    uint8_t* ok = static_cast<uint8_t*>(a.k.data) +
+                  ((cur.t * a.k.ts + cur.h * a.k.hs + 32 * G + 8 * t4) << (k_dtype == KVQ_DT_BF16 ? 1 : 2));
+    uint8_t* ov = static_cast<uint8_t*>(a.v.data) +
+                  ((cur.t * a.v.ts + cur.h * a.v.hs + 32 * G + 8 * t4) << (v_dtype == KVQ_DT_BF16 ? 1 : 2));
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      if (hb + i >= h1) break;
+    for (int i = 0; i < kHeads; ++i) {
+      if (i >= hpu || cur.h + i >= Hk) break;
       float x[2][8];
       if constexpr (ROT) {
         uint32_t pk[4], pv[4];
-        code_pairs<FMT>(word[i][0], pk);
-        code_pairs<FMT>(word[i][1], pv);
+        code_operands<FMT>(word[i][0], pk);
+        code_operands<FMT>(word[i][1], pv);
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            mma_f16(c, pk[2 * s], pv[2 * s], pk[2 * s + 1], pv[2 * s + 1], H.at(s, 0, nt), H.at(s, 1, nt));
+          float c[4];
+          mma_f16_c(c, pk[0], pv[0], pk[1], pv[1], H.at(0, 0, nt), H.at(0, 1, nt), nt ? 0.f : c0, nt ? 0.f : c1,
+                    nt ? 0.f : c0, nt ? 0.f : c1);
+          mma_f16(c, pk[2], pv[2], pk[3], pv[3], H.at(1, 0, nt), H.at(1, 1, nt));
           x[0][2 * nt] = c[0];
           x[0][2 * nt + 1] = c[1];
           x[1][2 * nt] = c[2];
@@ -260,19 +342,32 @@ __global__ void __launch_bounds__(kLoadBlock) load_q4_kernel(const __grid_consta
       }
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const float f = __half2float(scale[i][kv]) * kBack;
+        const float f = __half2float(__ushort_as_half(scale[i][kv])) * kBack;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[kv][j] *= f;
+        for (int j = 0; j < 8; j += 2) {
+          uint64_t f2 = pk2(f, f);
           if constexpr (FMT == KVQ_FMT_TQ4 && ROT)
-            x[kv][j] = __uint_as_float(__float_as_uint(x[kv][j]) ^ ((sw << (31 - j)) & 0x80000000u));
-          if (at == kBad) x[kv][j] = NAN;
+            f2 = pk2(__uint_as_float(__float_as_uint(f) ^ ((sw << (31 - j)) & 0x80000000u)),
+                     __uint_as_float(__float_as_uint(f) ^ ((sw << (30 - j)) & 0x80000000u)));
+          upk2(mul2(pk2(x[kv][j], x[kv][j + 1]), f2), x[kv][j], x[kv][j + 1]);
         }
-        const RowsView& out = kv ? a.v : a.k;
-        if (at != kSkip && (kv ? with_v : with_k))
-          put_values<8>(out, t * out.ts + (hb + i) * out.hs + 32 * G + 8 * t4, x[kv]);
       }
+      if (stk) put_values<8>(ok, k_dtype, k_wide, x[0]);
+      if (stv) put_values<8>(ov, v_dtype, v_wide, x[1]);
+      ok += ok_step;
+      ov += ov_step;
     }
+    if (!more) break;
+    cur = nxt;
+    nxt = after;
+    more = more2;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        word[i][kv] = nword[i][kv];
+        scale[i][kv] = nscale[i][kv];
+      }
   }
 }
 
@@ -320,7 +415,7 @@ __global__ void __launch_bounds__(kLoadBlock) load_wide_kernel(const __grid_cons
         x[2 * i + 1] = f.y * sc;
       }
     }
-    put_values<16>(a.k, t * a.k.ts + c, x);
+    put_values<16>(element_at(a.k, t * a.k.ts + c), a.k.dtype, a.k.wide, x);
   } else {
     const uint32_t plane = fast_div(row, a.hk);
     const int head = static_cast<int>(row - plane * a.hk.d);
@@ -341,7 +436,7 @@ __global__ void __launch_bounds__(kLoadBlock) load_wide_kernel(const __grid_cons
         }
       }
     }
-    put_values<16>(out, t * out.ts + head * out.hs + c, x);
+    put_values<16>(element_at(out, t * out.ts + head * out.hs + c), out.dtype, out.wide, x);
   }
 }
 
@@ -355,18 +450,39 @@ cudaError_t launch_load(const LoadArgs& args, cudaStream_t s) {
   const int NG = D / 32, cpr = (fp8 ? D + a.c.rope_dim : D) / 16;
   const int64_t n_tok = a.n_tok;
   if (!wide) {
-    // enough warps to fill the GPU a few times over, several heads in each
-    const int64_t warps = (n_tok * NG + 7) / 8, target = (int64_t)device_sm_count() * 192;
-    int64_t hpw = 1;
-    if (warps * Hk > target) hpw = ((warps * Hk + target - 1) / target + kUnroll - 1) / kUnroll * kUnroll;
-    if (hpw > Hk) hpw = Hk;
-    const int64_t chunks = (Hk + hpw - 1) / hpw;
-    if (chunks > 65535) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>((warps + kLoadBlock / 32 - 1) / (kLoadBlock / 32)),
-                    static_cast<unsigned>(chunks)),
-        block(kLoadBlock);
+    // Units of 8 / NG tokens and hpu heads, walked by as many warps as are resident at
+    // once.  hpu: the one whose rounds cost least, a round its heads' work and about
+    // one head's for the unit itself (4096 tokens of 4 heads: one round and a bit of
+    // 4 heads would be two).
+    const int64_t resident = (int64_t)device_sm_count() * load_ctas(a.c.format);
+    const int64_t blocks8 = (n_tok * NG + 7) / 8;
+    int hpu = 1;
+    int64_t best = 0;
+    for (int h = 1; h <= kHeads; h *= 2) {
+      const int64_t units = blocks8 * ((Hk + h - 1) / h), warps = resident * (kLoadBlock / 32);
+      const int64_t cost = (units + warps - 1) / warps * (h + 1);
+      if (h == 1 || cost < best) best = cost, hpu = h;
+    }
+    // at most 2^30 units in a launch
+    const int64_t per_tok = (Hk + hpu - 1) / hpu, max_tok = (int64_t(1) << 30) / per_tok / 8 * 8;
+    if (max_tok < 8) return cudaErrorInvalidValue;
+    const FastDiv nb = make_fastdiv(static_cast<uint32_t>(per_tok));
+    const bool plain = kvs == 2 && a.k.wide && a.v.wide && a.k.dtype == a.v.dtype;
+    const int out = !plain ? kAny : a.k.dtype == KVQ_DT_BF16 ? kBf16 : kF32;
+    const dim3 block(kLoadBlock);
+    for (a.t0 = 0; a.t0 < n_tok; a.t0 += max_tok) {
+      a.n_tok = n_tok - a.t0 < max_tok ? n_tok : a.t0 + max_tok;  // tokens [t0, n_tok) in this launch
+      const int64_t units = ((a.n_tok - a.t0) * NG + 7) / 8 * per_tok;
+      int64_t ctas = (units + kLoadBlock / 32 - 1) / (kLoadBlock / 32);
+      if (ctas > resident) ctas = resident;
+      const dim3 grid(static_cast<unsigned>(ctas));
     cudaError_t e = cudaErrorInvalidValue;
-#define KVQ_LOAD(F, N, R) e = launch_pdl(load_q4_kernel<F, N, R>, grid, block, 0, s, a, static_cast<int>(hpw)); break
+#define KVQ_LOAD_OUT(F, N, R, O) launch_pdl(load_q4_kernel<F, N, R, O>, grid, block, 0, s, a, nb, hpu, static_cast<uint32_t>(units))
+#define KVQ_LOAD(F, N, R)                                  \
+  e = out == kBf16  ? KVQ_LOAD_OUT(F, N, R, kBf16)         \
+      : out == kF32 ? KVQ_LOAD_OUT(F, N, R, kF32)          \
+                    : KVQ_LOAD_OUT(F, N, R, kAny);         \
+  break
 #define KVQ_LOAD_NG(F, R)       \
   switch (NG) {                 \
     case 1: KVQ_LOAD(F, 1, R);  \
@@ -396,7 +512,9 @@ cudaError_t launch_load(const LoadArgs& args, cudaStream_t s) {
 #undef KVQ_LOAD_TQ
 #undef KVQ_LOAD_NG
 #undef KVQ_LOAD
-    if (e != cudaSuccess) return e;
+#undef KVQ_LOAD_OUT
+      if (e != cudaSuccess) return e;
+    }
     return cudaGetLastError();
   }
   const int64_t per_tok = fp8 ? cpr : (int64_t)cpr * Hk * kvs;  // threads of a token
