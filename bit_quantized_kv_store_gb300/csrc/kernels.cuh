@@ -143,7 +143,7 @@ struct NormRopeArgs {
   int64_t n_tok;
   int Hq, Hk;
   int rotate;  // 1: queries into the cache's space
-  int hpw;     // batches of heads a warp takes (set by the launch)
+  int64_t per;  // batches of heads a warp takes (set by the launch)
   int plane_wide;  // BF16: the planes start on 32-byte boundaries
   FastDiv ps;  // page_size
 };

@@ -36,7 +36,7 @@ namespace {
 
 constexpr int kNoStore = -1;
 constexpr int kMaxPairs = 128;
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 4, kMinCtas = 4;  // 128 registers
 constexpr int E = 16;  // elements of a lane
 
 // cos and sin of the token's rotary pairs, once per warp, in shared memory: chunk c of
@@ -65,10 +65,15 @@ __device__ __forceinline__ float2 angle(const RopeView& r, int pair, const int32
   return cs;
 }
 
-__device__ __forceinline__ void make_angles(const RopeView& r, int64_t tok, int lane, int32_t* status, float4* sh) {
-  int32_t pos[4];
+// The token's positions on the rope's axes.
+__device__ __forceinline__ void load_pos(const RopeView& r, int64_t tok, int32_t (&pos)[4]) {
 #pragma unroll
   for (int a = 0; a < 4; ++a) pos[a] = a < r.axes ? r.pos[a * r.pos_stride + tok] : 0;
+}
+
+__device__ __forceinline__ void make_angles(const RopeView& r, const int32_t (&pos)[4], int lane, int32_t* status,
+                                            float4* sh) {
+  __syncwarp();  // (the last token's have been read)
   for (int p = lane; p < (r.rot >> 1); p += 32) {
     const float2 cs = angle(r, p, pos, status);
     float* at = reinterpret_cast<float*>(&sh[chunk_place(p >> 1)]) + (p & 1);
@@ -159,162 +164,208 @@ __device__ __forceinline__ void rope_rows(const RopeView& r, const RopeLane& g, 
   }
 }
 
+// What a kernel is made for: whole vectors of one input and one output type, or
+// (kAny) whatever the views say.
+enum Mode { kAny, kBf16ToBf16, kBf16ToF32, kF32ToF32 };
+
 // FMT: the cache's format, or kNoStore for rows that are only normed and rotated
-// (then every head is a "query" and Hk is 0).  BF: every input is bf16.  LPR: lanes
-// of a row.  U: batches of queries worked on side by side, so that one's shuffles
-// are in flight during the other's arithmetic.
-template <int LPR, int FMT, bool BF, int U>
-__global__ void __launch_bounds__(32 * kMaxWarps, 2) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+// (then every head is a "query" and Hk is 0).  LPR: lanes of a row.  Bf16 queries go
+// by two batches side by side (U), so that one's shuffles are in flight during the
+// other's arithmetic.  All tokens' batches in one line are cut into equal ranges, one
+// for each warp (a.per batches): no warp waits for another's last token, and a warp
+// works out the angles of the few tokens that its range touches.  The next token's
+// positions, slot and first rows are loaded during a token's last batches.
+template <int LPR, int FMT, int MODE>
+__global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   __shared__ float4 angles_sh[kMaxWarps][2 * kChunks];
   pdl_wait();
   pdl_trigger();
   constexpr int D = E * LPR, RPW = 32 / LPR;
+  constexpr bool BF = MODE == kBf16ToBf16 || MODE == kBf16ToF32;
+  constexpr int U = BF ? 2 : 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
-  const int64_t tok = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
-  if (tok >= a.n_tok) return;
-  // this warp's batches of RPW heads: first the queries', then K's, then V's
-  const int qb = (a.Hq + RPW - 1) / RPW, kb = (a.Hk + RPW - 1) / RPW;
-  const int b0 = blockIdx.y * a.hpw, b1 = min(b0 + a.hpw, qb + 2 * kb);
+  // a token's batches of RPW heads: first the queries', then K's, then V's
+  const int qb = (a.Hq + RPW - 1) / RPW, kb = (a.Hk + RPW - 1) / RPW, total = qb + 2 * kb;
+  const int64_t all = a.n_tok * total;
+  int64_t left = ((int64_t)blockIdx.x * (blockDim.x >> 5) + warp) * a.per;  // this warp's first batch
+  if (left >= all) return;
+  int64_t tok = left / total;
+  int b0 = static_cast<int>(left - tok * total);
+  left = all - left < a.per ? all - left : a.per;  // its batches
 
-  // the next batch's rows, ahead of the work on a batch (and first of the angles)
-  RawRow<E, BF> next[U];
-  const uint8_t* at;  // the first one's address in this lane
-  const auto row_of = [&](const RowsView& v, int h) { return element_at(v, tok * v.ts + h * v.hs + E * l); };
-  const auto first_row = [&](int b) {  // of batch b, of whichever kind
-    const bool is_q = b < qb, is_v = b >= qb + kb;
-    const int h = (is_q ? b : is_v ? b - qb - kb : b - qb) * RPW + sub;
-    const RowsView& v = is_q ? a.q : is_v ? a.v : a.k;
-    at = row_of(v, h);
-    if (h < (is_q ? a.Hq : a.Hk)) load_raw_at<E, BF>(at, v.dtype, v.wide, next[0]);
+  const auto in_type = [&](const RowsView& v) { return MODE == kAny ? v.dtype : BF ? KVQ_DT_BF16 : KVQ_DT_F32; };
+  const auto wide = [&](const RowsView& v) { return MODE == kAny ? v.wide : 1; };
+  const int out_type = MODE == kAny ? a.qo.dtype : MODE == kBf16ToBf16 ? KVQ_DT_BF16 : KVQ_DT_F32;
+  // address of the lane's part of head h's row, and bytes from a batch of queries to the next
+  const auto row_of = [&](const RowsView& v, int type, int64_t t, int h) {
+    return static_cast<uint8_t*>(v.data) + ((t * v.ts + h * v.hs + E * l) << (type == KVQ_DT_BF16 ? 1 : 2));
   };
+  const int64_t step = (a.q.hs * RPW) << (in_type(a.q) == KVQ_DT_BF16 ? 1 : 2);
+  const int64_t out_step = (a.qo.hs * RPW) << (out_type == KVQ_DT_BF16 ? 1 : 2);
+
+  RawRow<E, BF> next[U];  // the rows after those being worked on
+  const uint8_t* at;      // the first one's address in this lane
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < (BF ? E / 2 : E); ++i) next[u].w[i] = 0;
-  const int64_t step = (a.q.hs * RPW) << (a.q.dtype == KVQ_DT_BF16 ? 1 : 2);  // to the next batch of queries
-  const int be = min(b1, qb);
-  first_row(b0);
+  const auto load_kv = [&](int64_t t, int b) {
+    const bool is_v = b >= qb + kb;
+    const int h = (is_v ? b - qb - kb : b - qb) * RPW + sub;
+    const RowsView& v = is_v ? a.v : a.k;
+    if (h < a.Hk) load_raw_at<E, BF>(row_of(v, in_type(v), t, h), in_type(v), wide(v), next[0]);
+  };
+  const auto load_q = [&](int b, int end) {  // U batches of queries from b on, before `end`, at `at`
 #pragma unroll
-  for (int u = 1; u < U; ++u)
-    if (b0 + u < be && (b0 + u) * RPW + sub < a.Hq) load_raw_at<E, BF>(at + u * step, a.q.dtype, a.q.wide, next[u]);
-  int32_t slot = -1;
-  if (FMT != kNoStore && b1 > qb) slot = a.slots[tok];
-  RopeLane g;
-  if (a.rope.rot != 0 && b0 < qb + kb) {
-    make_angles(a.rope, tok, lane, a.status, angles_sh[warp]);
-    g = rope_lane(a.rope, angles_sh[warp], lane, l);
-  }
+    for (int u = 0; u < U; ++u)
+      if (b + u < end && (b + u) * RPW + sub < a.Hq)
+        load_raw_at<E, BF>(at + u * step, in_type(a.q), wide(a.q), next[u]);
+  };
+  int32_t pos[4], slot = -1;
+  const auto first_rows = [&](int64_t t, int b, int end) {  // of token t's batches [b, end), with its positions and slot
+    if (b < qb) {
+      at = row_of(a.q, in_type(a.q), t, b * RPW + sub);
+      load_q(b, min(end, qb));
+    } else if (FMT != kNoStore) {
+      load_kv(t, b);
+    }
+    if (a.rope.rot != 0 && b < qb + kb) load_pos(a.rope, t, pos);
+    if (FMT != kNoStore && end > qb) slot = a.slots[t];
+  };
+  const auto end_of = [&](int b, int64_t n) { return static_cast<int>(n < total - b ? b + n : total); };
+  int b1 = end_of(b0, left);
+  first_rows(tok, b0, b1);
 
-  uint64_t w[E / 2];
+  RopeLane g;
+  if (a.rope.rot != 0) g = rope_lane(a.rope, angles_sh[warp], lane, l);
   uint32_t sw = 0;
   if constexpr (FMT == KVQ_FMT_TQ4) sw = lane_signs<E>(a.c.signs, l);
-  if (b0 < qb) {
-    if (a.qn.weight) load_weight<E>(a.qn, l, w);
-    const int64_t out_step = (a.qo.hs * RPW) << (a.qo.dtype == KVQ_DT_BF16 ? 1 : 2);
-    uint8_t* out = row_of(a.qo, b0 * RPW + sub);
-    for (int b = b0; b < be; b += U) {
-      uint64_t x[U][E / 2];
+  uint64_t w[E / 2];
+  int weights = 0;  // whose they are: 1 the queries', 2 the keys'
+
+  for (;;) {
+    const int be = min(b1, qb);
+    const bool stores = FMT != kNoStore && b1 > qb;
+    const int64_t rest = left - (b1 - b0);  // batches of the tokens after this one
+    const int nb1 = end_of(0, rest);
+    if (a.rope.rot != 0 && b0 < qb + kb) make_angles(a.rope, pos, lane, a.status, angles_sh[warp]);
+    const int32_t this_slot = slot;
+    if (b0 < qb) {
+      if (a.qn.weight && weights != 1) load_weight<E>(a.qn, l, w), weights = 1;
+      uint8_t* out = row_of(a.qo, out_type, tok, b0 * RPW + sub);
+      for (int b = b0; b < be; b += U) {
+        uint64_t x[U][E / 2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) unpack_row<E, BF>(next[u], x[u]);
-      if (b + U < be) {
-        at += U * step;
+        for (int u = 0; u < U; ++u) unpack_row<E, BF>(next[u], x[u]);
+        if (b + U < be) {
+          at += U * step;
+          load_q(b + U, be);
+        } else if (stores) {
+          load_kv(tok, qb);
+        } else if (rest > 0) {
+          first_rows(tok + 1, 0, nb1);
+        }
+        if (a.qn.weight) norm_rows<E, LPR, U>(x, w, a.qn.eps);
+        if (a.rope.rot != 0) rope_rows<U>(a.rope, g, l, x);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if constexpr (FMT == KVQ_FMT_Q4_HAD32) {
+            if (a.rotate) rotate_row_had32<E>(x[u], lane);
+          }
+          if constexpr (FMT == KVQ_FMT_TQ4) {
+            if (a.rotate) rotate_row_tq4<E, LPR>(x[u], sw, lane);
+          }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (b + U + u < be && (b + U + u) * RPW + sub < a.Hq)
-            load_raw_at<E, BF>(at + u * step, a.q.dtype, a.q.wide, next[u]);
-      } else if (FMT != kNoStore && b1 > qb) {
-        first_row(qb);
-      }
-      if (a.qn.weight) norm_rows<E, LPR, U>(x, w, a.qn.eps);
-      if (a.rope.rot != 0) rope_rows<U>(a.rope, g, l, x);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if constexpr (FMT == KVQ_FMT_Q4_HAD32) {
-          if (a.rotate) rotate_row_had32<E>(x[u], lane);
-        }
-        if constexpr (FMT == KVQ_FMT_TQ4) {
-          if (a.rotate) rotate_row_tq4<E, LPR>(x[u], sw, lane);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (b + u < be && (b + u) * RPW + sub < a.Hq)
-          write_row_at<E>(out + u * out_step, a.qo.dtype, a.qo.wide, x[u]);
-      out += U * out_step;
-    }
-  }
-  if constexpr (FMT != kNoStore) {
-    if (b1 <= qb || slot < 0) return;
-    if ((int64_t)slot >= (int64_t)a.c.num_pages * a.c.page_size) {
-      if (lane == 0) set_status(a.status, KVQ_DEV_BAD_SLOT);
-      return;
-    }
-    const uint32_t page = fast_div(static_cast<uint32_t>(slot), a.ps);
-    const uint32_t off = static_cast<uint32_t>(slot) - page * a.ps.d;
-    if (a.kn.weight && b0 < qb + kb) load_weight<E>(a.kn, l, w);
-    for (int b = max(b0, qb); b < b1; ++b) {
-      const bool is_v = b >= qb + kb;
-      const int h = (is_v ? b - qb - kb : b - qb) * RPW + sub;
-      const int64_t r = ((int64_t)page * a.Hk + h) * a.c.page_size + off;
-      uint64_t x1[1][E / 2];
-      uint64_t(&x)[E / 2] = x1[0];
-      unpack_row<E, BF>(next[0], x);
-      if (b + 1 < b1) first_row(b + 1);
-      if (!is_v) {
-        if (a.kn.weight) norm_rows<E, LPR, 1>(x1, w, a.kn.eps);
-        if (a.rope.rot != 0) rope_rows<1>(a.rope, g, l, x1);
-      }
-      void* codes = is_v ? a.c.v : a.c.k;
-      void* scales = is_v ? a.c.v_scale : a.c.k_scale;
-      if constexpr (FMT == KVQ_FMT_BF16) {
-        if (h < a.Hk)
-          write_row_at<E>(static_cast<uint16_t*>(codes) + r * D + E * l, KVQ_DT_BF16, a.plane_wide, x);
-      } else {
-        __half s16;
-        uint32_t word[2];
-        if constexpr (FMT == KVQ_FMT_TQ4) {
-          rotate_row_tq4<E, LPR>(x, sw, lane);
-          float y[E];
-#pragma unroll
-          for (int i = 0; i < E / 2; ++i) upk2(x[i], y[2 * i], y[2 * i + 1]);
-          tq4_row_codes<E, LPR>(y, word, s16);
-          if (h < a.Hk && l == 0) static_cast<__half*>(scales)[r] = s16;
-        } else {
-          constexpr bool ROT = FMT == KVQ_FMT_Q4_HAD32;
-          if constexpr (ROT) rotate_row_had32<E>(x, lane);
-          q4_row_codes<E, ROT>(x, word, s16);
-          if (h < a.Hk && l % (32 / E) == 0) static_cast<__half*>(scales)[r * (D / 32) + l / (32 / E)] = s16;
-        }
-        if (h < a.Hk) write_codes<E>(static_cast<uint8_t*>(codes) + r * (D / 2) + l * (E / 2), word);
+          if (b + u < be && (b + u) * RPW + sub < a.Hq) write_row_at<E>(out + u * out_step, out_type, wide(a.qo), x[u]);
+        out += U * out_step;
       }
     }
+    if constexpr (FMT != kNoStore) {
+      if (stores) {
+        const bool in_pool = (int64_t)this_slot < (int64_t)a.c.num_pages * a.c.page_size, keep = this_slot >= 0 && in_pool;
+        if (!in_pool && lane == 0) set_status(a.status, KVQ_DEV_BAD_SLOT);
+        const uint32_t page = keep ? fast_div(static_cast<uint32_t>(this_slot), a.ps) : 0;
+        const uint32_t off = static_cast<uint32_t>(this_slot) - page * a.ps.d;
+        if (a.kn.weight && b0 < qb + kb && weights != 2) load_weight<E>(a.kn, l, w), weights = 2;
+        for (int b = max(b0, qb); b < b1; ++b) {
+          const bool is_v = b >= qb + kb;
+          const int h = (is_v ? b - qb - kb : b - qb) * RPW + sub;
+          const int64_t r = ((int64_t)page * a.Hk + h) * a.c.page_size + off;
+          uint64_t x1[1][E / 2];
+          uint64_t(&x)[E / 2] = x1[0];
+          unpack_row<E, BF>(next[0], x);
+          if (b + 1 < b1) load_kv(tok, b + 1);
+          else if (rest > 0) first_rows(tok + 1, 0, nb1);
+          if (!keep) continue;
+          if (!is_v) {
+            if (a.kn.weight) norm_rows<E, LPR, 1>(x1, w, a.kn.eps);
+            if (a.rope.rot != 0) rope_rows<1>(a.rope, g, l, x1);
+          }
+          void* codes = is_v ? a.c.v : a.c.k;
+          void* scales = is_v ? a.c.v_scale : a.c.k_scale;
+          if constexpr (FMT == KVQ_FMT_BF16) {
+            if (h < a.Hk)
+              write_row_at<E>(static_cast<uint16_t*>(codes) + r * D + E * l, KVQ_DT_BF16, a.plane_wide, x);
+          } else {
+            __half s16;
+            uint32_t word[2];
+            if constexpr (FMT == KVQ_FMT_TQ4) {
+              rotate_row_tq4<E, LPR>(x, sw, lane);
+              float y[E];
+#pragma unroll
+              for (int i = 0; i < E / 2; ++i) upk2(x[i], y[2 * i], y[2 * i + 1]);
+              tq4_row_codes<E, LPR>(y, word, s16);
+              if (h < a.Hk && l == 0) static_cast<__half*>(scales)[r] = s16;
+            } else {
+              constexpr bool ROT = FMT == KVQ_FMT_Q4_HAD32;
+              if constexpr (ROT) rotate_row_had32<E>(x, lane);
+              q4_row_codes<E, ROT>(x, word, s16);
+              if (h < a.Hk && l % (32 / E) == 0) static_cast<__half*>(scales)[r * (D / 32) + l / (32 / E)] = s16;
+            }
+            if (h < a.Hk) write_codes<E>(static_cast<uint8_t*>(codes) + r * (D / 2) + l * (E / 2), word);
+          }
+        }
+      }
+    }
+    if (rest <= 0) break;
+    ++tok;
+    left = rest;
+    b0 = 0;
+    b1 = nb1;
   }
 }
 
 template <int LPR, int FMT>
 cudaError_t launch_one(NormRopeArgs a, cudaStream_t s) {
-  // Two waves of warps or more where there are rows for them (each warp computes
-  // its token's angles once, so no more than that), the batches evenly over them.
+  // One range of batches for each resident warp (an even number, for the pairs of
+  // query batches), one batch where there are fewer; and CTAs of fewer warps where
+  // that leaves SMs without one.
   constexpr int RPW = 32 / LPR;
-  const int total = (a.Hq + RPW - 1) / RPW + 2 * ((a.Hk + RPW - 1) / RPW);
-  const int64_t target = static_cast<int64_t>(device_sm_count()) * 48;
-  int64_t bpw = (a.n_tok * total + target - 1) / target;
-  if (bpw > total) bpw = total;
-  const int chunks = static_cast<int>((total + bpw - 1) / bpw);
-  a.hpw = (total + chunks - 1) / chunks;
-  int wpc = kMaxWarps;  // tokens per CTA
-  while (wpc > 1 && a.n_tok < wpc) wpc >>= 1;
-  const dim3 grid(static_cast<unsigned>((a.n_tok + wpc - 1) / wpc), (total + a.hpw - 1) / a.hpw);
-  const bool bf = (a.Hq == 0 || a.q.dtype == KVQ_DT_BF16) &&
-                  (a.Hk == 0 || (a.k.dtype == KVQ_DT_BF16 && a.v.dtype == KVQ_DT_BF16));
-  const dim3 block(32 * wpc);
+  const int64_t total = (a.Hq + RPW - 1) / RPW + 2 * ((a.Hk + RPW - 1) / RPW);
+  const int64_t n_sm = device_sm_count(), resident = n_sm * kMinCtas * kMaxWarps, all_batches = a.n_tok * total;
+  int64_t per = (all_batches + resident - 1) / resident;
+  if (per > 1) per = (per + 1) / 2 * 2;
+  a.per = per;
+  const int64_t warps = (all_batches + per - 1) / per;
+  int wpc = kMaxWarps;
+  while (wpc > 1 && warps < n_sm * wpc) wpc >>= 1;
+  const dim3 grid(static_cast<unsigned>((warps + wpc - 1) / wpc)), block(32 * wpc);
+  const bool kv = a.Hk > 0, q = a.Hq > 0;
+  const bool whole = (!q || (a.q.wide && a.qo.wide)) && (!kv || (a.k.wide && a.v.wide));
+  const auto all = [&](int t) { return (!q || a.q.dtype == t) && (!kv || (a.k.dtype == t && a.v.dtype == t)); };
+  const bool out_f32 = !q || a.qo.dtype == KVQ_DT_F32;
   cudaError_t e;
-  if (a.hpw == 1)
-    e = bf ? launch_pdl(norm_rope_kernel<LPR, FMT, true, 1>, grid, block, 0, s, a)
-           : launch_pdl(norm_rope_kernel<LPR, FMT, false, 1>, grid, block, 0, s, a);
+  if (!whole || per == 1)
+    e = launch_pdl(norm_rope_kernel<LPR, FMT, kAny>, grid, block, 0, s, a);
+  else if (all(KVQ_DT_BF16))
+    e = out_f32 ? launch_pdl(norm_rope_kernel<LPR, FMT, kBf16ToF32>, grid, block, 0, s, a)
+                : launch_pdl(norm_rope_kernel<LPR, FMT, kBf16ToBf16>, grid, block, 0, s, a);
+  else if (all(KVQ_DT_F32) && out_f32)
+    e = launch_pdl(norm_rope_kernel<LPR, FMT, kF32ToF32>, grid, block, 0, s, a);
   else
-    e = bf ? launch_pdl(norm_rope_kernel<LPR, FMT, true, 2>, grid, block, 0, s, a)
-           : launch_pdl(norm_rope_kernel<LPR, FMT, false, 2>, grid, block, 0, s, a);
+    e = launch_pdl(norm_rope_kernel<LPR, FMT, kAny>, grid, block, 0, s, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
