@@ -129,45 +129,47 @@ __global__ void __launch_bounds__(512) merge_diff_kernel(const MergeArgs a, cons
 // of which are in flight meanwhile.  (A cluster of 8 CTAs for each head of a batch
 // of 32 sequences of up to 8000 keys took 30 us of a 99 us decode: 3072 CTAs, each
 // with its own barriers for 32 KB of partials.)
-constexpr int kRowThreads = 512;
+// T threads: 512, or 256 for at most 16 partitions (rows 16 .. 31 are empty), which
+// lets three CTAs share an SM instead of one.
 constexpr int kRowMaxP = 1024;  // partitions whose weights fit in shared memory
 
+template <int T>
 struct RowMergeSmem {
-  float acc[2][32][256];
+  float acc[2][T / 16][256];
   float wr[2][32], z[2][32];
   float all[256], second[256];
   int nan[2], empty[2];
 };
 
-template <int kBatch>
-__global__ void __launch_bounds__(kRowThreads) merge_diff_row_kernel(const MergeArgs a, const DiffView d,
-                                                                     const void* signs) {
+template <int kBatch, int T>
+__global__ void __launch_bounds__(T) merge_diff_row_kernel(const MergeArgs a, const DiffView d, const void* signs) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  RowMergeSmem& sm = *reinterpret_cast<RowMergeSmem*>(smem_raw);
-  float2* wts = reinterpret_cast<float2*>(smem_raw + sizeof(RowMergeSmem));  // [2][np] (old, new) weights
+  constexpr int RG = T / 64;  // groups of rows; each takes rows rg, rg + RG, .. of 4 RG
+  RowMergeSmem<T>& sm = *reinterpret_cast<RowMergeSmem<T>*>(smem_raw);
+  float2* wts = reinterpret_cast<float2*>(smem_raw + sizeof(RowMergeSmem<T>));  // [2][np] (old, new) weights
   pdl_wait();
   pdl_trigger();
   constexpr int D = 32 * kDiffGroups;
   const int ho = blockIdx.x, b = blockIdx.y;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t out0 = ((int64_t)b * (a.Hq >> 1) + ho) * D;
-  const int32_t T = keys_of(a, b);
-  if (T <= 0) {
-    if (tid < D) put_out(d.out, d.out_dtype, out0 + tid, T < 0 ? NAN : 0.f);
+  const int32_t keys = keys_of(a, b);
+  if (keys <= 0) {
+    if (tid < D) put_out(d.out, d.out_dtype, out0 + tid, keys < 0 ? NAN : 0.f);
     return;
   }
-  const int np = static_cast<int>(((int64_t)T + a.part - 1) / a.part);
+  const int np = static_cast<int>(((int64_t)keys + a.part - 1) / a.part);
   const int64_t base = ((int64_t)b * a.Hq + 2 * ho) * a.P;  // map 1's partials follow map 0's
   const int chunk = tid & 63, rg = tid >> 6;
   const float* accp = a.ws_acc + base * D + 4 * chunk;
-  auto load = [&](int i0, float4 (&v)[kBatch][2][4]) {  // partitions i0 + 32 k + rg + 8 j of both maps
+  auto load = [&](int i0, float4 (&v)[kBatch][2][4]) {  // partitions i0 + 32 k + rg + RG j of both maps
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int i = i0 + 32 * k + rg + 8 * j;
+          const int i = i0 + 32 * k + rg + RG * j;
           v[k][m][j] = i < np ? *reinterpret_cast<const float4*>(accp + ((int64_t)m * a.P + i) * D)
                               : make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kRowThreads) merge_diff_row_kernel(const Merge
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int i = i0 + 32 * k + rg + 8 * j;
+          const int i = i0 + 32 * k + rg + RG * j;
           if (i >= np) continue;
           const float2 w = wts[m * np + i];
           const float4 u = v[k][m][j];
@@ -233,28 +235,37 @@ __global__ void __launch_bounds__(kRowThreads) merge_diff_row_kernel(const Merge
   for (int m = 0; m < 2; ++m)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = rg + 8 * j;
+      const int r = rg + RG * j;
       if (r >= np) continue;
       const float wr = sm.wr[m][r];
       *reinterpret_cast<float4*>(&sm.acc[m][r][4 * chunk]) =
           make_float4(A[m][j].x * wr, A[m][j].y * wr, A[m][j].z * wr, A[m][j].w * wr);
     }
   __syncthreads();
-  const int map = tid >> 8, col = tid & 255;
-  float o = 0.f, Z = 0.f;
-  const int rows = min(np, 32);
+  const int col = tid & 255, rows = min(np, 32);
+  const auto folded = [&](int m) {  // value col of map m
+    float o = 0.f, Z = 0.f;
 #pragma unroll 8
-  for (int r = 0; r < rows; ++r) {  // ascending rows, as in the fold
-    o += sm.acc[map][r][col];
-    Z += sm.z[map][r];
+    for (int r = 0; r < rows; ++r) {  // ascending rows, as in the fold
+      o += sm.acc[m][r][col];
+      Z += sm.z[m][r];
+    }
+    o = (sm.empty[m] || Z == 0.f) ? 0.f : o / Z;
+    return sm.nan[m] ? NAN : o;
+  };
+  float o0 = 0.f, o1 = 0.f;
+  if constexpr (T == 512) {
+    if (tid >= 256) sm.second[col] = folded(1);
+    else o0 = folded(0);
+    __syncthreads();
+    if (tid < 256) o1 = sm.second[col];
+  } else {
+    o0 = folded(0);
+    o1 = folded(1);
   }
-  o = (sm.empty[map] || Z == 0.f) ? 0.f : o / Z;
-  if (sm.nan[map]) o = NAN;
-  if (map == 1) sm.second[col] = o;
-  __syncthreads();
   const bool whole = d.norm.weight != nullptr || a.rotate_back == 2;
-  if (map == 0) {
-    float y = fmaf(-d.lambda[b * d.stride + ho], sm.second[col], o);
+  if (tid < 256) {
+    float y = fmaf(-d.lambda[b * d.stride + ho], o1, o0);
     if (a.rotate_back == 1) y = __fmul_rn(warp_fwht32(y, lane), kHadamardScale);
     if (!whole) put_out(d.out, d.out_dtype, out0 + col, y * d.scale);
     else sm.all[col] = y;
@@ -268,14 +279,13 @@ __global__ void __launch_bounds__(kRowThreads) merge_diff_row_kernel(const Merge
   for (int i = 0; i < kDiffE; ++i) put_out(d.out, d.out_dtype, out0 + kDiffE * lane + i, x[i]);
 }
 
-template <int kBatch>
+template <int kBatch, int T>
 cudaError_t launch_row(const MergeArgs& a, const DiffView& d, const void* signs, int B, cudaStream_t s) {
-  constexpr auto kern = merge_diff_row_kernel<kBatch>;
-  const int most = static_cast<int>(sizeof(RowMergeSmem)) + 2 * kRowMaxP * 8;
-  cudaError_t e = set_max_smem_once<kern>(most);
+  constexpr auto kern = merge_diff_row_kernel<kBatch, T>;
+  constexpr int fixed = static_cast<int>(sizeof(RowMergeSmem<T>));
+  cudaError_t e = set_max_smem_once<kern>(fixed + 2 * kRowMaxP * 8);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(a.Hq / 2, B), dim3(kRowThreads), sizeof(RowMergeSmem) + static_cast<size_t>(2) * a.P * 8,
-                    s, a, d, signs);
+  return launch_pdl(kern, dim3(a.Hq / 2, B), dim3(T), fixed + static_cast<size_t>(2) * a.P * 8, s, a, d, signs);
 }
 
 // One warp per (row, output head); lane l holds elements E l .. E l + E - 1.
@@ -318,7 +328,9 @@ cudaError_t launch_merge_diff(const MergeArgs& a, const DiffView& d, const kvq_c
   const int64_t heads = (int64_t)(a.Hq / 2) * B, n_sm = device_sm_count();
   cudaError_t e;
   if (a.P <= kRowMaxP && (a.P <= 32 || 2 * heads >= n_sm)) {
-    e = a.P <= 32 ? launch_row<1>(a, d, c.signs, B, s) : launch_row<2>(a, d, c.signs, B, s);
+    e = a.P <= 16   ? launch_row<1, 256>(a, d, c.signs, B, s)
+        : a.P <= 32 ? launch_row<1, 512>(a, d, c.signs, B, s)
+                    : launch_row<2, 512>(a, d, c.signs, B, s);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
   }
