@@ -153,7 +153,7 @@ NORM_ROPE_U = 26
 @pytest.mark.parametrize("width,rot,interleaved", [(64, 64, 0), (64, 32, 0), (64, 16, 0), (64, 6, 1), (128, 48, 0), (256, 240, 0), (128, 128, 1), (128, 96, 0),
                                                    (256, 64, 0), (256, 256, 0), (256, 96, 0), (256, 250, 1),
                                                    (512, 256, 0), (512, 64, 1)])
-@pytest.mark.parametrize("n,heads,axes", [(1, 1, 1), (1, 24, 3), (7, 3, 4), (300, 5, 2)])
+@pytest.mark.parametrize("n,heads,axes", [(1, 1, 1), (1, 24, 3), (7, 3, 4), (300, 5, 2), (3001, 9, 3)])
 @pytest.mark.parametrize("xt,yt", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32),
                                    (torch.bfloat16, torch.float32)])
 def test_norm_rope_against_64_bits(K, width, rot, interleaved, n, heads, axes, xt, yt):
@@ -259,7 +259,7 @@ def formats(K, D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256, 512])
-@pytest.mark.parametrize("n,Hq,Hk", [(1, 24, 4), (5, 3, 3), (32, 8, 1), (301, 12, 2)])
+@pytest.mark.parametrize("n,Hq,Hk", [(1, 24, 4), (5, 3, 3), (32, 8, 1), (301, 12, 2), (2501, 15, 3)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_norm_rope_store_equals_its_parts(K, D, n, Hq, Hk, dtype):
     """The same bytes in every plane and the same query bits as norm_rope into fp32,
@@ -309,6 +309,36 @@ def test_norm_rope_store_equals_its_parts(K, D, n, Hq, Hk, dtype):
             for other in (c, d):
                 assert torch.equal(other.k.view(torch.uint8), a.k.view(torch.uint8))
                 assert torch.equal(other.v.view(torch.uint8), a.v.view(torch.uint8))
+
+
+@pytest.mark.parametrize("n", [3, 2000])
+def test_norm_rope_store_mixed_types_and_strides(K, n):
+    """Queries, keys and values of different types, strides off 16 bytes and queries
+    rotated in place: the bits of contiguous fp32 inputs of the same values."""
+    D, Hq, Hk = 128, 6, 2
+    q, k, v = rnd((n, Hq, D), "mx q"), rnd((n, Hk, D), "mx k"), rnd((n, Hk, D), "mx v")
+    q, k, v = (t.bfloat16().float() for t in (q, k, v))
+    pos = positions(2, n, 5)
+    rope = rope_of(K, 32, 0, 2)[0]
+    qn, kn = K.Norm(rnd((D,), "mx wq"), 1e-6), K.Norm(rnd((D,), "mx wk", dtype=torch.bfloat16), 1e-6)
+    slots = torch.arange(n, dtype=torch.int32, device=DEV)
+
+    def run(q, k, v, **kw):
+        c = make_cache(K, K.FMT_Q4_HAD32, Hk, D, n // 16 + 1)
+        return c, K.norm_rope_store(c, q, k, v, slots, pos, rope=rope, q_norm=qn, k_norm=kn, **kw)
+
+    want, wq = run(q, k, v)
+    odd = torch.zeros(n, Hk, D + 1, device=DEV)
+    odd[..., 1:] = k
+    inplace = q.clone()
+    for args, kw in (((q.bfloat16(), k, v.bfloat16()), {}), ((q, odd[..., 1:], v.bfloat16()), {}),
+                     ((inplace, k.bfloat16(), v), dict(q_out=inplace)),
+                     ((q.bfloat16(), k.bfloat16(), v.bfloat16()), {}),
+                     ((q.transpose(0, 1).contiguous().transpose(0, 1), k, v), {})):
+        c, got = run(*args, **kw)
+        assert torch.equal(got, wq)
+        for name in ("k", "v", "k_scale", "v_scale"):
+            assert torch.equal(getattr(c, name).view(torch.uint8), getattr(want, name).view(torch.uint8))
 
 
 def test_norm_rope_store_queries_of_padding_tokens(K):
@@ -381,6 +411,42 @@ def test_load_against_64_bits(K, fmt, D, Hk, dtype):
         wide = torch.full((4, 2 * Hk, D + 1), 5.0, dtype=dtype, device=DEV)
         K.load(cache, slots[:4], k=wide[:, :Hk, 1:], v=wide[:, Hk:, 1:])
         assert torch.equal(wide[:, :Hk, 1:], both) and torch.equal(wide[:, Hk:, 1:], v) and (wide[..., 0] == 5).all()
+
+
+@pytest.mark.parametrize("fmt,D,Hk", [("Q4_HAD32", 32, 3), ("Q4_HAD32", 64, 5), ("Q4_HAD32", 128, 2),
+                                      ("Q4_HAD32", 256, 4), ("Q4_HAD32", 256, 9), ("TQ4", 64, 1), ("TQ4", 128, 6),
+                                      ("TQ4", 256, 4), ("Q4_0", 256, 8), ("BF16", 128, 3), ("FP8_ROW", 512, 1)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_load_many_rows(K, fmt, D, Hk, dtype):
+    """Enough rows that every warp takes several: by slot and by table, against the
+    same rows loaded a few at a time."""
+    f = getattr(K, "FMT_" + fmt)
+    n, pages = 23003, 1500
+    cache = make_cache(K, f, Hk, D, pages)
+    fill_random(cache, K, D + Hk)
+    perm = synth.page_permutation(pages, "many", fmt).to(torch.int32).to(DEV)
+    lens = [0, 9001, 5, 13997, 0]
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+    bt = torch.stack([perm[i * 100:i * 100 + 900] for i in range(5)])
+    starts = torch.tensor([0, 7, 3, 0, 1], dtype=torch.int32, device=DEV)
+    at = torch.cat([torch.arange(m, device=DEV) + int(starts[i]) for i, m in enumerate(lens)])
+    seq = torch.repeat_interleave(torch.arange(5, device=DEV), torch.tensor(lens, device=DEV))
+    slots = (bt.long()[seq, at // 16] * 16 + at % 16).to(torch.int32)
+    k, v = K.load_seqs(cache, bt, cu, n, starts=starts, dtype=dtype)
+    k2, v2 = K.load(cache, slots, dtype=dtype)
+    parts = [K.load(cache, slots[i:i + 4001], dtype=dtype) for i in range(0, n, 4001)]
+    small = [K.load(cache, slots[i:i + 3], dtype=dtype) for i in (0, 11000, n - 3)]
+    assert torch.equal(k, k2) and torch.equal(k, torch.cat([p[0] for p in parts]))
+    for i, p in zip((0, 11000, n - 3), small):
+        assert torch.equal(k[i:i + 3], p[0])
+    if v is not None:
+        assert torch.equal(v, v2) and torch.equal(v, torch.cat([p[1] for p in parts]))
+        # into strided outputs, and one plane alone
+        wide = torch.full((n, Hk, 2, D), 5.0, dtype=dtype, device=DEV)
+        K.load(cache, slots, k=wide[:, :, 0])
+        assert torch.equal(wide[:, :, 0], k) and (wide[:, :, 1] == 5).all()
+        K.load(cache, slots, v=wide[:, :, 1])
+        assert torch.equal(wide[:, :, 0], k) and torch.equal(wide[:, :, 1], v)
 
 
 @pytest.mark.parametrize("fmt", ["Q4_HAD32", "TQ4", "BF16", "FP8_ROW", "Q4_0"])
