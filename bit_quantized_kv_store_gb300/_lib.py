@@ -90,6 +90,9 @@ SIGNATURES = {
     "kvq_load": (_I32, [_CACHE, _P, _I64, _I32, _ROWS, _ROWS, _P, _P]),
     "kvq_load_seqs": (_I32, [_CACHE, _P, _I32, _I32, _P, _P, _I64, _I32, _ROWS, _ROWS, _P, _P]),
     "kvq_merge_diff": (_I32, [_CACHE, _P, _SZ, _I32, _I32, _P, _I32, _I32, _I32, _P, _I64, _NORM, _F, _P, _I32, _P]),
+    "kvq_prefill_diff_workspace_size": (_SZ, [_CACHE, _I32, _I32, _I32]),
+    "kvq_prefill_diff": (_I32, [_CACHE, _P, _I32, _I32, _I32, _I32, _P, _I32, _F, _P, _I64, _NORM, _F, _P, _SZ, _P, _I32,
+                                _P, _P]),
     "kvq_diff_heads": (_I32, [_P, _I64, _I32, _I32, _P, _I64, _NORM, _F, _P, _I32, _P]),
 }
 
@@ -426,7 +429,8 @@ def calls():
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kvq_calls", loader))
         loader.exec_module(module)
         module.init(tuple(ctypes.cast(getattr(L, "kvq_" + n), _P).value for n in
-                          ("norm_rope", "norm_rope_store", "load", "load_seqs", "merge_diff", "diff_heads")), _check)
+                          ("norm_rope", "norm_rope_store", "load", "load_seqs", "merge_diff", "diff_heads",
+                           "prefill_diff_workspace_size", "prefill_diff")), _check)
         _calls = module
     return _calls
 
@@ -531,7 +535,7 @@ def merge_diff(cache: Cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq
 
 def diff_heads(x, lam, norm=None, out_scale=1.0, out=None, dtype=torch.float32, stream=None):
     """The same difference of heads already merged: x fp32 [rows, Hq, width]
-    (prefill_attn's output) to [rows, Hq / 2, width]."""
+    (prefill_attn's or decode_merged's output) to [rows, Hq / 2, width]."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return diff_heads(x, lam, norm, out_scale, out, dtype)
@@ -557,14 +561,17 @@ def decode_diff(cache: Cache, q, seq_lens, block_tables, max_seq_len, sm_scale, 
 
 
 def prefill_diff(cache: Cache, q, q_start, block_table, sm_scale, lam, norm=None, out_scale=1.0, out=None,
-                 dtype=torch.float32, status=None, stream=None):
-    """Differential prefill of a prompt chunk: prefill_attn() of the Hq query heads,
-    then diff_heads(); returns [n, Hq / 2, D]."""
+                 dtype=torch.float32, workspace=None, status=None, stream=None):
+    """Differential prefill of a prompt chunk: query rows q [n, Hq, 256] at positions
+    q_start .. over the cache, each output head the difference of its two maps as in
+    merge_diff(); returns [n, Hq / 2, 256].  workspace: uint8 of
+    kvq_prefill_diff_workspace_size bytes (default: a new one)."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return prefill_diff(cache, q, q_start, block_table, sm_scale, lam, norm, out_scale, out, dtype, status)
-    return diff_heads(prefill_attn(cache, q, q_start, block_table, sm_scale, status=status), lam, norm, out_scale, out,
-                      dtype)
+            return prefill_diff(cache, q, q_start, block_table, sm_scale, lam, norm, out_scale, out, dtype, workspace,
+                                status)
+    return (_calls or calls()).prefill_diff(cache.address, q, q_start, block_table, sm_scale, lam, _handle(norm),
+                                            out_scale, out, dtype, workspace, status)
 
 
 def selftest_wait_timeout(d_status, stream=None):

@@ -856,6 +856,90 @@ int32_t kvq_merge_diff(const kvq_cache* cache, const void* workspace, size_t ws_
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
 }
 
+// A prompt chunk's partials: maxima, sums and contexts of every range of keys.
+struct PrefillDiffLayout {
+  int splits;
+  size_t m_off, z_off, acc_off, total;
+};
+
+static PrefillDiffLayout prefill_diff_layout(const kvq_cache* c, int n_q, int Hq, int q_start) {
+  PrefillDiffLayout w;
+  int n_sm = device_sm_count();
+  if (n_sm < 1) n_sm = 1;
+  w.splits = n_q > 0 ? prefill_splits(n_q, Hq, c->num_kv_heads, q_start, n_sm) : 1;
+  const size_t n = static_cast<size_t>(w.splits) * n_q * Hq;
+  w.m_off = 0;
+  w.z_off = round256(n * sizeof(float));
+  w.acc_off = 2 * w.z_off;
+  w.total = w.acc_off + n * 256 * sizeof(float);
+  return w;
+}
+
+// The shape of a differential prefill.
+static int32_t check_prefill_diff(const kvq_cache* c, int32_t n_q, int32_t Hq, int32_t q_start) {
+  if (!is_q4(c->format) || c->head_dim != 256) return KVQ_ERR_UNSUPPORTED;
+  if (n_q < 0 || q_start < 0 || Hq < 1 || Hq % c->num_kv_heads != 0) return KVQ_ERR_INVALID_ARG;
+  const int group = Hq / c->num_kv_heads;
+  if (group > 8 || group % 2 != 0) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(n_q) * Hq >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(q_start) + n_q >= (int64_t(1) << 31) - 64) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+size_t kvq_prefill_diff_workspace_size(const kvq_cache* cache, int32_t n_q, int32_t num_q_heads, int32_t q_start) {
+  if (check_cache(cache) != KVQ_OK || check_prefill_diff(cache, n_q, num_q_heads, q_start) != KVQ_OK) return 0;
+  return prefill_diff_layout(cache, n_q, num_q_heads, q_start).total;
+}
+
+int32_t kvq_prefill_diff(const kvq_cache* cache, const void* q, int32_t dtype, int32_t n_q, int32_t num_q_heads,
+                         int32_t q_start, const int32_t* d_block_table, int32_t max_pages, float sm_scale,
+                         const float* d_lambda, int64_t lambda_stride, const kvq_norm* norm, float out_scale,
+                         void* workspace, size_t ws_bytes, void* out, int32_t out_dtype, int32_t* d_status,
+                         void* stream) {
+  int32_t st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  st = check_prefill_diff(cache, n_q, num_q_heads, q_start);
+  if (st != KVQ_OK) return st;
+  if (!dtype_ok(dtype)) return KVQ_ERR_INVALID_ARG;
+  if (n_q == 0) return KVQ_OK;
+  if (!q || reinterpret_cast<uintptr_t>(q) % (dtype == KVQ_DT_F32 ? 4 : 2) != 0 || !d_block_table || max_pages < 1)
+    return KVQ_ERR_INVALID_ARG;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 32 != 0) return KVQ_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(q_start) + n_q > static_cast<int64_t>(max_pages) * cache->page_size)
+    return KVQ_ERR_INVALID_ARG;
+  DiffView d;
+  st = check_diff(d_lambda, lambda_stride, n_q, num_q_heads / 2, norm, out_scale, out, out_dtype, &d);
+  if (st != KVQ_OK) return st;
+  const PrefillDiffLayout w = prefill_diff_layout(cache, n_q, num_q_heads, q_start);
+  if (ws_bytes < w.total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+  const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->num_kv_heads * cache->page_size;
+  if (rows >= (1ull << 31)) return KVQ_ERR_UNSUPPORTED;
+  PrefillArgs a{};
+  a.c = *cache;
+  a.q = q;
+  a.dtype = dtype;
+  a.n_q = n_q;
+  a.Hq = num_q_heads;
+  a.group = num_q_heads / cache->num_kv_heads;
+  a.q_start = q_start;
+  a.block_table = d_block_table;
+  a.max_pages = max_pages;
+  a.qscale = sm_scale * kLog2e;
+  a.status = d_status;
+  a.rotate = cache->format == KVQ_FMT_Q4_HAD32 ? 1 : 0;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.ws_m = reinterpret_cast<float*>(ws + w.m_off);
+  a.ws_z = reinterpret_cast<float*>(ws + w.z_off);
+  a.ws_acc = reinterpret_cast<float*>(ws + w.acc_off);
+  a.splits = w.splits;
+  if (!encode_rows_map(&a.tm_k, cache->k, rows, 128, 16) || !encode_rows_map(&a.tm_v, cache->v, rows, 128, 16))
+    return cuda_fail(cudaErrorInvalidValue);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_prefill_tc(a, s);
+  if (e == cudaSuccess) e = launch_prefill_diff_merge(a, d, s);
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
 int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_t width, const float* d_lambda,
                        int64_t lambda_stride, const kvq_norm* norm, float out_scale, void* out, int32_t out_dtype,
                        void* stream) {

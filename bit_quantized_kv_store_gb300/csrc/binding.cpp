@@ -33,6 +33,8 @@ decltype(&kvq_load) p_load;
 decltype(&kvq_load_seqs) p_load_seqs;
 decltype(&kvq_merge_diff) p_merge_diff;
 decltype(&kvq_diff_heads) p_diff_heads;
+decltype(&kvq_prefill_diff_workspace_size) p_prefill_diff_workspace_size;
+decltype(&kvq_prefill_diff) p_prefill_diff;
 PyObject* raise_status;
 
 struct Refused {  // a Python error is set
@@ -406,13 +408,53 @@ PyObject* diff_heads(PyObject* const* a) {
   return given(a[4]) ? back(a[4]) : THPVariable_Wrap(out);
 }
 
+// prefill_diff(cache, q, q_start, block_table, sm_scale, lam, norm, out_scale, out, dtype, workspace, status)
+PyObject* prefill_diff(PyObject* const* a) {
+  const kvq_cache* c = cache_of(a[0]);
+  const at::Tensor &q = tensor(a[1], "q"), &bt = tensor(a[3], "block_table");
+  three(q, "q");
+  const int dev = device_of(q);
+  const int32_t qt = code_of(q.scalar_type(), "q");
+  if (!q.is_contiguous()) refuse(PyExc_ValueError, "q must be contiguous");
+  const int64_t n = q.size(0), Hq = q.size(1);
+  if (q.size(2) != c->head_dim || n > INT32_MAX || Hq > INT32_MAX)
+    refuse(PyExc_ValueError, "q must be [rows, heads, ", c->head_dim, "], got ", shape_of(q.sizes()));
+  on_device(bt, "block_table", dev);
+  of_type(bt, "block_table", at::kInt);
+  if (!bt.is_contiguous() || bt.numel() > INT32_MAX) refuse(PyExc_ValueError, "block_table must be contiguous");
+  const int32_t q_start = integer32(a[2], "q_start");
+  const at::Tensor out = diff_out(a[8], a[9], dev, n, Hq / 2, c->head_dim);
+  int64_t stride;
+  const float* lam = lambda_of(a[5], dev, n, Hq / 2, stride);
+  at::Tensor ws;
+  if (given(a[10])) {
+    ws = tensor(a[10], "workspace");
+    on_device(ws, "workspace", dev);
+    if (!ws.is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+  } else {
+    const size_t bytes = p_prefill_diff_workspace_size(c, static_cast<int32_t>(n), static_cast<int32_t>(Hq), q_start);
+    ws = at::detail::empty_cuda({static_cast<int64_t>(bytes)}, at::kByte,
+                                at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
+  }
+  checked(p_prefill_diff(c, q.data_ptr(), qt, static_cast<int32_t>(n), static_cast<int32_t>(Hq), q_start,
+                         static_cast<const int32_t*>(bt.data_ptr()), static_cast<int32_t>(bt.numel()),
+                         real(a[4], "sm_scale"), lam, stride, norm_of(a[6], "norm", dev, c->head_dim),
+                         real(a[7], "out_scale"), ws.data_ptr(), static_cast<size_t>(ws.numel()) * ws.element_size(),
+                         out.data_ptr(), code_of(out.scalar_type(), "out"), status_of(a[11], dev), stream_of(dev)),
+          "kvq_prefill_diff");
+  return given(a[8]) ? back(a[8]) : THPVariable_Wrap(out);
+}
+
 // init(addresses of the entry points, raise_status)
 PyObject* init(PyObject* const* a) {
   void** slots[] = {reinterpret_cast<void**>(&p_norm_rope), reinterpret_cast<void**>(&p_norm_rope_store),
                     reinterpret_cast<void**>(&p_load),      reinterpret_cast<void**>(&p_load_seqs),
-                    reinterpret_cast<void**>(&p_merge_diff), reinterpret_cast<void**>(&p_diff_heads)};
-  if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != 6) refuse(PyExc_TypeError, "six entry points");
-  for (int i = 0; i < 6; ++i) *slots[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
+                    reinterpret_cast<void**>(&p_merge_diff), reinterpret_cast<void**>(&p_diff_heads),
+                    reinterpret_cast<void**>(&p_prefill_diff_workspace_size),
+                    reinterpret_cast<void**>(&p_prefill_diff)};
+  constexpr int kEntries = sizeof(slots) / sizeof(slots[0]);
+  if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != kEntries) refuse(PyExc_TypeError, "bad entry points");
+  for (int i = 0; i < kEntries; ++i) *slots[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
   Py_INCREF(a[1]);
   Py_XDECREF(raise_status);
   raise_status = a[1];
@@ -449,6 +491,7 @@ PyMethodDef methods[] = {method<init, 2>("init"),
                          method<load_seqs, 10>("load_seqs"),
                          method<merge_diff, 13>("merge_diff"),
                          method<diff_heads, 6>("diff_heads"),
+                         method<prefill_diff, 12>("prefill_diff"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvq_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -288,6 +288,59 @@ cudaError_t launch_row(const MergeArgs& a, const DiffView& d, const void* signs,
   return launch_pdl(kern, dim3(a.Hq / 2, B), dim3(T), fixed + static_cast<size_t>(2) * a.P * 8, s, a, d, signs);
 }
 
+// The partials of a prompt chunk's ranges of keys, merged, subtracted and rotated
+// back: one warp per (row, output head), lane l holding values 8 l .. 8 l + 7 of the
+// head; ranges in ascending order.
+__global__ void __launch_bounds__(256) prefill_diff_merge_kernel(const __grid_constant__ PrefillArgs a, FastDiv hd,
+                                                                 int wide, const DiffView d) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int E = 8, W = 256;
+  const int lane = threadIdx.x & 31, heads = a.Hq / 2;
+  const uint32_t i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);  // row * output heads + head
+  if (i >= static_cast<uint32_t>(a.n_q) * heads) return;
+  const uint32_t row = fast_div(i, hd), h = i - row * hd.d;
+  const RowsView in{a.ws_acc, 0, 0, KVQ_DT_F32, 1};
+  const int64_t range = (int64_t)a.n_q * a.Hq;  // rows of a range
+  uint64_t y1[1][E / 2];
+  uint64_t(&y)[E / 2] = y1[0];
+#pragma unroll
+  for (int map = 0; map < 2; ++map) {
+    const int64_t r0 = 2 * (int64_t)i + map;
+    float M = -INFINITY;
+    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, a.ws_m[r0 + s * range]);
+    uint64_t o[E / 2];
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j) o[j] = pk2(0.f, 0.f);
+    float Z = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+      const int64_t r = r0 + s * range;
+      const float w = exp2f(a.ws_m[r] - M);  // NaN where the range's pages were bad
+      Z = fmaf(a.ws_z[r], w, Z);
+      RawRow<E, false> raw;
+      load_raw<E, false>(in, r * W, lane, raw);
+      uint64_t v[E / 2];
+      unpack_row<E, false>(raw, v);
+#pragma unroll
+      for (int j = 0; j < E / 2; ++j) o[j] = fma2(v[j], pk2(w, w), o[j]);
+    }
+    const float inv = __fdiv_rn(1.f, Z);
+    const float c = map == 0 ? inv : -d.lambda[row * d.stride + h] * inv;
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j) y[j] = map == 0 ? mul2(o[j], pk2(c, c)) : fma2(o[j], pk2(c, c), y[j]);
+  }
+  if (a.rotate) rotate_row_had32<E>(y, lane);
+  if (d.norm.weight) {
+    uint64_t w[E / 2];
+    load_weight<E>(d.norm, lane, w);
+    norm_rows<E, 32, 1>(y1, w, d.norm.eps);
+  }
+#pragma unroll
+  for (int j = 0; j < E / 2; ++j) y[j] = mul2(y[j], pk2(d.scale, d.scale));
+  const RowsView out{d.out, 0, 0, d.out_dtype, wide};
+  write_row<E>(out, (int64_t)i * W, lane, y);
+}
+
 // One warp per (row, output head); lane l holds elements E l .. E l + E - 1.
 template <int E>
 __global__ void __launch_bounds__(256) diff_heads_kernel(const float* __restrict__ x, int64_t n, FastDiv hd, int wide,
@@ -353,6 +406,15 @@ cudaError_t launch_merge_diff(const MergeArgs& a, const DiffView& d, const kvq_c
                   : cudaLaunchKernelEx(&cfg, merge_diff_kernel<8>, a, d, c.signs, whole);
   else
     e = cudaLaunchKernelEx(&cfg, merge_diff_kernel<4>, a, d, c.signs, whole);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_prefill_diff_merge(const PrefillArgs& a, const DiffView& d, cudaStream_t s) {
+  const int64_t n = (int64_t)a.n_q * (a.Hq / 2);
+  const int wide = (reinterpret_cast<uintptr_t>(d.out) & 31u) == 0 ? 1 : 0;
+  cudaError_t e = launch_pdl(prefill_diff_merge_kernel, dim3(static_cast<unsigned>((n + 7) / 8)), dim3(256), 0, s, a,
+                             make_fastdiv(static_cast<uint32_t>(a.Hq / 2)), wide, d);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

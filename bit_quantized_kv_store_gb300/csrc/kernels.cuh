@@ -106,6 +106,13 @@ struct PrefillArgs {
   float* out;
   int32_t* status;
   int rotate;  // 1: Hadamard format (rotate q, rotate the output back); 0: Q4_0
+  // ws_acc given: `splits` ranges of keys, and instead of the output every range's
+  // partial maxima and sums [splits][n_q][Hq] and contexts [splits][n_q][Hq][256]
+  // (unnormalised, in the cache's space)
+  float* ws_m;
+  float* ws_z;
+  float* ws_acc;
+  int splits;
 };
 
 // Strided activation rows (a kvq_rows as the kernels take it).
@@ -239,6 +246,10 @@ cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);
 // The merge of two maps' partials with their difference (tq: TQ4 rows), and the
 // difference of merged heads (diff.cu).
 cudaError_t launch_merge_diff(const MergeArgs& a, const DiffView& d, const kvq_cache& c, int B, cudaStream_t s);
+// The merge of a prompt chunk's partials with the difference of its maps (diff.cu),
+// and into how many ranges of keys they come (prefill_tc.cu).
+cudaError_t launch_prefill_diff_merge(const PrefillArgs& a, const DiffView& d, cudaStream_t s);
+int prefill_splits(int n_q, int Hq, int Hk, int q_start, int n_sm);
 cudaError_t launch_diff_heads(const float* x, int64_t rows, int Hq, int width, const DiffView& d, cudaStream_t s);
 
 }  // namespace kvq

@@ -454,7 +454,7 @@ cudaError_t launch_load(const LoadArgs& args, cudaStream_t s) {
     // once.  hpu: the one whose rounds cost least, a round its heads' work and about
     // one head's for the unit itself (4096 tokens of 4 heads: one round and a bit of
     // 4 heads would be two).
-    const int64_t resident = (int64_t)device_sm_count() * load_ctas(a.c.format);
+    const int64_t n_sm = device_sm_count() > 0 ? device_sm_count() : 1, resident = n_sm * load_ctas(a.c.format);
     const int64_t blocks8 = (n_tok * NG + 7) / 8;
     int hpu = 1;
     int64_t best = 0;

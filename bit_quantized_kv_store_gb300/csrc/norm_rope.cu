@@ -344,7 +344,7 @@ cudaError_t launch_one(NormRopeArgs a, cudaStream_t s) {
   // that leaves SMs without one.
   constexpr int RPW = 32 / LPR;
   const int64_t total = (a.Hq + RPW - 1) / RPW + 2 * ((a.Hk + RPW - 1) / RPW);
-  const int64_t n_sm = device_sm_count(), resident = n_sm * kMinCtas * kMaxWarps, all_batches = a.n_tok * total;
+  const int64_t n_sm = device_sm_count() > 0 ? device_sm_count() : 1, resident = n_sm * kMinCtas * kMaxWarps, all_batches = a.n_tok * total;
   int64_t per = (all_batches + resident - 1) / resident;
   if (per > 1) per = (per + 1) / 2 * 2;
   a.per = per;

@@ -186,7 +186,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
   const int q0 = qb * qpb;
   const int nq_blk = min(qpb, a.n_q - q0);
   const int kmax = a.q_start + q0 + nq_blk;  // keys [0, kmax)
-  const int ntiles = (kmax + kPfKeys - 1) / kPfKeys;
+  // this CTA's tiles: one of the grid's gridDim.z ranges of them (no range is empty:
+  // the launch has at most as many as the first block has tiles)
+  const int all_tiles = (kmax + kPfKeys - 1) / kPfKeys;
+  const int tile0 = static_cast<int>((int64_t)all_tiles * blockIdx.z / gridDim.z);
+  const int ntiles = static_cast<int>((int64_t)all_tiles * (blockIdx.z + 1) / gridDim.z) - tile0;
+  const int kbase = tile0 * kPfKeys;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPfStages; ++s) {
@@ -221,15 +226,37 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
     const int iq = r / grp, h = r % grp;
     const bool valid = (r < qpb * grp) && (iq < nq_blk);
     const int64_t qrow = ((int64_t)(q0 + iq) * a.Hq + kvh * grp + h) * kPfDim;
+    // by 16 bytes at a time (a warp's loads touch 32 rows, a line each, whatever their
+    // width: value by value they took about 16 us of every CTA)
+    const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0;
     for (int G = 0; G < 8; ++G) {
       float x[32];
+      if (!valid) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float v = 0.f;
-        if (valid)
-          v = a.dtype == KVQ_DT_F32 ? static_cast<const float*>(a.q)[qrow + 32 * G + i]
-                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[qrow + 32 * G + i]);
-        x[i] = v;
+        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+      } else if (!vec) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = load_act(a.q, a.dtype, qrow + 32 * G + i);
+      } else if (a.dtype == KVQ_DT_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 v = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + qrow + 32 * G)[i];
+          x[4 * i] = v.x;
+          x[4 * i + 1] = v.y;
+          x[4 * i + 2] = v.z;
+          x[4 * i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + qrow + 32 * G)[i];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = word_at(v, j);
+            x[8 * i + 2 * j] = __uint_as_float(w << 16);
+            x[8 * i + 2 * j + 1] = __uint_as_float(w & 0xFFFF0000u);
+          }
+        }
       }
       const bool rot = a.rotate != 0;  // Q4_0: the query as given
       if (rot) fwht32_regs(x);
@@ -273,7 +300,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
         uint32_t bytes = 0;
         for (int pg = 0; pg < 4; ++pg) {
           rows[pg] = -1;
-          const int key0 = j * kPfKeys + 16 * pg;
+          const int key0 = kbase + j * kPfKeys + 16 * pg;
           if (key0 >= kmax) continue;
           const int32_t page = bt[key0 / c.page_size];
           if (page < 0 || page >= c.num_pages) {
@@ -373,7 +400,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
       if (!ok) break;
       tc_fence_after();
       const uint32_t sadr = tbase + lane_off + kTmS + 64 * b;
-      const int lim = valid ? qpos - j * kPfKeys : -1;  // keys i <= lim of this tile are visible
+      const int lim = valid ? qpos - kbase - j * kPfKeys : -1;  // keys i <= lim of this tile are visible
       // pass 1: the row maximum over the visible keys, 16 columns at a time
       float tmax = -INFINITY;
 #pragma unroll 1
@@ -439,7 +466,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
     if (ok) {
       tc_fence_after();
       const bool bad = sm.poison != 0 || sm.abort != 0;
-      const float inv = (z > 0.f) ? 1.f / z : 0.f;
+      const bool part = a.ws_acc != nullptr;  // a partial: as it is, in the cache's space
+      const float inv = part ? 1.f : (z > 0.f) ? 1.f / z : 0.f;
+      const int64_t prow_i = (((int64_t)blockIdx.z * a.n_q + q0 + iq) * a.Hq + kvh * grp + h);
+      if (part && valid) {
+        a.ws_m[prow_i] = bad ? NAN : m_run;
+        a.ws_z[prow_i] = z;
+      }
       for (int G = 0; G < 8; ++G) {
         uint32_t o[32];
         __syncwarp();  // reconverge after the previous iteration's per-row store
@@ -448,14 +481,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
         float x[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * inv;
-        const bool rot = a.rotate != 0;  // Q4_0: nothing to rotate back
+        const bool rot = a.rotate != 0 && !part;  // Q4_0: nothing to rotate back
         if (rot) {
           fwht32_regs(x);
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = __fmul_rn(x[i], kHadamardScale);
         }
         if (valid) {
-          float* dst = a.out + ((int64_t)(q0 + iq) * a.Hq + kvh * grp + h) * kPfDim + 32 * G;
+          float* dst = (part ? a.ws_acc + prow_i * kPfDim
+                             : a.out + ((int64_t)(q0 + iq) * a.Hq + kvh * grp + h) * kPfDim) + 32 * G;
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4*>(dst + i) =
@@ -477,7 +511,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
       const int s = j % kPfStages;
       if (!pf_wait_warp(sm, &sm.rawk_full[s], (j / kPfStages) & 1, a.status)) break;
       const uint32_t st_codes = smem_u32(sm.rawk[s].codes), st_scales = smem_u32(sm.rawk[s].scales);
-      const int jk0 = j * kPfKeys;
+      const int jk0 = kbase + j * kPfKeys;
       for (int half = 0; half < 2; ++half) {
         // QK(j-1) has read this half of K_a, K_b
         if (j > 0 && !pf_wait_warp(sm, &sm.k_free[half], (j - 1) & 1, a.status)) {
@@ -530,7 +564,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
       if (!pf_wait_warp(sm, &sm.rawv_full[s], (j / kPfStages) & 1, a.status)) break;
       if (j > 0 && !pf_wait_warp(sm, &sm.pv_done, (j - 1) & 1, a.status)) break;  // PV(j-1) is done with vt
       const uint32_t st_codes = smem_u32(sm.rawv[s].codes), st_scales = smem_u32(sm.rawv[s].scales);
-      const int jk0 = j * kPfKeys;
+      const int jk0 = kbase + j * kPfKeys;
 #pragma unroll 1
       for (int kbl = 0; kbl < 2; ++kbl) {
         const int kbk = 2 * vw + kbl;
@@ -567,13 +601,35 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
   if (warp == 1) tmem_dealloc(tbase, 512);
 }
 
+// Ranges of keys that a prompt chunk is cut into when its partials are merged
+// afterwards (kvq_prefill_diff).  One CTA takes 128 / group query positions of a KV
+// head, and a chunk of 1024 at depth 4096 is 196 CTAs on 152 SMs: two waves, the
+// second a quarter full.  The count that costs least, in the time of a 64-key tile
+// (2.3 us): the waves' tiles, 5 for a CTA's start and end, and the partials written
+// and read back (2 KB a row at about 5 TB/s).  Measured at that size: 395 us in one
+// range, 305 us in three.
+int prefill_splits(int n_q, int Hq, int Hk, int q_start, int n_sm) {
+  const int qpb = 128 / (Hq / Hk);
+  const int64_t ctas = (int64_t)((n_q + qpb - 1) / qpb) * Hk;
+  const int first = (q_start + (n_q < qpb ? n_q : qpb) + kPfKeys - 1) / kPfKeys;  // the first block's tiles
+  const int last = (q_start + n_q + kPfKeys - 1) / kPfKeys;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= 32 && s <= first; ++s) {
+    const int64_t waves = (ctas * s + n_sm - 1) / n_sm;
+    const double cost = waves * ((double)((last + s - 1) / s) + 5) + s * ((double)n_q * Hq * 1.7e-4);
+    if (s == 1 || cost < least) least = cost, best = s;
+  }
+  return best;
+}
+
 cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t s) {
   if (a.n_q == 0) return cudaSuccess;
   const size_t smem = sizeof(PfSmem) + 1024;
   cudaError_t e = set_max_smem_once<prefill_tc_kernel>(static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int qpb = 128 / a.group;
-  dim3 grid((a.n_q + qpb - 1) / qpb, a.c.num_kv_heads);
+  dim3 grid((a.n_q + qpb - 1) / qpb, a.c.num_kv_heads, a.ws_acc ? a.splits : 1);
   e = launch_pdl(prefill_tc_kernel, grid, dim3(kPfThreads), smem, s, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

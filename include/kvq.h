@@ -546,8 +546,31 @@ int32_t kvq_merge_diff(const kvq_cache* cache, const void* workspace, size_t ws_
                        int32_t rotate_back, const float* d_lambda, int64_t lambda_stride, const kvq_norm* norm,
                        float out_scale, void* out, int32_t out_dtype, void* stream);
 
+/* Size in bytes of the workspace kvq_prefill_diff needs on the current device (0 for
+ * a shape it refuses): partials of every row and query head for each of the ranges
+ * that the keys are cut into. */
+size_t kvq_prefill_diff_workspace_size(const kvq_cache* cache, int32_t n_q, int32_t num_q_heads, int32_t q_start);
+
+/* kvq_prefill_diff -- differential attention of a prompt chunk: kvq_prefill_attn of
+ * both maps and their difference.  The keys are cut into ranges so that a chunk of
+ * few rows still fills the GPU; the ranges' partials go to the workspace and are
+ * merged in order, subtracted, rotated back, normed and scaled by a second kernel.
+ * (The number of ranges depends on the chunk's size and depth: a row's value in
+ * chunks of other sizes is the same up to rounding.)
+ *   q, dtype, n_q, num_q_heads, q_start, d_block_table, max_pages, sm_scale,
+ *       d_status as for kvq_prefill_attn, num_q_heads / num_kv_heads 2, 4, 6 or 8.
+ *   workspace: device, 32-byte aligned; its contents do not matter.
+ *   out: device [n_q][num_q_heads / 2][256] of out_dtype.  Rows that meet a page
+ *       outside the pool come out NaN (KVQ_DEV_BAD_PAGE).
+ * Q4_HAD32 and Q4_0, head_dim 256. */
+int32_t kvq_prefill_diff(const kvq_cache* cache, const void* q, int32_t dtype, int32_t n_q, int32_t num_q_heads,
+                         int32_t q_start, const int32_t* d_block_table, int32_t max_pages, float sm_scale,
+                         const float* d_lambda, int64_t lambda_stride, const kvq_norm* norm, float out_scale,
+                         void* workspace, size_t ws_bytes, void* out, int32_t out_dtype, int32_t* d_status,
+                         void* stream);
+
 /* kvq_diff_heads -- the same difference of heads already merged and rotated back
- * (kvq_prefill_attn's output): x: device fp32 [rows][num_q_heads][width],
+ * (kvq_prefill_attn's or kvq_decode_merged's output): x: device fp32 [rows][num_q_heads][width],
  * contiguous, num_q_heads even, width 64, 128, 256 or 512.  out must not overlap
  * x. */
 int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_t width, const float* d_lambda,

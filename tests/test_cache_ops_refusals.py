@@ -211,7 +211,36 @@ def test_differential_refusals(K):
     assert heads(Hq=0) == K.ERR_INVALID_ARG
     assert heads(Hq=23) == K.ERR_INVALID_ARG
     assert heads(w=96) == K.ERR_UNSUPPORTED
-    for f in (merge, heads):
+    wp = L.kvq_prefill_diff_workspace_size(p(c), 4, 24, 40)
+    assert wp >= 4 * 24 * 258 * 4
+
+    def prefill(c=c, q=DUMMY, dt=0, n=4, Hq=24, q0=40, bt=DUMMY, mp=4, lam=DUMMY, ls=12, nm=None, sc=1.0, wsp=DUMMY,
+                wsb=wp, out=DUMMY, od=0):
+        return L.kvq_prefill_diff(p(c), q, dt, n, Hq, q0, bt, mp, 0.1, lam, ls, p(nm), sc, wsp, wsb, out, od, None, None)
+
+    assert prefill(c=None) == K.ERR_INVALID_ARG
+    assert prefill(c=_desc(K, fmt=1)) == K.ERR_UNSUPPORTED
+    assert prefill(c=_tq4_desc(K)) == K.ERR_UNSUPPORTED
+    assert prefill(c=_desc(K, D=128)) == K.ERR_UNSUPPORTED
+    assert prefill(Hq=12) == K.ERR_UNSUPPORTED
+    assert prefill(Hq=40) == K.ERR_UNSUPPORTED
+    assert prefill(Hq=26) == K.ERR_INVALID_ARG
+    assert prefill(n=-1) == K.ERR_INVALID_ARG
+    assert prefill(n=0) == K.OK
+    assert prefill(q0=-1) == K.ERR_INVALID_ARG
+    assert prefill(q0=61) == K.ERR_INVALID_ARG                             # past the block table
+    assert prefill(n=1 << 27, Hq=32, mp=1 << 30) == K.ERR_UNSUPPORTED
+    assert prefill(q=None) == K.ERR_INVALID_ARG
+    assert prefill(q=DUMMY + 2) == K.ERR_INVALID_ARG
+    assert prefill(dt=2) == K.ERR_INVALID_ARG
+    assert prefill(bt=None) == K.ERR_INVALID_ARG
+    assert prefill(mp=0) == K.ERR_INVALID_ARG
+    assert prefill(wsp=None) == K.ERR_INVALID_ARG
+    assert prefill(wsp=DUMMY + 16) == K.ERR_INVALID_ARG
+    assert prefill(wsb=wp - 1) == K.ERR_WORKSPACE_TOO_SMALL
+    assert L.kvq_prefill_diff_workspace_size(p(c), 4, 12, 40) == 0
+    assert L.kvq_prefill_diff_workspace_size(None, 4, 24, 40) == 0
+    for f in (merge, heads, prefill):
         assert f(lam=None) == K.ERR_INVALID_ARG
         assert f(lam=DUMMY + 1) == K.ERR_INVALID_ARG
         assert f(ls=-1) == K.ERR_INVALID_ARG

@@ -725,18 +725,65 @@ def test_decode_diff_against_the_oracle(K, fmt):
     assert (np.abs(got - want) <= 2e-3 * big * (1 + lam.numpy()[:, None])).all()
 
 
-def test_prefill_diff_is_the_difference_of_the_prefill(K):
-    T0, n, Hk, Hq = 100, 37, 4, 24
-    cache = make_cache(K, K.FMT_Q4_HAD32, Hk, 256, 10)
-    k, v = rnd((T0 + n, Hk, 256), "pd k"), rnd((T0 + n, Hk, 256), "pd v")
-    K.store(cache, k, v, torch.arange(T0 + n, dtype=torch.int32, device=DEV))
-    q = rnd((n, Hq, 256), "pd q", dtype=torch.bfloat16)
-    bt = torch.arange(10, dtype=torch.int32, device=DEV)
-    lam = torch.rand(n, 12, device=DEV)
-    w = K.Norm(rnd((256,), "pd w"), 1e-5)
-    o = K.prefill_attn(cache, q, T0, bt, 1 / 16)
-    assert torch.equal(K.prefill_diff(cache, q, T0, bt, 1 / 16, lam, norm=w, out_scale=0.8),
-                       K.diff_heads(o, lam, norm=w, out_scale=0.8))
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "Q4_0"])
+@pytest.mark.parametrize("T0,n,Hk,group", [(0, 1, 4, 6), (0, 70, 1, 2), (100, 37, 4, 6), (1500, 16, 2, 8), (2000, 130, 1, 4),
+                                           (63, 300, 8, 6), (4000, 1000, 4, 6)])
+def test_prefill_diff_against_64_bits(K, fmt, T0, n, Hk, group):
+    """Chunks of one row to many, cut into one to 32 ranges of keys, against 64-bit
+    attention over the same rows; each map within the prefill's 2e-3 of its largest output."""
+    Hq = Hk * group
+    pages = (T0 + n + 15) // 16 + 2
+    cache = make_cache(K, getattr(K, "FMT_" + fmt), Hk, 256, pages)
+    k, v = rnd((T0 + n, Hk, 256), "pd k", n), rnd((T0 + n, Hk, 256), "pd v", n)
+    perm = synth.page_permutation(pages, "pd", n).to(torch.int32).to(DEV)
+    at = torch.arange(T0 + n, device=DEV)
+    slots = (perm.long()[at // 16] * 16 + at % 16).to(torch.int32)
+    K.store(cache, k, v, slots)
+    q = rnd((n, Hq, 256), "pd q", n, dtype=torch.bfloat16, scale=2.0)
+    lam = torch.rand(n, Hq // 2, device=DEV)
+    w = rnd((256,), "pd w")
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    rk, rv = (x.double() for x in K.load(cache, slots, dtype=torch.float32))
+    rows = sorted({0, n - 1, n // 2, n // 3, min(n - 1, 21), min(n - 1, 64)})
+    ref = []
+    for i in rows:
+        p = torch.softmax(torch.einsum("hd,thd->ht", q[i].double(), rk[:T0 + i + 1].repeat_interleave(group, 1)) / 16, -1)
+        ref.append(torch.einsum("ht,thd->hd", p, rv[:T0 + i + 1].repeat_interleave(group, 1)))
+    ref = torch.stack(ref)
+    for norm, scale in ((None, 1.0), (K.Norm(w, 1e-5), 0.8)):
+        got = K.prefill_diff(cache, q, T0, perm, 1 / 16, lam, norm=norm, out_scale=scale, status=status)
+        assert got.shape == (n, Hq // 2, 256) and torch.isfinite(got).all()
+        y = diff64(ref, lam[rows], None, 0.0, 1.0, K)
+        want = diff64(ref, lam[rows], norm, 0.0, scale, K)
+        e = 2e-3 * ref.abs().amax((1, 2), keepdim=True) * (1 + lam[rows].double()[..., None])
+        tol = e * scale
+        if norm is not None:
+            r = 1 / torch.sqrt((y * y).mean(-1, keepdim=True) + norm.eps)
+            tol = tol * w.double().abs() * r * (1 + y.abs() * r)
+        assert ((got[rows].double() - want).abs() <= tol).all()
+        # a workspace of the caller's, bf16, one lambda row for all
+        ws = torch.empty(K.lib().kvq_prefill_diff_workspace_size(cache.ref, n, Hq, T0), dtype=torch.uint8, device=DEV)
+        one = K.prefill_diff(cache, q, T0, perm, 1 / 16, lam[0].contiguous(), norm=norm, out_scale=scale, workspace=ws)
+        bf = K.prefill_diff(cache, q, T0, perm, 1 / 16, lam[:1].expand(n, -1).contiguous(), norm=norm, out_scale=scale,
+                            dtype=torch.bfloat16)
+        assert torch.equal(one.bfloat16(), bf)
+    assert K.read_status(status) == 0
+    if n > 1:
+        with pytest.raises(K.KvqError):
+            K.prefill_diff(cache, q, T0, perm, 1 / 16, lam, workspace=ws[:-1].clone())
+
+
+def test_prefill_diff_bad_page(K):
+    """Rows that attend a page outside the pool come out NaN, rows before it do not."""
+    cache = make_cache(K, K.FMT_Q4_HAD32, 4, 256, 200)
+    fill_random(cache, K, 3)
+    n, T0 = 30, 3000
+    bt = torch.arange(200, dtype=torch.int32, device=DEV)
+    bt[40] = 4000
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q = rnd((n, 24, 256), "bp q", scale=0.1)
+    out = K.prefill_diff(cache, q, T0, bt, 1 / 16, torch.rand(12, device=DEV), status=status)
+    assert torch.isnan(out).all() and K.read_status(status) == K.DEV_BAD_PAGE
 
 
 # ------------------------------------------------------------------ a run of them together
