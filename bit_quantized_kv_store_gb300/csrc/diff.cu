@@ -11,6 +11,9 @@
 // 24 GB card)", section "What it is", with the subtraction before the rotation
 // back (the rotation is linear, so it runs once instead of twice) and the norm on
 // the result, without the merged heads going through memory.
+//
+// Bound: latency (one 32769-token sequence: 3.5 us after the decode's 12.7, the
+// partials 1.6 MB in L2; a ragged batch of 32 up to 8000: 5.5 us after 63, 12.6 MB).
 #include "merge_fold.cuh"
 #include "rows.cuh"
 #include "tq4_code.cuh"
@@ -120,17 +123,17 @@ __global__ void __launch_bounds__(512) merge_diff_kernel(const MergeArgs a, cons
   }
 }
 
-// Many heads, or few partitions: one CTA of 512 threads per (output head,
-// sequence).  The fold's arithmetic (merge_fold.cuh) in another arrangement, with
+// Many heads, or few partitions: one CTA of T threads per (output head, sequence).  The fold's arithmetic (merge_fold.cuh) in another arrangement, with
 // the same bits: the running maximum of row r of 32 (partitions r, r + 32, ...)
 // does not depend on the values, so one warp per map works out the rescaling
 // weights of every partition once; the other dimension, 64 chunks of 4 values in
-// 8 groups of 4 rows, is then plain multiply-adds over coalesced loads, the first
-// of which are in flight meanwhile.  (A cluster of 8 CTAs for each head of a batch
-// of 32 sequences of up to 8000 keys took 30 us of a 99 us decode: 3072 CTAs, each
-// with its own barriers for 32 KB of partials.)
-// T threads: 512, or 256 for at most 16 partitions (rows 16 .. 31 are empty), which
-// lets three CTAs share an SM instead of one.
+// T / 64 groups of 4 rows, is then plain multiply-adds over coalesced loads, the
+// first of which are in flight meanwhile.  T: 512, or 256 for at most 16 partitions
+// (rows 16 .. 31 are empty), which lets three CTAs share an SM instead of one.
+// A batch of 32 sequences of up to 8000 keys, 16 partitions a head: 5.5 us; 12 us
+// with 512 threads, 30 us with the cluster of 8 CTAs a head (3072 CTAs, each with
+// its own barriers for 32 KB of partials).  One sequence's 12 heads of 65 partitions:
+// 6.8 us here, 4.8 us there (the wait for the decode included).
 constexpr int kRowMaxP = 1024;  // partitions whose weights fit in shared memory
 
 template <int T>

@@ -6,7 +6,7 @@
 // log-sum-exp merge kernel over the (m, z, cl) partials).
 //
 // One CTA of 256 threads per (32 output values, query head, sequence), one
-// pass over the partials.  Thread (row r = tid / 8, chunk c = tid % 8) takes
+// pass over the partials (merge_fold.cuh).  Thread (row r = tid / 8, chunk c = tid % 8) takes
 // partitions r, r + 32, r + 64, ... in ascending order: it loads their m (and,
 // for c == 0, z) and the float4 chunk c of their acc, four (or eight)
 // partitions per batch with every load of a batch issued before any use, and keeps a running

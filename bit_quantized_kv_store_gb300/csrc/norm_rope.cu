@@ -18,13 +18,22 @@
 //
 // A lane holds 16 consecutive elements of a row (32 bytes of bf16, one load), so a
 // row of 256 lies over 16 lanes and a warp works on two heads of its token at once
-// (D = 64, 128, 512: eight, four, one): against one row for a whole warp (183
-// instructions a row of 256, 24.7 us for 4099 tokens of 24 heads) the reductions,
-// the butterflies across lanes and the addressing are shared by more rows.  A warp
-// takes `hpw` heads of one token, one batch after another with the next one's loads
-// in flight; the angles (the same for every head) are computed once per warp,
-// spread over its lanes, and read back from shared memory.  Bound: memory for a
-// prompt chunk, the launch for a decode step.
+// (D = 64, 128, 512: eight, four, one); with a row over the whole warp, 8 elements
+// to a lane, a row took 183 instructions (now 92) and 4099 tokens of 24 heads
+// 24.7 us, since the reductions, the butterflies across lanes and the addressing
+// were shared by fewer rows.  The angles (the same for every head) are worked out
+// once per token and warp, spread over its lanes, and read back from shared memory.
+//
+// Bound.  4099 x 24 heads of 256, bf16 to bf16 with norm and three axes: 18.7 us, 101
+// MB, 5.4 TB/s (80 % of the measured copy; the same kernel without norm and rotation
+// takes as long, so what is left is filling and draining the memory pipe).  4096
+// tokens of 24 + 4 + 4 heads to rotated fp32 queries and 4-bit rows: 38.5 us, 172 MB,
+// 4.5 TB/s; 31 us without the norm, the rotations and the codes' arithmetic, the
+// rest is issue (20.2 M instructions at 51 %).  One token: the launch.
+// Measured and not kept: K and V rows two batches side by side like the queries'
+// (spills; the 4096-token chunk with its read-back 43.9 -> 49.8 us), one batch at
+// 80 registers and 24 warps an SM (49.7 us), five CTAs of four warps at 102
+// registers (53.7 us).
 //
 // This translation unit is compiled with -fmad=false.
 #include "rows.cuh"
@@ -36,7 +45,7 @@ namespace {
 
 constexpr int kNoStore = -1;
 constexpr int kMaxPairs = 128;
-constexpr int kMaxWarps = 4, kMinCtas = 4;  // 128 registers
+constexpr int kMaxWarps = 4, kMinCtas = 4;  // of a CTA, and CTAs of an SM (128 registers)
 constexpr int E = 16;  // elements of a lane
 
 // cos and sin of the token's rotary pairs, once per warp, in shared memory: chunk c of
@@ -344,7 +353,8 @@ cudaError_t launch_one(NormRopeArgs a, cudaStream_t s) {
   // that leaves SMs without one.
   constexpr int RPW = 32 / LPR;
   const int64_t total = (a.Hq + RPW - 1) / RPW + 2 * ((a.Hk + RPW - 1) / RPW);
-  const int64_t n_sm = device_sm_count() > 0 ? device_sm_count() : 1, resident = n_sm * kMinCtas * kMaxWarps, all_batches = a.n_tok * total;
+  const int64_t n_sm = device_sm_count() > 0 ? device_sm_count() : 1;
+  const int64_t resident = n_sm * kMinCtas * kMaxWarps, all_batches = a.n_tok * total;
   int64_t per = (all_batches + resident - 1) / resident;
   if (per > 1) per = (per + 1) / 2 * 2;
   a.per = per;

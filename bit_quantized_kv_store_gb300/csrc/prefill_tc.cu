@@ -605,9 +605,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
 // afterwards (kvq_prefill_diff).  One CTA takes 128 / group query positions of a KV
 // head, and a chunk of 1024 at depth 4096 is 196 CTAs on 152 SMs: two waves, the
 // second a quarter full.  The count that costs least, in the time of a 64-key tile
-// (2.3 us): the waves' tiles, 5 for a CTA's start and end, and the partials written
-// and read back (2 KB a row at about 5 TB/s).  Measured at that size: 395 us in one
-// range, 305 us in three.
+// (2.2 us): the waves' tiles, 7 for a CTA's start and end, and the partials written
+// and read back (2 KB a row at about 5 TB/s).  Measured, merge included: 1024 rows
+// at 4096 in three ranges 314 us, 64 rows at 4000 in eight 42 us; the prefill alone
+// in one range 365 and 159 us.
 int prefill_splits(int n_q, int Hq, int Hk, int q_start, int n_sm) {
   const int qpb = 128 / (Hq / Hk);
   const int64_t ctas = (int64_t)((n_q + qpb - 1) / qpb) * Hk;
@@ -617,7 +618,7 @@ int prefill_splits(int n_q, int Hq, int Hk, int q_start, int n_sm) {
   double least = 0;
   for (int s = 1; s <= 32 && s <= first; ++s) {
     const int64_t waves = (ctas * s + n_sm - 1) / n_sm;
-    const double cost = waves * ((double)((last + s - 1) / s) + 5) + s * ((double)n_q * Hq * 1.7e-4);
+    const double cost = waves * ((double)((last + s - 1) / s) + 7) + s * ((double)n_q * Hq * 1.7e-4);
     if (s == 1 || cost < least) least = cost, best = s;
   }
   return best;

@@ -58,10 +58,10 @@ typedef enum {
 
 /* Bits of the device status word (int32, caller-owned, zero it before use). */
 enum {
-  KVQ_DEV_BAD_SLOT = 1,      /* store: slot outside the pool */
+  KVQ_DEV_BAD_SLOT = 1,      /* store, load: slot outside the pool */
   KVQ_DEV_BAD_PAGE = 2,      /* a block-table entry outside [0, num_pages) */
-  KVQ_DEV_BAD_LENGTH = 4,    /* a sequence length < 0 or > the stated maximum */
-  KVQ_DEV_BAD_INDEX = 8,     /* a selected index outside [0, seq_len) */
+  KVQ_DEV_BAD_LENGTH = 4,    /* a sequence length < 0 or > the stated maximum; a position outside its table */
+  KVQ_DEV_BAD_INDEX = 8,     /* a selected index outside [0, seq_len); a rope axis past num_axes */
   KVQ_DEV_TIMEOUT = 16       /* a bounded wait on an asynchronous copy gave up */
 };
 

@@ -101,9 +101,9 @@ def rotated_back64(cache, x, K):
     return x
 
 
-def make_cache(K, fmt, Hk, D, pages, seed=0):
+def make_cache(K, fmt, Hk, D, pages, seed=0, ps=16):
     signs = synth.sign_mask(D, "cache_ops", seed) if fmt == K.FMT_TQ4 else None
-    return K.Cache(fmt, Hk, D, 16, pages, rope_dim=64 if fmt == K.FMT_FP8_ROW else 0, signs=signs)
+    return K.Cache(fmt, Hk, D, ps, pages, rope_dim=64 if fmt == K.FMT_FP8_ROW else 0, signs=signs)
 
 
 def fill_random(cache, K, seed):
@@ -151,7 +151,7 @@ NORM_ROPE_U = 26
 
 
 @pytest.mark.parametrize("width,rot,interleaved", [(64, 64, 0), (64, 32, 0), (64, 16, 0), (64, 6, 1), (128, 48, 0), (256, 240, 0), (128, 128, 1), (128, 96, 0),
-                                                   (256, 64, 0), (256, 256, 0), (256, 96, 0), (256, 250, 1),
+                                                   (256, 64, 0), (256, 256, 0), (256, 96, 0), (256, 250, 1), (64, 2, 1), (512, 16, 0),
                                                    (512, 256, 0), (512, 64, 1)])
 @pytest.mark.parametrize("n,heads,axes", [(1, 1, 1), (1, 24, 3), (7, 3, 4), (300, 5, 2), (3001, 9, 3)])
 @pytest.mark.parametrize("xt,yt", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32),
@@ -367,16 +367,13 @@ def check_values(got, want):
     assert (err <= tol + 2.0 ** -133).all(), f"{(err / (tol + 1e-300)).max().item()} of the tolerance"
 
 
-@pytest.mark.parametrize("fmt,D", [("Q4_HAD32", 32), ("Q4_HAD32", 64), ("Q4_HAD32", 128), ("Q4_HAD32", 256),
-                                   ("Q4_0", 32), ("Q4_0", 256), ("TQ4", 64), ("TQ4", 128), ("TQ4", 256), ("BF16", 96),
-                                   ("BF16", 256), ("FP8_ROW", 512), ("FP8_ROW", 32)])
-@pytest.mark.parametrize("Hk", [1, 3, 8])
+@pytest.mark.parametrize("fmt,D,Hk", [(f, D, Hk) for f, D in (
+    ("Q4_HAD32", 32), ("Q4_HAD32", 64), ("Q4_HAD32", 128), ("Q4_HAD32", 256), ("Q4_0", 32), ("Q4_0", 256), ("TQ4", 64),
+    ("TQ4", 128), ("TQ4", 256), ("BF16", 96), ("BF16", 256)) for Hk in (1, 3, 8)] + [("FP8_ROW", 512, 1), ("FP8_ROW", 32, 1)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_load_against_64_bits(K, fmt, D, Hk, dtype):
     f = getattr(K, "FMT_" + fmt)
     fp8 = f == K.FMT_FP8_ROW
-    if fp8 and Hk > 1:
-        pytest.skip("fp8 latent rows have one head")
     cache = make_cache(K, f, Hk, D, 9)
     fill_random(cache, K, D * 10 + Hk)
     n = 133
@@ -514,6 +511,76 @@ def test_load_seqs_ragged(K, fmt):
                        k=torch.full((3, Hk, want.shape[-1]), 2.0, dtype=torch.bfloat16, device=DEV))
     assert (e == 2).all()
     K.load_seqs(*args, 0)
+
+
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "TQ4", "BF16"])
+@pytest.mark.parametrize("ps", [48, 256])
+def test_other_page_sizes(K, fmt, ps):
+    """Pages of 48 and 256 slots: stored and loaded as in a cache of 16-slot pages."""
+    f, n, Hk, D = getattr(K, "FMT_" + fmt), 700, 3, 128
+    pages = n // ps + 3
+    a, b = make_cache(K, f, Hk, D, pages, ps=ps), make_cache(K, f, Hk, D, n // 16 + 1)
+    q, k, v = rnd((n, 6, D), "ps q"), rnd((n, Hk, D), "ps k"), rnd((n, Hk, D), "ps v")
+    perm = synth.page_permutation(pages, "ps", ps).to(DEV)
+    at = torch.arange(n, device=DEV)
+    slots = (perm[at // ps] * ps + at % ps).to(torch.int32)
+    qa = K.norm_rope_store(a, q, k, v, slots)
+    qb = K.norm_rope_store(b, q, k, v, at.to(torch.int32))
+    assert torch.equal(qa, qb)
+    want = K.load(b, at.to(torch.int32))
+    cu = torch.tensor([0, 300, n], dtype=torch.int32, device=DEV)
+    st = torch.tensor([0, 300], dtype=torch.int32, device=DEV)
+    bt = perm.to(torch.int32).expand(2, -1).contiguous()
+    for got in (K.load(a, slots), K.load_seqs(a, bt, cu, n, starts=st)):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_load_seqs_of_many_sequences(K):
+    """A thousand sequences, most of them of no or one position."""
+    cache = make_cache(K, K.FMT_Q4_HAD32, 2, 64, 60)
+    fill_random(cache, K, 9)
+    lens = synth.ragged_lengths(1000, 0, 3, "many seqs")
+    lens[::7] = 0
+    lens[500] = 200
+    bt = torch.stack([synth.page_permutation(60, "ms", i)[:13] for i in range(1000)]).to(torch.int32).to(DEV)
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), torch.cumsum(lens, 0)]).to(torch.int32).to(DEV)
+    n = int(cu[-1])
+    seq = torch.repeat_interleave(torch.arange(1000), lens).to(DEV)
+    at = torch.arange(n, device=DEV) - cu.long()[seq]
+    slots = (bt.long()[seq, at // 16] * 16 + at % 16).to(torch.int32)
+    got, want = K.load_seqs(cache, bt, cu, n), K.load(cache, slots)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_more_than_2_31_elements(K):
+    """Activations and outputs of more than 2^31 elements: their last rows are those
+    of a call on them alone."""
+    n, H, W = 351003, 24, 256
+    x = torch.zeros(n, H, W, dtype=torch.bfloat16, device=DEV)
+    x[-5:] = rnd((5, H, W), "2^31", dtype=torch.bfloat16)
+    norm = K.Norm(rnd((W,), "2^31 w"), 1e-6)
+    rope, _, _ = rope_of(K, 64, 0, 1)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    y = K.norm_rope(x, pos, rope=rope, norm=norm)
+    assert torch.equal(y[-5:], K.norm_rope(x[-5:], pos[-5:], rope=rope, norm=norm))
+    assert y[:-5].abs().max() == 0
+    del x
+    z = torch.zeros(n, H, W, device=DEV)
+    z[-5:] = y[-5:].float()
+    lam = torch.rand(n, H // 2, device=DEV)
+    d = K.diff_heads(z, lam, norm=norm, dtype=torch.bfloat16)
+    assert torch.equal(d[-5:], K.diff_heads(z[-5:], lam[-5:], norm=norm, dtype=torch.bfloat16))
+    assert d[:-5].abs().max() == 0
+    del y, z, d
+    cache = make_cache(K, K.FMT_Q4_HAD32, 8, 256, 2)
+    fill_random(cache, K, 4)
+    m = 1050007
+    slots = (torch.arange(m, device=DEV) % 32).to(torch.int32)
+    k, v = K.load(cache, slots)
+    small = K.load(cache, slots[:32])
+    last = slots[-7:].long()
+    assert torch.equal(k[-7:], small[0][last]) and torch.equal(v[-7:], small[1][last])
+    torch.cuda.empty_cache()
 
 
 def test_rows_past_two_gigabytes(K):
