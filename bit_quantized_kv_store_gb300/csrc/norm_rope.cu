@@ -27,13 +27,12 @@
 // Bound.  4099 x 24 heads of 256, bf16 to bf16 with norm and three axes: 18.7 us, 101
 // MB, 5.4 TB/s (80 % of the measured copy; the same kernel without norm and rotation
 // takes as long, so what is left is filling and draining the memory pipe).  4096
-// tokens of 24 + 4 + 4 heads to rotated fp32 queries and 4-bit rows: 38.5 us, 172 MB,
-// 4.5 TB/s; 31 us without the norm, the rotations and the codes' arithmetic, the
+// tokens of 24 + 4 + 4 heads to rotated fp32 queries and 4-bit rows: 36.5 us, 172 MB,
+// 4.7 TB/s; 31 us without the norm, the rotations and the codes' arithmetic, the
 // rest is issue (20.2 M instructions at 51 %).  One token: the launch.
-// Measured and not kept: K and V rows two batches side by side like the queries'
-// (spills; the 4096-token chunk with its read-back 43.9 -> 49.8 us), one batch at
-// 80 registers and 24 warps an SM (49.7 us), five CTAs of four warps at 102
-// registers (53.7 us).
+// Measured and not kept (the 4096-token chunk with its read-back, 41.7 us): K and V
+// rows two batches side by side like the queries' 47.3 us, one batch at 80 registers
+// and 24 warps an SM 49.7 us, five CTAs of four warps at 96 registers 51.4 us.
 //
 // This translation unit is compiled with -fmad=false.
 #include "rows.cuh"
@@ -275,7 +274,14 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(con
           first_rows(tok + 1, 0, nb1);
         }
         if (a.qn.weight) norm_rows<E, LPR, U>(x, w, a.qn.eps);
-        if (a.rope.rot != 0) rope_rows<U>(a.rope, g, l, x);
+        if (a.rope.rot != 0) {
+          if constexpr (FMT == kNoStore) {
+            rope_rows<U>(a.rope, g, l, x);
+          } else {  // one after the other: the partners of both would spill
+#pragma unroll
+            for (int u = 0; u < U; ++u) rope_rows<1>(a.rope, g, l, *reinterpret_cast<uint64_t(*)[1][E / 2]>(&x[u]));
+          }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if constexpr (FMT == KVQ_FMT_Q4_HAD32) {
