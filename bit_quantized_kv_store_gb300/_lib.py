@@ -488,7 +488,9 @@ def norm_rope_store(cache: Cache, q, k, v, slot_mapping, positions=None, rope=No
     D] normed, position-rotated and (rotate) turned into the cache's space, the
     keys normed, position-rotated and stored, the values stored.  Returns q_out
     (default: a new fp32 tensor) for decode_attn, or with rotate=False for the
-    calls that take unrotated queries.  q None: keys and values only."""
+    calls that take unrotated queries.  q None: keys and values only.  An fp8 cache
+    takes k [tokens, 1, 576] (latent part normed, rope part rotated), v None and
+    absorbed queries [tokens, Hq, 576] (rope part rotated)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return norm_rope_store(cache, q, k, v, slot_mapping, positions, rope, q_norm, k_norm, q_out, rotate, status)

@@ -31,7 +31,8 @@ SAN_FLAGS = ["-Xcompiler", "-fsanitize=address", "-Xcompiler", "-fsanitize=undef
 if SANITIZE:
     FLAGS = FLAGS + SAN_FLAGS
 # The store computes codes that must be bit-exact: no fused multiply-adds there.
-PER_FILE = {"store.cu": ["-fmad=false"], "tq4.cu": ["-fmad=false"], "norm_rope.cu": ["-fmad=false"]}
+PER_FILE = {"store.cu": ["-fmad=false"], "tq4.cu": ["-fmad=false"], "norm_rope.cu": ["-fmad=false"],
+            "latent.cu": ["-fmad=false"]}
 
 
 def _tool_env():

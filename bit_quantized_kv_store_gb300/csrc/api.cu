@@ -722,16 +722,20 @@ int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq
   int32_t st = check_cache(cache);
   if (st != KVQ_OK) return st;
   if (n_tok < 0 || (rotate != 0 && rotate != 1) || !q != !q_out) return KVQ_ERR_INVALID_ARG;
-  const int D = cache->head_dim, Hk = cache->num_kv_heads;
-  if (cache->format == KVQ_FMT_FP8_ROW || !norm_rope_width(D)) return KVQ_ERR_UNSUPPORTED;
+  // fp8 latent rows: one tensor of both parts, the norm on the first, the rope on the second
+  const bool fp8 = cache->format == KVQ_FMT_FP8_ROW;
+  const int Hk = cache->num_kv_heads, D = fp8 ? cache->head_dim + cache->rope_dim : cache->head_dim;
+  const int rope_width = fp8 ? cache->rope_dim : D;
+  if (fp8 ? cache->head_dim != 512 || cache->rope_dim != 64 : !norm_rope_width(D)) return KVQ_ERR_UNSUPPORTED;
+  if (fp8 && (v || q_norm)) return KVQ_ERR_INVALID_ARG;
   if (n_tok == 0) return KVQ_OK;
-  if (!k || !v || !d_slot_mapping || (q && q->heads < 1)) return KVQ_ERR_INVALID_ARG;
+  if (!k || (!v && !fp8) || !d_slot_mapping || (q && q->heads < 1)) return KVQ_ERR_INVALID_ARG;
   if ((q && q->heads > kMaxHeads) || Hk > kMaxHeads || n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   NormRopeArgs a{};
   st = check_rows(k, Hk, D, &a.k);
-  if (st == KVQ_OK) st = check_rows(v, Hk, D, &a.v);
+  if (st == KVQ_OK && !fp8) st = check_rows(v, Hk, D, &a.v);
   if (st == KVQ_OK) st = check_norm(k_norm, &a.kn);
-  if (st == KVQ_OK) st = check_rope(rope, D, d_pos, pos_stride, n_tok, &a.rope);
+  if (st == KVQ_OK) st = check_rope(rope, rope_width, d_pos, pos_stride, n_tok, &a.rope);
   if (q) {
     if (st == KVQ_OK) st = check_rows(q, q->heads, D, &a.q);
     if (st == KVQ_OK) st = check_rows(q_out, q->heads, D, &a.qo);
@@ -753,7 +757,8 @@ int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq
   a.rotate = rotate;
   a.plane_wide = (reinterpret_cast<uintptr_t>(cache->k) | reinterpret_cast<uintptr_t>(cache->v)) % 32 == 0 ? 1 : 0;
   a.ps = make_fastdiv(static_cast<uint32_t>(cache->page_size));
-  cudaError_t e = launch_norm_rope(a, D, cache->format, static_cast<cudaStream_t>(stream));
+  cudaError_t e = fp8 ? launch_latent(a, static_cast<cudaStream_t>(stream))
+                      : launch_norm_rope(a, D, cache->format, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
 }
 

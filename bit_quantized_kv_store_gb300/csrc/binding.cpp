@@ -238,11 +238,15 @@ PyObject* norm_rope(PyObject* const* a) {
 // norm_rope_store(cache, q, k, v, slots, positions, rope, q_norm, k_norm, q_out, rotate, status)
 PyObject* norm_rope_store(PyObject* const* a) {
   const kvq_cache* c = cache_of(a[0]);
-  const at::Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+  const bool fp8 = c->format == KVQ_FMT_FP8_ROW;  // one tensor of latent and rope parts, no v
+  const at::Tensor& k = tensor(a[2], "k");
   three(k, "k");
   const int dev = device_of(k);
-  const int64_t n = k.size(0), D = c->head_dim, Hk = c->num_kv_heads;
-  const kvq_rows rk = rows(k, "k", dev, n, Hk, D), rv = rows(v, "v", dev, n, Hk, D);
+  const int64_t n = k.size(0), Hk = c->num_kv_heads, D = c->head_dim + (fp8 ? c->rope_dim : 0);
+  const kvq_rows rk = rows(k, "k", dev, n, Hk, D);
+  if (fp8 && given(a[3])) refuse(PyExc_ValueError, "fp8 latent rows take no v");
+  kvq_rows rv;
+  if (!fp8) rv = rows(tensor(a[3], "v"), "v", dev, n, Hk, D);
   kvq_rows rq, ro;
   at::Tensor out;
   const bool with_q = given(a[1]);
@@ -257,8 +261,8 @@ PyObject* norm_rope_store(PyObject* const* a) {
     refuse(PyExc_ValueError, "q_out without q");
   }
   const Turned r = rope_of(a[6], a[5], dev, n);
-  checked(p_norm_rope_store(c, with_q ? &rq : nullptr, &rk, &rv, n, norm_of(a[7], "q_norm", dev, D),
-                            norm_of(a[8], "k_norm", dev, D), r.rope, r.pos, r.stride,
+  checked(p_norm_rope_store(c, with_q ? &rq : nullptr, &rk, fp8 ? nullptr : &rv, n,
+                            norm_of(a[7], "q_norm", dev, c->head_dim), norm_of(a[8], "k_norm", dev, c->head_dim), r.rope, r.pos, r.stride,
                             ints(tensor(a[4], "slot_mapping"), "slot_mapping", dev, {n}), with_q ? &ro : nullptr,
                             integer32(a[10], "rotate"), status_of(a[11], dev), stream_of(dev)),
           "kvq_norm_rope_store");

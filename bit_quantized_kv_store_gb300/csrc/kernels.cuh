@@ -241,6 +241,8 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t s);
 // Norm and rotary positions of rows of `width`; fmt: the cache's format, or -1
 // for rows that are only normed and rotated (norm_rope.cu).
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int width, int fmt, cudaStream_t s);
+// Fp8 latent rows and absorbed queries on the way into the cache (latent.cu).
+cudaError_t launch_latent(const NormRopeArgs& a, cudaStream_t s);
 // Rows of the cache as the values they stand for (load.cu).
 cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);
 // The merge of two maps' partials with their difference (tq: TQ4 rows), and the

@@ -12,9 +12,8 @@
 // This translation unit is compiled with -fmad=false: every operation below is
 // a single IEEE-rounded fp32 operation, so the codes are bit-exact with the
 // definition in kvq.h.
-#include <cuda_fp8.h>
-
 #include "f32x2.cuh"
+#include "fp8_code.cuh"
 #include "kernels.cuh"
 #include "q4_code.cuh"
 
@@ -338,11 +337,6 @@ __global__ void store_bf16_kernel(kvq_cache c, const void* __restrict__ k, const
       *vd = __float2bfloat16_rn(static_cast<const float*>(v)[i]);
     }
   }
-}
-
-__device__ __forceinline__ uint8_t e4m3_encode(float x) {
-  if (isnan(x)) return 0;  // NaN is stored as the inert code 0
-  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3));
 }
 
 // One block (128 threads) per token: latent part and rope part each get amax,

@@ -484,14 +484,18 @@ int32_t kvq_norm_rope(const kvq_rows* x, const kvq_rows* y, int64_t n_tok, int32
  *       q_out may be q itself.  With rotate, q_out is fp32 (for the decode
  *       calls); without, either type (kvq_prefill_attn, kvq_decode_step and
  *       kvq_decode_attn_unrotated take their queries unrotated, contiguous).
- *   k, v: [n_tok][num_kv_heads][head_dim].
+ *   k, v: [n_tok][num_kv_heads][head_dim] (FP8_ROW: below).
  *   q_norm, k_norm, rope: NULL where the model has none.
  *   d_pos, pos_stride as for kvq_norm_rope; d_slot_mapping and d_status as for
  *       kvq_store (a token whose slot is negative or out of range is not stored;
  *       its queries are still written).
- * Formats Q4_HAD32, Q4_0, TQ4 and BF16 with head_dim 64, 128 or 256 (BF16 also
- * 512); FP8_ROW: KVQ_ERR_UNSUPPORTED (its parts: kvq_norm_rope of the latent and
- * of the rope columns, then kvq_store). */
+ * The slots of one call are distinct (a row stored twice may hold parts of both).
+ * Formats Q4_HAD32, Q4_0, TQ4 and BF16 with head_dim 64, 128 or 256 (BF16 also 512).
+ * FP8_ROW (head_dim 512, rope_dim 64): k is [n_tok][1][576], the latent part normed
+ * (k_norm, of 512) and the rope part position-rotated (rope, of 64), v and q_norm
+ * NULL; q and q_out are [n_tok][num_q_heads][576], absorbed queries whose rope part is
+ * position-rotated and whose latent part is taken over (rotate makes no difference,
+ * but that q_out is then fp32, for the decode). */
 int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq_rows* k, const kvq_rows* v,
                             int64_t n_tok, const kvq_norm* q_norm, const kvq_norm* k_norm, const kvq_rope* rope,
                             const int32_t* d_pos, int64_t pos_stride, const int32_t* d_slot_mapping,
@@ -505,6 +509,7 @@ int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq
  *       take 0, as in kvq_merge); 0: in the cache's space.
  * The value is the code's times its scale, rotated back from exact sums of the
  * codes (the 4-bit formats), in fp32, rounded once into the output's type.
+ * k and v must not overlap; the same slot may come twice.
  * A negative slot leaves its token's rows as they were; a slot >= num_pages *
  * page_size writes NaN there and sets KVQ_DEV_BAD_SLOT in the optional status. */
 int32_t kvq_load(const kvq_cache* cache, const int32_t* d_slots, int64_t n_tok, int32_t rotate_back,

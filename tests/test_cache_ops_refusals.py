@@ -112,7 +112,21 @@ def test_norm_rope_store_refusals(K):
                                      None)
 
     assert call(c=None) == K.ERR_INVALID_ARG
-    assert call(c=_desc(K, fmt=2, Hk=1, D=512, rope=64)) == K.ERR_UNSUPPORTED
+    # fp8 latent rows: 512 + 64, no v, no norm of the queries
+    fp8 = _desc(K, fmt=2, Hk=1, D=512, rope=64)
+    lk, lq, lo = rows(K, heads=1, ts=576, hs=576), rows(K, heads=16, ts=9216, hs=576), \
+        rows(K, heads=16, ts=9216, hs=576, ptr=8192)
+    latent = lambda c=fp8, k=lk, v=None, q=lq, qo=lo, **kw: call(c=c, k=k, v=v, q=q, qo=qo, **kw)
+    assert latent(n=0) == K.OK
+    assert latent(c=_desc(K, fmt=2, Hk=1, D=256, rope=64)) == K.ERR_UNSUPPORTED
+    assert latent(c=_desc(K, fmt=2, Hk=1, D=512, rope=32)) == K.ERR_UNSUPPORTED
+    assert latent(v=lk) == K.ERR_INVALID_ARG
+    assert latent(qn=norm(K)) == K.ERR_INVALID_ARG
+    assert latent(k=None) == K.ERR_INVALID_ARG
+    assert latent(k=rows(K, heads=2, ts=1152, hs=576)) == K.ERR_INVALID_ARG
+    assert latent(rp=rope(K, rot=128)) == K.ERR_INVALID_ARG                # wider than the rope part
+    assert latent(rp=rope(K, rot=40)) == K.ERR_UNSUPPORTED
+    assert latent(qo=rows(K, heads=16, ts=8192, hs=512, ptr=8192)) == K.ERR_INVALID_ARG
     assert call(c=_desc(K, D=32)) == K.ERR_UNSUPPORTED
     assert call(c=_desc(K, fmt=1, D=96)) == K.ERR_UNSUPPORTED
     assert call(c=_tq4_desc(K, signs=None)) == K.ERR_INVALID_ARG

@@ -341,6 +341,51 @@ def test_norm_rope_store_mixed_types_and_strides(K, n):
             assert torch.equal(getattr(c, name).view(torch.uint8), getattr(want, name).view(torch.uint8))
 
 
+@pytest.mark.parametrize("n,Hq", [(1, 128), (1, 3), (40, 16), (700, 5)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_rope_store_latent_rows(K, n, Hq, dtype):
+    """Fp8 latent rows: the bytes of norm_rope on either part and the store, and the
+    query bits of norm_rope on the rope part beside the latent part as it is."""
+    pages = n // 16 + 2
+    at = torch.arange(n, device=DEV)
+    perm = synth.page_permutation(pages, "latent", n).to(DEV)
+    slots = (perm[at // 16] * 16 + at % 16).to(torch.int32)
+    if n > 20:
+        slots[3], slots[9] = -1, pages * 16
+    row = (synth.latent_rows(n, 576, DEV, "latent", n) * 2).to(dtype)
+    row[n // 2, 512:] = 0
+    wide = torch.zeros(n, 1, 640, dtype=dtype, device=DEV)       # beside other columns of one projection
+    wide[:, 0, 32:608] = row
+    k = wide[..., 32:608]
+    q = rnd((n, Hq, 576), "latent q", n, Hq, dtype=dtype)
+    norm = K.Norm(rnd((512,), "latent w", dtype=dtype), 1e-6)
+    for inter, axes, with_rope, with_norm in ((1, 1, 1, 1), (0, 2, 1, 1), (1, 1, 0, 1), (0, 1, 1, 0)):
+        rope = rope_of(K, 64, inter, axes)[0] if with_rope else None
+        pos = positions(axes, n, 7) if with_rope else None
+        kn = norm if with_norm else None
+        a, b = make_cache(K, K.FMT_FP8_ROW, 1, 512, pages), make_cache(K, K.FMT_FP8_ROW, 1, 512, pages)
+        sa, sb = (torch.zeros(1, dtype=torch.int32, device=DEV) for _ in range(2))
+        got = K.norm_rope_store(a, q, k, None, slots, pos, rope=rope, k_norm=kn, status=sa)
+        parts = torch.empty(n, 1, 576, device=DEV)
+        K.norm_rope(k[..., :512], norm=kn, out=parts[..., :512])
+        K.norm_rope(k[..., 512:], pos, rope=rope, out=parts[..., 512:])
+        K.store(b, parts, None, slots, status=sb)
+        for name in ("k", "v", "k_scale", "v_scale"):
+            assert torch.equal(getattr(a, name).view(torch.uint8), getattr(b, name).view(torch.uint8)), name
+        want = q.float().clone()
+        K.norm_rope(q[..., 512:], pos, rope=rope, out=want[..., 512:])
+        assert torch.equal(got, want)
+        assert K.read_status(sa) == K.read_status(sb) == (K.DEV_BAD_SLOT if n > 20 else 0)
+        c = make_cache(K, K.FMT_FP8_ROW, 1, 512, pages)
+        mine = q.clone()                                          # rotated in place, in its own type
+        K.norm_rope_store(c, mine, k.contiguous(), None, slots, pos, rope=rope, k_norm=kn, q_out=mine, rotate=False)
+        assert torch.equal(mine, want.to(dtype))
+        d = make_cache(K, K.FMT_FP8_ROW, 1, 512, pages)
+        assert K.norm_rope_store(d, None, k, None, slots, pos, rope=rope, k_norm=kn) is None
+        for other in (c, d):
+            assert torch.equal(other.k, a.k) and torch.equal(other.v, a.v)
+
+
 def test_norm_rope_store_queries_of_padding_tokens(K):
     """A token without a slot still has its queries; n = 0 writes nothing."""
     a = make_cache(K, K.FMT_Q4_HAD32, 2, 256, 2)
