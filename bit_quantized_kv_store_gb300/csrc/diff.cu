@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(512) merge_diff_kernel(const MergeArgs a, cons
 // first of which are in flight meanwhile.  T: 512, or 256 for at most 16 partitions
 // (rows 16 .. 31 are empty), which lets three CTAs share an SM instead of one.
 // A batch of 32 sequences of up to 8000 keys, 16 partitions a head: 5.5 us; 12 us
-// with 512 threads, 30 us with the cluster of 8 CTAs a head (3072 CTAs, each with
+// with 512 threads, 30 us with the cluster of 8 CTAs a head (thousands, each with
 // its own barriers for 32 KB of partials).  One sequence's 12 heads of 65 partitions:
 // 6.8 us here, 4.8 us there (the wait for the decode included).
 constexpr int kRowMaxP = 1024;  // partitions whose weights fit in shared memory

@@ -25,7 +25,7 @@
 // Bound: memory (in bf16 the outputs are 3.6 times the codes' bytes).  262144 tokens
 // of 4 heads to bf16: 222 us, 1.38 GB, 6.2 TB/s (92 % of the measured copy).  20011
 // tokens of TQ4 rows to fp32: 34.9 us, 185 MB, 5.3 TB/s (78 %; the exchanges between
-// lanes are half of its 22.8 M instructions).  A lane writes 16 bytes next to its
+// lanes are a third of its 22.8 M instructions).  A lane writes 16 bytes next to its
 // neighbours' or 32 by itself: stores of 16 bytes 32 apart reached 4.1 TB/s, these
 // 7.5 TB/s, in a kernel that only writes.
 #include <cuda_fp8.h>

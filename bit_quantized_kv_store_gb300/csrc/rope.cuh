@@ -4,8 +4,9 @@
 // The angle of a pair is 2 pi times the fraction of pos * turns, turns a 64-bit
 // fixed-point fraction of a turn: the product wraps modulo one turn exactly, so
 // a far position costs nothing in accuracy (an fp32 angle of 262144 radians is
-// off by 0.016) and no fp64.  Its top 32 bits as a float in [-1, 1) go to
-// sincospif: the rounding there is at most 2^-25 of half a turn, 1e-7 radians.
+// off by 0.016) and no fp64.  Its top 32 bits less the nearest quarter turn go to
+// sincospif as a float of at most a quarter of half a turn: the rounding there is
+// at most 2^-27 of half a turn, 2.4e-8 radians.
 // Translation units that include this are compiled with -fmad=false, so that their
 // rows agree bit for bit.
 #pragma once
@@ -32,13 +33,19 @@ __device__ __forceinline__ float2 angle(const RopeView& r, int pair, const int32
   for (int a = 1; a < 4; ++a)
     if (axis == a) p = pos[a];
   const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(p)) * (w & ~uint64_t(3));
-  float t = __fmul_rn(static_cast<float>(static_cast<int32_t>(phase >> 32)), 4.656612873077393e-10f);  // 2^-31
+  // the nearest quarter turn, and what is left of it in half turns, |t| <= 1/4
+  const uint32_t h = static_cast<uint32_t>(phase >> 32) + 0x20000000u;
+  const uint32_t quarter = h >> 30;
+  float t = __fmul_rn(static_cast<float>(static_cast<int32_t>(h & 0x3FFFFFFFu) - 0x20000000), 4.656612873077393e-10f);
   if (axis >= r.axes) {
     set_status(status, KVQ_DEV_BAD_INDEX);
     t = NAN;
   }
-  float2 cs;
-  sincospif(t, &cs.y, &cs.x);
+  float s, c;
+  sincospif(t, &s, &c);
+  float2 cs = (quarter & 1) ? make_float2(s, c) : make_float2(c, s);
+  if ((quarter + 1) & 2) cs.x = -cs.x;
+  if (quarter & 2) cs.y = -cs.y;
   return cs;
 }
 

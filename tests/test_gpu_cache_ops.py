@@ -144,9 +144,9 @@ def positions(axes, n, seed):
 # squares (at most 10 levels of a tree plus the square itself, halved by the root:
 # 6), mean and eps (1), rsqrt (2 ulp = 4), weight + offset (1), the two products
 # (2), the rotation's product and fused add (2); cos and sin: the angle's rounding
-# to a float (2^-25 of half a turn: pi / 2 u) and sincospi's 2 ulp (4 u).  21 and a
-# half; with the table's 2^-63 turns times 2^31 (a quarter of 2^-30 rad: 4 u, only at
-# positions near 2^31) under 26.
+# to a float (2^-27 of half a turn: 0.4 u) and its cut to 2^-32 of a turn (0.03 u),
+# and sincospi's 2 ulp (4 u).  20 and a half; with the table's 2^-63 turns times 2^31
+# (a quarter of 2^-30 rad: 4 u, only at positions near 2^31) under 26.
 NORM_ROPE_U = 26
 
 
