@@ -20,12 +20,14 @@
 // warp tile is 8 groups of K and the same 8 of V (the 16 rows of the operand); the
 // columns of the matrix are ordered so that a thread's results are 8 consecutive
 // values, and the terms so that it loads 8 consecutive codes as one word.  The TQ4
-// rows' remaining stages, between the groups of a row, are stages across lanes.
+// rows' stages between the groups of a row come first, as a product from the left
+// with the groups' +-1 matrix; its sums enter the second product as two fp16 terms.
+// (As stages across lanes on the results they were a third of the instructions.)
 //
 // Bound: memory (in bf16 the outputs are 3.6 times the codes' bytes).  262144 tokens
-// of 4 heads to bf16: 222 us, 1.38 GB, 6.2 TB/s (92 % of the measured copy).  20011
-// tokens of TQ4 rows to fp32: 34.9 us, 185 MB, 5.3 TB/s (78 %; the exchanges between
-// lanes are a third of its 22.8 M instructions).  A lane writes 16 bytes next to its
+// of 4 heads to bf16: 220 us, 1.38 GB, 6.3 TB/s (93 % of the measured copy).  20011
+// tokens of TQ4 rows to fp32: 34.4 us, 185 MB, 5.4 TB/s; 200011 to bf16: 280 us, 1.03 GB,
+// issue (the look-ups, the sums in two terms).  A lane writes 16 bytes next to its
 // neighbours' or 32 by itself: stores of 16 bytes 32 apart reached 4.1 TB/s, these
 // 7.5 TB/s, in a kernel that only writes.
 #include <cuda_fp8.h>
@@ -133,10 +135,10 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&p)[4]) {
       const uint32_t sel = s ? m >> 16 : m;
       const uint32_t lo = prmt(tq4_table(0, 0), tq4_table(4, 0), sel);
       uint32_t hi = prmt(tq4_table(0, 1), tq4_table(4, 1), sel);
-      uint32_t sg = s ? w >> 16 : w & 0xFFFFu;  // their signs into the levels' high bytes
-      sg = (sg | sg << 8) & 0x00FF00FFu;
-      sg = (sg | sg << 4) & 0x08080808u;
-      hi |= sg << 4;
+      // their signs into the levels' high bytes: every code byte twice, the first with
+      // its low nibble's sign (bit 3) moved up, the second with its high nibble's (bit 7)
+      const uint32_t y = prmt(w, 0u, s ? 0x3322u : 0x1100u);
+      hi |= ((y & 0xFF00FF00u) | ((y << 4) & 0x00FF00FFu)) & 0x80808080u;
       p[2 * s] = prmt(lo, hi, 0x5140u);
       p[2 * s + 1] = prmt(lo, hi, 0x7362u);
     }
@@ -191,6 +193,17 @@ struct SignMatrix {
   }
 };
 
+// A sum of 8 TQ4 levels, a multiple of 2^-13 below 22, as two exact fp16 terms: the
+// nearest multiple of 2^-6 (adding 1.5 * 2^17 rounds to one) and what is left.
+__device__ __forceinline__ void split_sums(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const uint64_t x = pk2(x0, x1), m2 = pk2(196608.0f, 196608.0f), h = sub2(add2(x, m2), m2);
+  float a, b;
+  upk2(h, a, b);
+  hi = pack_half2(a, b);
+  upk2(sub2(x, h), a, b);
+  lo = pack_half2(a, b);
+}
+
 // The codes of a word as mma operands.  4-bit formats: left biased, 1024 + c in the
 // pairs of even elements and 1024 + 16 c in those of odd ones, whose matrix entries
 // are +-1/16: the biases, 1024 and 64, cancel in every sum but outputs 0 and 1,
@@ -216,17 +229,21 @@ __device__ __forceinline__ void code_operands(uint32_t w, uint32_t (&p)[4]) {
 // block-table entry, two dependent loads) two units ahead, its codes and scales one
 // ahead, the transform and the stores.  (One unit to a warp, each paying the chain
 // of loads by itself: 262 us for 262144 tokens; with the outputs' types known to the
-// compiler and three CTAs of an SM 222 us.)
+// compiler and three CTAs of an SM 220 us; the warps on equal ranges of units next to
+// one another, far apart in memory, 245 us.)
 // nb divides by a token's units; a launch has fewer than 2^31.  OUT: what is written,
 // kBf16 or kF32 (K and V both, whole vectors), or kAny (as the views say).
+// FEW: one or two heads, and a unit is all heads of kHeads / Hk token blocks; lane l
+// finds the row of the unit's token l, and the tiles take them from there.
 constexpr int kHeads = 4;
-// CTAs of an SM: three (80 registers), two for the TQ4 rows (their exchange of 16
-// values spills at 80: 20011 tokens in fp32 45 us, against 37 us).
-__host__ __device__ constexpr int load_ctas(int fmt) { return fmt == KVQ_FMT_TQ4 ? 2 : 3; }
+// CTAs of an SM: three (80 registers), two for the TQ4 rows, whose sums spill at 80
+// (20011 tokens in fp32 61 us, against 34 us), and for FEW with its row addresses (two
+// heads of 200011 tokens 111 us, against 95 us).
+__host__ __device__ constexpr int load_ctas(int fmt, bool few) { return few || fmt == KVQ_FMT_TQ4 ? 2 : 3; }
 enum Out { kAny, kBf16, kF32 };
 
-template <int FMT, int NG, bool ROT, int OUT>
-__global__ void __launch_bounds__(kLoadBlock, load_ctas(FMT)) load_q4_kernel(const __grid_constant__ LoadArgs a,
+template <int FMT, int NG, bool ROT, int OUT, bool FEW>
+__global__ void __launch_bounds__(kLoadBlock, load_ctas(FMT, FEW)) load_q4_kernel(const __grid_constant__ LoadArgs a,
                                                                              FastDiv nb, int hpu, uint32_t units) {
   pdl_wait();
   pdl_trigger();
@@ -238,10 +255,23 @@ __global__ void __launch_bounds__(kLoadBlock, load_ctas(FMT)) load_q4_kernel(con
   const int v_dtype = OUT == kAny ? a.v.dtype : k_dtype;
   const int k_wide = OUT == kAny ? a.k.wide : 1, v_wide = OUT == kAny ? a.v.wide : 1;
   const SignMatrix<FMT> H(lane);
-  uint32_t sw = 0;
-  if constexpr (FMT == KVQ_FMT_TQ4 && ROT) sw = static_cast<const uint32_t*>(a.c.signs)[G] >> (8 * t4);
+  uint64_t sign2[4];  // TQ4: the row signs of the lane's 8 outputs, +-1
+  if constexpr (FMT == KVQ_FMT_TQ4 && ROT) {
+    const uint32_t sw = static_cast<const uint32_t*>(a.c.signs)[G] >> (8 * t4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      sign2[j] = pk2((sw >> (2 * j)) & 1u ? -1.f : 1.f, (sw >> (2 * j + 1)) & 1u ? -1.f : 1.f);
+  }
   constexpr float kBack = !ROT ? 1.0f : FMT == KVQ_FMT_TQ4 ? tq4_row_scale<NG>() : kHadamardScale;
   const float c0 = FMT != KVQ_FMT_TQ4 && t4 == 0 ? kBias0 : 0.f, c1 = FMT != KVQ_FMT_TQ4 && t4 == 0 ? kBias1 : 0.f;
+  uint32_t hg = 0;  // TQ4: row g of the groups' +-1 matrix, terms 2 t4 and 2 t4 + 1, zero between tokens
+  if constexpr (FMT == KVQ_FMT_TQ4 && ROT) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int k = 2 * t4 + e;
+      if (g / NG == k / NG) hg |= ((__popc(G & (k % NG)) & 1) ? 0xBC00u : 0x3C00u) << (16 * e);
+    }
+  }
   // bytes between the heads of a token's rows
   const int64_t code_step = (int64_t)a.c.page_size * (D / 2);
   const int64_t scale_step = (int64_t)a.c.page_size * (FMT == KVQ_FMT_TQ4 ? 2 : 2 * NG);
@@ -252,36 +282,58 @@ __global__ void __launch_bounds__(kLoadBlock, load_ctas(FMT)) load_q4_kernel(con
     int h, why;
     Where at;
   };
+  constexpr int TB = 8 / NG;  // tokens of a tile
+  const int hs = FEW ? Hk >> 1 : 0;
   auto place = [&](uint32_t u, Unit& x) {
-    const uint32_t tb = fast_div(u, nb);
-    x.h = static_cast<int>(u - tb * nb.d) * hpu;
-    x.t = a.t0 + (int64_t)tb * (8 / NG) + g / NG;
     int32_t page = 0, why = 0;
     uint32_t off = 0;
-    x.at = x.t < a.n_tok ? locate(a, x.t, page, off, why) : kSkip;
-    x.why = why;
-    x.row = ((int64_t)page * Hk + x.h) * a.c.page_size + off;
+    if constexpr (FEW) {
+      const int n = (kHeads >> hs) * TB;  // the unit's tokens, at most 32
+      x.h = 0;
+      x.t = a.t0 + (int64_t)u * n;
+      x.at = lane < n && x.t + lane < a.n_tok ? locate(a, x.t + lane, page, off, why) : kSkip;
+      if (x.at == kBad) set_status(a.status, why);
+      x.row = x.at == kRow ? (int64_t)page * Hk * a.c.page_size + off : x.at == kBad ? -2 : -1;
+    } else {
+      const uint32_t tb = fast_div(u, nb);
+      x.h = static_cast<int>(u - tb * nb.d) * hpu;
+      x.t = a.t0 + (int64_t)tb * TB + g / NG;
+      x.at = x.t < a.n_tok ? locate(a, x.t, page, off, why) : kSkip;
+      x.why = why;
+      x.row = ((int64_t)page * Hk + x.h) * a.c.page_size + off;
+    }
   };
+  // FEW: the lane's token of tile i within the unit, and the tile's head
+  auto token = [&](int i) { return (i >> hs) * TB + g / NG; };
+  auto head = [&](int i) { return i & ((1 << hs) - 1); };
   uint32_t word[kHeads][2];
   uint16_t scale[kHeads][2];
   auto fetch = [&](const Unit& x, uint32_t (&w)[kHeads][2], uint16_t (&sc)[kHeads][2]) {
-    const int64_t code0 = x.row * (D / 2) + 16 * G + 4 * t4;
-    const int64_t scale0 = FMT == KVQ_FMT_TQ4 ? 2 * x.row : (x.row * NG + G) * 2;
-    const uint8_t *ck = static_cast<const uint8_t*>(a.c.k) + code0, *cv = static_cast<const uint8_t*>(a.c.v) + code0;
-    const uint8_t *sk = static_cast<const uint8_t*>(a.c.k_scale) + scale0,
-                  *sv = static_cast<const uint8_t*>(a.c.v_scale) + scale0;
+    auto code_at = [&](int64_t row) { return row * (D / 2) + 16 * G + 4 * t4; };
+    auto scale_at = [&](int64_t row) { return FMT == KVQ_FMT_TQ4 ? 2 * row : (row * NG + G) * 2; };
+    const int64_t code0 = code_at(x.row), scale0 = scale_at(x.row);
+    const uint8_t *ck = static_cast<const uint8_t*>(a.c.k), *cv = static_cast<const uint8_t*>(a.c.v);
+    const uint8_t *sk = static_cast<const uint8_t*>(a.c.k_scale), *sv = static_cast<const uint8_t*>(a.c.v_scale);
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
       w[i][0] = w[i][1] = 0;
       sc[i][0] = sc[i][1] = 0x7E00;  // a position without a row stands for NaN
-      if (x.at == kRow && i < hpu && x.h + i < Hk) {
+      bool have = x.at == kRow && i < hpu && x.h + i < Hk;
+      int64_t ca = code0 + i * code_step, sa = scale0 + i * scale_step;
+      if constexpr (FEW) {
+        const int64_t row = __shfl_sync(0xffffffffu, x.row, token(i));
+        have = row >= 0;
+        ca = code_at(row) + head(i) * code_step;
+        sa = scale_at(row) + head(i) * scale_step;
+      }
+      if (have) {
         if (with_k) {
-          w[i][0] = *reinterpret_cast<const uint32_t*>(ck + i * code_step);
-          sc[i][0] = *reinterpret_cast<const uint16_t*>(sk + i * scale_step);
+          w[i][0] = *reinterpret_cast<const uint32_t*>(ck + ca);
+          sc[i][0] = *reinterpret_cast<const uint16_t*>(sk + sa);
         }
         if (with_v) {
-          w[i][1] = *reinterpret_cast<const uint32_t*>(cv + i * code_step);
-          sc[i][1] = *reinterpret_cast<const uint16_t*>(sv + i * scale_step);
+          w[i][1] = *reinterpret_cast<const uint32_t*>(cv + ca);
+          sc[i][1] = *reinterpret_cast<const uint16_t*>(sv + sa);
         }
       }
     }
@@ -307,41 +359,52 @@ __global__ void __launch_bounds__(kLoadBlock, load_ctas(FMT)) load_q4_kernel(con
       more2 = units - u > stride;
       if (more2) place(u + stride, after);
     }
-    if (cur.at == kBad && cur.h == 0 && G == 0 && t4 == 0) set_status(a.status, cur.why);
-    const bool stk = cur.at != kSkip && with_k, stv = cur.at != kSkip && with_v;
-    uint8_t* ok = static_cast<uint8_t*>(a.k.data) +
-                  ((cur.t * a.k.ts + cur.h * a.k.hs + 32 * G + 8 * t4) << (k_dtype == KVQ_DT_BF16 ? 1 : 2));
-    uint8_t* ov = static_cast<uint8_t*>(a.v.data) +
-                  ((cur.t * a.v.ts + cur.h * a.v.hs + 32 * G + 8 * t4) << (v_dtype == KVQ_DT_BF16 ? 1 : 2));
+    if (!FEW && cur.at == kBad && cur.h == 0 && G == 0 && t4 == 0) set_status(a.status, cur.why);
+    bool here = cur.at != kSkip;
+    const int k_shift = k_dtype == KVQ_DT_BF16 ? 1 : 2, v_shift = v_dtype == KVQ_DT_BF16 ? 1 : 2;
+    uint8_t* ok = static_cast<uint8_t*>(a.k.data) + ((cur.t * a.k.ts + cur.h * a.k.hs + 32 * G + 8 * t4) << k_shift);
+    uint8_t* ov = static_cast<uint8_t*>(a.v.data) + ((cur.t * a.v.ts + cur.h * a.v.hs + 32 * G + 8 * t4) << v_shift);
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-      if (i >= hpu || cur.h + i >= Hk) break;
+      uint8_t *dk = ok, *dv = ov;
+      if constexpr (FEW) {
+        here = __shfl_sync(0xffffffffu, cur.row, token(i)) != -1;
+        dk += (token(i) * a.k.ts + head(i) * a.k.hs) << k_shift;
+        dv += (token(i) * a.v.ts + head(i) * a.v.hs) << v_shift;
+      } else if (i >= hpu || cur.h + i >= Hk) {
+        break;
+      }
       float x[2][8];
       if constexpr (ROT) {
         uint32_t pk[4], pv[4];
         code_operands<FMT>(word[i][0], pk);
         code_operands<FMT>(word[i][1], pv);
+        uint32_t lk[4], lv[4];  // TQ4: what the sums over the groups have below fp16
+        if constexpr (FMT == KVQ_FMT_TQ4) {
+          // the transform over the row's groups first: H of the groups times the pairs,
+          // turned so that the groups are the terms; K and V are two blocks of one product
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float d[4];
+            mma_f16_c(d, hg, 0u, 0u, hg, movmatrix_trans(pk[q]), movmatrix_trans(pv[q]), 0.f, 0.f, 0.f, 0.f);
+            split_sums(d[0], d[1], pk[q], lk[q]);
+            split_sums(d[2], d[3], pv[q], lv[q]);
+          }
+        }
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
           float c[4];
           mma_f16_c(c, pk[0], pv[0], pk[1], pv[1], H.at(0, 0, nt), H.at(0, 1, nt), nt ? 0.f : c0, nt ? 0.f : c1,
                     nt ? 0.f : c0, nt ? 0.f : c1);
           mma_f16(c, pk[2], pv[2], pk[3], pv[3], H.at(1, 0, nt), H.at(1, 1, nt));
+          if constexpr (FMT == KVQ_FMT_TQ4) {
+            mma_f16(c, lk[0], lv[0], lk[1], lv[1], H.at(0, 0, nt), H.at(0, 1, nt));
+            mma_f16(c, lk[2], lv[2], lk[3], lv[3], H.at(1, 0, nt), H.at(1, 1, nt));
+          }
           x[0][2 * nt] = c[0];
           x[0][2 * nt + 1] = c[1];
           x[1][2 * nt] = c[2];
           x[1][2 * nt + 1] = c[3];
-        }
-        if constexpr (FMT == KVQ_FMT_TQ4) {
-#pragma unroll
-          for (int o = 1; o < NG; o <<= 1) {  // the stages between the row's groups
-            const float sgn = (G & o) ? -1.f : 1.f;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                x[kv][j] = __fmaf_rn(x[kv][j], sgn, __shfl_xor_sync(0xffffffffu, x[kv][j], 4 * o));
-          }
         }
       } else {
         code_values<FMT>(word[i][0], x[0]);
@@ -353,16 +416,16 @@ __global__ void __launch_bounds__(kLoadBlock, load_ctas(FMT)) load_q4_kernel(con
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           uint64_t f2 = pk2(f, f);
-          if constexpr (FMT == KVQ_FMT_TQ4 && ROT)
-            f2 = pk2(__uint_as_float(__float_as_uint(f) ^ ((sw << (31 - j)) & 0x80000000u)),
-                     __uint_as_float(__float_as_uint(f) ^ ((sw << (30 - j)) & 0x80000000u)));
+          if constexpr (FMT == KVQ_FMT_TQ4 && ROT) f2 = mul2(f2, sign2[j / 2]);
           upk2(mul2(pk2(x[kv][j], x[kv][j + 1]), f2), x[kv][j], x[kv][j + 1]);
         }
       }
-      if (stk) put_values<8>(ok, k_dtype, k_wide, x[0]);
-      if (stv) put_values<8>(ov, v_dtype, v_wide, x[1]);
-      ok += ok_step;
-      ov += ov_step;
+      if (here && with_k) put_values<8>(dk, k_dtype, k_wide, x[0]);
+      if (here && with_v) put_values<8>(dv, v_dtype, v_wide, x[1]);
+      if constexpr (!FEW) {
+        ok += ok_step;
+        ov += ov_step;
+      }
     }
     if (!more) break;
     cur = nxt;
@@ -459,37 +522,48 @@ cudaError_t launch_load(const LoadArgs& args, cudaStream_t s) {
   if (!wide) {
     // Units of 8 / NG tokens and hpu heads, walked by as many warps as are resident at
     // once.  hpu: the one whose rounds cost least, a round its heads' work and about
-    // one head's for the unit itself (4096 tokens of 4 heads: one round and a bit of
-    // 4 heads would be two).
+    // one head's for the unit itself, times the CTAs that share an SM (4096 tokens of 4
+    // heads: one round and a bit of 4 heads would be two).
     const int64_t n_sm = device_sm_count() > 0 ? device_sm_count() : 1;
-    const int64_t resident = n_sm * load_ctas(a.c.format);
     const int64_t blocks8 = (n_tok * NG + 7) / 8;
-    int hpu = 1;
+    auto cost = [&](int64_t units, int tiles, int ctas) {
+      const int64_t warps = n_sm * ctas * (kLoadBlock / 32);
+      return (units + warps - 1) / warps * ctas * (tiles + 1);
+    };
+    int ctas_sm = load_ctas(a.c.format, false), hpu = 1;
     int64_t best = 0;
     for (int h = 1; h <= kHeads; h *= 2) {
-      const int64_t units = blocks8 * ((Hk + h - 1) / h), warps = resident * (kLoadBlock / 32);
-      const int64_t cost = (units + warps - 1) / warps * (h + 1);
-      if (h == 1 || cost < best) best = cost, hpu = h;
+      const int64_t c = cost(blocks8 * ((Hk + h - 1) / h), h, ctas_sm);
+      if (h == 1 || c < best) best = c, hpu = h;
     }
+    // One or two heads: a unit of several token blocks instead, by the same costs (one
+    // head of 200011 tokens 50 us so, 96 us by single blocks; of 4001 tokens 3.5 and 4.4
+    // us; 2048 tokens are one round of single blocks).
+    const bool plain = kvs == 2 && a.k.wide && a.v.wide && a.k.dtype == a.v.dtype;
+    const int64_t tpu = Hk <= 2 ? kHeads / Hk : 1;
+    const bool few = plain && tpu > 1 && cost((blocks8 + tpu - 1) / tpu, kHeads, load_ctas(a.c.format, true)) < best;
+    if (few) ctas_sm = load_ctas(a.c.format, true);
+    const int64_t resident = n_sm * ctas_sm;
     // at most 2^30 units in a launch
-    const int64_t per_tok = (Hk + hpu - 1) / hpu, max_tok = (int64_t(1) << 30) / per_tok / 8 * 8;
+    const int64_t per_tok = few ? 1 : (Hk + hpu - 1) / hpu, max_tok = (int64_t(1) << 30) / per_tok / 8 * 8;
     if (max_tok < 8) return cudaErrorInvalidValue;
     const FastDiv nb = make_fastdiv(static_cast<uint32_t>(per_tok));
-    const bool plain = kvs == 2 && a.k.wide && a.v.wide && a.k.dtype == a.v.dtype;
     const int out = !plain ? kAny : a.k.dtype == KVQ_DT_BF16 ? kBf16 : kF32;
     const dim3 block(kLoadBlock);
     for (a.t0 = 0; a.t0 < n_tok; a.t0 += max_tok) {
       a.n_tok = n_tok - a.t0 < max_tok ? n_tok : a.t0 + max_tok;  // tokens [t0, n_tok) in this launch
-      const int64_t units = ((a.n_tok - a.t0) * NG + 7) / 8 * per_tok;
+      const int64_t blocks = ((a.n_tok - a.t0) * NG + 7) / 8;
+      const int64_t units = few ? (blocks + tpu - 1) / tpu : blocks * per_tok;
       int64_t ctas = (units + kLoadBlock / 32 - 1) / (kLoadBlock / 32);
       if (ctas > resident) ctas = resident;
       const dim3 grid(static_cast<unsigned>(ctas));
-    cudaError_t e = cudaErrorInvalidValue;
-#define KVQ_LOAD_OUT(F, N, R, O) launch_pdl(load_q4_kernel<F, N, R, O>, grid, block, 0, s, a, nb, hpu, static_cast<uint32_t>(units))
-#define KVQ_LOAD(F, N, R)                                  \
-  e = out == kBf16  ? KVQ_LOAD_OUT(F, N, R, kBf16)         \
-      : out == kF32 ? KVQ_LOAD_OUT(F, N, R, kF32)          \
-                    : KVQ_LOAD_OUT(F, N, R, kAny);         \
+      cudaError_t e = cudaErrorInvalidValue;
+#define KVQ_LOAD_OUT(F, N, R, O, W) \
+  launch_pdl(load_q4_kernel<F, N, R, O, W>, grid, block, 0, s, a, nb, hpu, static_cast<uint32_t>(units))
+#define KVQ_LOAD(F, N, R)                                                                         \
+  e = out == kBf16  ? few ? KVQ_LOAD_OUT(F, N, R, kBf16, true) : KVQ_LOAD_OUT(F, N, R, kBf16, false) \
+      : out == kF32 ? few ? KVQ_LOAD_OUT(F, N, R, kF32, true) : KVQ_LOAD_OUT(F, N, R, kF32, false)   \
+                    : KVQ_LOAD_OUT(F, N, R, kAny, false);                                         \
   break
 #define KVQ_LOAD_NG(F, R)       \
   switch (NG) {                 \

@@ -455,6 +455,35 @@ def test_load_against_64_bits(K, fmt, D, Hk, dtype):
         assert torch.equal(wide[:, :Hk, 1:], both) and torch.equal(wide[:, Hk:, 1:], v) and (wide[..., 0] == 5).all()
 
 
+@pytest.mark.parametrize("fmt,D", [("Q4_HAD32", 32), ("Q4_HAD32", 64), ("Q4_HAD32", 128), ("Q4_HAD32", 256),
+                                   ("TQ4", 64), ("TQ4", 128), ("TQ4", 256), ("Q4_0", 32), ("Q4_0", 256)])
+@pytest.mark.parametrize("Hk", [1, 2])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_load_few_heads(K, fmt, D, Hk, dtype):
+    """One and two heads in more rows than one round of the warps, among them positions
+    that keep what they hold, positions without a row, and views with gaps: against the
+    same rows loaded a few at a time, bit for bit."""
+    n, pages = 40037, 2600
+    cache = make_cache(K, getattr(K, "FMT_" + fmt), Hk, D, pages)
+    fill_random(cache, K, D + Hk)
+    g = torch.Generator(device=DEV).manual_seed(D + Hk)
+    slots = torch.randperm(pages * 16, generator=g, device=DEV)[:n].to(torch.int32)
+    skip, bad = [0, 3, 32, 17000, n - 1], [1, 33, 20001, n - 2]
+    broken = slots.clone()
+    broken[skip], broken[bad] = -1, pages * 16
+    bufs = [torch.full((n, 2 * Hk, D), 777.0, dtype=dtype, device=DEV) for _ in range(2)]
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    K.load(cache, broken, k=bufs[0][:, :Hk], v=bufs[1][:, Hk:], status=status)
+    assert K.read_status(status) == K.DEV_BAD_SLOT
+    parts = [K.load(cache, slots[i:i + 997], dtype=dtype) for i in range(0, n, 997)]
+    want = [torch.cat([p[j] for p in parts]) for j in range(2)]
+    for w in want:
+        w[skip], w[bad] = 777.0, float("nan")
+    assert torch.equal(bufs[0][:, :Hk].nan_to_num(nan=-5.0), want[0].nan_to_num(nan=-5.0))
+    assert torch.equal(bufs[1][:, Hk:].nan_to_num(nan=-5.0), want[1].nan_to_num(nan=-5.0))
+    assert (bufs[0][:, Hk:] == 777).all() and (bufs[1][:, :Hk] == 777).all()
+
+
 @pytest.mark.parametrize("fmt,D,Hk", [("Q4_HAD32", 32, 3), ("Q4_HAD32", 64, 5), ("Q4_HAD32", 128, 2),
                                       ("Q4_HAD32", 256, 4), ("Q4_HAD32", 256, 9), ("TQ4", 64, 1), ("TQ4", 128, 6),
                                       ("TQ4", 256, 4), ("Q4_0", 256, 8), ("BF16", 128, 3), ("FP8_ROW", 512, 1)])
