@@ -52,18 +52,22 @@ enum Mode { kAny, kBf16ToBf16, kBf16ToF32, kF32ToF32 };
 // for each warp (a.per batches): no warp waits for another's last token, and a warp
 // works out the angles of the few tokens that its range touches.  The next token's
 // positions, slot and first rows are loaded during a token's last batches.
-template <int LPR, int FMT, int MODE>
+// FEW (rows that are only normed and rotated, few heads): a batch is one head of RPW
+// tokens next to one another instead, each with its own angles ("token" then stands
+// for such a group).
+template <int LPR, int FMT, int MODE, bool FEW>
 __global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-  __shared__ float4 angles_sh[kMaxWarps][2 * kChunks];
+  constexpr int kTokenChunks = FEW ? E * LPR / 4 + E * LPR / 32 : kChunks;  // of a copy of a token's angles
+  __shared__ float4 angles_sh[kMaxWarps][(FEW ? 32 / LPR : 1) * 2 * kTokenChunks];
   pdl_wait();
   pdl_trigger();
   constexpr int D = E * LPR, RPW = 32 / LPR;
   constexpr bool BF = MODE == kBf16ToBf16 || MODE == kBf16ToF32;
-  constexpr int U = BF ? 2 : 1;
+  constexpr int U = BF && !FEW ? 2 : 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
   // a token's batches of RPW heads: first the queries', then K's, then V's
-  const int qb = (a.Hq + RPW - 1) / RPW, kb = (a.Hk + RPW - 1) / RPW, total = qb + 2 * kb;
-  const int64_t all = a.n_tok * total;
+  const int qb = FEW ? a.Hq : (a.Hq + RPW - 1) / RPW, kb = (a.Hk + RPW - 1) / RPW, total = qb + 2 * kb;
+  const int64_t all = (FEW ? (a.n_tok + RPW - 1) / RPW : a.n_tok) * total;
   int64_t left = ((int64_t)blockIdx.x * (blockDim.x >> 5) + warp) * a.per;  // this warp's first batch
   if (left >= all) return;
   int64_t tok = left / total;
@@ -73,12 +77,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(con
   const auto in_type = [&](const RowsView& v) { return MODE == kAny ? v.dtype : BF ? KVQ_DT_BF16 : KVQ_DT_F32; };
   const auto wide = [&](const RowsView& v) { return MODE == kAny ? v.wide : 1; };
   const int out_type = MODE == kAny ? a.qo.dtype : MODE == kBf16ToBf16 ? KVQ_DT_BF16 : KVQ_DT_F32;
+  const auto query = [&](int b) { return FEW ? b : b * RPW + sub; };  // the lane's head of a batch
+  const auto token = [&](int64_t t) { return FEW ? t * RPW + sub : t; };
+  const auto live = [&](int64_t t, int b) { return FEW ? token(t) < a.n_tok : query(b) < a.Hq; };
   // address of the lane's part of head h's row, and bytes from a batch of queries to the next
   const auto row_of = [&](const RowsView& v, int type, int64_t t, int h) {
     return static_cast<uint8_t*>(v.data) + ((t * v.ts + h * v.hs + E * l) << (type == KVQ_DT_BF16 ? 1 : 2));
   };
-  const int64_t step = (a.q.hs * RPW) << (in_type(a.q) == KVQ_DT_BF16 ? 1 : 2);
-  const int64_t out_step = (a.qo.hs * RPW) << (out_type == KVQ_DT_BF16 ? 1 : 2);
+  const int64_t step = (a.q.hs * (FEW ? 1 : RPW)) << (in_type(a.q) == KVQ_DT_BF16 ? 1 : 2);
+  const int64_t out_step = (a.qo.hs * (FEW ? 1 : RPW)) << (out_type == KVQ_DT_BF16 ? 1 : 2);
 
   RawRow<E, BF> next[U];  // the rows after those being worked on
   const uint8_t* at;      // the first one's address in this lane
@@ -92,21 +99,21 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(con
     const RowsView& v = is_v ? a.v : a.k;
     if (h < a.Hk) load_raw_at<E, BF>(row_of(v, in_type(v), t, h), in_type(v), wide(v), next[0]);
   };
-  const auto load_q = [&](int b, int end) {  // U batches of queries from b on, before `end`, at `at`
+  const auto load_q = [&](int64_t t, int b, int end) {  // U batches of queries from b on, before `end`, at `at`
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (b + u < end && (b + u) * RPW + sub < a.Hq)
+      if (b + u < end && live(t, b + u))
         load_raw_at<E, BF>(at + u * step, in_type(a.q), wide(a.q), next[u]);
   };
-  int32_t pos[4], slot = -1;
+  int32_t pos[4] = {}, slot = -1;
   const auto first_rows = [&](int64_t t, int b, int end) {  // of token t's batches [b, end), with its positions and slot
     if (b < qb) {
-      at = row_of(a.q, in_type(a.q), t, b * RPW + sub);
-      load_q(b, min(end, qb));
+      at = row_of(a.q, in_type(a.q), token(t), query(b));
+      load_q(t, b, min(end, qb));
     } else if (FMT != kNoStore) {
       load_kv(t, b);
     }
-    if (a.rope.rot != 0 && b < qb + kb) load_pos(a.rope, t, pos);
+    if (a.rope.rot != 0 && b < qb + kb && (!FEW || live(t, b))) load_pos(a.rope, token(t), pos);
     if (FMT != kNoStore && end > qb) slot = a.slots[t];
   };
   const auto end_of = [&](int b, int64_t n) { return static_cast<int>(n < total - b ? b + n : total); };
@@ -114,7 +121,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(con
   first_rows(tok, b0, b1);
 
   RopeLane g;
-  if (a.rope.rot != 0) g = rope_lane(a.rope, angles_sh[warp], lane, l);
+  float4* const angles = angles_sh[warp] + (FEW ? sub * 2 * kTokenChunks : 0);
+  if (a.rope.rot != 0) g = rope_lane<kTokenChunks>(a.rope, angles, lane, l);
   uint32_t sw = 0;
   if constexpr (FMT == KVQ_FMT_TQ4) sw = lane_signs<E>(a.c.signs, l);
   uint64_t w[E / 2];
@@ -125,18 +133,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(con
     const bool stores = FMT != kNoStore && b1 > qb;
     const int64_t rest = left - (b1 - b0);  // batches of the tokens after this one
     const int nb1 = end_of(0, rest);
-    if (a.rope.rot != 0 && b0 < qb + kb) make_angles(a.rope, pos, lane, a.status, angles_sh[warp]);
+    if (a.rope.rot != 0 && b0 < qb + kb) make_angles<FEW ? LPR : 32, kTokenChunks>(a.rope, pos, FEW ? l : lane, a.status, angles);
     const int32_t this_slot = slot;
     if (b0 < qb) {
       if (a.qn.weight && weights != 1) load_weight<E>(a.qn, l, w), weights = 1;
-      uint8_t* out = row_of(a.qo, out_type, tok, b0 * RPW + sub);
+      uint8_t* out = row_of(a.qo, out_type, token(tok), query(b0));
       for (int b = b0; b < be; b += U) {
         uint64_t x[U][E / 2];
 #pragma unroll
         for (int u = 0; u < U; ++u) unpack_row<E, BF>(next[u], x[u]);
         if (b + U < be) {
           at += U * step;
-          load_q(b + U, be);
+          load_q(tok, b + U, be);
         } else if (stores) {
           load_kv(tok, qb);
         } else if (rest > 0) {
@@ -162,7 +170,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(con
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (b + u < be && (b + u) * RPW + sub < a.Hq) write_row_at<E>(out + u * out_step, out_type, wide(a.qo), x[u]);
+          if (b + u < be && live(tok, b + u)) write_row_at<E>(out + u * out_step, out_type, wide(a.qo), x[u]);
         out += U * out_step;
       }
     }
@@ -221,17 +229,17 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(con
   }
 }
 
-template <int LPR, int FMT>
-cudaError_t launch_one(NormRopeArgs a, cudaStream_t s) {
+template <int LPR, int FMT, bool FEW>
+cudaError_t launch_ranges(NormRopeArgs a, cudaStream_t s) {
   // One range of batches for each resident warp (an even number, for the pairs of
   // query batches), one batch where there are fewer; and CTAs of fewer warps where
   // that leaves SMs without one.
   constexpr int RPW = 32 / LPR;
-  const int64_t total = (a.Hq + RPW - 1) / RPW + 2 * ((a.Hk + RPW - 1) / RPW);
+  const int64_t total = FEW ? a.Hq : (a.Hq + RPW - 1) / RPW + 2 * ((a.Hk + RPW - 1) / RPW);
   const int64_t n_sm = device_sm_count() > 0 ? device_sm_count() : 1;
-  const int64_t resident = n_sm * kMinCtas * kMaxWarps, all_batches = a.n_tok * total;
+  const int64_t resident = n_sm * kMinCtas * kMaxWarps, all_batches = (FEW ? (a.n_tok + RPW - 1) / RPW : a.n_tok) * total;
   int64_t per = (all_batches + resident - 1) / resident;
-  if (per > 1) per = (per + 1) / 2 * 2;
+  if (per > 1 && !FEW) per = (per + 1) / 2 * 2;
   a.per = per;
   const int64_t warps = (all_batches + per - 1) / per;
   int wpc = kMaxWarps;
@@ -243,16 +251,29 @@ cudaError_t launch_one(NormRopeArgs a, cudaStream_t s) {
   const bool out_f32 = !q || a.qo.dtype == KVQ_DT_F32;
   cudaError_t e;
   if (!whole || per == 1)
-    e = launch_pdl(norm_rope_kernel<LPR, FMT, kAny>, grid, block, 0, s, a);
+    e = launch_pdl(norm_rope_kernel<LPR, FMT, kAny, FEW>, grid, block, 0, s, a);
   else if (all(KVQ_DT_BF16))
-    e = out_f32 ? launch_pdl(norm_rope_kernel<LPR, FMT, kBf16ToF32>, grid, block, 0, s, a)
-                : launch_pdl(norm_rope_kernel<LPR, FMT, kBf16ToBf16>, grid, block, 0, s, a);
+    e = out_f32 ? launch_pdl(norm_rope_kernel<LPR, FMT, kBf16ToF32, FEW>, grid, block, 0, s, a)
+                : launch_pdl(norm_rope_kernel<LPR, FMT, kBf16ToBf16, FEW>, grid, block, 0, s, a);
   else if (all(KVQ_DT_F32) && out_f32)
-    e = launch_pdl(norm_rope_kernel<LPR, FMT, kF32ToF32>, grid, block, 0, s, a);
+    e = launch_pdl(norm_rope_kernel<LPR, FMT, kF32ToF32, FEW>, grid, block, 0, s, a);
   else
-    e = launch_pdl(norm_rope_kernel<LPR, FMT, kAny>, grid, block, 0, s, a);
+    e = launch_pdl(norm_rope_kernel<LPR, FMT, kAny, FEW>, grid, block, 0, s, a);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
+}
+
+template <int LPR, int FMT>
+cudaError_t launch_one(const NormRopeArgs& a, cudaStream_t s) {
+  // Few heads: half a batch of one token's heads or more would be empty, and there are
+  // more such batches than resident warps (one head of 128, 10336 tokens: 8.9 us so,
+  // 13.2 us by tokens; one of 64, 16384 tokens: 5.8 and 12.8 us; below that many tokens
+  // the angles are better spread over a whole warp).
+  constexpr int RPW = 32 / LPR;
+  if constexpr (FMT == kNoStore && RPW > 1)
+    if (2 * a.Hq <= RPW && a.n_tok > (int64_t)device_sm_count() * kMinCtas * kMaxWarps)
+      return launch_ranges<LPR, FMT, true>(a, s);
+  return launch_ranges<LPR, FMT, false>(a, s);
 }
 
 }  // namespace

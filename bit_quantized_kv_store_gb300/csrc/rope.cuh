@@ -55,15 +55,18 @@ __device__ __forceinline__ void load_pos(const RopeView& r, int64_t tok, int32_t
   for (int a = 0; a < 4; ++a) pos[a] = a < r.axes ? r.pos[a * r.pos_stride + tok] : 0;
 }
 
+// LANES lanes work out one token's angles, `lane` this one's place among them; CH: the
+// chunks of a copy.
+template <int LANES = 32, int CH = kChunks>
 __device__ __forceinline__ void make_angles(const RopeView& r, const int32_t (&pos)[4], int lane, int32_t* status,
                                             float4* sh) {
   __syncwarp();  // (the last token's have been read)
-  for (int p = lane; p < (r.rot >> 1); p += 32) {
+  for (int p = lane; p < (r.rot >> 1); p += LANES) {
     const float2 cs = angle(r, p, pos, status);
     float* at = reinterpret_cast<float*>(&sh[chunk_place(p >> 1)]) + (p & 1);
     at[0] = cs.x;
     at[2] = cs.y;
-    at += 4 * kChunks;
+    at += 4 * CH;
     at[0] = cs.x;
     at[2] = -cs.y;
   }
@@ -80,6 +83,7 @@ struct RopeLane {
   bool in[2];           // whether a block is rotated at all
 };
 
+template <int CH = kChunks>
 __device__ __forceinline__ RopeLane rope_lane(const RopeView& r, const float4* sh, int lane, int l) {
   RopeLane g;
   const int half = r.rot >> 1;
@@ -89,7 +93,7 @@ __device__ __forceinline__ RopeLane rope_lane(const RopeView& r, const float4* s
     g.in[k] = e < r.rot;
     const bool first = e < half;
     g.src[k] = lane - l + (!g.in[k] ? e : first ? e + half : e - half) / kRopeE;
-    g.cs[k] = sh + (first ? kChunks : 0) + chunk_place(g.in[k] ? (first ? e : e - half) / 2 : 0);
+    g.cs[k] = sh + (first ? CH : 0) + chunk_place(g.in[k] ? (first ? e : e - half) / 2 : 0);
   }
   if (r.interleaved) g.cs[0] = sh + chunk_place(g.in[0] ? kRopeE * l / 4 : 0);
   return g;

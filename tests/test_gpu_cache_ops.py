@@ -220,6 +220,28 @@ def test_norm_rope_strides_and_in_place(K, width, dtype):
     assert torch.equal(K.norm_rope(one, norm=norm), K.norm_rope(one.contiguous(), norm=norm))
 
 
+@pytest.mark.parametrize("width,heads,rot", [(64, 1, 64), (64, 1, 32), (64, 3, 64), (64, 4, 32), (64, 4, 64),
+                                             (128, 1, 128), (128, 1, 96), (128, 2, 32), (128, 2, 64), (128, 2, 128),
+                                             (256, 1, 32), (256, 1, 64), (256, 1, 96), (256, 1, 192), (256, 1, 256)])
+@pytest.mark.parametrize("interleaved,axes", [(0, 1), (1, 3)])
+@pytest.mark.parametrize("xt,yt", [(torch.bfloat16, torch.bfloat16), (torch.bfloat16, torch.float32),
+                                   (torch.float32, torch.float32), (torch.float32, torch.bfloat16)])
+def test_norm_rope_few_heads_of_many_tokens(K, width, heads, rot, interleaved, axes, xt, yt):
+    """One to four heads of more tokens than the warps that are resident: bit for bit the
+    rows that calls of a few tokens give, and nothing beside them."""
+    n = 5003
+    rope, _, _ = rope_of(K, rot, interleaved, axes)
+    pos = positions(axes, n, 7) if axes > 1 else positions(1, n, 7)[0]
+    x = rnd((n, heads + 1, width), "few", width, heads, dtype=xt)[:, :heads]
+    norm = K.Norm(rnd((width,), "few w", width), offset=1.0) if axes == 1 else None
+    buf, out = guarded((n, heads, width), yt)
+    K.norm_rope(x, pos, rope=rope, norm=norm, out=out)
+    want = [K.norm_rope(x[i:i + 701], pos[..., i:i + 701].contiguous(), rope=rope, norm=norm, dtype=yt)
+            for i in range(0, n, 701)]
+    assert torch.equal(out, torch.cat(want))
+    assert (buf[:64] == 777).all() and (buf[-64:] == 777).all()
+
+
 def test_norm_rope_values_that_are_not_numbers(K):
     """Infinities and NaN stay in their rows (and pairs); what lies past rot_dim stays as it is."""
     x = rnd((4, 2, 256), "nan")
