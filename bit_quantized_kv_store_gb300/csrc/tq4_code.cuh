@@ -100,20 +100,34 @@ __device__ __forceinline__ void tq4_row_codes(const float (&y)[E], uint32_t (&wo
   if (__hisinf(s16)) s16 = __ushort_as_half(0x7BFFu);  // saturate to 65504
   const float s = __half2float(s16);
 
+  // Element y has the code of the rounded quotient q = y / s: its magnitude is the number
+  // of midpoints below |q|, bit 3 is q < 0.  Without the division: s (11 bits) times a
+  // midpoint (at most 13) is exact, and the float above it divided by s lies more than
+  // half a step above the midpoint (its step is more than 2^-24 of it, half the
+  // midpoint's at most that), so |q| > mid exactly where |y| > s mid.  q is -0 where
+  // |y| / s <= 2^-150; both sides times 2^126 s are normal numbers.
+  float t[7];
+#pragma unroll
+  for (int j = 0; j < 7; ++j) t[j] = __fmul_rn(s, tq4_mid(j));
+  const float tiny = __fmul_rn(s, -5.9604644775390625e-8f);  // -2^-24 s
 #pragma unroll
   for (int q = 0; q < (E + 7) / 8; ++q) word[q] = 0;
 #pragma unroll
   for (int i = 0; i < E; ++i) {
-    uint32_t code = 0;
-    if (s > 0.0f) {
-      const float q = __fdiv_rn(y[i], s);
-      const float a = fabsf(q);
-      uint32_t m = 0;
+    const float a = fabsf(y[i]);
+    const bool hi = a > t[3];
+    const bool mid = a > (hi ? t[5] : t[1]);
+    const bool lo = a > (hi ? (mid ? t[6] : t[4]) : (mid ? t[2] : t[0]));
+    const bool neg = __fmul_rn(y[i], 8.507059173023461586e37f) < tiny;
+    uint32_t& w = word[i >> 3];
+    if (hi) w |= 4u << (4 * (i & 7));
+    if (mid) w |= 2u << (4 * (i & 7));
+    if (lo) w |= 1u << (4 * (i & 7));
+    if (neg) w |= 8u << (4 * (i & 7));
+  }
+  if (!(s > 0.0f)) {
 #pragma unroll
-      for (int j = 0; j < 7; ++j) m += a > tq4_mid(j) ? 1u : 0u;
-      code = (q < 0.0f ? 8u : 0u) | m;
-    }
-    word[i >> 3] |= code << (4 * (i & 7));
+    for (int q = 0; q < (E + 7) / 8; ++q) word[q] = 0;
   }
   s16_out = s16;
 }
