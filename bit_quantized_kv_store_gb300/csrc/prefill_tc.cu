@@ -15,9 +15,7 @@
 //                 for the other -- codes by 2-D TMA boxes of 16 rows with the
 //                 128-byte swizzle, scales by 1-D bulk copies;
 //  * warp 1       MMA issuer (one thread) and tensor-memory owner;
-//  * warps 4..7   softmax: one tensor-memory lane (= one row) per thread; they
-//                 also rotate and split the queries at the start and normalise,
-//                 rotate back and store the output at the end;
+//  * warps 4..7   softmax: one tensor-memory lane (= one row) per thread;
 //  * warps 8, 9, 12, 13   decode K exactly as the sum of two f16 terms
 //                 K_a = f16((c-8)s), K_b = (c-8)s - K_a (exact), written by
 //                 stmatrix, in two halves of 128 dims so that the next tile's
@@ -25,6 +23,12 @@
 //                 second half;
 //  * warps 10, 11, 14, 15 decode V: f16((c-8)s), written transposed (keys
 //                 contiguous per value dim) by stmatrix.trans.
+// At the start warps 4..15 rotate and split the queries and at the end they normalise,
+// rotate back and store the output: a third of the head's 8 groups each (a warp
+// reaches the tensor-memory lanes of its number modulo 4).  (By the softmax warps
+// alone 1024 rows at 4096 in three ranges took 313 us, so 300 us.  All warps wait for
+// the queries: producers that loaded the first tiles meanwhile cost every later tile
+// 12 %, 4096 rows at 16384 4.43 ms instead of 3.92 ms.)
 // Warp w runs on SM sub-partition w % 4, so each sub-partition holds a softmax
 // warp and decoders of one kind only; the decoders' and the softmax's loops are
 // kept rolled (16-column / 8-key steps) so that the four roles' code sharing a
@@ -44,6 +48,7 @@
 // rescales O lazily, only when the running maximum grows by more than 8 (base
 // 2), so P stays <= 256.
 #include "kernels.cuh"
+#include "rows.cuh"
 #include "tc05.cuh"
 
 namespace kvq {
@@ -81,6 +86,7 @@ struct PfSmem {
   uint64_t k_ready[2], k_free[2];  // per half of the head dims
   uint64_t s_full[2], s_free[2];   // per S buffer
   uint64_t v_ready, p_full, pv_done, drained;
+  float inv[128];  // per row: 1 / z, at the end
   uint32_t tmem_base;
   int abort;
   int poison;
@@ -220,16 +226,21 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
   const uint32_t tbase = sm.tmem_base;
   const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
 
-  if (warp >= 4 && warp < 8) {
+  // warps 4..15: this thread's row, and the groups of 32 dims that it prepares and stores
+  const int r = 32 * (warp & 3) + lane;
+  const int iq = r / grp, h = r % grp;
+  const bool valid = (r < qpb * grp) && (iq < nq_blk);
+  const int G0 = 3 * ((warp >> 2) - 1), G1 = min(G0 + 3, 8);
+  const bool part = a.ws_acc != nullptr;  // partials: as they are, in the cache's space
+  const int64_t prow_i = ((int64_t)blockIdx.z * a.n_q + q0 + iq) * a.Hq + kvh * grp + h;
+  if (warp >= 4) {
     // ---------------- queries: rotate, scale, split; q_hi -> TMEM, q_lo -> smem
-    const int r = 32 * (warp - 4) + lane;
-    const int iq = r / grp, h = r % grp;
-    const bool valid = (r < qpb * grp) && (iq < nq_blk);
     const int64_t qrow = ((int64_t)(q0 + iq) * a.Hq + kvh * grp + h) * kPfDim;
     // by 16 bytes at a time (a warp's loads touch 32 rows, a line each, whatever their
     // width: value by value they took about 16 us of every CTA)
     const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0;
-    for (int G = 0; G < 8; ++G) {
+#pragma unroll 1
+    for (int G = G0; G < G1; ++G) {
       float x[32];
       if (!valid) {
 #pragma unroll
@@ -381,13 +392,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
       // every MMA issued so far has finished before tensor memory is released
       // (bounded, and independent of the abort flag)
       umma_commit(&sm.drained);
-      mbar_wait_bounded(&sm.drained, 0);
+      if (!mbar_wait_bounded(&sm.drained, 0)) {
+        atomicExch(&sm.abort, 1);
+        set_status(a.status, KVQ_DEV_TIMEOUT);
+      }
     }
   } else if (warp >= 4 && warp < 8) {
     // ---------------- softmax, one row per thread
-    const int r = 32 * (warp - 4) + lane;
-    const int iq = r / grp, h = r % grp;
-    const bool valid = (r < qpb * grp) && (iq < nq_blk);
     const int qpos = a.q_start + q0 + iq;  // keys 0 .. qpos
     uint8_t* prow = sm.p + (r >> 3) * 1024 + (r & 7) * 16;
     // tcgen05.ld/st are warp-collective (.sync.aligned): every branch around
@@ -461,41 +472,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
       fence_proxy_async();
       warp_arrive(&sm.p_full, lane);
     }
-    // ---------------- epilogue: O / z, rotate back, store
-    if (ok) ok = pf_wait_warp(sm, &sm.pv_done, (ntiles - 1) & 1, a.status);
-    if (ok) {
-      tc_fence_after();
-      const bool bad = sm.poison != 0 || sm.abort != 0;
-      const bool part = a.ws_acc != nullptr;  // a partial: as it is, in the cache's space
-      const float inv = part ? 1.f : (z > 0.f) ? 1.f / z : 0.f;
-      const int64_t prow_i = (((int64_t)blockIdx.z * a.n_q + q0 + iq) * a.Hq + kvh * grp + h);
-      if (part && valid) {
-        a.ws_m[prow_i] = bad ? NAN : m_run;
-        a.ws_z[prow_i] = z;
-      }
-      for (int G = 0; G < 8; ++G) {
-        uint32_t o[32];
-        __syncwarp();  // reconverge after the previous iteration's per-row store
-        tmem_ld32(tbase + lane_off + kTmO + 32 * G, o);
-        tmem_wait_ld();
-        float x[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * inv;
-        const bool rot = a.rotate != 0 && !part;  // Q4_0: nothing to rotate back
-        if (rot) {
-          fwht32_regs(x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __fmul_rn(x[i], kHadamardScale);
-        }
-        if (valid) {
-          float* dst = (part ? a.ws_acc + prow_i * kPfDim
-                             : a.out + ((int64_t)(q0 + iq) * a.Hq + kvh * grp + h) * kPfDim) + 32 * G;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(dst + i) =
-                bad ? make_float4(NAN, NAN, NAN, NAN) : make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        }
-      }
+    sm.inv[r] = part ? 1.f : (z > 0.f) ? 1.f / z : 0.f;
+    if (part && valid) {
+      a.ws_m[prow_i] = m_run;
+      a.ws_z[prow_i] = z;
     }
   } else if (warp >= 8 && (warp & 2) == 0) {
     // ---------------- K decoder (warps 8, 9, 12, 13): key blocks 2kw, 2kw+1 of every tile, by halves
@@ -596,6 +576,44 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
 
   pdl_trigger();
   tc_fence_before();
+  __syncthreads();  // every product has finished
+  tc_fence_after();
+  if (warp >= 4) {
+    // ---------------- epilogue: O / z, rotate back, store
+    const bool bad = sm.poison != 0 || sm.abort != 0;
+    const float inv = sm.inv[r];
+    if (part && bad && valid && warp < 8) a.ws_m[prow_i] = NAN;
+    float* const dst0 = part ? a.ws_acc + prow_i * kPfDim
+                             : a.out + ((int64_t)(q0 + iq) * a.Hq + kvh * grp + h) * kPfDim;
+    const bool wide = (reinterpret_cast<uintptr_t>(dst0) & 31u) == 0;  // whole sectors
+#pragma unroll 1
+    for (int G = G0; G < G1; ++G) {
+      uint32_t o[32];
+      __syncwarp();  // reconverge after the previous iteration's per-row store
+      tmem_ld32(tbase + lane_off + kTmO + 32 * G, o);
+      tmem_wait_ld();
+      float x[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * inv;
+      const bool rot = a.rotate != 0 && !part;  // Q4_0: nothing to rotate back
+      if (rot) {
+        fwht32_regs(x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = __fmul_rn(x[i], kHadamardScale);
+      }
+      if (!valid) continue;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(bad ? NAN : x[i]);
+      if (wide) {
+        st_words<32>(dst0 + 32 * G, o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<uint4*>(dst0 + 32 * G + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+      }
+    }
+    tc_fence_before();
+  }
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tbase, 512);
@@ -607,8 +625,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
 // second a quarter full.  The count that costs least, in the time of a 64-key tile
 // (2.2 us): the waves' tiles, 7 for a CTA's start and end, and the partials written
 // and read back (2 KB a row at about 5 TB/s).  Measured, merge included: 1024 rows
-// at 4096 in three ranges 314 us, 64 rows at 4000 in eight 42 us; the prefill alone
-// in one range 365 and 159 us.
+// at 4096 in three ranges 300 us, 64 rows at 4000 in eight 39 us; the prefill alone
+// in one range 361 and 157 us.  (4 or 2 instead of 7 choose the same counts for chunks
+// of 16 to 1024 rows.)
 int prefill_splits(int n_q, int Hq, int Hk, int q_start, int n_sm) {
   const int qpb = 128 / (Hq / Hk);
   const int64_t ctas = (int64_t)((n_q + qpb - 1) / qpb) * Hk;
