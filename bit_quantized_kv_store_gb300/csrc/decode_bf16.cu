@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kBfWarps * 32, 2) decode_bf16_kernel(const __g
   extern __shared__ uint8_t smem_raw[];
   BfSmem& sm = *reinterpret_cast<BfSmem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int p = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
   int32_t T;

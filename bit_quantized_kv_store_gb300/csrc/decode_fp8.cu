@@ -152,7 +152,7 @@ __global__ void __launch_bounds__((kF8Warps + 1) * 32, 1) decode_fp8_kernel(cons
   extern __shared__ uint8_t smem_raw[];
   F8Smem& sm = *reinterpret_cast<F8Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int hblk = blockIdx.x, p = blockIdx.y, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const kvq_cache& c = a.c;
   const int head0 = hblk * kF8Heads;

@@ -582,7 +582,7 @@ __device__ __forceinline__ void q4_fold_load(float4 (&v)[kQ4FoldCols][4], const 
 __device__ __forceinline__ void q4_fold(const float* m, const float* z, const float* acc, int64_t hs, int n,
                                         int group, float* wts, float* zsum, bool final, float* om, float* oz,
                                         float* oacc, int64_t ohs, float* out, bool rotate_back) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   float* mx = zsum + 8;  // [group]: the heads' maxima
   const int ncol = group * (kQ4D / 4);
   const int t = threadIdx.x;
@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(kQ4Warps * 32, MINB ? MINB : q4_min_blocks(NT)
       *reinterpret_cast<Q4Smem<NT, GATHER, VR>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   constexpr int kTile = q4_tile_bytes<GATHER>();
   const int p = blockIdx.x, kvh = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   // rows [b, b + nr): one sequence, or a slice of a window's rows
   const int b = WIN ? blockIdx.z * a.rows_per_cta : blockIdx.z;
@@ -1543,7 +1543,7 @@ __global__ void __launch_bounds__(2 * kRoles * 32, 2) decode_q4_spec_kernel(cons
   SpecSmem<GATHER>& sm =
       *reinterpret_cast<SpecSmem<GATHER>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int p = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const bool scorer = warp < kRoles;
   const int rw = warp & (kRoles - 1);  // the warp's index within its role

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(T) merge_diff_row_kernel(const MergeArgs a, co
   pdl_trigger();
   constexpr int D = 32 * kDiffGroups;
   const int ho = blockIdx.x, b = blockIdx.y;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = warp_index();
   const int64_t out0 = ((int64_t)b * (a.Hq >> 1) + ho) * D;
   const int32_t keys = keys_of(a, b);
   if (keys <= 0) {
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(256) prefill_diff_merge_kernel(const __grid_co
   pdl_trigger();
   constexpr int E = 8, W = 256;
   const int lane = threadIdx.x & 31, heads = a.Hq / 2;
-  const uint32_t i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);  // row * output heads + head
+  const uint32_t i = blockIdx.x * (blockDim.x >> 5) + warp_index();  // row * output heads + head
   if (i >= static_cast<uint32_t>(a.n_q) * heads) return;
   const uint32_t row = fast_div(i, hd), h = i - row * hd.d;
   const RowsView in{a.ws_acc, 0, 0, KVQ_DT_F32, 1};
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(256) diff_heads_kernel(const float* __restrict
   pdl_trigger();
   constexpr int W = 32 * E;
   const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);  // row * output heads + head
+  const int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp_index();  // row * output heads + head
   if (i >= n) return;
   const uint32_t row = fast_div(static_cast<uint32_t>(i), hd), h = static_cast<uint32_t>(i) - row * hd.d;
   const RowsView in{const_cast<float*>(x), 0, 0, KVQ_DT_F32, wide};

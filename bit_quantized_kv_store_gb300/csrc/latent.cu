@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_kernel(const __grid_consta
   __shared__ float4 angles_sh[kWarps][2 * kChunks];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = warp_index();
   const int64_t tok = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
   if (tok >= a.n_tok) return;
   // rows [h0, h1) of the token; row Hq is the latent row

@@ -20,8 +20,8 @@
 // were shared by fewer rows.  The angles (the same for every head) are worked out
 // once per token and warp, spread over its lanes, and read back from shared memory.
 //
-// Bound.  4099 x 24 heads of 256, bf16 to bf16 with norm and three axes: 18.7 us, 101
-// MB, 5.4 TB/s (80 % of the measured copy; the same kernel without norm and rotation
+// Bound.  4099 x 24 heads of 256, bf16 to bf16 with norm and three axes: 17.7 us, 101
+// MB, 5.7 TB/s (84 % of the measured copy; the same kernel without norm and rotation
 // takes as long, so what is left is filling and draining the memory pipe).  4096
 // tokens of 24 + 4 + 4 heads to rotated fp32 queries and 4-bit rows: 36.5 us, 172 MB,
 // 4.7 TB/s; 31 us without the norm, the rotations and the codes' arithmetic, the
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, kMinCtas) norm_rope_kernel(con
   constexpr int D = E * LPR, RPW = 32 / LPR;
   constexpr bool BF = MODE == kBf16ToBf16 || MODE == kBf16ToF32;
   constexpr int U = BF && !FEW ? 2 : 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, sub = lane / LPR;
+  const int lane = threadIdx.x & 31, warp = warp_index(), l = lane % LPR, sub = lane / LPR;
   // a token's batches of RPW heads: first the queries', then K's, then V's
   const int qb = FEW ? a.Hq : (a.Hq + RPW - 1) / RPW, kb = (a.Hk + RPW - 1) / RPW, total = qb + 2 * kb;
   const int64_t all = (FEW ? (a.n_tok + RPW - 1) / RPW : a.n_tok) * total;

@@ -25,10 +25,10 @@
 //                 contiguous per value dim) by stmatrix.trans.
 // At the start warps 4..15 rotate and split the queries and at the end they normalise,
 // rotate back and store the output: a third of the head's 8 groups each (a warp
-// reaches the tensor-memory lanes of its number modulo 4).  (By the softmax warps
-// alone 1024 rows at 4096 in three ranges took 313 us, so 300 us.  All warps wait for
-// the queries: producers that loaded the first tiles meanwhile cost every later tile
-// 12 %, 4096 rows at 16384 4.43 ms instead of 3.92 ms.)
+// reaches the tensor-memory lanes of its number modulo 4).  Only the MMA issuer waits
+// for the queries; the first tiles are loaded and decoded meanwhile.  (By the softmax
+// warps alone, everybody waiting: one row 12.7 us, so 9.8 us.  Without the warp's number
+// known to be uniform this cost every tile 12 %.)
 // Warp w runs on SM sub-partition w % 4, so each sub-partition holds a softmax
 // warp and decoders of one kind only; the decoders' and the softmax's loops are
 // kept rolled (16-column / 8-key steps) so that the four roles' code sharing a
@@ -85,7 +85,7 @@ struct PfSmem {
   uint64_t rawv_full[kPfStages], rawv_empty[kPfStages];
   uint64_t k_ready[2], k_free[2];  // per half of the head dims
   uint64_t s_full[2], s_free[2];   // per S buffer
-  uint64_t v_ready, p_full, pv_done, drained;
+  uint64_t v_ready, p_full, pv_done, drained, q_ready;
   float inv[128];  // per row: 1 / z, at the end
   uint32_t tmem_base;
   int abort;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
   pdl_wait();
   extern __shared__ uint8_t smem_raw[];
   PfSmem& sm = *reinterpret_cast<PfSmem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int qb = blockIdx.x, kvh = blockIdx.y;
   const kvq_cache& c = a.c;
   const int grp = a.group;
@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
     mbar_init(&sm.p_full, 4);
     mbar_init(&sm.pv_done, 1);
     mbar_init(&sm.drained, 1);
+    mbar_init(&sm.q_ready, 12);
     sm.abort = 0;
     sm.poison = 0;
     fence_barrier_init();
@@ -289,9 +290,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
     tmem_wait_st();
     fence_proxy_async();
     tc_fence_before();
+    warp_arrive(&sm.q_ready, lane);
   }
-  __syncthreads();  // queries ready (TMEM and shared memory)
-  tc_fence_after();
 
   if (warp == 0 || warp == 2) {
     // ---------------- producers: K pages (warp 0), V pages (warp 2)
@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
       const uint64_t dql = umma_desc(smem_u32(sm.qlo), 128, 4096);
       const uint64_t dp = umma_desc(smem_u32(sm.p), 128, 1024), dvt = umma_desc(smem_u32(sm.vt), 128, 1024);
       const uint32_t tq = tbase + kTmQhi;
-      bool ok = true;
+      bool ok = pf_wait(sm, &sm.q_ready, 0, a.status);  // queries ready (TMEM and shared memory)
+      tc_fence_after();
       for (int j = 0; j <= ntiles && ok; ++j) {
         if (j < ntiles) {
           const int b = j & 1;
@@ -623,11 +624,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
 // afterwards (kvq_prefill_diff).  One CTA takes 128 / group query positions of a KV
 // head, and a chunk of 1024 at depth 4096 is 196 CTAs on 152 SMs: two waves, the
 // second a quarter full.  The count that costs least, in the time of a 64-key tile
-// (2.2 us): the waves' tiles, 7 for a CTA's start and end, and the partials written
+// (2.0 us): the waves' tiles, 7 for a CTA's start and end, and the partials written
 // and read back (2 KB a row at about 5 TB/s).  Measured, merge included: 1024 rows
-// at 4096 in three ranges 300 us, 64 rows at 4000 in eight 39 us; the prefill alone
-// in one range 361 and 157 us.  (4 or 2 instead of 7 choose the same counts for chunks
-// of 16 to 1024 rows.)
+// at 4096 in three ranges 278 us, 64 rows at 4000 in eight 35 us; the prefill alone
+// in one range 339 and 148 us.  (4 or 2 instead of 7 choose the same counts for chunks of
+// 16 to 1024 rows.)
 int prefill_splits(int n_q, int Hq, int Hk, int q_start, int n_sm) {
   const int qpb = 128 / (Hq / Hk);
   const int64_t ctas = (int64_t)((n_q + qpb - 1) / qpb) * Hk;

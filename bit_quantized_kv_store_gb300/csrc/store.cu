@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(256) store_q4_group_kernel(kvq_cache c, const 
   pdl_wait();
   pdl_trigger();
   store_q4_group_warp<NG, ROT>(c, k, v, dtype, n_tok, slots, status,
-                               (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), hk, ps);
+                               (int64_t)blockIdx.x * (blockDim.x >> 5) + warp_index(), hk, ps);
 }
 
 // BF16 comparison format: plain copy / RNE conversion of each value.
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(256) rotate_kernel(const void* __restrict__ x,
                                                      int64_t n_groups) {
   pdl_wait();
   pdl_trigger();
-  rotate_warp(x, dtype, y, n_groups, (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5));
+  rotate_warp(x, dtype, y, n_groups, (int64_t)blockIdx.x * (blockDim.x >> 5) + warp_index());
 }
 
 // The decode step's two independent preparations in one launch: blocks

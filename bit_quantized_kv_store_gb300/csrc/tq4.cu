@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(256) store_tq4_kernel(kvq_cache c, const void*
   pdl_trigger();
   constexpr int D = 32 * E;
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp_index();
   const int Hk = c.num_kv_heads;
   if (row >= n_tok * Hk * 2) return;
   const int kv = static_cast<int>(row & 1);
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(256) tq4_rotate_kernel(const void* __restrict_
   pdl_trigger();
   constexpr int D = 32 * E;
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp_index();
   if (row >= rows) return;
   float v[E];
 #pragma unroll
