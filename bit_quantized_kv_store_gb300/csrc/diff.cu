@@ -12,8 +12,8 @@
 // back (the rotation is linear, so it runs once instead of twice) and the norm on
 // the result, without the merged heads going through memory.
 //
-// Bound: latency (one 32769-token sequence: 3.5 us after the decode's 12.7, the
-// partials 1.6 MB in L2; a ragged batch of 32 up to 8000: 5.5 us after 63, 12.6 MB).
+// Bound: latency (one 32769-token sequence: 3.5 us after the decode's 12.4, the
+// partials 1.6 MB in L2; a ragged batch of 32 up to 8000: 5.5 us after 61, 12.6 MB).
 #include "merge_fold.cuh"
 #include "rows.cuh"
 #include "tq4_code.cuh"
@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(512) merge_diff_kernel(const MergeArgs a, cons
   }
 }
 
-// Many heads, or few partitions: one CTA of T threads per (output head, sequence).  The fold's arithmetic (merge_fold.cuh) in another arrangement, with
-// the same bits: the running maximum of row r of 32 (partitions r, r + 32, ...)
+// Many heads, or few partitions: one CTA of T threads per (output head, sequence).
+// The fold's arithmetic (merge_fold.cuh) in another arrangement, with the same bits: the running maximum of row r of 32 (partitions r, r + 32, ...)
 // does not depend on the values, so one warp per map works out the rescaling
 // weights of every partition once; the other dimension, 64 chunks of 4 values in
 // T / 64 groups of 4 rows, is then plain multiply-adds over coalesced loads, the

@@ -23,9 +23,9 @@
 // Bound.  4099 x 24 heads of 256, bf16 to bf16 with norm and three axes: 17.7 us, 101
 // MB, 5.7 TB/s (84 % of the measured copy; the same kernel without norm and rotation
 // takes as long, so what is left is filling and draining the memory pipe).  4096
-// tokens of 24 + 4 + 4 heads to rotated fp32 queries and 4-bit rows: 36.5 us, 172 MB,
+// tokens of 24 + 4 + 4 heads to rotated fp32 queries and 4-bit rows: 36.2 us, 172 MB,
 // 4.7 TB/s; 31 us without the norm, the rotations and the codes' arithmetic, the
-// rest is issue (20.2 M instructions at 51 %).  One token: the launch.
+// rest is issue (20.2 M instructions at 52 %).  One token: the launch.
 // Measured and not kept (the 4096-token chunk with its read-back, 41.7 us): K and V
 // rows two batches side by side like the queries' 47.3 us, one batch at 80 registers
 // and 24 warps an SM 49.7 us, five CTAs of four warps at 96 registers 51.4 us.
