@@ -505,7 +505,7 @@ int32_t kvq_prefill_attn(const kvq_cache* cache, const void* q, int32_t dtype, i
   if (dtype != KVQ_DT_F32 && dtype != KVQ_DT_BF16) return KVQ_ERR_INVALID_ARG;
   if (num_q_heads / cache->num_kv_heads > 8) return KVQ_ERR_UNSUPPORTED;
   if (n_q == 0) return KVQ_OK;
-  if (!q || !out || !d_block_table || max_pages < 1) return KVQ_ERR_INVALID_ARG;
+  if (!q || !out || !aligned16(out) || !d_block_table || max_pages < 1) return KVQ_ERR_INVALID_ARG;
   if (static_cast<int64_t>(q_start) + n_q > static_cast<int64_t>(max_pages) * cache->page_size)
     return KVQ_ERR_INVALID_ARG;
   PrefillArgs a{};

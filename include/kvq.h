@@ -343,7 +343,7 @@ int32_t kvq_merge(const kvq_cache* cache, const void* workspace, size_t ws_bytes
  * q_start + i) attends keys 0 .. q_start + i of the sequence whose block table is
  * d_block_table; the chunk's own keys must already be stored (kvq_store).
  *   q:   device [n_q, num_q_heads, head_dim] of dtype, unrotated.
- *   out: device fp32 [n_q, num_q_heads, head_dim], rotated back.
+ *   out: device fp32 [n_q, num_q_heads, head_dim], 16-byte aligned, rotated back.
  *   Q4 only; head_dim == 256; num_q_heads / num_kv_heads <= 8. */
 int32_t kvq_prefill_attn(const kvq_cache* cache, const void* q, int32_t dtype, int32_t n_q,
                          int32_t num_q_heads, int32_t q_start, const int32_t* d_block_table,

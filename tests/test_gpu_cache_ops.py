@@ -949,6 +949,30 @@ def test_prefill_diff_bad_page(K):
     assert torch.isnan(out).all() and K.read_status(status) == K.DEV_BAD_PAGE
 
 
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "Q4_0"])
+@pytest.mark.parametrize("n,Hq", [(1, 8), (45, 24), (200, 12)])
+def test_prefill_attn_places_of_its_tensors(K, fmt, n, Hq):
+    """Outputs and queries off a 32-byte boundary: the same bits, nothing beside them; an
+    output off its 16 bytes is refused."""
+    T0 = 100
+    cache = make_cache(K, getattr(K, "FMT_" + fmt), 4, 256, 40)
+    fill_random(cache, K, n)
+    bt = torch.arange(40, dtype=torch.int32, device=DEV)
+    q = rnd((n, Hq, 256), "place q", n, scale=0.3)
+    want = K.prefill_attn(cache, q, T0, bt, 1 / 16)
+    for shift in (4, 8, 12):
+        buf = torch.full((n * Hq * 256 + 64,), 777.0, device=DEV)
+        out = buf[shift:shift + q.numel()].view(n, Hq, 256)
+        moved = torch.empty(q.numel() + 64, device=DEV)[shift // 4:shift // 4 + q.numel()].view(n, Hq, 256)
+        moved.copy_(q)
+        K.prefill_attn(cache, moved, T0, bt, 1 / 16, out=out)
+        assert torch.equal(out, want)
+        assert (buf[:shift] == 777).all() and (buf[shift + q.numel():] == 777).all()
+    off = torch.empty(q.numel() + 64, device=DEV)[1:1 + q.numel()].view(n, Hq, 256)
+    with pytest.raises(K.KvqError):
+        K.prefill_attn(cache, q, T0, bt, 1 / 16, out=off)
+
+
 # ------------------------------------------------------------------ a run of them together
 
 def serve_step(K, s):
