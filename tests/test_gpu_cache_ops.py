@@ -242,6 +242,24 @@ def test_norm_rope_few_heads_of_many_tokens(K, width, heads, rot, interleaved, a
     assert (buf[:64] == 777).all() and (buf[-64:] == 777).all()
 
 
+@pytest.mark.parametrize("width,heads,rot,interleaved", [(64, 1, 2, 1), (64, 2, 6, 1), (64, 4, 16, 0), (128, 1, 16, 0),
+                                                         (128, 2, 126, 1), (256, 1, 250, 1), (256, 1, 240, 0)])
+def test_norm_rope_few_heads_other_rotary_widths(K, width, heads, rot, interleaved):
+    """Rotary widths that end inside a lane, in place, strided, the last batch part
+    empty: bit for bit the rows of calls of a few tokens."""
+    n = 9002
+    axes = min(3, rot // 2)
+    rope, _, _ = rope_of(K, rot, interleaved, axes)
+    pos = positions(axes, n, 9) if axes > 1 else positions(1, n, 9)[0]
+    base = rnd((n, 3, heads, width), "few odd", width, heads, dtype=torch.bfloat16)
+    x = base[:, 1]
+    want = torch.cat([K.norm_rope(x[i:i + 501], pos[..., i:i + 501].contiguous(), rope=rope) for i in range(0, n, 501)])
+    beside = base.clone()
+    K.norm_rope(x, pos, rope=rope, out=x)
+    assert torch.equal(x, want)
+    assert torch.equal(base[:, 0], beside[:, 0]) and torch.equal(base[:, 2], beside[:, 2])
+
+
 def test_norm_rope_values_that_are_not_numbers(K):
     """Infinities and NaN stay in their rows (and pairs); what lies past rot_dim stays as it is."""
     x = rnd((4, 2, 256), "nan")
