@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(T) merge_diff_row_kernel(const MergeArgs a, co
     bool nan_seen = false;
     for (int i = lane; i < np; i += 32) {
       const float mi = m[i], zi = z[i];
-      nan_seen |= isnan(mi);
+      nan_seen |= isnan(mi) || isnan(zi);
       const float Mn = fmaxf(Mt, mi);
       float2 w = make_float2(1.f, 0.f);
       if (Mn != -INFINITY) {

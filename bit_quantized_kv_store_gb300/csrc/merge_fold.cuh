@@ -53,7 +53,7 @@ __device__ __forceinline__ float merge_fold(const float* m, const float* z, cons
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (i0 + 32 * k >= np) break;
-      nan_seen |= isnan(mv[k]);
+      nan_seen |= isnan(mv[k]) || isnan(zv[k]);  // (a bad page; keys whose every score is NaN, m = -inf)
       const float Mn = fmaxf(Mt, mv[k]);
       if (Mn == -INFINITY) continue;  // nothing attended so far
       const float wo = exp2f(Mt - Mn), wn = exp2f(mv[k] - Mn);

@@ -331,7 +331,8 @@ int32_t kvq_decode_attn_unrotated(const kvq_cache* cache, const void* q, int32_t
  * bit-reproducible), then out = blockdiag(H) o when rotate_back != 0 (Q4_HAD32),
  * or out = s * (H o) / sqrt(D) (TQ4: a second launch on out; the other formats
  * take rotate_back = 0).
- * A sequence with no keys gives zeros.  Arguments as for kvq_decode_attn.
+ * A sequence with no keys gives zeros; a NaN maximum or sum among its partials (a
+ * bad page, scores that are not numbers) NaN.  Arguments as for kvq_decode_attn.
  * out: device fp32 [num_seqs, num_q_heads, value width]. */
 int32_t kvq_merge(const kvq_cache* cache, const void* workspace, size_t ws_bytes, int32_t num_seqs,
                   int32_t num_q_heads, const int32_t* d_seq_lens, int32_t max_seq_len, int32_t n_sel,

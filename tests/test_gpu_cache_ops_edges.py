@@ -1,0 +1,54 @@
+"""The calls around the cache at values and layouts that the other tests leave out:
+keys and queries that are not numbers."""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_cache_ops import DEV, diff_problem, rnd
+from tests.test_gpu_parity import K  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ keys and queries that are not numbers
+
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "Q4_0", "TQ4", "BF16"])
+@pytest.mark.parametrize("T", [1, 2, 513, 512 * 33 + 1, 512 * 130 + 1])
+def test_a_key_that_is_not_a_number(K, fmt, T):
+    """The last key of one KV head is NaN, for most lengths alone in its partition: the
+    heads that attend it are NaN in the merge and in both arrangements of its
+    difference, the others as they are without it.  (Q4_0: a NaN among numbers is
+    stored as code 0 under their scale, so that the row stays finite.)"""
+    cache, q, lens, bt, T, ws = diff_problem(K, getattr(K, "FMT_" + fmt), [T])
+    lam = torch.rand(12, device=DEV)
+    at = T - 1
+    slot = (bt[0, at // 16] * 16 + at % 16).to(torch.int32)[None]
+    k, v = rnd((1, 4, 256), "nan key"), rnd((1, 4, 256), "nan value")
+    results = []
+    for bad in (False, True):
+        if bad:
+            k[0, 1, 7] = math.nan
+        K.store(cache, k, v, slot)
+        heads = K.decode(cache, q, lens, bt, T, 1 / 16, ws).clone()
+        results.append((heads, K.decode_diff(cache, q, lens, bt, T, 1 / 16, ws, lam)))
+    (h0, d0), (h1, d1) = results
+    gone = torch.isfinite if fmt == "Q4_0" else torch.isnan
+    assert gone(h1[0, 6:12]).all() and gone(d1[0, 3:6]).all()
+    for a, b, hit in ((h0, h1, slice(6, 12)), (d0, d1, slice(3, 6))):
+        keep = torch.ones(a.shape[1], dtype=torch.bool, device=DEV)
+        keep[hit] = False
+        assert torch.isfinite(a).all() and torch.equal(a[0, keep], b[0, keep])
+
+
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "Q4_0", "TQ4", "BF16"])
+@pytest.mark.parametrize("T", [1, 700, 40000])
+def test_a_query_that_is_not_a_number(K, fmt, T):
+    cache, q, lens, bt, T, ws = diff_problem(K, getattr(K, "FMT_" + fmt), [T])
+    lam = torch.rand(12, device=DEV)
+    q[0, 5, 9] = math.nan
+    heads = K.decode(cache, q, lens, bt, T, 1 / 16, ws)
+    assert torch.isnan(heads[0, 5]).all() and torch.isfinite(heads[0, :5]).all() and torch.isfinite(heads[0, 6:]).all()
+    for norm in (None, K.Norm(torch.ones(256, device=DEV))):
+        y = K.decode_diff(cache, q, lens, bt, T, 1 / 16, ws, lam, norm=norm)
+        assert torch.isnan(y[0, 2]).all() and torch.isfinite(y[0, :2]).all() and torch.isfinite(y[0, 3:]).all()
