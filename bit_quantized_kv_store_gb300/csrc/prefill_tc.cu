@@ -47,6 +47,8 @@
 // MMA issuer runs P.V of tile j after the scores of tile j+1.  The softmax
 // rescales O lazily, only when the running maximum grows by more than 8 (base
 // 2), so P stays <= 256.
+#include <climits>
+
 #include "kernels.cuh"
 #include "rows.cuh"
 #include "tc05.cuh"
@@ -89,7 +91,7 @@ struct PfSmem {
   float inv[128];  // per row: 1 / z, at the end
   uint32_t tmem_base;
   int abort;
-  int poison;
+  int bad_key;  // the first key in a page outside the pool (INT_MAX: none): rows from it on come out NaN
 };
 static_assert(sizeof(PfSmem) + 1024 <= 232448, "prefill shared memory exceeds the 227 KB per-CTA limit");
 
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
     mbar_init(&sm.drained, 1);
     mbar_init(&sm.q_ready, 12);
     sm.abort = 0;
-    sm.poison = 0;
+    sm.bad_key = INT_MAX;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
         if (!pf_wait(sm, &empty[s], ((j / kPfStages) & 1) ^ 1, a.status)) break;
         PfRaw& st = ring[s];
         int64_t rows[4];
-        uint32_t bytes = 0;
+        uint32_t bytes = 0, gone = 0;  // gone: bad pages
         for (int pg = 0; pg < 4; ++pg) {
           rows[pg] = -1;
           const int key0 = kbase + j * kPfKeys + 16 * pg;
@@ -316,11 +318,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
           const int32_t page = bt[key0 / c.page_size];
           if (page < 0 || page >= c.num_pages) {
             set_status(a.status, KVQ_DEV_BAD_PAGE);
-            sm.poison = 1;
+            atomicMin(&sm.bad_key, key0);
+            gone |= 1u << pg;
             continue;
           }
           rows[pg] = ((int64_t)page * c.num_kv_heads + kvh) * c.page_size + key0 % c.page_size;
           bytes += 16 * 128 + 16 * 16;
+        }
+        if (gone != 0) {
+          // rows before a bad page mask its keys: 0 x V must be 0, whatever the stage holds
+#pragma unroll 1
+          for (int i = 0; i < 64; ++i)
+            if ((gone >> (i >> 4)) & 1u) reinterpret_cast<uint4*>(st.scales)[i] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async();  // (before a later tile's copy into the same bytes)
         }
         if (bytes == 0) {
           mbar_arrive(&full[s]);
@@ -581,8 +591,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
   tc_fence_after();
   if (warp >= 4) {
     // ---------------- epilogue: O / z, rotate back, store
-    const bool bad = sm.poison != 0 || sm.abort != 0;
-    const float inv = sm.inv[r];
+    const bool bad = a.q_start + q0 + iq >= sm.bad_key || sm.abort != 0;
+    const float inv = bad ? NAN : sm.inv[r];
     if (part && bad && valid && warp < 8) a.ws_m[prow_i] = NAN;
     float* const dst0 = part ? a.ws_acc + prow_i * kPfDim
                              : a.out + ((int64_t)(q0 + iq) * a.Hq + kvh * grp + h) * kPfDim;
@@ -604,7 +614,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
       }
       if (!valid) continue;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(bad ? NAN : x[i]);
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
       if (wide) {
         st_words<32>(dst0 + 32 * G, o);
       } else {

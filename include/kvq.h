@@ -345,6 +345,10 @@ int32_t kvq_merge(const kvq_cache* cache, const void* workspace, size_t ws_bytes
  * d_block_table; the chunk's own keys must already be stored (kvq_store).
  *   q:   device [n_q, num_q_heads, head_dim] of dtype, unrotated.
  *   out: device fp32 [n_q, num_q_heads, head_dim], 16-byte aligned, rotated back.
+ *       Rows that attend a page outside the pool come out NaN (KVQ_DEV_BAD_PAGE), the
+ *       rows before it as they are without it.
+ *       (128 / group neighbouring positions share their products with V: a V row that is
+ *       not a number also reaches those of them that lie before it.)
  *   Q4 only; head_dim == 256; num_q_heads / num_kv_heads <= 8. */
 int32_t kvq_prefill_attn(const kvq_cache* cache, const void* q, int32_t dtype, int32_t n_q,
                          int32_t num_q_heads, int32_t q_start, const int32_t* d_block_table,
@@ -566,8 +570,8 @@ size_t kvq_prefill_diff_workspace_size(const kvq_cache* cache, int32_t n_q, int3
  *   q, dtype, n_q, num_q_heads, q_start, d_block_table, max_pages, sm_scale,
  *       d_status as for kvq_prefill_attn, num_q_heads / num_kv_heads 2, 4, 6 or 8.
  *   workspace: device, 32-byte aligned; its contents do not matter.
- *   out: device [n_q][num_q_heads / 2][256] of out_dtype.  Rows that meet a page
- *       outside the pool come out NaN (KVQ_DEV_BAD_PAGE).
+ *   out: device [n_q][num_q_heads / 2][256] of out_dtype.  Bad pages as for
+ *       kvq_prefill_attn.
  * Q4_HAD32 and Q4_0, head_dim 256. */
 int32_t kvq_prefill_diff(const kvq_cache* cache, const void* q, int32_t dtype, int32_t n_q, int32_t num_q_heads,
                          int32_t q_start, const int32_t* d_block_table, int32_t max_pages, float sm_scale,

@@ -1,11 +1,11 @@
 """The calls around the cache at values and layouts that the other tests leave out:
-keys and queries that are not numbers."""
+keys and queries that are not numbers, a bad page inside a prompt chunk."""
 import math
 
 import pytest
 import torch
 
-from tests.test_gpu_cache_ops import DEV, diff_problem, rnd
+from tests.test_gpu_cache_ops import DEV, diff_problem, fill_random, make_cache, rnd
 from tests.test_gpu_parity import K  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +52,35 @@ def test_a_query_that_is_not_a_number(K, fmt, T):
     for norm in (None, K.Norm(torch.ones(256, device=DEV))):
         y = K.decode_diff(cache, q, lens, bt, T, 1 / 16, ws, lam, norm=norm)
         assert torch.isnan(y[0, 2]).all() and torch.isfinite(y[0, :2]).all() and torch.isfinite(y[0, 3:]).all()
+
+
+# ------------------------------------------------------------------ a bad page inside a prompt chunk
+
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "Q4_0"])
+@pytest.mark.parametrize("T0,n,bad", [(0, 200, 2), (0, 200, 5), (1000, 100, 64), (40, 1, 1)])
+def test_rows_before_a_bad_page(K, fmt, T0, n, bad):
+    """Rows that attend the page are NaN, the rows before it what they are with a good
+    one, also those that share a query block with NaN rows."""
+    f = getattr(K, "FMT_" + fmt)
+    pages = (T0 + n + 15) // 16
+    cache = make_cache(K, f, 4, 256, pages)
+    fill_random(cache, K, n)
+    junk = make_cache(K, f, 4, 256, pages)      # fills the shared memory with rows of NaN first
+    for name in ("k", "v"):
+        getattr(junk, name + "_scale").fill_(math.nan)
+    bt = torch.arange(pages, dtype=torch.int32, device=DEV)
+    broken = bt.clone()
+    broken[bad] = pages
+    q = rnd((n, 24, 256), "bp rows", n, scale=0.1)
+    lam = torch.rand(12, device=DEV)
+    first = max(0, min(n, 16 * bad - T0))        # the first row that attends the page
+    for call in (lambda c, t, s: K.prefill_attn(c, q, T0, t, 1 / 16, status=s),
+                 lambda c, t, s: K.prefill_diff(c, q, T0, t, 1 / 16, lam, status=s),
+                 lambda c, t, s: K.prefill_diff(c, q, T0, t, 1 / 16, lam, norm=K.Norm(torch.ones(256, device=DEV)), status=s)):
+        want = call(cache, bt, None)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        call(junk, bt, None)
+        got = call(cache, broken, status)
+        assert K.read_status(status) == K.DEV_BAD_PAGE
+        assert torch.isfinite(want).all() and torch.equal(got[:first], want[:first])
+        assert torch.isnan(got[first:]).all()
