@@ -620,20 +620,22 @@ int32_t kvq_read_status(const void* d_status, int32_t* host_code, void* stream) 
 
 static bool dtype_ok(int32_t d) { return d == KVQ_DT_F32 || d == KVQ_DT_BF16; }
 
-// Checks of a strided activation tensor of `heads` heads of `width` values and its
-// view (whole-vector access where every row starts on a 32-byte boundary).
-static int32_t check_rows(const kvq_rows* r, int32_t heads, int32_t width, RowsView* v) {
+// Checks of a strided activation tensor of n_tok tokens' `heads` heads of `width`
+// values and its view (whole-vector access where every row starts on a 32-byte boundary).
+// The stride of a dimension of one element reaches nothing and is taken as 0.
+static int32_t check_rows(const kvq_rows* r, int64_t n_tok, int32_t heads, int32_t width, RowsView* v) {
   if (!r) return KVQ_ERR_INVALID_ARG;
   if (!r->data || !dtype_ok(r->dtype) || r->heads != heads) return KVQ_ERR_INVALID_ARG;
-  if (r->tok_stride < 0 || r->head_stride < 0) return KVQ_ERR_INVALID_ARG;
+  const int64_t ts = n_tok > 1 ? r->tok_stride : 0, hs = heads > 1 ? r->head_stride : 0;
+  if (ts < 0 || hs < 0) return KVQ_ERR_INVALID_ARG;
   const uint64_t esz = r->dtype == KVQ_DT_F32 ? 4 : 2;
   const uintptr_t base = reinterpret_cast<uintptr_t>(r->data);
   if (base % esz != 0) return KVQ_ERR_INVALID_ARG;
   // offsets are products in 64 bits
-  if (r->tok_stride > (int64_t(1) << 31) || r->head_stride > (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
-  const uint64_t off = base | static_cast<uint64_t>(r->tok_stride) * esz | static_cast<uint64_t>(r->head_stride) * esz |
+  if (ts > (int64_t(1) << 31) || hs > (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
+  const uint64_t off = base | static_cast<uint64_t>(ts) * esz | static_cast<uint64_t>(hs) * esz |
                        static_cast<uint64_t>(width) * esz;
-  *v = RowsView{r->data, r->tok_stride, r->head_stride, r->dtype, off % 32 == 0 ? 1 : 0};
+  *v = RowsView{r->data, ts, hs, r->dtype, off % 32 == 0 ? 1 : 0};
   return KVQ_OK;
 }
 
@@ -644,6 +646,11 @@ static bool rows_distinct(const kvq_rows* r, int64_t n_tok, int32_t width) {
   if (r->heads == 1 || n_tok == 1) return true;
   // tokens outside heads, or heads outside tokens
   return ts >= (r->heads - 1) * hs + width || hs >= (n_tok - 1) * ts + width;
+}
+
+// Written in place: the same rows of the same type, or other data altogether.
+static bool in_place_or_apart(const RowsView& x, const RowsView& y) {
+  return x.data != y.data || (x.dtype == y.dtype && x.ts == y.ts && x.hs == y.hs);
 }
 
 static int32_t check_norm(const kvq_norm* n, NormView* v) {
@@ -698,15 +705,13 @@ int32_t kvq_norm_rope(const kvq_rows* x, const kvq_rows* y, int64_t n_tok, int32
   if (!x || !y || x->heads < 1) return KVQ_ERR_INVALID_ARG;
   if (x->heads > kMaxHeads || n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   NormRopeArgs a{};
-  int32_t st = check_rows(x, x->heads, width, &a.q);
-  if (st == KVQ_OK) st = check_rows(y, x->heads, width, &a.qo);
+  int32_t st = check_rows(x, n_tok, x->heads, width, &a.q);
+  if (st == KVQ_OK) st = check_rows(y, n_tok, x->heads, width, &a.qo);
   if (st == KVQ_OK) st = check_norm(norm, &a.qn);
   if (st == KVQ_OK) st = check_rope(rope, width, d_pos, pos_stride, n_tok, &a.rope);
   if (st != KVQ_OK) return st;
   if (!rows_distinct(y, n_tok, width)) return KVQ_ERR_INVALID_ARG;
-  if (x->data == y->data &&
-      (x->dtype != y->dtype || x->tok_stride != y->tok_stride || x->head_stride != y->head_stride))
-    return KVQ_ERR_INVALID_ARG;
+  if (!in_place_or_apart(a.q, a.qo)) return KVQ_ERR_INVALID_ARG;
   a.status = d_status;
   a.n_tok = n_tok;
   a.Hq = x->heads;
@@ -732,20 +737,18 @@ int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq
   if (!k || (!v && !fp8) || !d_slot_mapping || (q && q->heads < 1)) return KVQ_ERR_INVALID_ARG;
   if ((q && q->heads > kMaxHeads) || Hk > kMaxHeads || n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   NormRopeArgs a{};
-  st = check_rows(k, Hk, D, &a.k);
-  if (st == KVQ_OK && !fp8) st = check_rows(v, Hk, D, &a.v);
+  st = check_rows(k, n_tok, Hk, D, &a.k);
+  if (st == KVQ_OK && !fp8) st = check_rows(v, n_tok, Hk, D, &a.v);
   if (st == KVQ_OK) st = check_norm(k_norm, &a.kn);
   if (st == KVQ_OK) st = check_rope(rope, rope_width, d_pos, pos_stride, n_tok, &a.rope);
   if (q) {
-    if (st == KVQ_OK) st = check_rows(q, q->heads, D, &a.q);
-    if (st == KVQ_OK) st = check_rows(q_out, q->heads, D, &a.qo);
+    if (st == KVQ_OK) st = check_rows(q, n_tok, q->heads, D, &a.q);
+    if (st == KVQ_OK) st = check_rows(q_out, n_tok, q->heads, D, &a.qo);
     if (st == KVQ_OK) st = check_norm(q_norm, &a.qn);
     if (st != KVQ_OK) return st;
     if (rotate && q_out->dtype != KVQ_DT_F32) return KVQ_ERR_INVALID_ARG;
     if (!rows_distinct(q_out, n_tok, D)) return KVQ_ERR_INVALID_ARG;
-    if (q->data == q_out->data && (q->dtype != q_out->dtype || q->tok_stride != q_out->tok_stride ||
-                                   q->head_stride != q_out->head_stride))
-      return KVQ_ERR_INVALID_ARG;
+    if (!in_place_or_apart(a.q, a.qo)) return KVQ_ERR_INVALID_ARG;
   }
   if (st != KVQ_OK) return st;
   a.c = *cache;
@@ -774,11 +777,11 @@ static int32_t load_impl(const kvq_cache* cache, LoadArgs& a, int32_t rotate_bac
   if (a.n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   int32_t st = KVQ_OK;
   if (k) {
-    st = check_rows(k, cache->num_kv_heads, width, &a.k);
+    st = check_rows(k, a.n_tok, cache->num_kv_heads, width, &a.k);
     if (st == KVQ_OK && !rows_distinct(k, a.n_tok, width)) st = KVQ_ERR_INVALID_ARG;
   }
   if (st == KVQ_OK && v) {
-    st = check_rows(v, cache->num_kv_heads, width, &a.v);
+    st = check_rows(v, a.n_tok, cache->num_kv_heads, width, &a.v);
     if (st == KVQ_OK && !rows_distinct(v, a.n_tok, width)) st = KVQ_ERR_INVALID_ARG;
   }
   if (st != KVQ_OK) return st;

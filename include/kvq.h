@@ -426,8 +426,9 @@ int32_t kvq_decode_noalloc(const kvq_cache* cache, const float* q, int32_t num_s
  * quantised) in kernels of their own; here they are one pass with the store. */
 
 /* Activations [tokens][heads][width], the last dimension contiguous, the other
- * two with strides in elements: a slice of a fused projection, a head beside its
- * gate, or a plain contiguous tensor. */
+ * two with strides in elements (0 .. 2^31; that of one token, or one head, does not
+ * count): a slice of a fused projection, a head beside its gate, or a plain
+ * contiguous tensor. */
 typedef struct kvq_rows {
   void* data;          /* device; read or written, as the call says */
   int32_t dtype;       /* KVQ_DT_F32 or KVQ_DT_BF16 */

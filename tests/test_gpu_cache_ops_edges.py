@@ -1,5 +1,6 @@
 """The calls around the cache at values and layouts that the other tests leave out:
-keys and queries that are not numbers, a bad page inside a prompt chunk."""
+keys and queries that are not numbers, a bad page inside a prompt chunk,
+strides that no element uses."""
 import math
 
 import pytest
@@ -84,3 +85,40 @@ def test_rows_before_a_bad_page(K, fmt, T0, n, bad):
         assert K.read_status(status) == K.DEV_BAD_PAGE
         assert torch.isfinite(want).all() and torch.equal(got[:first], want[:first])
         assert torch.isnan(got[first:]).all()
+
+
+# ------------------------------------------------------------------ strides that no element uses
+
+def test_strides_of_single_elements_do_not_count(K):
+    """One token, or one head, with a stride that nothing is reached by: the rows of the
+    plain layout, in place as well."""
+    x = rnd((1, 4, 256), "single")
+    norm = K.Norm(rnd((256,), "single w"))
+    want = K.norm_rope(x, norm=norm)
+    for tok in (0, 1, 1024, 1025, 2 ** 33):
+        y = x.clone()
+        odd = torch.as_strided(y, (1, 4, 256), (tok, 256, 1))
+        assert torch.equal(K.norm_rope(odd, norm=norm), want)
+        K.norm_rope(odd, norm=norm, out=y)
+        assert torch.equal(y, want)
+    one = rnd((7, 1, 256), "single head")
+    want = K.norm_rope(one, norm=norm)
+    for head in (0, 1, 257, 2 ** 33):
+        y = one.clone()
+        odd = torch.as_strided(y, (7, 1, 256), (256, head, 1))
+        assert torch.equal(K.norm_rope(odd, norm=norm), want)
+        K.norm_rope(y, norm=norm, out=odd)
+        assert torch.equal(y, want)
+    cache = make_cache(K, K.FMT_Q4_HAD32, 1, 256, 2)
+    fill_random(cache, K, 1)
+    slots = torch.tensor([5], dtype=torch.int32, device=DEV)
+    k, v = K.load(cache, slots)
+    out = torch.zeros(1, 1, 256, dtype=torch.bfloat16, device=DEV)
+    odd = torch.as_strided(out, (1, 1, 256), (2 ** 34, 3, 1))
+    K.load(cache, slots, k=odd)
+    assert torch.equal(out, k)
+    again = make_cache(K, K.FMT_Q4_HAD32, 1, 256, 2)
+    plain = make_cache(K, K.FMT_Q4_HAD32, 1, 256, 2)
+    K.norm_rope_store(again, None, torch.as_strided(x, (1, 1, 256), (2 ** 34, 2 ** 35, 1)), x[:, :1], slots)
+    K.norm_rope_store(plain, None, x[:, :1], x[:, :1], slots)
+    assert torch.equal(again.k, plain.k) and torch.equal(again.v, plain.v)
