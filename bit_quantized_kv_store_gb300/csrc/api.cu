@@ -672,7 +672,7 @@ static int32_t check_rope(const kvq_rope* r, int32_t width, const int32_t* pos, 
       r->reserved != 0 || !r->table || reinterpret_cast<uintptr_t>(r->table) % 8 != 0)
     return KVQ_ERR_INVALID_ARG;
   if (r->rot_dim > 256 || (!r->interleaved && r->rot_dim % 16 != 0)) return KVQ_ERR_UNSUPPORTED;
-  if (!pos || reinterpret_cast<uintptr_t>(pos) % 4 != 0 || (r->num_axes > 1 && pos_stride < n_tok))
+  if (!pos || reinterpret_cast<uintptr_t>(pos) % 4 != 0 || (r->num_axes > 1 && pos_stride != 0 && pos_stride < n_tok))
     return KVQ_ERR_INVALID_ARG;
   *v = RopeView{r->table, pos, pos_stride, r->rot_dim, r->interleaved, r->num_axes};
   return KVQ_OK;

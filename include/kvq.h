@@ -472,8 +472,8 @@ int32_t kvq_rope_table(const double* inv_freq, const int32_t* axis, int32_t pair
  * y may be x itself (same data, dtype and strides); other overlaps of x and y
  * are not allowed.  width 64, 128, 256 or 512.  Arithmetic in fp32, rounded once
  * into y's type.
- *   d_pos: device int32 [num_axes][n_tok], axis a's at a * pos_stride (elements;
- *       may be NULL without rope).
+ *   d_pos: device int32 [num_axes][n_tok], axis a's at a * pos_stride (elements, 0:
+ *       every axis has the same; may be NULL without rope).
  *   d_status: optional; a table word whose axis is >= num_axes turns its pair to
  *       NaN and sets KVQ_DEV_BAD_INDEX. */
 int32_t kvq_norm_rope(const kvq_rows* x, const kvq_rows* y, int64_t n_tok, int32_t width, const kvq_norm* norm,

@@ -1,12 +1,12 @@
 """The calls around the cache at values and layouts that the other tests leave out:
 keys and queries that are not numbers, a bad page inside a prompt chunk,
-strides that no element uses."""
+strides that no element uses, positions that axes share."""
 import math
 
 import pytest
 import torch
 
-from tests.test_gpu_cache_ops import DEV, diff_problem, fill_random, make_cache, rnd
+from tests.test_gpu_cache_ops import DEV, diff_problem, fill_random, make_cache, rnd, rope_of
 from tests.test_gpu_parity import K  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -122,3 +122,14 @@ def test_strides_of_single_elements_do_not_count(K):
     K.norm_rope_store(again, None, torch.as_strided(x, (1, 1, 256), (2 ** 34, 2 ** 35, 1)), x[:, :1], slots)
     K.norm_rope_store(plain, None, x[:, :1], x[:, :1], slots)
     assert torch.equal(again.k, plain.k) and torch.equal(again.v, plain.v)
+
+
+def test_positions_that_all_axes_share(K):
+    """Text positions broadcast over three axes: those of three equal rows."""
+    n = 37
+    rope = rope_of(K, 64, 0, 3)[0]
+    x = rnd((n, 4, 128), "shared positions")
+    pos = torch.arange(100, 100 + n, dtype=torch.int32, device=DEV)
+    want = K.norm_rope(x, pos.repeat(3, 1), rope=rope)
+    assert torch.equal(K.norm_rope(x, pos.expand(3, n), rope=rope), want)
+    assert torch.equal(K.norm_rope(x[:1], pos[:1].expand(3, 1), rope=rope), want[:1])
