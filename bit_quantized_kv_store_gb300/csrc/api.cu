@@ -20,6 +20,11 @@ static int32_t cuda_fail(cudaError_t e) {
 
 int32_t record_cuda_failure(cudaError_t e) { return cuda_fail(e); }
 
+// Of metadata: int32 words on their own boundaries (NULL is).
+template <typename... P>
+static bool aligned4(const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3u) == 0;
+}
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The two 4-bit formats share planes, layout and kernels (Q4_0 without the rotation).
@@ -50,7 +55,7 @@ static int32_t check_cache(const kvq_cache* c) {
     if (c->rope_dim != 0) return KVQ_ERR_INVALID_ARG;
   } else {
     if (c->num_kv_heads != 1 || c->rope_dim <= 0 || c->rope_dim % 16 != 0) return KVQ_ERR_INVALID_ARG;
-    if (!c->k_scale || !c->v_scale) return KVQ_ERR_INVALID_ARG;
+    if (!c->k_scale || !c->v_scale || !aligned4(c->k_scale) || !aligned4(c->v_scale)) return KVQ_ERR_INVALID_ARG;
   }
   return KVQ_OK;
 }
@@ -702,7 +707,7 @@ int32_t kvq_norm_rope(const kvq_rows* x, const kvq_rows* y, int64_t n_tok, int32
   if (n_tok < 0 || width <= 0) return KVQ_ERR_INVALID_ARG;
   if (!norm_rope_width(width)) return KVQ_ERR_UNSUPPORTED;
   if (n_tok == 0) return KVQ_OK;
-  if (!x || !y || x->heads < 1) return KVQ_ERR_INVALID_ARG;
+  if (!x || !y || x->heads < 1 || !aligned4(d_status)) return KVQ_ERR_INVALID_ARG;
   if (x->heads > kMaxHeads || n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   NormRopeArgs a{};
   int32_t st = check_rows(x, n_tok, x->heads, width, &a.q);
@@ -734,7 +739,8 @@ int32_t kvq_norm_rope_store(const kvq_cache* cache, const kvq_rows* q, const kvq
   if (fp8 ? cache->head_dim != 512 || cache->rope_dim != 64 : !norm_rope_width(D)) return KVQ_ERR_UNSUPPORTED;
   if (fp8 && (v || q_norm)) return KVQ_ERR_INVALID_ARG;
   if (n_tok == 0) return KVQ_OK;
-  if (!k || (!v && !fp8) || !d_slot_mapping || (q && q->heads < 1)) return KVQ_ERR_INVALID_ARG;
+  if (!k || (!v && !fp8) || !d_slot_mapping || !aligned4(d_slot_mapping, d_status) || (q && q->heads < 1))
+    return KVQ_ERR_INVALID_ARG;
   if ((q && q->heads > kMaxHeads) || Hk > kMaxHeads || n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   NormRopeArgs a{};
   st = check_rows(k, n_tok, Hk, D, &a.k);
@@ -774,6 +780,7 @@ static int32_t load_impl(const kvq_cache* cache, LoadArgs& a, int32_t rotate_bac
   if (rotate_back && cache->format != KVQ_FMT_Q4_HAD32 && cache->format != KVQ_FMT_TQ4) return KVQ_ERR_INVALID_ARG;
   if (a.n_tok < 0 || (fp8 && v) || (!k && !v)) return KVQ_ERR_INVALID_ARG;
   if (a.n_tok == 0) return KVQ_OK;
+  if (!aligned4(a.slots, a.block_tables, a.starts, a.cu_lens, a.status)) return KVQ_ERR_INVALID_ARG;
   if (a.n_tok >= (int64_t(1) << 31)) return KVQ_ERR_UNSUPPORTED;
   int32_t st = KVQ_OK;
   if (k) {
@@ -849,7 +856,7 @@ int32_t kvq_merge_diff(const kvq_cache* cache, const void* workspace, size_t ws_
     return KVQ_ERR_UNSUPPORTED;
   if (rotate_back && cache->format != KVQ_FMT_Q4_HAD32 && cache->format != KVQ_FMT_TQ4) return KVQ_ERR_INVALID_ARG;
   if (num_seqs == 0) return KVQ_OK;
-  if (!workspace || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || !aligned4(d_seq_lens)) return KVQ_ERR_INVALID_ARG;
   DiffView d;
   st = check_diff(d_lambda, lambda_stride, num_seqs, num_q_heads / 2, norm, out_scale, out, out_dtype, &d);
   if (st != KVQ_OK) return st;
@@ -912,7 +919,8 @@ int32_t kvq_prefill_diff(const kvq_cache* cache, const void* q, int32_t dtype, i
   if (n_q == 0) return KVQ_OK;
   if (!q || reinterpret_cast<uintptr_t>(q) % (dtype == KVQ_DT_F32 ? 4 : 2) != 0 || !d_block_table || max_pages < 1)
     return KVQ_ERR_INVALID_ARG;
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 32 != 0) return KVQ_ERR_INVALID_ARG;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 32 != 0 || !aligned4(d_block_table, d_status))
+    return KVQ_ERR_INVALID_ARG;
   if (static_cast<int64_t>(q_start) + n_q > static_cast<int64_t>(max_pages) * cache->page_size)
     return KVQ_ERR_INVALID_ARG;
   DiffView d;

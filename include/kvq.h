@@ -423,7 +423,8 @@ int32_t kvq_decode_noalloc(const kvq_cache* cache, const float* q, int32_t num_s
  * What a model does to its queries, keys and values just before the cache (norms
  * per head, rotary positions), and the rows read back out of it.  The pages'
  * producers do the first ([P3] KV8 base commit: the fresh normed and roped row is
- * quantised) in kernels of their own; here they are one pass with the store. */
+ * quantised) in kernels of their own; here they are one pass with the store.
+ * Metadata (slots, positions, tables, lengths, status words) off its 4 bytes is refused. */
 
 /* Activations [tokens][heads][width], the last dimension contiguous, the other
  * two with strides in elements (0 .. 2^31; that of one token, or one head, does not
