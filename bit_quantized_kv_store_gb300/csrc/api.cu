@@ -692,9 +692,15 @@ int32_t kvq_rope_table(const double* inv_freq, const int32_t* axis, int32_t pair
   for (int32_t i = 0; i < pairs; ++i)
     if (!(fabs(inv_freq[i]) < INFINITY) || (axis && (axis[i] < 0 || axis[i] > 3))) return KVQ_ERR_INVALID_ARG;
   for (int32_t i = 0; i < pairs; ++i) {
-    const double t = fmod(fabs(inv_freq[i]) * 0.15915494309189534561, 1.0);  // turns: radians / (2 pi)
+    // turns = radians / (2 pi) as a double and what it leaves, 1 / (2 pi) itself in two
+    // doubles: a double alone is off by 2^-56 of a turn for a radian a step, 2^-25 at
+    // position 2^31
+    const double f = fabs(inv_freq[i]), turns = f * 0.15915494309189535;
+    const double left = fma(f, -9.839338337591243e-18, fma(f, 0.15915494309189535, -turns));
     // units of 2^-62 of a turn, modulo a turn (the shift drops what is above it)
-    uint64_t q = static_cast<uint64_t>(rint(t * 4611686018427387904.0));
+    const double unit = 4611686018427387904.0, t = fmod(turns, 1.0) * unit, whole = rint(t);
+    uint64_t q = static_cast<uint64_t>(whole) +
+                 static_cast<uint64_t>(static_cast<int64_t>(rint((t - whole) + fmod(left, 1.0) * unit)));
     if (inv_freq[i] < 0) q = 0 - q;
     table[i] = (q << 2) | static_cast<uint64_t>(axis ? axis[i] : 0);
   }

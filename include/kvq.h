@@ -464,8 +464,8 @@ typedef struct kvq_rope {
 
 /* kvq_rope_table -- words of a kvq_rope's table (host memory) from the pairs'
  * angles per position step, inv_freq [pairs] in radians (finite), and their axes
- * (NULL: all 0; each 0 .. 3).  Turns are rounded to 2^-62 of a turn from the
- * doubles given. */
+ * (NULL: all 0; each 0 .. 3).  Turns are within 2^-62 of a turn of the
+ * doubles given (below 2^40 radians). */
 int32_t kvq_rope_table(const double* inv_freq, const int32_t* axis, int32_t pairs, uint64_t* table);
 
 /* kvq_norm_rope -- norm and rotary positions of `n_tok` tokens' rows in one pass
