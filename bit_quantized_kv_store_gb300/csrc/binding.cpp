@@ -15,10 +15,11 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <exception>
 #include <sstream>
-#include <stdexcept>
 #include <string>
 
 #include "../../include/kvq.h"
@@ -465,7 +466,8 @@ PyObject* init(PyObject* const* a) {
   return back(Py_None);
 }
 
-// A function of N positional arguments; every C++ exception becomes a Python one.
+// A function of N positional arguments; every C++ exception becomes a Python one, torch's
+// their own (a failed allocation: torch.OutOfMemoryError).
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
@@ -475,8 +477,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
     return F(args);
   } catch (const Refused&) {
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception&) {
+    torch::translate_exception_to_python(std::current_exception());
   } catch (...) {
     PyErr_SetString(PyExc_RuntimeError, "kvq: unknown error");
   }

@@ -1,6 +1,6 @@
 """The calls around the cache at values and layouts that the other tests leave out:
 keys and queries that are not numbers, a bad page inside a prompt chunk,
-strides that no element uses, positions that axes share."""
+strides that no element uses, positions that axes share, outputs that do not fit."""
 import math
 
 import pytest
@@ -133,3 +133,15 @@ def test_positions_that_all_axes_share(K):
     want = K.norm_rope(x, pos.repeat(3, 1), rope=rope)
     assert torch.equal(K.norm_rope(x, pos.expand(3, n), rope=rope), want)
     assert torch.equal(K.norm_rope(x[:1], pos[:1].expand(3, 1), rope=rope), want[:1])
+
+
+def test_an_output_that_does_not_fit(K):
+    """As an allocation of torch's own: the caller can tell it from other errors."""
+    x = torch.zeros(1, 1, 512, device=DEV).expand(2 ** 30, 1, 512)       # 2 TB of output
+    with pytest.raises(torch.OutOfMemoryError):
+        K.norm_rope(x)
+    c = make_cache(K, K.FMT_Q4_HAD32, 4, 256, 2)
+    bt, cu = torch.zeros(1, 2, dtype=torch.int32, device=DEV), torch.zeros(2, dtype=torch.int32, device=DEV)
+    with pytest.raises(torch.OutOfMemoryError):
+        K.load_seqs(c, bt, cu, 2 ** 31 - 1)                              # 4 TB
+    assert torch.equal(K.norm_rope(x[:3]), x[:3])
