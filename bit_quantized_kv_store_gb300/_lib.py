@@ -437,12 +437,20 @@ def calls():
 
 class Norm:
     """Root-mean-square norm of a head's row: x / sqrt(mean(x^2) + eps) * (weight +
-    offset).  weight: [width] fp32 or bf16 on the device (kept, not copied)."""
+    offset).  weight: [width] fp32 or bf16 on the device, kept, not copied: a call reads
+    the tensor as it is then, also after its storage was replaced or its type changed."""
 
     def __init__(self, weight, eps=1e-6, offset=0.0):
-        self.weight, self.eps, self.offset, self.width = weight, eps, offset, weight.numel()
-        self.desc = NormDesc(_ptr(weight), _dtype_code(weight), eps, offset)
-        self.handle = (ctypes.addressof(self.desc), self.width, weight.get_device())
+        _ptr(weight), _dtype_code(weight)
+        self.weight, self.eps, self.offset = weight, eps, offset
+
+    @property
+    def width(self):
+        return self.weight.numel()
+
+    @property
+    def handle(self):
+        return self.weight, self.eps, self.offset
 
 
 class Rope:
@@ -450,7 +458,7 @@ class Rope:
     turned by position * inv_freq[i] radians.  inv_freq: floats (theta ** (-2 i /
     rot_dim), or a model's scaled ones).  axes: the position axis of every pair
     (default 0: one axis).  interleaved: pairs (2i, 2i + 1) instead of
-    (i, i + rot_dim / 2)."""
+    (i, i + rot_dim / 2).  The table is the rope's own, made once."""
 
     def __init__(self, inv_freq, axes=None, interleaved=False, device="cuda"):
         n = len(inv_freq)

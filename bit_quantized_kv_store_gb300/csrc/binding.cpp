@@ -150,7 +150,7 @@ int32_t integer32(PyObject* o, const char* what) {
   return static_cast<int32_t>(v);
 }
 
-// A handle of the Python side: (address of its C structure, its width or axes, its device).
+// A handle of the Python side: (address of its C structure, its axes, its device).
 struct Handle {
   const void* at;
   long long n, dev;
@@ -161,12 +161,34 @@ Handle handle(PyObject* o, const char* what) {
                 integer(PyTuple_GET_ITEM(o, 2), what)};
 }
 
-const kvq_norm* norm_of(PyObject* o, const char* what, int dev, int64_t width) {
-  if (!given(o)) return nullptr;
-  const Handle h = handle(o, what);
-  if (h.n != width) refuse(PyExc_ValueError, what, " is for rows of ", h.n, ", not ", width);
-  if (h.dev != dev) refuse(PyExc_ValueError, what, " is on cuda:", h.dev, ", the current device is cuda:", dev);
-  return static_cast<const kvq_norm*>(h.at);
+float real(PyObject* o, const char* what) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(PyExc_TypeError, what, " must be a number");
+  }
+  return static_cast<float>(v);
+}
+
+// A norm of the Python side, (weight, eps, offset): the weight's address is read in every
+// call, since its storage may have been replaced since the last one.
+struct Normed {
+  kvq_norm norm{};
+  bool is_given = false;
+  const kvq_norm* get() const { return is_given ? &norm : nullptr; }
+};
+Normed norm_of(PyObject* o, const char* what, int dev, int64_t width) {
+  Normed r;
+  if (!given(o)) return r;
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 3) refuse(PyExc_TypeError, "bad ", what);
+  const at::Tensor& w = tensor(PyTuple_GET_ITEM(o, 0), "a norm's weight");
+  if (w.numel() != width) refuse(PyExc_ValueError, what, " is for rows of ", w.numel(), ", not ", width);
+  on_device(w, what, dev);
+  if (!w.is_contiguous()) refuse(PyExc_ValueError, "the weight of ", what, " must be contiguous");
+  r.norm = kvq_norm{w.data_ptr(), code_of(w.scalar_type(), what), real(PyTuple_GET_ITEM(o, 1), "eps"),
+                    real(PyTuple_GET_ITEM(o, 2), "offset")};
+  r.is_given = true;
+  return r;
 }
 
 // The rope and its positions, int32 [n] (one axis) or [axes, n].
@@ -230,7 +252,7 @@ PyObject* norm_rope(PyObject* const* a) {
   else y = fresh(n, heads, width, scalar_type(a[5], x.scalar_type()), dev);
   const kvq_rows ry = rows(y, "out", dev, n, heads, width);
   const Turned r = rope_of(a[2], a[1], dev, n);
-  checked(p_norm_rope(&rx, &ry, n, static_cast<int32_t>(width), norm_of(a[3], "norm", dev, width), r.rope, r.pos,
+  checked(p_norm_rope(&rx, &ry, n, static_cast<int32_t>(width), norm_of(a[3], "norm", dev, width).get(), r.rope, r.pos,
                       r.stride, status_of(a[6], dev), stream_of(dev)),
           "kvq_norm_rope");
   return given(a[4]) ? back(a[4]) : THPVariable_Wrap(y);
@@ -263,7 +285,8 @@ PyObject* norm_rope_store(PyObject* const* a) {
   }
   const Turned r = rope_of(a[6], a[5], dev, n);
   checked(p_norm_rope_store(c, with_q ? &rq : nullptr, &rk, fp8 ? nullptr : &rv, n,
-                            norm_of(a[7], "q_norm", dev, c->head_dim), norm_of(a[8], "k_norm", dev, c->head_dim), r.rope, r.pos, r.stride,
+                            norm_of(a[7], "q_norm", dev, c->head_dim).get(),
+                            norm_of(a[8], "k_norm", dev, c->head_dim).get(), r.rope, r.pos, r.stride,
                             ints(tensor(a[4], "slot_mapping"), "slot_mapping", dev, {n}), with_q ? &ro : nullptr,
                             integer32(a[10], "rotate"), status_of(a[11], dev), stream_of(dev)),
           "kvq_norm_rope_store");
@@ -364,15 +387,6 @@ at::Tensor diff_out(PyObject* o, PyObject* dtype, int dev, int64_t n, int64_t he
   return t;
 }
 
-float real(PyObject* o, const char* what) {
-  const double v = PyFloat_AsDouble(o);
-  if (v == -1.0 && PyErr_Occurred()) {
-    PyErr_Clear();
-    refuse(PyExc_TypeError, what, " must be a number");
-  }
-  return static_cast<float>(v);
-}
-
 // merge_diff(cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq_len, lam, norm, out_scale, out, dtype, n_sel,
 //            rotate_back)
 PyObject* merge_diff(PyObject* const* a) {
@@ -388,7 +402,7 @@ PyObject* merge_diff(PyObject* const* a) {
   const float* lam = lambda_of(a[6], dev, B, Hq / 2, stride);
   checked(p_merge_diff(c, ws.data_ptr(), static_cast<size_t>(ws.numel()) * ws.element_size(), B, Hq,
                        ints(lens, "seq_lens", dev, {B}), integer32(a[5], "max_seq_len"), integer32(a[11], "n_sel"),
-                       rotates(c, a[12]), lam, stride, norm_of(a[7], "norm", dev, c->head_dim),
+                       rotates(c, a[12]), lam, stride, norm_of(a[7], "norm", dev, c->head_dim).get(),
                        real(a[8], "out_scale"), out.data_ptr(), code_of(out.scalar_type(), "out"), stream_of(dev)),
           "kvq_merge_diff");
   return given(a[9]) ? back(a[9]) : THPVariable_Wrap(out);
@@ -407,7 +421,7 @@ PyObject* diff_heads(PyObject* const* a) {
   int64_t stride;
   const float* lam = lambda_of(a[1], dev, n, Hq / 2, stride);
   checked(p_diff_heads(static_cast<const float*>(x.data_ptr()), n, static_cast<int32_t>(Hq),
-                       static_cast<int32_t>(width), lam, stride, norm_of(a[2], "norm", dev, width),
+                       static_cast<int32_t>(width), lam, stride, norm_of(a[2], "norm", dev, width).get(),
                        real(a[3], "out_scale"), out.data_ptr(), code_of(out.scalar_type(), "out"), stream_of(dev)),
           "kvq_diff_heads");
   return given(a[4]) ? back(a[4]) : THPVariable_Wrap(out);
@@ -443,7 +457,7 @@ PyObject* prefill_diff(PyObject* const* a) {
   }
   checked(p_prefill_diff(c, q.data_ptr(), qt, static_cast<int32_t>(n), static_cast<int32_t>(Hq), q_start,
                          static_cast<const int32_t*>(bt.data_ptr()), static_cast<int32_t>(bt.numel()),
-                         real(a[4], "sm_scale"), lam, stride, norm_of(a[6], "norm", dev, c->head_dim),
+                         real(a[4], "sm_scale"), lam, stride, norm_of(a[6], "norm", dev, c->head_dim).get(),
                          real(a[7], "out_scale"), ws.data_ptr(), static_cast<size_t>(ws.numel()) * ws.element_size(),
                          out.data_ptr(), code_of(out.scalar_type(), "out"), status_of(a[11], dev), stream_of(dev)),
           "kvq_prefill_diff");

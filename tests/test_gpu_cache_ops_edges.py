@@ -145,3 +145,40 @@ def test_an_output_that_does_not_fit(K):
     with pytest.raises(torch.OutOfMemoryError):
         K.load_seqs(c, bt, cu, 2 ** 31 - 1)                              # 4 TB
     assert torch.equal(K.norm_rope(x[:3]), x[:3])
+
+
+# ------------------------------------------------------------------ a norm's weight
+
+def test_a_norm_follows_its_weight(K):
+    """A parameter whose storage, type or place changes after the Norm was made: calls
+    take it as it is, or refuse it."""
+    x = rnd((3, 2, 256), "follow")
+    new = [rnd((256,), "follow w", i) for i in range(3)]
+    param = torch.nn.Parameter(new[0].clone(), requires_grad=False)
+    norm = K.Norm(param, 1e-6, 1.0)
+    c = make_cache(K, K.FMT_Q4_HAD32, 2, 256, 2)
+    slots = torch.arange(3, dtype=torch.int32, device=DEV)
+
+    def check(w):
+        for got, want in ((K.norm_rope(x, norm=norm), K.norm_rope(x, norm=K.Norm(w, 1e-6, 1.0))),
+                          (K.diff_heads(x, torch.ones(1, device=DEV), norm=norm),
+                           K.diff_heads(x, torch.ones(1, device=DEV), norm=K.Norm(w, 1e-6, 1.0))),
+                          (K.norm_rope_store(c, x, x, x, slots, q_norm=norm),
+                           K.norm_rope_store(c, x, x, x, slots, q_norm=K.Norm(w, 1e-6, 1.0)))):
+            assert torch.equal(got, want)
+
+    check(new[0])
+    param.data = new[1].clone()
+    check(new[1])
+    param.data = new[2].bfloat16()
+    check(new[2].bfloat16())
+    norm.weight = new[0]
+    check(new[0])
+    norm.weight = param
+    for bad in (torch.ones(128, device=DEV), torch.ones(512, device=DEV)[::2], torch.ones(256)):
+        param.data = bad
+        with pytest.raises(ValueError):
+            K.norm_rope(x, norm=norm)
+    param.data = torch.ones(256, device=DEV, dtype=torch.float16)
+    with pytest.raises(TypeError):
+        K.norm_rope(x, norm=norm)
