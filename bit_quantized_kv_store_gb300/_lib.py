@@ -212,21 +212,20 @@ class Cache:
         self.refresh()
 
     def refresh(self):
-        for t in (self.k, self.v, self.k_scale, self.v_scale, self.signs):
-            if t is not None and not (t.is_cuda and t.is_contiguous()):
-                raise ValueError("kvq: cache planes must be contiguous CUDA tensors")
+        planes = [t for t in (self.k, self.v, self.k_scale, self.v_scale, self.signs) if t is not None]
+        if not all(t.is_cuda and t.is_contiguous() for t in planes):
+            raise ValueError("kvq: cache planes must be contiguous CUDA tensors")
+        if len({t.get_device() for t in planes}) != 1:
+            raise ValueError("kvq: cache planes must be on one device")
         self.desc = CacheDesc(self.fmt, self.Hk, self.D, self.rope, self.page_size, self.num_pages,
                               self.k.data_ptr(), 0 if self.k_scale is None else self.k_scale.data_ptr(),
                               self.v.data_ptr(), 0 if self.v_scale is None else self.v_scale.data_ptr(),
                               0 if self.signs is None else self.signs.data_ptr())
+        self.handle = (ctypes.addressof(self.desc), self.k.get_device())
 
     @property
     def ref(self):
         return ctypes.byref(self.desc)
-
-    @property
-    def address(self):
-        return ctypes.addressof(self.desc)
 
     def nbytes(self):
         return sum(t.numel() * t.element_size() for t in (self.k, self.v, self.k_scale, self.v_scale) if t is not None)
@@ -502,7 +501,7 @@ def norm_rope_store(cache: Cache, q, k, v, slot_mapping, positions=None, rope=No
     if stream is not None:
         with torch.cuda.stream(stream):
             return norm_rope_store(cache, q, k, v, slot_mapping, positions, rope, q_norm, k_norm, q_out, rotate, status)
-    return (_calls or calls()).norm_rope_store(cache.address, q, k, v, slot_mapping, positions, _handle(rope),
+    return (_calls or calls()).norm_rope_store(cache.handle, q, k, v, slot_mapping, positions, _handle(rope),
                                                _handle(q_norm), _handle(k_norm), q_out, rotate, status)
 
 
@@ -513,7 +512,7 @@ def load(cache: Cache, slots, k=None, v=None, dtype=torch.bfloat16, rotate_back=
     if stream is not None:
         with torch.cuda.stream(stream):
             return load(cache, slots, k, v, dtype, rotate_back, status)
-    return (_calls or calls()).load(cache.address, slots, k, v, dtype, rotate_back, status)
+    return (_calls or calls()).load(cache.handle, slots, k, v, dtype, rotate_back, status)
 
 
 def load_seqs(cache: Cache, block_tables, cu_lens, n_tok, starts=None, k=None, v=None, dtype=torch.bfloat16,
@@ -525,7 +524,7 @@ def load_seqs(cache: Cache, block_tables, cu_lens, n_tok, starts=None, k=None, v
     if stream is not None:
         with torch.cuda.stream(stream):
             return load_seqs(cache, block_tables, cu_lens, n_tok, starts, k, v, dtype, rotate_back, status)
-    return (_calls or calls()).load_seqs(cache.address, block_tables, cu_lens, n_tok, starts, k, v, dtype, rotate_back,
+    return (_calls or calls()).load_seqs(cache.handle, block_tables, cu_lens, n_tok, starts, k, v, dtype, rotate_back,
                                          status)
 
 
@@ -539,7 +538,7 @@ def merge_diff(cache: Cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq
         with torch.cuda.stream(stream):
             return merge_diff(cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq_len, lam, norm, out_scale, out,
                               dtype, n_sel, rotate_back)
-    return (_calls or calls()).merge_diff(cache.address, workspace, num_seqs, num_q_heads, seq_lens, max_seq_len, lam,
+    return (_calls or calls()).merge_diff(cache.handle, workspace, num_seqs, num_q_heads, seq_lens, max_seq_len, lam,
                                           _handle(norm), out_scale, out, dtype, n_sel, rotate_back)
 
 
@@ -580,7 +579,7 @@ def prefill_diff(cache: Cache, q, q_start, block_table, sm_scale, lam, norm=None
         with torch.cuda.stream(stream):
             return prefill_diff(cache, q, q_start, block_table, sm_scale, lam, norm, out_scale, out, dtype, workspace,
                                 status)
-    return (_calls or calls()).prefill_diff(cache.address, q, q_start, block_table, sm_scale, lam, _handle(norm),
+    return (_calls or calls()).prefill_diff(cache.handle, q, q_start, block_table, sm_scale, lam, _handle(norm),
                                             out_scale, out, dtype, workspace, status)
 
 

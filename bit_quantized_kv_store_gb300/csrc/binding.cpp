@@ -216,9 +216,13 @@ Turned rope_of(PyObject* o, PyObject* positions, int dev, int64_t n) {
   return r;
 }
 
-const kvq_cache* cache_of(PyObject* o) {
-  const void* p = PyLong_AsVoidPtr(o);
+// A cache of the Python side, (address of its C structure, its planes' device).
+const kvq_cache* cache_of(PyObject* o, int dev) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) refuse(PyExc_TypeError, "bad cache");
+  const void* p = PyLong_AsVoidPtr(PyTuple_GET_ITEM(o, 0));
   if (!p) refuse(PyExc_TypeError, "bad cache");
+  const long long d = integer(PyTuple_GET_ITEM(o, 1), "a cache's device");
+  if (d != dev) refuse(PyExc_ValueError, "the cache is on cuda:", d, ", the current device is cuda:", dev);
   return static_cast<const kvq_cache*>(p);
 }
 
@@ -260,11 +264,11 @@ PyObject* norm_rope(PyObject* const* a) {
 
 // norm_rope_store(cache, q, k, v, slots, positions, rope, q_norm, k_norm, q_out, rotate, status)
 PyObject* norm_rope_store(PyObject* const* a) {
-  const kvq_cache* c = cache_of(a[0]);
-  const bool fp8 = c->format == KVQ_FMT_FP8_ROW;  // one tensor of latent and rope parts, no v
   const at::Tensor& k = tensor(a[2], "k");
   three(k, "k");
   const int dev = device_of(k);
+  const kvq_cache* c = cache_of(a[0], dev);
+  const bool fp8 = c->format == KVQ_FMT_FP8_ROW;  // one tensor of latent and rope parts, no v
   const int64_t n = k.size(0), Hk = c->num_kv_heads, D = c->head_dim + (fp8 ? c->rope_dim : 0);
   const kvq_rows rk = rows(k, "k", dev, n, Hk, D);
   if (fp8 && given(a[3])) refuse(PyExc_ValueError, "fp8 latent rows take no v");
@@ -331,9 +335,9 @@ int32_t rotates(const kvq_cache* c, PyObject* o) {
 
 // load(cache, slots, k, v, dtype, rotate_back, status)
 PyObject* load(PyObject* const* a) {
-  const kvq_cache* c = cache_of(a[0]);
   const at::Tensor& slots = tensor(a[1], "slots");
   const int dev = device_of(slots);
+  const kvq_cache* c = cache_of(a[0], dev);
   if (slots.dim() != 1) refuse(PyExc_ValueError, "slots must be [tokens], got ", shape_of(slots.sizes()));
   const int64_t n = slots.size(0);
   const int32_t* at = ints(slots, "slots", dev, {n});
@@ -346,9 +350,9 @@ PyObject* load(PyObject* const* a) {
 
 // load_seqs(cache, block_tables, cu_lens, n_tok, starts, k, v, dtype, rotate_back, status)
 PyObject* load_seqs(PyObject* const* a) {
-  const kvq_cache* c = cache_of(a[0]);
   const at::Tensor &bt = tensor(a[1], "block_tables"), &cu = tensor(a[2], "cu_lens");
   const int dev = device_of(cu);
+  const kvq_cache* c = cache_of(a[0], dev);
   if (cu.dim() != 1 || cu.size(0) < 1)
     refuse(PyExc_ValueError, "cu_lens must be [sequences + 1], got ", shape_of(cu.sizes()));
   if (bt.dim() != 2) refuse(PyExc_ValueError, "block_tables must be [sequences, pages], got ", shape_of(bt.sizes()));
@@ -390,9 +394,9 @@ at::Tensor diff_out(PyObject* o, PyObject* dtype, int dev, int64_t n, int64_t he
 // merge_diff(cache, workspace, num_seqs, num_q_heads, seq_lens, max_seq_len, lam, norm, out_scale, out, dtype, n_sel,
 //            rotate_back)
 PyObject* merge_diff(PyObject* const* a) {
-  const kvq_cache* c = cache_of(a[0]);
   const at::Tensor &ws = tensor(a[1], "workspace"), &lens = tensor(a[4], "seq_lens");
   const int dev = device_of(lens);
+  const kvq_cache* c = cache_of(a[0], dev);
   on_device(ws, "workspace", dev);
   if (!ws.is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
   const int32_t B = integer32(a[2], "num_seqs"), Hq = integer32(a[3], "num_q_heads");
@@ -429,10 +433,10 @@ PyObject* diff_heads(PyObject* const* a) {
 
 // prefill_diff(cache, q, q_start, block_table, sm_scale, lam, norm, out_scale, out, dtype, workspace, status)
 PyObject* prefill_diff(PyObject* const* a) {
-  const kvq_cache* c = cache_of(a[0]);
   const at::Tensor &q = tensor(a[1], "q"), &bt = tensor(a[3], "block_table");
   three(q, "q");
   const int dev = device_of(q);
+  const kvq_cache* c = cache_of(a[0], dev);
   const int32_t qt = code_of(q.scalar_type(), "q");
   if (!q.is_contiguous()) refuse(PyExc_ValueError, "q must be contiguous");
   const int64_t n = q.size(0), Hq = q.size(1);

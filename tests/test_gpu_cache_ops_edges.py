@@ -182,3 +182,25 @@ def test_a_norm_follows_its_weight(K):
     param.data = torch.ones(256, device=DEV, dtype=torch.float16)
     with pytest.raises(TypeError):
         K.norm_rope(x, norm=norm)
+
+
+def test_a_cache_on_another_device_is_refused(K):
+    """Every call compares the cache's device with its tensors' (here the handle names a
+    device that the planes are not on)."""
+    c = make_cache(K, K.FMT_Q4_HAD32, 2, 256, 4)
+    x, q = rnd((3, 2, 256), "dev"), rnd((1, 4, 256), "dev q")
+    slots = torch.arange(3, dtype=torch.int32, device=DEV)
+    bt, cu = torch.arange(4, dtype=torch.int32, device=DEV)[None], torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    ws, lens, lam = K.alloc_workspace(c, 1, 4, 64), torch.tensor([3], dtype=torch.int32, device=DEV), torch.ones(2, device=DEV)
+    calls = (lambda: K.norm_rope_store(c, x, x, x, slots), lambda: K.load(c, slots), lambda: K.load_seqs(c, bt, cu, 3),
+             lambda: K.merge_diff(c, ws, 1, 4, lens, 64, lam), lambda: K.prefill_diff(c, q, 2, bt, 1 / 16, lam))
+    K.decode_diff(c, q, lens, bt, 64, 1 / 16, ws, lam)
+    for call in calls:
+        call()
+    c.handle = (c.handle[0], 1)
+    for call in calls:
+        with pytest.raises(ValueError, match="cache is on cuda:1"):
+            call()
+    c.refresh()
+    for call in calls:
+        call()
