@@ -2,8 +2,9 @@
 
 Each translation unit is compiled by nvcc in parallel, then linked into
 ``bit_quantized_kv_store_gb300/_build/libkvq.so``; the compiled part of the Python
-binding becomes ``_kvq_calls.so`` beside it.  A unit is rebuilt only when
-its source or a header is newer than its object file.
+binding becomes ``_kvq_calls.so`` beside it, where there is a torch to bind to.  A
+unit is rebuilt only when its source or a header is newer than its object file, the
+binding also for another interpreter or torch.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import concurrent.futures as cf
 import glob
 import os
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -23,6 +25,7 @@ SANITIZE = os.environ.get("KVQ_SANITIZE") == "1"
 BUILD = os.path.join(PKG, "_build_san" if SANITIZE else "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
 CALLS = os.path.join(BUILD, "_kvq_calls.so")  # csrc/binding.cpp
+CALLS_STAMP = CALLS + ".for"
 
 ARCH = ["-gencode", "arch=compute_103a,code=compute_103a" if SANITIZE else "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", f"-I{os.path.join(ROOT, 'include')}"]
@@ -71,14 +74,26 @@ def _compile(src, verbose_ptxas=False):
     return obj, r.stderr
 
 
+def _made_for(torch):
+    """What the compiled part of the binding was made for: an interpreter and a torch."""
+    return f"{sys.version}\n{sysconfig.get_config_var('SOABI')}\n{torch.__version__} {torch.__file__}\n"
+
+
 def _build_calls():
-    """The compiled part of the Python binding, against the installed torch."""
-    import torch
+    """The compiled part of the Python binding, against the installed torch.  Without
+    torch there is no binding to build: the library serves programs of the C ABI alone."""
+    try:
+        import torch
+    except ImportError:
+        return
     src, header = os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "kvq.h")
     tdir = os.path.dirname(os.path.abspath(torch.__file__))
-    newest = max(os.path.getmtime(f) for f in (src, header, os.path.join(tdir, "version.py")))
-    if os.path.exists(CALLS) and os.path.getmtime(CALLS) >= newest:
-        return
+    made_for = _made_for(torch)
+    if os.path.exists(CALLS) and os.path.exists(CALLS_STAMP):
+        with open(CALLS_STAMP) as f:
+            same = f.read() == made_for
+        if same and os.path.getmtime(CALLS) >= max(os.path.getmtime(p) for p in (src, header)):
+            return
     cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-o", tmp, src,
@@ -88,7 +103,12 @@ def _build_calls():
     r = subprocess.run(cmd, capture_output=True, text=True, env=_tool_env())
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(CALLS_STAMP):
+        os.remove(CALLS_STAMP)  # (never the new module's stamp beside the old module)
     os.replace(tmp, CALLS)
+    with open(tmp, "w") as f:
+        f.write(made_for)
+    os.replace(tmp, CALLS_STAMP)
 
 
 def build(verbose_ptxas=False) -> str:
@@ -97,7 +117,6 @@ def build(verbose_ptxas=False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         calls = ex.submit(_build_calls)
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        calls.result()
     objs = [o for o, _ in results]
     if verbose_ptxas:
         for _, log in results:
@@ -110,9 +129,9 @@ def build(verbose_ptxas=False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    calls.result()  # (its failure is raised with the library in place)
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(verbose_ptxas="-v" in sys.argv))
