@@ -1,5 +1,5 @@
 """The calls around the cache at values and layouts that the other tests leave out:
-keys and queries that are not numbers, a bad page inside a prompt chunk,
+keys, queries and rows that are not numbers, a bad page inside a prompt chunk,
 strides that no element uses, positions that axes share, outputs that do not fit."""
 import math
 
@@ -85,6 +85,94 @@ def test_rows_before_a_bad_page(K, fmt, T0, n, bad):
         assert K.read_status(status) == K.DEV_BAD_PAGE
         assert torch.isfinite(want).all() and torch.equal(got[:first], want[:first])
         assert torch.isnan(got[first:]).all()
+
+
+# ------------------------------------------------------------------ rows that are not numbers, on the way in and back
+
+BAD = {"nan": math.nan, "inf": math.inf, "-inf": -math.inf, "huge": 3e38}
+
+
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "Q4_0", "TQ4", "BF16", "FP8_ROW"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", sorted(BAD))
+def test_store_of_values_that_are_not_numbers(K, fmt, dtype, kind):
+    """norm_rope_store's bytes are kvq_store's for rows with NaN, infinities and values
+    whose sums overflow, with and without norm and rotation; rows without them are untouched by
+    their neighbours; read back, NaN stays in its group (row, part)."""
+    f = getattr(K, "FMT_" + fmt)
+    fp8 = f == K.FMT_FP8_ROW
+    n, Hk, D, W = 9, 1 if fp8 else 3, 512 if fp8 else 256, 576 if fp8 else 256
+    k, v, q = rnd((n, Hk, W), "bv k"), rnd((n, Hk, W), "bv v"), rnd((n, 6, W), "bv q")
+    clean = k.clone(), v.clone()
+    for x in (k, v, q):
+        x[2, 0, 5] = BAD[kind]
+        x[4, -1, 40], x[4, -1, 41] = BAD[kind], -BAD[kind]
+        x[6, 0, 520 if fp8 else 255] = BAD[kind]
+    k, v, q = (x.to(dtype) for x in (k, v, q))
+    slots = torch.arange(n, dtype=torch.int32, device=DEV)
+    rope = rope_of(K, 64, 0, 1)[0]
+    pos = torch.arange(n, dtype=torch.int32, device=DEV) * 7
+    for norm, rp in ((None, None), (K.Norm(rnd((D,), "bv w"), 1e-6), rope)):
+        a, b = make_cache(K, f, Hk, D, 2), make_cache(K, f, Hk, D, 2)
+        got = K.norm_rope_store(a, q, k, None if fp8 else v, slots, pos if rp else None, rope=rp,
+                                q_norm=None if fp8 else norm, k_norm=norm)
+        if fp8:
+            k32, q32 = torch.empty(n, Hk, W, device=DEV), q.float().clone()
+            K.norm_rope(k[..., :512], norm=norm, out=k32[..., :512])
+            K.norm_rope(k[..., 512:], pos if rp else None, rope=rp, out=k32[..., 512:])
+            K.norm_rope(q[..., 512:], pos if rp else None, rope=rp, out=q32[..., 512:])
+            K.store(b, k32, None, slots)
+            want = q32
+        else:
+            k32 = K.norm_rope(k, pos if rp else None, rope=rp, norm=norm, dtype=torch.float32)
+            want = K.norm_rope(q, pos if rp else None, rope=rp, norm=norm, dtype=torch.float32)
+            K.store(b, k32, v.float().contiguous(), slots)
+            want = K.rotate_query(want) if f == K.FMT_Q4_HAD32 else K.tq4_rotate(b, want) if f == K.FMT_TQ4 else want
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got.nan_to_num(nan=0.0), want.nan_to_num(nan=0.0))
+        for name in ("k", "v", "k_scale", "v_scale"):
+            ta, tb = getattr(a, name), getattr(b, name)
+            if ta is None:
+                continue
+            if ta.dtype != torch.uint8:
+                assert torch.equal(torch.isnan(ta), torch.isnan(tb)), name
+                ta, tb = ta.float().nan_to_num(nan=0.0), tb.float().nan_to_num(nan=0.0)
+            assert torch.equal(ta, tb), name
+        good = [0, 1, 3, 5, 7, 8]
+        back = K.load(a, slots, dtype=torch.float32)
+        c = make_cache(K, f, Hk, D, 2)
+        ck, cv = (x.to(dtype) for x in clean)
+        K.norm_rope_store(c, None, ck, None if fp8 else cv, slots, pos if rp else None, rope=rp, k_norm=norm)
+        for x, y in zip(back, K.load(c, slots, dtype=torch.float32)):
+            if x is not None:
+                assert torch.equal(x[good], y[good]) and torch.isfinite(x[good]).all()
+    if kind == "nan" and not fp8:      # (values: stored as they are; fp8 holds NaN as zero)
+        hit = torch.zeros(n, Hk, D, dtype=torch.bool, device=DEV)
+        group = {"Q4_HAD32": 32, "TQ4": 256, "BF16": 1}.get(fmt)
+        for t, h, e in ((2, 0, 5), (4, Hk - 1, 40), (4, Hk - 1, 41), (6, 0, 255)):
+            if group:
+                hit[t, h, e // group * group:(e // group + 1) * group] = True
+        if group:
+            assert torch.equal(torch.isnan(back[1]), hit)
+
+
+def test_heads_that_are_not_numbers(K):
+    """diff_heads: NaN and infinity stay in their head (without a norm, in their element)."""
+    x = rnd((5, 8, 256), "dh nan")
+    lam = torch.rand(4, device=DEV)
+    bad = x.clone()
+    bad[1, 2, 7], bad[2, 5, 8], bad[3, 0, 9], bad[3, 1, 9] = math.nan, math.inf, math.inf, math.inf
+    for norm in (None, K.Norm(torch.ones(256, device=DEV), 1e-5)):
+        want, got = K.diff_heads(x, lam, norm=norm), K.diff_heads(bad, lam, norm=norm)
+        hit = torch.zeros(5, 4, dtype=torch.bool, device=DEV)
+        hit[1, 1] = hit[2, 2] = hit[3, 0] = True
+        assert torch.equal(got[~hit], want[~hit])
+        if norm is None:
+            where = torch.zeros(5, 4, 256, dtype=torch.bool, device=DEV)
+            where[1, 1, 7] = where[2, 2, 8] = where[3, 0, 9] = True
+            assert torch.equal(~torch.isfinite(got), where) and torch.equal(got[~where], want[~where])
+        else:
+            assert torch.isnan(got[1, 1]).all() and torch.isnan(got[3, 0]).all()
 
 
 # ------------------------------------------------------------------ strides that no element uses
