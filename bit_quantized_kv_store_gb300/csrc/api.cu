@@ -685,7 +685,9 @@ static int32_t check_rope(const kvq_rope* r, int32_t width, const int32_t* pos, 
 
 static bool norm_rope_width(int32_t w) { return w == 64 || w == 128 || w == 256 || w == 512; }
 
-constexpr int32_t kMaxHeads = 16384;  // (a grid dimension of the norm and rope kernel)
+// Of every call that norms and rotates (the latent rows' kernel has a token's heads in a
+// grid dimension, the others keep to the same).
+constexpr int32_t kMaxHeads = 16384;
 
 int32_t kvq_rope_table(const double* inv_freq, const int32_t* axis, int32_t pairs, uint64_t* table) {
   if (!inv_freq || !table || pairs < 1) return KVQ_ERR_INVALID_ARG;

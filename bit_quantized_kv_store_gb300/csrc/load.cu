@@ -25,9 +25,12 @@
 // (As stages across lanes on the results they were a third of the instructions.)
 //
 // Bound: memory (in bf16 the outputs are 3.6 times the codes' bytes).  262144 tokens
-// of 4 heads to bf16: 220 us, 1.38 GB, 6.3 TB/s (93 % of the measured copy).  20011
-// tokens of TQ4 rows to fp32: 34.4 us, 185 MB, 5.4 TB/s; 200011 to bf16: 280 us, 1.03 GB,
-// issue (the look-ups, the sums in two terms).  A lane writes 16 bytes next to its
+// of 4 heads to bf16: 218 us, 1.38 GB, 6.3 TB/s (93 % of the measured copy).  20011
+// tokens of TQ4 rows to fp32: 34.1 us, 185 MB, 5.4 TB/s; 200011 to bf16: 265 us, 1.03 GB:
+// the look-ups and the sums in two terms take 120 registers, and at 16 warps an SM half
+// the issue slots wait (the FEW kernels spill 16 to 36 bytes a thread besides).  Rows
+// without codes (load_wide_kernel): 65536 tokens of 4 bf16 heads 84 us, 6.4 TB/s;
+// 262144 fp8 rows to bf16 81 us, 5.6 TB/s.  A lane writes 16 bytes next to its
 // neighbours' or 32 by itself: stores of 16 bytes 32 apart reached 4.1 TB/s, these
 // 7.5 TB/s, in a kernel that only writes.
 #include <cuda_fp8.h>

@@ -20,13 +20,17 @@
 // were shared by fewer rows.  The angles (the same for every head) are worked out
 // once per token and warp, spread over its lanes, and read back from shared memory.
 //
-// Bound.  4099 x 24 heads of 256, bf16 to bf16 with norm and three axes: 17.7 us, 101
-// MB, 5.7 TB/s (84 % of the measured copy; the same kernel without norm and rotation
-// takes as long, so what is left is filling and draining the memory pipe).  4096
-// tokens of 24 + 4 + 4 heads to rotated fp32 queries and 4-bit rows: 36.2 us, 172 MB,
-// 4.7 TB/s; 31 us without the norm, the rotations and the codes' arithmetic, the
-// rest is issue (20.2 M instructions at 52 %).  One token: the launch.
-// Measured and not kept (the 4096-token chunk with its read-back, 41.7 us): K and V
+// Bound (times of calls in a graph).  4099 x 24 heads of 256, bf16 to bf16 with norm
+// and three axes: 19.1 us, 101 MB, 5.3 TB/s (78 % of the measured copy; the same kernel
+// without norm and rotation takes as long, so what is left is filling and draining the
+// memory pipe).  4096 tokens of 24 + 4 + 4 heads to rotated fp32 queries and 4-bit rows:
+// 34.2 us, 172 MB, 5.0 TB/s (Q4_0 rows 32.2, bf16 rows 33.0 us, floors 25.5 and 27.3);
+// 31 us without the norm, the rotations and the codes' arithmetic.  The rest is latency at
+// 16 warps an SM: 20.2 M instructions leave half the issue slots empty, waiting for
+// shared memory and the shuffles.  TQ4 rows 49.5 us: four of their eight butterfly
+// stages go across lanes, 64 shuffles a row, and the kernels of one type spill 52 to 68
+// bytes a thread.  One token: the launch.
+// Measured and not kept (the 4096-token chunk with its read-back, then 41.7 us): K and V
 // rows two batches side by side like the queries' 47.3 us, one batch at 80 registers
 // and 24 warps an SM 49.7 us, five CTAs of four warps at 96 registers 51.4 us.
 //
@@ -234,7 +238,7 @@ cudaError_t launch_ranges(NormRopeArgs a, cudaStream_t s) {
   // One range of batches for each resident warp, one batch where there are fewer; and
   // CTAs of fewer warps where that leaves SMs without one.  (Rounded up to an even
   // number, for the pairs of query batches: 1001 fp32 tokens of 32 + 8 + 8 heads of 128
-  // with their read-back 14.0 us instead of 13.0, 4096 tokens 41.8 instead of 41.3.)
+  // with their read-back 16.3 us instead of 15.0, 4096 tokens 41.5 instead of 40.9.)
   constexpr int RPW = 32 / LPR;
   const int64_t total = FEW ? a.Hq : (a.Hq + RPW - 1) / RPW + 2 * ((a.Hk + RPW - 1) / RPW);
   const int64_t n_sm = device_sm_count() > 0 ? device_sm_count() : 1;
@@ -250,6 +254,10 @@ cudaError_t launch_ranges(NormRopeArgs a, cudaStream_t s) {
   const auto all = [&](int t) { return (!q || a.q.dtype == t) && (!kv || (a.k.dtype == t && a.v.dtype == t)); };
   const bool out_f32 = !q || a.qo.dtype == KVQ_DT_F32;
   cudaError_t e;
+  // One batch a warp: the kernel of any type, which takes it alone.  Two batches side by
+  // side have nothing to overlap then and cost TQ4 rows their spills (100 tokens of 24 + 4
+  // heads 4.5 us so, 5.4 us by type; bf16 rows 3.65 and 3.8 us; one token of 4-bit rows
+  // 3.1 to 3.3 and 3.0 to 3.1 us).
   if (!whole || per == 1)
     e = launch_pdl(norm_rope_kernel<LPR, FMT, kAny, FEW>, grid, block, 0, s, a);
   else if (all(KVQ_DT_BF16))
@@ -266,8 +274,8 @@ cudaError_t launch_ranges(NormRopeArgs a, cudaStream_t s) {
 template <int LPR, int FMT>
 cudaError_t launch_one(const NormRopeArgs& a, cudaStream_t s) {
   // Few heads: half a batch of one token's heads or more would be empty, and there are
-  // more such batches than resident warps (one head of 128, 10336 tokens: 8.9 us so,
-  // 13.2 us by tokens; one of 64, 16384 tokens: 5.8 and 12.8 us; below that many tokens
+  // more such batches than resident warps (one head of 128, 10336 tokens: 8.5 us so,
+  // 13.2 us by tokens; one of 64, 16384 tokens: 5.3 and 12.8 us; below that many tokens
   // the angles are better spread over a whole warp).
   constexpr int RPW = 32 / LPR;
   if constexpr (FMT == kNoStore && RPW > 1)

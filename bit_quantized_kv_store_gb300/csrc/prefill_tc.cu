@@ -635,9 +635,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
 // head, and a chunk of 1024 at depth 4096 is 196 CTAs on 152 SMs: two waves, the
 // second a quarter full.  The count that costs least, in the time of a 64-key tile
 // (2.0 us): the waves' tiles, 7 for a CTA's start and end, and the partials written
-// and read back (2 KB a row at about 5 TB/s).  Measured, merge included: 1024 rows
-// at 4096 in three ranges 278 us, 64 rows at 4000 in eight 35 us; the prefill alone
-// in one range 339 and 148 us.  (4 or 2 instead of 7 choose the same counts for chunks of
+// and read back (2 KB a row at about 6 TB/s).  Measured, merge included: 1024 rows
+// at 4096 in three ranges 277 us, 64 rows at 4000 in eight 36 us; the prefill alone
+// in one range 338 and 147 us.  (4 or 2 instead of 7 choose the same counts for chunks of
 // 16 to 1024 rows.)
 int prefill_splits(int n_q, int Hq, int Hk, int q_start, int n_sm) {
   const int qpb = 128 / (Hq / Hk);
