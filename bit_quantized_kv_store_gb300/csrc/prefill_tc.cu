@@ -91,6 +91,7 @@ struct PfSmem {
   float inv[128];  // per row: 1 / z, at the end
   uint32_t tmem_base;
   int abort;
+  int nan_key[8];  // per group: the first key of a partly masked tile whose V scale is not finite (INT_MAX: none)
   int bad_key;  // the first key in a page outside the pool (INT_MAX: none): rows from it on come out NaN
 };
 static_assert(sizeof(PfSmem) + 1024 <= 232448, "prefill shared memory exceeds the 227 KB per-CTA limit");
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
     mbar_init(&sm.q_ready, 12);
     sm.abort = 0;
     sm.bad_key = INT_MAX;
+    for (int G = 0; G < 8; ++G) sm.nan_key[G] = INT_MAX;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(&sm.tmem_base, 512);
@@ -562,6 +564,24 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
         const int key = 8 * kbk + krow;
         uint4 sc = pf_lds128(st_scales + key * 16);
         if (jk0 + key >= kmax) sc = make_uint4(0, 0, 0, 0);  // zero scale past kmax: stale codes give zero
+        if (jk0 + kPfKeys > a.q_start + q0) {
+          // a tile that some row masks in part: a scale that is not finite would reach that
+          // row, too (0 x NaN); it is taken out here, and the rows that attend its key get
+          // their NaN at the end (an exponent of all ones carries into its half's sign bit)
+          const uint32_t e0 = sc.x & 0x7C007C00u, e1 = sc.y & 0x7C007C00u, e2 = sc.z & 0x7C007C00u, e3 = sc.w & 0x7C007C00u;
+          if (((e0 + 0x04000400u) | (e1 + 0x04000400u) | (e2 + 0x04000400u) | (e3 + 0x04000400u)) & 0x80008000u) {
+#pragma unroll 1
+            for (int G = 0; G < 8; ++G) {
+              const uint32_t half = 0xFFFFu << (16 * (G & 1));
+              if ((word_at(sc, G >> 1) & half & 0x7C007C00u) != (half & 0x7C007C00u)) continue;
+              atomicMin(&sm.nan_key[G], jk0 + key);
+              if (G >> 1 == 0) sc.x &= ~half;
+              else if (G >> 1 == 1) sc.y &= ~half;
+              else if (G >> 1 == 2) sc.z &= ~half;
+              else sc.w &= ~half;
+            }
+          }
+        }
         __half2 s2[8];
 #pragma unroll
         for (int G = 0; G < 8; ++G) s2[G] = scale_pair(word_at(sc, G >> 1), G & 1);
@@ -599,13 +619,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_tc_kernel(const __grid_
     const bool wide = (reinterpret_cast<uintptr_t>(dst0) & 31u) == 0;  // whole sectors
 #pragma unroll 1
     for (int G = G0; G < G1; ++G) {
+      const float f = a.q_start + q0 + iq >= sm.nan_key[G] ? NAN : inv;
       uint32_t o[32];
       __syncwarp();  // reconverge after the previous iteration's per-row store
       tmem_ld32(tbase + lane_off + kTmO + 32 * G, o);
       tmem_wait_ld();
       float x[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * inv;
+      for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]) * f;
       const bool rot = a.rotate != 0 && !part;  // Q4_0: nothing to rotate back
       if (rot) {
         fwht32_regs(x);

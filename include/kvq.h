@@ -347,8 +347,8 @@ int32_t kvq_merge(const kvq_cache* cache, const void* workspace, size_t ws_bytes
  *   out: device fp32 [n_q, num_q_heads, head_dim], 16-byte aligned, rotated back.
  *       Rows that attend a page outside the pool come out NaN (KVQ_DEV_BAD_PAGE), the
  *       rows before it as they are without it.
- *       (128 / group neighbouring positions share their products with V: a V row that is
- *       not a number also reaches those of them that lie before it.)
+ *       (Values are fp16 operands here: magnitudes above 65504, of scales above 8188,
+ *       are infinite, also to the masked rows of their query block.)
  *   Q4 only; head_dim == 256; num_q_heads / num_kv_heads <= 8. */
 int32_t kvq_prefill_attn(const kvq_cache* cache, const void* q, int32_t dtype, int32_t n_q,
                          int32_t num_q_heads, int32_t q_start, const int32_t* d_block_table,

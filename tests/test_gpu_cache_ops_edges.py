@@ -87,6 +87,37 @@ def test_rows_before_a_bad_page(K, fmt, T0, n, bad):
         assert torch.isnan(got[first:]).all()
 
 
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "Q4_0"])
+@pytest.mark.parametrize("T0,n,at", [(0, 200, 0), (0, 200, 70), (0, 200, 199), (1000, 100, 1031), (1000, 100, 3), (4000, 700, 4400)])
+def test_rows_before_a_key_that_is_not_a_number(K, fmt, T0, n, at):
+    """A chunk's rows that mask a NaN key or value are what they are without it; those
+    that attend a NaN value lose its group of 32, those that attend a NaN key everything."""
+    cache = make_cache(K, getattr(K, "FMT_" + fmt), 4, 256, (T0 + n + 15) // 16)
+    fill_random(cache, K, n)
+    bt = torch.arange(cache.num_pages, dtype=torch.int32, device=DEV)
+    q = rnd((n, 24, 256), "nan rows", n, scale=0.1)
+    lam = torch.rand(12, device=DEV)
+    first = max(0, at - T0)
+    calls = (lambda: K.prefill_attn(cache, q, T0, bt, 1 / 16), lambda: K.prefill_diff(cache, q, T0, bt, 1 / 16, lam))
+    want = [f() for f in calls]
+    for plane, groups, lost in (("v_scale", [3], slice(96, 128)), ("v_scale", [0, 7], None), ("k_scale", [5], slice(0, 256))):
+        scales = getattr(cache, plane)
+        keep = scales.clone()
+        for G in groups:
+            scales[at // 16, 2, at % 16, G] = math.nan
+        for f, w in zip(calls, want):
+            got, heads = f(), w.shape[1] // 4           # heads of a KV head
+            hit = torch.zeros_like(got, dtype=torch.bool)
+            mine = hit[first:, 2 * heads:3 * heads]
+            if lost is None:
+                mine[..., :32] = mine[..., 224:] = True
+            else:
+                mine[..., lost] = True
+            # (of 2.4 million random scales a few are above 8188: -8 of them is infinite in the kernel's fp16)
+            assert torch.isnan(got[hit]).all() and torch.allclose(got[~hit], w[~hit], rtol=0, atol=0, equal_nan=True)
+        scales.copy_(keep)
+
+
 # ------------------------------------------------------------------ rows that are not numbers, on the way in and back
 
 BAD = {"nan": math.nan, "inf": math.inf, "-inf": -math.inf, "huge": 3e38}
