@@ -247,6 +247,8 @@ int32_t kvq_decode_attn(const kvq_cache* cache, const float* q, int32_t num_seqs
  * block table repeated for every row.  A row whose length is out of range is
  * skipped and flagged (KVQ_DEV_BAD_LENGTH; the merge writes NaN for it), the
  * others are unaffected.
+ * (The rows of a slice share their products with V: a V row that is not a number also
+ * reaches those that mask it.)
  * Merge with kvq_merge(num_seqs = num_rows, d_seq_lens = d_row_lens).
  *   q: device fp32 [num_rows, num_q_heads, head_dim] (rotated, as for
  *      kvq_decode_attn); d_row_lens: device int32 [num_rows];

@@ -55,6 +55,22 @@ def test_a_query_that_is_not_a_number(K, fmt, T):
         assert torch.isnan(y[0, 2]).all() and torch.isfinite(y[0, :2]).all() and torch.isfinite(y[0, 3:]).all()
 
 
+@pytest.mark.parametrize("fmt", ["Q4_HAD32", "Q4_0", "TQ4", "BF16"])
+@pytest.mark.parametrize("T", [1, 15, 700, 513, 40003])
+def test_slots_behind_the_end_that_are_not_numbers(K, fmt, T):
+    """The last page's slots behind the sequence hold NaN rows: the outputs are those
+    over finite ones."""
+    f = getattr(K, "FMT_" + fmt)
+    cache, q, lens, bt, T, ws = diff_problem(K, f, [T])
+    lam = torch.rand(12, device=DEV)
+    want = K.decode(cache, q, lens, bt, T, 1 / 16, ws), K.decode_diff(cache, q, lens, bt, T, 1 / 16, ws, lam)
+    page = bt[0, (T - 1) // 16].long()
+    for name in ("k", "v") if f == K.FMT_BF16 else ("k_scale", "v_scale"):
+        getattr(cache, name)[page, :, T % 16 or 16:] = math.nan
+    got = K.decode(cache, q, lens, bt, T, 1 / 16, ws), K.decode_diff(cache, q, lens, bt, T, 1 / 16, ws, lam)
+    assert torch.isfinite(want[0]).all() and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ------------------------------------------------------------------ a bad page inside a prompt chunk
 
 @pytest.mark.parametrize("fmt", ["Q4_HAD32", "Q4_0"])
