@@ -93,6 +93,10 @@ SIGNATURES = {
     "kvq_prefill_diff_workspace_size": (_SZ, [_CACHE, _I32, _I32, _I32]),
     "kvq_prefill_diff": (_I32, [_CACHE, _P, _I32, _I32, _I32, _I32, _P, _I32, _F, _P, _I64, _NORM, _F, _P, _SZ, _P, _I32,
                                 _P, _P]),
+    "kvq_attn_workspace_size": (_SZ, [_CACHE, _I32, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "kvq_decode_local": (_I32, [_CACHE, _ROWS, _I32, _P, _P, _I32, _I32, _I32, _I32, _F, _P, _SZ, _ROWS, _P, _P]),
+    "kvq_attn_seqs": (_I32, [_CACHE, _ROWS, _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _F, _P, _SZ, _ROWS, _P,
+                             _P]),
     "kvq_diff_heads": (_I32, [_P, _I64, _I32, _I32, _P, _I64, _NORM, _F, _P, _I32, _P]),
 }
 
@@ -429,7 +433,8 @@ def calls():
         loader.exec_module(module)
         module.init(tuple(ctypes.cast(getattr(L, "kvq_" + n), _P).value for n in
                           ("norm_rope", "norm_rope_store", "load", "load_seqs", "merge_diff", "diff_heads",
-                           "prefill_diff_workspace_size", "prefill_diff")), _check)
+                           "prefill_diff_workspace_size", "prefill_diff", "attn_workspace_size", "decode_local",
+                           "attn_seqs")), _check)
         _calls = module
     return _calls
 
@@ -581,6 +586,47 @@ def prefill_diff(cache: Cache, q, q_start, block_table, sm_scale, lam, norm=None
                                 status)
     return (_calls or calls()).prefill_diff(cache.handle, q, q_start, block_table, sm_scale, lam, _handle(norm),
                                             out_scale, out, dtype, workspace, status)
+
+
+def attn_workspace_size(cache: Cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window=0, sinks=0):
+    return lib().kvq_attn_workspace_size(cache.ref, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window, sinks)
+
+
+def alloc_attn_workspace(cache: Cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window=0, sinks=0,
+                         device="cuda"):
+    """The workspace of attn_seqs(); with n_rows = num_seqs and max_rows = 1 of decode_local()."""
+    n = attn_workspace_size(cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window, sinks)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def decode_local(cache: Cache, q, seq_lens, block_tables, max_seq_len, sm_scale, window, sinks=0, out=None,
+                 dtype=torch.float32, workspace=None, status=None, stream=None):
+    """One decode step that sees a sliding window and the first tokens: row b of q [B, Hq,
+    D] (unrotated, any strides with a contiguous last dimension) is sequence b's newest
+    token, seq_lens[b] - 1, and sees its last `window` tokens (0: all) and the first
+    `sinks`.  Block-table entries of pages that are not seen may be anything.  Returns
+    out [B, Hq, D] (default: a new tensor of `dtype`).  Any format but fp8, D 64, 128 or
+    256.  workspace: of alloc_attn_workspace() (default: a new one)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return decode_local(cache, q, seq_lens, block_tables, max_seq_len, sm_scale, window, sinks, out, dtype,
+                                workspace, status)
+    return (_calls or calls()).attn_rows(cache.handle, q, None, seq_lens, block_tables, 1, max_seq_len, sm_scale, window,
+                                         sinks, out, dtype, workspace, status)
+
+
+def attn_seqs(cache: Cache, q, cu_rows, seq_lens, block_tables, max_rows, max_seq_len, sm_scale, window=0, sinks=0,
+              out=None, dtype=torch.float32, workspace=None, status=None, stream=None):
+    """Causal attention of new rows of several sequences: rows cu_rows[b] .. cu_rows[b + 1]
+    - 1 of q [rows, Hq, D] are the last tokens of sequence b, which has seq_lens[b] stored
+    ones (theirs among them).  window and sinks as in decode_local(); max_rows: the most
+    rows that a sequence has.  Returns out [rows, Hq, D]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return attn_seqs(cache, q, cu_rows, seq_lens, block_tables, max_rows, max_seq_len, sm_scale, window, sinks,
+                             out, dtype, workspace, status)
+    return (_calls or calls()).attn_rows(cache.handle, q, cu_rows, seq_lens, block_tables, max_rows, max_seq_len,
+                                         sm_scale, window, sinks, out, dtype, workspace, status)
 
 
 def selftest_wait_timeout(d_status, stream=None):

@@ -685,7 +685,7 @@ static int32_t check_rope(const kvq_rope* r, int32_t width, const int32_t* pos, 
 
 static bool norm_rope_width(int32_t w) { return w == 64 || w == 128 || w == 256 || w == 512; }
 
-// Of every call that norms and rotates (the latent rows' kernel has a token's heads in a
+// Of every call that norms and rotates, and of those over several sequences (the latent rows' kernel has a token's heads in a
 // grid dimension, the others keep to the same).
 constexpr int32_t kMaxHeads = 16384;
 
@@ -976,6 +976,120 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
   if (st != KVQ_OK) return st;
   cudaError_t e = launch_diff_heads(x, rows, num_q_heads, width, d, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+// ---------------------------------------------------------------- several sequences, windows
+
+// The shape of rows over a cache, in `a` with its window and sinks brought to what they say
+// for sequences of at most max_seq_len tokens.
+static int32_t check_attn_shape(const kvq_cache* c, int32_t n_rows, int32_t num_seqs, int32_t Hq, int32_t max_rows,
+                                int32_t max_seq_len, int32_t window, int32_t sinks, SeqAttnArgs* a) {
+  int32_t st = check_cache(c);
+  if (st != KVQ_OK) return st;
+  if (c->format == KVQ_FMT_FP8_ROW) return KVQ_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return KVQ_ERR_UNSUPPORTED;
+  if (n_rows < 0 || num_seqs < 0 || Hq < 1 || Hq % c->num_kv_heads != 0 || max_rows < 0 || max_seq_len < 0 ||
+      window < 0 || sinks < 0)
+    return KVQ_ERR_INVALID_ARG;
+  const int group = Hq / c->num_kv_heads;
+  if (group > 64 || num_seqs > 65535 || Hq > kMaxHeads) return KVQ_ERR_UNSUPPORTED;
+  // positions and row numbers are 32-bit in the kernels, with room for a window below them
+  if (max_seq_len >= (1 << 30) || n_rows >= (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+  a->c = *c;
+  a->n_rows = n_rows;
+  a->num_seqs = num_seqs;
+  a->Hq = Hq;
+  a->group = group;
+  a->max_rows = max_rows < n_rows ? max_rows : n_rows;
+  a->max_seq_len = max_seq_len;
+  a->window = window < max_seq_len ? window : 0;  // every key is in it
+  a->sinks = a->window == 0 ? 0 : sinks < max_seq_len ? sinks : max_seq_len;
+  if (static_cast<int64_t>(a->max_rows) * group + 7 >= int64_t(8) * 65535 / c->num_kv_heads) return KVQ_ERR_UNSUPPORTED;
+  return KVQ_OK;
+}
+
+struct AttnLayout {
+  FewPlan few;
+  size_t m_off, z_off, acc_off, total;
+};
+
+static AttnLayout attn_layout(const SeqAttnArgs& a) {
+  AttnLayout w{};
+  int n_sm = device_sm_count();
+  if (n_sm < 1) n_sm = 1;
+  w.few = few_plan(a.c, a.num_seqs, a.Hq, a.max_rows, a.max_seq_len, a.window, a.sinks, n_sm);
+  if (w.few.ranges > 1) {
+    const size_t n = static_cast<size_t>(w.few.ranges) * a.n_rows * a.Hq;
+    w.z_off = round256(n * sizeof(float));
+    w.acc_off = 2 * w.z_off;
+    w.total = w.acc_off + n * a.c.head_dim * sizeof(float);
+  }
+  return w;
+}
+
+size_t kvq_attn_workspace_size(const kvq_cache* cache, int32_t n_rows, int32_t num_seqs, int32_t num_q_heads,
+                               int32_t max_rows, int32_t max_seq_len, int32_t window, int32_t sinks) {
+  SeqAttnArgs a{};
+  if (check_attn_shape(cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window, sinks, &a) != KVQ_OK) return 0;
+  return attn_layout(a).total;
+}
+
+static int32_t attn_impl(const kvq_cache* cache, const kvq_rows* q, int32_t n_rows, int32_t num_seqs,
+                         const int32_t* d_cu_rows, const int32_t* d_seq_lens, const int32_t* d_block_tables,
+                         int32_t max_pages, int32_t max_rows, int32_t max_seq_len, int32_t window, int32_t sinks,
+                         float sm_scale, void* workspace, size_t ws_bytes, const kvq_rows* out, int32_t* d_status,
+                         void* stream) {
+  if (!q || !out) return KVQ_ERR_INVALID_ARG;
+  SeqAttnArgs a{};
+  int32_t st = check_attn_shape(cache, n_rows, num_seqs, q->heads, max_rows, max_seq_len, window, sinks, &a);
+  if (st != KVQ_OK) return st;
+  if (num_seqs == 0 || n_rows == 0 || max_rows == 0) return KVQ_OK;
+  if (!d_seq_lens || !d_block_tables || max_pages < 1 || !aligned4(d_cu_rows, d_seq_lens, d_block_tables, d_status))
+    return KVQ_ERR_INVALID_ARG;
+  if (!(fabsf(sm_scale) < INFINITY)) return KVQ_ERR_INVALID_ARG;
+  st = check_rows(q, n_rows, q->heads, cache->head_dim, &a.q);
+  if (st == KVQ_OK) st = check_rows(out, n_rows, q->heads, cache->head_dim, &a.out);
+  if (st != KVQ_OK) return st;
+  if (!rows_distinct(out, n_rows, cache->head_dim) || a.q.data == a.out.data) return KVQ_ERR_INVALID_ARG;
+  if (max_seq_len > static_cast<int64_t>(max_pages) * cache->page_size) return KVQ_ERR_INVALID_ARG;
+  // cache rows are 32-bit in the kernels
+  const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * cache->num_kv_heads * cache->page_size;
+  if (rows >= (1ull << 31)) return KVQ_ERR_UNSUPPORTED;
+  const AttnLayout w = attn_layout(a);
+  if (w.total > 0) {
+    if (ws_bytes < w.total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
+    if (!workspace || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+  }
+  a.cu_rows = d_cu_rows;
+  a.seq_lens = d_seq_lens;
+  a.block_tables = d_block_tables;
+  a.max_pages = max_pages;
+  a.qscale = sm_scale * kLog2e;
+  a.status = d_status;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.ws_m = reinterpret_cast<float*>(ws + w.m_off);
+  a.ws_z = reinterpret_cast<float*>(ws + w.z_off);
+  a.ws_acc = reinterpret_cast<float*>(ws + w.acc_off);
+  cudaError_t e = launch_attn_few(a, w.few, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
+}
+
+int32_t kvq_decode_local(const kvq_cache* cache, const kvq_rows* q, int32_t num_seqs, const int32_t* d_seq_lens,
+                         const int32_t* d_block_tables, int32_t max_pages_per_seq, int32_t max_seq_len,
+                         int32_t window, int32_t sinks, float sm_scale, void* workspace, size_t ws_bytes,
+                         const kvq_rows* out, int32_t* d_status, void* stream) {
+  return attn_impl(cache, q, num_seqs, num_seqs, nullptr, d_seq_lens, d_block_tables, max_pages_per_seq, 1, max_seq_len,
+                   window, sinks, sm_scale, workspace, ws_bytes, out, d_status, stream);
+}
+
+int32_t kvq_attn_seqs(const kvq_cache* cache, const kvq_rows* q, int32_t n_rows, int32_t num_seqs,
+                      const int32_t* d_cu_rows, const int32_t* d_seq_lens, const int32_t* d_block_tables,
+                      int32_t max_pages_per_seq, int32_t max_rows, int32_t max_seq_len, int32_t window,
+                      int32_t sinks, float sm_scale, void* workspace, size_t ws_bytes, const kvq_rows* out,
+                      int32_t* d_status, void* stream) {
+  if (num_seqs > 0 && n_rows > 0 && max_rows > 0 && !d_cu_rows) return KVQ_ERR_INVALID_ARG;
+  return attn_impl(cache, q, n_rows, num_seqs, d_cu_rows, d_seq_lens, d_block_tables, max_pages_per_seq, max_rows,
+                   max_seq_len, window, sinks, sm_scale, workspace, ws_bytes, out, d_status, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,897 @@
+// attn_few.cu -- attention of few rows a sequence (single new tokens, draft rows, short
+// chunks) over the paged cache, with a sliding window and sinks, every row format.
+//
+// For a row at position p:  o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m) over the keys j
+// that it sees (seqs.cuh), s_j = sm_scale log2(e) q . k_j, m a running reference.
+//
+// Bound by memory where a batch is large (each row of the cache is read once, 288 bytes
+// a key and KV head of the 4-bit rows at 256 wide), by latency where it is not: a window
+// of 4096 keys of one sequence is 4.7 MB, 0.7 us of the memory's time.  So the keys of a
+// block of 8 columns (row x query head of one KV head) are dealt out to the warps of a
+// cluster of CTAs, tile by tile, each warp with a ring of its own that cp.async fills;
+// nothing synchronises between the first load and the last product.  The warps' partials
+// are folded in shared memory, the CTAs' through distributed shared memory, in a fixed
+// order, and the output is rotated back and rounded by the same launch.  Where one
+// cluster would leave most of the GPU idle, several write partials and a second kernel
+// folds them.
+//
+// 4-bit groups: a key's codes enter the tensor cores unsigned, without a conversion: c in
+// bits 2 to 5 of a half is the subnormal c 2^-22, in bits 6 to 9 16 c 2^-22, and the query
+// of such a dim carries the 1/16; the 8 that codes are biased by is in the accumulator's
+// start (-8 sum q over the group).  So a group of scores is exact up to the query, which is
+// split into two halves (22 bits), and its scale multiplies the fp32 sum.  (The tensor cores
+// line products of subnormals up as if their exponent were 2^-14 and cut a sum 23 bits
+// below: 2^-15 of a code times the largest query element, a 2^-15 part of a score.  For
+// values, whose small sums count, that is too much: they are converted, exactly, to c - 8.)
+// On the way out the scale multiplies p instead of 32 values: p' = fp16(fp16(p) s), two
+// roundings of 2^-12.  The softmax's reference counts the key's largest scale in (m bounds
+// s_j + log2 smax_j), so p' keeps its bits whatever the scales are.
+// TQ4 rows: levels by byte lookups (tq4_levels.cuh), the row's scale on scores and p.
+// bf16 rows: as they are; q and p in two bf16 halves (16 bits).
+#include <algorithm>
+#include <climits>
+
+#include "f32x2.cuh"
+#include "rows.cuh"
+#include "seqs.cuh"
+#include "tq4_levels.cuh"
+
+namespace kvq {
+
+constexpr uint32_t kCodeLo = 0x003C003Cu, kCodeHi = 0x03C003C0u;  // c 2^-22, 16 c 2^-22
+enum { kFewQ4 = 0, kFewTq4 = 1, kFewBf16 = 2 };
+
+template <int FMT, int D>
+struct FewShape {
+  static constexpr bool kBf = FMT == kFewBf16;
+  static constexpr int kRow = kBf ? 2 * D : D / 2;           // bytes of a row of the k or v plane
+  static constexpr int kChunks = kRow / 16;                  // 16-byte chunks of it
+  static constexpr int kScaleRow = FMT == kFewQ4 ? D / 16 : FMT == kFewTq4 ? 2 : 0;  // bytes of its scales
+  static constexpr int kBlocks = kBf && D == 256 ? 1 : 2;    // 16-key blocks of a tile
+  static constexpr int kKeys = 16 * kBlocks;
+  static constexpr int kPlane = kKeys * kRow;
+  static constexpr int kScales = kKeys * kScaleRow;
+  static constexpr int kStage = (2 * kPlane + 2 * kScales + 127) / 128 * 128;
+  static constexpr int kStages = 2;
+  static constexpr int kSteps = D / 16;                      // k-steps of the score product
+};
+
+template <int FMT, int D, int WARPS>
+struct FewSmem {
+  using S = FewShape<FMT, D>;
+  static constexpr int kRing = S::kStage * S::kStages * WARPS;
+  static constexpr int kFold = WARPS * 8 * D * 4;
+  union {
+    __align__(128) uint8_t ring[kRing > kFold ? kRing : kFold];
+    float fold[WARPS][8][D];
+  };
+  uint4 qf[S::kSteps][32];  // per k-step and lane: (high b0, b1, low b0, b1) of the score product's B operand
+  float2 bias[D / 32][4];   // 4-bit groups: -8 sum of the group's queries (heads 2t, 2t + 1), as the codes' units
+  float factor[8];          // per column: what its scores' units are worth
+  float fm[WARPS][8], fz[WARPS][8];
+  float m[8], z[8];
+  float acc[8][D];          // this CTA's partial
+};
+
+__device__ __forceinline__ void few_ldsm(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void few_ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint4 few_lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+// W words (1, 2 or 4) of shared memory.
+template <int W>
+__device__ __forceinline__ void few_lds(uint32_t a, uint32_t (&r)[W]) {
+  if constexpr (W == 4) {
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+  } else if constexpr (W == 2) {
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(a));
+  } else {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(a));
+  }
+}
+__device__ __forceinline__ uint32_t few_lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ bool not_finite(uint32_t bf16) { return (bf16 & 0x7F80u) == 0x7F80u; }
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ float half_lo(uint32_t w) { return __low2float(u32_as_h2(w)); }
+__device__ __forceinline__ float half_hi(uint32_t w) { return __high2float(u32_as_h2(w)); }
+__device__ __forceinline__ float half_of(uint32_t h) { return __half2float(__ushort_as_half(static_cast<unsigned short>(h))); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The value at this CTA's shared address in CTA `rank` of the cluster.
+__device__ __forceinline__ float cluster_ld(const float* p, uint32_t rank) {
+  uint32_t at;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
+
+// Byte offset of chunk c of row r in a plane's tile: rows of 16 kChunks bytes, the chunks
+// turned so that eight rows' chunks of one number lie in eight different sixteenths of
+// 128 bytes (what ldmatrix reads at once).
+template <int CHUNKS>
+__device__ __forceinline__ uint32_t few_off(int r, int c) {
+  if constexpr (CHUNKS >= 8) return r * CHUNKS * 16 + ((c ^ (r & 7)) << 4);
+  else return r * CHUNKS * 16 + ((c ^ ((r / (8 / CHUNKS)) & (CHUNKS - 1))) << 4);
+}
+
+__device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+  const float2 f = __bfloat1622float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_bf16(x0 - f.x, x1 - f.y);
+}
+
+// The D-point signed transform of a row whose element 32 G + lane is x[G].
+template <int NG>
+__device__ __forceinline__ void few_tq4_turn(float (&x)[NG], const uint32_t* signs, int lane, bool inverse) {
+  if (!inverse) {
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+      if ((signs[G] >> lane) & 1u) x[G] = -x[G];
+  }
+#pragma unroll
+  for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane);
+#pragma unroll
+  for (int h = 1; h < NG; h <<= 1)
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+      if (!(G & h)) {
+        const float u = x[G], v = x[G + h];
+        x[G] = u + v;
+        x[G + h] = u - v;
+      }
+  const float c = NG == 8 ? 0.0625f : NG == 4 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+  for (int G = 0; G < NG; ++G) x[G] *= c;
+  if (inverse) {
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+      if ((signs[G] >> lane) & 1u) x[G] = -x[G];
+  }
+}
+
+// Rows of columns: column 8 cb + n of a sequence is row (8 cb + n) / group, query head
+// (8 cb + n) % group of the KV head.
+template <int FMT, int D>
+__device__ __forceinline__ void few_store(const SeqAttnArgs& a, int row, int head, int e, float y) {
+  const int64_t at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + e;
+  if (a.out.dtype == KVQ_DT_F32) static_cast<float*>(a.out.data)[at] = y;
+  else static_cast<__nv_bfloat16*>(a.out.data)[at] = __float2bfloat16_rn(y);
+}
+
+template <int FMT, int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_constant__ SeqAttnArgs a) {
+  using S = FewShape<FMT, D>;
+  constexpr int NG = D / 32;
+  extern __shared__ uint8_t smem_raw[];
+  FewSmem<FMT, D, WARPS>& sm =
+      *reinterpret_cast<FewSmem<FMT, D, WARPS>*>(smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u));
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const kvq_cache& c = a.c;
+  const int b = blockIdx.z, kvh = blockIdx.y % c.num_kv_heads, cb = blockIdx.y / c.num_kv_heads;
+
+  // what the sequence's rows see (metadata only: before the kernel in front is done)
+  const SeqRows sr = seq_rows(a, b, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+  const int cols = min(8, sr.n * a.group - 8 * cb);
+  if (cols <= 0 || sr.state == kRowsSkip) {
+    pdl_wait();
+    pdl_trigger();
+    return;
+  }
+  const int base = sr.T - sr.n;  // position of the sequence's row 0
+  const int i0 = 8 * cb / a.group, i1 = (8 * cb + cols - 1) / a.group;
+  if (sr.state == kRowsNan) {
+    pdl_wait();
+    pdl_trigger();
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i < cols * D; i += WARPS * 32) {
+        const int col = 8 * cb + i / D;
+        few_store<FMT, D>(a, sr.first + col / a.group, kvh * a.group + col % a.group, i % D, NAN);
+      }
+    return;
+  }
+  const int p0 = base + i0, p1 = base + i1;
+  KeyBlocks kb{0, 0, 0};
+  if (p1 >= 0) kb = key_blocks(p0, p1, a.window, a.sinks);
+  const int all_tiles = (kb.count + S::kBlocks - 1) / S::kBlocks;
+  const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * blockIdx.x / gridDim.x);
+  const int tile1 = static_cast<int>(static_cast<int64_t>(all_tiles) * (blockIdx.x + 1) / gridDim.x);
+  const int my_tiles = tile1 - tile0 > warp ? (tile1 - tile0 - warp + WARPS - 1) / WARPS : 0;
+
+  // This warp's tiles are tile0 + warp + WARPS i.  Lane l holds the cache row of block l of
+  // 32 at a time (32 / kBlocks tiles): -1 a page outside the pool, -2 behind the last block.
+  constexpr int kBatch = 32 / S::kBlocks;
+  const int32_t* table = a.block_tables + static_cast<int64_t>(b) * a.max_pages;
+  auto find_rows = [&](int i) {
+    const int tile = i + lane / S::kBlocks;
+    const int blk = (tile0 + warp + WARPS * tile) * S::kBlocks + lane % S::kBlocks;
+    if (tile >= my_tiles || blk >= kb.count) return -2;
+    const int key = kb.block_of(blk) * 16;
+    const int page = table[key / c.page_size];
+    if (page < 0 || page >= c.num_pages) return -1;
+    return (page * c.num_kv_heads + kvh) * c.page_size + key % c.page_size;
+  };
+  int rows_now = find_rows(0), rows_next = find_rows(kBatch);
+  bool bad_page = rows_now == -1;
+  pdl_wait();
+
+  uint8_t* const ring = sm.ring + warp * (S::kStage * S::kStages);
+  auto issue = [&](int i) {  // the loads of tile i, into its stage of the ring
+    uint8_t* st = ring + (i % S::kStages) * S::kStage;
+#pragma unroll
+    for (int sub = 0; sub < S::kBlocks; ++sub) {
+      const int row0 = __shfl_sync(0xffffffffu, rows_now, (i % kBatch) * S::kBlocks + sub);
+      if (row0 < 0) continue;
+      const uint8_t* ks = static_cast<const uint8_t*>(c.k) + static_cast<int64_t>(row0) * S::kRow;
+      const uint8_t* vs = static_cast<const uint8_t*>(c.v) + static_cast<int64_t>(row0) * S::kRow;
+      uint8_t* dk = st + sub * 16 * S::kRow;
+#pragma unroll
+      for (int j = lane; j < 16 * S::kChunks; j += 32) {
+        const uint32_t off = few_off<S::kChunks>(j / S::kChunks, j % S::kChunks);
+        cp_async_16(dk + off, ks + 16 * j);
+        cp_async_16(dk + S::kPlane + off, vs + 16 * j);
+      }
+      if constexpr (S::kScaleRow > 0) {
+        uint8_t* ds = st + 2 * S::kPlane + sub * 16 * S::kScaleRow;
+        constexpr int kN = S::kScaleRow;  // 16-byte chunks of 16 rows' scales
+        const int j = lane & 15;
+        const void* plane = lane < 16 ? c.k_scale : c.v_scale;
+        if (j < kN)
+          cp_async_16(ds + (lane < 16 ? 0 : S::kScales) + 16 * j,
+                      static_cast<const uint8_t*>(plane) + static_cast<int64_t>(row0) * S::kScaleRow + 16 * j);
+      }
+    }
+  };
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  if (my_tiles > 0) issue(0);
+  commit();
+
+  // ---------------- queries: into the cache's space, scaled to 2^10 .. 2^11, split
+  for (int n = warp; n < 8; n += WARPS) {
+    float x[NG];
+    const int col = 8 * cb + n;
+    const bool live = n < cols;
+    const int64_t at = live ? static_cast<int64_t>(sr.first + col / a.group) * a.q.ts +
+                                  static_cast<int64_t>(kvh * a.group + col % a.group) * a.q.hs
+                            : 0;
+#pragma unroll
+    for (int G = 0; G < NG; ++G) x[G] = live ? load_act(a.q.data, a.q.dtype, at + 32 * G + lane) : 0.f;
+    if (c.format == KVQ_FMT_Q4_HAD32) {
+#pragma unroll
+      for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane) * kHadamardScale;
+    } else if (FMT == kFewTq4) {
+      few_tq4_turn<NG>(x, static_cast<const uint32_t*>(c.signs), lane, false);
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int G = 0; G < NG; ++G) {
+      x[G] *= a.qscale;
+      top = fmaxf(top, fabsf(x[G]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if constexpr (FMT == kFewBf16) {
+      // lane holds elements 32 G + lane; pairs by the neighbour
+#pragma unroll
+      for (int G = 0; G < NG; ++G) {
+        const float y = __shfl_down_sync(0xffffffffu, x[G], 1);
+        if ((lane & 1) == 0) {
+          uint32_t hi, lo;
+          split_bf16x2(x[G], y, hi, lo);
+          const int e = lane & 15, step = 2 * G + (lane >> 4);  // element e of the step: b0 0 .. 7, b1 8 .. 15
+          uint32_t* f = reinterpret_cast<uint32_t*>(&sm.qf[step][n * 4 + ((e & 7) >> 1)]);
+          f[e >> 3] = hi;
+          f[2 + (e >> 3)] = lo;
+        }
+      }
+      if (lane == 0) sm.factor[n] = 1.f;
+    } else {
+      // a power of two takes the largest element to [2^10, 2^11); NaN and infinities stay
+      int ex = 0;
+      if (top > 0.f && top < INFINITY) ex = 10 - (static_cast<int>(__float_as_uint(fmaxf(top, 1e-30f)) >> 23) - 127);
+      const float up = __uint_as_float(static_cast<uint32_t>(min(ex, 110) + 127) << 23);
+#pragma unroll
+      for (int G = 0; G < NG; ++G) {
+        const int j = lane & 7;
+        // element 8 t + j of group G in the order in which the codes come out of their words
+        const int step = FMT == kFewQ4 ? 2 * G + ((j & 3) >> 1) : 2 * G + (j >> 2);
+        const int reg = FMT == kFewQ4 ? j & 1 : (j >> 1) & 1;
+        const int half = FMT == kFewQ4 ? j >> 2 : j & 1;
+        const float y = x[G] * up * (FMT == kFewQ4 && reg ? 0.0625f : 1.f);
+        const __half hi = __float2half_rn(y);
+        const __half lo = __float2half_rn(y - __half2float(hi));
+        __half* f = reinterpret_cast<__half*>(&sm.qf[step][n * 4 + (lane >> 3)]);
+        f[2 * reg + half] = hi;
+        f[4 + 2 * reg + half] = lo;
+        if constexpr (FMT == kFewQ4) {
+          float sum = (__half2float(hi) + __half2float(lo)) * (reg ? 16.f : 1.f);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          if (lane == 0) reinterpret_cast<float*>(&sm.bias[G][n >> 1])[n & 1] = sum * -1.9073486328125e-06f;  // -8 2^-22
+        }
+      }
+      if (lane == 0) sm.factor[n] = (FMT == kFewQ4 ? 4194304.f : 1.f) / up;
+    }
+  }
+  __syncthreads();
+
+  // ---------------- the keys
+  const uint32_t qf = smem_u32(&sm.qf[0][lane]);
+  const float f0 = sm.factor[2 * t], f1 = sm.factor[2 * t + 1];
+  // positions of columns 2t, 2t + 1 and g (before any key where there is no such column)
+  auto pos_of = [&](int n) { return n < cols ? base + (8 * cb + n) / a.group : INT_MIN / 2; };
+  const int pc0 = pos_of(2 * t), pc1 = pos_of(2 * t + 1), pcg = pos_of(g);
+
+  float acc[D / 16][4];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, z0 = 0.f, z1 = 0.f;
+
+#pragma unroll 1
+  for (int i = 0; i < my_tiles; ++i) {
+    // ---- the next tile's loads, then wait for this one's
+    if (i + 1 < my_tiles) {
+      if ((i + 1) % kBatch == 0) {
+        rows_now = rows_next;
+        rows_next = find_rows(i + 1 + kBatch);
+        bad_page |= rows_now == -1;
+      }
+      issue(i + 1);
+    }
+    commit();
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+
+    const uint8_t* st = ring + (i % S::kStages) * S::kStage;
+    const uint32_t kbase = smem_u32(st), vbase = kbase + S::kPlane, ksc = kbase + 2 * S::kPlane, vsc = ksc + S::kScales;
+    const int blk0 = (tile0 + warp + WARPS * i) * S::kBlocks;
+    int key0[S::kBlocks];
+    bool edge = false;  // some key that some column does not see
+#pragma unroll
+    for (int sub = 0; sub < S::kBlocks; ++sub) {
+      key0[sub] = blk0 + sub < kb.count ? kb.block_of(blk0 + sub) * 16 : INT_MAX / 2;
+      edge |= !all_visible(key0[sub], 16, p0, p1, a.window, a.sinks);
+    }
+
+    // ---------------- scores of keys g, g + 8 of each block, columns 2t, 2t + 1
+    float s[S::kBlocks][4];
+#pragma unroll
+    for (int sub = 0; sub < S::kBlocks; ++sub)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[sub][j] = 0.f;
+    if constexpr (FMT == kFewBf16) {
+      float sl[S::kBlocks][4] = {};
+      const int kr = (lane & 7) + 8 * ((lane >> 3) & 1), kc = lane >> 4;
+#pragma unroll
+      for (int ks = 0; ks < S::kSteps; ++ks) {
+        const uint4 q = few_lds128(qf + ks * 512);
+#pragma unroll
+        for (int sub = 0; sub < S::kBlocks; ++sub) {
+          uint32_t ak[4];
+          few_ldsm(kbase + sub * 16 * S::kRow + few_off<S::kChunks>(kr, 2 * ks + kc), ak);
+          mma_bf16(s[sub], ak[0], ak[1], ak[2], ak[3], q.x, q.y);
+          mma_bf16(sl[sub], ak[0], ak[1], ak[2], ak[3], q.z, q.w);
+        }
+      }
+#pragma unroll
+      for (int sub = 0; sub < S::kBlocks; ++sub)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[sub][j] += sl[sub][j];
+    } else {
+      // ldmatrix: matrices (keys 0-7, chunk 2u), (keys 8-15, 2u), (keys 0-7, 2u + 1), (keys 8-15, 2u + 1)
+      const int lr = lane & 15, lc = lane >> 4;
+      float sl[S::kBlocks][4] = {};
+      constexpr int kSW = FMT == kFewQ4 ? D / 64 : 1;  // words of a key's scales
+      uint32_t sk[S::kBlocks][2][kSW];
+      if constexpr (FMT == kFewQ4) {
+#pragma unroll
+        for (int sub = 0; sub < S::kBlocks; ++sub) {
+          few_lds<kSW>(ksc + (sub * 16 + g) * S::kScaleRow, sk[sub][0]);
+          few_lds<kSW>(ksc + (sub * 16 + g + 8) * S::kScaleRow, sk[sub][1]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u) {
+        uint32_t r[S::kBlocks][4];
+#pragma unroll
+        for (int sub = 0; sub < S::kBlocks; ++sub)
+          few_ldsm(kbase + sub * 16 * S::kRow + few_off<S::kChunks>(lr, 2 * u + lc), r[sub]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int G = 2 * u + e;
+          const uint4 qa = few_lds128(qf + (2 * G) * 512), qb = few_lds128(qf + (2 * G + 1) * 512);
+          if constexpr (FMT == kFewQ4) {
+            const float2 bi = sm.bias[G][t];
+#pragma unroll
+            for (int sub = 0; sub < S::kBlocks; ++sub) {
+              const uint32_t ra = r[sub][2 * e], rb = r[sub][2 * e + 1];
+              const uint32_t al = ra << 2, bl = rb << 2, ah = ra >> 6, bh = rb >> 6;
+              const uint32_t a0 = al & kCodeLo, a1 = bl & kCodeLo, a2 = al & kCodeHi, a3 = bl & kCodeHi;
+              const uint32_t c0 = ah & kCodeLo, c1 = bh & kCodeLo, c2 = ah & kCodeHi, c3 = bh & kCodeHi;
+              float d[4];
+              mma_f16_c(d, a0, a1, a2, a3, qa.x, qa.y, bi.x, bi.y, bi.x, bi.y);
+              mma_f16(d, c0, c1, c2, c3, qb.x, qb.y);
+              mma_f16(d, a0, a1, a2, a3, qa.z, qa.w);
+              mma_f16(d, c0, c1, c2, c3, qb.z, qb.w);
+              const float sg = e ? half_hi(sk[sub][0][u]) : half_lo(sk[sub][0][u]);
+              const float sh = e ? half_hi(sk[sub][1][u]) : half_lo(sk[sub][1][u]);
+              s[sub][0] = fmaf(sg, d[0], s[sub][0]);
+              s[sub][1] = fmaf(sg, d[1], s[sub][1]);
+              s[sub][2] = fmaf(sh, d[2], s[sub][2]);
+              s[sub][3] = fmaf(sh, d[3], s[sub][3]);
+            }
+          } else {
+#pragma unroll
+            for (int sub = 0; sub < S::kBlocks; ++sub) {
+              const uint4 A = tq4_levels8(r[sub][2 * e]), B = tq4_levels8(r[sub][2 * e + 1]);
+              mma_f16(s[sub], A.x, B.x, A.y, B.y, qa.x, qa.y);
+              mma_f16(sl[sub], A.x, B.x, A.y, B.y, qa.z, qa.w);
+              mma_f16(s[sub], A.z, B.z, A.w, B.w, qb.x, qb.y);
+              mma_f16(sl[sub], A.z, B.z, A.w, B.w, qb.z, qb.w);
+            }
+          }
+        }
+      }
+      if constexpr (FMT == kFewTq4) {
+#pragma unroll
+        for (int sub = 0; sub < S::kBlocks; ++sub) {
+          const float sg = half_of(few_lds16(ksc + 2 * (sub * 16 + g))), sh = half_of(few_lds16(ksc + 2 * (sub * 16 + g + 8)));
+          s[sub][0] = (s[sub][0] + sl[sub][0]) * sg;
+          s[sub][1] = (s[sub][1] + sl[sub][1]) * sg;
+          s[sub][2] = (s[sub][2] + sl[sub][2]) * sh;
+          s[sub][3] = (s[sub][3] + sl[sub][3]) * sh;
+        }
+      }
+#pragma unroll
+      for (int sub = 0; sub < S::kBlocks; ++sub) {
+        s[sub][0] *= f0;
+        s[sub][1] *= f1;
+        s[sub][2] *= f0;
+        s[sub][3] *= f1;
+      }
+    }
+
+    // ---------------- what is not seen; pages outside the pool
+    const bool any_bad = __any_sync(0xffffffffu, bad_page);
+    uint32_t strange[S::kBlocks] = {};  // bf16: rows of V that some column does not see and that hold infinities or NaN
+    uint32_t keep[S::kBlocks][2];  // of column g: masks of the pairs of keys 2t, 2t + 1 and 2t + 8, 2t + 9
+    if (edge || any_bad) {
+#pragma unroll
+      for (int sub = 0; sub < S::kBlocks; ++sub) {
+        bool gone = false;
+        if (any_bad) {
+          const int blk = blk0 + sub;
+          if (blk < kb.count) {
+            const int page = table[kb.block_of(blk) * 16 / c.page_size];
+            gone = page < 0 || page >= c.num_pages;
+          }
+          if (gone && lane == 0) set_status(a.status, KVQ_DEV_BAD_PAGE);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = key0[sub] + g + 8 * (j >> 1);
+          if (!key_visible(key, j & 1 ? pc1 : pc0, a.window, a.sinks)) s[sub][j] = -INFINITY;
+          else if (gone) s[sub][j] = NAN;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = key0[sub] + 2 * t + 8 * h;
+          keep[sub][h] = (key_visible(key, pcg, a.window, a.sinks) ? 0x0000FFFFu : 0u) |
+                         (key_visible(key + 1, pcg, a.window, a.sinks) ? 0xFFFF0000u : 0u);
+        }
+        if constexpr (FMT == kFewBf16) {
+          // values that no column sees, and those of a bad page, become zeros: 0 x NaN is NaN
+#pragma unroll 1
+          for (int r = 0; r < 16; ++r) {
+            uint4* at = reinterpret_cast<uint4*>(ring + (i % S::kStages) * S::kStage + S::kPlane + (sub * 16 + r) * S::kRow) + lane;
+            if (gone || !any_visible(key0[sub] + r, p0, p1, a.window, a.sinks)) {
+              if (lane < S::kChunks) *at = make_uint4(0, 0, 0, 0);
+            } else if (p0 < p1) {
+              bool odd = false;
+              if (lane < S::kChunks) {
+                const uint4 v = *at;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) odd |= not_finite(word_of(v, w) & 0xFFFFu) || not_finite(word_of(v, w) >> 16);
+              }
+              if (__any_sync(0xffffffffu, odd)) strange[sub] |= 1u << r;
+            }
+          }
+        }
+      }
+      __syncwarp();
+    }
+
+    // ---------------- the key's largest value scale, as the reference counts it
+    float lsv = 0.f;  // of key `lane` of the tile
+    bool wide = false;
+    if constexpr (FMT == kFewQ4) {
+      constexpr int kSW = D / 64;
+      uint32_t w[kSW];
+      few_lds<kSW>(vsc + lane * S::kScaleRow, w);
+      __half2 h = u32_as_h2(w[0]);
+#pragma unroll
+      for (int k = 1; k < kSW; ++k) h = __hmax2(h, u32_as_h2(w[k]));
+      const float top = fmaxf(__low2float(h), __high2float(h));
+      lsv = fminf(fmaxf(log2f(top), -10.f), 16.f);
+      wide = lsv > 4.f;
+    } else if constexpr (FMT == kFewTq4) {
+      lsv = fminf(fmaxf(log2f(half_of(few_lds16(vsc + 2 * lane))), -60.f), 16.f);
+    }
+
+    // ---------------- online softmax (base 2)
+    float top0 = -INFINITY, top1 = -INFINITY;
+    float lg[S::kBlocks][2];
+#pragma unroll
+    for (int sub = 0; sub < S::kBlocks; ++sub) {
+      lg[sub][0] = lg[sub][1] = 0.f;
+      if constexpr (FMT != kFewBf16) {
+        lg[sub][0] = __shfl_sync(0xffffffffu, lsv, sub * 16 + g);
+        lg[sub][1] = __shfl_sync(0xffffffffu, lsv, sub * 16 + g + 8);
+      }
+      top0 = fmaxf(top0, fmaxf(s[sub][0] + lg[sub][0], s[sub][2] + lg[sub][1]));
+      top1 = fmaxf(top1, fmaxf(s[sub][1] + lg[sub][0], s[sub][3] + lg[sub][1]));
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
+      top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
+    }
+    // the reference follows when it is passed by more than 4 (p' stays below 2^4)
+    const bool up0 = top0 > m0 + 4.f, up1 = top1 > m1 + 4.f;
+    if (__any_sync(0xffffffffu, up0 || up1)) {
+      const float c0 = up0 ? fast_exp2(m0 - top0) : 1.f, c1 = up1 ? fast_exp2(m1 - top1) : 1.f;
+      if (up0) m0 = top0;
+      if (up1) m1 = top1;
+      z0 *= c0;
+      z1 *= c1;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        acc[k][0] *= c0;
+        acc[k][1] *= c1;
+        acc[k][2] *= c0;
+        acc[k][3] *= c1;
+      }
+    }
+    const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+    float p[S::kBlocks][4];
+#pragma unroll
+    for (int sub = 0; sub < S::kBlocks; ++sub) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[sub][j] = fast_exp2(s[sub][j] - (j & 1 ? u1 : u0));
+      z0 += p[sub][0] + p[sub][2];
+      z1 += p[sub][1] + p[sub][3];
+    }
+
+    // ---------------- context: value dims on M, keys on K, columns on N
+    if constexpr (FMT == kFewBf16) {
+      const int vr = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
+#pragma unroll
+      for (int sub = 0; sub < S::kBlocks; ++sub) {
+        uint32_t h01, l01, h23, l23;
+        split_bf16x2(p[sub][0], p[sub][1], h01, l01);
+        split_bf16x2(p[sub][2], p[sub][3], h23, l23);
+        const uint32_t bh0 = movmatrix_trans(h01), bl0 = movmatrix_trans(l01);
+        const uint32_t bh1 = movmatrix_trans(h23), bl1 = movmatrix_trans(l23);
+        // an infinity or NaN reaches the columns that see its key, one value at a time, and is
+        // zero to the products, where it would reach every column (0 x NaN)
+#pragma unroll 1
+        for (uint32_t left = strange[sub]; left != 0; left &= left - 1) {
+          const int r = __ffs(left) - 1;
+          const float q0 = __shfl_sync(0xffffffffu, r < 8 ? p[sub][0] : p[sub][2], (r & 7) * 4 + t);
+          const float q1 = __shfl_sync(0xffffffffu, r < 8 ? p[sub][1] : p[sub][3], (r & 7) * 4 + t);
+          const bool on0 = key_visible(key0[sub] + r, pc0, a.window, a.sinks);
+          const bool on1 = key_visible(key0[sub] + r, pc1, a.window, a.sinks);
+          const uint32_t row = vbase + (sub * 16 + r) * S::kRow;
+#pragma unroll
+          for (int mb = 0; mb < D / 16; ++mb)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w = few_lds16(row + (few_off<S::kChunks>(sub * 16 + r, 2 * mb + h) - (sub * 16 + r) * S::kRow) + 2 * g);
+              if (not_finite(w)) {
+                if (on0) acc[mb][2 * h] = fmaf(q0, __uint_as_float(w << 16), acc[mb][2 * h]);
+                if (on1) acc[mb][2 * h + 1] = fmaf(q1, __uint_as_float(w << 16), acc[mb][2 * h + 1]);
+              }
+            }
+          __syncwarp();
+          if (lane < S::kChunks) {
+            uint32_t* at = reinterpret_cast<uint32_t*>(ring + (i % S::kStages) * S::kStage + S::kPlane + (sub * 16 + r) * S::kRow) + 4 * lane;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t x = at[w];
+              at[w] = (not_finite(x & 0xFFFFu) ? 0u : x & 0xFFFFu) | (not_finite(x >> 16) ? 0u : x & 0xFFFF0000u);
+            }
+          }
+          __syncwarp();
+        }
+#pragma unroll
+        for (int mb = 0; mb < D / 16; ++mb) {
+          uint32_t av[4];
+          few_ldsm_t(vbase + sub * 16 * S::kRow + few_off<S::kChunks>(vr, 2 * mb + vc), av);
+          mma_bf16(acc[mb], av[0], av[1], av[2], av[3], bh0, bh1);
+          mma_bf16(acc[mb], av[0], av[1], av[2], av[3], bl0, bl1);
+        }
+      }
+    } else {
+      const int lr = lane & 15, lc = lane >> 4;
+      const bool any_wide = FMT == kFewQ4 && __any_sync(0xffffffffu, wide);
+#pragma unroll
+      for (int sub = 0; sub < S::kBlocks; ++sub) {
+        if constexpr (FMT == kFewTq4) {
+          const float sg = half_of(few_lds16(vsc + 2 * (sub * 16 + g))), sh = half_of(few_lds16(vsc + 2 * (sub * 16 + g + 8)));
+          p[sub][0] *= sg;
+          p[sub][1] *= sg;
+          p[sub][2] *= sh;
+          p[sub][3] *= sh;
+        } else if (any_wide) {  // (scales above 16: p in units of the key's scale, below)
+          const float eg = exp2f(rintf(lg[sub][0])), eh = exp2f(rintf(lg[sub][1]));
+          p[sub][0] *= eg;
+          p[sub][1] *= eg;
+          p[sub][2] *= eh;
+          p[sub][3] *= eh;
+        }
+        uint32_t b0 = movmatrix_trans(pack_half2(p[sub][0], p[sub][1]));
+        uint32_t b1 = movmatrix_trans(pack_half2(p[sub][2], p[sub][3]));
+        constexpr int kSW = FMT == kFewQ4 ? D / 64 : 1;
+        uint32_t sv[4][kSW];  // scales of keys 2t, 2t + 1, 2t + 8, 2t + 9
+        if constexpr (FMT == kFewQ4) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = 2 * t + (k & 1) + 8 * (k >> 1);
+            few_lds<kSW>(vsc + (sub * 16 + key) * S::kScaleRow, sv[k]);
+            if (any_wide) {
+              const float ek = exp2f(-rintf(__shfl_sync(0xffffffffu, lsv, sub * 16 + key)));
+              const __half2 e2 = __float2half2_rn(ek);
+#pragma unroll
+              for (int w = 0; w < kSW; ++w) sv[k][w] = h2_as_u32(__hmul2(u32_as_h2(sv[k][w]), e2));
+            }
+          }
+        } else if (edge || any_bad) {
+          b0 &= keep[sub][0];  // (a scale that is not a number reaches no column that does not see it)
+          b1 &= keep[sub][1];
+        }
+#pragma unroll
+        for (int u = 0; u < D / 64; ++u) {
+          uint32_t r[4];
+          few_ldsm_t(vbase + sub * 16 * S::kRow + few_off<S::kChunks>(lr, 2 * u + lc), r);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int G = 2 * u + e;
+            const uint32_t ra = r[2 * e], rb = r[2 * e + 1];  // keys 2t, 2t + 1 and 2t + 8, 2t + 9; dims 4g .. 4g + 3
+            if constexpr (FMT == kFewQ4) {
+              const uint32_t sel = e ? 0x7632u : 0x5410u;
+              uint32_t w0 = h2_as_u32(__hmul2(u32_as_h2(b0), u32_as_h2(prmt(sv[0][u], sv[1][u], sel))));
+              uint32_t w1 = h2_as_u32(__hmul2(u32_as_h2(b1), u32_as_h2(prmt(sv[2][u], sv[3][u], sel))));
+              if (edge || any_bad) {
+                w0 &= keep[sub][0];
+                w1 &= keep[sub][1];
+              }
+              const uint32_t ah = ra >> 8, bh = rb >> 8;
+              mma_f16(acc[2 * G], nib_lo_pair(ra), nib_hi_pair(ra), nib_lo_pair(rb), nib_hi_pair(rb), w0, w1);
+              mma_f16(acc[2 * G + 1], nib_lo_pair(ah), nib_hi_pair(ah), nib_lo_pair(bh), nib_hi_pair(bh), w0, w1);
+            } else {
+              const uint4 A = tq4_levels8(ra), B = tq4_levels8(rb);  // (x, y): key 2t's dims 0 .. 3, (z, w): key 2t + 1's
+              mma_f16(acc[2 * G], prmt(A.x, A.z, 0x5410u), prmt(A.x, A.z, 0x7632u), prmt(B.x, B.z, 0x5410u),
+                      prmt(B.x, B.z, 0x7632u), b0, b1);
+              mma_f16(acc[2 * G + 1], prmt(A.y, A.w, 0x5410u), prmt(A.y, A.w, 0x7632u), prmt(B.y, B.w, 0x5410u),
+                      prmt(B.y, B.w, 0x7632u), b0, b1);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+  pdl_trigger();
+
+  // ---------------- the warps' partials, folded
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    z0 += __shfl_xor_sync(0xffffffffu, z0, o);
+    z1 += __shfl_xor_sync(0xffffffffu, z1, o);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();  // every ring is done with
+  if (g == 0) {
+    sm.fm[warp][2 * t] = m0;
+    sm.fm[warp][2 * t + 1] = m1;
+    sm.fz[warp][2 * t] = z0;
+    sm.fz[warp][2 * t + 1] = z1;
+  }
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    if constexpr (FMT == kFewBf16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sm.fold[warp][2 * t + (j & 1)][16 * k + g + 8 * (j >> 1)] = acc[k][j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int dim = 32 * (k >> 1) + 4 * g + 2 * (k & 1) + (j >> 1);
+        sm.fold[warp][2 * t + (j & 1)][dim] = acc[k][j];
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 8 * D; i += WARPS * 32) {
+    const int n = i / D, e = i % D;
+    float M = -INFINITY, Z = 0.f, A = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm.fm[w][n]);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      // (a NaN sum goes on even where no score of its warp was a number)
+      const float f = sm.fm[w][n] == -INFINITY ? (sm.fz[w][n] == sm.fz[w][n] ? 0.f : NAN) : fast_exp2(sm.fm[w][n] - M);
+      Z = fmaf(sm.fz[w][n], f, Z);
+      A = fmaf(sm.fold[w][n][e], f, A);
+    }
+    sm.acc[n][e] = A;
+    if (e == 0) sm.m[n] = M, sm.z[n] = Z;
+  }
+  const uint32_t cs = cluster_size(), rank = cluster_rank();
+  if (cs > 1) cluster_sync_all();
+  else __syncthreads();
+
+  // ---------------- the cluster's partials: CTA `rank` takes every cs-th piece
+  const int range = blockIdx.x / cs, ranges = gridDim.x / cs;
+  constexpr bool kWhole = FMT == kFewTq4;  // its rotation spans the row
+  for (int item = rank * WARPS + warp; item < (kWhole ? cols : cols * NG); item += cs * WARPS) {
+    const int n = kWhole ? item : item / NG;
+    float M = -INFINITY, Z = 0.f;
+    for (uint32_t r = 0; r < cs; ++r) M = fmaxf(M, cs > 1 ? cluster_ld(&sm.m[n], r) : sm.m[n]);
+    float x[kWhole ? NG : 1] = {};
+    for (uint32_t r = 0; r < cs; ++r) {
+      const float mr = cs > 1 ? cluster_ld(&sm.m[n], r) : sm.m[n], zr = cs > 1 ? cluster_ld(&sm.z[n], r) : sm.z[n];
+      const float f = mr == -INFINITY ? (zr == zr ? 0.f : NAN) : fast_exp2(mr - M);
+      Z = fmaf(zr, f, Z);
+#pragma unroll
+      for (int k = 0; k < (kWhole ? NG : 1); ++k) {
+        const float* at = &sm.acc[n][32 * (kWhole ? k : item % NG) + lane];
+        x[k] = fmaf(cs > 1 ? cluster_ld(at, r) : *at, f, x[k]);
+      }
+    }
+    const int col = 8 * cb + n, row = sr.first + col / a.group, head = kvh * a.group + col % a.group;
+    if (ranges > 1) {
+      const int64_t part = (static_cast<int64_t>(range) * a.n_rows + row) * a.Hq + head;
+      if (lane == 0 && (kWhole || item % NG == 0)) a.ws_m[part] = M, a.ws_z[part] = Z;
+#pragma unroll
+      for (int k = 0; k < (kWhole ? NG : 1); ++k) a.ws_acc[part * D + 32 * (kWhole ? k : item % NG) + lane] = x[k];
+      continue;
+    }
+    const float inv = Z == 0.f ? 0.f : 1.f / Z;
+#pragma unroll
+    for (int k = 0; k < (kWhole ? NG : 1); ++k) x[k] *= inv;
+    if constexpr (kWhole) few_tq4_turn<(kWhole ? NG : 1)>(x, static_cast<const uint32_t*>(c.signs), lane, true);
+    else if (c.format == KVQ_FMT_Q4_HAD32) x[0] = warp_fwht32(x[0], lane) * kHadamardScale;
+#pragma unroll
+    for (int k = 0; k < (kWhole ? NG : 1); ++k)
+      few_store<FMT, D>(a, row, head, 32 * (kWhole ? k : item % NG) + lane, x[k]);
+  }
+  if (cs > 1) cluster_sync_all();  // (its shared memory is read until here)
+}
+
+// The ranges' partials of every row and head, folded in order, rotated back and rounded: a
+// warp for each.
+template <int D>
+__global__ void __launch_bounds__(128) attn_few_merge_kernel(const __grid_constant__ SeqAttnArgs a, int ranges) {
+  constexpr int NG = D / 32;
+  pdl_wait();
+  pdl_trigger();
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const SeqRows sr = seq_rows(a, blockIdx.y, false);
+  const int i = blockIdx.x * 4 + warp;
+  if (sr.state != kRowsOk || i >= sr.n * a.Hq) return;
+  const int row = sr.first + i / a.Hq, head = i % a.Hq;
+  const int64_t stride = static_cast<int64_t>(a.n_rows) * a.Hq, part = static_cast<int64_t>(row) * a.Hq + head;
+  float M = -INFINITY, Z = 0.f, x[NG] = {};
+  for (int r = lane; r < ranges; r += 32) M = fmaxf(M, a.ws_m[part + r * stride]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 4
+  for (int r = 0; r < ranges; ++r) {
+    const float mr = a.ws_m[part + r * stride], zr = a.ws_z[part + r * stride];
+    const float f = mr == -INFINITY ? (zr == zr ? 0.f : NAN) : fast_exp2(mr - M);
+    Z = fmaf(zr, f, Z);
+    const float* at = a.ws_acc + (part + r * stride) * D + lane;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) x[k] = fmaf(at[32 * k], f, x[k]);
+  }
+  const float inv = Z == 0.f ? 0.f : 1.f / Z;
+#pragma unroll
+  for (int k = 0; k < NG; ++k) x[k] *= inv;
+  if (a.c.format == KVQ_FMT_TQ4) {
+    few_tq4_turn<NG>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
+  } else if (a.c.format == KVQ_FMT_Q4_HAD32) {
+#pragma unroll
+    for (int k = 0; k < NG; ++k) x[k] = warp_fwht32(x[k], lane) * kHadamardScale;
+  }
+#pragma unroll
+  for (int k = 0; k < NG; ++k) few_store<0, D>(a, row, head, 32 * k + lane, x[k]);
+}
+
+FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
+                 int n_sm) {
+  const int group = Hq / c.num_kv_heads;
+  const int64_t blocks = static_cast<int64_t>(num_seqs) * c.num_kv_heads * ((static_cast<int64_t>(max_rows) * group + 7) / 8);
+  int64_t keys = max_seq_len;
+  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + 64 + 8 / group);
+  FewPlan p{1, 1, 4};
+  const int64_t want = std::max<int64_t>(1, (2 * static_cast<int64_t>(n_sm) + blocks - 1) / std::max<int64_t>(blocks, 1));
+  const int64_t most = std::max<int64_t>(1, keys / 128);  // a tile for every warp
+  const int64_t splits = std::min(want, most);
+  while (p.cluster < 8 && p.cluster * 2 <= splits) p.cluster *= 2;
+  p.ranges = static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(1, splits / p.cluster)));
+  return p;
+}
+
+template <int FMT, int D, int WARPS>
+static cudaError_t launch_few(const SeqAttnArgs& a, const FewPlan& p, cudaStream_t s) {
+  constexpr auto kern = attn_few_kernel<FMT, D, WARPS>;
+  const size_t smem = sizeof(FewSmem<FMT, D, WARPS>) + 128;
+  static_assert(sizeof(FewSmem<FMT, D, WARPS>) + 128 <= 232448, "shared memory");
+  cudaError_t e = set_max_smem_once<kern>(static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int64_t cbs = (static_cast<int64_t>(a.max_rows) * a.group + 7) / 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.cluster * p.ranges, static_cast<unsigned>(cbs * a.c.num_kv_heads), a.num_seqs);
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(p.cluster), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess || p.ranges == 1) return e;
+  const dim3 grid((static_cast<unsigned>(a.max_rows) * a.Hq + 3) / 4, a.num_seqs);
+  return launch_pdl(attn_few_merge_kernel<D>, grid, dim3(128), 0, s, a, p.ranges);
+}
+
+template <int FMT>
+static cudaError_t launch_few_dim(const SeqAttnArgs& a, const FewPlan& p, cudaStream_t s) {
+  switch (a.c.head_dim) {
+    case 64: return launch_few<FMT, 64, 4>(a, p, s);
+    case 128: return launch_few<FMT, 128, 4>(a, p, s);
+    default: return launch_few<FMT, 256, 4>(a, p, s);
+  }
+}
+
+cudaError_t launch_attn_few(const SeqAttnArgs& a, const FewPlan& p, cudaStream_t s) {
+  if (a.num_seqs == 0 || a.n_rows == 0 || a.max_rows == 0) return cudaSuccess;
+  if (a.c.format == KVQ_FMT_BF16) return launch_few_dim<kFewBf16>(a, p, s);
+  if (a.c.format == KVQ_FMT_TQ4) return launch_few_dim<kFewTq4>(a, p, s);
+  return launch_few_dim<kFewQ4>(a, p, s);
+}
+
+}  // namespace kvq

@@ -36,6 +36,9 @@ decltype(&kvq_merge_diff) p_merge_diff;
 decltype(&kvq_diff_heads) p_diff_heads;
 decltype(&kvq_prefill_diff_workspace_size) p_prefill_diff_workspace_size;
 decltype(&kvq_prefill_diff) p_prefill_diff;
+decltype(&kvq_attn_workspace_size) p_attn_workspace_size;
+decltype(&kvq_decode_local) p_decode_local;
+decltype(&kvq_attn_seqs) p_attn_seqs;
 PyObject* raise_status;
 
 struct Refused {  // a Python error is set
@@ -468,13 +471,65 @@ PyObject* prefill_diff(PyObject* const* a) {
   return given(a[8]) ? back(a[8]) : THPVariable_Wrap(out);
 }
 
+// attn_rows(cache, q, cu_rows or None, seq_lens, block_tables, max_rows, max_seq_len, sm_scale, window, sinks, out,
+//           dtype, workspace, status)
+// cu_rows None: one row for every sequence (decode_local).
+PyObject* attn_rows(PyObject* const* a) {
+  const at::Tensor &q = tensor(a[1], "q"), &lens = tensor(a[3], "seq_lens"), &bt = tensor(a[4], "block_tables");
+  three(q, "q");
+  const int dev = device_of(q);
+  const kvq_cache* c = cache_of(a[0], dev);
+  const bool ragged = given(a[2]);
+  const int64_t n = q.size(0), Hq = q.size(1), D = c->head_dim;
+  if (lens.dim() != 1) refuse(PyExc_ValueError, "seq_lens must be [sequences], got ", shape_of(lens.sizes()));
+  if (bt.dim() != 2) refuse(PyExc_ValueError, "block_tables must be [sequences, pages], got ", shape_of(bt.sizes()));
+  const int64_t B = lens.size(0), pages = bt.size(1);
+  if (n > INT32_MAX || B > INT32_MAX || pages > INT32_MAX) refuse(PyExc_ValueError, "too many rows, sequences or pages");
+  if (!ragged && n != B) refuse(PyExc_ValueError, "q has ", n, " rows for ", B, " sequences");
+  const kvq_rows rq = rows(q, "q", dev, n, Hq, D);
+  const int32_t* cu = ragged ? ints(tensor(a[2], "cu_rows"), "cu_rows", dev, {B + 1}) : nullptr;
+  const int32_t* ln = ints(lens, "seq_lens", dev, {B});
+  const int32_t* tables = ints(bt, "block_tables", dev, {B, pages});
+  const int32_t max_rows = ragged ? integer32(a[5], "max_rows") : 1, max_len = integer32(a[6], "max_seq_len");
+  const int32_t window = integer32(a[8], "window"), sinks = integer32(a[9], "sinks");
+  const at::Tensor out = given(a[10]) ? tensor(a[10], "out") : fresh(n, Hq, D, scalar_type(a[11], at::kFloat), dev);
+  const kvq_rows ro = rows(out, "out", dev, n, Hq, D);
+  at::Tensor ws;
+  if (given(a[12])) {
+    ws = tensor(a[12], "workspace");
+    on_device(ws, "workspace", dev);
+    if (!ws.is_contiguous()) refuse(PyExc_ValueError, "workspace must be contiguous");
+  } else {
+    const size_t bytes = p_attn_workspace_size(c, static_cast<int32_t>(n), static_cast<int32_t>(B),
+                                               static_cast<int32_t>(Hq), max_rows, max_len, window, sinks);
+    ws = at::detail::empty_cuda({static_cast<int64_t>(bytes)}, at::kByte,
+                                at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
+  }
+  const size_t ws_bytes = static_cast<size_t>(ws.numel()) * ws.element_size();
+  const float scale = real(a[7], "sm_scale");
+  int32_t* status = status_of(a[13], dev);
+  if (ragged)
+    checked(p_attn_seqs(c, &rq, static_cast<int32_t>(n), static_cast<int32_t>(B), cu, ln, tables,
+                        static_cast<int32_t>(pages), max_rows, max_len, window, sinks, scale, ws.data_ptr(), ws_bytes,
+                        &ro, status, stream_of(dev)),
+            "kvq_attn_seqs");
+  else
+    checked(p_decode_local(c, &rq, static_cast<int32_t>(B), ln, tables, static_cast<int32_t>(pages), max_len, window,
+                           sinks, scale, ws.data_ptr(), ws_bytes, &ro, status, stream_of(dev)),
+            "kvq_decode_local");
+  return given(a[10]) ? back(a[10]) : THPVariable_Wrap(out);
+}
+
 // init(addresses of the entry points, raise_status)
 PyObject* init(PyObject* const* a) {
   void** slots[] = {reinterpret_cast<void**>(&p_norm_rope), reinterpret_cast<void**>(&p_norm_rope_store),
                     reinterpret_cast<void**>(&p_load),      reinterpret_cast<void**>(&p_load_seqs),
                     reinterpret_cast<void**>(&p_merge_diff), reinterpret_cast<void**>(&p_diff_heads),
                     reinterpret_cast<void**>(&p_prefill_diff_workspace_size),
-                    reinterpret_cast<void**>(&p_prefill_diff)};
+                    reinterpret_cast<void**>(&p_prefill_diff),
+                    reinterpret_cast<void**>(&p_attn_workspace_size),
+                    reinterpret_cast<void**>(&p_decode_local),
+                    reinterpret_cast<void**>(&p_attn_seqs)};
   constexpr int kEntries = sizeof(slots) / sizeof(slots[0]);
   if (!PyTuple_Check(a[0]) || PyTuple_GET_SIZE(a[0]) != kEntries) refuse(PyExc_TypeError, "bad entry points");
   for (int i = 0; i < kEntries; ++i) *slots[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(a[0], i));
@@ -516,6 +571,7 @@ PyMethodDef methods[] = {method<init, 2>("init"),
                          method<merge_diff, 13>("merge_diff"),
                          method<diff_heads, 6>("diff_heads"),
                          method<prefill_diff, 12>("prefill_diff"),
+                         method<attn_rows, 14>("attn_rows"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kvq_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -155,6 +155,32 @@ struct NormRopeArgs {
   FastDiv ps;  // page_size
 };
 
+// Rows of several sequences over the paged cache, causal, with a window and sinks
+// (attn_few.cu).
+struct SeqAttnArgs {
+  kvq_cache c;
+  RowsView q, out;
+  const int32_t* cu_rows;  // [num_seqs + 1]; NULL: one row for every sequence
+  const int32_t* seq_lens;
+  const int32_t* block_tables;
+  int max_pages;
+  int num_seqs, n_rows, max_rows, max_seq_len;
+  int window, sinks;
+  int Hq, group;
+  float qscale;  // sm_scale * log2(e)
+  int32_t* status;
+  // more than one cluster for a block of columns: partials [ranges][n_rows][Hq], contexts
+  // [ranges][n_rows][Hq][head_dim] (unnormalised, in the cache's space)
+  float* ws_m;
+  float* ws_z;
+  float* ws_acc;
+};
+
+// How attn_few cuts the keys: `ranges` clusters of `cluster` CTAs, of 4 or 8 warps.
+struct FewPlan {
+  int cluster, ranges, warps;
+};
+
 // Rows read back (load.cu).
 struct LoadArgs {
   kvq_cache c;
@@ -243,6 +269,10 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_norm_rope(const NormRopeArgs& a, int width, int fmt, cudaStream_t s);
 // Fp8 latent rows and absorbed queries on the way into the cache (latent.cu).
 cudaError_t launch_latent(const NormRopeArgs& a, cudaStream_t s);
+// Attention of the rows of several sequences (attn_few.cu).
+FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
+                 int n_sm);
+cudaError_t launch_attn_few(const SeqAttnArgs& a, const FewPlan& p, cudaStream_t s);
 // Rows of the cache as the values they stand for (load.cu).
 cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);
 // The merge of two maps' partials with their difference, and the

@@ -1,0 +1,74 @@
+// seqs.cuh -- the rows of several sequences over a paged cache, and the keys that they
+// see: the last n rows of a sequence of T stored tokens sit at positions T - n .. T - 1,
+// and the row at position p sees key j when j <= p and, with a window, j > p - window or
+// j < sinks.  Shared by the attention kernels over ragged batches.
+#pragma once
+#include "kernels.cuh"
+
+namespace kvq {
+
+struct SeqRows {
+  int first;  // the sequence's first row in q and out
+  int n;      // its rows
+  int T;      // its stored tokens
+  int state;  // kRowsOk, or why it is not computed
+};
+enum { kRowsOk = 0, kRowsSkip = 1 /* left as they are */, kRowsNan = 2 /* NaN */ };
+
+// Sequence b's rows; bad metadata is reported by the threads with `report`.
+__device__ __forceinline__ SeqRows seq_rows(const SeqAttnArgs& a, int b, bool report) {
+  SeqRows s;
+  int last;
+  if (a.cu_rows) {
+    s.first = a.cu_rows[b];
+    last = a.cu_rows[b + 1];
+  } else {
+    s.first = b;
+    last = b + 1;
+  }
+  s.T = a.seq_lens[b];
+  s.n = last - s.first;
+  s.state = kRowsOk;
+  if (s.first < 0 || last < s.first || last > a.n_rows || s.n > a.max_rows) {
+    s.state = kRowsSkip;
+    s.n = 0;
+  } else if (s.T < 0 || s.T > a.max_seq_len || static_cast<int64_t>(s.T) > static_cast<int64_t>(a.max_pages) * a.c.page_size) {
+    s.state = kRowsNan;
+  }
+  if (s.state != kRowsOk && report) set_status(a.status, KVQ_DEV_BAD_LENGTH);
+  return s;
+}
+
+__device__ __forceinline__ bool key_visible(int key, int p, int window, int sinks) {
+  return key <= p && (window == 0 || key > p - window || key < sinks);
+}
+
+// The 16-key blocks that rows at positions p0 .. p1 (p1 >= 0) see some key of: blocks
+// 0 .. head - 1 (the sinks', where a gap lies behind them), then from `body` on; block i
+// of `count` is block_of(i).
+struct KeyBlocks {
+  int head, body, count;
+  __device__ __forceinline__ int block_of(int i) const { return i < head ? i : i - head + body; }
+};
+__device__ __forceinline__ KeyBlocks key_blocks(int p0, int p1, int window, int sinks) {
+  KeyBlocks k{0, 0, 0};
+  const int end = (p1 >> 4) + 1;
+  if (window > 0) {
+    k.head = min((sinks + 15) >> 4, end);
+    const int lo = max(p0, 0) - window + 1;
+    k.body = max(max(lo, 0) >> 4, k.head);
+  }
+  k.count = k.head + max(0, end - k.body);
+  return k;
+}
+
+// Whether every one of rows p0 .. p1 sees all keys k0 .. k0 + n - 1.
+__device__ __forceinline__ bool all_visible(int k0, int n, int p0, int p1, int window, int sinks) {
+  return k0 + n - 1 <= p0 && (window == 0 || k0 > p1 - window || k0 + n <= sinks);
+}
+// Whether some of rows p0 .. p1 sees key k (p0 <= p1).
+__device__ __forceinline__ bool any_visible(int k, int p0, int p1, int window, int sinks) {
+  return k <= p1 && (window == 0 || k > max(p0, k) - window || k < sinks);
+}
+
+}  // namespace kvq

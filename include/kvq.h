@@ -591,6 +591,51 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
                        int64_t lambda_stride, const kvq_norm* norm, float out_scale, void* out, int32_t out_dtype,
                        void* stream);
 
+/* ------------------------------------------------------------------ several sequences, windows
+ * Attention of new rows over the paged cache where a row sees less than everything, and
+ * where several sequences' rows come in one call.  A sequence's rows are its last ones:
+ * with T stored tokens (its new rows' keys among them, stored before the call) and n rows,
+ * row i sits at position p = T - n + i and sees key j when
+ *   j <= p,  and, with a window > 0,  j > p - window  or  j < sinks
+ * (the last `window` tokens, itself included, and the first `sinks` of the sequence).
+ * A row at a negative position (T < n) sees nothing and comes out as zeros.  window 0: no
+ * window, sinks make no difference.
+ * Pages of which no row sees any key are not looked at: their block-table entries may be
+ * anything (-1 for pages given back).  A row that sees a key of a page outside the pool is
+ * NaN (KVQ_DEV_BAD_PAGE), as is one that sees a key or value that is not a number; other
+ * rows are not reached by either.
+ * Any format but FP8_ROW, head_dim 64, 128 or 256, num_q_heads / num_kv_heads up to 64.
+ *   q, out: [rows][num_q_heads][head_dim], q unrotated, out rotated back and rounded once
+ *       into its type; out must not overlap q, nor its rows each other.
+ *   window, sinks >= 0; max_seq_len and max_rows bound the device's lengths and rows.
+ *   A sequence whose length is negative or above max_seq_len or its table: its rows are
+ *   NaN (KVQ_DEV_BAD_LENGTH).
+ *   workspace: device, 16-byte aligned, of kvq_attn_workspace_size bytes (NULL where that
+ *       is 0); its contents do not matter and nothing is kept in it between calls.
+ *   d_status: optional. */
+
+/* Size in bytes of the workspace of kvq_attn_seqs, and with max_rows = 1 and n_rows =
+ * num_seqs of kvq_decode_local, on the current device (0 also for a shape they refuse). */
+size_t kvq_attn_workspace_size(const kvq_cache* cache, int32_t n_rows, int32_t num_seqs, int32_t num_q_heads,
+                               int32_t max_rows, int32_t max_seq_len, int32_t window, int32_t sinks);
+
+/* kvq_decode_local -- one new row for every sequence: row b of q and out is sequence b's. */
+int32_t kvq_decode_local(const kvq_cache* cache, const kvq_rows* q, int32_t num_seqs, const int32_t* d_seq_lens,
+                         const int32_t* d_block_tables, int32_t max_pages_per_seq, int32_t max_seq_len,
+                         int32_t window, int32_t sinks, float sm_scale, void* workspace, size_t ws_bytes,
+                         const kvq_rows* out, int32_t* d_status, void* stream);
+
+/* kvq_attn_seqs -- ragged chunks: sequence b's rows are d_cu_rows[b] .. d_cu_rows[b + 1] - 1
+ * of q and out (device int32 [num_seqs + 1], ascending).
+ *   n_rows: the rows of q and out; those outside [d_cu_rows[0], d_cu_rows[num_seqs]) are
+ *   left as they were, as are those of a sequence of more than max_rows rows or whose rows
+ *   are not inside [0, n_rows) (KVQ_DEV_BAD_LENGTH). */
+int32_t kvq_attn_seqs(const kvq_cache* cache, const kvq_rows* q, int32_t n_rows, int32_t num_seqs,
+                      const int32_t* d_cu_rows, const int32_t* d_seq_lens, const int32_t* d_block_tables,
+                      int32_t max_pages_per_seq, int32_t max_rows, int32_t max_seq_len, int32_t window,
+                      int32_t sinks, float sm_scale, void* workspace, size_t ws_bytes, const kvq_rows* out,
+                      int32_t* d_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
