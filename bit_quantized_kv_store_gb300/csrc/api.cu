@@ -994,7 +994,7 @@ static int32_t check_attn_shape(const kvq_cache* c, int32_t n_rows, int32_t num_
   const int group = Hq / c->num_kv_heads;
   if (group > 64 || num_seqs > 65535 || Hq > kMaxHeads) return KVQ_ERR_UNSUPPORTED;
   // positions and row numbers are 32-bit in the kernels, with room for a window below them
-  if (max_seq_len >= (1 << 30) || n_rows >= (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+  if (max_seq_len >= (1 << 29) || n_rows >= (1 << 29)) return KVQ_ERR_UNSUPPORTED;
   a->c = *c;
   a->n_rows = n_rows;
   a->num_seqs = num_seqs;
@@ -1008,7 +1008,13 @@ static int32_t check_attn_shape(const kvq_cache* c, int32_t n_rows, int32_t num_
   return KVQ_OK;
 }
 
+// From here on a sequence's rows fill enough of a pair of CTAs (256 columns of row x query
+// head): 8 columns at a time read and convert the cache once for every 8.
+constexpr int kChunkColumns = 64;
+
 struct AttnLayout {
+  bool chunk;
+  int ranges;
   FewPlan few;
   size_t m_off, z_off, acc_off, total;
 };
@@ -1017,9 +1023,15 @@ static AttnLayout attn_layout(const SeqAttnArgs& a) {
   AttnLayout w{};
   int n_sm = device_sm_count();
   if (n_sm < 1) n_sm = 1;
-  w.few = few_plan(a.c, a.num_seqs, a.Hq, a.max_rows, a.max_seq_len, a.window, a.sinks, n_sm);
-  if (w.few.ranges > 1) {
-    const size_t n = static_cast<size_t>(w.few.ranges) * a.n_rows * a.Hq;
+  w.chunk = static_cast<int64_t>(a.max_rows) * a.group > kChunkColumns;
+  if (w.chunk) {
+    w.ranges = chunk_ranges(a.c, a.n_rows, a.num_seqs, a.Hq, a.max_rows, a.max_seq_len, a.window, a.sinks, n_sm);
+  } else {
+    w.few = few_plan(a.c, a.num_seqs, a.Hq, a.max_rows, a.max_seq_len, a.window, a.sinks, n_sm);
+    w.ranges = w.few.ranges;
+  }
+  if (w.ranges > 1) {
+    const size_t n = static_cast<size_t>(w.ranges) * a.n_rows * a.Hq;
     w.z_off = round256(n * sizeof(float));
     w.acc_off = 2 * w.z_off;
     w.total = w.acc_off + n * a.c.head_dim * sizeof(float);
@@ -1070,7 +1082,8 @@ static int32_t attn_impl(const kvq_cache* cache, const kvq_rows* q, int32_t n_ro
   a.ws_m = reinterpret_cast<float*>(ws + w.m_off);
   a.ws_z = reinterpret_cast<float*>(ws + w.z_off);
   a.ws_acc = reinterpret_cast<float*>(ws + w.acc_off);
-  cudaError_t e = launch_attn_few(a, w.few, static_cast<cudaStream_t>(stream));
+  cudaError_t e = w.chunk ? launch_attn_chunk(a, w.ranges, static_cast<cudaStream_t>(stream))
+                          : launch_attn_few(a, w.few, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : cuda_fail(e);
 }
 

@@ -1,0 +1,784 @@
+// attn_chunk.cu -- attention of many rows a sequence (prompt chunks) over the paged
+// cache, ragged, with a sliding window and sinks, every row format, on pairs of SMs
+// (tcgen05 with cta_group::2).
+//
+// For a row at position p:  o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m) over the keys j
+// that it sees (seqs.cuh), s_j = sm_scale log2(e) q . k_j, m a running reference.
+//
+// Bound by the tensor cores: 4 x rows x keys x head_dim operations against a tile of keys
+// that is read and decoded once for 256 rows.  A pair of CTAs takes 2 x floor(128 / group)
+// positions of a sequence and the query heads of one KV head, 128 rows in each CTA's
+// tensor memory, and walks the keys in tiles of 128.  B operands are shared by the pair:
+// each CTA decodes 64 of a tile's keys and, of all 128, half of the value dims, so the
+// decoding, the shared memory and its traffic are halved against one CTA alone (a product
+// of 128 x 128 reads 128 bytes a cycle of shared memory, all there is; of 256 x 128 over
+// the pair, 96).
+// Roles, per CTA: warp 0 of the first CTA issues the products (scores of tile j + 1, then
+// the context of tile j); warps 4 to 7 softmax, one row a thread; warps 8 to 11 decode
+// keys, 12 to 15 values, from global memory through registers (the next tile's codes are
+// loaded while this one's are converted) into operands without a swizzle: eight keys' 16
+// bytes make a core matrix, so eight lanes write 128 contiguous bytes.  Keys are K-major;
+// values lie with their dims contiguous (B with its columns contiguous), so neither is
+// transposed.  Scores alternate between two buffers of tensor memory; p (fp16) goes over
+// the scores it was made from and is the context product's A.
+// Queries, keys and values are fp16 here (each within 2^-12; bf16 rows: bf16, as they
+// are), a row's queries scaled by a power of two to 2^8 .. 2^9; p is fp16 (bf16), at most
+// 2^8: the softmax's reference follows when a row's scores pass it by more than 8.  Where a
+// scale above 4096 turns up (8 s may not fit fp16), the pair goes over its keys once more
+// with keys and values in units of 2^8; nobody else pays for that.
+#include <algorithm>
+#include <climits>
+
+#include "f32x2.cuh"
+#include "rows.cuh"
+#include "seqs.cuh"
+#include "tc05_pair.cuh"
+#include "tq4_levels.cuh"
+
+namespace kvq {
+
+constexpr int kCkTile = 128;    // keys of a tile: 8 blocks of 16
+constexpr int kCkThreads = 512;
+constexpr int kCkOdd = 1024;    // values that are not numbers, noted per CTA
+constexpr float kCkBigUnit = 0.00390625f;  // 2^-8: the unit of keys and values in the second pass
+enum { kCkQ4 = 0, kCkTq4 = 1, kCkBf16 = 2 };
+
+// tensor-memory columns (all 512 are allocated)
+constexpr uint32_t kCkS = 0;    // 2 x 128: scores of even and odd tiles, then p
+constexpr uint32_t kCkO = 256;  // head_dim: the output accumulator
+
+template <int D>
+struct __align__(1024) CkOperands {
+  // core matrices of 8 rows x 16 bytes: element (row, d) of q, k at (row / 8) 16 D + (d / 8) 128 + (row % 8) 16,
+  // element (key, n) of v at (n / 8) 2048 + (key / 8) 128 + (key % 8) 16, n its value dim in this CTA's half
+  uint8_t q[128 * D * 2];
+  uint8_t k[2][64 * D * 2];
+  uint8_t v[2][128 * D];
+};
+template <int D>
+struct CkSmem {
+  union {
+    CkOperands<D> op;
+    float out[128][D + 1];  // at the end: this CTA's rows
+  };
+  uint64_t k_ready[2], v_ready[2], p_ready[2];  // the first CTA's: 4 warps of each CTA arrive
+  uint64_t k_free[2], s_full[2], pv_done[2];    // each CTA's: the products arrive
+  uint64_t drained;
+  float factor[128];                            // per row: what its scores' units are worth
+  float m[128], z[128];
+  uint2 odd[kCkOdd];  // (key, dim or group and bits) of values of partly seen tiles that are not numbers
+  int odd_count, lost_lo, lost_hi;
+  int over;  // a key's or value's scale above 4096 was met
+  uint32_t tmem_base;
+  int abort;
+  int seq, block;
+};
+constexpr size_t kCkMinSmem = 120 * 1024;  // one CTA to an SM: pairs that wait for tensor memory crosswise would wait forever
+
+// Bounded wait, as the prefill's: gives up on the CTA's abort flag or after about 2 s.
+template <int D>
+__device__ __forceinline__ bool ck_wait(CkSmem<D>& sm, uint64_t* bar, uint32_t parity, int32_t* status) {
+  if (pair_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 0;; ++it) {
+    if (pair_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 31u) {
+      if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
+      if (global_timer_ns() - t0 > 2000000000ull) {
+        atomicExch(&sm.abort, 1);
+        set_status(status, KVQ_DEV_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+template <int D>
+__device__ __forceinline__ bool ck_wait_warp(CkSmem<D>& sm, uint64_t* bar, uint32_t parity, int32_t* status) {
+  return __all_sync(0xffffffffu, ck_wait(sm, bar, parity, status));
+}
+
+__device__ __forceinline__ float ck_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void ck_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void ck_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ void ck_fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void ck_sts(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ bool ck_not_finite16(uint32_t bf16) { return (bf16 & 0x7F80u) == 0x7F80u; }
+
+// Which tile of keys this is, for everybody who walks them.
+struct CkWalk {
+  KeyBlocks kb;
+  int tile0, tiles;
+  int p0, p1, window, sinks;
+  __device__ __forceinline__ int key_of(int tile, int blk) const {  // the first key of block `blk` of 8
+    const int i = (tile0 + tile) * 8 + blk;
+    return i < kb.count ? kb.block_of(i) * 16 : kNoKey;
+  }
+  // Some row does not see some key of it.
+  __device__ __forceinline__ bool edge(int tile) const {
+    const int first = key_of(tile, 0), last = key_of(tile, 7);
+    return last - first != 7 * 16 || !all_visible(first, kCkTile, p0, p1, window, sinks);
+  }
+};
+
+// 8 codes of a word as fp16 operands, times (s, s): 4-bit groups in the order 0 4 1 5 2 6 3 7,
+// TQ4 codes in their own.
+template <int FMT>
+__device__ __forceinline__ void ck_decode8(uint32_t w, __half2 s2, uint32_t (&o)[4]) {
+  if constexpr (FMT == kCkQ4) {
+    const uint32_t h = w >> 8;
+    o[0] = h2_as_u32(__hmul2(u32_as_h2(nib_lo_pair(w)), s2));
+    o[1] = h2_as_u32(__hmul2(u32_as_h2(nib_hi_pair(w)), s2));
+    o[2] = h2_as_u32(__hmul2(u32_as_h2(nib_lo_pair(h)), s2));
+    o[3] = h2_as_u32(__hmul2(u32_as_h2(nib_hi_pair(h)), s2));
+  } else {
+    const uint4 l = tq4_levels8(w);
+    o[0] = h2_as_u32(__hmul2(u32_as_h2(l.x), s2));
+    o[1] = h2_as_u32(__hmul2(u32_as_h2(l.y), s2));
+    o[2] = h2_as_u32(__hmul2(u32_as_h2(l.z), s2));
+    o[3] = h2_as_u32(__hmul2(u32_as_h2(l.w), s2));
+  }
+}
+// Where element j of 8 lies among them, and the element that lies at position i.
+template <int FMT>
+__device__ __forceinline__ int ck_pos(int j) { return FMT == kCkQ4 ? (j & 3) * 2 + (j >> 2) : j; }
+template <int FMT>
+__device__ __forceinline__ int ck_elem(int i) { return FMT == kCkQ4 ? (i >> 1) + 4 * (i & 1) : i; }
+
+// Note a value that is not a number of a key that not every row sees.
+template <int D>
+__device__ __forceinline__ void ck_note(CkSmem<D>& sm, int key, uint32_t what) {
+  const int i = atomicAdd(&sm.odd_count, 1);
+  if (i < kCkOdd) {
+    sm.odd[i] = make_uint2(static_cast<uint32_t>(key), what);
+  } else {
+    atomicMin(&sm.lost_lo, key);
+    atomicMax(&sm.lost_hi, key);
+  }
+}
+
+// ---------------------------------------------------------------- the decoders' part
+// Four warps convert one plane's part of every tile: IS_K: 64 keys (those of this CTA),
+// all dims; else 128 keys, this CTA's half of the dims.
+template <int FMT, int D, bool IS_K>
+__device__ __forceinline__ void ck_decode(const SeqAttnArgs& a, CkSmem<D>& sm, const CkWalk& wk, int kvh, int rank,
+                                          bool big) {
+  const kvq_cache& c = a.c;
+  const int tid = threadIdx.x & 127, lane = tid & 31;
+  constexpr bool kBf = FMT == kCkBf16;
+  constexpr int kKeys = IS_K ? 64 : 128;
+  constexpr int kRowChunks = kBf ? D / 8 : D / 32;               // 16-byte chunks of a row
+  constexpr int kC = IS_K ? kRowChunks : kRowChunks / 2;         // of them here
+  constexpr int kUnits = kKeys * kC / 128;                       // a thread's
+  const uint8_t* plane = static_cast<const uint8_t*>(IS_K ? c.k : c.v);
+  const uint16_t* scales = static_cast<const uint16_t*>(IS_K ? c.k_scale : c.v_scale);
+  const int chunk0 = IS_K ? 0 : rank * kC;
+  uint64_t* const ready = IS_K ? sm.k_ready : sm.v_ready;
+  uint64_t* const freed = IS_K ? sm.k_free : sm.pv_done;
+  const uint32_t ready_at[2] = {pair_addr(&ready[0], 0), pair_addr(&ready[1], 0)};
+  const uint32_t buf[2] = {smem_u32(IS_K ? sm.op.k[0] : sm.op.v[0]), smem_u32(IS_K ? sm.op.k[1] : sm.op.v[1])};
+  const int page_shift_blocks = c.page_size >> 4;
+  const int32_t* table = a.block_tables + static_cast<int64_t>(sm.seq) * a.max_pages;
+
+  // Lane l: the cache row of block l & 7 of the tile's (this CTA's four of them for keys):
+  // -1 a page outside the pool, -2 no such block.
+  auto find_rows = [&](int tile) {
+    if (tile >= wk.tiles) return -2;
+    const int key = wk.key_of(tile, IS_K ? rank * 4 + (lane & 3) : lane & 7);
+    if (key == kNoKey) return -2;
+    const int blk = key >> 4, pg = blk / page_shift_blocks;
+    const int page = table[pg];
+    if (page < 0 || page >= c.num_pages) {
+      set_status(a.status, KVQ_DEV_BAD_PAGE);
+      return -1;
+    }
+    return (page * c.num_kv_heads + kvh) * c.page_size + (blk - pg * page_shift_blocks) * 16;
+  };
+  auto unit_key = [&](int i) { return ((tid + 128 * i) / (8 * kC)) * 8 + (tid & 7); };
+  auto unit_chunk = [&](int i) { return ((tid + 128 * i) >> 3) % kC; };
+  // A unit's place among the operands (its first 16 bytes).
+  auto place = [&](int i, int sixteen) {
+    const int key = unit_key(i), n16 = unit_chunk(i) * (kBf ? 1 : 4) + sixteen;
+    return IS_K ? (key >> 3) * 16 * D + n16 * 128 + (key & 7) * 16 : n16 * 2048 + (key >> 3) * 128 + (key & 7) * 16;
+  };
+
+  if constexpr (kBf) {
+    auto fetch = [&](int tile, int rows) {  // into its buffer
+      const uint32_t at = buf[tile & 1];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int key = unit_key(i);
+        const int row0 = __shfl_sync(0xffffffffu, rows, key >> 4);
+        const uint32_t dst = at + place(i, 0);
+        if (row0 >= 0) {
+          const uint8_t* src = plane + (static_cast<int64_t>(row0) + (key & 15)) * (2 * D) + (chunk0 + unit_chunk(i)) * 16;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+        } else {
+          const uint32_t x = IS_K && row0 == -1 ? 0x7FFF7FFFu : 0u;
+          ck_sts(dst, x, x, x, x);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int rows_next = find_rows(0);
+    if (wk.tiles > 0) fetch(0, rows_next);
+    rows_next = find_rows(1);
+    for (int j = 0; j < wk.tiles; ++j) {
+      if (j + 1 < wk.tiles) {
+        if (j >= 1 && !ck_wait_warp(sm, &freed[(j + 1) & 1], ((j - 1) >> 1) & 1, a.status)) return;
+        fetch(j + 1, rows_next);
+        rows_next = find_rows(j + 2);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+      }
+      if constexpr (!IS_K) {
+        if (wk.edge(j)) {  // 0 x NaN: what not every row sees is taken out and noted
+#pragma unroll 1
+          for (int i = 0; i < kUnits; ++i) {
+            const uint32_t at = buf[j & 1] + place(i, 0);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+            bool found = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+              if (ck_not_finite16(x)) {
+                found = true;
+                const int key = unit_key(i);
+                ck_note(sm, wk.key_of(j, key >> 4) + (key & 15), static_cast<uint32_t>((chunk0 + unit_chunk(i)) * 8 + e) << 16 | x);
+                w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+              }
+            }
+            if (found) ck_sts(at, w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      ck_fence_async();
+      __syncwarp();
+      if (lane == 0) pair_arrive(ready_at[j & 1]);
+    }
+  } else {
+    uint4 code[kUnits];
+    uint32_t scale[kUnits];
+    auto load = [&](int rows) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int key = unit_key(i);
+        const int row0 = __shfl_sync(0xffffffffu, rows, key >> 4);
+        code[i] = make_uint4(0, 0, 0, 0);
+        scale[i] = IS_K && row0 == -1 ? 0x7E00u : 0u;  // a bad page's scores are NaN
+        if (row0 >= 0) {
+          const int64_t row = static_cast<int64_t>(row0) + (key & 15);
+          const int ch = chunk0 + unit_chunk(i);
+          code[i] = __ldg(reinterpret_cast<const uint4*>(plane + row * (D / 2)) + ch);
+          scale[i] = __ldg(scales + (FMT == kCkQ4 ? row * (D / 32) + ch : row));
+        }
+      }
+    };
+    load(find_rows(0));
+    int rows_next = find_rows(1);
+    const int first = big ? wk.tiles : 0;  // tiles of the pass before: buffers and barriers go on from there
+    bool over = false;
+#pragma unroll 1
+    for (int j = 0; j < wk.tiles; ++j) {
+      const int J = first + j;
+      uint4 now[kUnits];
+      uint32_t s_now[kUnits];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) now[i] = code[i], s_now[i] = scale[i];
+      if (j + 1 < wk.tiles) load(rows_next);
+      rows_next = find_rows(j + 2);
+      if constexpr (!IS_K) {
+        if (wk.edge(j)) {  // 0 x NaN: what not every row sees is taken out and noted
+#pragma unroll
+          for (int i = 0; i < kUnits; ++i)
+            if ((s_now[i] & 0x7C00u) == 0x7C00u) {
+              const int key = unit_key(i);
+              ck_note(sm, wk.key_of(j, key >> 4) + (key & 15), static_cast<uint32_t>(chunk0 + unit_chunk(i)) << 16);
+              s_now[i] = 0;
+            }
+        }
+      }
+      if (J >= 2 && !ck_wait_warp(sm, &freed[J & 1], ((J >> 1) - 1) & 1, a.status)) return;
+      const uint32_t at = buf[J & 1];
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        // (scales above 4096: products that may pass 65504; NaN is not among them)
+        over |= (s_now[i] & 0x7FFFu) > 0x6C00u && (s_now[i] & 0x7FFFu) <= 0x7C00u;
+        __half2 s2 = u32_as_h2(prmt(s_now[i], 0u, 0x1010u));
+        if (big) s2 = __hmul2(s2, __float2half2_rn(kCkBigUnit));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t o[4];
+          ck_decode8<FMT>(w == 0 ? now[i].x : w == 1 ? now[i].y : w == 2 ? now[i].z : now[i].w, s2, o);
+          ck_sts(at + place(i, w), o[0], o[1], o[2], o[3]);
+        }
+      }
+      ck_fence_async();
+      __syncwarp();
+      if (lane == 0) pair_arrive(ready_at[J & 1]);
+    }
+    if (over) sm.over = 1;
+  }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_constant__ SeqAttnArgs a) {
+  constexpr int NG = D / 32;
+  constexpr bool kBf = FMT == kCkBf16;
+  extern __shared__ uint8_t smem_raw[];
+  CkSmem<D>& sm = *reinterpret_cast<CkSmem<D>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(pair_rank());
+  const int kvh = blockIdx.y, grp = a.group, qpb = 128 / grp;
+  pdl_wait();
+
+  // ---------------- which rows: blocks of 2 qpb positions, sequence by sequence, the last
+  // (longest) of a sequence first
+  if (warp == 0) {
+    const int want = blockIdx.x >> 1;
+    const bool report = blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+    int seq = -1, block = 0, before = 0;
+    for (int b0 = 0; b0 < a.num_seqs && (seq < 0 || report); b0 += 32) {
+      int mine = 0;
+      if (b0 + lane < a.num_seqs) {
+        const SeqRows r = seq_rows(a, b0 + lane);
+        if (report && r.state != kRowsOk) set_status(a.status, KVQ_DEV_BAD_LENGTH);
+        mine = (r.n + 2 * qpb - 1) / (2 * qpb);
+      }
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const uint32_t over = __ballot_sync(0xffffffffu, before + upto > want);
+      if (seq < 0 && over != 0) {
+        const int l = __ffs(over) - 1;
+        const int last = before + __shfl_sync(0xffffffffu, upto, l) - 1;
+        seq = b0 + l;
+        block = last - want;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) sm.seq = seq, sm.block = block;
+  }
+  if (threadIdx.x == 32) {
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&sm.k_ready[h], 8);
+      mbar_init(&sm.v_ready[h], 8);
+      mbar_init(&sm.p_ready[h], 8);
+      mbar_init(&sm.k_free[h], 1);
+      mbar_init(&sm.s_full[h], 1);
+      mbar_init(&sm.pv_done[h], 1);
+    }
+    mbar_init(&sm.drained, 1);
+    sm.abort = 0;
+    sm.odd_count = 0;
+    sm.over = 0;
+    sm.lost_lo = INT_MAX;
+    sm.lost_hi = -1;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int seq = sm.seq;
+  if (seq < 0) {  // more blocks than there are (the grid is sized by a bound)
+    pdl_trigger();
+    return;
+  }
+  const SeqRows sr = seq_rows(a, seq);
+  const int base = sr.T - sr.n;
+  const int ib = sm.block * 2 * qpb, i0 = ib + rank * qpb;  // the pair's, this CTA's first row
+  const int my_rows = max(0, min(qpb, sr.n - i0)) * grp;
+  if (sr.state == kRowsNan) {
+    pdl_trigger();
+    if (blockIdx.z == 0)
+      for (int i = threadIdx.x; i < my_rows * D; i += kCkThreads) {
+        const int r = i / D;
+        seq_store(a, sr.first + i0 + r / grp, kvh * grp + r % grp, i % D, NAN);
+      }
+    return;
+  }
+  CkWalk wk;
+  wk.p0 = base + ib;
+  wk.p1 = base + min(sr.n, ib + 2 * qpb) - 1;
+  wk.window = a.window;
+  wk.sinks = a.sinks;
+  wk.kb = KeyBlocks{0, 0, 0};
+  if (wk.p1 >= 0) wk.kb = key_blocks(wk.p0, wk.p1, a.window, a.sinks);
+  const int all_tiles = (wk.kb.count + 7) / 8;
+  wk.tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * blockIdx.z / gridDim.z);
+  wk.tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (blockIdx.z + 1) / gridDim.z) - wk.tile0;
+  const int nt = wk.tiles;
+
+  if (warp == 1) pair_tmem_alloc(&sm.tmem_base, 512);
+
+  // ---------------- queries: into the cache's space, scaled, fp16 (bf16 rows: bf16)
+#pragma unroll 1
+  for (int r = warp; r < 128; r += kCkThreads / 32) {
+    float x[NG];
+    const bool live = r < my_rows;
+    const int64_t at = live ? static_cast<int64_t>(sr.first + i0 + r / grp) * a.q.ts +
+                                  static_cast<int64_t>(kvh * grp + r % grp) * a.q.hs
+                            : 0;
+#pragma unroll
+    for (int G = 0; G < NG; ++G) x[G] = live ? load_act(a.q.data, a.q.dtype, at + 32 * G + lane) : 0.f;
+    uint8_t* dst = sm.op.q + (r >> 3) * 16 * D + (r & 7) * 16 + (lane >> 3) * 128 + 2 * ck_pos<FMT>(lane & 7);
+    if constexpr (kBf) {
+      // (the scale multiplies the scores: bf16 queries enter as they are)
+#pragma unroll
+      for (int G = 0; G < NG; ++G)
+        *reinterpret_cast<__nv_bfloat16*>(dst + 512 * G) = __float2bfloat16_rn(a.qscale < 0.f ? -x[G] : x[G]);
+      if (lane == 0) sm.factor[r] = fmaxf(fabsf(a.qscale), 1e-37f);
+    } else {
+      if (a.c.format == KVQ_FMT_Q4_HAD32) {
+#pragma unroll
+        for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane) * kHadamardScale;
+      } else if (FMT == kCkTq4) {
+        tq4_turn_lanes<NG>(x, static_cast<const uint32_t*>(a.c.signs), lane, false);
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int G = 0; G < NG; ++G) {
+        x[G] *= a.qscale;
+        top = fmaxf(top, fabsf(x[G]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      int ex = 0;
+      if (top > 0.f && top < INFINITY) ex = 8 - (static_cast<int>(__float_as_uint(fmaxf(top, 1e-30f)) >> 23) - 127);
+      const float up = __uint_as_float(static_cast<uint32_t>(min(ex, 110) + 127) << 23);
+#pragma unroll
+      for (int G = 0; G < NG; ++G) *reinterpret_cast<__half*>(dst + 512 * G) = __float2half_rn(x[G] * up);
+      if (lane == 0) sm.factor[r] = 1.f / up;
+    }
+  }
+  ck_fence_async();
+  tc_fence_before();
+  __syncthreads();
+  pair_sync();  // both CTAs' queries, barriers and tensor memory
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+  const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+
+  bool big = false;  // the second pass
+  int first = 0;
+#pragma unroll 1
+  for (;;) {
+  // registers: 128 a thread at the launch; 56 + 208 + 112 + 112 of the four roles' 512 here
+  if (warp < 4) {
+    ck_regs_down<56>();
+    // ---------------- products
+    if (warp == 0 && rank == 0 && lane == 0) {
+      constexpr uint32_t id_qk = pair_idesc(kBf, false, 256, kCkTile), id_pv = pair_idesc(kBf, true, 256, D);
+      const uint64_t dq = umma_desc(smem_u32(sm.op.q), 128, 16 * D);
+      const uint64_t dk[2] = {umma_desc(smem_u32(sm.op.k[0]), 128, 16 * D), umma_desc(smem_u32(sm.op.k[1]), 128, 16 * D)};
+      const uint64_t dv[2] = {umma_desc(smem_u32(sm.op.v[0]), 128, 2048), umma_desc(smem_u32(sm.op.v[1]), 128, 2048)};
+      for (int j = 0; j <= nt; ++j) {
+        if (j < nt) {
+          const int J = first + j, b = J & 1;
+          if (!ck_wait(sm, &sm.k_ready[b], (J >> 1) & 1, a.status)) break;
+          tc_fence_after();
+          const uint32_t s = tbase + kCkS + 128 * b;
+#pragma unroll
+          for (int st = 0; st < D / 16; ++st) pair_umma_ss(s, dq + 16 * st, dk[b] + 16 * st, id_qk, st > 0 ? 1u : 0u);
+          pair_commit(&sm.k_free[b]);
+          pair_commit(&sm.s_full[b]);
+        }
+        if (j >= 1) {
+          const int jp = j - 1, J = first + jp, b = J & 1;
+          if (!ck_wait(sm, &sm.v_ready[b], (J >> 1) & 1, a.status)) break;
+          if (!ck_wait(sm, &sm.p_ready[b], (J >> 1) & 1, a.status)) break;
+          tc_fence_after();
+          const uint32_t p = tbase + kCkS + 128 * b;
+#pragma unroll
+          for (int st = 0; st < kCkTile / 16; ++st)
+            pair_umma_ts(tbase + kCkO, p + 8 * st, dv[b] + 16 * st, id_pv, jp > 0 || st > 0 ? 1u : 0u);
+          pair_commit(&sm.pv_done[b]);
+        }
+      }
+      // every product issued has finished before the operands and the tensor memory go
+      // (bounded, and independent of the abort flag)
+      pair_commit(&sm.drained);
+      const uint64_t t0 = global_timer_ns();
+      while (!pair_try_wait(&sm.drained, big ? 1 : 0)) {
+        if (global_timer_ns() - t0 > 2000000000ull) {
+          atomicExch(&sm.abort, 1);
+          set_status(a.status, KVQ_DEV_TIMEOUT);
+          break;
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ---------------- softmax, one row a thread
+    ck_regs_up<208>();
+    const int r = 32 * (warp & 3) + lane;
+    const int p = r < my_rows ? base + i0 + r / grp : -kNoKey;
+    const float f = sm.factor[r] * (big ? 1.f / kCkBigUnit : 1.f);
+    const uint32_t ready_at[2] = {pair_addr(&sm.p_ready[0], 0), pair_addr(&sm.p_ready[1], 0)};
+    float m_run = -INFINITY, z = 0.f;
+    for (int j = 0; j < nt; ++j) {
+      const int J = first + j, b = J & 1;
+      if (!ck_wait_warp(sm, &sm.s_full[b], (J >> 1) & 1, a.status)) break;
+      tc_fence_after();
+      const uint32_t s_at = tbase + lane_off + kCkS + 128 * b;
+      const bool edge = wk.edge(j);
+      uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};  // of the tile's keys
+      if (edge) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int key = wk.key_of(j, k);
+          auto below = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u; };
+          uint32_t bits = below(p - key + 1);
+          if (a.window > 0) bits &= ~below(p - a.window - key + 1) | below(a.sinks - key);
+          seen[k >> 1] = (seen[k >> 1] & (k & 1 ? 0x0000FFFFu : 0xFFFF0000u)) | bits << (16 * (k & 1));
+        }
+      }
+      uint32_t v[128];
+      tmem_ld32(s_at, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+      tmem_ld32(s_at + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+      tmem_ld32(s_at + 64, reinterpret_cast<uint32_t(&)[32]>(v[64]));
+      tmem_ld32(s_at + 96, reinterpret_cast<uint32_t(&)[32]>(v[96]));
+      tmem_wait_ld();
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (!((seen[i >> 5] >> (i & 31)) & 1u)) v[i] = 0xFF800000u;
+      }
+      float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < 128; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) t4[k] = ck_max3(t4[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+      float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+      if (top != -INFINITY) top *= f;
+      const bool raise = top > m_run + 8.f;
+      float corr = 1.f;
+      if (raise) {
+        corr = m_run == -INFINITY ? 1.f : fast_exp2(m_run - top);  // (z and the context are zero until then)
+        z *= corr;
+        m_run = top;
+      }
+      const float mu = m_run == -INFINITY ? 0.f : m_run;
+      if (j > 0 && __any_sync(0xffffffffu, raise && corr != 1.f)) {
+        if (!ck_wait_warp(sm, &sm.pv_done[(J - 1) & 1], ((J - 1) >> 1) & 1, a.status)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int cc = 0; cc < D / 16; ++cc) {
+          uint32_t o[16];
+          tmem_ld16(tbase + lane_off + kCkO + 16 * cc, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+          tmem_st16(tbase + lane_off + kCkO + 16 * cc, o);
+        }
+        tmem_wait_st();
+      }
+      const uint64_t f2 = pk2(f, f), mu2 = pk2(-mu, -mu);
+      uint64_t z2[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        float e0, e1;
+        upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, mu2), e0, e1);
+        e0 = fast_exp2(e0);
+        e1 = fast_exp2(e1);
+        z2[i & 1] = add2(z2[i & 1], pk2(e0, e1));
+        v[i] = kBf ? pack_bf16(e0, e1) : pack_half2(e0, e1);
+        if (i == 31) tmem_st32(s_at, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+      }
+      tmem_st32(s_at + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+      {
+        float e0, e1;
+        upk2(add2(z2[0], z2[1]), e0, e1);
+        z += e0 + e1;
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) pair_arrive(ready_at[b]);
+    }
+    sm.m[r] = m_run;
+    sm.z[r] = z;
+    const int last = first + nt - 1;
+    if (nt > 0) ck_wait_warp(sm, &sm.pv_done[last & 1], (last >> 1) & 1, a.status);
+    ck_regs_down<128>();
+  } else {
+    ck_regs_down<112>();
+    if (warp < 12) ck_decode<FMT, D, true>(a, sm, wk, kvh, rank, big);
+    else ck_decode<FMT, D, false>(a, sm, wk, kvh, rank, big);
+  }
+  // (nobody takes registers back before the softmax warps have had theirs: a warpgroup with
+  // nothing to do would otherwise leave them waiting for ever)
+  __syncwarp();
+  __syncthreads();
+  if (warp < 4) ck_regs_up<128>();
+  if (warp >= 8) ck_regs_up<128>();
+  if constexpr (!kBf) {
+    if (big) break;
+    __syncwarp();
+    tc_fence_before();
+    pair_sync();
+    tc_fence_after();
+    big = (pair_ld_u32(pair_addr(&sm.over, 0)) | pair_ld_u32(pair_addr(&sm.over, 1))) != 0;
+    if (!big) break;
+    first = nt;
+    if (threadIdx.x == 0) sm.odd_count = 0, sm.lost_lo = INT_MAX, sm.lost_hi = -1;
+    pair_sync();
+  } else {
+    break;
+  }
+  }
+
+  // ---------------- the rows: out of tensor memory, over the operands, rotated back, stored
+  pdl_trigger();
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();  // every product has finished (the softmax warps waited for the last)
+  tc_fence_after();
+  const int ranges = gridDim.z;
+  {
+    const int r = 32 * (warp & 3) + lane, part = warp >> 2;
+    const float zr = sm.z[r];
+    const float unit = big ? 1.f / kCkBigUnit : 1.f;
+    const float inv = sm.abort ? NAN : ranges > 1 ? unit : zr == 0.f ? 0.f : unit / zr;
+#pragma unroll 1
+    for (int cc = 0; cc < D / 64; ++cc) {
+      const int col = part * (D / 4) + 16 * cc;
+      uint32_t o[16];
+      if (nt > 0) {
+        tmem_ld16(tbase + lane_off + kCkO + col, o);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sm.out[r][col + (i & 8) + ck_elem<FMT>(i & 7)] = __uint_as_float(o[i]) * inv;
+    }
+  }
+  tc_fence_before();
+  pair_sync();  // both CTAs' rows and notes; nobody needs the tensor memory any more
+  if (warp == 1) pair_tmem_dealloc(tbase, 512);
+  // values that are not numbers, into the rows that see their keys
+  for (int other = 0; other < 2; ++other) {
+    const int count = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd_count, other)));
+    if (count == 0) continue;
+    for (int r = threadIdx.x; r < my_rows; r += kCkThreads) {
+      const int p = base + i0 + r / grp;
+      for (int i = 0; i < min(count, kCkOdd); ++i) {
+        const int key = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd[i].x, other)));
+        if (!key_visible(key, p, a.window, a.sinks)) continue;
+        const uint32_t what = pair_ld_u32(pair_addr(&sm.odd[i].y, other));
+        if constexpr (kBf) {
+          sm.out[r][what >> 16] += __uint_as_float(what << 16);
+        } else {
+          for (int e = 0; e < 32; ++e) sm.out[r][(what >> 16) * 32 + e] = NAN;
+        }
+      }
+      if (count > kCkOdd) {
+        // those that found no room: rows that see a key between the first and the last of them
+        const int lo = static_cast<int>(pair_ld_u32(pair_addr(&sm.lost_lo, other)));
+        const int hi = static_cast<int>(pair_ld_u32(pair_addr(&sm.lost_hi, other)));
+        bool hit = false;
+        for (int key = lo; key <= hi && !hit; ++key) hit = key_visible(key, p, a.window, a.sinks);
+        if (hit)
+          for (int e = 0; e < D; ++e) sm.out[r][e] = NAN;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int r = warp; r < my_rows; r += kCkThreads / 32) {
+    float x[NG];
+#pragma unroll
+    for (int G = 0; G < NG; ++G) x[G] = sm.out[r][32 * G + lane];
+    const int row = sr.first + i0 + r / grp, head = kvh * grp + r % grp;
+    if (ranges > 1) {
+      const int64_t at = (static_cast<int64_t>(blockIdx.z) * a.n_rows + row) * a.Hq + head;
+      if (lane == 0) a.ws_m[at] = sm.m[r], a.ws_z[at] = sm.z[r];
+#pragma unroll
+      for (int G = 0; G < NG; ++G) a.ws_acc[at * D + 32 * G + lane] = x[G];
+      continue;
+    }
+    if (a.c.format == KVQ_FMT_Q4_HAD32) {
+#pragma unroll
+      for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane) * kHadamardScale;
+    } else if (FMT == kCkTq4) {
+      tq4_turn_lanes<NG>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
+    }
+#pragma unroll
+    for (int G = 0; G < NG; ++G) seq_store(a, row, head, 32 * G + lane, x[G]);
+  }
+  pair_sync();  // (its notes are read until here)
+}
+
+// The pairs of CTAs of a call, by a bound: sequences' blocks are whole.
+static int64_t chunk_blocks(int n_rows, int num_seqs, int max_rows, int group) {
+  const int64_t per = 2 * (128 / group);
+  return std::min<int64_t>((max_rows + per - 1) / per * num_seqs, n_rows / per + num_seqs);
+}
+
+int chunk_ranges(const kvq_cache& c, int n_rows, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
+                 int n_sm) {
+  const int group = Hq / c.num_kv_heads;
+  const int64_t items = chunk_blocks(n_rows, num_seqs, max_rows, group) * c.num_kv_heads;
+  int64_t keys = max_seq_len;
+  if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + std::min(max_rows, 256 / group) + 32);
+  const int64_t tiles = (keys + kCkTile - 1) / kCkTile;
+  const int64_t pairs = std::max(1, n_sm / 2);
+  if (items <= 0 || 2 * items > pairs) return 1;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(pairs / items, tiles / 4), 32)));
+}
+
+template <int FMT, int D>
+static cudaError_t launch_chunk(const SeqAttnArgs& a, int ranges, cudaStream_t s) {
+  constexpr auto kern = attn_chunk_kernel<FMT, D>;
+  constexpr size_t smem = std::max(sizeof(CkSmem<D>) + 1024, kCkMinSmem);
+  static_assert(smem <= 232448, "shared memory");
+  cudaError_t e = set_max_smem_once<kern>(static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * chunk_blocks(a.n_rows, a.num_seqs, a.max_rows, a.group)), a.c.num_kv_heads,
+                     ranges);
+  cfg.blockDim = dim3(kCkThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess || ranges == 1) return e;
+  return launch_attn_merge(a, ranges, s);
+}
+
+template <int FMT>
+static cudaError_t launch_chunk_dim(const SeqAttnArgs& a, int ranges, cudaStream_t s) {
+  switch (a.c.head_dim) {
+    case 64: return launch_chunk<FMT, 64>(a, ranges, s);
+    case 128: return launch_chunk<FMT, 128>(a, ranges, s);
+    default: return launch_chunk<FMT, 256>(a, ranges, s);
+  }
+}
+
+cudaError_t launch_attn_chunk(const SeqAttnArgs& a, int ranges, cudaStream_t s) {
+  if (a.num_seqs == 0 || a.n_rows == 0 || a.max_rows == 0) return cudaSuccess;
+  if (a.c.format == KVQ_FMT_BF16) return launch_chunk_dim<kCkBf16>(a, ranges, s);
+  if (a.c.format == KVQ_FMT_TQ4) return launch_chunk_dim<kCkTq4>(a, ranges, s);
+  return launch_chunk_dim<kCkQ4>(a, ranges, s);
+}
+
+}  // namespace kvq

@@ -148,44 +148,6 @@ __device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, u
   lo = pack_bf16(x0 - f.x, x1 - f.y);
 }
 
-// The D-point signed transform of a row whose element 32 G + lane is x[G].
-template <int NG>
-__device__ __forceinline__ void few_tq4_turn(float (&x)[NG], const uint32_t* signs, int lane, bool inverse) {
-  if (!inverse) {
-#pragma unroll
-    for (int G = 0; G < NG; ++G)
-      if ((signs[G] >> lane) & 1u) x[G] = -x[G];
-  }
-#pragma unroll
-  for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane);
-#pragma unroll
-  for (int h = 1; h < NG; h <<= 1)
-#pragma unroll
-    for (int G = 0; G < NG; ++G)
-      if (!(G & h)) {
-        const float u = x[G], v = x[G + h];
-        x[G] = u + v;
-        x[G + h] = u - v;
-      }
-  const float c = NG == 8 ? 0.0625f : NG == 4 ? 0.08838834764831845f : 0.125f;
-#pragma unroll
-  for (int G = 0; G < NG; ++G) x[G] *= c;
-  if (inverse) {
-#pragma unroll
-    for (int G = 0; G < NG; ++G)
-      if ((signs[G] >> lane) & 1u) x[G] = -x[G];
-  }
-}
-
-// Rows of columns: column 8 cb + n of a sequence is row (8 cb + n) / group, query head
-// (8 cb + n) % group of the KV head.
-template <int FMT, int D>
-__device__ __forceinline__ void few_store(const SeqAttnArgs& a, int row, int head, int e, float y) {
-  const int64_t at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + e;
-  if (a.out.dtype == KVQ_DT_F32) static_cast<float*>(a.out.data)[at] = y;
-  else static_cast<__nv_bfloat16*>(a.out.data)[at] = __float2bfloat16_rn(y);
-}
-
 template <int FMT, int D, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_constant__ SeqAttnArgs a) {
   using S = FewShape<FMT, D>;
@@ -199,11 +161,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
   const int b = blockIdx.z, kvh = blockIdx.y % c.num_kv_heads, cb = blockIdx.y / c.num_kv_heads;
 
   // what the sequence's rows see (metadata only: before the kernel in front is done)
-  const SeqRows sr = seq_rows(a, b, blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0);
+  const SeqRows sr = seq_rows(a, b);
   const int cols = min(8, sr.n * a.group - 8 * cb);
   if (cols <= 0 || sr.state == kRowsSkip) {
     pdl_wait();
     pdl_trigger();
+    if (sr.state != kRowsOk && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+      set_status(a.status, KVQ_DEV_BAD_LENGTH);
     return;
   }
   const int base = sr.T - sr.n;  // position of the sequence's row 0
@@ -211,10 +175,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
   if (sr.state == kRowsNan) {
     pdl_wait();
     pdl_trigger();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, KVQ_DEV_BAD_LENGTH);
     if (blockIdx.x == 0)
       for (int i = threadIdx.x; i < cols * D; i += WARPS * 32) {
         const int col = 8 * cb + i / D;
-        few_store<FMT, D>(a, sr.first + col / a.group, kvh * a.group + col % a.group, i % D, NAN);
+        seq_store(a, sr.first + col / a.group, kvh * a.group + col % a.group, i % D, NAN);
       }
     return;
   }
@@ -288,7 +253,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
 #pragma unroll
       for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane) * kHadamardScale;
     } else if (FMT == kFewTq4) {
-      few_tq4_turn<NG>(x, static_cast<const uint32_t*>(c.signs), lane, false);
+      tq4_turn_lanes<NG>(x, static_cast<const uint32_t*>(c.signs), lane, false);
     }
     float top = 0.f;
 #pragma unroll
@@ -347,7 +312,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
   const uint32_t qf = smem_u32(&sm.qf[0][lane]);
   const float f0 = sm.factor[2 * t], f1 = sm.factor[2 * t + 1];
   // positions of columns 2t, 2t + 1 and g (before any key where there is no such column)
-  auto pos_of = [&](int n) { return n < cols ? base + (8 * cb + n) / a.group : INT_MIN / 2; };
+  auto pos_of = [&](int n) { return n < cols ? base + (8 * cb + n) / a.group : -kNoKey; };
   const int pc0 = pos_of(2 * t), pc1 = pos_of(2 * t + 1), pcg = pos_of(g);
 
   float acc[D / 16][4];
@@ -379,7 +344,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
     bool edge = false;  // some key that some column does not see
 #pragma unroll
     for (int sub = 0; sub < S::kBlocks; ++sub) {
-      key0[sub] = blk0 + sub < kb.count ? kb.block_of(blk0 + sub) * 16 : INT_MAX / 2;
+      key0[sub] = blk0 + sub < kb.count ? kb.block_of(blk0 + sub) * 16 : kNoKey;
       edge |= !all_visible(key0[sub], 16, p0, p1, a.window, a.sinks);
     }
 
@@ -789,11 +754,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
     const float inv = Z == 0.f ? 0.f : 1.f / Z;
 #pragma unroll
     for (int k = 0; k < (kWhole ? NG : 1); ++k) x[k] *= inv;
-    if constexpr (kWhole) few_tq4_turn<(kWhole ? NG : 1)>(x, static_cast<const uint32_t*>(c.signs), lane, true);
+    if constexpr (kWhole) tq4_turn_lanes<(kWhole ? NG : 1)>(x, static_cast<const uint32_t*>(c.signs), lane, true);
     else if (c.format == KVQ_FMT_Q4_HAD32) x[0] = warp_fwht32(x[0], lane) * kHadamardScale;
 #pragma unroll
     for (int k = 0; k < (kWhole ? NG : 1); ++k)
-      few_store<FMT, D>(a, row, head, 32 * (kWhole ? k : item % NG) + lane, x[k]);
+      seq_store(a, row, head, 32 * (kWhole ? k : item % NG) + lane, x[k]);
   }
   if (cs > 1) cluster_sync_all();  // (its shared memory is read until here)
 }
@@ -801,12 +766,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
 // The ranges' partials of every row and head, folded in order, rotated back and rounded: a
 // warp for each.
 template <int D>
-__global__ void __launch_bounds__(128) attn_few_merge_kernel(const __grid_constant__ SeqAttnArgs a, int ranges) {
+__global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__ SeqAttnArgs a, int ranges) {
   constexpr int NG = D / 32;
   pdl_wait();
   pdl_trigger();
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const SeqRows sr = seq_rows(a, blockIdx.y, false);
+  const SeqRows sr = seq_rows(a, blockIdx.y);
   const int i = blockIdx.x * 4 + warp;
   if (sr.state != kRowsOk || i >= sr.n * a.Hq) return;
   const int row = sr.first + i / a.Hq, head = i % a.Hq;
@@ -828,13 +793,22 @@ __global__ void __launch_bounds__(128) attn_few_merge_kernel(const __grid_consta
 #pragma unroll
   for (int k = 0; k < NG; ++k) x[k] *= inv;
   if (a.c.format == KVQ_FMT_TQ4) {
-    few_tq4_turn<NG>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
+    tq4_turn_lanes<NG>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
   } else if (a.c.format == KVQ_FMT_Q4_HAD32) {
 #pragma unroll
     for (int k = 0; k < NG; ++k) x[k] = warp_fwht32(x[k], lane) * kHadamardScale;
   }
 #pragma unroll
-  for (int k = 0; k < NG; ++k) few_store<0, D>(a, row, head, 32 * k + lane, x[k]);
+  for (int k = 0; k < NG; ++k) seq_store(a, row, head, 32 * k + lane, x[k]);
+}
+
+cudaError_t launch_attn_merge(const SeqAttnArgs& a, int ranges, cudaStream_t s) {
+  const dim3 grid((static_cast<unsigned>(a.max_rows) * a.Hq + 3) / 4, a.num_seqs);
+  switch (a.c.head_dim) {
+    case 64: return launch_pdl(attn_merge_kernel<64>, grid, dim3(128), 0, s, a, ranges);
+    case 128: return launch_pdl(attn_merge_kernel<128>, grid, dim3(128), 0, s, a, ranges);
+    default: return launch_pdl(attn_merge_kernel<256>, grid, dim3(128), 0, s, a, ranges);
+  }
 }
 
 FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
@@ -874,8 +848,7 @@ static cudaError_t launch_few(const SeqAttnArgs& a, const FewPlan& p, cudaStream
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, kern, a);
   if (e != cudaSuccess || p.ranges == 1) return e;
-  const dim3 grid((static_cast<unsigned>(a.max_rows) * a.Hq + 3) / 4, a.num_seqs);
-  return launch_pdl(attn_few_merge_kernel<D>, grid, dim3(128), 0, s, a, p.ranges);
+  return launch_attn_merge(a, p.ranges, s);
 }
 
 template <int FMT>

@@ -156,7 +156,7 @@ struct NormRopeArgs {
 };
 
 // Rows of several sequences over the paged cache, causal, with a window and sinks
-// (attn_few.cu).
+// (attn_few.cu, attn_chunk.cu).
 struct SeqAttnArgs {
   kvq_cache c;
   RowsView q, out;
@@ -273,6 +273,12 @@ cudaError_t launch_latent(const NormRopeArgs& a, cudaStream_t s);
 FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
                  int n_sm);
 cudaError_t launch_attn_few(const SeqAttnArgs& a, const FewPlan& p, cudaStream_t s);
+// The fold of their partials, and of those of the next.
+cudaError_t launch_attn_merge(const SeqAttnArgs& a, int ranges, cudaStream_t s);
+// Many rows a sequence (attn_chunk.cu), and into how many ranges the keys are cut.
+int chunk_ranges(const kvq_cache& c, int n_rows, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
+                 int n_sm);
+cudaError_t launch_attn_chunk(const SeqAttnArgs& a, int ranges, cudaStream_t s);
 // Rows of the cache as the values they stand for (load.cu).
 cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);
 // The merge of two maps' partials with their difference, and the

@@ -15,8 +15,11 @@ struct SeqRows {
 };
 enum { kRowsOk = 0, kRowsSkip = 1 /* left as they are */, kRowsNan = 2 /* NaN */ };
 
-// Sequence b's rows; bad metadata is reported by the threads with `report`.
-__device__ __forceinline__ SeqRows seq_rows(const SeqAttnArgs& a, int b, bool report) {
+// Behind every key and (negative) before every position; lengths and rows stay below it.
+constexpr int kNoKey = 1 << 29;
+
+// Sequence b's rows.
+__device__ __forceinline__ SeqRows seq_rows(const SeqAttnArgs& a, int b) {
   SeqRows s;
   int last;
   if (a.cu_rows) {
@@ -35,7 +38,6 @@ __device__ __forceinline__ SeqRows seq_rows(const SeqAttnArgs& a, int b, bool re
   } else if (s.T < 0 || s.T > a.max_seq_len || static_cast<int64_t>(s.T) > static_cast<int64_t>(a.max_pages) * a.c.page_size) {
     s.state = kRowsNan;
   }
-  if (s.state != kRowsOk && report) set_status(a.status, KVQ_DEV_BAD_LENGTH);
   return s;
 }
 
@@ -69,6 +71,42 @@ __device__ __forceinline__ bool all_visible(int k0, int n, int p0, int p1, int w
 // Whether some of rows p0 .. p1 sees key k (p0 <= p1).
 __device__ __forceinline__ bool any_visible(int k, int p0, int p1, int window, int sinks) {
   return k <= p1 && (window == 0 || k > max(p0, k) - window || k < sinks);
+}
+
+// The D-point signed transform of a row whose element 32 G + lane is x[G].
+template <int NG>
+__device__ __forceinline__ void tq4_turn_lanes(float (&x)[NG], const uint32_t* signs, int lane, bool inverse) {
+  if (!inverse) {
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+      if ((signs[G] >> lane) & 1u) x[G] = -x[G];
+  }
+#pragma unroll
+  for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane);
+#pragma unroll
+  for (int h = 1; h < NG; h <<= 1)
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+      if (!(G & h)) {
+        const float u = x[G], v = x[G + h];
+        x[G] = u + v;
+        x[G + h] = u - v;
+      }
+  const float c = NG == 8 ? 0.0625f : NG == 4 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+  for (int G = 0; G < NG; ++G) x[G] *= c;
+  if (inverse) {
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+      if ((signs[G] >> lane) & 1u) x[G] = -x[G];
+  }
+}
+
+// One output value, rounded into its type.
+__device__ __forceinline__ void seq_store(const SeqAttnArgs& a, int row, int head, int e, float y) {
+  const int64_t at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + e;
+  if (a.out.dtype == KVQ_DT_F32) static_cast<float*>(a.out.data)[at] = y;
+  else static_cast<__nv_bfloat16*>(a.out.data)[at] = __float2bfloat16_rn(y);
 }
 
 }  // namespace kvq

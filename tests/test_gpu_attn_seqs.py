@@ -25,6 +25,8 @@ from tests.test_gpu_parity import K  # noqa: F401
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+LEVELS = (0.12841796875, 0.387939453125, 0.65673828125, 0.9423828125, 1.255859375, 1.6181640625, 2.068359375,
+          2.732421875)
 FMTS = {"q4_had32": 0, "bf16": 1, "q4_0": 3, "tq4": 4}
 
 
@@ -124,11 +126,21 @@ class Batch:
                 out[self.cu[b]:self.cu[b + 1], h] = o
                 half = 2.0 ** -9 if self.fmt == "bf16" else 2.0 ** -12
                 u2 = half ** 2 / 3
-                s2 = (qh ** 2) @ (kh ** 2).T * self.scale ** 2 * 2 * u2  # of a score: q and k rounded
+                s2 = (qh ** 2) @ (kh ** 2).T * 2  # of a score: q and k rounded
+                if self.fmt == "tq4":
+                    # level x scale: a rounding is one for all elements of a row with that level, +-
+                    pg = self.table[b].long()[key // self.ps]
+                    mag = kh.abs() / self.cache.k_scale[pg, h // self.group, key % self.ps].double()[:, None]
+                    s2 = s2 / 2 + sum((qh @ torch.where((mag - m).abs() < 1e-2, kh, 0.0).T) ** 2 for m in LEVELS)
+                s2 = s2 * self.scale ** 2 * u2
                 s2 = torch.where(seen, s2, 0.0)
                 # a relative error of a score's p_j moves the output by w_j (v_j - o), one of p' alone by w_j v_j
                 m = (w ** 2 * s2) @ vo ** 2 - 2 * o * ((w ** 2 * s2) @ vo) + o ** 2 * (w ** 2 * s2).sum(-1, keepdim=True)
-                var[self.cu[b]:self.cu[b + 1], h] = m.clamp(min=0) + (w ** 2 @ vo ** 2) * 2 * u2 + self.mix(w ** 2 @ vh ** 2) * u2
+                own = self.mix(w ** 2 @ vh ** 2)
+                if self.fmt == "tq4":  # (as for keys)
+                    mag = vh.abs() / self.cache.v_scale[pg, h // self.group, key % self.ps].double()[:, None]
+                    own = w ** 2 @ sum(self.turn(torch.where((mag - m_).abs() < 1e-2, vh, 0.0), inverse=True) ** 2 for m_ in LEVELS)
+                var[self.cu[b]:self.cu[b + 1], h] = m.clamp(min=0) + (w ** 2 @ vo ** 2) * 2 * u2 + own * u2
         return out, var
 
     def check(self, got, window=0, sinks=0, rows=None):
