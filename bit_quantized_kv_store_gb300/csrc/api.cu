@@ -1070,7 +1070,7 @@ static int32_t attn_impl(const kvq_cache* cache, const kvq_rows* q, int32_t n_ro
   const AttnLayout w = attn_layout(a);
   if (w.total > 0) {
     if (ws_bytes < w.total) return KVQ_ERR_WORKSPACE_TOO_SMALL;
-    if (!workspace || !aligned16(workspace)) return KVQ_ERR_INVALID_ARG;
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 32 != 0) return KVQ_ERR_INVALID_ARG;
   }
   a.cu_rows = d_cu_rows;
   a.seq_lens = d_seq_lens;

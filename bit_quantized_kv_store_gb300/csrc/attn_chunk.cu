@@ -61,7 +61,8 @@ struct CkSmem {
     CkOperands<D> op;
     float out[128][D + 1];  // at the end: this CTA's rows
   };
-  uint64_t k_ready[2], v_ready[2], p_ready[2];  // the first CTA's: 4 warps of each CTA arrive
+  // the CTA's 4 warps (q_ready: 8) arrive, and at the first CTA's the second's forwarder
+  uint64_t k_ready[2], v_ready[2], p_ready[2], q_ready;
   uint64_t k_free[2], s_full[2], pv_done[2];    // each CTA's: the products arrive
   uint64_t drained;
   float factor[128];                            // per row: what its scores' units are worth
@@ -75,13 +76,15 @@ struct CkSmem {
 };
 constexpr size_t kCkMinSmem = 120 * 1024;  // one CTA to an SM: pairs that wait for tensor memory crosswise would wait forever
 
-// Bounded wait, as the prefill's: gives up on the CTA's abort flag or after about 2 s.
-template <int D>
+// Bounded wait, as the prefill's: gives up on the CTA's abort flag or after about 2 s.  PAIR:
+// what the other CTA did before it arrived is visible, too.
+template <bool PAIR = false, int D>
 __device__ __forceinline__ bool ck_wait(CkSmem<D>& sm, uint64_t* bar, uint32_t parity, int32_t* status) {
-  if (pair_try_wait(bar, parity)) return true;
+  auto done = [&] { return PAIR ? pair_try_wait(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 0;; ++it) {
-    if (pair_try_wait(bar, parity)) return true;
+    if (done()) return true;
     if ((it & 31u) == 31u) {
       if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
       if (global_timer_ns() - t0 > 2000000000ull) {
@@ -102,11 +105,6 @@ __device__ __forceinline__ float ck_max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-template <int N>
-__device__ __forceinline__ void ck_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void ck_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-__device__ __forceinline__ void ck_fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void ck_sts(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -152,6 +150,102 @@ __device__ __forceinline__ int ck_pos(int j) { return FMT == kCkQ4 ? (j & 3) * 2
 template <int FMT>
 __device__ __forceinline__ int ck_elem(int i) { return FMT == kCkQ4 ? (i >> 1) + 4 * (i & 1) : i; }
 
+// 8 values of every group of 32 of a row, the first of them element `at` of the view (< 0:
+// zeros).
+template <int NG>
+__device__ __forceinline__ void ck_load_row(const RowsView& v, int64_t at, float (&x)[NG][8]) {
+  if (at < 0) {
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[G][e] = 0.f;
+  } else if (v.dtype == KVQ_DT_BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(v.data) + at;
+    uint32_t w[NG][4];
+#pragma unroll
+    for (int G = 0; G < NG; ++G) {
+      if (v.wide) {
+        ld_words<4>(p + 32 * G, w[G]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[G][i] = p[32 * G + 2 * i] | static_cast<uint32_t>(p[32 * G + 2 * i + 1]) << 16;
+      }
+    }
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[G][2 * i] = __uint_as_float(w[G][i] << 16);
+        x[G][2 * i + 1] = __uint_as_float(w[G][i] & 0xFFFF0000u);
+      }
+  } else {
+    const float* p = static_cast<const float*>(v.data) + at;
+#pragma unroll
+    for (int G = 0; G < NG; ++G) {
+      if (v.wide) {
+        ld_words<8>(p + 32 * G, reinterpret_cast<uint32_t*>(x[G]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[G][e] = p[32 * G + e];
+      }
+    }
+  }
+}
+
+// The rows' rotation (ALL: the D-point one with signs, else each group's), for rows whose
+// elements 32 G + 8 (lane >> 3) + e are x[G][e].
+template <int NG, bool ALL>
+__device__ __forceinline__ void ck_turn(float (&x)[NG][8], const uint32_t* signs, int lane, bool inverse) {
+  auto flip = [&] {
+#pragma unroll
+    for (int G = 0; G < NG; ++G) {
+      const uint32_t s = signs[G] >> (8 * (lane >> 3));
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if ((s >> e) & 1u) x[G][e] = -x[G][e];
+    }
+  };
+  if (ALL && !inverse) flip();
+#pragma unroll
+  for (int G = 0; G < NG; ++G) {
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!(e & h)) {
+          const float u = x[G][e], v = x[G][e + h];
+          x[G][e] = u + v;
+          x[G][e + h] = u - v;
+        }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = __shfl_xor_sync(0xffffffffu, x[G][e], o);
+        x[G][e] = lane & o ? y - x[G][e] : x[G][e] + y;
+      }
+  }
+  if constexpr (ALL) {
+#pragma unroll
+    for (int h = 1; h < NG; h <<= 1)
+#pragma unroll
+      for (int G = 0; G < NG; ++G)
+        if (!(G & h))
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float u = x[G][e], v = x[G + h][e];
+            x[G][e] = u + v;
+            x[G + h][e] = u - v;
+          }
+  }
+  const float c = !ALL ? kHadamardScale : NG == 8 ? 0.0625f : NG == 4 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+  for (int G = 0; G < NG; ++G)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[G][e] *= c;
+  if (ALL && inverse) flip();
+}
+
 // Note a value that is not a number of a key that not every row sees.
 template <int D>
 __device__ __forceinline__ void ck_note(CkSmem<D>& sm, int key, uint32_t what) {
@@ -182,7 +276,6 @@ __device__ __forceinline__ void ck_decode(const SeqAttnArgs& a, CkSmem<D>& sm, c
   const int chunk0 = IS_K ? 0 : rank * kC;
   uint64_t* const ready = IS_K ? sm.k_ready : sm.v_ready;
   uint64_t* const freed = IS_K ? sm.k_free : sm.pv_done;
-  const uint32_t ready_at[2] = {pair_addr(&ready[0], 0), pair_addr(&ready[1], 0)};
   const uint32_t buf[2] = {smem_u32(IS_K ? sm.op.k[0] : sm.op.v[0]), smem_u32(IS_K ? sm.op.k[1] : sm.op.v[1])};
   const int page_shift_blocks = c.page_size >> 4;
   const int32_t* table = a.block_tables + static_cast<int64_t>(sm.seq) * a.max_pages;
@@ -261,9 +354,9 @@ __device__ __forceinline__ void ck_decode(const SeqAttnArgs& a, CkSmem<D>& sm, c
           }
         }
       }
-      ck_fence_async();
+      fence_proxy_async();
       __syncwarp();
-      if (lane == 0) pair_arrive(ready_at[j & 1]);
+      if (lane == 0) mbar_arrive(&ready[j & 1]);
     }
   } else {
     uint4 code[kUnits];
@@ -322,9 +415,9 @@ __device__ __forceinline__ void ck_decode(const SeqAttnArgs& a, CkSmem<D>& sm, c
           ck_sts(at + place(i, w), o[0], o[1], o[2], o[3]);
         }
       }
-      ck_fence_async();
+      fence_proxy_async();
       __syncwarp();
-      if (lane == 0) pair_arrive(ready_at[J & 1]);
+      if (lane == 0) mbar_arrive(&ready[J & 1]);
     }
     if (over) sm.over = 1;
   }
@@ -375,14 +468,15 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   }
   if (threadIdx.x == 32) {
     for (int h = 0; h < 2; ++h) {
-      mbar_init(&sm.k_ready[h], 8);
-      mbar_init(&sm.v_ready[h], 8);
-      mbar_init(&sm.p_ready[h], 8);
+      mbar_init(&sm.k_ready[h], rank == 0 ? 5 : 4);
+      mbar_init(&sm.v_ready[h], rank == 0 ? 5 : 4);
+      mbar_init(&sm.p_ready[h], rank == 0 ? 5 : 4);
       mbar_init(&sm.k_free[h], 1);
       mbar_init(&sm.s_full[h], 1);
       mbar_init(&sm.pv_done[h], 1);
     }
     mbar_init(&sm.drained, 1);
+    mbar_init(&sm.q_ready, rank == 0 ? 9 : 8);
     sm.abort = 0;
     sm.odd_count = 0;
     sm.over = 0;
@@ -423,71 +517,92 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
 
   if (warp == 1) pair_tmem_alloc(&sm.tmem_base, 512);
 
-  // ---------------- queries: into the cache's space, scaled, fp16 (bf16 rows: bf16)
-#pragma unroll 1
-  for (int r = warp; r < 128; r += kCkThreads / 32) {
-    float x[NG];
-    const bool live = r < my_rows;
-    const int64_t at = live ? static_cast<int64_t>(sr.first + i0 + r / grp) * a.q.ts +
-                                  static_cast<int64_t>(kvh * grp + r % grp) * a.q.hs
-                            : 0;
-#pragma unroll
-    for (int G = 0; G < NG; ++G) x[G] = live ? load_act(a.q.data, a.q.dtype, at + 32 * G + lane) : 0.f;
-    uint8_t* dst = sm.op.q + (r >> 3) * 16 * D + (r & 7) * 16 + (lane >> 3) * 128 + 2 * ck_pos<FMT>(lane & 7);
-    if constexpr (kBf) {
-      // (the scale multiplies the scores: bf16 queries enter as they are)
-#pragma unroll
-      for (int G = 0; G < NG; ++G)
-        *reinterpret_cast<__nv_bfloat16*>(dst + 512 * G) = __float2bfloat16_rn(a.qscale < 0.f ? -x[G] : x[G]);
-      if (lane == 0) sm.factor[r] = fmaxf(fabsf(a.qscale), 1e-37f);
-    } else {
-      if (a.c.format == KVQ_FMT_Q4_HAD32) {
-#pragma unroll
-        for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane) * kHadamardScale;
-      } else if (FMT == kCkTq4) {
-        tq4_turn_lanes<NG>(x, static_cast<const uint32_t*>(a.c.signs), lane, false);
-      }
-      float top = 0.f;
-#pragma unroll
-      for (int G = 0; G < NG; ++G) {
-        x[G] *= a.qscale;
-        top = fmaxf(top, fabsf(x[G]));
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      int ex = 0;
-      if (top > 0.f && top < INFINITY) ex = 8 - (static_cast<int>(__float_as_uint(fmaxf(top, 1e-30f)) >> 23) - 127);
-      const float up = __uint_as_float(static_cast<uint32_t>(min(ex, 110) + 127) << 23);
-#pragma unroll
-      for (int G = 0; G < NG; ++G) *reinterpret_cast<__half*>(dst + 512 * G) = __float2half_rn(x[G] * up);
-      if (lane == 0) sm.factor[r] = 1.f / up;
-    }
-  }
-  ck_fence_async();
   tc_fence_before();
   __syncthreads();
-  pair_sync();  // both CTAs' queries, barriers and tensor memory
+  pair_sync();  // both CTAs' barriers and tensor memory
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
   const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+
+  // ---------------- queries (warps 0 to 7, while the decoders begin): into the cache's
+  // space, scaled, fp16 (bf16 rows: bf16).  Lane (row l & 7, eighth l >> 3) holds 8 values of
+  // every group of 32, so a warp loads 64 bytes of eight rows at once and writes whole core
+  // matrices.
+  if (warp < 8) {
+#pragma unroll 1
+    for (int r0 = 8 * warp; r0 < 128; r0 += 64) {
+      const int r = r0 + (lane & 7);
+      float x[NG][8];
+      ck_load_row<NG>(a.q, r < my_rows ? static_cast<int64_t>(sr.first + i0 + r / grp) * a.q.ts +
+                                             static_cast<int64_t>(kvh * grp + r % grp) * a.q.hs + 8 * (lane >> 3)
+                                       : -1, x);
+      float f = 0.f;
+      if constexpr (kBf) {
+        // (the scale multiplies the scores: bf16 queries enter as they are)
+        if (a.qscale < 0.f) {
+#pragma unroll
+          for (int G = 0; G < NG; ++G)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[G][e] = -x[G][e];
+        }
+        f = fmaxf(fabsf(a.qscale), 1e-37f);
+      } else {
+        if (a.c.format == KVQ_FMT_Q4_HAD32) ck_turn<NG, false>(x, nullptr, lane, false);
+        else if (FMT == kCkTq4) ck_turn<NG, true>(x, static_cast<const uint32_t*>(a.c.signs), lane, false);
+        float top = 0.f;
+#pragma unroll
+        for (int G = 0; G < NG; ++G)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[G][e] *= a.qscale;
+            top = fmaxf(top, fabsf(x[G][e]));
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        int ex = 0;
+        if (top > 0.f && top < INFINITY) ex = 8 - (static_cast<int>(__float_as_uint(fmaxf(top, 1e-30f)) >> 23) - 127);
+        const float up = __uint_as_float(static_cast<uint32_t>(min(ex, 110) + 127) << 23);
+#pragma unroll
+        for (int G = 0; G < NG; ++G)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[G][e] *= up;
+        f = 1.f / up;
+      }
+      const uint32_t dst = smem_u32(sm.op.q) + (r >> 3) * 16 * D + (r & 7) * 16 + (lane >> 3) * 128;
+#pragma unroll
+      for (int G = 0; G < NG; ++G) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float lo = x[G][ck_elem<FMT>(2 * i)], hi = x[G][ck_elem<FMT>(2 * i + 1)];
+          w[i] = kBf ? pack_bf16(lo, hi) : pack_half2(lo, hi);
+        }
+        ck_sts(dst + 512 * G, w[0], w[1], w[2], w[3]);
+      }
+      if (lane < 8) sm.factor[r] = f;
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_ready);
+    asm volatile("bar.sync 1, 256;" ::: "memory");  // (the softmax warps read the factors)
+  }
 
   bool big = false;  // the second pass
   int first = 0;
 #pragma unroll 1
   for (;;) {
-  // registers: 128 a thread at the launch; 56 + 208 + 112 + 112 of the four roles' 512 here
   if (warp < 4) {
-    ck_regs_down<56>();
     // ---------------- products
     if (warp == 0 && rank == 0 && lane == 0) {
       constexpr uint32_t id_qk = pair_idesc(kBf, false, 256, kCkTile), id_pv = pair_idesc(kBf, true, 256, D);
       const uint64_t dq = umma_desc(smem_u32(sm.op.q), 128, 16 * D);
       const uint64_t dk[2] = {umma_desc(smem_u32(sm.op.k[0]), 128, 16 * D), umma_desc(smem_u32(sm.op.k[1]), 128, 16 * D)};
       const uint64_t dv[2] = {umma_desc(smem_u32(sm.op.v[0]), 128, 2048), umma_desc(smem_u32(sm.op.v[1]), 128, 2048)};
-      for (int j = 0; j <= nt; ++j) {
+      const bool ok = ck_wait<true>(sm, &sm.q_ready, 0, a.status);
+      for (int j = 0; j <= nt && ok; ++j) {
         if (j < nt) {
           const int J = first + j, b = J & 1;
-          if (!ck_wait(sm, &sm.k_ready[b], (J >> 1) & 1, a.status)) break;
+          if (!ck_wait<true>(sm, &sm.k_ready[b], (J >> 1) & 1, a.status)) break;
           tc_fence_after();
           const uint32_t s = tbase + kCkS + 128 * b;
 #pragma unroll
@@ -497,8 +612,8 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
         }
         if (j >= 1) {
           const int jp = j - 1, J = first + jp, b = J & 1;
-          if (!ck_wait(sm, &sm.v_ready[b], (J >> 1) & 1, a.status)) break;
-          if (!ck_wait(sm, &sm.p_ready[b], (J >> 1) & 1, a.status)) break;
+          if (!ck_wait<true>(sm, &sm.v_ready[b], (J >> 1) & 1, a.status)) break;
+          if (!ck_wait<true>(sm, &sm.p_ready[b], (J >> 1) & 1, a.status)) break;
           tc_fence_after();
           const uint32_t p = tbase + kCkS + 128 * b;
 #pragma unroll
@@ -518,14 +633,22 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
           break;
         }
       }
+    } else if (warp > 0 && rank == 1 && lane == 0) {
+      // ---------------- the second CTA's operands, announced to the first by a thread with
+      // nothing else in flight (a release to the cluster waits for all that its thread has)
+      uint64_t* const mine = warp == 1 ? sm.k_ready : warp == 2 ? sm.v_ready : sm.p_ready;
+      if (warp == 1 && !big && ck_wait(sm, &sm.q_ready, 0, a.status)) pair_arrive(pair_addr(&sm.q_ready, 0));
+      for (int j = 0; j < nt; ++j) {
+        const int J = first + j;
+        if (!ck_wait(sm, &mine[J & 1], (J >> 1) & 1, a.status)) break;
+        pair_arrive(pair_addr(&mine[J & 1], 0));
+      }
     }
   } else if (warp < 8) {
     // ---------------- softmax, one row a thread
-    ck_regs_up<208>();
     const int r = 32 * (warp & 3) + lane;
     const int p = r < my_rows ? base + i0 + r / grp : -kNoKey;
     const float f = sm.factor[r] * (big ? 1.f / kCkBigUnit : 1.f);
-    const uint32_t ready_at[2] = {pair_addr(&sm.p_ready[0], 0), pair_addr(&sm.p_ready[1], 0)};
     float m_run = -INFINITY, z = 0.f;
     for (int j = 0; j < nt; ++j) {
       const int J = first + j, b = J & 1;
@@ -544,22 +667,28 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
           seen[k >> 1] = (seen[k >> 1] & (k & 1 ? 0x0000FFFFu : 0xFFFF0000u)) | bits << (16 * (k & 1));
         }
       }
-      uint32_t v[128];
-      tmem_ld32(s_at, reinterpret_cast<uint32_t(&)[32]>(v[0]));
-      tmem_ld32(s_at + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
-      tmem_ld32(s_at + 64, reinterpret_cast<uint32_t(&)[32]>(v[64]));
-      tmem_ld32(s_at + 96, reinterpret_cast<uint32_t(&)[32]>(v[96]));
-      tmem_wait_ld();
-      if (edge) {
+      // the maximum; then p of the second half, still in registers, and of the first, read again
+      // (p goes over the scores)
+      uint32_t v[64];
+      auto half = [&](int h) {
+        tmem_ld32(s_at + 64 * h, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+        tmem_ld32(s_at + 64 * h + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+        tmem_wait_ld();
+        if (edge) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (!((seen[i >> 5] >> (i & 31)) & 1u)) v[i] = 0xFF800000u;
-      }
+          for (int i = 0; i < 64; ++i)
+            if (!(((i < 32 ? seen[2 * h] : seen[2 * h + 1]) >> (i & 31)) & 1u)) v[i] = 0xFF800000u;
+        }
+      };
       float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < 128; i += 8)
+      for (int h = 0; h < 2; ++h) {
+        half(h);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) t4[k] = ck_max3(t4[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+        for (int i = 0; i < 64; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t4[k] = ck_max3(t4[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+      }
       float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
       if (top != -INFINITY) top *= f;
       const bool raise = top > m_run + 8.f;
@@ -586,17 +715,22 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
       }
       const uint64_t f2 = pk2(f, f), mu2 = pk2(-mu, -mu);
       uint64_t z2[2] = {0, 0};
+      uint32_t pk[2][32];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        float e0, e1;
-        upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, mu2), e0, e1);
-        e0 = fast_exp2(e0);
-        e1 = fast_exp2(e1);
-        z2[i & 1] = add2(z2[i & 1], pk2(e0, e1));
-        v[i] = kBf ? pack_bf16(e0, e1) : pack_half2(e0, e1);
-        if (i == 31) tmem_st32(s_at, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+      for (int h = 1; h >= 0; --h) {
+        if (h == 0) half(0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          float e0, e1;
+          upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, mu2), e0, e1);
+          e0 = fast_exp2(e0);
+          e1 = fast_exp2(e1);
+          z2[i & 1] = add2(z2[i & 1], pk2(e0, e1));
+          pk[h][i] = kBf ? pack_bf16(e0, e1) : pack_half2(e0, e1);
+        }
       }
-      tmem_st32(s_at + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+      tmem_st32(s_at, pk[0]);
+      tmem_st32(s_at + 32, pk[1]);
       {
         float e0, e1;
         upk2(add2(z2[0], z2[1]), e0, e1);
@@ -605,30 +739,25 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) pair_arrive(ready_at[b]);
+      if (lane == 0) mbar_arrive(&sm.p_ready[b]);
     }
     sm.m[r] = m_run;
     sm.z[r] = z;
     const int last = first + nt - 1;
     if (nt > 0) ck_wait_warp(sm, &sm.pv_done[last & 1], (last >> 1) & 1, a.status);
-    ck_regs_down<128>();
   } else {
-    ck_regs_down<112>();
     if (warp < 12) ck_decode<FMT, D, true>(a, sm, wk, kvh, rank, big);
     else ck_decode<FMT, D, false>(a, sm, wk, kvh, rank, big);
   }
-  // (nobody takes registers back before the softmax warps have had theirs: a warpgroup with
-  // nothing to do would otherwise leave them waiting for ever)
+  // Both CTAs are done: every product has finished (the softmax warps waited for the last).
   __syncwarp();
+  tc_fence_before();
   __syncthreads();
-  if (warp < 4) ck_regs_up<128>();
-  if (warp >= 8) ck_regs_up<128>();
+  pdl_trigger();
+  pair_sync();
+  tc_fence_after();
   if constexpr (!kBf) {
     if (big) break;
-    __syncwarp();
-    tc_fence_before();
-    pair_sync();
-    tc_fence_after();
     big = (pair_ld_u32(pair_addr(&sm.over, 0)) | pair_ld_u32(pair_addr(&sm.over, 1))) != 0;
     if (!big) break;
     first = nt;
@@ -640,17 +769,13 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   }
 
   // ---------------- the rows: out of tensor memory, over the operands, rotated back, stored
-  pdl_trigger();
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();  // every product has finished (the softmax warps waited for the last)
-  tc_fence_after();
   const int ranges = gridDim.z;
   {
     const int r = 32 * (warp & 3) + lane, part = warp >> 2;
     const float zr = sm.z[r];
     const float unit = big ? 1.f / kCkBigUnit : 1.f;
-    const float inv = sm.abort ? NAN : ranges > 1 ? unit : zr == 0.f ? 0.f : unit / zr;
+    const bool failed = (pair_ld_u32(pair_addr(&sm.abort, 0)) | pair_ld_u32(pair_addr(&sm.abort, 1))) != 0;
+    const float inv = failed ? NAN : ranges > 1 ? unit : zr == 0.f ? 0.f : unit / zr;
 #pragma unroll 1
     for (int cc = 0; cc < D / 64; ++cc) {
       const int col = part * (D / 4) + 16 * cc;
@@ -667,8 +792,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     }
   }
   tc_fence_before();
-  pair_sync();  // both CTAs' rows and notes; nobody needs the tensor memory any more
-  if (warp == 1) pair_tmem_dealloc(tbase, 512);
+  __syncthreads();
   // values that are not numbers, into the rows that see their keys
   for (int other = 0; other < 2; ++other) {
     const int count = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd_count, other)));
@@ -698,28 +822,54 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   }
   __syncthreads();
 #pragma unroll 1
-  for (int r = warp; r < my_rows; r += kCkThreads / 32) {
-    float x[NG];
+  for (int r0 = 8 * warp; r0 < my_rows; r0 += 8 * (kCkThreads / 32)) {
+    const int r = r0 + (lane & 7);  // (rows behind the last are zeros, or of no consequence)
+    float x[NG][8];
 #pragma unroll
-    for (int G = 0; G < NG; ++G) x[G] = sm.out[r][32 * G + lane];
+    for (int G = 0; G < NG; ++G)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[G][e] = sm.out[r][32 * G + 8 * (lane >> 3) + e];
     const int row = sr.first + i0 + r / grp, head = kvh * grp + r % grp;
+    if (ranges == 1) {
+      if (a.c.format == KVQ_FMT_Q4_HAD32) ck_turn<NG, false>(x, nullptr, lane, true);
+      else if (FMT == kCkTq4) ck_turn<NG, true>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
+    }
+    if (r >= my_rows) continue;
     if (ranges > 1) {
       const int64_t at = (static_cast<int64_t>(blockIdx.z) * a.n_rows + row) * a.Hq + head;
-      if (lane == 0) a.ws_m[at] = sm.m[r], a.ws_z[at] = sm.z[r];
+      if (lane < 8) a.ws_m[at] = sm.m[r], a.ws_z[at] = sm.z[r];
 #pragma unroll
-      for (int G = 0; G < NG; ++G) a.ws_acc[at * D + 32 * G + lane] = x[G];
+      for (int G = 0; G < NG; ++G)
+        st_words<8>(a.ws_acc + at * D + 32 * G + 8 * (lane >> 3), reinterpret_cast<const uint32_t*>(x[G]));
       continue;
     }
-    if (a.c.format == KVQ_FMT_Q4_HAD32) {
+    const int64_t at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + 8 * (lane >> 3);
 #pragma unroll
-      for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane) * kHadamardScale;
-    } else if (FMT == kCkTq4) {
-      tq4_turn_lanes<NG>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
+    for (int G = 0; G < NG; ++G) {
+      if (a.out.dtype == KVQ_DT_F32) {
+        float* p = static_cast<float*>(a.out.data) + at + 32 * G;
+        if (a.out.wide) {
+          st_words<8>(p, reinterpret_cast<const uint32_t*>(x[G]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = x[G][e];
+        }
+      } else {
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out.data) + at + 32 * G;
+        if (a.out.wide) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[G][2 * i], x[G][2 * i + 1]);
+          st_words<4>(p, w);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = __float2bfloat16_rn(x[G][e]);
+        }
+      }
     }
-#pragma unroll
-    for (int G = 0; G < NG; ++G) seq_store(a, row, head, 32 * G + lane, x[G]);
   }
-  pair_sync();  // (its notes are read until here)
+  pair_sync();  // (its notes are read until here, and its tensor memory)
+  if (warp == 1) pair_tmem_dealloc(tbase, 512);
 }
 
 // The pairs of CTAs of a call, by a bound: sequences' blocks are whole.

@@ -610,7 +610,7 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
  *   window, sinks >= 0; max_seq_len and max_rows bound the device's lengths and rows.
  *   A sequence whose length is negative or above max_seq_len or its table: its rows are
  *   NaN (KVQ_DEV_BAD_LENGTH).
- *   workspace: device, 16-byte aligned, of kvq_attn_workspace_size bytes (NULL where that
+ *   workspace: device, 32-byte aligned, of kvq_attn_workspace_size bytes (NULL where that
  *       is 0); its contents do not matter and nothing is kept in it between calls.
  *   d_status: optional. */
 
