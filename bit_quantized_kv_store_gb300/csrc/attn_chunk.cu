@@ -39,7 +39,8 @@ namespace kvq {
 
 constexpr int kCkTile = 128;    // keys of a tile: 8 blocks of 16
 constexpr int kCkThreads = 512;
-constexpr int kCkOdd = 1024;    // values that are not numbers, noted per CTA
+constexpr int kCkRing = 5;       // units of raw codes that a decoding thread has in flight, and one
+constexpr int kCkOdd = 512;    // values that are not numbers, noted per CTA
 constexpr float kCkBigUnit = 0.00390625f;  // 2^-8: the unit of keys and values in the second pass
 enum { kCkQ4 = 0, kCkTq4 = 1, kCkBf16 = 2 };
 
@@ -61,6 +62,8 @@ struct CkSmem {
     CkOperands<D> op;
     float out[128][D + 1];  // at the end: this CTA's rows
   };
+  uint4 raw[2][kCkRing][128];  // per plane, slot and decoding thread
+  uint32_t raw_scale[2][kCkRing][128];
   // the CTA's 4 warps (q_ready: 8) arrive, and at the first CTA's the second's forwarder
   uint64_t k_ready[2], v_ready[2], p_ready[2], q_ready;
   uint64_t k_free[2], s_full[2], pv_done[2];    // each CTA's: the products arrive
@@ -119,11 +122,16 @@ struct CkWalk {
     const int i = (tile0 + tile) * 8 + blk;
     return i < kb.count ? kb.block_of(i) * 16 : kNoKey;
   }
-  // Some row does not see some key of it.
-  __device__ __forceinline__ bool edge(int tile) const {
-    const int first = key_of(tile, 0), last = key_of(tile, 7);
-    return last - first != 7 * 16 || !all_visible(first, kCkTile, p0, p1, window, sinks);
+  // Tiles [plain0, plain1) of the whole walk lie behind the sinks' blocks and every row sees
+  // all of their keys; in the others (edges) some row may not.
+  int plain0, plain1;
+  __device__ __forceinline__ void find_plain() {
+    const int shift = kb.head - kb.body;  // block i of the walk is block i - shift of the sequence
+    plain0 = (kb.head + 7) >> 3;
+    if (window > 0) plain0 = max(plain0, (((max(p1 - window + 1, 0) + 15) >> 4) + shift + 7) >> 3);
+    plain1 = p0 < kCkTile - 1 ? 0 : ((((p0 - kCkTile + 1) >> 4) + shift) >> 3) + 1;
   }
+  __device__ __forceinline__ bool edge(int tile) const { return tile0 + tile < plain0 || tile0 + tile >= plain1; }
 };
 
 // 8 codes of a word as fp16 operands, times (s, s): 4-bit groups in the order 0 4 1 5 2 6 3 7,
@@ -277,7 +285,6 @@ __device__ __forceinline__ void ck_decode(const SeqAttnArgs& a, CkSmem<D>& sm, c
   uint64_t* const ready = IS_K ? sm.k_ready : sm.v_ready;
   uint64_t* const freed = IS_K ? sm.k_free : sm.pv_done;
   const uint32_t buf[2] = {smem_u32(IS_K ? sm.op.k[0] : sm.op.v[0]), smem_u32(IS_K ? sm.op.k[1] : sm.op.v[1])};
-  const int page_shift_blocks = c.page_size >> 4;
   const int32_t* table = a.block_tables + static_cast<int64_t>(sm.seq) * a.max_pages;
 
   // Lane l: the cache row of block l & 7 of the tile's (this CTA's four of them for keys):
@@ -286,13 +293,13 @@ __device__ __forceinline__ void ck_decode(const SeqAttnArgs& a, CkSmem<D>& sm, c
     if (tile >= wk.tiles) return -2;
     const int key = wk.key_of(tile, IS_K ? rank * 4 + (lane & 3) : lane & 7);
     if (key == kNoKey) return -2;
-    const int blk = key >> 4, pg = blk / page_shift_blocks;
+    const int blk = key >> 4, pg = static_cast<int>(fast_div(static_cast<uint32_t>(blk), a.page_blocks));
     const int page = table[pg];
     if (page < 0 || page >= c.num_pages) {
       set_status(a.status, KVQ_DEV_BAD_PAGE);
       return -1;
     }
-    return (page * c.num_kv_heads + kvh) * c.page_size + (blk - pg * page_shift_blocks) * 16;
+    return (page * c.num_kv_heads + kvh) * c.page_size + (blk - pg * static_cast<int>(a.page_blocks.d)) * 16;
   };
   auto unit_key = [&](int i) { return ((tid + 128 * i) / (8 * kC)) * 8 + (tid & 7); };
   auto unit_chunk = [&](int i) { return ((tid + 128 * i) >> 3) % kC; };
@@ -359,67 +366,88 @@ __device__ __forceinline__ void ck_decode(const SeqAttnArgs& a, CkSmem<D>& sm, c
       if (lane == 0) mbar_arrive(&ready[j & 1]);
     }
   } else {
-    uint4 code[kUnits];
-    uint32_t scale[kUnits];
-    auto load = [&](int rows) {
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int key = unit_key(i);
-        const int row0 = __shfl_sync(0xffffffffu, rows, key >> 4);
-        code[i] = make_uint4(0, 0, 0, 0);
-        scale[i] = IS_K && row0 == -1 ? 0x7E00u : 0u;  // a bad page's scores are NaN
-        if (row0 >= 0) {
-          const int64_t row = static_cast<int64_t>(row0) + (key & 15);
-          const int ch = chunk0 + unit_chunk(i);
-          code[i] = __ldg(reinterpret_cast<const uint4*>(plane + row * (D / 2)) + ch);
-          scale[i] = __ldg(scales + (FMT == kCkQ4 ? row * (D / 32) + ch : row));
-        }
-      }
-    };
-    load(find_rows(0));
-    int rows_next = find_rows(1);
+    // A thread's units: key groups (of 8) kg0 + i kSpan, always the same chunk and the same key
+    // of 16.  Their codes and scales come through a ring of its own in shared memory, kCkRing
+    // units ahead (nobody else reads them, so only its own copies are waited for).
+    constexpr int kSpan = 16 / kC;
+    static_assert(kSpan % 2 == 0 && kUnits * kSpan * 8 == kKeys, "units");
+    const int kg0 = tid / (8 * kC), chunk = chunk0 + (tid >> 3) % kC, in16 = (kg0 & 1) * 8 + (tid & 7);
+    const uint8_t* const code_at = plane + in16 * (D / 2) + chunk * 16;
+    // (copies of 4 bytes: the scale beside another)
+    const int scale_i = FMT == kCkQ4 ? in16 * (D / 32) + chunk : in16;
+    const uint16_t* const scale_at = scales + (scale_i & ~1);
+    const uint32_t pick = scale_i & 1 ? 0x3232u : 0x1010u;
+    const uint32_t dst0 = IS_K ? kg0 * 16 * D + (tid >> 3) % kC * 512 + (tid & 7) * 16
+                               : (tid >> 3) % kC * 8192 + kg0 * 128 + (tid & 7) * 16;
+    constexpr uint32_t kStepUnit = IS_K ? kSpan * 16 * D : kSpan * 128, kStepWord = IS_K ? 128 : 2048;
+    const uint32_t ring = smem_u32(&sm.raw[IS_K ? 0 : 1][0][tid]), ring_s = smem_u32(&sm.raw_scale[IS_K ? 0 : 1][0][tid]);
     const int first = big ? wk.tiles : 0;  // tiles of the pass before: buffers and barriers go on from there
-    bool over = false;
+    uint32_t top = 0;
+    int rows = find_rows(0), rows_next = find_rows(1);
+    int at_tile = 0, at_unit = 0, at_slot = 0;  // of the next unit to be fetched
+    auto fetch = [&] {
+      const int row0 = __shfl_sync(0xffffffffu, rows, (kg0 >> 1) + at_unit * (kSpan / 2));
+      if (row0 >= 0) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + at_slot * 2048),
+                     "l"(code_at + static_cast<int64_t>(row0) * (D / 2))
+                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ring_s + at_slot * 512),
+                     "l"(scale_at + static_cast<int64_t>(row0) * (FMT == kCkQ4 ? D / 32 : 1))
+                     : "memory");
+      } else {  // no such key: zeros; a bad page's scores are NaN
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ring_s + at_slot * 512), "r"(IS_K && row0 == -1 ? 0x7E007E00u : 0u) : "memory");
+      }
+      at_slot = at_slot == kCkRing - 1 ? 0 : at_slot + 1;
+      if (++at_unit == kUnits) {
+        at_unit = 0;
+        rows = rows_next;
+        rows_next = find_rows(++at_tile + 1);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < kCkRing - 1; ++i) fetch();
+    int slot = 0;
 #pragma unroll 1
     for (int j = 0; j < wk.tiles; ++j) {
       const int J = first + j;
-      uint4 now[kUnits];
-      uint32_t s_now[kUnits];
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) now[i] = code[i], s_now[i] = scale[i];
-      if (j + 1 < wk.tiles) load(rows_next);
-      rows_next = find_rows(j + 2);
-      if constexpr (!IS_K) {
-        if (wk.edge(j)) {  // 0 x NaN: what not every row sees is taken out and noted
-#pragma unroll
-          for (int i = 0; i < kUnits; ++i)
-            if ((s_now[i] & 0x7C00u) == 0x7C00u) {
-              const int key = unit_key(i);
-              ck_note(sm, wk.key_of(j, key >> 4) + (key & 15), static_cast<uint32_t>(chunk0 + unit_chunk(i)) << 16);
-              s_now[i] = 0;
-            }
-        }
-      }
+      const bool edge = !IS_K && wk.edge(j);
       if (J >= 2 && !ck_wait_warp(sm, &freed[J & 1], ((J >> 1) - 1) & 1, a.status)) return;
-      const uint32_t at = buf[J & 1];
-#pragma unroll
+      uint32_t at = buf[J & 1] + dst0;
+#pragma unroll 1
       for (int i = 0; i < kUnits; ++i) {
-        // (scales above 4096: products that may pass 65504; NaN is not among them)
-        over |= (s_now[i] & 0x7FFFu) > 0x6C00u && (s_now[i] & 0x7FFFu) <= 0x7C00u;
-        __half2 s2 = u32_as_h2(prmt(s_now[i], 0u, 0x1010u));
+        fetch();
+        asm volatile("cp.async.wait_group %0;" ::"n"(kCkRing - 1) : "memory");
+        uint32_t x[4], sw;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                     : "r"(ring + slot * 2048)
+                     : "memory");
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(ring_s + slot * 512) : "memory");
+        slot = slot == kCkRing - 1 ? 0 : slot + 1;
+        uint32_t ss = prmt(sw, 0u, pick);
+        if (edge && (ss & 0x7C00u) == 0x7C00u) {  // 0 x NaN: what not every row sees is taken out and noted
+          const int kg = kg0 + i * kSpan;
+          ck_note(sm, wk.key_of(j, kg >> 1) + in16, static_cast<uint32_t>(chunk) << 16);
+          ss = 0;
+        }
+        top = max(top, ss & 0x7FFFu);
+        __half2 s2 = u32_as_h2(ss);
         if (big) s2 = __hmul2(s2, __float2half2_rn(kCkBigUnit));
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int k = 0; k < 4; ++k) {
           uint32_t o[4];
-          ck_decode8<FMT>(w == 0 ? now[i].x : w == 1 ? now[i].y : w == 2 ? now[i].z : now[i].w, s2, o);
-          ck_sts(at + place(i, w), o[0], o[1], o[2], o[3]);
+          ck_decode8<FMT>(x[k], s2, o);
+          ck_sts(at + k * kStepWord, o[0], o[1], o[2], o[3]);
         }
+        at += kStepUnit;
       }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ready[J & 1]);
     }
-    if (over) sm.over = 1;
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (those behind the last tile's are markers)
+    if (top > 0x6C00u) sm.over = 1;  // above 4096: products that may pass 65504
   }
 }
 
@@ -513,6 +541,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   const int all_tiles = (wk.kb.count + 7) / 8;
   wk.tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * blockIdx.z / gridDim.z);
   wk.tiles = static_cast<int>(static_cast<int64_t>(all_tiles) * (blockIdx.z + 1) / gridDim.z) - wk.tile0;
+  wk.find_plain();
   const int nt = wk.tiles;
 
   if (warp == 1) pair_tmem_alloc(&sm.tmem_base, 512);
@@ -667,25 +696,24 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
           seen[k >> 1] = (seen[k >> 1] & (k & 1 ? 0x0000FFFFu : 0xFFFF0000u)) | bits << (16 * (k & 1));
         }
       }
-      // the maximum; then p of the second half, still in registers, and of the first, read again
-      // (p goes over the scores)
-      uint32_t v[64];
-      auto half = [&](int h) {
-        tmem_ld32(s_at + 64 * h, reinterpret_cast<uint32_t(&)[32]>(v[0]));
-        tmem_ld32(s_at + 64 * h + 32, reinterpret_cast<uint32_t(&)[32]>(v[32]));
+
+      auto load = [&](int cc, uint32_t (&v)[32]) {
+        tmem_ld32(s_at + 32 * cc, v);
         tmem_wait_ld();
         if (edge) {
+          const uint32_t sn = (32==32? (cc==0?seen[0]:cc==1?seen[1]:cc==2?seen[2]:seen[3]) : ((cc<2?seen[0]:cc<4?seen[1]:cc<6?seen[2]:seen[3])>>(16*(cc&1))));
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!(((i < 32 ? seen[2 * h] : seen[2 * h + 1]) >> (i & 31)) & 1u)) v[i] = 0xFF800000u;
+          for (int i = 0; i < 32; ++i)
+            if (!((sn >> i) & 1u)) v[i] = 0xFF800000u;
         }
       };
       float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t v[32];
+        load(cc, v);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        half(h);
-#pragma unroll
-        for (int i = 0; i < 64; i += 8)
+        for (int i = 0; i < 32; i += 8)
 #pragma unroll
           for (int k = 0; k < 4; ++k) t4[k] = ck_max3(t4[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
       }
@@ -715,22 +743,21 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
       }
       const uint64_t f2 = pk2(f, f), mu2 = pk2(-mu, -mu);
       uint64_t z2[2] = {0, 0};
-      uint32_t pk[2][32];
+#pragma unroll 2
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t v[32], pk[16];
+        load(cc, v);
 #pragma unroll
-      for (int h = 1; h >= 0; --h) {
-        if (h == 0) half(0);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 16; ++i) {
           float e0, e1;
           upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, mu2), e0, e1);
           e0 = fast_exp2(e0);
           e1 = fast_exp2(e1);
           z2[i & 1] = add2(z2[i & 1], pk2(e0, e1));
-          pk[h][i] = kBf ? pack_bf16(e0, e1) : pack_half2(e0, e1);
+          pk[i] = kBf ? pack_bf16(e0, e1) : pack_half2(e0, e1);
         }
+        tmem_st16(s_at + 16 * cc, pk);
       }
-      tmem_st32(s_at, pk[0]);
-      tmem_st32(s_at + 32, pk[1]);
       {
         float e0, e1;
         upk2(add2(z2[0], z2[1]), e0, e1);

@@ -169,6 +169,7 @@ struct SeqAttnArgs {
   int Hq, group;
   float qscale;  // sm_scale * log2(e)
   int32_t* status;
+  FastDiv page_blocks;  // 16-key blocks of a page
   // more than one cluster for a block of columns: partials [ranges][n_rows][Hq], contexts
   // [ranges][n_rows][Hq][head_dim] (unnormalised, in the cache's space)
   float* ws_m;
