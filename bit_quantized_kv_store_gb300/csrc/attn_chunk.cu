@@ -22,7 +22,7 @@
 // transposed.  Scores alternate between two buffers of tensor memory; p (fp16) goes over
 // the scores it was made from and is the context product's A.
 // Queries, keys and values are fp16 here (each within 2^-12; bf16 rows: bf16, as they
-// are), a row's queries scaled by a power of two to 2^8 .. 2^9; p is fp16 (bf16), at most
+// are), a row's queries scaled by a power of two (to at most 2^15); p is fp16 (bf16), at most
 // 2^8: the softmax's reference follows when a row's scores pass it by more than 8.  Where a
 // scale above 4096 turns up (8 s may not fit fp16), the pair goes over its keys once more
 // with keys and values in units of 2^8; nobody else pays for that.
@@ -64,7 +64,7 @@ struct CkSmem {
   };
   uint4 raw[2][kCkRing][128];  // per plane, slot and decoding thread
   uint32_t raw_scale[2][kCkRing][128];
-  // the CTA's 4 warps (q_ready: 8) arrive, and at the first CTA's the second's forwarder
+  // the CTA's 4 warps (q_ready: 16) arrive, and at the first CTA's the second's forwarder
   uint64_t k_ready[2], v_ready[2], p_ready[2], q_ready;
   uint64_t k_free[2], s_full[2], pv_done[2];    // each CTA's: the products arrive
   uint64_t drained;
@@ -157,102 +157,6 @@ template <int FMT>
 __device__ __forceinline__ int ck_pos(int j) { return FMT == kCkQ4 ? (j & 3) * 2 + (j >> 2) : j; }
 template <int FMT>
 __device__ __forceinline__ int ck_elem(int i) { return FMT == kCkQ4 ? (i >> 1) + 4 * (i & 1) : i; }
-
-// 8 values of every group of 32 of a row, the first of them element `at` of the view (< 0:
-// zeros).
-template <int NG>
-__device__ __forceinline__ void ck_load_row(const RowsView& v, int64_t at, float (&x)[NG][8]) {
-  if (at < 0) {
-#pragma unroll
-    for (int G = 0; G < NG; ++G)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[G][e] = 0.f;
-  } else if (v.dtype == KVQ_DT_BF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(v.data) + at;
-    uint32_t w[NG][4];
-#pragma unroll
-    for (int G = 0; G < NG; ++G) {
-      if (v.wide) {
-        ld_words<4>(p + 32 * G, w[G]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[G][i] = p[32 * G + 2 * i] | static_cast<uint32_t>(p[32 * G + 2 * i + 1]) << 16;
-      }
-    }
-#pragma unroll
-    for (int G = 0; G < NG; ++G)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[G][2 * i] = __uint_as_float(w[G][i] << 16);
-        x[G][2 * i + 1] = __uint_as_float(w[G][i] & 0xFFFF0000u);
-      }
-  } else {
-    const float* p = static_cast<const float*>(v.data) + at;
-#pragma unroll
-    for (int G = 0; G < NG; ++G) {
-      if (v.wide) {
-        ld_words<8>(p + 32 * G, reinterpret_cast<uint32_t*>(x[G]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[G][e] = p[32 * G + e];
-      }
-    }
-  }
-}
-
-// The rows' rotation (ALL: the D-point one with signs, else each group's), for rows whose
-// elements 32 G + 8 (lane >> 3) + e are x[G][e].
-template <int NG, bool ALL>
-__device__ __forceinline__ void ck_turn(float (&x)[NG][8], const uint32_t* signs, int lane, bool inverse) {
-  auto flip = [&] {
-#pragma unroll
-    for (int G = 0; G < NG; ++G) {
-      const uint32_t s = signs[G] >> (8 * (lane >> 3));
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if ((s >> e) & 1u) x[G][e] = -x[G][e];
-    }
-  };
-  if (ALL && !inverse) flip();
-#pragma unroll
-  for (int G = 0; G < NG; ++G) {
-#pragma unroll
-    for (int h = 1; h < 8; h <<= 1)
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (!(e & h)) {
-          const float u = x[G][e], v = x[G][e + h];
-          x[G][e] = u + v;
-          x[G][e + h] = u - v;
-        }
-#pragma unroll
-    for (int o = 8; o < 32; o <<= 1)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = __shfl_xor_sync(0xffffffffu, x[G][e], o);
-        x[G][e] = lane & o ? y - x[G][e] : x[G][e] + y;
-      }
-  }
-  if constexpr (ALL) {
-#pragma unroll
-    for (int h = 1; h < NG; h <<= 1)
-#pragma unroll
-      for (int G = 0; G < NG; ++G)
-        if (!(G & h))
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float u = x[G][e], v = x[G + h][e];
-            x[G][e] = u + v;
-            x[G + h][e] = u - v;
-          }
-  }
-  const float c = !ALL ? kHadamardScale : NG == 8 ? 0.0625f : NG == 4 ? 0.08838834764831845f : 0.125f;
-#pragma unroll
-  for (int G = 0; G < NG; ++G)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[G][e] *= c;
-  if (ALL && inverse) flip();
-}
 
 // Note a value that is not a number of a key that not every row sees.
 template <int D>
@@ -504,7 +408,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
       mbar_init(&sm.pv_done[h], 1);
     }
     mbar_init(&sm.drained, 1);
-    mbar_init(&sm.q_ready, rank == 0 ? 9 : 8);
+    mbar_init(&sm.q_ready, rank == 0 ? 17 : 16);
     sm.abort = 0;
     sm.odd_count = 0;
     sm.over = 0;
@@ -553,67 +457,85 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   const uint32_t tbase = sm.tmem_base;
   const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
 
-  // ---------------- queries (warps 0 to 7, while the decoders begin): into the cache's
-  // space, scaled, fp16 (bf16 rows: bf16).  Lane (row l & 7, eighth l >> 3) holds 8 values of
-  // every group of 32, so a warp loads 64 bytes of eight rows at once and writes whole core
-  // matrices.
-  if (warp < 8) {
-#pragma unroll 1
-    for (int r0 = 8 * warp; r0 < 128; r0 += 64) {
-      const int r = r0 + (lane & 7);
+  // ---------------- queries, eight rows a warp: into the cache's space, scaled, fp16 (bf16
+  // rows: bf16).  Lane (row l & 7, eighth l >> 3) holds 8 values of a group of 32, so a warp
+  // loads 64 bytes of eight rows at once and writes whole core matrices.  Group after group
+  // in a rolled loop (the code is fetched once a CTA; unrolled it took longer than the loads),
+  // scaled by a bound: rotated values are at most sqrt(32) times the row's largest.
+  {
+    const int r = 8 * warp + (lane & 7);
+    const int64_t q_at = r < my_rows ? static_cast<int64_t>(sr.first + i0 + r / grp) * a.q.ts +
+                                           static_cast<int64_t>(kvh * grp + r % grp) * a.q.hs + 8 * (lane >> 3)
+                                     : -1;
+    const uint32_t dst = smem_u32(sm.op.q) + warp * 16 * D + (lane & 7) * 16 + (lane >> 3) * 128;
+    auto put = [&](int G, const float(&x)[8], float by) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float lo = x[ck_elem<FMT>(2 * i)] * by, hi = x[ck_elem<FMT>(2 * i + 1)] * by;
+        w[i] = kBf ? pack_bf16(lo, hi) : pack_half2(lo, hi);
+      }
+      ck_sts(dst + 512 * G, w[0], w[1], w[2], w[3]);
+    };
+    // the power of two that takes a bound `top` to at most 2^15; NaN and infinities stay
+    auto scale_for = [](float top) {
+      int ex = 0;
+      if (top > 0.f && top < INFINITY) ex = 14 - (static_cast<int>(__float_as_uint(fmaxf(top, 1e-30f)) >> 23) - 127);
+      return __uint_as_float(static_cast<uint32_t>(max(min(ex, 110), -110) + 127) << 23);
+    };
+    float f;
+    if constexpr (FMT == kCkTq4) {
       float x[NG][8];
-      ck_load_row<NG>(a.q, r < my_rows ? static_cast<int64_t>(sr.first + i0 + r / grp) * a.q.ts +
-                                             static_cast<int64_t>(kvh * grp + r % grp) * a.q.hs + 8 * (lane >> 3)
-                                       : -1, x);
-      float f = 0.f;
-      if constexpr (kBf) {
-        // (the scale multiplies the scores: bf16 queries enter as they are)
-        if (a.qscale < 0.f) {
+      seq_load_row<NG>(a.q, q_at, x);
+      seq_turn<NG, true>(x, static_cast<const uint32_t*>(a.c.signs), lane, false);
+      float top = 0.f;
 #pragma unroll
-          for (int G = 0; G < NG; ++G)
+      for (int G = 0; G < NG; ++G)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[G][e] = -x[G][e];
-        }
-        f = fmaxf(fabsf(a.qscale), 1e-37f);
-      } else {
-        if (a.c.format == KVQ_FMT_Q4_HAD32) ck_turn<NG, false>(x, nullptr, lane, false);
-        else if (FMT == kCkTq4) ck_turn<NG, true>(x, static_cast<const uint32_t*>(a.c.signs), lane, false);
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[G][e]));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      const float up = scale_for(top);
+#pragma unroll
+      for (int G = 0; G < NG; ++G) put(G, x[G], up);
+      f = a.qscale / up;
+    } else {
+      const bool rot = a.c.format == KVQ_FMT_Q4_HAD32;
+      float up = 1.f;
+      if constexpr (!kBf) {
         float top = 0.f;
+        float x[NG][8];
+        seq_load_row<NG>(a.q, q_at, x);  // (all at once: they come from far)
 #pragma unroll
         for (int G = 0; G < NG; ++G)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[G][e] *= a.qscale;
-            top = fmaxf(top, fabsf(x[G][e]));
-          }
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[G][e]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-        int ex = 0;
-        if (top > 0.f && top < INFINITY) ex = 8 - (static_cast<int>(__float_as_uint(fmaxf(top, 1e-30f)) >> 23) - 127);
-        const float up = __uint_as_float(static_cast<uint32_t>(min(ex, 110) + 127) << 23);
-#pragma unroll
-        for (int G = 0; G < NG; ++G)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[G][e] *= up;
-        f = 1.f / up;
+        up = scale_for(rot ? top * 5.65685424949238f : top);
       }
-      const uint32_t dst = smem_u32(sm.op.q) + (r >> 3) * 16 * D + (r & 7) * 16 + (lane >> 3) * 128;
-#pragma unroll
+#pragma unroll 2
+      for (int G = 0; G < NG; ++G) {
+        float x[1][8];
+        seq_load_row<1>(a.q, q_at < 0 ? -1 : q_at + 32 * G, x);
+        if (rot) seq_turn<1, false>(x, nullptr, lane, false);
+        put(G, x[0], up);
+      }
+      f = a.qscale / up;
+    }
+    // (the factor of a row's scores is not negative: the maximum is taken before it)
+    if (f < 0.f) {
+#pragma unroll 1
       for (int G = 0; G < NG; ++G) {
         uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float lo = x[G][ck_elem<FMT>(2 * i)], hi = x[G][ck_elem<FMT>(2 * i + 1)];
-          w[i] = kBf ? pack_bf16(lo, hi) : pack_half2(lo, hi);
-        }
-        ck_sts(dst + 512 * G, w[0], w[1], w[2], w[3]);
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(dst + 512 * G) : "memory");
+        ck_sts(dst + 512 * G, w[0] ^ 0x80008000u, w[1] ^ 0x80008000u, w[2] ^ 0x80008000u, w[3] ^ 0x80008000u);
       }
-      if (lane < 8) sm.factor[r] = f;
     }
+    if (lane < 8) sm.factor[r] = fmaxf(fabsf(f), 1e-37f);
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_ready);
-    asm volatile("bar.sync 1, 256;" ::: "memory");  // (the softmax warps read the factors)
   }
 
   bool big = false;  // the second pass
@@ -677,6 +599,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     // ---------------- softmax, one row a thread
     const int r = 32 * (warp & 3) + lane;
     const int p = r < my_rows ? base + i0 + r / grp : -kNoKey;
+    ck_wait_warp(sm, &sm.q_ready, 0, a.status);  // (the factors)
     const float f = sm.factor[r] * (big ? 1.f / kCkBigUnit : 1.f);
     float m_run = -INFINITY, z = 0.f;
     for (int j = 0; j < nt; ++j) {
@@ -848,49 +771,58 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     }
   }
   __syncthreads();
-#pragma unroll 1
-  for (int r0 = 8 * warp; r0 < my_rows; r0 += 8 * (kCkThreads / 32)) {
-    const int r = r0 + (lane & 7);  // (rows behind the last are zeros, or of no consequence)
-    float x[NG][8];
-#pragma unroll
-    for (int G = 0; G < NG; ++G)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[G][e] = sm.out[r][32 * G + 8 * (lane >> 3) + e];
+  {
+    const int r = 8 * warp + (lane & 7);  // (rows behind the last are zeros, or of no consequence)
     const int row = sr.first + i0 + r / grp, head = kvh * grp + r % grp;
-    if (ranges == 1) {
-      if (a.c.format == KVQ_FMT_Q4_HAD32) ck_turn<NG, false>(x, nullptr, lane, true);
-      else if (FMT == kCkTq4) ck_turn<NG, true>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
-    }
-    if (r >= my_rows) continue;
-    if (ranges > 1) {
-      const int64_t at = (static_cast<int64_t>(blockIdx.z) * a.n_rows + row) * a.Hq + head;
-      if (lane < 8) a.ws_m[at] = sm.m[r], a.ws_z[at] = sm.z[r];
+    const bool live = r < my_rows;
+    const int64_t out_at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + 8 * (lane >> 3);
+    const int64_t part = (static_cast<int64_t>(blockIdx.z) * a.n_rows + row) * a.Hq + head;
+    auto get = [&](int G, float(&x)[8]) {
 #pragma unroll
-      for (int G = 0; G < NG; ++G)
-        st_words<8>(a.ws_acc + at * D + 32 * G + 8 * (lane >> 3), reinterpret_cast<const uint32_t*>(x[G]));
-      continue;
-    }
-    const int64_t at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + 8 * (lane >> 3);
-#pragma unroll
-    for (int G = 0; G < NG; ++G) {
-      if (a.out.dtype == KVQ_DT_F32) {
-        float* p = static_cast<float*>(a.out.data) + at + 32 * G;
+      for (int e = 0; e < 8; ++e) x[e] = sm.out[r][32 * G + 8 * (lane >> 3) + e];
+    };
+    auto put = [&](int G, const float(&x)[8]) {
+      if (!live) return;
+      if (ranges > 1) {
+        st_words<8>(a.ws_acc + part * D + 32 * G + 8 * (lane >> 3), reinterpret_cast<const uint32_t*>(x));
+      } else if (a.out.dtype == KVQ_DT_F32) {
+        float* p = static_cast<float*>(a.out.data) + out_at + 32 * G;
         if (a.out.wide) {
-          st_words<8>(p, reinterpret_cast<const uint32_t*>(x[G]));
+          st_words<8>(p, reinterpret_cast<const uint32_t*>(x));
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = x[G][e];
+          for (int e = 0; e < 8; ++e) p[e] = x[e];
         }
       } else {
-        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out.data) + at + 32 * G;
+        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out.data) + out_at + 32 * G;
         if (a.out.wide) {
           uint32_t w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[G][2 * i], x[G][2 * i + 1]);
+          for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
           st_words<4>(p, w);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = __float2bfloat16_rn(x[G][e]);
+          for (int e = 0; e < 8; ++e) p[e] = __float2bfloat16_rn(x[e]);
+        }
+      }
+    };
+    if (8 * warp < my_rows) {
+      if (ranges > 1 && live && lane < 8) a.ws_m[part] = sm.m[r], a.ws_z[part] = sm.z[r];
+      if (FMT == kCkTq4 && ranges == 1) {
+        float x[NG][8];
+#pragma unroll
+        for (int G = 0; G < NG; ++G) get(G, x[G]);
+        seq_turn<NG, true>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
+#pragma unroll
+        for (int G = 0; G < NG; ++G) put(G, x[G]);
+      } else {
+        const bool rot = ranges == 1 && a.c.format == KVQ_FMT_Q4_HAD32;
+#pragma unroll 2
+        for (int G = 0; G < NG; ++G) {
+          float x[1][8];
+          get(G, x[0]);
+          if (rot) seq_turn<1, false>(x, nullptr, lane, true);
+          put(G, x[0]);
         }
       }
     }

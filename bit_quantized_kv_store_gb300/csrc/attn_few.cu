@@ -18,8 +18,8 @@
 // 4-bit groups: a key's codes enter the tensor cores unsigned, without a conversion: c in
 // bits 2 to 5 of a half is the subnormal c 2^-22, in bits 6 to 9 16 c 2^-22, and the query
 // of such a dim carries the 1/16; the 8 that codes are biased by is in the accumulator's
-// start (-8 sum q over the group).  So a group of scores is exact up to the query, which is
-// split into two halves (22 bits), and its scale multiplies the fp32 sum.  (The tensor cores
+// start (-8 sum q over the group).  So a group of scores is exact up to the query (fp16,
+// 2^-12), and its scale multiplies the fp32 sum.  (The tensor cores
 // line products of subnormals up as if their exponent were 2^-14 and cut a sum 23 bits
 // below: 2^-15 of a code times the largest query element, a 2^-15 part of a score.  For
 // values, whose small sums count, that is too much: they are converted, exactly, to c - 8.)
@@ -47,7 +47,7 @@ struct FewShape {
   static constexpr int kRow = kBf ? 2 * D : D / 2;           // bytes of a row of the k or v plane
   static constexpr int kChunks = kRow / 16;                  // 16-byte chunks of it
   static constexpr int kScaleRow = FMT == kFewQ4 ? D / 16 : FMT == kFewTq4 ? 2 : 0;  // bytes of its scales
-  static constexpr int kBlocks = kBf && D == 256 ? 1 : 2;    // 16-key blocks of a tile
+  static constexpr int kBlocks = 1;                          // 16-key blocks of a tile
   static constexpr int kKeys = 16 * kBlocks;
   static constexpr int kPlane = kKeys * kRow;
   static constexpr int kScales = kKeys * kScaleRow;
@@ -65,12 +65,14 @@ struct FewSmem {
     __align__(128) uint8_t ring[kRing > kFold ? kRing : kFold];
     float fold[WARPS][8][D];
   };
-  uint4 qf[S::kSteps][32];  // per k-step and lane: (high b0, b1, low b0, b1) of the score product's B operand
+  // per lane, the score product's B operand: of a group's two steps; bf16 rows: of a step, (high b0, b1, low b0, b1)
+  uint4 qf[S::kBf ? S::kSteps : S::kSteps / 2][32];
   float2 bias[D / 32][4];   // 4-bit groups: -8 sum of the group's queries (heads 2t, 2t + 1), as the codes' units
   float factor[8];          // per column: what its scores' units are worth
-  float fm[WARPS][8], fz[WARPS][8];
-  float m[8], z[8];
-  float acc[8][D];          // this CTA's partial
+  float fm[WARPS][8], fz[WARPS][8], fw[WARPS][8];  // per warp and column: reference, sum, weight
+  float m_own[8], z_own[8];
+  float m[16][8], z[16][8];  // per CTA of the cluster and column
+  __align__(16) float acc[8 * D];  // this CTA's pieces of the cluster's partials: [CTA][piece][values]
 };
 
 __device__ __forceinline__ void few_ldsm(uint32_t addr, uint32_t (&r)[4]) {
@@ -99,6 +101,11 @@ __device__ __forceinline__ void few_lds(uint32_t a, uint32_t (&r)[W]) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(a));
   }
 }
+__device__ __forceinline__ uint32_t few_lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ uint32_t few_lds16(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
@@ -123,13 +130,19 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The value at this CTA's shared address in CTA `rank` of the cluster.
-__device__ __forceinline__ float cluster_ld(const float* p, uint32_t rank) {
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+// Store to this CTA's shared address in CTA `rank` of the cluster.
+__device__ __forceinline__ void cluster_st(float* p, uint32_t rank, float v) {
   uint32_t at;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
-  return v;
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ void cluster_st4(float* p, uint32_t rank, const float4& v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
 // Byte offset of chunk c of row r in a plane's tile: rows of 16 kChunks bytes, the chunks
@@ -149,7 +162,7 @@ __device__ __forceinline__ void split_bf16x2(float x0, float x1, uint32_t& hi, u
 }
 
 template <int FMT, int D, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_constant__ SeqAttnArgs a) {
+__global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 4) attn_few_kernel(const __grid_constant__ SeqAttnArgs a) {
   using S = FewShape<FMT, D>;
   constexpr int NG = D / 32;
   extern __shared__ uint8_t smem_raw[];
@@ -183,6 +196,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
       }
     return;
   }
+  if (cluster_size() > 1) cluster_arrive();  // waited for before the first store to another CTA
   const int p0 = base + i0, p1 = base + i1;
   KeyBlocks kb{0, 0, 0};
   if (p1 >= 0) kb = key_blocks(p0, p1, a.window, a.sinks);
@@ -199,10 +213,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
     const int tile = i + lane / S::kBlocks;
     const int blk = (tile0 + warp + WARPS * tile) * S::kBlocks + lane % S::kBlocks;
     if (tile >= my_tiles || blk >= kb.count) return -2;
-    const int key = kb.block_of(blk) * 16;
-    const int page = table[key / c.page_size];
+    const int at = kb.block_of(blk), pg = static_cast<int>(fast_div(static_cast<uint32_t>(at), a.page_blocks));
+    const int page = table[pg];
     if (page < 0 || page >= c.num_pages) return -1;
-    return (page * c.num_kv_heads + kvh) * c.page_size + key % c.page_size;
+    return (page * c.num_kv_heads + kvh) * c.page_size + (at - pg * static_cast<int>(a.page_blocks.d)) * 16;
   };
   int rows_now = find_rows(0), rows_next = find_rows(kBatch);
   bool bad_page = rows_now == -1;
@@ -219,7 +233,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
       const uint8_t* vs = static_cast<const uint8_t*>(c.v) + static_cast<int64_t>(row0) * S::kRow;
       uint8_t* dk = st + sub * 16 * S::kRow;
 #pragma unroll
-      for (int j = lane; j < 16 * S::kChunks; j += 32) {
+      for (int jj = 0; jj < (16 * S::kChunks + 31) / 32; ++jj) {
+        const int j = lane + 32 * jj;
         const uint32_t off = few_off<S::kChunks>(j / S::kChunks, j % S::kChunks);
         cp_async_16(dk + off, ks + 16 * j);
         cp_async_16(dk + S::kPlane + off, vs + 16 * j);
@@ -236,75 +251,94 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
     }
   };
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-  if (my_tiles > 0) issue(0);
-  commit();
+#pragma unroll 1
+  for (int i = 0; i < S::kStages - 1; ++i) {
+    if (i < my_tiles) issue(i);
+    commit();
+  }
 
-  // ---------------- queries: into the cache's space, scaled to 2^10 .. 2^11, split
-  for (int n = warp; n < 8; n += WARPS) {
-    float x[NG];
-    const int col = 8 * cb + n;
-    const bool live = n < cols;
-    const int64_t at = live ? static_cast<int64_t>(sr.first + col / a.group) * a.q.ts +
-                                  static_cast<int64_t>(kvh * a.group + col % a.group) * a.q.hs
-                            : 0;
+  // ---------------- queries: into the cache's space, scaled to 2^10 .. 2^11, fp16 (bf16
+  // rows: two bf16 halves).  Lane
+  // (column l & 7, eighth l >> 3) holds 8 values of a group of 32; a warp has the groups
+  // warp, warp + 4, ... (TQ4, whose rotation spans the row: it works out all and writes these).
+  {
+    const int n = lane & 7, eighth = lane >> 3, col = 8 * cb + n;
+    constexpr bool kAll = FMT == kFewTq4;
+    constexpr int kMine = kAll ? NG : (NG + WARPS - 1) / WARPS;
+    const int64_t q_at = static_cast<int64_t>(sr.first + col / a.group) * a.q.ts +
+                         static_cast<int64_t>(kvh * a.group + col % a.group) * a.q.hs + 8 * eighth;
+    float x[kMine][8];
+    if constexpr (kAll) {
+      seq_load_row<NG>(a.q, n < cols ? q_at : -1, x);
+      seq_turn<NG, true>(x, static_cast<const uint32_t*>(c.signs), lane, false);
+    } else {
 #pragma unroll
-    for (int G = 0; G < NG; ++G) x[G] = live ? load_act(a.q.data, a.q.dtype, at + 32 * G + lane) : 0.f;
-    if (c.format == KVQ_FMT_Q4_HAD32) {
-#pragma unroll
-      for (int G = 0; G < NG; ++G) x[G] = warp_fwht32(x[G], lane) * kHadamardScale;
-    } else if (FMT == kFewTq4) {
-      tq4_turn_lanes<NG>(x, static_cast<const uint32_t*>(c.signs), lane, false);
+      for (int k = 0; k < kMine; ++k)
+        seq_load_row<1>(a.q, n < cols && warp + WARPS * k < NG ? q_at + 32 * (warp + WARPS * k) : -1,
+                        reinterpret_cast<float(&)[1][8]>(x[k]));
+      if (c.format == KVQ_FMT_Q4_HAD32) seq_turn<kMine, false>(x, nullptr, lane, false);
     }
     float top = 0.f;
 #pragma unroll
-    for (int G = 0; G < NG; ++G) {
-      x[G] *= a.qscale;
-      top = fmaxf(top, fabsf(x[G]));
-    }
+    for (int k = 0; k < kMine; ++k)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if constexpr (FMT == kFewBf16) {
-      // lane holds elements 32 G + lane; pairs by the neighbour
-#pragma unroll
-      for (int G = 0; G < NG; ++G) {
-        const float y = __shfl_down_sync(0xffffffffu, x[G], 1);
-        if ((lane & 1) == 0) {
-          uint32_t hi, lo;
-          split_bf16x2(x[G], y, hi, lo);
-          const int e = lane & 15, step = 2 * G + (lane >> 4);  // element e of the step: b0 0 .. 7, b1 8 .. 15
-          uint32_t* f = reinterpret_cast<uint32_t*>(&sm.qf[step][n * 4 + ((e & 7) >> 1)]);
-          f[e >> 3] = hi;
-          f[2 + (e >> 3)] = lo;
-        }
+      for (int e = 0; e < 8; ++e) {
+        x[k][e] *= a.qscale;
+        top = fmaxf(top, fabsf(x[k][e]));
       }
-      if (lane == 0) sm.factor[n] = 1.f;
-    } else {
+    if constexpr (FMT != kFewBf16) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+      if constexpr (!kAll) {
+        if (eighth == 0) sm.fm[warp][n] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) top = fmaxf(top, sm.fm[w][n]);
+      }
+    }
+    float up = 1.f, unit = 1.f;
+    if constexpr (FMT != kFewBf16) {
       // a power of two takes the largest element to [2^10, 2^11); NaN and infinities stay
       int ex = 0;
       if (top > 0.f && top < INFINITY) ex = 10 - (static_cast<int>(__float_as_uint(fmaxf(top, 1e-30f)) >> 23) - 127);
-      const float up = __uint_as_float(static_cast<uint32_t>(min(ex, 110) + 127) << 23);
+      up = __uint_as_float(static_cast<uint32_t>(min(ex, 110) + 127) << 23);
+      unit = (FMT == kFewQ4 ? 4194304.f : 1.f) / up;
+    }
 #pragma unroll
-      for (int G = 0; G < NG; ++G) {
-        const int j = lane & 7;
-        // element 8 t + j of group G in the order in which the codes come out of their words
-        const int step = FMT == kFewQ4 ? 2 * G + ((j & 3) >> 1) : 2 * G + (j >> 2);
-        const int reg = FMT == kFewQ4 ? j & 1 : (j >> 1) & 1;
-        const int half = FMT == kFewQ4 ? j >> 2 : j & 1;
-        const float y = x[G] * up * (FMT == kFewQ4 && reg ? 0.0625f : 1.f);
-        const __half hi = __float2half_rn(y);
-        const __half lo = __float2half_rn(y - __half2float(hi));
-        __half* f = reinterpret_cast<__half*>(&sm.qf[step][n * 4 + (lane >> 3)]);
-        f[2 * reg + half] = hi;
-        f[4 + 2 * reg + half] = lo;
+    for (int k = 0; k < kMine; ++k) {
+      const int G = kAll ? k : warp + WARPS * k;
+      if (G % WARPS != warp || G >= NG) continue;
+      uint32_t hi[4];
+      if constexpr (FMT == kFewBf16) {
+        // elements 8 eighth .. + 7 of the group: pairs t of the step 2G + eighth / 2, its B register eighth % 2
+#pragma unroll
+        for (int t4 = 0; t4 < 4; ++t4) {
+          uint32_t lo;
+          split_bf16x2(x[k][2 * t4], x[k][2 * t4 + 1], hi[t4], lo);
+          uint32_t* f = reinterpret_cast<uint32_t*>(&sm.qf[2 * G + (eighth >> 1)][n * 4 + t4]);
+          f[eighth & 1] = hi[t4];
+          f[2 + (eighth & 1)] = lo;
+        }
+      } else {
+        // the order in which the codes come out of their words: 4-bit groups (0, 4) (1, 5) / 16
+        // (2, 6) (3, 7) / 16, TQ4 in turn
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y0 = x[k][FMT == kFewQ4 ? i : 2 * i] * up, y1 = x[k][FMT == kFewQ4 ? i + 4 : 2 * i + 1] * up;
+          const float part = FMT == kFewQ4 && (i & 1) ? 0.0625f : 1.f;
+          hi[i] = pack_half2(y0 * part, y1 * part);
+          if constexpr (FMT == kFewQ4) sum += (half_lo(hi[i]) + half_hi(hi[i])) * (i & 1 ? 16.f : 1.f);
+        }
+        sm.qf[G][n * 4 + eighth] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         if constexpr (FMT == kFewQ4) {
-          float sum = (__half2float(hi) + __half2float(lo)) * (reg ? 16.f : 1.f);
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          if (lane == 0) reinterpret_cast<float*>(&sm.bias[G][n >> 1])[n & 1] = sum * -1.9073486328125e-06f;  // -8 2^-22
+          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          if (eighth == 0) reinterpret_cast<float*>(&sm.bias[G][n >> 1])[n & 1] = sum * -1.9073486328125e-06f;  // -8 2^-22
         }
       }
-      if (lane == 0) sm.factor[n] = (FMT == kFewQ4 ? 4194304.f : 1.f) / up;
     }
+    if (warp == 0 && lane < 8) sm.factor[n] = unit;
   }
   __syncthreads();
 
@@ -324,17 +358,18 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
 
 #pragma unroll 1
   for (int i = 0; i < my_tiles; ++i) {
-    // ---- the next tile's loads, then wait for this one's
-    if (i + 1 < my_tiles) {
-      if ((i + 1) % kBatch == 0) {
+    // ---- the loads of a tile ahead, then wait for this one's
+    const int ahead = i + S::kStages - 1;
+    if (ahead < my_tiles) {
+      if (ahead % kBatch == 0) {
         rows_now = rows_next;
-        rows_next = find_rows(i + 1 + kBatch);
+        rows_next = find_rows(ahead + kBatch);
         bad_page |= rows_now == -1;
       }
-      issue(i + 1);
+      issue(ahead);
     }
     commit();
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
     __syncwarp();
 
     const uint8_t* st = ring + (i % S::kStages) * S::kStage;
@@ -357,7 +392,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
     if constexpr (FMT == kFewBf16) {
       float sl[S::kBlocks][4] = {};
       const int kr = (lane & 7) + 8 * ((lane >> 3) & 1), kc = lane >> 4;
-#pragma unroll
+#pragma unroll 4
       for (int ks = 0; ks < S::kSteps; ++ks) {
         const uint4 q = few_lds128(qf + ks * 512);
 #pragma unroll
@@ -376,25 +411,24 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
       // ldmatrix: matrices (keys 0-7, chunk 2u), (keys 8-15, 2u), (keys 0-7, 2u + 1), (keys 8-15, 2u + 1)
       const int lr = lane & 15, lc = lane >> 4;
       float sl[S::kBlocks][4] = {};
-      constexpr int kSW = FMT == kFewQ4 ? D / 64 : 1;  // words of a key's scales
-      uint32_t sk[S::kBlocks][2][kSW];
-      if constexpr (FMT == kFewQ4) {
-#pragma unroll
-        for (int sub = 0; sub < S::kBlocks; ++sub) {
-          few_lds<kSW>(ksc + (sub * 16 + g) * S::kScaleRow, sk[sub][0]);
-          few_lds<kSW>(ksc + (sub * 16 + g + 8) * S::kScaleRow, sk[sub][1]);
-        }
-      }
-#pragma unroll
+#pragma unroll 1
       for (int u = 0; u < D / 64; ++u) {
         uint32_t r[S::kBlocks][4];
+        uint32_t sk[S::kBlocks][2];  // two groups' scales of keys g, g + 8
+#pragma unroll
+        for (int sub = 0; sub < S::kBlocks; ++sub) {
+          if constexpr (FMT == kFewQ4) {
+            sk[sub][0] = few_lds32(ksc + (sub * 16 + g) * S::kScaleRow + 4 * u);
+            sk[sub][1] = few_lds32(ksc + (sub * 16 + g + 8) * S::kScaleRow + 4 * u);
+          }
+        }
 #pragma unroll
         for (int sub = 0; sub < S::kBlocks; ++sub)
           few_ldsm(kbase + sub * 16 * S::kRow + few_off<S::kChunks>(lr, 2 * u + lc), r[sub]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int G = 2 * u + e;
-          const uint4 qa = few_lds128(qf + (2 * G) * 512), qb = few_lds128(qf + (2 * G + 1) * 512);
+          const uint4 qa = few_lds128(qf + G * 512);  // B of the group's two steps
           if constexpr (FMT == kFewQ4) {
             const float2 bi = sm.bias[G][t];
 #pragma unroll
@@ -405,11 +439,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
               const uint32_t c0 = ah & kCodeLo, c1 = bh & kCodeLo, c2 = ah & kCodeHi, c3 = bh & kCodeHi;
               float d[4];
               mma_f16_c(d, a0, a1, a2, a3, qa.x, qa.y, bi.x, bi.y, bi.x, bi.y);
-              mma_f16(d, c0, c1, c2, c3, qb.x, qb.y);
-              mma_f16(d, a0, a1, a2, a3, qa.z, qa.w);
-              mma_f16(d, c0, c1, c2, c3, qb.z, qb.w);
-              const float sg = e ? half_hi(sk[sub][0][u]) : half_lo(sk[sub][0][u]);
-              const float sh = e ? half_hi(sk[sub][1][u]) : half_lo(sk[sub][1][u]);
+              mma_f16(d, c0, c1, c2, c3, qa.z, qa.w);
+              const float sg = e ? half_hi(sk[sub][0]) : half_lo(sk[sub][0]);
+              const float sh = e ? half_hi(sk[sub][1]) : half_lo(sk[sub][1]);
               s[sub][0] = fmaf(sg, d[0], s[sub][0]);
               s[sub][1] = fmaf(sg, d[1], s[sub][1]);
               s[sub][2] = fmaf(sh, d[2], s[sub][2]);
@@ -420,9 +452,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
             for (int sub = 0; sub < S::kBlocks; ++sub) {
               const uint4 A = tq4_levels8(r[sub][2 * e]), B = tq4_levels8(r[sub][2 * e + 1]);
               mma_f16(s[sub], A.x, B.x, A.y, B.y, qa.x, qa.y);
-              mma_f16(sl[sub], A.x, B.x, A.y, B.y, qa.z, qa.w);
-              mma_f16(s[sub], A.z, B.z, A.w, B.w, qb.x, qb.y);
-              mma_f16(sl[sub], A.z, B.z, A.w, B.w, qb.z, qb.w);
+              mma_f16(sl[sub], A.z, B.z, A.w, B.w, qa.z, qa.w);
             }
           }
         }
@@ -502,15 +532,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
     if constexpr (FMT == kFewQ4) {
       constexpr int kSW = D / 64;
       uint32_t w[kSW];
-      few_lds<kSW>(vsc + lane * S::kScaleRow, w);
+      few_lds<kSW>(vsc + (lane & (S::kKeys - 1)) * S::kScaleRow, w);
       __half2 h = u32_as_h2(w[0]);
 #pragma unroll
       for (int k = 1; k < kSW; ++k) h = __hmax2(h, u32_as_h2(w[k]));
       const float top = fmaxf(__low2float(h), __high2float(h));
-      lsv = fminf(fmaxf(log2f(top), -10.f), 16.f);
+      lsv = fminf(fmaxf(__log2f(top), -10.f), 16.f);
       wide = lsv > 4.f;
     } else if constexpr (FMT == kFewTq4) {
-      lsv = fminf(fmaxf(log2f(half_of(few_lds16(vsc + 2 * lane))), -60.f), 16.f);
+      lsv = fminf(fmaxf(__log2f(half_of(few_lds16(vsc + 2 * (lane & (S::kKeys - 1))))), -60.f), 16.f);
     }
 
     // ---------------- online softmax (base 2)
@@ -706,9 +736,9 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 8 * D; i += WARPS * 32) {
-    const int n = i / D, e = i % D;
-    float M = -INFINITY, Z = 0.f, A = 0.f;
+  if (threadIdx.x < 8) {
+    const int n = threadIdx.x;
+    float M = -INFINITY, Z = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm.fm[w][n]);
 #pragma unroll
@@ -716,51 +746,126 @@ __global__ void __launch_bounds__(WARPS * 32, 1) attn_few_kernel(const __grid_co
       // (a NaN sum goes on even where no score of its warp was a number)
       const float f = sm.fm[w][n] == -INFINITY ? (sm.fz[w][n] == sm.fz[w][n] ? 0.f : NAN) : fast_exp2(sm.fm[w][n] - M);
       Z = fmaf(sm.fz[w][n], f, Z);
-      A = fmaf(sm.fold[w][n][e], f, A);
+      sm.fw[w][n] = f;
     }
-    sm.acc[n][e] = A;
-    if (e == 0) sm.m[n] = M, sm.z[n] = Z;
+    sm.m_own[n] = M;
+    sm.z_own[n] = Z;
   }
+  __syncthreads();
+  // The CTA's partial goes piece by piece to the CTAs of the cluster that fold and store it: a
+  // piece is a column's group of 32 values (TQ4: the whole column, which its rotation spans),
+  // piece i is CTA i % cs's.  Stores to another CTA's shared memory wait for nothing.
   const uint32_t cs = cluster_size(), rank = cluster_rank();
+  constexpr bool kWhole = FMT == kFewTq4;
+  constexpr int kPiece = kWhole ? D : 32, kPieces = 8 * D / kPiece;
+  if (cs > 1) cluster_wait();  // (every CTA has begun)
+  const int per_cta = kPieces / static_cast<int>(cs);
+#pragma unroll 2
+  for (int i = 4 * threadIdx.x; i < 8 * D; i += 4 * WARPS * 32) {
+    const int n = i / D, e = i % D, piece = i / kPiece;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      const float f = sm.fw[w][n];
+      const float4 v = *reinterpret_cast<const float4*>(&sm.fold[w][n][e]);
+      A.x = fmaf(v.x, f, A.x);
+      A.y = fmaf(v.y, f, A.y);
+      A.z = fmaf(v.z, f, A.z);
+      A.w = fmaf(v.w, f, A.w);
+    }
+    const uint32_t owner = static_cast<uint32_t>(piece) % cs;
+    cluster_st4(&sm.acc[(static_cast<int>(rank) * per_cta + piece / static_cast<int>(cs)) * kPiece + i % kPiece], owner, A);
+  }
+  // (the references and sums to everybody)
+  for (int i = threadIdx.x; i < 8 * static_cast<int>(cs); i += WARPS * 32) {
+    cluster_st(&sm.m[rank][i & 7], i >> 3, sm.m_own[i & 7]);
+    cluster_st(&sm.z[rank][i & 7], i >> 3, sm.z_own[i & 7]);
+  }
   if (cs > 1) cluster_sync_all();
   else __syncthreads();
 
-  // ---------------- the cluster's partials: CTA `rank` takes every cs-th piece
+  // ---------------- the cluster's partials of this CTA's pieces, folded in order
   const int range = blockIdx.x / cs, ranges = gridDim.x / cs;
-  constexpr bool kWhole = FMT == kFewTq4;  // its rotation spans the row
-  for (int item = rank * WARPS + warp; item < (kWhole ? cols : cols * NG); item += cs * WARPS) {
-    const int n = kWhole ? item : item / NG;
-    float M = -INFINITY, Z = 0.f;
-    for (uint32_t r = 0; r < cs; ++r) M = fmaxf(M, cs > 1 ? cluster_ld(&sm.m[n], r) : sm.m[n]);
-    float x[kWhole ? NG : 1] = {};
-    for (uint32_t r = 0; r < cs; ++r) {
-      const float mr = cs > 1 ? cluster_ld(&sm.m[n], r) : sm.m[n], zr = cs > 1 ? cluster_ld(&sm.z[n], r) : sm.z[n];
+  // (a piece of 32 by eight lanes, four values each; a column by a warp, D / 32 values each)
+  constexpr int kLanes = kWhole ? 32 : 8, kV = kWhole ? NG : 4;
+  const int sub = lane % kLanes;
+#pragma unroll 1
+  for (int local0 = warp * (32 / kLanes); local0 < per_cta; local0 += WARPS * (32 / kLanes)) {
+    const int local = min(local0 + lane / kLanes, per_cta - 1);  // (the last one again, where there are fewer)
+    const int piece = local * static_cast<int>(cs) + static_cast<int>(rank), n = piece * kPiece / D;
+    float M = -INFINITY, Z = 0.f, x[kV] = {};
+#pragma unroll 4
+    for (int r = 0; r < static_cast<int>(cs); ++r) M = fmaxf(M, sm.m[r][n]);
+#pragma unroll 4
+    for (int r = 0; r < static_cast<int>(cs); ++r) {
+      const float mr = sm.m[r][n], zr = sm.z[r][n];
       const float f = mr == -INFINITY ? (zr == zr ? 0.f : NAN) : fast_exp2(mr - M);
       Z = fmaf(zr, f, Z);
+      const float* at = &sm.acc[(r * per_cta + local) * kPiece];
+      if constexpr (kWhole) {
 #pragma unroll
-      for (int k = 0; k < (kWhole ? NG : 1); ++k) {
-        const float* at = &sm.acc[n][32 * (kWhole ? k : item % NG) + lane];
-        x[k] = fmaf(cs > 1 ? cluster_ld(at, r) : *at, f, x[k]);
+        for (int k = 0; k < kV; ++k) x[k] = fmaf(at[32 * k + sub], f, x[k]);
+      } else {
+        const float4 v = *reinterpret_cast<const float4*>(at + 4 * sub);
+        x[0] = fmaf(v.x, f, x[0]);
+        x[1] = fmaf(v.y, f, x[1]);
+        x[2] = fmaf(v.z, f, x[2]);
+        x[3] = fmaf(v.w, f, x[3]);
       }
     }
     const int col = 8 * cb + n, row = sr.first + col / a.group, head = kvh * a.group + col % a.group;
+    const int e0 = kWhole ? 0 : piece * 32 % D + 4 * sub;
+    const bool live = n < cols;
     if (ranges > 1) {
+      if (!live) continue;
       const int64_t part = (static_cast<int64_t>(range) * a.n_rows + row) * a.Hq + head;
-      if (lane == 0 && (kWhole || item % NG == 0)) a.ws_m[part] = M, a.ws_z[part] = Z;
+      if (sub == 0 && e0 == 0) a.ws_m[part] = M, a.ws_z[part] = Z;
+      if constexpr (kWhole) {
 #pragma unroll
-      for (int k = 0; k < (kWhole ? NG : 1); ++k) a.ws_acc[part * D + 32 * (kWhole ? k : item % NG) + lane] = x[k];
+        for (int k = 0; k < kV; ++k) a.ws_acc[part * D + 32 * k + sub] = x[k];
+      } else {
+        *reinterpret_cast<float4*>(a.ws_acc + part * D + e0) = make_float4(x[0], x[1], x[2], x[3]);
+      }
       continue;
     }
     const float inv = Z == 0.f ? 0.f : 1.f / Z;
 #pragma unroll
-    for (int k = 0; k < (kWhole ? NG : 1); ++k) x[k] *= inv;
-    if constexpr (kWhole) tq4_turn_lanes<(kWhole ? NG : 1)>(x, static_cast<const uint32_t*>(c.signs), lane, true);
-    else if (c.format == KVQ_FMT_Q4_HAD32) x[0] = warp_fwht32(x[0], lane) * kHadamardScale;
+    for (int k = 0; k < kV; ++k) x[k] *= inv;
+    if constexpr (kWhole) {
+      tq4_turn_lanes<kV>(x, static_cast<const uint32_t*>(c.signs), lane, true);
+      if (live) {
 #pragma unroll
-    for (int k = 0; k < (kWhole ? NG : 1); ++k)
-      seq_store(a, row, head, 32 * (kWhole ? k : item % NG) + lane, x[k]);
+        for (int k = 0; k < kV; ++k) seq_store(a, row, head, 32 * k + sub, x[k]);
+      }
+    } else {
+      if (c.format == KVQ_FMT_Q4_HAD32) {
+        const float s0 = x[0] + x[1], d0 = x[0] - x[1], s1 = x[2] + x[3], d1 = x[2] - x[3];
+        x[0] = s0 + s1;
+        x[1] = d0 + d1;
+        x[2] = s0 - s1;
+        x[3] = d0 - d1;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float y = __shfl_xor_sync(0xffffffffu, x[k], o);
+            x[k] = lane & o ? y - x[k] : x[k] + y;
+          }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] *= kHadamardScale;
+      }
+      if (live) {
+        const int64_t at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + e0;
+        if (a.out.wide && a.out.dtype == KVQ_DT_BF16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out.data) + at) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+        else if (a.out.wide)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out.data) + at) = make_float4(x[0], x[1], x[2], x[3]);
+        else
+#pragma unroll
+          for (int k = 0; k < 4; ++k) seq_store(a, row, head, e0 + k, x[k]);
+      }
+    }
   }
-  if (cs > 1) cluster_sync_all();  // (its shared memory is read until here)
 }
 
 // The ranges' partials of every row and head, folded in order, rotated back and rounded: a
@@ -813,15 +918,19 @@ cudaError_t launch_attn_merge(const SeqAttnArgs& a, int ranges, cudaStream_t s) 
 
 FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
                  int n_sm) {
-  const int group = Hq / c.num_kv_heads;
+  const int group = Hq / c.num_kv_heads, D = c.head_dim;
   const int64_t blocks = static_cast<int64_t>(num_seqs) * c.num_kv_heads * ((static_cast<int64_t>(max_rows) * group + 7) / 8);
   int64_t keys = max_seq_len;
   if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + 64 + 8 / group);
-  FewPlan p{1, 1, 4};
-  const int64_t want = std::max<int64_t>(1, (2 * static_cast<int64_t>(n_sm) + blocks - 1) / std::max<int64_t>(blocks, 1));
-  const int64_t most = std::max<int64_t>(1, keys / 128);  // a tile for every warp
+  // One wave of CTAs: four of the 4-bit rows' to an SM (registers), of the bf16 rows' as many as
+  // their rings leave room for.
+  const int fit = c.format != KVQ_FMT_BF16 ? 4 : D == 256 ? 1 : D == 128 ? 2 : 4;
+  const int64_t want = std::max<int64_t>(1, fit * static_cast<int64_t>(n_sm) / std::max<int64_t>(blocks, 1));
+  const int64_t most = std::max<int64_t>(1, (keys + 63) / 64);  // a block for every warp
   const int64_t splits = std::min(want, most);
-  while (p.cluster < 8 && p.cluster * 2 <= splits) p.cluster *= 2;
+  FewPlan p{1, 1, 4};
+  const int widest = c.format == KVQ_FMT_TQ4 ? 8 : 16;  // (a CTA for every piece that is folded)
+  while (p.cluster < widest && p.cluster * 2 <= splits) p.cluster *= 2;
   p.ranges = static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(1, splits / p.cluster)));
   return p;
 }
@@ -832,6 +941,8 @@ static cudaError_t launch_few(const SeqAttnArgs& a, const FewPlan& p, cudaStream
   const size_t smem = sizeof(FewSmem<FMT, D, WARPS>) + 128;
   static_assert(sizeof(FewSmem<FMT, D, WARPS>) + 128 <= 232448, "shared memory");
   cudaError_t e = set_max_smem_once<kern>(static_cast<int>(smem));
+  if (e == cudaSuccess && p.cluster > 8)  // (opted into by the kernel)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   const int64_t cbs = (static_cast<int64_t>(a.max_rows) * a.group + 7) / 8;
   cudaLaunchConfig_t cfg = {};

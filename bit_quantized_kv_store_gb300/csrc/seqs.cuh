@@ -3,7 +3,7 @@
 // and the row at position p sees key j when j <= p and, with a window, j > p - window or
 // j < sinks.  Shared by the attention kernels over ragged batches.
 #pragma once
-#include "kernels.cuh"
+#include "rows.cuh"
 
 namespace kvq {
 
@@ -107,6 +107,102 @@ __device__ __forceinline__ void seq_store(const SeqAttnArgs& a, int row, int hea
   const int64_t at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + e;
   if (a.out.dtype == KVQ_DT_F32) static_cast<float*>(a.out.data)[at] = y;
   else static_cast<__nv_bfloat16*>(a.out.data)[at] = __float2bfloat16_rn(y);
+}
+
+// 8 values of every group of 32 of a row, the first of them element `at` of the view (< 0:
+// zeros).
+template <int NG>
+__device__ __forceinline__ void seq_load_row(const RowsView& v, int64_t at, float (&x)[NG][8]) {
+  if (at < 0) {
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[G][e] = 0.f;
+  } else if (v.dtype == KVQ_DT_BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(v.data) + at;
+    uint32_t w[NG][4];
+#pragma unroll
+    for (int G = 0; G < NG; ++G) {
+      if (v.wide) {
+        ld_words<4>(p + 32 * G, w[G]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[G][i] = p[32 * G + 2 * i] | static_cast<uint32_t>(p[32 * G + 2 * i + 1]) << 16;
+      }
+    }
+#pragma unroll
+    for (int G = 0; G < NG; ++G)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[G][2 * i] = __uint_as_float(w[G][i] << 16);
+        x[G][2 * i + 1] = __uint_as_float(w[G][i] & 0xFFFF0000u);
+      }
+  } else {
+    const float* p = static_cast<const float*>(v.data) + at;
+#pragma unroll
+    for (int G = 0; G < NG; ++G) {
+      if (v.wide) {
+        ld_words<8>(p + 32 * G, reinterpret_cast<uint32_t*>(x[G]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[G][e] = p[32 * G + e];
+      }
+    }
+  }
+}
+
+// The rows' rotation (ALL: the D-point one with signs, else each group's), for rows whose
+// elements 32 G + 8 (lane >> 3) + e are x[G][e].
+template <int NG, bool ALL>
+__device__ __forceinline__ void seq_turn(float (&x)[NG][8], const uint32_t* signs, int lane, bool inverse) {
+  auto flip = [&] {
+#pragma unroll
+    for (int G = 0; G < NG; ++G) {
+      const uint32_t s = signs[G] >> (8 * (lane >> 3));
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if ((s >> e) & 1u) x[G][e] = -x[G][e];
+    }
+  };
+  if (ALL && !inverse) flip();
+#pragma unroll
+  for (int G = 0; G < NG; ++G) {
+#pragma unroll
+    for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!(e & h)) {
+          const float u = x[G][e], v = x[G][e + h];
+          x[G][e] = u + v;
+          x[G][e + h] = u - v;
+        }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = __shfl_xor_sync(0xffffffffu, x[G][e], o);
+        x[G][e] = lane & o ? y - x[G][e] : x[G][e] + y;
+      }
+  }
+  if constexpr (ALL) {
+#pragma unroll
+    for (int h = 1; h < NG; h <<= 1)
+#pragma unroll
+      for (int G = 0; G < NG; ++G)
+        if (!(G & h))
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float u = x[G][e], v = x[G + h][e];
+            x[G][e] = u + v;
+            x[G + h][e] = u - v;
+          }
+  }
+  const float c = !ALL ? kHadamardScale : NG == 8 ? 0.0625f : NG == 4 ? 0.08838834764831845f : 0.125f;
+#pragma unroll
+  for (int G = 0; G < NG; ++G)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[G][e] *= c;
+  if (ALL && inverse) flip();
 }
 
 }  // namespace kvq
