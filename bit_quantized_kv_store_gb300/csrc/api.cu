@@ -1079,6 +1079,7 @@ static int32_t attn_impl(const kvq_cache* cache, const kvq_rows* q, int32_t n_ro
   a.qscale = sm_scale * kLog2e;
   a.status = d_status;
   a.page_blocks = make_fastdiv(static_cast<uint32_t>(cache->page_size / 16));
+  a.per = w.chunk ? 0 : w.few.per;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.ws_m = reinterpret_cast<float*>(ws + w.m_off);
   a.ws_z = reinterpret_cast<float*>(ws + w.z_off);

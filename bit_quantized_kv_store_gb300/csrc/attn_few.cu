@@ -196,13 +196,27 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
       }
     return;
   }
-  if (cluster_size() > 1) cluster_arrive();  // waited for before the first store to another CTA
   const int p0 = base + i0, p1 = base + i1;
   KeyBlocks kb{0, 0, 0};
   if (p1 >= 0) kb = key_blocks(p0, p1, a.window, a.sinks);
-  const int all_tiles = (kb.count + S::kBlocks - 1) / S::kBlocks;
-  const int tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * blockIdx.x / gridDim.x);
-  const int tile1 = static_cast<int>(static_cast<int64_t>(all_tiles) * (blockIdx.x + 1) / gridDim.x);
+  // its part of the blocks: a share, or (ragged sequences) so many of them
+  const int all_tiles = kb.count;
+  int tile0, tile1, ranges;
+  if (a.per > 0) {
+    tile0 = min(all_tiles, a.per * static_cast<int>(blockIdx.x));
+    tile1 = min(all_tiles, tile0 + a.per);
+    ranges = max(1, (all_tiles + a.per - 1) / a.per);
+    if (static_cast<int>(blockIdx.x) >= ranges) {
+      pdl_wait();
+      pdl_trigger();
+      return;
+    }
+  } else {
+    tile0 = static_cast<int>(static_cast<int64_t>(all_tiles) * blockIdx.x / gridDim.x);
+    tile1 = static_cast<int>(static_cast<int64_t>(all_tiles) * (blockIdx.x + 1) / gridDim.x);
+    ranges = gridDim.x / cluster_size();
+  }
+  if (cluster_size() > 1) cluster_arrive();  // waited for before the first store to another CTA
   const int my_tiles = tile1 - tile0 > warp ? (tile1 - tile0 - warp + WARPS - 1) / WARPS : 0;
 
   // This warp's tiles are tile0 + warp + WARPS i.  Lane l holds the cache row of block l of
@@ -785,7 +799,7 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
   else __syncthreads();
 
   // ---------------- the cluster's partials of this CTA's pieces, folded in order
-  const int range = blockIdx.x / cs, ranges = gridDim.x / cs;
+  const int range = blockIdx.x / cs;
   // (a piece of 32 by eight lanes, four values each; a column by a warp, D / 32 values each)
   constexpr int kLanes = kWhole ? 32 : 8, kV = kWhole ? NG : 4;
   const int sub = lane % kLanes;
@@ -880,6 +894,12 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__
   const int i = blockIdx.x * 4 + warp;
   if (sr.state != kRowsOk || i >= sr.n * a.Hq) return;
   const int row = sr.first + i / a.Hq, head = i % a.Hq;
+  if (a.per > 0) {  // as many as the column's block was cut into; one: stored already
+    const int cb = (i / a.Hq * a.group + head % a.group) >> 3, base = sr.T - sr.n;
+    const int p1 = base + (min(8 * cb + 8, sr.n * a.group) - 1) / a.group;
+    ranges = p1 < 0 ? 1 : (key_blocks(base + 8 * cb / a.group, p1, a.window, a.sinks).count + a.per - 1) / a.per;
+    if (ranges <= 1) return;
+  }
   const int64_t stride = static_cast<int64_t>(a.n_rows) * a.Hq, part = static_cast<int64_t>(row) * a.Hq + head;
   float M = -INFINITY, Z = 0.f, x[NG] = {};
   for (int r = lane; r < ranges; r += 32) M = fmaxf(M, a.ws_m[part + r * stride]);
@@ -928,10 +948,30 @@ FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max
   const int64_t want = std::max<int64_t>(1, fit * static_cast<int64_t>(n_sm) / std::max<int64_t>(blocks, 1));
   const int64_t most = std::max<int64_t>(1, (keys + 63) / 64);  // a block for every warp
   const int64_t splits = std::min(want, most);
-  FewPlan p{1, 1, 4};
+  FewPlan p{1, 1, 0};
+  if (window == 0 && num_seqs > 1) {
+    // Sequences of any lengths: so many blocks of 16 keys a CTA, that sequences of half the
+    // longest fill a wave (16 of 8000 tokens, 1 to 5 rows of 6 heads: equal shares 108 us,
+    // so 64).  At least eight blocks for every warp, at most 32 ranges.
+    const int64_t all = (keys + 15) / 16;
+    int64_t per = (all * blocks / 2 + fit * static_cast<int64_t>(n_sm) - 1) / (fit * static_cast<int64_t>(n_sm));
+    per = std::max<int64_t>(std::max<int64_t>(per, 32), (all + 31) / 32);
+    p.per = static_cast<int>((per + 3) / 4 * 4);
+    p.ranges = static_cast<int>(std::max<int64_t>(1, (all + p.per - 1) / p.per));
+    if (p.ranges == 1) p.per = 0;
+    return p;
+  }
   const int widest = c.format == KVQ_FMT_TQ4 ? 8 : 16;  // (a CTA for every piece that is folded)
   while (p.cluster < widest && p.cluster * 2 <= splits) p.cluster *= 2;
-  p.ranges = static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(1, splits / p.cluster)));
+  // Further clusters only where they save more than their fold costs (a second launch, about
+  // 3 us; a block takes a warp about 1.2 us): a window of 4096 keys of one sequence, 16 CTAs
+  // 11.5 us, 64 CTAs 12.5 us.
+  const int64_t most_ranges = std::min<int64_t>(64, splits / p.cluster);
+  double least = 0;
+  for (int64_t r = 1; r <= most_ranges; ++r) {
+    const double cost = 1.2 * static_cast<double>((keys + 64 * p.cluster * r - 1) / (64 * p.cluster * r)) + (r > 1 ? 3 + 0.05 * r : 0);
+    if (r == 1 || cost < least) least = cost, p.ranges = static_cast<int>(r);
+  }
   return p;
 }
 

@@ -170,6 +170,7 @@ struct SeqAttnArgs {
   float qscale;  // sm_scale * log2(e)
   int32_t* status;
   FastDiv page_blocks;  // 16-key blocks of a page
+  int per;  // attn_few: FewPlan::per
   // more than one cluster for a block of columns: partials [ranges][n_rows][Hq], contexts
   // [ranges][n_rows][Hq][head_dim] (unnormalised, in the cache's space)
   float* ws_m;
@@ -177,9 +178,10 @@ struct SeqAttnArgs {
   float* ws_acc;
 };
 
-// How attn_few cuts the keys: `ranges` clusters of `cluster` CTAs, of 4 or 8 warps.
+// How attn_few cuts the keys: `ranges` clusters of `cluster` CTAs, equal shares (per = 0) or
+// `per` blocks of 16 keys to a CTA (cluster 1).
 struct FewPlan {
-  int cluster, ranges, warps;
+  int cluster, ranges, per;
 };
 
 // Rows read back (load.cu).
