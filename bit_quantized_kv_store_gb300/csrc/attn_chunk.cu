@@ -68,6 +68,7 @@ struct CkSmem {
   uint64_t k_ready[2], v_ready[2], p_ready[2], q_ready;
   uint64_t k_free[2], s_full[2], pv_done[2];    // each CTA's: the products arrive
   uint64_t drained;
+  uint32_t row_top[128];                        // per row: its largest query element
   float factor[128];                            // per row: what its scores' units are worth
   float m[128], z[128];
   uint2 odd[kCkOdd];  // (key, dim or group and bits) of values of partly seen tiles that are not numbers
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     }
     if (lane == 0) sm.seq = seq, sm.block = block;
   }
+  if (threadIdx.x < 128) sm.row_top[threadIdx.x] = 0;
   if (threadIdx.x == 32) {
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sm.k_ready[h], rank == 0 ? 5 : 4);
@@ -451,42 +453,39 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   if (warp == 1) pair_tmem_alloc(&sm.tmem_base, 512);
 
   tc_fence_before();
-  __syncthreads();
-  pair_sync();  // both CTAs' barriers and tensor memory
-  tc_fence_after();
-  const uint32_t tbase = sm.tmem_base;
-  const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  __syncwarp();
+  pair_arrive_all();  // both CTAs' barriers and tensor memory (waited for behind the queries)
 
-  // ---------------- queries, eight rows a warp: into the cache's space, scaled, fp16 (bf16
-  // rows: bf16).  Lane (row l & 7, eighth l >> 3) holds 8 values of a group of 32, so a warp
-  // loads 64 bytes of eight rows at once and writes whole core matrices.  Group after group
-  // in a rolled loop (the code is fetched once a CTA; unrolled it took longer than the loads),
-  // scaled by a bound: rotated values are at most sqrt(32) times the row's largest.
+  // ---------------- queries: into the cache's space, scaled, fp16 (bf16 rows: bf16).  A thread
+  // has a row's group of 32 (two of them at 256 wide), which it rotates in registers; eight
+  // lanes write a core matrix.  The scale is a row's power of two that takes a bound of its
+  // values to 2^14 .. 2^15: rotated ones are at most sqrt(32) times the row's largest.
+  // (TQ4, whose rotation spans the row: eight rows a warp, four lanes a row.)
   {
-    const int r = 8 * warp + (lane & 7);
-    const int64_t q_at = r < my_rows ? static_cast<int64_t>(sr.first + i0 + r / grp) * a.q.ts +
-                                           static_cast<int64_t>(kvh * grp + r % grp) * a.q.hs + 8 * (lane >> 3)
-                                     : -1;
-    const uint32_t dst = smem_u32(sm.op.q) + warp * 16 * D + (lane & 7) * 16 + (lane >> 3) * 128;
-    auto put = [&](int G, const float(&x)[8], float by) {
+    // the power of two that takes a bound `top` to 2^14 .. 2^15; NaN and infinities stay
+    auto scale_for = [](float top) {
+      int ex = 0;
+      if (top > 0.f && top < INFINITY) ex = 14 - (static_cast<int>(__float_as_uint(fmaxf(top, 1e-30f)) >> 23) - 127);
+      return __uint_as_float(static_cast<uint32_t>(max(min(ex, 110), -110) + 127) << 23);
+    };
+    // (the factor of a row's scores is not negative: the maximum is taken before it)
+    const float sign = a.qscale < 0.f ? -1.f : 1.f;
+    auto q_at = [&](int r) {
+      return static_cast<int64_t>(sr.first + i0 + r / grp) * a.q.ts + static_cast<int64_t>(kvh * grp + r % grp) * a.q.hs;
+    };
+    auto pack = [&](const float* x, float by, uint32_t at) {  // eight values of a row
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float lo = x[ck_elem<FMT>(2 * i)] * by, hi = x[ck_elem<FMT>(2 * i + 1)] * by;
         w[i] = kBf ? pack_bf16(lo, hi) : pack_half2(lo, hi);
       }
-      ck_sts(dst + 512 * G, w[0], w[1], w[2], w[3]);
+      ck_sts(at, w[0], w[1], w[2], w[3]);
     };
-    // the power of two that takes a bound `top` to at most 2^15; NaN and infinities stay
-    auto scale_for = [](float top) {
-      int ex = 0;
-      if (top > 0.f && top < INFINITY) ex = 14 - (static_cast<int>(__float_as_uint(fmaxf(top, 1e-30f)) >> 23) - 127);
-      return __uint_as_float(static_cast<uint32_t>(max(min(ex, 110), -110) + 127) << 23);
-    };
-    float f;
     if constexpr (FMT == kCkTq4) {
+      const int r = 8 * warp + (lane & 7);
       float x[NG][8];
-      seq_load_row<NG>(a.q, q_at, x);
+      seq_load_row<NG>(a.q, r < my_rows ? q_at(r) + 8 * (lane >> 3) : -1, x);
       seq_turn<NG, true>(x, static_cast<const uint32_t*>(a.c.signs), lane, false);
       float top = 0.f;
 #pragma unroll
@@ -496,47 +495,52 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
       const float up = scale_for(top);
+      const uint32_t dst = smem_u32(sm.op.q) + warp * 16 * D + (lane & 7) * 16 + (lane >> 3) * 128;
 #pragma unroll
-      for (int G = 0; G < NG; ++G) put(G, x[G], up);
-      f = a.qscale / up;
+      for (int G = 0; G < NG; ++G) pack(x[G], up * sign, dst + 512 * G);
+      if (lane < 8) sm.factor[r] = fmaxf(fabsf(a.qscale) / up, 1e-37f);
     } else {
+      const int r = 32 * (warp & 3) + lane;
       const bool rot = a.c.format == KVQ_FMT_Q4_HAD32;
+      constexpr int kMine = NG >= 4 ? NG / 4 : 1;
+      float x[kMine][4][8];
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        const int G = (warp >> 2) + 4 * k;
+        const bool on = r < my_rows && G < NG;
+        seq_load_32(a.q, on ? q_at(r) + 32 * G : -1, x[k]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[k][i >> 3][i & 7]));
+      }
       float up = 1.f;
       if constexpr (!kBf) {
-        float top = 0.f;
-        float x[NG][8];
-        seq_load_row<NG>(a.q, q_at, x);  // (all at once: they come from far)
-#pragma unroll
-        for (int G = 0; G < NG; ++G)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[G][e]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+        atomicMax(&sm.row_top[r], __float_as_uint(top));  // (not negative: ordered as its bits)
+        __syncthreads();
+        top = __uint_as_float(sm.row_top[r]);
         up = scale_for(rot ? top * 5.65685424949238f : top);
       }
-#pragma unroll 2
-      for (int G = 0; G < NG; ++G) {
-        float x[1][8];
-        seq_load_row<1>(a.q, q_at < 0 ? -1 : q_at + 32 * G, x);
-        if (rot) seq_turn<1, false>(x, nullptr, lane, false);
-        put(G, x[0], up);
+      const uint32_t dst = smem_u32(sm.op.q) + (r >> 3) * 16 * D + (r & 7) * 16;
+#pragma unroll
+      for (int k = 0; k < kMine; ++k) {
+        const int G = (warp >> 2) + 4 * k;
+        if (G >= NG) continue;
+        if (rot) seq_turn_32(x[k]);
+        const float by = up * sign * (rot ? kHadamardScale : 1.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pack(x[k][i], by, dst + (4 * G + i) * 128);
       }
-      f = a.qscale / up;
+      if (warp < 4) sm.factor[r] = fmaxf(fabsf(a.qscale) / up, 1e-37f);
     }
-    // (the factor of a row's scores is not negative: the maximum is taken before it)
-    if (f < 0.f) {
-#pragma unroll 1
-      for (int G = 0; G < NG; ++G) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(dst + 512 * G) : "memory");
-        ck_sts(dst + 512 * G, w[0] ^ 0x80008000u, w[1] ^ 0x80008000u, w[2] ^ 0x80008000u, w[3] ^ 0x80008000u);
-      }
-    }
-    if (lane < 8) sm.factor[r] = fmaxf(fabsf(f), 1e-37f);
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_ready);
   }
+
+  pair_wait_all();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+  const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
 
   bool big = false;  // the second pass
   int first = 0;
@@ -720,28 +724,50 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
 
   // ---------------- the rows: out of tensor memory, over the operands, rotated back, stored
   const int ranges = gridDim.z;
+  const int noted = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd_count, 0)) + pair_ld_u32(pair_addr(&sm.odd_count, 1)));
+  // A thread takes a row's groups of 32 out of tensor memory, rotates them back and stores
+  // them.  Over the operands and eight rows a warp where a rotation spans the row (TQ4) or
+  // some value is not a number.
+  const bool staged = (FMT == kCkTq4 && ranges == 1) || noted != 0;
   {
-    const int r = 32 * (warp & 3) + lane, part = warp >> 2;
+    const int r = 32 * (warp & 3) + lane, row = sr.first + i0 + r / grp, head = kvh * grp + r % grp;
+    const bool live = r < my_rows, rot = a.c.format == KVQ_FMT_Q4_HAD32 && ranges == 1;
     const float zr = sm.z[r];
     const float unit = big ? 1.f / kCkBigUnit : 1.f;
     const bool failed = (pair_ld_u32(pair_addr(&sm.abort, 0)) | pair_ld_u32(pair_addr(&sm.abort, 1))) != 0;
     const float inv = failed ? NAN : ranges > 1 ? unit : zr == 0.f ? 0.f : unit / zr;
+    const int64_t part = (static_cast<int64_t>(blockIdx.z) * a.n_rows + row) * a.Hq + head;
+    if (ranges > 1 && live && warp < 4) a.ws_m[part] = sm.m[r], a.ws_z[part] = zr;
 #pragma unroll 1
-    for (int cc = 0; cc < D / 64; ++cc) {
-      const int col = part * (D / 4) + 16 * cc;
-      uint32_t o[16];
+    for (int G = warp >> 2; G < NG; G += 4) {
+      uint32_t o[32];
+      __syncwarp();
       if (nt > 0) {
-        tmem_ld16(tbase + lane_off + kCkO + col, o);
+        tmem_ld32(tbase + lane_off + kCkO + 32 * G, o);
         tmem_wait_ld();
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = 0;
+        for (int i = 0; i < 32; ++i) o[i] = 0;
       }
+      float x[4][8];
+      const float by = inv * (rot ? kHadamardScale : 1.f);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sm.out[r][col + (i & 8) + ck_elem<FMT>(i & 7)] = __uint_as_float(o[i]) * inv;
+      for (int i = 0; i < 32; ++i) x[i >> 3][ck_elem<FMT>(i & 7)] = __uint_as_float(o[i]) * by;
+      if (staged) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sm.out[r][32 * G + i] = x[i >> 3][i & 7];
+        continue;
+      }
+      if (rot) seq_turn_32(x);
+      if (!live) continue;
+      if (ranges > 1) seq_store_32(a.ws_acc + part * D + 32 * G, KVQ_DT_F32, true, x);
+      else
+        seq_store_32(element_at(a.out, static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + 32 * G),
+                     a.out.dtype, a.out.wide, x);
     }
   }
   tc_fence_before();
+  if (staged) {
   __syncthreads();
   // values that are not numbers, into the rows that see their keys
   for (int other = 0; other < 2; ++other) {
@@ -807,7 +833,6 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
       }
     };
     if (8 * warp < my_rows) {
-      if (ranges > 1 && live && lane < 8) a.ws_m[part] = sm.m[r], a.ws_z[part] = sm.z[r];
       if (FMT == kCkTq4 && ranges == 1) {
         float x[NG][8];
 #pragma unroll
@@ -821,11 +846,12 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
         for (int G = 0; G < NG; ++G) {
           float x[1][8];
           get(G, x[0]);
-          if (rot) seq_turn<1, false>(x, nullptr, lane, true);
+          if (rot) seq_turn<1, false, false>(x, nullptr, lane, true);
           put(G, x[0]);
         }
       }
     }
+  }
   }
   pair_sync();  // (its notes are read until here, and its tensor memory)
   if (warp == 1) pair_tmem_dealloc(tbase, 512);

@@ -151,9 +151,9 @@ __device__ __forceinline__ void seq_load_row(const RowsView& v, int64_t at, floa
   }
 }
 
-// The rows' rotation (ALL: the D-point one with signs, else each group's), for rows whose
+// The rows' rotation (ALL: the D-point one with signs, else each group's; SCALE: to norm 1), for rows whose
 // elements 32 G + 8 (lane >> 3) + e are x[G][e].
-template <int NG, bool ALL>
+template <int NG, bool ALL, bool SCALE = true>
 __device__ __forceinline__ void seq_turn(float (&x)[NG][8], const uint32_t* signs, int lane, bool inverse) {
   auto flip = [&] {
 #pragma unroll
@@ -197,12 +197,91 @@ __device__ __forceinline__ void seq_turn(float (&x)[NG][8], const uint32_t* sign
             x[G + h][e] = u - v;
           }
   }
-  const float c = !ALL ? kHadamardScale : NG == 8 ? 0.0625f : NG == 4 ? 0.08838834764831845f : 0.125f;
+  if constexpr (SCALE) {
+    const float c = !ALL ? kHadamardScale : NG == 8 ? 0.0625f : NG == 4 ? 0.08838834764831845f : 0.125f;
 #pragma unroll
-  for (int G = 0; G < NG; ++G)
+    for (int G = 0; G < NG; ++G)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[G][e] *= c;
+      for (int e = 0; e < 8; ++e) x[G][e] *= c;
+  }
   if (ALL && inverse) flip();
+}
+
+// 32 consecutive values of a row, from element `at` of the view on (< 0: zeros).
+__device__ __forceinline__ void seq_load_32(const RowsView& v, int64_t at, float (&x)[4][8]) {
+  if (at < 0) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i >> 3][i & 7] = 0.f;
+  } else if (v.dtype == KVQ_DT_BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(v.data) + at;
+    uint32_t w[16];
+    if (v.wide) {
+      ld_words<16>(p, w);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = p[2 * i] | static_cast<uint32_t>(p[2 * i + 1]) << 16;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i >> 2][2 * (i & 3)] = __uint_as_float(w[i] << 16);
+      x[i >> 2][2 * (i & 3) + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    const float* p = static_cast<const float*>(v.data) + at;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (v.wide) {
+        ld_words<8>(p + 8 * i, reinterpret_cast<uint32_t*>(x[i]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] = p[8 * i + e];
+      }
+    }
+  }
+}
+
+// The 32-point butterfly of one thread's values, no scaling.
+__device__ __forceinline__ void seq_turn_32(float (&x)[4][8]) {
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!(i & h)) {
+        const int k = i + h;
+        const float u = x[i >> 3][i & 7], v = x[k >> 3][k & 7];
+        x[i >> 3][i & 7] = u + v;
+        x[k >> 3][k & 7] = u - v;
+      }
+}
+
+// 32 consecutive values to `at`, rounded into its type (`wide`: on a 32-byte boundary).
+__device__ __forceinline__ void seq_store_32(void* at, int dtype, bool wide, const float (&x)[4][8]) {
+  if (dtype == KVQ_DT_F32) {
+    float* p = static_cast<float*>(at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (wide) {
+        st_words<8>(p + 8 * i, reinterpret_cast<const uint32_t*>(x[i]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[8 * i + e] = x[i][e];
+      }
+    }
+  } else {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (wide) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = pack_bf16(x[2 * i + (e >> 2)][2 * (e & 3)], x[2 * i + (e >> 2)][2 * (e & 3) + 1]);
+        st_words<8>(p + 16 * i, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) p[16 * i + e] = __float2bfloat16_rn(x[2 * i + (e >> 3)][e & 7]);
+      }
+    }
+  }
 }
 
 }  // namespace kvq

@@ -17,6 +17,9 @@ __device__ __forceinline__ void pair_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ void pair_arrive_all() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void pair_wait_all() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // The address of `p` (in this CTA's shared memory) in CTA `rank` of the pair.
 __device__ __forceinline__ uint32_t pair_addr(const void* p, uint32_t rank) {
   uint32_t a;
