@@ -174,187 +174,209 @@ __device__ __forceinline__ void ck_note(CkSmem<D>& sm, int key, uint32_t what) {
 // ---------------------------------------------------------------- the decoders' part
 // Four warps convert one plane's part of every tile: IS_K: 64 keys (those of this CTA),
 // all dims; else 128 keys, this CTA's half of the dims.
+struct CkFetch {  // what a decoding thread fetches next
+  int rows, rows_next;  // lane l: the cache rows of block l & 7 of tiles `tile`, `tile` + 1
+  int tile, unit, slot;
+};
+
 template <int FMT, int D, bool IS_K>
-__device__ __forceinline__ void ck_decode(const SeqAttnArgs& a, CkSmem<D>& sm, const CkWalk& wk, int kvh, int rank,
-                                          bool big) {
-  const kvq_cache& c = a.c;
-  const int tid = threadIdx.x & 127, lane = tid & 31;
-  constexpr bool kBf = FMT == kCkBf16;
-  constexpr int kKeys = IS_K ? 64 : 128;
-  constexpr int kRowChunks = kBf ? D / 8 : D / 32;               // 16-byte chunks of a row
-  constexpr int kC = IS_K ? kRowChunks : kRowChunks / 2;         // of them here
-  constexpr int kUnits = kKeys * kC / 128;                       // a thread's
-  const uint8_t* plane = static_cast<const uint8_t*>(IS_K ? c.k : c.v);
-  const uint16_t* scales = static_cast<const uint16_t*>(IS_K ? c.k_scale : c.v_scale);
-  const int chunk0 = IS_K ? 0 : rank * kC;
-  uint64_t* const ready = IS_K ? sm.k_ready : sm.v_ready;
-  uint64_t* const freed = IS_K ? sm.k_free : sm.pv_done;
-  const uint32_t buf[2] = {smem_u32(IS_K ? sm.op.k[0] : sm.op.v[0]), smem_u32(IS_K ? sm.op.k[1] : sm.op.v[1])};
-  const int32_t* table = a.block_tables + static_cast<int64_t>(sm.seq) * a.max_pages;
+struct CkPart {
+  static constexpr bool kBf = FMT == kCkBf16;
+  static constexpr int kKeys = IS_K ? 64 : 128;
+  static constexpr int kRowChunks = kBf ? D / 8 : D / 32;        // 16-byte chunks of a row
+  static constexpr int kC = IS_K ? kRowChunks : kRowChunks / 2;  // of them here
+  static constexpr int kUnits = kKeys * kC / 128;                // a thread's
+  // 4-bit rows: a thread's units are key groups (of 8) kg0 + i kSpan, always the same chunk and
+  // the same key of 16.  Their codes and scales come through a ring of its own in shared
+  // memory, kCkRing - 1 units ahead (nobody else reads them, so only its own copies are
+  // waited for).
+  static constexpr int kSpan = kBf ? 0 : 16 / kC;
+  const SeqAttnArgs& a;
+  CkSmem<D>& sm;
+  const CkWalk& wk;
+  const int kvh, rank, tid;
+
+  __device__ __forceinline__ int kg0() const { return tid / (8 * kC); }
+  __device__ __forceinline__ int chunk() const { return (IS_K ? 0 : rank * kC) + (tid >> 3) % kC; }
+  __device__ __forceinline__ int in16() const { return (kg0() & 1) * 8 + (tid & 7); }
+  __device__ __forceinline__ uint32_t buf(int b) const { return smem_u32(IS_K ? sm.op.k[b] : sm.op.v[b]); }
 
   // Lane l: the cache row of block l & 7 of the tile's (this CTA's four of them for keys):
   // -1 a page outside the pool, -2 no such block.
-  auto find_rows = [&](int tile) {
+  __device__ __forceinline__ int find_rows(int tile) const {
     if (tile >= wk.tiles) return -2;
+    const int lane = tid & 31;
     const int key = wk.key_of(tile, IS_K ? rank * 4 + (lane & 3) : lane & 7);
     if (key == kNoKey) return -2;
     const int blk = key >> 4, pg = static_cast<int>(fast_div(static_cast<uint32_t>(blk), a.page_blocks));
-    const int page = table[pg];
-    if (page < 0 || page >= c.num_pages) {
+    const int page = a.block_tables[static_cast<int64_t>(sm.seq) * a.max_pages + pg];
+    if (page < 0 || page >= a.c.num_pages) {
       set_status(a.status, KVQ_DEV_BAD_PAGE);
       return -1;
     }
-    return (page * c.num_kv_heads + kvh) * c.page_size + (blk - pg * static_cast<int>(a.page_blocks.d)) * 16;
-  };
-  auto unit_key = [&](int i) { return ((tid + 128 * i) / (8 * kC)) * 8 + (tid & 7); };
-  auto unit_chunk = [&](int i) { return ((tid + 128 * i) >> 3) % kC; };
-  // A unit's place among the operands (its first 16 bytes).
-  auto place = [&](int i, int sixteen) {
-    const int key = unit_key(i), n16 = unit_chunk(i) * (kBf ? 1 : 4) + sixteen;
+    return (page * a.c.num_kv_heads + kvh) * a.c.page_size + (blk - pg * static_cast<int>(a.page_blocks.d)) * 16;
+  }
+  // bf16 rows: unit i's key of the tile, and its place among the operands.
+  __device__ __forceinline__ int unit_key(int i) const { return ((tid + 128 * i) / (8 * kC)) * 8 + (tid & 7); }
+  __device__ __forceinline__ int unit_chunk(int i) const { return ((tid + 128 * i) >> 3) % kC; }
+  __device__ __forceinline__ int place(int i) const {
+    const int key = unit_key(i), n16 = unit_chunk(i);
     return IS_K ? (key >> 3) * 16 * D + n16 * 128 + (key & 7) * 16 : n16 * 2048 + (key >> 3) * 128 + (key & 7) * 16;
-  };
+  }
 
-  if constexpr (kBf) {
-    auto fetch = [&](int tile, int rows) {  // into its buffer
-      const uint32_t at = buf[tile & 1];
-#pragma unroll
+  // The next unit (bf16 rows: tile, into the operands themselves; J: its number of both passes).
+  __device__ __forceinline__ void fetch(CkFetch& f, int J) const {
+    const kvq_cache& c = a.c;
+    if constexpr (kBf) {
+      const uint8_t* plane = static_cast<const uint8_t*>(IS_K ? c.k : c.v);
+      const uint32_t at = buf(J & 1);
+#pragma unroll 4
       for (int i = 0; i < kUnits; ++i) {
         const int key = unit_key(i);
-        const int row0 = __shfl_sync(0xffffffffu, rows, key >> 4);
-        const uint32_t dst = at + place(i, 0);
+        const int row0 = __shfl_sync(0xffffffffu, f.rows, key >> 4);
+        const uint32_t dst = at + place(i);
         if (row0 >= 0) {
-          const uint8_t* src = plane + (static_cast<int64_t>(row0) + (key & 15)) * (2 * D) + (chunk0 + unit_chunk(i)) * 16;
+          const uint8_t* src = plane + (static_cast<int64_t>(row0) + (key & 15)) * (2 * D) + ((IS_K ? 0 : rank * kC) + unit_chunk(i)) * 16;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-        } else {
+        } else {  // no such key: zeros; a bad page's scores are NaN
           const uint32_t x = IS_K && row0 == -1 ? 0x7FFF7FFFu : 0u;
           ck_sts(dst, x, x, x, x);
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    int rows_next = find_rows(0);
-    if (wk.tiles > 0) fetch(0, rows_next);
-    rows_next = find_rows(1);
-    for (int j = 0; j < wk.tiles; ++j) {
-      if (j + 1 < wk.tiles) {
-        if (j >= 1 && !ck_wait_warp(sm, &freed[(j + 1) & 1], ((j - 1) >> 1) & 1, a.status)) return;
-        fetch(j + 1, rows_next);
-        rows_next = find_rows(j + 2);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-      } else {
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-      }
-      if constexpr (!IS_K) {
-        if (wk.edge(j)) {  // 0 x NaN: what not every row sees is taken out and noted
-#pragma unroll 1
-          for (int i = 0; i < kUnits; ++i) {
-            const uint32_t at = buf[j & 1] + place(i, 0);
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
-            bool found = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
-              if (ck_not_finite16(x)) {
-                found = true;
-                const int key = unit_key(i);
-                ck_note(sm, wk.key_of(j, key >> 4) + (key & 15), static_cast<uint32_t>((chunk0 + unit_chunk(i)) * 8 + e) << 16 | x);
-                w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-              }
-            }
-            if (found) ck_sts(at, w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ready[j & 1]);
-    }
-  } else {
-    // A thread's units: key groups (of 8) kg0 + i kSpan, always the same chunk and the same key
-    // of 16.  Their codes and scales come through a ring of its own in shared memory, kCkRing
-    // units ahead (nobody else reads them, so only its own copies are waited for).
-    constexpr int kSpan = 16 / kC;
-    static_assert(kSpan % 2 == 0 && kUnits * kSpan * 8 == kKeys, "units");
-    const int kg0 = tid / (8 * kC), chunk = chunk0 + (tid >> 3) % kC, in16 = (kg0 & 1) * 8 + (tid & 7);
-    const uint8_t* const code_at = plane + in16 * (D / 2) + chunk * 16;
-    // (copies of 4 bytes: the scale beside another)
-    const int scale_i = FMT == kCkQ4 ? in16 * (D / 32) + chunk : in16;
-    const uint16_t* const scale_at = scales + (scale_i & ~1);
-    const uint32_t pick = scale_i & 1 ? 0x3232u : 0x1010u;
-    const uint32_t dst0 = IS_K ? kg0 * 16 * D + (tid >> 3) % kC * 512 + (tid & 7) * 16
-                               : (tid >> 3) % kC * 8192 + kg0 * 128 + (tid & 7) * 16;
-    constexpr uint32_t kStepUnit = IS_K ? kSpan * 16 * D : kSpan * 128, kStepWord = IS_K ? 128 : 2048;
-    const uint32_t ring = smem_u32(&sm.raw[IS_K ? 0 : 1][0][tid]), ring_s = smem_u32(&sm.raw_scale[IS_K ? 0 : 1][0][tid]);
-    const int first = big ? wk.tiles : 0;  // tiles of the pass before: buffers and barriers go on from there
-    uint32_t top = 0;
-    int rows = find_rows(0), rows_next = find_rows(1);
-    int at_tile = 0, at_unit = 0, at_slot = 0;  // of the next unit to be fetched
-    auto fetch = [&] {
-      const int row0 = __shfl_sync(0xffffffffu, rows, (kg0 >> 1) + at_unit * (kSpan / 2));
+      f.rows = f.rows_next;
+      f.rows_next = find_rows(++f.tile + 1);
+    } else {
+      static_assert(kSpan % 2 == 0 && kUnits * kSpan * 8 == kKeys, "units");
+      const int row0 = __shfl_sync(0xffffffffu, f.rows, (kg0() >> 1) + f.unit * (kSpan / 2));
+      const uint32_t ring = smem_u32(&sm.raw[IS_K ? 0 : 1][0][tid]) + f.slot * 2048;
+      const uint32_t ring_s = smem_u32(&sm.raw_scale[IS_K ? 0 : 1][0][tid]) + f.slot * 512;
       if (row0 >= 0) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + at_slot * 2048),
-                     "l"(code_at + static_cast<int64_t>(row0) * (D / 2))
+        const uint8_t* code_at = static_cast<const uint8_t*>(IS_K ? c.k : c.v) + in16() * (D / 2) + chunk() * 16;
+        // (copies of 4 bytes: the scale beside another)
+        const uint16_t* scale_at = static_cast<const uint16_t*>(IS_K ? c.k_scale : c.v_scale) + (scale_index() & ~1);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring), "l"(code_at + static_cast<int64_t>(row0) * (D / 2))
                      : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ring_s + at_slot * 512),
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ring_s),
                      "l"(scale_at + static_cast<int64_t>(row0) * (FMT == kCkQ4 ? D / 32 : 1))
                      : "memory");
       } else {  // no such key: zeros; a bad page's scores are NaN
-        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ring_s + at_slot * 512), "r"(IS_K && row0 == -1 ? 0x7E007E00u : 0u) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ring_s), "r"(IS_K && row0 == -1 ? 0x7E007E00u : 0u) : "memory");
       }
-      at_slot = at_slot == kCkRing - 1 ? 0 : at_slot + 1;
-      if (++at_unit == kUnits) {
-        at_unit = 0;
-        rows = rows_next;
-        rows_next = find_rows(++at_tile + 1);
+      f.slot = f.slot == kCkRing - 1 ? 0 : f.slot + 1;
+      if (++f.unit == kUnits) {
+        f.unit = 0;
+        f.rows = f.rows_next;
+        f.rows_next = find_rows(++f.tile + 1);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-#pragma unroll 1
-    for (int i = 0; i < kCkRing - 1; ++i) fetch();
-    int slot = 0;
-#pragma unroll 1
-    for (int j = 0; j < wk.tiles; ++j) {
-      const int J = first + j;
-      const bool edge = !IS_K && wk.edge(j);
-      if (J >= 2 && !ck_wait_warp(sm, &freed[J & 1], ((J >> 1) - 1) & 1, a.status)) return;
-      uint32_t at = buf[J & 1] + dst0;
-#pragma unroll 1
-      for (int i = 0; i < kUnits; ++i) {
-        fetch();
-        asm volatile("cp.async.wait_group %0;" ::"n"(kCkRing - 1) : "memory");
-        uint32_t x[4], sw;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                     : "r"(ring + slot * 2048)
-                     : "memory");
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(ring_s + slot * 512) : "memory");
-        slot = slot == kCkRing - 1 ? 0 : slot + 1;
-        uint32_t ss = prmt(sw, 0u, pick);
-        if (edge && (ss & 0x7C00u) == 0x7C00u) {  // 0 x NaN: what not every row sees is taken out and noted
-          const int kg = kg0 + i * kSpan;
-          ck_note(sm, wk.key_of(j, kg >> 1) + in16, static_cast<uint32_t>(chunk) << 16);
-          ss = 0;
-        }
-        top = max(top, ss & 0x7FFFu);
-        __half2 s2 = u32_as_h2(ss);
-        if (big) s2 = __hmul2(s2, __float2half2_rn(kCkBigUnit));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[4];
-          ck_decode8<FMT>(x[k], s2, o);
-          ck_sts(at + k * kStepWord, o[0], o[1], o[2], o[3]);
-        }
-        at += kStepUnit;
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ready[J & 1]);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // (those behind the last tile's are markers)
-    if (top > 0x6C00u) sm.over = 1;  // above 4096: products that may pass 65504
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-}
+  __device__ __forceinline__ int scale_index() const { return FMT == kCkQ4 ? in16() * (D / 32) + chunk() : in16(); }
+
+  // The first loads, of a pass whose first tile is number `first`.
+  __device__ __forceinline__ CkFetch begin(int first) const {
+    CkFetch f{find_rows(0), find_rows(1), 0, 0, 0};
+    if constexpr (kBf) {
+      if (wk.tiles > 0) fetch(f, first);
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kCkRing - 1; ++i) fetch(f, 0);
+    }
+    return f;
+  }
+
+  // All tiles.  big: the second pass, in units of 2^8; the buffers' and barriers' order goes on.
+  __device__ __forceinline__ void run(CkFetch f, bool big) const {
+    uint64_t* const ready = IS_K ? sm.k_ready : sm.v_ready;
+    uint64_t* const freed = IS_K ? sm.k_free : sm.pv_done;
+    const int lane = tid & 31;
+    if constexpr (kBf) {
+#pragma unroll 1
+      for (int j = 0; j < wk.tiles; ++j) {
+        if (j + 1 < wk.tiles) {
+          if (j >= 1 && !ck_wait_warp(sm, &freed[(j + 1) & 1], ((j - 1) >> 1) & 1, a.status)) return;
+          fetch(f, j + 1);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        if constexpr (!IS_K) {
+          if (wk.edge(j)) {  // 0 x NaN: what not every row sees is taken out and noted
+#pragma unroll 1
+            for (int i = 0; i < kUnits; ++i) {
+              const uint32_t at = buf(j & 1) + place(i);
+              uint32_t w[4];
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+              bool found = false;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
+                if (ck_not_finite16(x)) {
+                  found = true;
+                  const int key = unit_key(i);
+                  ck_note(sm, wk.key_of(j, key >> 4) + (key & 15), static_cast<uint32_t>((rank * kC + unit_chunk(i)) * 8 + e) << 16 | x);
+                  w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                }
+              }
+              if (found) ck_sts(at, w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ready[j & 1]);
+      }
+    } else {
+      const int kg = kg0();
+      const uint32_t pick = scale_index() & 1 ? 0x3232u : 0x1010u;
+      const uint32_t dst0 = IS_K ? kg * 16 * D + (tid >> 3) % kC * 512 + (tid & 7) * 16
+                                 : (tid >> 3) % kC * 8192 + kg * 128 + (tid & 7) * 16;
+      constexpr uint32_t kStepUnit = IS_K ? kSpan * 16 * D : kSpan * 128, kStepWord = IS_K ? 128 : 2048;
+      const uint32_t ring = smem_u32(&sm.raw[IS_K ? 0 : 1][0][tid]), ring_s = smem_u32(&sm.raw_scale[IS_K ? 0 : 1][0][tid]);
+      const int first = big ? wk.tiles : 0;
+      uint32_t top = 0;
+      int slot = 0;
+#pragma unroll 1
+      for (int j = 0; j < wk.tiles; ++j) {
+        const int J = first + j;
+        const bool edge = !IS_K && wk.edge(j);
+        if (J >= 2 && !ck_wait_warp(sm, &freed[J & 1], ((J >> 1) - 1) & 1, a.status)) return;
+        uint32_t at = buf(J & 1) + dst0;
+#pragma unroll 1
+        for (int i = 0; i < kUnits; ++i) {
+          fetch(f, 0);
+          asm volatile("cp.async.wait_group %0;" ::"n"(kCkRing - 1) : "memory");
+          uint32_t x[4], sw;
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                       : "r"(ring + slot * 2048)
+                       : "memory");
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(ring_s + slot * 512) : "memory");
+          slot = slot == kCkRing - 1 ? 0 : slot + 1;
+          uint32_t ss = prmt(sw, 0u, pick);
+          if (edge && (ss & 0x7C00u) == 0x7C00u) {  // 0 x NaN: what not every row sees is taken out and noted
+            ck_note(sm, wk.key_of(j, (kg + i * kSpan) >> 1) + in16(), static_cast<uint32_t>(chunk()) << 16);
+            ss = 0;
+          }
+          top = max(top, ss & 0x7FFFu);
+          __half2 s2 = u32_as_h2(ss);
+          if (big) s2 = __hmul2(s2, __float2half2_rn(kCkBigUnit));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[4];
+            ck_decode8<FMT>(x[k], s2, o);
+            ck_sts(at + k * kStepWord, o[0], o[1], o[2], o[3]);
+          }
+          at += kStepUnit;
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ready[J & 1]);
+      }
+      if (top > 0x6C00u) sm.over = 1;  // above 4096: products that may pass 65504
+    }
+  }
+};
 
 // ---------------------------------------------------------------- the kernel
 
@@ -455,6 +477,11 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   tc_fence_before();
   __syncwarp();
   pair_arrive_all();  // both CTAs' barriers and tensor memory (waited for behind the queries)
+
+  // ---------------- the decoders' first loads, ahead of the queries
+  CkFetch fetch{};
+  if (warp >= 12) fetch = CkPart<FMT, D, false>{a, sm, wk, kvh, rank, static_cast<int>(threadIdx.x & 127)}.begin(0);
+  else if (warp >= 8) fetch = CkPart<FMT, D, true>{a, sm, wk, kvh, rank, static_cast<int>(threadIdx.x & 127)}.begin(0);
 
   // ---------------- queries: into the cache's space, scaled, fp16 (bf16 rows: bf16).  A thread
   // has a row's group of 32 (two of them at 256 wide), which it rotates in registers; eight
@@ -700,8 +727,16 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     const int last = first + nt - 1;
     if (nt > 0) ck_wait_warp(sm, &sm.pv_done[last & 1], (last >> 1) & 1, a.status);
   } else {
-    if (warp < 12) ck_decode<FMT, D, true>(a, sm, wk, kvh, rank, big);
-    else ck_decode<FMT, D, false>(a, sm, wk, kvh, rank, big);
+    if (warp < 12) {
+      const CkPart<FMT, D, true> part{a, sm, wk, kvh, rank, static_cast<int>(threadIdx.x & 127)};
+      if (big) fetch = part.begin(first);
+      part.run(fetch, big);
+    } else {
+      const CkPart<FMT, D, false> part{a, sm, wk, kvh, rank, static_cast<int>(threadIdx.x & 127)};
+      if (big) fetch = part.begin(first);
+      part.run(fetch, big);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (those behind the last tile's, or behind a wait that gave up)
   }
   // Both CTAs are done: every product has finished (the softmax warps waited for the last).
   __syncwarp();

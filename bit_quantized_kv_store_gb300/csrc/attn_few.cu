@@ -980,9 +980,7 @@ static cudaError_t launch_few(const SeqAttnArgs& a, const FewPlan& p, cudaStream
   constexpr auto kern = attn_few_kernel<FMT, D, WARPS>;
   const size_t smem = sizeof(FewSmem<FMT, D, WARPS>) + 128;
   static_assert(sizeof(FewSmem<FMT, D, WARPS>) + 128 <= 232448, "shared memory");
-  cudaError_t e = set_max_smem_once<kern>(static_cast<int>(smem));
-  if (e == cudaSuccess && p.cluster > 8)  // (opted into by the kernel)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  cudaError_t e = set_max_smem_once<kern, true>(static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int64_t cbs = (static_cast<int64_t>(a.max_rows) * a.group + 7) / 8;
   cudaLaunchConfig_t cfg = {};

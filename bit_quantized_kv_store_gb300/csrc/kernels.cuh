@@ -230,13 +230,14 @@ int device_sm_count();
 
 // Raise Kern's dynamic shared-memory limit to `bytes`, once per CUDA context
 // (the attribute lives as long as the context; a context of another ID, or one
-// whose ID cannot be read, sets it again).
-template <auto Kern>
+// whose ID cannot be read, sets it again).  WIDE: clusters of more than 8 CTAs, too.
+template <auto Kern, bool WIDE = false>
 cudaError_t set_max_smem_once(int bytes) {
   static std::atomic<unsigned long long> done_ctx{0};
   const unsigned long long ctx = current_context_id();
   if (ctx != 0 && done_ctx.load(std::memory_order_acquire) == ctx) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (WIDE && e == cudaSuccess) e = cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && ctx != 0) done_ctx.store(ctx, std::memory_order_release);
   return e;
 }

@@ -217,6 +217,7 @@ CHUNKS = [  # lens, rows
     ([40, 17, 300, 1], [3, 17, 40, 0]),
     ([200, 64, 0, 130, 77], [200, 64, 0, 1, 70]),
     ([3, 50], [9, 2]),  # rows at negative positions
+    ([40, 0, 300], [100, 70, 90]),
     ([1500], [333]),
     ([700, 900], [129, 260]),
 ]
@@ -375,9 +376,13 @@ def test_far_pages(K):
     new = torch.arange(pages - 44, pages, device=DEV)
     for t in (b.cache.k, b.cache.v, b.cache.k_scale, b.cache.v_scale):
         t[new] = t[used].clone()
-    want, one = b.attn(), b.attn(100, 3)
+    def both():
+        few = K.decode_local(b.cache, b.q[:1], ints([700]), b.table, 700, b.scale, 0)
+        return b.attn(), b.attn(100, 3), few
+
+    want = both()
     b.table[0, :44] = new.to(torch.int32)
-    assert torch.equal(b.attn(), want) and torch.equal(b.attn(100, 3), one)
+    assert all(torch.equal(x, y) for x, y in zip(both(), want))
 
 
 def test_with_the_calls_around(K):
@@ -405,3 +410,55 @@ def test_with_the_calls_around(K):
         b.cache, b.table, b.q, b.n, b.cu, b.scale = cache, table, q, sum(rows), [0, *itertools.accumulate(rows)], D ** -0.5
         b.check(got, W, S)
     assert lens[0] + 1 == done[0]
+
+
+def test_workspace_is_asked_for(K):
+    b = Batch(K, "q4_had32", 1, 256, 16, [40000], [1], 4, seed=27)
+    size = K.attn_workspace_size(b.cache, 1, 1, 4, 1, 40000)
+    assert size > 0
+    for bad in (torch.empty(size - 1, dtype=torch.uint8, device=DEV), torch.empty(0, dtype=torch.uint8, device=DEV)):
+        with pytest.raises(K.KvqError):
+            b.local(0, workspace=bad)
+    with pytest.raises(K.KvqError):  # off its 32 bytes
+        b.local(0, workspace=torch.empty(size + 64, dtype=torch.uint8, device=DEV)[16:])
+    ws = torch.full((size + 64,), 7, dtype=torch.uint8, device=DEV)
+    assert torch.equal(b.local(0, workspace=ws[32:-32]), b.local(0))
+    assert bool((ws[:32] == 7).all()) and bool((ws[-32:] == 7).all())
+
+
+def test_tensors_that_are_refused(K):
+    b = Batch(K, "q4_had32", 2, 128, 16, [50, 20], [2, 1], 2, seed=29)
+    good = dict(cache=b.cache, q=b.q, cu_rows=ints(b.cu), seq_lens=ints(b.lens), block_tables=b.table, max_rows=2,
+                max_seq_len=50, sm_scale=0.1)
+    K.attn_seqs(**good)
+    for name, bad in (("q", b.q.double()), ("q", b.q[..., :64]), ("q", b.q.cpu()), ("q", b.q[:, :3]), ("q", b.q[..., ::2]),
+                      ("cu_rows", ints(b.cu)[:2]), ("cu_rows", ints(b.cu).long()), ("seq_lens", ints([50])),
+                      ("block_tables", b.table[:1]), ("block_tables", b.table[:, ::2]), ("max_seq_len", -1), ("window", -1),
+                      ("sinks", -2), ("max_rows", -1), ("out", torch.empty(3, 4, 64, device=DEV)), ("out", b.q),
+                      ("out", torch.empty(3, 4, 128, dtype=torch.float16, device=DEV)), ("dtype", torch.float16),
+                      ("sm_scale", math.nan), ("max_seq_len", 10 ** 6), ("status", torch.zeros(1, device=DEV)),
+                      ("workspace", torch.zeros(1))):
+        with pytest.raises((ValueError, TypeError, K.KvqError)):
+            K.attn_seqs(**{**good, name: bad})
+    fp8 = K.Cache(K.FMT_FP8_ROW, 1, 512, 16, 4, rope_dim=64)
+    with pytest.raises(K.KvqError):
+        K.decode_local(fp8, torch.zeros(1, 16, 512, device=DEV), ints([1]), ints([[0]]), 16, 1.0, 0)
+
+
+def test_same_bits_whatever_the_batch(K):
+    """A window's row does not depend on the sequences beside it, nor on other calls under way."""
+    b = Batch(K, "tq4", 2, 128, 16, [3000, 3000, 900], [1, 1, 1], 4, seed=31)
+    want = b.local(500, 4)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(4):
+        for s in streams:
+            outs.append(b.local(500, 4, stream=s))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    c = Batch(K, "q4_had32", 1, 256, 16, [700, 400], [150, 90], 6, seed=33)
+    chunk = c.attn(200, 4)
+    outs = [c.attn(200, 4, stream=s) for s in streams for _ in range(4)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, chunk) for o in outs)
