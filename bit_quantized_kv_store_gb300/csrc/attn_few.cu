@@ -47,7 +47,7 @@ struct FewShape {
   static constexpr int kRow = kBf ? 2 * D : D / 2;           // bytes of a row of the k or v plane
   static constexpr int kChunks = kRow / 16;                  // 16-byte chunks of it
   static constexpr int kScaleRow = FMT == kFewQ4 ? D / 16 : FMT == kFewTq4 ? 2 : 0;  // bytes of its scales
-  static constexpr int kBlocks = 1;                          // 16-key blocks of a tile
+  static constexpr int kBlocks = kBf || D == 256 ? 1 : 2;    // 16-key blocks of a tile
   static constexpr int kKeys = 16 * kBlocks;
   static constexpr int kPlane = kKeys * kRow;
   static constexpr int kScales = kKeys * kScaleRow;
@@ -200,12 +200,13 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
   KeyBlocks kb{0, 0, 0};
   if (p1 >= 0) kb = key_blocks(p0, p1, a.window, a.sinks);
   // its part of the blocks: a share, or (ragged sequences) so many of them
-  const int all_tiles = kb.count;
+  const int all_tiles = (kb.count + S::kBlocks - 1) / S::kBlocks;
   int tile0, tile1, ranges;
   if (a.per > 0) {
-    tile0 = min(all_tiles, a.per * static_cast<int>(blockIdx.x));
-    tile1 = min(all_tiles, tile0 + a.per);
-    ranges = max(1, (all_tiles + a.per - 1) / a.per);
+    const int per = a.per / S::kBlocks;
+    tile0 = min(all_tiles, per * static_cast<int>(blockIdx.x));
+    tile1 = min(all_tiles, tile0 + per);
+    ranges = max(1, (all_tiles + per - 1) / per);
     if (static_cast<int>(blockIdx.x) >= ranges) {
       pdl_wait();
       pdl_trigger();
