@@ -980,6 +980,11 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
 
 // ---------------------------------------------------------------- several sequences, windows
 
+// From here on a sequence's rows fill enough of a pair of CTAs (256 columns of row x query
+// head): 8 columns at a time read and convert the cache once for every 8.
+constexpr int kChunkColumns = 64;
+static bool is_chunk(const SeqAttnArgs& a) { return static_cast<int64_t>(a.max_rows) * a.group > kChunkColumns; }
+
 // The shape of rows over a cache, in `a` with its window and sinks brought to what they say
 // for sequences of at most max_seq_len tokens.
 static int32_t check_attn_shape(const kvq_cache* c, int32_t n_rows, int32_t num_seqs, int32_t Hq, int32_t max_rows,
@@ -1004,13 +1009,14 @@ static int32_t check_attn_shape(const kvq_cache* c, int32_t n_rows, int32_t num_
   a->max_seq_len = max_seq_len;
   a->window = window < max_seq_len ? window : 0;  // every key is in it
   a->sinks = a->window == 0 ? 0 : sinks < max_seq_len ? sinks : max_seq_len;
-  if (static_cast<int64_t>(a->max_rows) * group + 7 >= int64_t(8) * 65535 / c->num_kv_heads) return KVQ_ERR_UNSUPPORTED;
+  // the kernels' grids: blocks of 8 columns and KV heads in one dimension, or pairs of CTAs
+  if (!is_chunk(*a)) {
+    if ((static_cast<int64_t>(a->max_rows) * group + 7) / 8 * c->num_kv_heads > 65535) return KVQ_ERR_UNSUPPORTED;
+  } else if (2 * chunk_blocks(n_rows, num_seqs, a->max_rows, group) * c->num_kv_heads >= (int64_t(1) << 31)) {
+    return KVQ_ERR_UNSUPPORTED;
+  }
   return KVQ_OK;
 }
-
-// From here on a sequence's rows fill enough of a pair of CTAs (256 columns of row x query
-// head): 8 columns at a time read and convert the cache once for every 8.
-constexpr int kChunkColumns = 64;
 
 struct AttnLayout {
   bool chunk;
@@ -1023,7 +1029,7 @@ static AttnLayout attn_layout(const SeqAttnArgs& a) {
   AttnLayout w{};
   int n_sm = device_sm_count();
   if (n_sm < 1) n_sm = 1;
-  w.chunk = static_cast<int64_t>(a.max_rows) * a.group > kChunkColumns;
+  w.chunk = is_chunk(a);
   if (w.chunk) {
     w.ranges = chunk_ranges(a.c, a.n_rows, a.num_seqs, a.Hq, a.max_rows, a.max_seq_len, a.window, a.sinks, n_sm);
   } else {

@@ -28,6 +28,12 @@
 // s_j + log2 smax_j), so p' keeps its bits whatever the scales are.
 // TQ4 rows: levels by byte lookups (tq4_levels.cuh), the row's scale on scores and p.
 // bf16 rows: as they are; q and p in two bf16 halves (16 bits).
+//
+// Measured (one GB300, a graph of calls): one token, window 1024 7.6 us; 32 sequences, windows
+// of 4096 keys 47 us (149 MB, 3.2 TB/s: about 560 instructions a block of 16 keys, 72 % of the
+// issue slots while the keys last, and 15 us of start and fold); 16 bf16 sequences, windows of
+// 1024 15.9 us (67 MB, 4.2 TB/s).  Loops are rolled because a call is short: unrolled, fetching
+// the code took most of it (11.7 us for the first).
 #include <algorithm>
 #include <climits>
 

@@ -279,7 +279,9 @@ FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max
 cudaError_t launch_attn_few(const SeqAttnArgs& a, const FewPlan& p, cudaStream_t s);
 // The fold of their partials, and of those of the next.
 cudaError_t launch_attn_merge(const SeqAttnArgs& a, int ranges, cudaStream_t s);
-// Many rows a sequence (attn_chunk.cu), and into how many ranges the keys are cut.
+// Many rows a sequence (attn_chunk.cu): the pairs of CTAs of a KV head and a range, and into
+// how many ranges the keys are cut.
+int64_t chunk_blocks(int n_rows, int num_seqs, int max_rows, int group);
 int chunk_ranges(const kvq_cache& c, int n_rows, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
                  int n_sm);
 cudaError_t launch_attn_chunk(const SeqAttnArgs& a, int ranges, cudaStream_t s);

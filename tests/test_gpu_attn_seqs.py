@@ -462,3 +462,9 @@ def test_same_bits_whatever_the_batch(K):
     outs = [c.attn(200, 4, stream=s) for s in streams for _ in range(4)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, chunk) for o in outs)
+
+
+def test_many_rows(K):
+    """A whole prompt at once, longer than a grid dimension's 65535 blocks of 8 columns."""
+    b = Batch(K, "q4_0", 8, 64, 64, [22000], [22000], 3, seed=35)
+    b.check(b.attn(40, 5), 40, 5)
