@@ -165,9 +165,11 @@ __device__ __forceinline__ int ck_pos(int j) { return FMT == kCkQ4 ? (j & 3) * 2
 template <int FMT>
 __device__ __forceinline__ int ck_elem(int i) { return FMT == kCkQ4 ? (i >> 1) + 4 * (i & 1) : i; }
 
-// Note a value that is not a number of a key that not every row sees.
+// Note a value that is not a number, of a key that some row sees (else it is of no
+// consequence: a slot behind the end, or between sinks and window) and not every one.
 template <int D>
-__device__ __forceinline__ void ck_note(CkSmem<D>& sm, int key, uint32_t what) {
+__device__ __forceinline__ void ck_note(CkSmem<D>& sm, const CkWalk& wk, int key, uint32_t what) {
+  if (!any_visible(key, wk.p0, wk.p1, wk.window, wk.sinks)) return;
   const int i = atomicAdd(&sm.odd_count, 1);
   if (i < kCkOdd) {
     sm.odd[i] = make_uint2(static_cast<uint32_t>(key), what);
@@ -320,7 +322,7 @@ struct CkPart {
                 if (ck_not_finite16(x)) {
                   found = true;
                   const int key = unit_key(i);
-                  ck_note(sm, wk.key_of(j, key >> 4) + (key & 15), static_cast<uint32_t>((rank * kC + unit_chunk(i)) * 8 + e) << 16 | x);
+                  ck_note(sm, wk, wk.key_of(j, key >> 4) + (key & 15), static_cast<uint32_t>((rank * kC + unit_chunk(i)) * 8 + e) << 16 | x);
                   w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
                 }
               }
@@ -361,7 +363,7 @@ struct CkPart {
           slot = slot == kCkRing - 1 ? 0 : slot + 1;
           uint32_t ss = prmt(sw, 0u, pick);
           if (edge && (ss & 0x7C00u) == 0x7C00u) {  // 0 x NaN: what not every row sees is taken out and noted
-            ck_note(sm, wk.key_of(j, (kg + i * kSpan) >> 1) + in16(), static_cast<uint32_t>(chunk()) << 16);
+            ck_note(sm, wk, wk.key_of(j, (kg + i * kSpan) >> 1) + in16(), static_cast<uint32_t>(chunk()) << 16);
             ss = 0;
           }
           const uint32_t size = ss & 0x7FFFu;
@@ -584,188 +586,189 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   int first = 0;
 #pragma unroll 1
   for (;;) {
-  if (warp < 4) {
-    // ---------------- products
-    if (warp == 0 && rank == 0 && lane == 0) {
-      constexpr uint32_t id_qk = pair_idesc(kBf, false, 256, kCkTile), id_pv = pair_idesc(kBf, true, 256, D);
-      const uint64_t dq = umma_desc(smem_u32(sm.op.q), 128, 16 * D);
-      const uint64_t dk[2] = {umma_desc(smem_u32(sm.op.k[0]), 128, 16 * D), umma_desc(smem_u32(sm.op.k[1]), 128, 16 * D)};
-      const uint64_t dv[2] = {umma_desc(smem_u32(sm.op.v[0]), 128, 2048), umma_desc(smem_u32(sm.op.v[1]), 128, 2048)};
-      const bool ok = ck_wait<true>(sm, &sm.q_ready, 0, a.status);
-      for (int j = 0; j <= nt && ok; ++j) {
-        if (j < nt) {
-          const int J = first + j, b = J & 1;
-          if (!ck_wait<true>(sm, &sm.k_ready[b], (J >> 1) & 1, a.status)) break;
-          tc_fence_after();
-          const uint32_t s = tbase + kCkS + 128 * b;
+    if (warp < 4) {
+      // ---------------- products
+      if (warp == 0 && rank == 0 && lane == 0) {
+        constexpr uint32_t id_qk = pair_idesc(kBf, false, 256, kCkTile), id_pv = pair_idesc(kBf, true, 256, D);
+        const uint64_t dq = umma_desc(smem_u32(sm.op.q), 128, 16 * D);
+        const uint64_t dk[2] = {umma_desc(smem_u32(sm.op.k[0]), 128, 16 * D), umma_desc(smem_u32(sm.op.k[1]), 128, 16 * D)};
+        const uint64_t dv[2] = {umma_desc(smem_u32(sm.op.v[0]), 128, 2048), umma_desc(smem_u32(sm.op.v[1]), 128, 2048)};
+        const bool ok = ck_wait<true>(sm, &sm.q_ready, 0, a.status);
+        for (int j = 0; j <= nt && ok; ++j) {
+          if (j < nt) {
+            const int J = first + j, b = J & 1;
+            if (!ck_wait<true>(sm, &sm.k_ready[b], (J >> 1) & 1, a.status)) break;
+            tc_fence_after();
+            const uint32_t s = tbase + kCkS + 128 * b;
 #pragma unroll
-          for (int st = 0; st < D / 16; ++st) pair_umma_ss(s, dq + 16 * st, dk[b] + 16 * st, id_qk, st > 0 ? 1u : 0u);
-          pair_commit(&sm.k_free[b]);
-          pair_commit(&sm.s_full[b]);
+            for (int st = 0; st < D / 16; ++st) pair_umma_ss(s, dq + 16 * st, dk[b] + 16 * st, id_qk, st > 0 ? 1u : 0u);
+            pair_commit(&sm.k_free[b]);
+            pair_commit(&sm.s_full[b]);
+          }
+          if (j >= 1) {
+            const int jp = j - 1, J = first + jp, b = J & 1;
+            if (!ck_wait<true>(sm, &sm.v_ready[b], (J >> 1) & 1, a.status)) break;
+            if (!ck_wait<true>(sm, &sm.p_ready[b], (J >> 1) & 1, a.status)) break;
+            tc_fence_after();
+            const uint32_t p = tbase + kCkS + 128 * b;
+#pragma unroll
+            for (int st = 0; st < kCkTile / 16; ++st)
+              pair_umma_ts(tbase + kCkO, p + 8 * st, dv[b] + 16 * st, id_pv, jp > 0 || st > 0 ? 1u : 0u);
+            pair_commit(&sm.pv_done[b]);
+          }
         }
-        if (j >= 1) {
-          const int jp = j - 1, J = first + jp, b = J & 1;
-          if (!ck_wait<true>(sm, &sm.v_ready[b], (J >> 1) & 1, a.status)) break;
-          if (!ck_wait<true>(sm, &sm.p_ready[b], (J >> 1) & 1, a.status)) break;
-          tc_fence_after();
-          const uint32_t p = tbase + kCkS + 128 * b;
-#pragma unroll
-          for (int st = 0; st < kCkTile / 16; ++st)
-            pair_umma_ts(tbase + kCkO, p + 8 * st, dv[b] + 16 * st, id_pv, jp > 0 || st > 0 ? 1u : 0u);
-          pair_commit(&sm.pv_done[b]);
+        // every product issued has finished before the operands and the tensor memory go
+        // (bounded, and independent of the abort flag)
+        pair_commit(&sm.drained);
+        const uint64_t t0 = global_timer_ns();
+        while (!pair_try_wait(&sm.drained, big ? 1 : 0)) {
+          if (global_timer_ns() - t0 > 2000000000ull) {
+            atomicExch(&sm.abort, 1);
+            set_status(a.status, KVQ_DEV_TIMEOUT);
+            break;
+          }
+        }
+      } else if (warp > 0 && rank == 1 && lane == 0) {
+        // ---------------- the second CTA's operands, announced to the first by a thread with
+        // nothing else in flight (a release to the cluster waits for all that its thread has)
+        uint64_t* const mine = warp == 1 ? sm.k_ready : warp == 2 ? sm.v_ready : sm.p_ready;
+        if (warp == 1 && !big && ck_wait(sm, &sm.q_ready, 0, a.status)) pair_arrive(pair_addr(&sm.q_ready, 0));
+        for (int j = 0; j < nt; ++j) {
+          const int J = first + j;
+          if (!ck_wait(sm, &mine[J & 1], (J >> 1) & 1, a.status)) break;
+          pair_arrive(pair_addr(&mine[J & 1], 0));
         }
       }
-      // every product issued has finished before the operands and the tensor memory go
-      // (bounded, and independent of the abort flag)
-      pair_commit(&sm.drained);
-      const uint64_t t0 = global_timer_ns();
-      while (!pair_try_wait(&sm.drained, big ? 1 : 0)) {
-        if (global_timer_ns() - t0 > 2000000000ull) {
-          atomicExch(&sm.abort, 1);
-          set_status(a.status, KVQ_DEV_TIMEOUT);
-          break;
-        }
-      }
-    } else if (warp > 0 && rank == 1 && lane == 0) {
-      // ---------------- the second CTA's operands, announced to the first by a thread with
-      // nothing else in flight (a release to the cluster waits for all that its thread has)
-      uint64_t* const mine = warp == 1 ? sm.k_ready : warp == 2 ? sm.v_ready : sm.p_ready;
-      if (warp == 1 && !big && ck_wait(sm, &sm.q_ready, 0, a.status)) pair_arrive(pair_addr(&sm.q_ready, 0));
+    } else if (warp < 8) {
+      // ---------------- softmax, one row a thread
+      const int r = 32 * (warp & 3) + lane;
+      const int p = r < my_rows ? base + i0 + r / grp : -kNoKey;
+      ck_wait_warp(sm, &sm.q_ready, 0, a.status);  // (the factors)
+      const float f = sm.factor[r] * (big ? 1.f / kCkBigUnit : 1.f);
+      float m_run = -INFINITY, z = 0.f;
       for (int j = 0; j < nt; ++j) {
-        const int J = first + j;
-        if (!ck_wait(sm, &mine[J & 1], (J >> 1) & 1, a.status)) break;
-        pair_arrive(pair_addr(&mine[J & 1], 0));
-      }
-    }
-  } else if (warp < 8) {
-    // ---------------- softmax, one row a thread
-    const int r = 32 * (warp & 3) + lane;
-    const int p = r < my_rows ? base + i0 + r / grp : -kNoKey;
-    ck_wait_warp(sm, &sm.q_ready, 0, a.status);  // (the factors)
-    const float f = sm.factor[r] * (big ? 1.f / kCkBigUnit : 1.f);
-    float m_run = -INFINITY, z = 0.f;
-    for (int j = 0; j < nt; ++j) {
-      const int J = first + j, b = J & 1;
-      if (!ck_wait_warp(sm, &sm.s_full[b], (J >> 1) & 1, a.status)) break;
-      tc_fence_after();
-      const uint32_t s_at = tbase + lane_off + kCkS + 128 * b;
-      const bool edge = wk.edge(j);
-      uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};  // of the tile's keys
-      if (edge) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int key = wk.key_of(j, k);
-          auto below = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u; };
-          uint32_t bits = below(p - key + 1);
-          if (a.window > 0) bits &= ~below(p - a.window - key + 1) | below(a.sinks - key);
-          seen[k >> 1] = (seen[k >> 1] & (k & 1 ? 0x0000FFFFu : 0xFFFF0000u)) | bits << (16 * (k & 1));
-        }
-      }
-
-      auto load = [&](int cc, uint32_t (&v)[32]) {
-        tmem_ld32(s_at + 32 * cc, v);
-        tmem_wait_ld();
-        if (edge) {
-          const uint32_t sn = (32==32? (cc==0?seen[0]:cc==1?seen[1]:cc==2?seen[2]:seen[3]) : ((cc<2?seen[0]:cc<4?seen[1]:cc<6?seen[2]:seen[3])>>(16*(cc&1))));
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!((sn >> i) & 1u)) v[i] = 0xFF800000u;
-        }
-      };
-      float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {
-        uint32_t v[32];
-        load(cc, v);
-#pragma unroll
-        for (int i = 0; i < 32; i += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) t4[k] = ck_max3(t4[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
-      }
-      float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-      if (top != -INFINITY) top *= f;
-      const bool raise = top > m_run + 8.f;
-      float corr = 1.f;
-      if (raise) {
-        corr = m_run == -INFINITY ? 1.f : fast_exp2(m_run - top);  // (z and the context are zero until then)
-        z *= corr;
-        m_run = top;
-      }
-      const float mu = m_run == -INFINITY ? 0.f : m_run;
-      if (j > 0 && __any_sync(0xffffffffu, raise && corr != 1.f)) {
-        if (!ck_wait_warp(sm, &sm.pv_done[(J - 1) & 1], ((J - 1) >> 1) & 1, a.status)) break;
+        const int J = first + j, b = J & 1;
+        if (!ck_wait_warp(sm, &sm.s_full[b], (J >> 1) & 1, a.status)) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int cc = 0; cc < D / 16; ++cc) {
-          uint32_t o[16];
-          tmem_ld16(tbase + lane_off + kCkO + 16 * cc, o);
-          tmem_wait_ld();
+        const uint32_t s_at = tbase + lane_off + kCkS + 128 * b;
+        const bool edge = wk.edge(j);
+        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};  // of the tile's keys
+        if (edge) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
-          tmem_st16(tbase + lane_off + kCkO + 16 * cc, o);
+          for (int k = 0; k < 8; ++k) {
+            const int key = wk.key_of(j, k);
+            auto below = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xFFFFu : (1u << n) - 1u; };
+            uint32_t bits = below(p - key + 1);
+            if (a.window > 0) bits &= ~below(p - a.window - key + 1) | below(a.sinks - key);
+            seen[k >> 1] = (seen[k >> 1] & (k & 1 ? 0x0000FFFFu : 0xFFFF0000u)) | bits << (16 * (k & 1));
+          }
+        }
+        auto load = [&](int cc, uint32_t (&v)[32]) {  // 32 of the tile's scores
+          tmem_ld32(s_at + 32 * cc, v);
+          tmem_wait_ld();
+          if (edge) {
+            const uint32_t on = cc == 0 ? seen[0] : cc == 1 ? seen[1] : cc == 2 ? seen[2] : seen[3];
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((on >> i) & 1u)) v[i] = 0xFF800000u;
+          }
+        };
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t v[32];
+          load(cc, v);
+#pragma unroll
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t4[k] = ck_max3(t4[k], __uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
+        }
+        float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        if (top != -INFINITY) top *= f;
+        // the reference is raised only when a row's scores passed it by more than 8 (base 2)
+        const bool raise = top > m_run + 8.f;
+        float corr = 1.f;
+        if (raise) {
+          corr = m_run == -INFINITY ? 1.f : fast_exp2(m_run - top);  // (z and the context are zero until then)
+          z *= corr;
+          m_run = top;
+        }
+        const float mu = m_run == -INFINITY ? 0.f : m_run;
+        if (j > 0 && __any_sync(0xffffffffu, raise && corr != 1.f)) {
+          if (!ck_wait_warp(sm, &sm.pv_done[(J - 1) & 1], ((J - 1) >> 1) & 1, a.status)) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < D / 16; ++cc) {
+            uint32_t o[16];
+            tmem_ld16(tbase + lane_off + kCkO + 16 * cc, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * corr);
+            tmem_st16(tbase + lane_off + kCkO + 16 * cc, o);
+          }
+          tmem_wait_st();
+        }
+        const uint64_t f2 = pk2(f, f), mu2 = pk2(-mu, -mu);
+        uint64_t z2[2] = {0, 0};
+        // p of 32 keys goes to 16 columns whose scores have been read
+#pragma unroll 2
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t v[32], pk[16];
+          load(cc, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float e0, e1;
+            upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, mu2), e0, e1);
+            e0 = fast_exp2(e0);
+            e1 = fast_exp2(e1);
+            z2[i & 1] = add2(z2[i & 1], pk2(e0, e1));
+            pk[i] = kBf ? pack_bf16(e0, e1) : pack_half2(e0, e1);
+          }
+          tmem_st16(s_at + 16 * cc, pk);
+        }
+        {
+          float e0, e1;
+          upk2(add2(z2[0], z2[1]), e0, e1);
+          z += e0 + e1;
         }
         tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[b]);
       }
-      const uint64_t f2 = pk2(f, f), mu2 = pk2(-mu, -mu);
-      uint64_t z2[2] = {0, 0};
-#pragma unroll 2
-      for (int cc = 0; cc < 4; ++cc) {
-        uint32_t v[32], pk[16];
-        load(cc, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float e0, e1;
-          upk2(fma2(pk2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, mu2), e0, e1);
-          e0 = fast_exp2(e0);
-          e1 = fast_exp2(e1);
-          z2[i & 1] = add2(z2[i & 1], pk2(e0, e1));
-          pk[i] = kBf ? pack_bf16(e0, e1) : pack_half2(e0, e1);
-        }
-        tmem_st16(s_at + 16 * cc, pk);
-      }
-      {
-        float e0, e1;
-        upk2(add2(z2[0], z2[1]), e0, e1);
-        z += e0 + e1;
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_ready[b]);
-    }
-    sm.m[r] = m_run;
-    sm.z[r] = z;
-    const int last = first + nt - 1;
-    if (nt > 0) ck_wait_warp(sm, &sm.pv_done[last & 1], (last >> 1) & 1, a.status);
-  } else {
-    if (warp < 12) {
-      const CkPart<FMT, D, true> part{a, sm, wk, kvh, rank, static_cast<int>(threadIdx.x & 127)};
-      if (big) fetch = part.begin(first);
-      part.run(fetch, big);
+      sm.m[r] = m_run;
+      sm.z[r] = z;
+      const int last = first + nt - 1;
+      if (nt > 0) ck_wait_warp(sm, &sm.pv_done[last & 1], (last >> 1) & 1, a.status);
     } else {
-      const CkPart<FMT, D, false> part{a, sm, wk, kvh, rank, static_cast<int>(threadIdx.x & 127)};
-      if (big) fetch = part.begin(first);
-      part.run(fetch, big);
+      if (warp < 12) {
+        const CkPart<FMT, D, true> part{a, sm, wk, kvh, rank, static_cast<int>(threadIdx.x & 127)};
+        if (big) fetch = part.begin(first);
+        part.run(fetch, big);
+      } else {
+        const CkPart<FMT, D, false> part{a, sm, wk, kvh, rank, static_cast<int>(threadIdx.x & 127)};
+        if (big) fetch = part.begin(first);
+        part.run(fetch, big);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");  // (those behind the last tile's, or behind a wait that gave up)
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // (those behind the last tile's, or behind a wait that gave up)
-  }
-  // Both CTAs are done: every product has finished (the softmax warps waited for the last).
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  pdl_trigger();
-  pair_sync();
-  tc_fence_after();
-  if constexpr (!kBf) {
-    if (big) break;
-    big = (pair_ld_u32(pair_addr(&sm.over, 0)) | pair_ld_u32(pair_addr(&sm.over, 1))) != 0;
-    if (!big) break;
-    first = nt;
-    if (threadIdx.x == 0) sm.odd_count = 0, sm.lost_lo = INT_MAX, sm.lost_hi = -1;
+    // Both CTAs are done: every product has finished (the softmax warps waited for the last).
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    pdl_trigger();
     pair_sync();
-  } else {
-    break;
-  }
+    tc_fence_after();
+    if constexpr (!kBf) {
+      if (big) break;
+      big = (pair_ld_u32(pair_addr(&sm.over, 0)) | pair_ld_u32(pair_addr(&sm.over, 1))) != 0;
+      if (!big) break;
+      first = nt;
+      if (threadIdx.x == 0) sm.odd_count = 0, sm.lost_lo = INT_MAX, sm.lost_hi = -1;
+      pair_sync();
+    } else {
+      break;
+    }
   }
 
   // ---------------- the rows: out of tensor memory, over the operands, rotated back, stored
@@ -814,90 +817,90 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   }
   tc_fence_before();
   if (staged) {
-  __syncthreads();
-  // values that are not numbers, into the rows that see their keys
-  for (int other = 0; other < 2; ++other) {
-    const int count = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd_count, other)));
-    if (count == 0) continue;
-    for (int r = threadIdx.x; r < my_rows; r += kCkThreads) {
-      const int p = base + i0 + r / grp;
-      for (int i = 0; i < min(count, kCkOdd); ++i) {
-        const int key = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd[i].x, other)));
-        if (!key_visible(key, p, a.window, a.sinks)) continue;
-        const uint32_t what = pair_ld_u32(pair_addr(&sm.odd[i].y, other));
-        if constexpr (kBf) {
-          sm.out[r][what >> 16] += __uint_as_float(what << 16);
-        } else {
-          for (int e = 0; e < 32; ++e) sm.out[r][(what >> 16) * 32 + e] = NAN;
+    __syncthreads();
+    // values that are not numbers, into the rows that see their keys
+    for (int other = 0; other < 2; ++other) {
+      const int count = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd_count, other)));
+      if (count == 0) continue;
+      for (int r = threadIdx.x; r < my_rows; r += kCkThreads) {
+        const int p = base + i0 + r / grp;
+        for (int i = 0; i < min(count, kCkOdd); ++i) {
+          const int key = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd[i].x, other)));
+          if (!key_visible(key, p, a.window, a.sinks)) continue;
+          const uint32_t what = pair_ld_u32(pair_addr(&sm.odd[i].y, other));
+          if constexpr (kBf) {
+            sm.out[r][what >> 16] += __uint_as_float(what << 16);
+          } else {
+            for (int e = 0; e < 32; ++e) sm.out[r][(what >> 16) * 32 + e] = NAN;
+          }
         }
-      }
-      if (count > kCkOdd) {
-        // those that found no room: rows that see a key between the first and the last of them
-        const int lo = static_cast<int>(pair_ld_u32(pair_addr(&sm.lost_lo, other)));
-        const int hi = static_cast<int>(pair_ld_u32(pair_addr(&sm.lost_hi, other)));
-        bool hit = false;
-        for (int key = lo; key <= hi && !hit; ++key) hit = key_visible(key, p, a.window, a.sinks);
-        if (hit)
-          for (int e = 0; e < D; ++e) sm.out[r][e] = NAN;
+        if (count > kCkOdd) {
+          // those that found no room: rows that see a key between the first and the last of them
+          const int lo = static_cast<int>(pair_ld_u32(pair_addr(&sm.lost_lo, other)));
+          const int hi = static_cast<int>(pair_ld_u32(pair_addr(&sm.lost_hi, other)));
+          bool hit = false;
+          for (int key = lo; key <= hi && !hit; ++key) hit = key_visible(key, p, a.window, a.sinks);
+          if (hit)
+            for (int e = 0; e < D; ++e) sm.out[r][e] = NAN;
+        }
       }
     }
-  }
-  __syncthreads();
-  {
-    const int r = 8 * warp + (lane & 7);  // (rows behind the last are zeros, or of no consequence)
-    const int row = sr.first + i0 + r / grp, head = kvh * grp + r % grp;
-    const bool live = r < my_rows;
-    const int64_t out_at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + 8 * (lane >> 3);
-    const int64_t part = (static_cast<int64_t>(blockIdx.z) * a.n_rows + row) * a.Hq + head;
-    auto get = [&](int G, float(&x)[8]) {
+    __syncthreads();
+    {
+      const int r = 8 * warp + (lane & 7);  // (rows behind the last are zeros, or of no consequence)
+      const int row = sr.first + i0 + r / grp, head = kvh * grp + r % grp;
+      const bool live = r < my_rows;
+      const int64_t out_at = static_cast<int64_t>(row) * a.out.ts + static_cast<int64_t>(head) * a.out.hs + 8 * (lane >> 3);
+      const int64_t part = (static_cast<int64_t>(blockIdx.z) * a.n_rows + row) * a.Hq + head;
+      auto get = [&](int G, float(&x)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = sm.out[r][32 * G + 8 * (lane >> 3) + e];
-    };
-    auto put = [&](int G, const float(&x)[8]) {
-      if (!live) return;
-      if (ranges > 1) {
-        st_words<8>(a.ws_acc + part * D + 32 * G + 8 * (lane >> 3), reinterpret_cast<const uint32_t*>(x));
-      } else if (a.out.dtype == KVQ_DT_F32) {
-        float* p = static_cast<float*>(a.out.data) + out_at + 32 * G;
-        if (a.out.wide) {
-          st_words<8>(p, reinterpret_cast<const uint32_t*>(x));
+        for (int e = 0; e < 8; ++e) x[e] = sm.out[r][32 * G + 8 * (lane >> 3) + e];
+      };
+      auto put = [&](int G, const float(&x)[8]) {
+        if (!live) return;
+        if (ranges > 1) {
+          st_words<8>(a.ws_acc + part * D + 32 * G + 8 * (lane >> 3), reinterpret_cast<const uint32_t*>(x));
+        } else if (a.out.dtype == KVQ_DT_F32) {
+          float* p = static_cast<float*>(a.out.data) + out_at + 32 * G;
+          if (a.out.wide) {
+            st_words<8>(p, reinterpret_cast<const uint32_t*>(x));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = x[e];
+          }
         } else {
+          __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out.data) + out_at + 32 * G;
+          if (a.out.wide) {
+            uint32_t w[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = x[e];
+            for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+            st_words<4>(p, w);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = __float2bfloat16_rn(x[e]);
+          }
         }
-      } else {
-        __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.out.data) + out_at + 32 * G;
-        if (a.out.wide) {
-          uint32_t w[4];
+      };
+      if (8 * warp < my_rows) {
+        if (FMT == kCkTq4 && ranges == 1) {
+          float x[NG][8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-          st_words<4>(p, w);
+          for (int G = 0; G < NG; ++G) get(G, x[G]);
+          seq_turn<NG, true>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
+#pragma unroll
+          for (int G = 0; G < NG; ++G) put(G, x[G]);
         } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = __float2bfloat16_rn(x[e]);
-        }
-      }
-    };
-    if (8 * warp < my_rows) {
-      if (FMT == kCkTq4 && ranges == 1) {
-        float x[NG][8];
-#pragma unroll
-        for (int G = 0; G < NG; ++G) get(G, x[G]);
-        seq_turn<NG, true>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
-#pragma unroll
-        for (int G = 0; G < NG; ++G) put(G, x[G]);
-      } else {
-        const bool rot = ranges == 1 && a.c.format == KVQ_FMT_Q4_HAD32;
+          const bool rot = ranges == 1 && a.c.format == KVQ_FMT_Q4_HAD32;
 #pragma unroll 2
-        for (int G = 0; G < NG; ++G) {
-          float x[1][8];
-          get(G, x[0]);
-          if (rot) seq_turn<1, false, false>(x, nullptr, lane, true);
-          put(G, x[0]);
+          for (int G = 0; G < NG; ++G) {
+            float x[1][8];
+            get(G, x[0]);
+            if (rot) seq_turn<1, false, false>(x, nullptr, lane, true);
+            put(G, x[0]);
+          }
         }
       }
     }
-  }
   }
   pair_sync();  // (its notes are read until here, and its tensor memory)
   if (warp == 1) pair_tmem_dealloc(tbase, 512);

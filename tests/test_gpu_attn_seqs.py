@@ -468,3 +468,21 @@ def test_many_rows(K):
     """A whole prompt at once, longer than a grid dimension's 65535 blocks of 8 columns."""
     b = Batch(K, "q4_0", 8, 64, 64, [22000], [22000], 3, seed=35)
     b.check(b.attn(40, 5), 40, 5)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows", [1, 3, 150])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 0), (50, 5), (300, 37)])
+def test_slots_that_nobody_sees(K, fmt, rows, window, sinks):
+    """Whatever lies behind a sequence's end, or between sinks and window, reaches nobody."""
+    b = Batch(K, fmt, 2, 256, 64, [777, 300], [rows, rows], 3, seed=37)
+    want = b.attn(window, sinks)
+    hidden = torch.ones(b.cache.num_pages, 64, dtype=torch.bool, device=DEV)
+    for i, T in enumerate(b.lens):
+        key = torch.arange(T, device=DEV)
+        if window:
+            key = key[(key < sinks) | (key > T - rows - window)]
+        hidden[b.table[i].long()[key // 64], key % 64] = False
+    for p in (b.cache.k, b.cache.v) if fmt == "bf16" else (b.cache.k_scale, b.cache.v_scale):
+        p.transpose(1, 2)[hidden] = math.nan
+    assert torch.equal(b.attn(window, sinks), want)
