@@ -83,6 +83,7 @@ struct CkSmem {
   uint32_t tmem_base;
   int abort;
   int seq, block;
+  SeqRows rows_of;  // the sequence's
 };
 constexpr size_t kCkMinSmem = 120 * 1024;  // one CTA to an SM: pairs that wait for tensor memory crosswise would wait forever
 
@@ -182,8 +183,12 @@ __device__ __forceinline__ void ck_note(CkSmem<D>& sm, const CkWalk& wk, int key
 // ---------------------------------------------------------------- the decoders' part
 // Four warps convert one plane's part of every tile: IS_K: 64 keys (those of this CTA),
 // all dims; else 128 keys, this CTA's half of the dims.
-struct CkFetch {  // what a decoding thread fetches next
-  int rows, rows_next;  // lane l: the cache rows of block l & 7 of tiles `tile`, `tile` + 1
+// What a decoding thread fetches next. Pages are looked up for four tiles at once, one lane a
+// block, and four tiles ahead: a tile's own look-up, waited for, held the first fetch of a pair
+// back by a trip to memory (8 prompts 205 -> 197 us, five ragged chunks 447 -> 437).
+struct CkFetch {
+  int rows;  // lane l: the cache row of block l & 7 of tile l >> 3 of four
+  int page;  // and that block's page of the next four, as the table has it
   int tile, unit, slot;
 };
 
@@ -209,20 +214,34 @@ struct CkPart {
   __device__ __forceinline__ int in16() const { return (kg0() & 1) * 8 + (tid & 7); }
   __device__ __forceinline__ uint32_t buf(int b) const { return smem_u32(IS_K ? sm.op.k[b] : sm.op.v[b]); }
 
-  // Lane l: the cache row of block l & 7 of the tile's (this CTA's four of them for keys):
-  // -1 a page outside the pool, -2 no such block.
-  __device__ __forceinline__ int find_rows(int tile) const {
-    if (tile >= wk.tiles) return -2;
-    const int lane = tid & 31;
-    const int key = wk.key_of(tile, IS_K ? rank * 4 + (lane & 3) : lane & 7);
+  // Lane l: the first key of block l & 7 (of keys: of this CTA's four) of tile t0 + l / 8.
+  __device__ __forceinline__ int lane_key(int t0) const {
+    const int lane = tid & 31, tile = t0 + (lane >> 3);
+    return tile < wk.tiles && (!IS_K || (lane & 7) < 4) ? wk.key_of(tile, IS_K ? rank * 4 + (lane & 3) : lane & 7) : kNoKey;
+  }
+  // Its page in the sequence's table: looked at only where the row is made of it, four tiles
+  // later, so that the load is not waited for.
+  __device__ __forceinline__ int find_page(int t0) const {
+    const int key = lane_key(t0);
+    if (key == kNoKey) return 0;
+    return a.block_tables[static_cast<int64_t>(sm.seq) * a.max_pages + fast_div(static_cast<uint32_t>(key >> 4), a.page_blocks)];
+  }
+  // Its cache row: -1 a page outside the pool, -2 no such block.
+  __device__ __forceinline__ int row_of(int t0, int page) const {
+    const int key = lane_key(t0);
     if (key == kNoKey) return -2;
-    const int blk = key >> 4, pg = static_cast<int>(fast_div(static_cast<uint32_t>(blk), a.page_blocks));
-    const int page = a.block_tables[static_cast<int64_t>(sm.seq) * a.max_pages + pg];
     if (page < 0 || page >= a.c.num_pages) {
       set_status(a.status, KVQ_DEV_BAD_PAGE);
       return -1;
     }
+    const int blk = key >> 4, pg = static_cast<int>(fast_div(static_cast<uint32_t>(blk), a.page_blocks));
     return (page * a.c.num_kv_heads + kvh) * a.c.page_size + (blk - pg * static_cast<int>(a.page_blocks.d)) * 16;
+  }
+  __device__ __forceinline__ void next_tile(CkFetch& f) const {
+    if ((++f.tile & 3) == 0) {
+      f.rows = row_of(f.tile, f.page);
+      f.page = find_page(f.tile + 4);
+    }
   }
   // bf16 rows: unit i's key of the tile, and its place among the operands.
   __device__ __forceinline__ int unit_key(int i) const { return ((tid + 128 * i) / (8 * kC)) * 8 + (tid & 7); }
@@ -241,7 +260,7 @@ struct CkPart {
 #pragma unroll 4
       for (int i = 0; i < kUnits; ++i) {
         const int key = unit_key(i);
-        const int row0 = __shfl_sync(0xffffffffu, f.rows, key >> 4);
+        const int row0 = __shfl_sync(0xffffffffu, f.rows, (f.tile & 3) * 8 + (key >> 4));
         const uint32_t dst = at + place(i);
         if (row0 >= 0) {
           const uint8_t* src = plane + (static_cast<int64_t>(row0) + (key & 15)) * (2 * D) + ((IS_K ? 0 : rank * kC) + unit_chunk(i)) * 16;
@@ -251,11 +270,10 @@ struct CkPart {
           ck_sts(dst, x, x, x, x);
         }
       }
-      f.rows = f.rows_next;
-      f.rows_next = find_rows(++f.tile + 1);
+      next_tile(f);
     } else {
       static_assert(kSpan % 2 == 0 && kUnits * kSpan * 8 == kKeys, "units");
-      const int row0 = __shfl_sync(0xffffffffu, f.rows, (kg0() >> 1) + f.unit * (kSpan / 2));
+      const int row0 = __shfl_sync(0xffffffffu, f.rows, (f.tile & 3) * 8 + (kg0() >> 1) + f.unit * (kSpan / 2));
       const uint32_t ring = smem_u32(&sm.raw[IS_K ? 0 : 1][0][tid]) + f.slot * 2048;
       const uint32_t ring_s = smem_u32(&sm.raw_scale[IS_K ? 0 : 1][0][tid]) + f.slot * 512;
       if (row0 >= 0) {
@@ -273,8 +291,7 @@ struct CkPart {
       f.slot = f.slot == kCkRing - 1 ? 0 : f.slot + 1;
       if (++f.unit == kUnits) {
         f.unit = 0;
-        f.rows = f.rows_next;
-        f.rows_next = find_rows(++f.tile + 1);
+        next_tile(f);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -283,7 +300,9 @@ struct CkPart {
 
   // The first loads, of a pass whose first tile is number `first`.
   __device__ __forceinline__ CkFetch begin(int first) const {
-    CkFetch f{find_rows(0), find_rows(1), 0, 0, 0};
+    CkFetch f{0, find_page(0), 0, 0, 0};
+    f.rows = row_of(0, f.page);
+    f.page = find_page(4);
     if constexpr (kBf) {
       if (wk.tiles > 0) fetch(f, first);
     } else {
@@ -399,7 +418,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
   const int rank = static_cast<int>(pair_rank());
   // One sequence: a KV head after another, so that whoever runs reads the same keys (4096 rows
   // at 16384 1409 us, the heads side by side 1428).  Several: every block's heads side by side,
-  // so that no long block begins late (five ragged chunks 447 us, head after head 457).
+  // so that no long block begins late (five ragged chunks: 10 us of 457 less than head after head).
   const int kv_heads = a.c.num_kv_heads, item = blockIdx.x >> 1, items = gridDim.x >> 1;
   const int kvh = a.num_seqs == 1 ? item / (items / kv_heads) : item % kv_heads, grp = a.group, qpb = 128 / grp;
   pdl_wait();
@@ -412,8 +431,9 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     int seq = -1, block = 0, before = 0;
     for (int b0 = 0; b0 < a.num_seqs && (seq < 0 || report); b0 += 32) {
       int mine = 0;
+      SeqRows r{};
       if (b0 + lane < a.num_seqs) {
-        const SeqRows r = seq_rows(a, b0 + lane);
+        r = seq_rows(a, b0 + lane);
         if (report && r.state != kRowsOk) set_status(a.status, KVQ_DEV_BAD_LENGTH);
         mine = (r.n + 2 * qpb - 1) / (2 * qpb);
       }
@@ -429,6 +449,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
         const int last = before + __shfl_sync(0xffffffffu, upto, l) - 1;
         seq = b0 + l;
         block = last - want;
+        if (lane == l) sm.rows_of = r;
       }
       before += __shfl_sync(0xffffffffu, upto, 31);
     }
@@ -459,7 +480,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     pdl_trigger();
     return;
   }
-  const SeqRows sr = seq_rows(a, seq);
+  const SeqRows sr = sm.rows_of;
   const int base = sr.T - sr.n;
   const int ib = sm.block * 2 * qpb, i0 = ib + rank * qpb;  // the pair's, this CTA's first row
   const int my_rows = max(0, min(qpb, sr.n - i0)) * grp;
