@@ -889,16 +889,18 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
   }
 }
 
-// The ranges' partials of every row and head, folded in order, rotated back and rounded: a
-// warp for each.
+// The ranges' partials of a row and head, folded in a fixed order, rotated back and rounded.
+// Four warps take every fourth range: one warp's loads of all of them, four in flight, were
+// 0.4 us a range.
 template <int D>
 __global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__ SeqAttnArgs a, int ranges) {
   constexpr int NG = D / 32;
+  __shared__ float sm_x[4][D], sm_z[4];
   pdl_wait();
   pdl_trigger();
   const int warp = warp_index(), lane = threadIdx.x & 31;
   const SeqRows sr = seq_rows(a, blockIdx.y);
-  const int i = blockIdx.x * 4 + warp;
+  const int i = blockIdx.x;
   if (sr.state != kRowsOk || i >= sr.n * a.Hq) return;
   const int row = sr.first + i / a.Hq, head = i % a.Hq;
   if (a.per > 0) {  // as many as the column's block was cut into; one: stored already
@@ -913,7 +915,7 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll 4
-  for (int r = 0; r < ranges; ++r) {
+  for (int r = warp; r < ranges; r += 4) {
     const float mr = a.ws_m[part + r * stride], zr = a.ws_z[part + r * stride];
     const float f = mr == -INFINITY ? (zr == zr ? 0.f : NAN) : fast_exp2(mr - M);
     Z = fmaf(zr, f, Z);
@@ -921,9 +923,18 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__
 #pragma unroll
     for (int k = 0; k < NG; ++k) x[k] = fmaf(at[32 * k], f, x[k]);
   }
+#pragma unroll
+  for (int k = 0; k < NG; ++k) sm_x[warp][32 * k + lane] = x[k];
+  if (lane == 0) sm_z[warp] = Z;
+  __syncthreads();
+  if (warp != 0) return;
+  Z = (sm_z[0] + sm_z[1]) + (sm_z[2] + sm_z[3]);
   const float inv = Z == 0.f ? 0.f : 1.f / Z;
 #pragma unroll
-  for (int k = 0; k < NG; ++k) x[k] *= inv;
+  for (int k = 0; k < NG; ++k) {
+    const int e = 32 * k + lane;
+    x[k] = ((sm_x[0][e] + sm_x[1][e]) + (sm_x[2][e] + sm_x[3][e])) * inv;
+  }
   if (a.c.format == KVQ_FMT_TQ4) {
     tq4_turn_lanes<NG>(x, static_cast<const uint32_t*>(a.c.signs), lane, true);
   } else if (a.c.format == KVQ_FMT_Q4_HAD32) {
@@ -935,7 +946,7 @@ __global__ void __launch_bounds__(128) attn_merge_kernel(const __grid_constant__
 }
 
 cudaError_t launch_attn_merge(const SeqAttnArgs& a, int ranges, cudaStream_t s) {
-  const dim3 grid((static_cast<unsigned>(a.max_rows) * a.Hq + 3) / 4, a.num_seqs);
+  const dim3 grid(static_cast<unsigned>(a.max_rows) * a.Hq, a.num_seqs);
   switch (a.c.head_dim) {
     case 64: return launch_pdl(attn_merge_kernel<64>, grid, dim3(128), 0, s, a, ranges);
     case 128: return launch_pdl(attn_merge_kernel<128>, grid, dim3(128), 0, s, a, ranges);
