@@ -980,10 +980,23 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
 
 // ---------------------------------------------------------------- several sequences, windows
 
-// From here on a sequence's rows fill enough of a pair of CTAs (256 columns of row x query
-// head): 8 columns at a time read and convert the cache once for every 8.
-constexpr int kChunkColumns = 64;
-static bool is_chunk(const SeqAttnArgs& a) { return static_cast<int64_t>(a.max_rows) * a.group > kChunkColumns; }
+// From so many columns (row x query head of one KV head) on a sequence's rows fill enough of a
+// pair of CTAs (256 columns); up to there 8 at a time convert the cache's rows again.  Measured,
+// few rows' kernel / many rows', us:
+//   4-bit, 256 wide: 16 sequences up to 8000, 36 columns 89 / 111, 48 106 / 111, 60 134 / 112;
+//     one of 30000, 24 columns 41 / 37, 48 68 / 39; windows of 1000 of 16, 30 columns 27 / 27, 48 37 / 27
+//   TQ4, 256 wide: 16 sequences, 30 columns 112 / 122, 36 133 / 123; one, 30 columns 73 / 43
+//   TQ4, 128 wide: 16 sequences, 40 columns 132 / 140, 48 157 / 141; one, 40 columns 69 / 52
+//   4-bit, 128 wide: 16 sequences, 48 columns 104 / 128, 64 129 / 128; one, 40 columns 47 / 48
+//   bf16, 256 wide: 16 sequences, 60 columns 187 / 213, 96 255 / 216; one, 60 columns 119 / 61
+//   bf16, 128 wide: 16 sequences, 64 columns 144 / 178; one, 48 columns 63 / 65
+static int few_columns(const kvq_cache& c) {
+  if (c.format == KVQ_FMT_TQ4) return c.head_dim == 256 ? 32 : 40;
+  return c.format != KVQ_FMT_BF16 && c.head_dim == 256 ? 40 : 64;
+}
+static bool is_chunk(const SeqAttnArgs& a) {
+  return a.max_rows > 1 && static_cast<int64_t>(a.max_rows) * a.group > few_columns(a.c);
+}
 
 // The shape of rows over a cache, in `a` with its window and sinks brought to what they say
 // for sequences of at most max_seq_len tokens.

@@ -962,10 +962,7 @@ FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max
   if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + 64 + 8 / group);
   // One wave of CTAs: four of the 4-bit rows' to an SM (registers), of the bf16 rows' as many as
   // their rings leave room for.
-  const int fit = c.format != KVQ_FMT_BF16 ? 4 : D == 256 ? 1 : D == 128 ? 2 : 4;
-  const int64_t want = std::max<int64_t>(1, fit * static_cast<int64_t>(n_sm) / std::max<int64_t>(blocks, 1));
-  const int64_t most = std::max<int64_t>(1, (keys + 63) / 64);  // a block for every warp
-  const int64_t splits = std::min(want, most);
+  const int fit = c.format != KVQ_FMT_BF16 || D == 64 ? 4 : D == 256 ? 1 : 3;
   FewPlan p{1, 1, 0};
   if (window == 0 && num_seqs > 1) {
     // Sequences of any lengths: so many blocks of 16 keys a CTA, that sequences of half the
@@ -979,16 +976,36 @@ FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max
     if (p.ranges == 1) p.per = 0;
     return p;
   }
-  const int widest = c.format == KVQ_FMT_TQ4 ? 8 : 16;  // (a CTA for every piece that is folded)
-  while (p.cluster < widest && p.cluster * 2 <= splits) p.cluster *= 2;
-  // Further clusters only where they save more than their fold costs (a second launch, about
-  // 3 us; a block takes a warp about 1.2 us): a window of 4096 keys of one sequence, 16 CTAs
-  // 11.5 us, 64 CTAs 12.5 us.
-  const int64_t most_ranges = std::min<int64_t>(64, splits / p.cluster);
+  // Clusters and ranges by what they are expected to cost: the blocks of a warp, which slow one
+  // another down on an SM, more CTAs' beginnings, and a second launch for the fold of ranges.
+  // All have to run at once: the clusters of a size that fit were counted (152 SMs, four CTAs to
+  // an SM 148 of 4, 74 of 8, 33 of 16; one to an SM 36, 15 and 7), and a second wave costs what
+  // the first does.  So of one sequence of 30000 tokens with 4 rows of 24 heads 46 us with three
+  // clusters of 16 for each block of columns, 35 with eleven of 4; bf16 rows, one row, 45 and 27.
+  // Clusters of 16 lie unevenly over the SMs and come as one range only (a window of 4096 keys of
+  // one sequence).  TQ4 has 8 pieces that are folded, a CTA for each.
+  const bool bf = c.format == KVQ_FMT_BF16;
+  const int sub = !bf && D <= 128 ? 2 : 1;  // blocks of a warp's step
+  const double unit = D / 256. * (bf ? 1.3 : c.format == KVQ_FMT_TQ4 ? 1.4 : 1.);
+  const double step[4] = {1.2, 1.5, 1.9, 2.45};  // us a block, 1 to 4 CTAs on the SM
+  const int64_t all = (keys + 15) / 16;
   double least = 0;
-  for (int64_t r = 1; r <= most_ranges; ++r) {
-    const double cost = 1.2 * static_cast<double>((keys + 64 * p.cluster * r - 1) / (64 * p.cluster * r)) + (r > 1 ? 3 + 0.05 * r : 0);
-    if (r == 1 || cost < least) least = cost, p.ranges = static_cast<int>(r);
+  for (int cs = c.format == KVQ_FMT_TQ4 ? 8 : 16; cs >= 1; cs /= 2) {
+    const double share = cs == 16 ? 0.73 : cs == 8 ? (fit == 1 ? 0.78 : 0.88) : cs == 4 ? 0.94 : 1.;
+    const int64_t room = static_cast<int64_t>(share * fit * n_sm / cs);
+    for (int64_t r = 1; r <= (cs == 16 ? 1 : 64); ++r) {
+      const int64_t per_step = 4 * sub * cs * r;
+      if ((blocks * r > room && cs * r > 1) || (cs * r > 1 && per_step >= 2 * all)) break;
+      const int64_t k = std::max<int64_t>(1, std::min<int64_t>(fit, (blocks * r * cs + n_sm - 1) / n_sm));
+      const double waves = blocks > room ? static_cast<double>(blocks) / static_cast<double>(room) : 1.;
+      const double cost = waves * (1.2 * static_cast<double>(k) + unit * step[k - 1] * static_cast<double>((all + per_step - 1) / per_step * sub)) +
+                          (r > 1 ? 2.5 + 0.06 * static_cast<double>(r) : 0.);
+      if (least == 0 || cost < least) {
+        least = cost;
+        p.cluster = cs;
+        p.ranges = static_cast<int>(r);
+      }
+    }
   }
   return p;
 }

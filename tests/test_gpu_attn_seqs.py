@@ -486,3 +486,22 @@ def test_slots_that_nobody_sees(K, fmt, rows, window, sinks):
     for p in (b.cache.k, b.cache.v) if fmt == "bf16" else (b.cache.k_scale, b.cache.v_scale):
         p.transpose(1, 2)[hidden] = math.nan
     assert torch.equal(b.attn(window, sinks), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 2, 4, 8, 9, 10, 11, 16, 17])
+def test_rows_at_which_the_work_is_split_otherwise(K, fmt, D, rows):
+    """Numbers of columns on both sides of the kernels' ranges (32, 36, 40, 64 and 68 of 4
+    heads), one long sequence (clusters and their fold) and several of unequal lengths."""
+    for lens in ([4099], [3001, rows, 700]):
+        b = Batch(K, fmt, 2, D, 16, lens, [rows] * len(lens), 4, seed=rows, dtype=torch.float32)
+        b.check(b.attn(), 0, 0)
+        b.check(b.attn(900, 7), 900, 7)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_window_of_one_row_over_many_clusters(K, fmt):
+    b = Batch(K, fmt, 1, 128, 64, [20000], [1], 8, seed=3, dtype=torch.float32)
+    b.check(b.attn(), 0, 0)
+    b.check(b.local(15000, 33), 15000, 33)
