@@ -980,22 +980,28 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
 
 // ---------------------------------------------------------------- several sequences, windows
 
-// From so many columns (row x query head of one KV head) on a sequence's rows fill enough of a
-// pair of CTAs (256 columns); up to there 8 at a time convert the cache's rows again.  Measured,
-// few rows' kernel / many rows', us:
-//   4-bit, 256 wide: 16 sequences up to 8000, 36 columns 89 / 111, 48 106 / 111, 60 134 / 112;
-//     one of 30000, 24 columns 41 / 37, 48 68 / 39; windows of 1000 of 16, 30 columns 27 / 27, 48 37 / 27
-//   TQ4, 256 wide: 16 sequences, 30 columns 112 / 122, 36 133 / 123; one, 30 columns 73 / 43
-//   TQ4, 128 wide: 16 sequences, 40 columns 132 / 140, 48 157 / 141; one, 40 columns 69 / 52
-//   4-bit, 128 wide: 16 sequences, 48 columns 104 / 128, 64 129 / 128; one, 40 columns 47 / 48
-//   bf16, 256 wide: 16 sequences, 60 columns 187 / 213, 96 255 / 216; one, 60 columns 119 / 61
-//   bf16, 128 wide: 16 sequences, 64 columns 144 / 178; one, 48 columns 63 / 65
-static int few_columns(const kvq_cache& c) {
-  if (c.format == KVQ_FMT_TQ4) return c.head_dim == 256 ? 32 : 40;
-  return c.format != KVQ_FMT_BF16 && c.head_dim == 256 ? 40 : 64;
+// Up to so many columns (row x query head of one KV head) a sequence: the few rows' kernel, which
+// converts the cache's rows again for every 8; above, a pair of CTAs takes up to 256.  Sequences
+// of any lengths fill the GPU with pieces either way; one sequence, or windows, leave the few
+// rows' clusters uneven.  Measured on both sides, few rows' kernel / many rows', us:
+//   16 sequences up to 30000    one sequence of 30000      16 windows of 1000
+//   4-bit, 256 wide   48 columns 295 / 381, 60 342 / 382   24 41 / 37, 36 48 / 38   30 27 / 27, 36 37 / 27
+//    (up to 8000)     48 columns 106 / 111, 60 120 / 112
+//   TQ4, 256 wide     36 columns 332 / 414, 48 440 / 415   24 49 / 42, 30 73 / 43   24 32 / 32, 30 40 / 32
+//   bf16, 256 wide    60 columns 632 / 785, 96 937 / 789   24 50 / 59, 36 75 / 59   24 25 / 38, 30 46 / 38
+//   4-bit, 128 wide   64 columns 371 / 412                 40 47 / 49, 60 85 / 50   64 26 / 42
+//   TQ4, 128 wide     48 columns 419 / 440, 60 528 / 442   24 46 / 51, 40 69 / 52   48 38 / 47
+//   bf16, 128 wide    64 columns 415 / 587                 48 63 / 65, 64 77 / 65   48 25 / 50, 64 42 / 52
+static int few_columns(const SeqAttnArgs& a) {
+  const bool ragged = a.num_seqs > 1 && a.window == 0, wide = a.c.head_dim == 256;
+  switch (a.c.format) {
+    case KVQ_FMT_TQ4: return ragged ? (wide ? 40 : 48) : (wide ? 24 : 32);
+    case KVQ_FMT_BF16: return ragged ? 64 : wide ? 32 : 48;
+    default: return ragged ? (wide ? 48 : 64) : (wide ? 32 : 48);
+  }
 }
 static bool is_chunk(const SeqAttnArgs& a) {
-  return a.max_rows > 1 && static_cast<int64_t>(a.max_rows) * a.group > few_columns(a.c);
+  return a.max_rows > 1 && static_cast<int64_t>(a.max_rows) * a.group > few_columns(a);
 }
 
 // The shape of rows over a cache, in `a` with its window and sinks brought to what they say
