@@ -117,6 +117,10 @@ __device__ __forceinline__ uint32_t few_lds16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
 }
+// The power of two that a key's p takes over from its scales, by the largest one's logarithm: 1
+// where no scale is above 16, so that such a key beside it, or behind a sequence's end, or what
+// is left of another in shared memory, does not change how others are rounded.
+__device__ __forceinline__ float wide_unit(float lsv) { return lsv > 4.f ? exp2f(rintf(lsv)) : 1.f; }
 __device__ __forceinline__ bool not_finite(uint32_t bf16) { return (bf16 & 0x7F80u) == 0x7F80u; }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ float half_lo(uint32_t w) { return __low2float(u32_as_h2(w)); }
@@ -668,8 +672,8 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
           p[sub][1] *= sg;
           p[sub][2] *= sh;
           p[sub][3] *= sh;
-        } else if (any_wide) {  // (scales above 16: p in units of the key's scale, below)
-          const float eg = exp2f(rintf(lg[sub][0])), eh = exp2f(rintf(lg[sub][1]));
+        } else if (any_wide) {  // (a key with a scale above 16: its p in units of the scale, here and below)
+          const float eg = wide_unit(lg[sub][0]), eh = wide_unit(lg[sub][1]);
           p[sub][0] *= eg;
           p[sub][1] *= eg;
           p[sub][2] *= eh;
@@ -685,8 +689,8 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
             const int key = 2 * t + (k & 1) + 8 * (k >> 1);
             few_lds<kSW>(vsc + (sub * 16 + key) * S::kScaleRow, sv[k]);
             if (any_wide) {
-              const float ek = exp2f(-rintf(__shfl_sync(0xffffffffu, lsv, sub * 16 + key)));
-              const __half2 e2 = __float2half2_rn(ek);
+              const float ek = wide_unit(__shfl_sync(0xffffffffu, lsv, sub * 16 + key));
+              const __half2 e2 = __float2half2_rn(1.f / ek);  // (a power of two: exact)
 #pragma unroll
               for (int w = 0; w < kSW; ++w) sv[k][w] = h2_as_u32(__hmul2(u32_as_h2(sv[k][w]), e2));
             }
