@@ -183,11 +183,11 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
   const kvq_cache& c = a.c;
   const int b = blockIdx.z, kvh = blockIdx.y % c.num_kv_heads, cb = blockIdx.y / c.num_kv_heads;
 
-  // what the sequence's rows see (metadata only: before the kernel in front is done)
+  // what the sequence's rows see (lengths, rows and tables are often made by the kernel in front)
+  pdl_wait();
   const SeqRows sr = seq_rows(a, b);
   const int cols = min(8, sr.n * a.group - 8 * cb);
   if (cols <= 0 || sr.state == kRowsSkip) {
-    pdl_wait();
     pdl_trigger();
     if (sr.state != kRowsOk && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
       set_status(a.status, KVQ_DEV_BAD_LENGTH);
@@ -196,7 +196,6 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
   const int base = sr.T - sr.n;  // position of the sequence's row 0
   const int i0 = 8 * cb / a.group, i1 = (8 * cb + cols - 1) / a.group;
   if (sr.state == kRowsNan) {
-    pdl_wait();
     pdl_trigger();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) set_status(a.status, KVQ_DEV_BAD_LENGTH);
     if (blockIdx.x == 0)
@@ -218,7 +217,6 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
     tile1 = min(all_tiles, tile0 + per);
     ranges = max(1, (all_tiles + per - 1) / per);
     if (static_cast<int>(blockIdx.x) >= ranges) {
-      pdl_wait();
       pdl_trigger();
       return;
     }
@@ -245,7 +243,6 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
   };
   int rows_now = find_rows(0), rows_next = find_rows(kBatch);
   bool bad_page = rows_now == -1;
-  pdl_wait();
 
   uint8_t* const ring = sm.ring + warp * (S::kStage * S::kStages);
   auto issue = [&](int i) {  // the loads of tile i, into its stage of the ring

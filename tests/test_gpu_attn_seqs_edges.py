@@ -3,7 +3,7 @@ tests/test_gpu_attn_seqs.py leaves out; its plain 64-bit arithmetic and toleranc
 import pytest
 import torch
 
-from tests.test_gpu_attn_seqs import DEV, FMTS, Batch
+from tests.test_gpu_attn_seqs import DEV, FMTS, Batch, ints
 from tests.test_gpu_parity import K  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +35,54 @@ def test_large_scales_that_nobody_sees(K, fmt, D, rows, window, sinks):
     for s in (b.cache.k_scale, b.cache.v_scale):
         s.transpose(1, 2)[hidden] = 60000.0
     assert torch.equal(b.attn(window, sinks), want)
+
+
+# ------------------------------------------------------------------ metadata made on the device
+
+def write(dst, src):
+    """By a kernel (a copy between tensors of one type may be the copy engine's)."""
+    torch.add(src, 0, out=dst)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows", [[1, 1, 1], [3, 1, 5], [150, 1, 40]])
+@pytest.mark.parametrize("last", ["seq_lens", "cu_rows", "block_tables"])
+def test_metadata_written_right_before(K, fmt, rows, last):
+    """Lengths, row numbers and tables that a kernel writes directly in front of a call, in a
+    stream and in a graph, count as if the device had been waited for."""
+    b = Batch(K, fmt, 2, 128, 16, [5000, 333, 700], rows, 3, seed=41)
+    right = {"seq_lens": ints(b.lens), "cu_rows": ints(b.cu), "block_tables": b.table}
+    # what a call that did not wait would see: other lengths, no rows, no pages
+    before = {"seq_lens": ints([17, 300, 1]), "cu_rows": ints([0] * 4), "block_tables": torch.full_like(b.table, -1)}
+    now = {k: v.clone() for k, v in before.items()}
+    out = torch.empty(b.n, 6, 128, device=DEV)
+    ws = {w: K.alloc_attn_workspace(b.cache, b.n, 3, 6, max(rows), 5000, w) for w in (0, 600)}
+
+    def call(meta, window):
+        if max(rows) == 1 and last != "cu_rows":
+            return K.decode_local(b.cache, b.q, meta["seq_lens"], meta["block_tables"], 5000, b.scale, window, out=out,
+                                  workspace=ws[window])
+        return K.attn_seqs(b.cache, b.q, meta["cu_rows"], meta["seq_lens"], meta["block_tables"], max(rows), 5000, b.scale,
+                           window=window, out=out, workspace=ws[window])
+
+    def step(window):
+        for name in sorted(right, key=lambda n: n == last):
+            write(now[name], right[name])
+        call(now, window)
+        for name in right:
+            write(now[name], before[name])
+
+    for window in (0, 600):
+        want = call(right, window).clone()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            out.zero_()
+            step(window)
+            assert torch.equal(out, want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(window)
+        for _ in range(5):
+            out.zero_()
+            graph.replay()
+            assert torch.equal(out, want)
