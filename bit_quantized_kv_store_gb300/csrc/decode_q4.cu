@@ -882,10 +882,22 @@ __global__ void __launch_bounds__(kQ4Warps * 32, MINB ? MINB : q4_min_blocks(NT)
   const int b = WIN ? blockIdx.z * a.rows_per_cta : blockIdx.z;
   const int nr = WIN ? min(a.rows_per_cta, a.nrows - b) : 1;
 
-  // Metadata first: the lengths and block tables are caller inputs that no
-  // kernel of this library writes, so they are read before the wait on the
-  // previous kernel of the stream (programmatic dependent launch) and their
-  // latency overlaps it.  The cache, the queries and every write come after.
+  // Only the barriers are set up before the wait on the previous kernel of the
+  // stream (programmatic dependent launch): lengths and block tables, too, are
+  // often written by it.  Lane i's page, of the partition's tile i, is loaded
+  // beside the length, not behind it.
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kQ4Warps; ++w) mbar_init(&sm.kbar[w], kQ4TPW);
+    for (int i = 0; i < VR; ++i) mbar_init(&sm.vfull[i], kQ4RoundTiles);
+    mbar_init(&sm.vempty, kQ4Warps);
+    sm.poison = 0;
+    fence_barrier_init();
+  }
+  const int k0 = p * a.part;
+  const uint32_t key0 = static_cast<uint32_t>(k0) + 16u * lane;
+  const int key_page = static_cast<int>(key0 / static_cast<uint32_t>(a.c.page_size));
+  pdl_wait();
+  const int32_t page = !GATHER && key_page < a.max_pages ? a.block_tables[(int64_t)b * a.bt_stride + key_page] : -1;
   int32_t T;                // keys of the CTA's longest row
   int32_t Tmin = 0;         // window: keys of its shortest row (a bad row counts 0)
   int32_t row_len = 0;      // window: lane i < nr holds the length of row b + i
@@ -914,7 +926,6 @@ __global__ void __launch_bounds__(kQ4Warps * 32, MINB ? MINB : q4_min_blocks(NT)
   }
   const int nparts = bad_len ? 0 : (T + a.part - 1) / a.part;
   const bool active = p < nparts;  // CTA-uniform
-  const int k0 = p * a.part;
   const int k1 = min(k0 + a.part, T);
   const int ntiles = active ? (k1 - k0 + 15) / 16 : 0;
   const int nrounds = (ntiles + kQ4RoundTiles - 1) / kQ4RoundTiles;  // <= 4
@@ -938,22 +949,11 @@ __global__ void __launch_bounds__(kQ4Warps * 32, MINB ? MINB : q4_min_blocks(NT)
   int32_t tile_row = -1;
   bool bad_page = false;
   if (!GATHER && lane < ntiles) {
-    const int key0 = k0 + 16 * lane;
-    const int32_t page = a.block_tables[(int64_t)b * a.bt_stride + key0 / a.c.page_size];
     if (page < 0 || page >= a.c.num_pages)
       bad_page = true;
     else
-      tile_row = static_cast<int32_t>(((int64_t)page * a.c.num_kv_heads + kvh) * a.c.page_size + key0 % a.c.page_size);
+      tile_row = static_cast<int32_t>(((int64_t)page * a.c.num_kv_heads + kvh) * a.c.page_size + static_cast<int>(key0 % a.c.page_size));
   }
-  if (active && threadIdx.x == 0) {
-    for (int w = 0; w < kQ4Warps; ++w) mbar_init(&sm.kbar[w], kQ4TPW);
-    for (int i = 0; i < VR; ++i) mbar_init(&sm.vfull[i], kQ4RoundTiles);
-    mbar_init(&sm.vempty, kQ4Warps);
-    sm.poison = 0;
-    fence_barrier_init();
-  }
-
-  pdl_wait();
   if constexpr (LM) {
     // no partition will count in: partition 0's CTA writes the outputs itself
     // (NaN for an invalid length, zeros for an empty sequence)
@@ -1519,35 +1519,35 @@ __global__ void __launch_bounds__(2 * kRoles * 32, 2) decode_q4_spec_kernel(cons
   const bool scorer = warp < kRoles;
   const int rw = warp & (kRoles - 1);  // the warp's index within its role
 
-  // metadata before the wait on the previous kernel (as in the round kernel);
-  // a gather's entries are checked against the sequence one by one instead
-  const int32_t T = GATHER ? a.n_sel : a.seq_lens[b];
-  const bool bad_len = !GATHER && (T < 0 || T > a.max_seq_len || (int64_t)T > (int64_t)a.max_pages * a.c.page_size);
-  const int nparts = bad_len ? 0 : (T + a.part - 1) / a.part;
-  const bool active = p < nparts;
-  const int k0 = p * a.part;
-  const int k1 = min(k0 + a.part, T);
-  const int ntiles = active ? (k1 - k0 + 15) / 16 : 0;
-  const int nrounds = (ntiles + kQ4RoundTiles - 1) / kQ4RoundTiles;
-  int32_t tile_row = -1;
-  bool bad_page = false;
-  if (!GATHER && lane < ntiles) {
-    const int key0 = k0 + 16 * lane;
-    const int32_t page = a.block_tables[(int64_t)b * a.bt_stride + key0 / a.c.page_size];
-    if (page < 0 || page >= a.c.num_pages)
-      bad_page = true;
-    else
-      tile_row = static_cast<int32_t>(((int64_t)page * a.c.num_kv_heads + kvh) * a.c.page_size + key0 % a.c.page_size);
-  }
-  if (active && threadIdx.x == 0) {
+  // the barriers, then the wait on the previous kernel (as in the round kernel)
+  if (threadIdx.x == 0) {
     for (int k = 0; k < 2; ++k)
       for (int w = 0; w < kRoles; ++w) mbar_init(&sm.kbar[k][w], 2);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.vfull[i], kQ4RoundTiles);
     sm.poison = 0;
     fence_barrier_init();
   }
-
+  const int k0 = p * a.part;
+  const uint32_t key0 = static_cast<uint32_t>(k0) + 16u * lane;
+  const int key_page = static_cast<int>(key0 / static_cast<uint32_t>(a.c.page_size));
   pdl_wait();
+  // (a gather's entries are checked against the sequence one by one)
+  const int32_t page = !GATHER && key_page < a.max_pages ? a.block_tables[(int64_t)b * a.bt_stride + key_page] : -1;
+  const int32_t T = GATHER ? a.n_sel : a.seq_lens[b];
+  const bool bad_len = !GATHER && (T < 0 || T > a.max_seq_len || (int64_t)T > (int64_t)a.max_pages * a.c.page_size);
+  const int nparts = bad_len ? 0 : (T + a.part - 1) / a.part;
+  const bool active = p < nparts;
+  const int k1 = min(k0 + a.part, T);
+  const int ntiles = active ? (k1 - k0 + 15) / 16 : 0;
+  const int nrounds = (ntiles + kQ4RoundTiles - 1) / kQ4RoundTiles;
+  int32_t tile_row = -1;
+  bool bad_page = false;
+  if (!GATHER && lane < ntiles) {
+    if (page < 0 || page >= a.c.num_pages)
+      bad_page = true;
+    else
+      tile_row = static_cast<int32_t>(((int64_t)page * a.c.num_kv_heads + kvh) * a.c.page_size + static_cast<int>(key0 % a.c.page_size));
+  }
   if (bad_len) {
     if (threadIdx.x == 0 && p == 0 && kvh == 0) set_status(a.status, KVQ_DEV_BAD_LENGTH);
     return;  // the merge writes NaN for this sequence

@@ -35,6 +35,8 @@
  *    selected indices) cannot be checked on the host.  Kernels check it and, on a
  *    bad value, skip the access, write NaN to the affected output and OR a
  *    KVQ_DEV_* bit into the caller's status word; nothing traps.
+ *    It is read on `stream` like everything else: the kernel or copy directly in
+ *    front of a call may write it.
  *  - Every kernel that waits (on a TMA copy) does so with an iteration limit and
  *    reports KVQ_DEV_TIMEOUT instead of hanging.
  */

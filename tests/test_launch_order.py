@@ -35,14 +35,18 @@ def test_kernels_are_found():
             "merge_kernel", "load_q4_kernel"} <= names
 
 
-def waiting(files):
-    return [k for k in KERNELS if "pdl_wait()" in k[2] and k[0] in files]
-
-
 def ahead_of_the_wait(body):
     return [a or b for a, b in READS.findall(body[:body.index("pdl_wait()")])]
 
 
-@pytest.mark.parametrize("file,name,body", waiting({"attn_few.cu", "attn_chunk.cu"}), ids=lambda x: x if len(x) < 40 else "")
-def test_attention_of_several_sequences_waits_first(file, name, body):
+@pytest.mark.parametrize("file,name,body", [k for k in KERNELS if "pdl_wait()" in k[2]], ids=lambda x: x if len(x) < 40 else "")
+def test_metadata_is_read_behind_the_wait(file, name, body):
     assert ahead_of_the_wait(body) == []
+
+
+def test_kernels_launched_ahead_wait():
+    launched = set()
+    for path in glob.glob(os.path.join(CSRC, "*.cu")):
+        launched |= set(re.findall(r"launch_pdl\((\w+)", open(path).read()))
+    without = {name for _, name, body in KERNELS if "pdl_wait()" not in body}
+    assert launched & {name for _, name, _ in KERNELS} and not launched & without
