@@ -22,8 +22,12 @@
 // transposed.  Scores alternate between two buffers of tensor memory; p (fp16) goes over
 // the scores it was made from and is the context product's A.
 // Queries, keys and values are fp16 here (each within 2^-12; bf16 rows: bf16, as they
-// are), a row's queries scaled by a power of two (to at most 2^15); p is fp16 (bf16), at most
-// 2^8: the softmax's reference follows when a row's scores pass it by more than 8.  Where a
+// are), a row's queries scaled by a power of two (to at most 2^15).  p is fp16: 2^(7 + s - m), at
+// most 2^15, as the reference m follows when a row's scores pass it by more than 8 (by more than
+// 6, for two bits more of p: 4096 rows at 16384 1498 -> 1677 us).  So a weight down to 2^-21 of
+// the row's largest keeps its 11 bits, and one below is off by up to 2^-32 of the largest: where
+// nearly all of the weight falls on a token whose value is near zero, as on a sequence's first,
+// the output is made of such weights.  (bf16 rows: p is bf16, 2^(s - m) up to 2^8.)  Where a
 // scale above 4096 turns up (8 s may not fit fp16), the pair goes over its keys once more
 // with keys and values in units of 2^8; nobody else pays for that.
 //
@@ -48,6 +52,8 @@ constexpr int kCkThreads = 512;
 constexpr int kCkRing = 5;       // units of raw codes that a decoding thread has in flight, and one
 constexpr int kCkOdd = 512;    // values that are not numbers, noted per CTA
 constexpr float kCkBigUnit = 0.00390625f;  // 2^-8: the unit of keys and values in the second pass
+constexpr float kCkRaise = 8.f;  // a row's reference is raised when its scores passed it by more
+constexpr float kCkHead = 7.f;   // p = 2^(this + s - m), at most 2^15 (fp16)
 enum { kCkQ4 = 0, kCkTq4 = 1, kCkBf16 = 2 };
 
 // tensor-memory columns (all 512 are allocated)
@@ -706,15 +712,15 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
         }
         float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         if (top != -INFINITY) top *= f;
-        // the reference is raised only when a row's scores passed it by more than 8 (base 2)
-        const bool raise = top > m_run + 8.f;
+        // the reference is raised only when a row's scores passed it by more (base 2)
+        const bool raise = top > m_run + kCkRaise;
         float corr = 1.f;
         if (raise) {
           corr = m_run == -INFINITY ? 1.f : fast_exp2(m_run - top);  // (z and the context are zero until then)
           z *= corr;
           m_run = top;
         }
-        const float mu = m_run == -INFINITY ? 0.f : m_run;
+        const float mu = m_run == -INFINITY ? 0.f : m_run - (kBf ? 0.f : kCkHead);
         if (j > 0 && __any_sync(0xffffffffu, raise && corr != 1.f)) {
           if (!ck_wait_warp(sm, &sm.pv_done[(J - 1) & 1], ((J - 1) >> 1) & 1, a.status)) break;
           tc_fence_after();

@@ -24,8 +24,9 @@
 // below: 2^-15 of a code times the largest query element, a 2^-15 part of a score.  For
 // values, whose small sums count, that is too much: they are converted, exactly, to c - 8.)
 // On the way out the scale multiplies p instead of 32 values: p' = fp16(fp16(p) s), two
-// roundings of 2^-12.  The softmax's reference counts the key's largest scale in (m bounds
-// s_j + log2 smax_j), so p' keeps its bits whatever the scales are.
+// roundings of 2^-11 at most.  p = 2^(11 + s_j - m), where m follows when s_j + log2 of the key's
+// largest scale (if that is above 1) passes it by more than 4: p and p' use fp16 up to 2^15, and
+// keep their bits down to 2^-25 of the largest p.  (TQ4 rows: p' = fp16(p s), and m counts small scales, too.)
 // TQ4 rows: levels by byte lookups (tq4_levels.cuh), the row's scale on scores and p.
 // bf16 rows: as they are; q and p in two bf16 halves (16 bits).
 //
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
 #pragma unroll
       for (int k = 1; k < kSW; ++k) h = __hmax2(h, u32_as_h2(w[k]));
       const float top = fmaxf(__low2float(h), __high2float(h));
-      lsv = fminf(fmaxf(__log2f(top), -10.f), 16.f);
+      lsv = fminf(fmaxf(__log2f(top), 0.f), 16.f);
       wide = lsv > 4.f;
     } else if constexpr (FMT == kFewTq4) {
       lsv = fminf(fmaxf(__log2f(half_of(few_lds16(vsc + 2 * (lane & (S::kKeys - 1))))), -60.f), 16.f);
@@ -583,7 +584,7 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
       top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
       top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
     }
-    // the reference follows when it is passed by more than 4 (p' stays below 2^4)
+    // the reference follows when it is passed by more than 4 (p' stays below 2^15)
     const bool up0 = top0 > m0 + 4.f, up1 = top1 > m1 + 4.f;
     if (__any_sync(0xffffffffu, up0 || up1)) {
       const float c0 = up0 ? fast_exp2(m0 - top0) : 1.f, c1 = up1 ? fast_exp2(m1 - top1) : 1.f;
@@ -599,7 +600,8 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
         acc[k][3] *= c1;
       }
     }
-    const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+    constexpr float kHead = FMT == kFewBf16 ? 0.f : 11.f;
+    const float u0 = m0 == -INFINITY ? 0.f : m0 - kHead, u1 = m1 == -INFINITY ? 0.f : m1 - kHead;
     float p[S::kBlocks][4];
 #pragma unroll
     for (int sub = 0; sub < S::kBlocks; ++sub) {

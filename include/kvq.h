@@ -606,8 +606,10 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
  * anything (-1 for pages given back).  A row that sees a key of a page outside the pool is
  * NaN (KVQ_DEV_BAD_PAGE), as is one that sees a key or value that is not a number; other
  * rows are not reached by either.
- * Queries, keys and values are fp16 operands (BF16: bf16), each rounded once where it is
- * not exact, sums and softmax statistics fp32.
+ * Queries, keys, values and the softmax's weights are fp16 operands (BF16: bf16), each rounded
+ * once where it is not exact (weights times 4-bit value scales twice), sums and softmax
+ * statistics fp32.  A weight below 2^-21 of its row's largest is off by up to 2^-32 of that.
+ * (BF16, few rows of a sequence: queries and weights in two bf16 halves.)
  * Any format but FP8_ROW, head_dim 64, 128 or 256, num_q_heads / num_kv_heads up to 64.
  *   q, out: [rows][num_q_heads][head_dim], q unrotated, out rotated back and rounded once
  *       into its type; out must not overlap q, nor its rows each other.

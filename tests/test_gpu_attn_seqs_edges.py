@@ -1,9 +1,11 @@
 """decode_local and attn_seqs where calls and values meet in ways that
 tests/test_gpu_attn_seqs.py leaves out; its plain 64-bit arithmetic and tolerances."""
+import math
+
 import pytest
 import torch
 
-from tests.test_gpu_attn_seqs import DEV, FMTS, Batch, ints
+from tests.test_gpu_attn_seqs import DEV, FMTS, Batch, ints, rnd
 from tests.test_gpu_parity import K  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -86,3 +88,47 @@ def test_metadata_written_right_before(K, fmt, rows, last):
             out.zero_()
             graph.replay()
             assert torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ weights far below a row's largest
+
+class OverSink(Batch):
+    """A first token whose score is 18, 20.5 or 23 powers of two above all others' (a head
+    each) and whose value is zero: the output is made of the others' weights.
+
+    p of the kernel for many rows (4-bit and TQ4 rows) is fp16 with the row's largest at 2^7 or
+    more, so a small one is also off by half a step of fp16's subnormals, 2^-25: 2^-32 of the
+    row's largest weight, here next to 1, in the mean square 2^-32 / sqrt(3) for every key."""
+
+    def __init__(self, K, fmt, D, rows, seed):
+        T = 6000
+        super().__init__(K, fmt, 1, D, 64, [T], [rows], 3, seed=seed, dtype=torch.float32)
+        u = torch.sign(rnd((D,), seed, D, "u"))
+        k, v = 0.05 * rnd((T, 1, D), seed, D, "keys"), rnd((T, 1, D), seed, D, "values")
+        k[0, 0], v[0] = u, 0.0
+        pos = torch.arange(T, device=DEV)
+        slots = self.table[0].long()[pos // 64] * 64 + pos % 64
+        K.store(self.cache, k.to(torch.bfloat16), v.to(torch.bfloat16), slots.to(torch.int32))
+        gap = torch.tensor([18.0, 20.5, 23.0], device=DEV)
+        self.q = (gap * math.log(2.0) / (self.scale * D))[:, None] * u + 0.1 * rnd((rows, 3, D), seed, D, "q")
+
+    def want(self, window=0, sinks=0):
+        out, var = super().want(window, sinks)
+        if self.n < 100 or self.fmt == "bf16":
+            return out, var
+        T = self.lens[0]
+        key, p = torch.arange(T, device=DEV), torch.arange(T - self.n, T, device=DEV)[:, None]
+        seen = key <= p
+        if window:
+            seen = seen & ((key > p - window) | (key < sinks))
+        _, v = self.kv(0, key)
+        return out, var + (seen.double() @ self.turn(v[0], inverse=True) ** 2)[:, None] * 2.0 ** -64 / 3
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 3, 150])
+def test_weights_far_below_the_largest(K, fmt, D, rows):
+    b = OverSink(K, fmt, D, rows, 45)
+    for window, sinks in ((0, 0), (4000, 1)):
+        b.check(b.attn(window, sinks), window, sinks)
