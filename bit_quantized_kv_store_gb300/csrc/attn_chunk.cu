@@ -37,7 +37,6 @@
 // to them through shared memory and issue slots.  Every role's loop is rolled: four roles
 // share a sub-partition's instruction fetch (unrolled 920 us).
 #include <algorithm>
-#include <climits>
 
 #include "f32x2.cuh"
 #include "rows.cuh"
@@ -50,7 +49,7 @@ namespace kvq {
 constexpr int kCkTile = 128;    // keys of a tile: 8 blocks of 16
 constexpr int kCkThreads = 512;
 constexpr int kCkRing = 5;       // units of raw codes that a decoding thread has in flight, and one
-constexpr int kCkOdd = 512;    // values that are not numbers, noted per CTA
+constexpr int kCkNotes = 512;  // keys that some rows of a pair see and others do not: up to 255 at either end
 constexpr float kCkBigUnit = 0.00390625f;  // 2^-8: the unit of keys and values in the second pass
 constexpr float kCkRaise = 8.f;  // a row's reference is raised when its scores passed it by more
 constexpr float kCkHead = 7.f;   // p = 2^(this + s - m), at most 2^15 (fp16)
@@ -83,8 +82,10 @@ struct CkSmem {
   uint32_t row_top[128];                        // per row: its largest query element
   float factor[128];                            // per row: what its scores' units are worth
   float m[128], z[128];
-  uint2 odd[kCkOdd];  // (key, dim or group and bits) of values of partly seen tiles that are not numbers
-  int odd_count, lost_lo, lost_hi;
+  // values that are not numbers, of keys that not every row sees: four bits a key, one for each of
+  // this CTA's groups (bf16 rows: one for this CTA's half of the dims)
+  uint32_t noted[kCkNotes / 8];
+  int any_noted;
   int over;  // a key's or value's scale above 4096 was met
   uint32_t tmem_base;
   int abort;
@@ -146,6 +147,15 @@ struct CkWalk {
     plain1 = p0 < kCkTile - 1 ? 0 : ((((p0 - kCkTile + 1) >> 4) + shift) >> 3) + 1;
   }
   __device__ __forceinline__ bool edge(int tile) const { return tile0 + tile < plain0 || tile0 + tile >= plain1; }
+  // The note of a key that some rows see and others do not: those behind the first row (1 ..
+  // 255), and those that its window holds and the last row's does not (257 .. 511).
+  enum { kEverybody = -1, kNobody = -2 };
+  __device__ __forceinline__ int note_of(int key) const {
+    if (!any_visible(key, p0, p1, window, sinks)) return kNobody;
+    if (all_visible(key, 1, p0, p1, window, sinks)) return kEverybody;
+    return key > p0 ? key - p0 : kCkNotes / 2 + key - (p0 - window);
+  }
+  __device__ __forceinline__ int key_of_note(int i) const { return i < kCkNotes / 2 ? p0 + i : p0 - window + i - kCkNotes / 2; }
 };
 
 // 8 codes of a word as fp16 operands, times (s, s): 4-bit groups in the order 0 4 1 5 2 6 3 7,
@@ -172,18 +182,18 @@ __device__ __forceinline__ int ck_pos(int j) { return FMT == kCkQ4 ? (j & 3) * 2
 template <int FMT>
 __device__ __forceinline__ int ck_elem(int i) { return FMT == kCkQ4 ? (i >> 1) + 4 * (i & 1) : i; }
 
-// Note a value that is not a number, of a key that some row sees (else it is of no
-// consequence: a slot behind the end, or between sinks and window) and not every one.
+// 0 x NaN: a value that is not a number, of a key that some rows do not see, is taken out of the
+// operands and noted, for the rows that do see it.  (One that every row sees stays; one that
+// nobody sees, in a slot behind the end or between sinks and window, is of no consequence.)
+// Whether to take it out; `bit`: its group here.
 template <int D>
-__device__ __forceinline__ void ck_note(CkSmem<D>& sm, const CkWalk& wk, int key, uint32_t what) {
-  if (!any_visible(key, wk.p0, wk.p1, wk.window, wk.sinks)) return;
-  const int i = atomicAdd(&sm.odd_count, 1);
-  if (i < kCkOdd) {
-    sm.odd[i] = make_uint2(static_cast<uint32_t>(key), what);
-  } else {
-    atomicMin(&sm.lost_lo, key);
-    atomicMax(&sm.lost_hi, key);
+__device__ __forceinline__ bool ck_note(CkSmem<D>& sm, const CkWalk& wk, int key, int bit) {
+  const int note = wk.note_of(key);
+  if (note >= 0) {
+    atomicOr(&sm.noted[note >> 3], 1u << (4 * (note & 7) + bit));
+    sm.any_noted = 1;
   }
+  return note != CkWalk::kEverybody;
 }
 
 // ---------------------------------------------------------------- the decoders' part
@@ -334,7 +344,7 @@ struct CkPart {
           asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         if constexpr (!IS_K) {
-          if (wk.edge(j)) {  // 0 x NaN: what not every row sees is taken out and noted
+          if (wk.edge(j)) {
 #pragma unroll 1
             for (int i = 0; i < kUnits; ++i) {
               const uint32_t at = buf(j & 1) + place(i);
@@ -345,10 +355,11 @@ struct CkPart {
               for (int e = 0; e < 8; ++e) {
                 const uint32_t x = (w[e >> 1] >> (16 * (e & 1))) & 0xFFFFu;
                 if (ck_not_finite16(x)) {
-                  found = true;
                   const int key = unit_key(i);
-                  ck_note(sm, wk, wk.key_of(j, key >> 4) + (key & 15), static_cast<uint32_t>((rank * kC + unit_chunk(i)) * 8 + e) << 16 | x);
-                  w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                  if (ck_note(sm, wk, wk.key_of(j, key >> 4) + (key & 15), 0)) {
+                    found = true;
+                    w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                  }
                 }
               }
               if (found) ck_sts(at, w[0], w[1], w[2], w[3]);
@@ -387,9 +398,8 @@ struct CkPart {
           asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(ring_s + slot * 512) : "memory");
           slot = slot == kCkRing - 1 ? 0 : slot + 1;
           uint32_t ss = prmt(sw, 0u, pick);
-          if (edge && (ss & 0x7C00u) == 0x7C00u) {  // 0 x NaN: what not every row sees is taken out and noted
-            ck_note(sm, wk, wk.key_of(j, (kg + i * kSpan) >> 1) + in16(), static_cast<uint32_t>(chunk()) << 16);
-            ss = 0;
+          if (edge && (ss & 0x7C00u) == 0x7C00u) {
+            if (ck_note(sm, wk, wk.key_of(j, (kg + i * kSpan) >> 1) + in16(), (tid >> 3) % kC)) ss = 0;
           }
           const uint32_t size = ss & 0x7FFFu;
           top = max(top, size > 0x7C00u ? 0u : size);  // (not a number: no matter)
@@ -462,6 +472,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     if (lane == 0) sm.seq = seq, sm.block = block;
   }
   if (threadIdx.x < 128) sm.row_top[threadIdx.x] = 0;
+  if (threadIdx.x >= 128 && threadIdx.x < 128 + kCkNotes / 8) sm.noted[threadIdx.x - 128] = 0;
   if (threadIdx.x == 32) {
     for (int h = 0; h < 2; ++h) {
       mbar_init(&sm.k_ready[h], rank == 0 ? 5 : 4);
@@ -474,10 +485,8 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     mbar_init(&sm.drained, 1);
     mbar_init(&sm.q_ready, rank == 0 ? 17 : 16);
     sm.abort = 0;
-    sm.odd_count = 0;
+    sm.any_noted = 0;
     sm.over = 0;
-    sm.lost_lo = INT_MAX;
-    sm.lost_hi = -1;
     fence_barrier_init();
   }
   __syncthreads();
@@ -791,7 +800,8 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
       big = (pair_ld_u32(pair_addr(&sm.over, 0)) | pair_ld_u32(pair_addr(&sm.over, 1))) != 0;
       if (!big) break;
       first = nt;
-      if (threadIdx.x == 0) sm.odd_count = 0, sm.lost_lo = INT_MAX, sm.lost_hi = -1;
+      if (threadIdx.x < kCkNotes / 8) sm.noted[threadIdx.x] = 0;
+      if (threadIdx.x == 0) sm.any_noted = 0;
       pair_sync();
     } else {
       break;
@@ -800,7 +810,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
 
   // ---------------- the rows: out of tensor memory, over the operands, rotated back, stored
   const int ranges = gridDim.z;
-  const int noted = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd_count, 0)) + pair_ld_u32(pair_addr(&sm.odd_count, 1)));
+  const uint32_t noted = pair_ld_u32(pair_addr(&sm.any_noted, 0)) | pair_ld_u32(pair_addr(&sm.any_noted, 1));
   // A thread takes a row's groups of 32 out of tensor memory, rotates them back and stores
   // them.  Over the operands and eight rows a warp where a rotation spans the row (TQ4) or
   // some value is not a number.
@@ -847,29 +857,31 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
     __syncthreads();
     // values that are not numbers, into the rows that see their keys
     for (int other = 0; other < 2; ++other) {
-      const int count = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd_count, other)));
-      if (count == 0) continue;
+      if (pair_ld_u32(pair_addr(&sm.any_noted, other)) == 0) continue;
       for (int r = threadIdx.x; r < my_rows; r += kCkThreads) {
         const int p = base + i0 + r / grp;
-        for (int i = 0; i < min(count, kCkOdd); ++i) {
-          const int key = static_cast<int>(pair_ld_u32(pair_addr(&sm.odd[i].x, other)));
-          if (!key_visible(key, p, a.window, a.sinks)) continue;
-          const uint32_t what = pair_ld_u32(pair_addr(&sm.odd[i].y, other));
-          if constexpr (kBf) {
-            sm.out[r][what >> 16] += __uint_as_float(what << 16);
-          } else {
-            for (int e = 0; e < 32; ++e) sm.out[r][(what >> 16) * 32 + e] = NAN;
+        for (int i8 = 0; i8 < kCkNotes / 8; ++i8)
+          for (uint32_t left = pair_ld_u32(pair_addr(&sm.noted[i8], other)); left != 0;) {
+            const int sub = (__ffs(left) - 1) >> 2, i = 8 * i8 + sub;
+            const uint32_t which = (left >> (4 * sub)) & 15u;
+            left &= ~(15u << (4 * sub));
+            if (!key_visible(wk.key_of_note(i), p, a.window, a.sinks)) continue;
+            if constexpr (kBf) {
+              // the value's elements, from the cache again (its page is a good one: it was read)
+              const int key = wk.key_of_note(i), pg = static_cast<int>(fast_div(static_cast<uint32_t>(key >> 4), a.page_blocks));
+              const int page = a.block_tables[static_cast<int64_t>(seq) * a.max_pages + pg];
+              const int64_t at = (static_cast<int64_t>(page) * kv_heads + kvh) * a.c.page_size + (key - pg * a.c.page_size);
+              const uint16_t* v = static_cast<const uint16_t*>(a.c.v) + at * D + other * (D / 2);
+              for (int e = 0; e < D / 2; ++e) {
+                const uint32_t x = v[e];
+                if (ck_not_finite16(x)) sm.out[r][other * (D / 2) + e] += __uint_as_float(x << 16);
+              }
+            } else {
+              for (int k = 0; k < (NG + 1) / 2; ++k)
+                if ((which >> k) & 1u)
+                  for (int e = 0; e < 32; ++e) sm.out[r][(other * (NG / 2) + k) * 32 + e] = NAN;
+            }
           }
-        }
-        if (count > kCkOdd) {
-          // those that found no room: rows that see a key between the first and the last of them
-          const int lo = static_cast<int>(pair_ld_u32(pair_addr(&sm.lost_lo, other)));
-          const int hi = static_cast<int>(pair_ld_u32(pair_addr(&sm.lost_hi, other)));
-          bool hit = false;
-          for (int key = lo; key <= hi && !hit; ++key) hit = key_visible(key, p, a.window, a.sinks);
-          if (hit)
-            for (int e = 0; e < D; ++e) sm.out[r][e] = NAN;
-        }
       }
     }
     __syncthreads();

@@ -604,8 +604,9 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
  * window, sinks make no difference.
  * Pages of which no row sees any key are not looked at: their block-table entries may be
  * anything (-1 for pages given back).  A row that sees a key of a page outside the pool is
- * NaN (KVQ_DEV_BAD_PAGE), as is one that sees a key or value that is not a number; other
- * rows are not reached by either.
+ * NaN (KVQ_DEV_BAD_PAGE), as is one that sees a NaN key and, in the value's dims (those that it
+ * is rotated with, too), one that sees a NaN value; an infinite value makes them infinite or
+ * NaN.  Other rows keep their bits.
  * Queries, keys, values and the softmax's weights are fp16 operands (BF16: bf16), each rounded
  * once where it is not exact (weights times 4-bit value scales twice), sums and softmax
  * statistics fp32.  A weight below 2^-21 of its row's largest is off by up to 2^-32 of that.

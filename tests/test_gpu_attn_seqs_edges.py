@@ -132,3 +132,31 @@ def test_weights_far_below_the_largest(K, fmt, D, rows):
     b = OverSink(K, fmt, D, rows, 45)
     for window, sinks in ((0, 0), (4000, 1)):
         b.check(b.attn(window, sinks), window, sinks)
+
+
+# ------------------------------------------------------------------ many values that are not numbers
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("rows", [3, 84, 130])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_rows_between_keys_that_are_not_numbers(K, fmt, D, rows, what):
+    """Two runs of whole tokens that are not numbers: the rows that see neither keep their
+    bits, those that see one are not finite."""
+    T, W = 484, 33
+    b = Batch(K, fmt, 2, D, 16, [T], [rows], 3, seed=47)
+    want = b.attn(W)
+    runs = [list(range(T - 84, T - 79)), list(range(T - 24, T - 19))]
+    for run, sign in zip(runs, (1, -1)):
+        for key in run:
+            at = int(b.table[0, key // 16]), slice(None), key % 16
+            (b.cache.v if fmt == "bf16" else b.cache.v_scale)[at] = what * sign
+    outs = [b.attn(W) for _ in range(3)]
+    for got in outs:
+        assert torch.equal(got.nan_to_num(777.0), outs[0].nan_to_num(777.0))
+    for i, p in enumerate(range(T - rows, T)):
+        seen = [any(p - W < key <= p for key in run) for run in runs]
+        if not any(seen):
+            assert torch.equal(outs[0][i], want[i]), p
+        else:  # (an infinite value's product with a weight's second half may be NaN)
+            assert not bool(outs[0][i].isfinite().any()), p
