@@ -680,7 +680,8 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
       const int r = 32 * (warp & 3) + lane;
       const int p = r < my_rows ? base + i0 + r / grp : -kNoKey;
       ck_wait_warp(sm, &sm.q_ready, 0, a.status);  // (the factors)
-      const float f = sm.factor[r] * (big ? 1.f / kCkBigUnit : 1.f);
+      const float f_all = sm.factor[r] * (big ? 1.f / kCkBigUnit : 1.f);
+      float f = f_all;
       float m_run = -INFINITY, z = 0.f;
       for (int j = 0; j < nt; ++j) {
         const int J = first + j, b = J & 1;
@@ -722,12 +723,20 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
         float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         if (top != -INFINITY) top *= f;
         // the reference is raised only when a row's scores passed it by more (base 2)
-        const bool raise = top > m_run + kCkRaise;
+        const bool raise = top - m_run > kCkRaise;
         float corr = 1.f;
         if (raise) {
           corr = m_run == -INFINITY ? 1.f : fast_exp2(m_run - top);  // (z and the context are zero until then)
           z *= corr;
           m_run = top;
+          if (fabsf(top) > kFarScore || f != f_all) {  // the row's scores from here on in other units
+            m_run = top * (f_all / f);
+            f = f_all;
+            if (fabsf(m_run) > kFarScore) {
+              f *= kFarScore / fabsf(m_run);
+              m_run = copysignf(kFarScore, m_run);
+            }
+          }
         }
         const float mu = m_run == -INFINITY ? 0.f : m_run - (kBf ? 0.f : kCkHead);
         if (j > 0 && __any_sync(0xffffffffu, raise && corr != 1.f)) {
@@ -772,7 +781,7 @@ __global__ void __launch_bounds__(kCkThreads, 1) attn_chunk_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_ready[b]);
       }
-      sm.m[r] = m_run;
+      sm.m[r] = m_run == -INFINITY ? m_run : m_run * (f_all / f);
       sm.z[r] = z;
       const int last = first + nt - 1;
       if (nt > 0) ck_wait_warp(sm, &sm.pv_done[last & 1], (last >> 1) & 1, a.status);

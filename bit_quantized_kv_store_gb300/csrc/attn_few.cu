@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
 
   // ---------------- the keys
   const uint32_t qf = smem_u32(&sm.qf[0][lane]);
-  const float f0 = sm.factor[2 * t], f1 = sm.factor[2 * t + 1];
+  float f0 = sm.factor[2 * t], f1 = sm.factor[2 * t + 1];
   // positions of columns 2t, 2t + 1 and g (before any key where there is no such column)
   auto pos_of = [&](int n) { return n < cols ? base + (8 * cb + n) / a.group : -kNoKey; };
   const int pc0 = pos_of(2 * t), pc1 = pos_of(2 * t + 1), pcg = pos_of(g);
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
     }
 
     // ---------------- online softmax (base 2)
-    float top0 = -INFINITY, top1 = -INFINITY;
+    float top0, top1;
     float lg[S::kBlocks][2];
 #pragma unroll
     for (int sub = 0; sub < S::kBlocks; ++sub) {
@@ -576,18 +576,44 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
         lg[sub][0] = __shfl_sync(0xffffffffu, lsv, sub * 16 + g);
         lg[sub][1] = __shfl_sync(0xffffffffu, lsv, sub * 16 + g + 8);
       }
-      top0 = fmaxf(top0, fmaxf(s[sub][0] + lg[sub][0], s[sub][2] + lg[sub][1]));
-      top1 = fmaxf(top1, fmaxf(s[sub][1] + lg[sub][0], s[sub][3] + lg[sub][1]));
     }
+    auto find_top = [&] {
+      top0 = top1 = -INFINITY;
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
-      top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
-    }
+      for (int sub = 0; sub < S::kBlocks; ++sub) {
+        top0 = fmaxf(top0, fmaxf(s[sub][0] + lg[sub][0], s[sub][2] + lg[sub][1]));
+        top1 = fmaxf(top1, fmaxf(s[sub][1] + lg[sub][0], s[sub][3] + lg[sub][1]));
+      }
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        top0 = fmaxf(top0, __shfl_xor_sync(0xffffffffu, top0, o));
+        top1 = fmaxf(top1, __shfl_xor_sync(0xffffffffu, top1, o));
+      }
+    };
+    find_top();
     // the reference follows when it is passed by more than 4 (p' stays below 2^15)
-    const bool up0 = top0 > m0 + 4.f, up1 = top1 > m1 + 4.f;
+    const bool up0 = top0 - m0 > 4.f, up1 = top1 - m1 > 4.f;
     if (__any_sync(0xffffffffu, up0 || up1)) {
       const float c0 = up0 ? fast_exp2(m0 - top0) : 1.f, c1 = up1 ? fast_exp2(m1 - top1) : 1.f;
+      if constexpr (FMT != kFewBf16) {
+        const float all0 = sm.factor[2 * t], all1 = sm.factor[2 * t + 1];
+        const bool new0 = up0 && (fabsf(top0) > kFarScore || f0 != all0), new1 = up1 && (fabsf(top1) > kFarScore || f1 != all1);
+        if (__any_sync(0xffffffffu, new0 || new1)) {  // a column's scores from here on in other units
+          auto unit = [](float top, float f, float all) {
+            const float far = fabsf(top * (all / f));
+            return far > kFarScore ? all * (kFarScore / far) : all;
+          };
+          const float g0 = new0 ? unit(top0, f0, all0) : f0, g1 = new1 ? unit(top1, f1, all1) : f1;
+          const float r0 = g0 / f0, r1 = g1 / f1;
+          f0 = g0;
+          f1 = g1;
+#pragma unroll
+          for (int sub = 0; sub < S::kBlocks; ++sub)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[sub][j] *= j & 1 ? r1 : r0;
+          find_top();
+        }
+      }
       if (up0) m0 = top0;
       if (up1) m1 = top1;
       z0 *= c0;
@@ -741,6 +767,10 @@ __global__ void __launch_bounds__(WARPS * 32, FMT == kFewBf16 && D == 256 ? 1 : 
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();  // every ring is done with
   if (g == 0) {
+    if constexpr (FMT != kFewBf16) {
+      if (m0 != -INFINITY) m0 *= sm.factor[2 * t] / f0;
+      if (m1 != -INFINITY) m1 *= sm.factor[2 * t + 1] / f1;
+    }
     sm.fm[warp][2 * t] = m0;
     sm.fm[warp][2 * t + 1] = m1;
     sm.fz[warp][2 * t] = z0;

@@ -41,6 +41,12 @@ __device__ __forceinline__ SeqRows seq_rows(const SeqAttnArgs& a, int b) {
   return s;
 }
 
+// Where a row's reference is a score (base 2) beyond this, its scores are taken in units that
+// bring the reference down to it, so that their differences, and with them p and its place in
+// fp16, are not off by as much as 32 bits are coarse there (32 at 2^28).  Two scores that differ
+// by more than their operands' rounding, 2^-11 of them, are still 500 powers of two apart.
+constexpr float kFarScore = 1048576.f;
+
 __device__ __forceinline__ bool key_visible(int key, int p, int window, int sinks) {
   return key <= p && (window == 0 || key > p - window || key < sinks);
 }

@@ -160,3 +160,44 @@ def test_rows_between_keys_that_are_not_numbers(K, fmt, D, rows, what):
             assert torch.equal(outs[0][i], want[i]), p
         else:  # (an infinite value's product with a weight's second half may be NaN)
             assert not bool(outs[0][i].isfinite().any()), p
+
+
+# ------------------------------------------------------------------ scores at which 32 bits are coarse
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("rows", [1, 3, 150])
+def test_scores_of_any_size(K, fmt, D, rows):
+    """One key's score is several times all others': its value is the output, at any size."""
+    T, key = 600, 100
+    b = Batch(K, fmt, 1, D, 64, [T], [rows], 3, seed=53)
+    u = torch.sign(rnd((D,), 53, D, "u"))
+    pos = torch.arange(T, device=DEV)
+    slots = b.table[0].long()[pos // 64] * 64 + pos % 64
+    k, v = rnd((T, 1, D), 53, D, "keys", scale=0.3), rnd((T, 1, D), 53, D, "values", scale=3.0)
+    k[key, 0] = 4 * u
+    K.store(b.cache, k.to(torch.bfloat16), v.to(torch.bfloat16), slots.to(torch.int32))
+    for size in (10, 24, 25, 26, 27, 28, 29, 30, 35, 40, 60):  # the score is about 2^size
+        b.q = ((2.0 ** size / (4 * D * b.scale)) * (u + 0.1 * rnd((rows, 3, D), 53, D, "q"))).to(torch.bfloat16)
+        b.check(b.attn(), 0, 0)
+        b.check(b.attn(520, 2), 520, 2)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("rows", [1, 3, 150])
+@pytest.mark.parametrize("first", [True, False])
+def test_scores_far_below_the_others(K, fmt, D, rows, first):
+    """The first (or the last) keys' scores are millions of powers of two below the others'."""
+    T = 1500
+    b = Batch(K, fmt, 1, D, 64, [T], [rows], 3, seed=55)
+    u = torch.sign(rnd((D,), 55, D, "u"))
+    pos = torch.arange(T, device=DEV)
+    slots = b.table[0].long()[pos // 64] * 64 + pos % 64
+    k, v = rnd((T, 1, D), 55, D, "keys"), rnd((T, 1, D), 55, D, "values")
+    far = slice(0, 700) if first else slice(800, T)
+    k[far] = -30000 * u * (1 + 0.1 * rnd((T, 1, 1), 55, D, "far")[far])
+    K.store(b.cache, k.to(torch.bfloat16), v.to(torch.bfloat16), slots.to(torch.int32))
+    b.q = (8 * u + rnd((rows, 3, D), 55, D, "q")).to(torch.bfloat16)
+    b.check(b.attn(), 0, 0)
+    b.check(b.attn(1300, 64), 1300, 64)
