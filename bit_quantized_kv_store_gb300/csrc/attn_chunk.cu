@@ -29,7 +29,7 @@
 // nearly all of the weight falls on a token whose value is near zero, as on a sequence's first,
 // the output is made of such weights.  (bf16 rows: p is bf16, 2^(s - m) up to 2^8.)  Where a
 // scale above 4096 turns up (8 s may not fit fp16), the pair goes over its keys once more
-// with keys and values in units of 2^8; nobody else pays for that.
+// with keys and values in units of 2^8; nobody else pays for that, nor do slots that no row sees set it off.
 //
 // Measured (one GB300, 24 / 4 heads of 256, 4-bit rows): 4096 rows at 16384 1473 us (1260
 // TFLOP/s), 2048 rows with a window of 4096 215 us.  The products alone, with everybody else
@@ -86,7 +86,7 @@ struct CkSmem {
   // this CTA's groups (bf16 rows: one for this CTA's half of the dims)
   uint32_t noted[kCkNotes / 8];
   int any_noted;
-  int over;  // a key's or value's scale above 4096 was met
+  int over;  // a scale above 4096 was met, of a key that some row sees
   uint32_t tmem_base;
   int abort;
   int seq, block;
@@ -378,7 +378,6 @@ struct CkPart {
       constexpr uint32_t kStepUnit = IS_K ? kSpan * 16 * D : kSpan * 128, kStepWord = IS_K ? 128 : 2048;
       const uint32_t ring = smem_u32(&sm.raw[IS_K ? 0 : 1][0][tid]), ring_s = smem_u32(&sm.raw_scale[IS_K ? 0 : 1][0][tid]);
       const int first = big ? wk.tiles : 0;
-      uint32_t top = 0;
       int slot = 0;
 #pragma unroll 1
       for (int j = 0; j < wk.tiles; ++j) {
@@ -398,11 +397,12 @@ struct CkPart {
           asm volatile("ld.shared.u32 %0, [%1];" : "=r"(sw) : "r"(ring_s + slot * 512) : "memory");
           slot = slot == kCkRing - 1 ? 0 : slot + 1;
           uint32_t ss = prmt(sw, 0u, pick);
-          if (edge && (ss & 0x7C00u) == 0x7C00u) {
-            if (ck_note(sm, wk, wk.key_of(j, (kg + i * kSpan) >> 1) + in16(), (tid >> 3) % kC)) ss = 0;
+          if ((ss & 0x7FFFu) > 0x6C00u) {  // above 4096: a product may pass 65504; or not a number
+            const int key = wk.key_of(j, (IS_K ? rank * 4 : 0) + ((kg + i * kSpan) >> 1)) + in16();
+            if (!any_visible(key, wk.p0, wk.p1, wk.window, wk.sinks)) ss = 0;
+            else if ((ss & 0x7C00u) != 0x7C00u) sm.over = 1;
+            else if (edge && ck_note(sm, wk, key, (tid >> 3) % kC)) ss = 0;
           }
-          const uint32_t size = ss & 0x7FFFu;
-          top = max(top, size > 0x7C00u ? 0u : size);  // (not a number: no matter)
           __half2 s2 = u32_as_h2(ss);
           if (big) s2 = __hmul2(s2, __float2half2_rn(kCkBigUnit));
 #pragma unroll
@@ -417,7 +417,6 @@ struct CkPart {
         __syncwarp();
         if (lane == 0) mbar_arrive(&ready[J & 1]);
       }
-      if (top > 0x6C00u) sm.over = 1;  // above 4096: products that may pass 65504
     }
   }
 };

@@ -201,3 +201,18 @@ def test_scores_far_below_the_others(K, fmt, D, rows, first):
     b.q = (8 * u + rnd((rows, 3, D), 55, D, "q")).to(torch.bfloat16)
     b.check(b.attn(), 0, 0)
     b.check(b.attn(1300, 64), 1300, 64)
+
+
+# ------------------------------------------------------------------ scales that need the second pass
+
+@pytest.mark.parametrize("fmt", SCALED)
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 5), (300, 37)])
+def test_large_scales_that_nobody_sees_beside_many_rows(K, fmt, D, window, sinks):
+    """As above: such slots do not send the rows over their keys once more, in other units."""
+    b = Batch(K, fmt, 2, D, 64, [777, 300], [150, 150], 3, seed=49, v_scale=1e-5)
+    want = b.attn(window, sinks)
+    hidden = unseen(b, window, sinks)
+    for s in (b.cache.k_scale, b.cache.v_scale):
+        s.transpose(1, 2)[hidden] = 60000.0
+    assert torch.equal(b.attn(window, sinks), want)
