@@ -29,7 +29,8 @@
 // nearly all of the weight falls on a token whose value is near zero, as on a sequence's first,
 // the output is made of such weights.  (bf16 rows: p is bf16, 2^(s - m) up to 2^8.)  Where a
 // scale above 4096 turns up (8 s may not fit fp16), the pair goes over its keys once more
-// with keys and values in units of 2^8; nobody else pays for that, nor do slots that no row sees set it off.
+// with keys and values in units of 8 (a scale below 2^-11 is then rounded to 2^-22); nobody else
+// pays for that, nor do slots that no row sees set it off.
 //
 // Measured (one GB300, 24 / 4 heads of 256, 4-bit rows): 4096 rows at 16384 1473 us (1260
 // TFLOP/s), 2048 rows with a window of 4096 215 us.  The products alone, with everybody else
@@ -50,7 +51,7 @@ constexpr int kCkTile = 128;    // keys of a tile: 8 blocks of 16
 constexpr int kCkThreads = 512;
 constexpr int kCkRing = 5;       // units of raw codes that a decoding thread has in flight, and one
 constexpr int kCkNotes = 512;  // keys that some rows of a pair see and others do not: up to 255 at either end
-constexpr float kCkBigUnit = 0.00390625f;  // 2^-8: the unit of keys and values in the second pass
+constexpr float kCkBigUnit = 0.125f;  // of keys and values in the second pass: 8 x 65504 fits fp16, and scales from 2^-11 on are exact
 constexpr float kCkRaise = 8.f;  // a row's reference is raised when its scores passed it by more
 constexpr float kCkHead = 7.f;   // p = 2^(this + s - m), at most 2^15 (fp16)
 enum { kCkQ4 = 0, kCkTq4 = 1, kCkBf16 = 2 };
@@ -328,7 +329,7 @@ struct CkPart {
     return f;
   }
 
-  // All tiles.  big: the second pass, in units of 2^8; the buffers' and barriers' order goes on.
+  // All tiles.  big: the second pass, in units of 8; the buffers' and barriers' order goes on.
   __device__ __forceinline__ void run(CkFetch f, bool big) const {
     uint64_t* const ready = IS_K ? sm.k_ready : sm.v_ready;
     uint64_t* const freed = IS_K ? sm.k_free : sm.pv_done;

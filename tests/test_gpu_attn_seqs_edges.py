@@ -216,3 +216,27 @@ def test_large_scales_that_nobody_sees_beside_many_rows(K, fmt, D, window, sinks
     for s in (b.cache.k_scale, b.cache.v_scale):
         s.transpose(1, 2)[hidden] = 60000.0
     assert torch.equal(b.attn(window, sinks), want)
+
+
+@pytest.mark.parametrize("fmt", SCALED)
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("plane", ["k", "v"])
+def test_small_scales_beside_large_ones(K, fmt, D, plane):
+    """One key with a scale of 60000 among small ones (4-bit rows: of a group of zeros)."""
+    T, rows, key = 600, 150, 100
+    small = 1e-3 if fmt == "tq4" else 5e-3  # scales of 1e-3 and up
+    b = Batch(K, fmt, 1, D, 64, [T], [rows], 3, seed=51, v_scale=small if plane == "v" else 1.0)
+    if plane == "k":
+        pos = torch.arange(T, device=DEV)
+        slots = b.table[0].long()[pos // 64] * 64 + pos % 64
+        k = (small * rnd((T, 1, D), 51, D, "small")).to(torch.bfloat16)
+        K.store(b.cache, k, rnd((T, 1, D), 51, D, "values", dtype=torch.bfloat16), slots.to(torch.int32))
+        b.q = (b.q.float() / small).to(torch.bfloat16)
+    at = int(b.table[0, key // 64]), 0, key % 64
+    code, scale = (b.cache.k, b.cache.k_scale) if plane == "k" else (b.cache.v, b.cache.v_scale)
+    if fmt == "tq4":
+        scale[at] = 60000.0
+    else:
+        scale[(*at, 1)] = 60000.0
+        code[at][16:32] = 0x88
+    b.check(b.attn(), 0, 0)
