@@ -118,10 +118,12 @@ __device__ __forceinline__ uint32_t few_lds16(uint32_t a) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
   return v;
 }
-// The power of two that a key's p takes over from its scales, by the largest one's logarithm: 1
-// where no scale is above 16, so that such a key beside it, or behind a sequence's end, or what
-// is left of another in shared memory, does not change how others are rounded.
-__device__ __forceinline__ float wide_unit(float lsv) { return lsv > 4.f ? exp2f(rintf(lsv)) : 1.f; }
+// The power of two that a key's p takes over from its scales, by the largest one's logarithm: 16
+// where that is above 16, so that p, below 2^(15 - lsv), keeps four bits more and scales of 2^-10
+// and up beside the large one lose none; 1 elsewhere, so that such a key beside it, or behind a
+// sequence's end, or what is left of another in shared memory, does not change how others are
+// rounded.
+__device__ __forceinline__ float wide_unit(float lsv) { return lsv > 4.f ? 16.f : 1.f; }
 __device__ __forceinline__ bool not_finite(uint32_t bf16) { return (bf16 & 0x7F80u) == 0x7F80u; }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ float half_lo(uint32_t w) { return __low2float(u32_as_h2(w)); }

@@ -240,3 +240,46 @@ def test_small_scales_beside_large_ones(K, fmt, D, plane):
         scale[(*at, 1)] = 60000.0
         code[at][16:32] = 0x88
     b.check(b.attn(), 0, 0)
+
+
+class BesideLarge(Batch):
+    """The token that nearly all of the weight falls on (16 powers of two above the others) has
+    one large value scale, of a group of zeros; its other groups are the output.
+
+    In the kernel for few rows a weight times a value scale is fp16 with the row's largest such
+    product (of a token's largest scale) at 2^11 or more, so it is also off by half a step of the
+    subnormals, 2^-25: 2^-36 of that product, here next to `large`, and its code multiplies it."""
+
+    def __init__(self, K, fmt, D, rows, large):
+        T, key = 600, 100
+        super().__init__(K, fmt, 1, D, 64, [T], [rows], 3, seed=57)
+        self.large = large
+        u = torch.sign(rnd((D,), 57, D, "u"))
+        pos = torch.arange(T, device=DEV)
+        slots = self.table[0].long()[pos // 64] * 64 + pos % 64
+        k, v = 0.05 * rnd((T, 1, D), 57, D, "keys"), rnd((T, 1, D), 57, D, "values")
+        k[key, 0] = u
+        K.store(self.cache, k.to(torch.bfloat16), v.to(torch.bfloat16), slots.to(torch.int32))
+        at = int(self.table[0, key // 64]), 0, key % 64
+        self.cache.v_scale[(*at, 1)] = large
+        self.cache.v[at][16:32] = 0x88
+        self.q = (16 * math.log(2.0) / (self.scale * D) * u + 0.1 * rnd((rows, 3, D), 57, D, "q")).to(torch.bfloat16)
+
+    def want(self, window=0, sinks=0):
+        out, var = super().want(window, sinks)
+        if self.n < 100:
+            key = torch.arange(self.lens[0], device=DEV)
+            pg, slot = self.table[0].long()[key // 64], key % 64
+            _, v = self.kv(0, key)
+            code = v[0] / self.cache.v_scale[pg, 0, slot].double().repeat_interleave(32, -1)
+            var = var + self.mix((code ** 2).sum(0)) * (2.0 ** -36 * self.large) ** 2 / 3
+        return out, var
+
+
+@pytest.mark.parametrize("fmt", ["q4_had32", "q4_0"])
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("rows", [1, 3, 150])
+@pytest.mark.parametrize("large", [17.0, 1000.0, 60000.0])
+def test_groups_beside_a_large_scale(K, fmt, D, rows, large):
+    b = BesideLarge(K, fmt, D, rows, large)
+    b.check(b.attn(), 0, 0)
