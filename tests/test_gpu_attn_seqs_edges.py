@@ -283,3 +283,111 @@ class BesideLarge(Batch):
 def test_groups_beside_a_large_scale(K, fmt, D, rows, large):
     b = BesideLarge(K, fmt, D, rows, large)
     b.check(b.attn(), 0, 0)
+
+
+# ------------------------------------------------------------------ shapes, places and scales that nothing above has
+
+def off_by(x, dtype, by=1):
+    """x in a buffer whose rows start `by` elements behind a boundary and end on odd ones."""
+    n, h, d = x.shape
+    flat = torch.full((n * (h + 1) * (d + 3) + by,), 7.0, dtype=dtype, device=DEV)
+    view = flat[by:].view(n, h + 1, d + 3)[:, :h, :d]
+    view.copy_(x)
+    return view
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 5, 130])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_off_their_boundaries(K, fmt, D, rows, dtype):
+    b = Batch(K, fmt, 2, D, 16, [500, 300], [rows, rows], 3, seed=61)
+    want = b.attn(90, 3, dtype=dtype)
+    place = off_by(torch.zeros_like(want, dtype=torch.float32), dtype)
+    q = off_by(b.q, dtype)
+    got = K.attn_seqs(b.cache, q, ints(b.cu), ints(b.lens), b.table, rows, 500, b.scale, window=90, sinks=3, out=place)
+    assert torch.equal(got, want)
+    around = place.as_strided((2 * rows, 7, D + 3), (7 * (D + 3), D + 3, 1))
+    assert bool((around[:, 6] == 7).all()) and bool((around[:, :, D:] == 7).all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_many_sequences(K, fmt):
+    """Hundreds of sequences: the many-row kernel finds its rows over several rounds."""
+    g = torch.Generator().manual_seed(63)
+    lens = torch.randint(0, 200, (700,), generator=g).tolist()
+    rows = [int(r) % (n + 1) for r, n in zip(torch.randint(0, 90, (700,), generator=g), lens)]
+    b = Batch(K, fmt, 1, 64, 32, lens, rows, 2, seed=63, pad=0)
+    b.check(b.attn(30, 2), 30, 2)
+    c = Batch(K, fmt, 1, 64, 32, lens, [1] * 700, 2, seed=64, pad=0)
+    c.check(c.local(0), 0, 0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows", [1, 3, 150])
+@pytest.mark.parametrize("scale", [0.0, -0.1, 1e-30])
+def test_other_scales_of_scores(K, fmt, rows, scale):
+    b = Batch(K, fmt, 2, 128, 16, [700, 90], [rows, rows], 3, seed=65)
+    b.scale = scale
+    b.check(b.attn(), 0, 0)
+    b.check(b.attn(60, 4), 60, 4)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("rows", [1, 5, 150])
+def test_queries_that_are_not_numbers(K, fmt, D, rows):
+    """A query's NaN or infinity reaches its own row and head, and nobody else."""
+    b = Batch(K, fmt, 2, D, 16, [500, 300], [rows, rows], 3, seed=67)
+    want = b.attn(90, 3)
+    b.q = b.q.clone()
+    b.q[rows - 1, 1, 5], b.q[rows, 4, 0] = math.nan, math.inf
+    got = b.attn(90, 3)
+    other = torch.ones(2 * rows, 6, dtype=torch.bool, device=DEV)
+    other[rows - 1, 1] = other[rows, 4] = False
+    assert torch.equal(got[other], want[other])
+    assert bool(got[rows - 1, 1].isnan().all()) and not bool(got[rows, 4].isfinite().all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows", [[1, 1], [3, 0], [150, 7]])
+def test_nothing_stored(K, fmt, rows):
+    """Sequences without a token: every row sits at a negative position."""
+    b = Batch(K, fmt, 2, 128, 16, [0, 0], rows, 3, seed=69)
+    for window, sinks in ((0, 0), (5, 3)):
+        out = torch.full((b.n, 6, 128), 7.0, device=DEV)
+        status = ints([0])
+        got = b.attn(window, sinks, out=out, status=status)
+        assert bool((got == 0).all()) and int(status) == 0
+
+
+# ------------------------------------------------------------------ where the work is split otherwise
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [6, 7, 12, 13])
+def test_columns_beside_the_limits(K, fmt, D, rows):
+    """24, 28, 48 and 52 columns: either side of the numbers at which the kernel for many rows
+    takes over from that for few (tests/test_gpu_attn_seqs.py has 32, 36, 40, 64 and 68)."""
+    for lens in ([2049], [1501, 700, rows]):
+        b = Batch(K, fmt, 2, D, 16, lens, [rows] * len(lens), 4, seed=rows, dtype=torch.float32)
+        b.check(b.attn(), 0, 0)
+        b.check(b.attn(900, 7), 900, 7)
+
+
+def test_rows_of_bad_lengths_are_left(K):
+    """Every row of a sequence that is not computed is left as it was, and the valid
+    sequences' rows keep their bits."""
+    b = Batch(K, "q4_had32", 2, 256, 16, [100, 60, 80], [10, 1, 5], 3, seed=21)
+    want = b.attn()
+    for cu, left, same in (([0, 10, 9, 14], slice(14, 16), slice(0, 9)),  # (the third's rows lie over the first's last)
+                           ([-1, 10, 11, 16], slice(0, 10), slice(10, 16)), ([0, 10, 11, 17], slice(11, 16), slice(0, 11)),
+                           ([0, 11, 12, 16], slice(0, 11), slice(0, 0))):
+        out = torch.full((16, 6, 256), 3.0, device=DEV)
+        status = ints([0])
+        K.attn_seqs(b.cache, b.q, ints(cu), ints(b.lens), b.table, 10, 100, b.scale, out=out, status=status)
+        assert int(status) == K.DEV_BAD_LENGTH
+        assert bool((out[left] == 3).all()) and torch.equal(out[same], want[same])
+        done = torch.ones(16, dtype=torch.bool, device=DEV)
+        done[left] = False
+        assert not bool((out[done] == 3).all(-1).any())
