@@ -94,6 +94,7 @@ SIGNATURES = {
     "kvq_prefill_diff": (_I32, [_CACHE, _P, _I32, _I32, _I32, _I32, _P, _I32, _F, _P, _I64, _NORM, _F, _P, _SZ, _P, _I32,
                                 _P, _P]),
     "kvq_attn_workspace_size": (_SZ, [_CACHE, _I32, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "kvq_attn_workspace_bound": (_SZ, [_CACHE, _I32, _I32, _I32, _I32, _I32, _I32, _I32]),
     "kvq_decode_local": (_I32, [_CACHE, _ROWS, _I32, _P, _P, _I32, _I32, _I32, _I32, _F, _P, _SZ, _ROWS, _P, _P]),
     "kvq_attn_seqs": (_I32, [_CACHE, _ROWS, _I32, _I32, _P, _P, _P, _I32, _I32, _I32, _I32, _I32, _F, _P, _SZ, _ROWS, _P,
                              _P]),
@@ -592,10 +593,17 @@ def attn_workspace_size(cache: Cache, n_rows, num_seqs, num_q_heads, max_rows, m
     return lib().kvq_attn_workspace_size(cache.ref, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window, sinks)
 
 
+def attn_workspace_bound(cache: Cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window=0, sinks=0):
+    return lib().kvq_attn_workspace_bound(cache.ref, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window, sinks)
+
+
 def alloc_attn_workspace(cache: Cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window=0, sinks=0,
-                         device="cuda"):
-    """The workspace of attn_seqs(); with n_rows = num_seqs and max_rows = 1 of decode_local()."""
-    n = attn_workspace_size(cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window, sinks)
+                         device="cuda", smaller=False):
+    """The workspace of attn_seqs(); with n_rows = num_seqs and max_rows = 1 of decode_local().
+    Of a call of this very shape (a smaller batch may need more); smaller: of every call with at
+    most so many rows, sequences, rows of one and tokens."""
+    size = attn_workspace_bound if smaller else attn_workspace_size
+    n = size(cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window, sinks)
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 

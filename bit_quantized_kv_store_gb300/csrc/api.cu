@@ -2,6 +2,7 @@
 // validation, workspace geometry and kernel launches.  Nothing here allocates.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -1069,6 +1070,17 @@ size_t kvq_attn_workspace_size(const kvq_cache* cache, int32_t n_rows, int32_t n
   SeqAttnArgs a{};
   if (check_attn_shape(cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window, sinks, &a) != KVQ_OK) return 0;
   return attn_layout(a).total;
+}
+
+size_t kvq_attn_workspace_bound(const kvq_cache* cache, int32_t n_rows, int32_t num_seqs, int32_t num_q_heads,
+                                int32_t max_rows, int32_t max_seq_len, int32_t window, int32_t sinks) {
+  SeqAttnArgs a{};
+  if (check_attn_shape(cache, n_rows, num_seqs, num_q_heads, max_rows, max_seq_len, window, sinks, &a) != KVQ_OK) return 0;
+  const int n_sm = std::max(1, device_sm_count());
+  int64_t n = few_partials(a.c, num_seqs > 1, n_sm);  // (windows, too: shorter sequences may all fit theirs)
+  if (a.max_rows > 1) n = std::max(n, chunk_partials(n_sm));
+  n = std::min(n, static_cast<int64_t>(64) * n_rows * num_q_heads);  // (no plan has more ranges)
+  return n == 0 ? 0 : 2 * round256(static_cast<size_t>(n) * sizeof(float)) + static_cast<size_t>(n) * a.c.head_dim * sizeof(float);
 }
 
 static int32_t attn_impl(const kvq_cache* cache, const kvq_rows* q, int32_t n_rows, int32_t num_seqs,

@@ -960,6 +960,10 @@ int64_t chunk_blocks(int n_rows, int num_seqs, int max_rows, int group) {
   return std::min<int64_t>((max_rows + per - 1) / per * num_seqs, n_rows / per + num_seqs);
 }
 
+// The partials (of a row and head) that no call passes: ranges x pairs is at most what runs at
+// once, and a pair has up to 256 rows.
+int64_t chunk_partials(int n_sm) { return static_cast<int64_t>(std::max(1, n_sm / 2)) * 256; }
+
 int chunk_ranges(const kvq_cache& c, int n_rows, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
                  int n_sm) {
   const int group = Hq / c.num_kv_heads;

@@ -989,15 +989,27 @@ cudaError_t launch_attn_merge(const SeqAttnArgs& a, int ranges, cudaStream_t s) 
   }
 }
 
+// One wave of CTAs: four of the 4-bit rows' to an SM (registers), of the bf16 rows' as many as
+// their rings leave room for.
+static int few_fit(const kvq_cache& c) {
+  return c.format != KVQ_FMT_BF16 || c.head_dim == 64 ? 4 : c.head_dim == 256 ? 1 : 3;
+}
+
+// The partials (of a row and head) that no plan passes: ranges x blocks of 8 columns is at most
+// what runs at once, in the pieces of ragged sequences 12 times that
+// (a piece has at least 0.339 all blocks / 2 fit n_sm blocks of 16 keys: 5.9 fit n_sm / blocks
+// ranges and one more, and two where there are partials at all).
+int64_t few_partials(const kvq_cache& c, bool ragged, int n_sm) {
+  return static_cast<int64_t>(ragged ? 12 : 1) * 8 * few_fit(c) * n_sm;
+}
+
 FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
                  int n_sm) {
   const int group = Hq / c.num_kv_heads, D = c.head_dim;
   const int64_t blocks = static_cast<int64_t>(num_seqs) * c.num_kv_heads * ((static_cast<int64_t>(max_rows) * group + 7) / 8);
   int64_t keys = max_seq_len;
   if (window > 0) keys = std::min<int64_t>(keys, static_cast<int64_t>(window) + sinks + 64 + 8 / group);
-  // One wave of CTAs: four of the 4-bit rows' to an SM (registers), of the bf16 rows' as many as
-  // their rings leave room for.
-  const int fit = c.format != KVQ_FMT_BF16 || D == 64 ? 4 : D == 256 ? 1 : 3;
+  const int fit = few_fit(c);
   FewPlan p{1, 1, 0};
   if (window == 0 && num_seqs > 1) {
     // Sequences of any lengths: so many blocks of 16 keys a CTA, that sequences of half the
@@ -1020,8 +1032,8 @@ FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max
   // an SM 148 of 4, 74 of 8, 33 of 16; one to an SM 36, 15 and 7), and a second wave costs what
   // the first does.  So of one sequence of 30000 tokens with 4 rows of 24 heads 46 us with three
   // clusters of 16 for each block of columns, 35 with eleven of 4; bf16 rows, one row, 45 and 27.
-  // Clusters of 16 lie unevenly over the SMs and come as one range only (a window of 4096 keys of
-  // one sequence).  TQ4 has 8 pieces that are folded, a CTA for each.
+  // Clusters of 16 lie unevenly over the SMs and come as one range only (a window of 1024 keys of
+  // one sequence; one of 4096 is nine clusters of 4).  TQ4 has 8 pieces that are folded, a CTA for each.
   const bool bf = c.format == KVQ_FMT_BF16;
   const int sub = !bf && D <= 128 ? 2 : 1;  // blocks of a warp's step
   const double unit = D / 256. * (bf ? 1.3 : c.format == KVQ_FMT_TQ4 ? 1.4 : 1.);

@@ -276,6 +276,7 @@ cudaError_t launch_latent(const NormRopeArgs& a, cudaStream_t s);
 // Attention of the rows of several sequences (attn_few.cu).
 FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
                  int n_sm);
+int64_t few_partials(const kvq_cache& c, bool ragged, int n_sm);
 cudaError_t launch_attn_few(const SeqAttnArgs& a, const FewPlan& p, cudaStream_t s);
 // The fold of their partials, and of those of the next.
 cudaError_t launch_attn_merge(const SeqAttnArgs& a, int ranges, cudaStream_t s);
@@ -284,6 +285,7 @@ cudaError_t launch_attn_merge(const SeqAttnArgs& a, int ranges, cudaStream_t s);
 int64_t chunk_blocks(int n_rows, int num_seqs, int max_rows, int group);
 int chunk_ranges(const kvq_cache& c, int n_rows, int num_seqs, int Hq, int max_rows, int max_seq_len, int window, int sinks,
                  int n_sm);
+int64_t chunk_partials(int n_sm);
 cudaError_t launch_attn_chunk(const SeqAttnArgs& a, int ranges, cudaStream_t s);
 // Rows of the cache as the values they stand for (load.cu).
 cudaError_t launch_load(const LoadArgs& a, cudaStream_t s);

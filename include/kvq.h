@@ -624,9 +624,17 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
  *   d_status: optional. */
 
 /* Size in bytes of the workspace of kvq_attn_seqs, and with max_rows = 1 and n_rows =
- * num_seqs of kvq_decode_local, on the current device (0 also for a shape they refuse). */
+ * num_seqs of kvq_decode_local, on the current device (0 also for a shape they refuse).
+ * Of that shape alone: how the keys are cut depends on it, and a smaller batch often needs
+ * more, where the larger one needs nothing.  One for several shapes:
+ * kvq_attn_workspace_bound -- enough for every call with at most n_rows rows, num_seqs sequences,
+ * max_rows rows of one and max_seq_len tokens, and the other arguments alike, whose rows are no
+ * more than its own num_seqs x max_rows (at most 60 MB for 256-wide heads on 152 SMs, and 64
+ * partials of every row and head). */
 size_t kvq_attn_workspace_size(const kvq_cache* cache, int32_t n_rows, int32_t num_seqs, int32_t num_q_heads,
                                int32_t max_rows, int32_t max_seq_len, int32_t window, int32_t sinks);
+size_t kvq_attn_workspace_bound(const kvq_cache* cache, int32_t n_rows, int32_t num_seqs, int32_t num_q_heads,
+                                int32_t max_rows, int32_t max_seq_len, int32_t window, int32_t sinks);
 
 /* kvq_decode_local -- one new row for every sequence: row b of q and out is sequence b's. */
 int32_t kvq_decode_local(const kvq_cache* cache, const kvq_rows* q, int32_t num_seqs, const int32_t* d_seq_lens,

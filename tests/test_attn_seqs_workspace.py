@@ -1,5 +1,7 @@
 """The workspace of the calls over several sequences, for shapes that need one on a GPU of any
 size, as the host sees it without one (no GPU needed)."""
+import random
+
 from tests.test_abi import _desc, K  # noqa: F401
 from tests.test_attn_seqs_refusals import q_rows
 from tests.test_cache_ops_refusals import DUMMY, p
@@ -40,3 +42,28 @@ def test_bad_workspaces_are_refused(K):
         assert call(None, size) == K.ERR_INVALID_ARG
         for off in (1, 4, 16):
             assert call(DUMMY + off, size) == K.ERR_INVALID_ARG
+
+
+def test_bound_covers_smaller_calls(K):
+    """Whatever part of a batch a call has; sizes themselves do not grow with it."""
+    rng = random.Random(3)
+    L = K.lib()
+
+    def log(hi):
+        return min(hi, int(hi ** rng.random()))
+
+    for _ in range(300):
+        c = _desc(K, fmt=rng.choice([0, 1, 3, 4]), D=rng.choice([64, 128, 256]))
+        seqs, rows, length = 1 + log(300), 1 + log(500), log(1 << 20)
+        n = rng.randint(1, seqs * rows)
+        window, sinks = rng.choice([(0, 0), (log(8192), rng.choice([0, 4, 100]))])
+        bound = L.kvq_attn_workspace_bound(p(c), n, seqs, 24, rows, length, window, sinks)
+        for _ in range(30):
+            b, r = 1 + log(seqs - 1) if seqs > 1 else 1, 1 + log(rows - 1) if rows > 1 else 1
+            m = min(n, rng.choice([b * r, rng.randint(1, b * r)]))
+            assert L.kvq_attn_workspace_size(p(c), m, b, 24, r, log(length), window, sinks) <= bound
+            assert L.kvq_attn_workspace_size(p(c), m, b, 24, r, length, window, sinks) <= bound
+            assert L.kvq_attn_workspace_size(p(c), m, b, 24, r, min(length, window), window, sinks) <= bound
+    assert L.kvq_attn_workspace_bound(None, 1, 1, 24, 1, 1024, 0, 0) == 0
+    assert L.kvq_attn_workspace_bound(p(_desc(K, D=512)), 1, 1, 24, 1, 1024, 0, 0) == 0
+    assert L.kvq_attn_workspace_bound(p(_desc(K)), 0, 0, 24, 1, 1024, 0, 0) == 0

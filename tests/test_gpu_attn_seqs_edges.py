@@ -391,3 +391,26 @@ def test_rows_of_bad_lengths_are_left(K):
         done = torch.ones(16, dtype=torch.bool, device=DEV)
         done[left] = False
         assert not bool((out[done] == 3).all(-1).any())
+
+
+# ------------------------------------------------------------------ one workspace for several shapes
+
+@pytest.mark.parametrize("window", [0, 4096])
+def test_one_workspace_for_every_batch(K, window):
+    lens = [20000, 9000, 300, 7000, 15000, 4000, 12000, 18000] * 4
+    b = Batch(K, "q4_had32", 4, 256, 16, lens, [1] * 32, 6, seed=71, pad=0)
+    ws = K.alloc_attn_workspace(b.cache, 32, 32, 24, 1, 20000, window, smaller=True)
+    lens = ints(lens)
+    needs = []
+    for n in range(1, 33):
+        args = (b.cache, b.q[:n], lens[:n], b.table[:n], 20000, b.scale, window)
+        needs.append(K.attn_workspace_size(b.cache, n, n, 24, 1, 20000, window))
+        assert needs[-1] <= ws.numel()
+        assert torch.equal(K.decode_local(*args, workspace=ws), K.decode_local(*args))
+    assert needs != sorted(needs)  # a size is its own shape's
+    for rows in (2, 9, 100):  # and few or many rows of fewer sequences
+        big = K.alloc_attn_workspace(b.cache, 800, 32, 24, 100, 20000, window, smaller=True)
+        for n in (1, 2, 3, 8):
+            q = b.q[:1].expand(n * rows, 24, 256)
+            args = (b.cache, q, ints(range(0, n * rows + 1, rows)), lens[:n], b.table[:n], rows, 20000, b.scale, window)
+            assert torch.equal(K.attn_seqs(*args, workspace=big), K.attn_seqs(*args))
