@@ -984,7 +984,11 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
 // Up to so many columns (row x query head of one KV head) a sequence: the few rows' kernel, which
 // converts the cache's rows again for every 8; above, a pair of CTAs takes up to 256.  Sequences
 // of any lengths fill the GPU with pieces either way; one sequence, or windows, leave the few
-// rows' clusters uneven.  Measured on both sides, few rows' kernel / many rows', us:
+// rows' clusters uneven.  Batches with windows take one sequence's limits: of the columns below
+// the slower kernel then runs for 64 of 4-bit and of bf16 rows 128 wide, 48 of TQ4, and 30 of
+// bf16 rows 256 wide.  64-wide heads take the 128-wide ones' limits, untimed, and one kernel
+// runs for a whole batch, by its longest chunk.  Measured on both sides, few rows' kernel / many
+// rows', us:
 //   16 sequences up to 30000    one sequence of 30000      16 windows of 1000
 //   4-bit, 256 wide   48 columns 295 / 381, 60 342 / 382   24 41 / 37, 36 48 / 38   30 27 / 27, 36 37 / 27
 //    (up to 8000)     48 columns 106 / 111, 60 120 / 112

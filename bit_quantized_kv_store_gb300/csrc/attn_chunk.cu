@@ -21,7 +21,7 @@
 // values lie with their dims contiguous (B with its columns contiguous), so neither is
 // transposed.  Scores alternate between two buffers of tensor memory; p (fp16) goes over
 // the scores it was made from and is the context product's A.
-// Queries, keys and values are fp16 here (each within 2^-12; bf16 rows: bf16, as they
+// Queries, keys and values are fp16 here (each within 2^-11; bf16 rows: bf16, as they
 // are), a row's queries scaled by a power of two (to at most 2^15).  p is fp16: 2^(7 + s - m), at
 // most 2^15, as the reference m follows when a row's scores pass it by more than 8 (by more than
 // 6, for two bits more of p: 4096 rows at 16384 1498 -> 1677 us).  So a weight down to 2^-21 of
@@ -32,8 +32,8 @@
 // with keys and values in units of 8 (a scale below 2^-11 is then rounded to 2^-22); nobody else
 // pays for that, nor do slots that no row sees set it off.
 //
-// Measured (one GB300, 24 / 4 heads of 256, 4-bit rows): 4096 rows at 16384 1473 us (1260
-// TFLOP/s), 2048 rows with a window of 4096 215 us.  The products alone, with everybody else
+// Measured (one GB300, 24 / 4 heads of 256, 4-bit rows): 4096 rows at 16384 1483 us (1251
+// TFLOP/s), 2048 rows with a window of 4096 222 us.  The products alone, with everybody else
 // only arriving, take 486 us of the 684 of 2048 rows at 16384; the softmax and the decoders add
 // to them through shared memory and issue slots.  Every role's loop is rolled: four roles
 // share a sub-partition's instruction fetch (unrolled 920 us).

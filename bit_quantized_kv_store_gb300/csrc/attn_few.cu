@@ -19,7 +19,7 @@
 // bits 2 to 5 of a half is the subnormal c 2^-22, in bits 6 to 9 16 c 2^-22, and the query
 // of such a dim carries the 1/16; the 8 that codes are biased by is in the accumulator's
 // start (-8 sum q over the group).  So a group of scores is exact up to the query (fp16,
-// 2^-12), and its scale multiplies the fp32 sum.  (The tensor cores
+// 2^-11), and its scale multiplies the fp32 sum.  (The tensor cores
 // line products of subnormals up as if their exponent were 2^-14 and cut a sum 23 bits
 // below: 2^-15 of a code times the largest query element, a 2^-15 part of a score.  For
 // values, whose small sums count, that is too much: they are converted, exactly, to c - 8.)
@@ -30,11 +30,12 @@
 // TQ4 rows: levels by byte lookups (tq4_levels.cuh), the row's scale on scores and p.
 // bf16 rows: as they are; q and p in two bf16 halves (16 bits).
 //
-// Measured (one GB300, a graph of calls): one token, window 1024 7.6 us; 32 sequences, windows
-// of 4096 keys 47 us (149 MB, 3.2 TB/s: about 560 instructions a block of 16 keys, 72 % of the
-// issue slots while the keys last, and 15 us of start and fold); 16 bf16 sequences, windows of
-// 1024 15.9 us (67 MB, 4.2 TB/s).  Loops are rolled because a call is short: unrolled, fetching
-// the code took most of it (11.7 us for the first).
+// Measured (one GB300, a graph of calls over inputs larger than L2): one token, window 1024 8.9
+// us; 32 sequences, windows of 4096 keys 48.6 us (149 MB, 3.06 TB/s: about 560 instructions a
+// block of 16 keys, 72 % of the issue slots while the keys last, and 15 us of start and fold); 16
+// bf16 sequences, windows of 1024 19.7 us (67 MB, 3.4 TB/s).  About 1.3 us of each is metadata
+// that is read behind the kernel in front, not beside it.  Loops are rolled because a call is
+// short: unrolled, fetching the code took most of it (the first 11.7 us, so 7.6 then).
 #include <algorithm>
 #include <climits>
 
@@ -1030,7 +1031,8 @@ FewPlan few_plan(const kvq_cache& c, int num_seqs, int Hq, int max_rows, int max
   // another down on an SM, more CTAs' beginnings, and a second launch for the fold of ranges.
   // All have to run at once: the clusters of a size that fit were counted (152 SMs, four CTAs to
   // an SM 148 of 4, 74 of 8, 33 of 16; one to an SM 36, 15 and 7), and a second wave costs what
-  // the first does.  So of one sequence of 30000 tokens with 4 rows of 24 heads 46 us with three
+  // the first does.  (The figures here are from before metadata was read behind the wait for the
+  // kernel in front, 1.3 us a call.)  So of one sequence of 30000 tokens with 4 rows of 24 heads 46 us with three
   // clusters of 16 for each block of columns, 35 with eleven of 4; bf16 rows, one row, 45 and 27.
   // Clusters of 16 lie unevenly over the SMs and come as one range only (a window of 1024 keys of
   // one sequence; one of 4096 is nine clusters of 4).  TQ4 has 8 pieces that are folded, a CTA for each.

@@ -646,7 +646,9 @@ int32_t kvq_decode_local(const kvq_cache* cache, const kvq_rows* q, int32_t num_
  * of q and out (device int32 [num_seqs + 1], ascending).
  *   n_rows: the rows of q and out; those outside [d_cu_rows[0], d_cu_rows[num_seqs]) are
  *   left as they were, as are those of a sequence of more than max_rows rows or whose rows
- *   are not inside [0, n_rows) (KVQ_DEV_BAD_LENGTH). */
+ *   are not inside [0, n_rows) (KVQ_DEV_BAD_LENGTH).
+ * One kernel runs for all sequences, by max_rows: single tokens beside long chunks are faster in
+ * a kvq_decode_local call of their own (window 0: everything is seen). */
 int32_t kvq_attn_seqs(const kvq_cache* cache, const kvq_rows* q, int32_t n_rows, int32_t num_seqs,
                       const int32_t* d_cu_rows, const int32_t* d_seq_lens, const int32_t* d_block_tables,
                       int32_t max_pages_per_seq, int32_t max_rows, int32_t max_seq_len, int32_t window,
