@@ -628,7 +628,8 @@ def attn_seqs(cache: Cache, q, cu_rows, seq_lens, block_tables, max_rows, max_se
     """Causal attention of new rows of several sequences: rows cu_rows[b] .. cu_rows[b + 1]
     - 1 of q [rows, Hq, D] are the last tokens of sequence b, which has seq_lens[b] stored
     ones (theirs among them).  window and sinks as in decode_local(); max_rows: the most
-    rows that a sequence has.  Returns out [rows, Hq, D]."""
+    rows that a sequence has.  Returns out [rows, Hq, D].  Over a bf16 cache many rows (64 of
+    max_rows x query heads of a KV head, or fewer) take queries and weights in 8 bits."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return attn_seqs(cache, q, cu_rows, seq_lens, block_tables, max_rows, max_seq_len, sm_scale, window, sinks,

@@ -612,7 +612,9 @@ int32_t kvq_diff_heads(const float* x, int64_t rows, int32_t num_q_heads, int32_
  * statistics fp32.  A weight below 2^-21 of its row's largest is off by up to 2^-32 of that
  * (few rows of a sequence, 4-bit formats: a weight times its value scale, by up to 2^-36 of the
  * row's largest weight times the largest scale of its token, if that is above 1).
- * (BF16, few rows of a sequence: queries and weights in two bf16 halves.)
+ * (BF16, few rows of a sequence: queries and weights in two bf16 halves; more rows: in one, 8
+ * bits, fp32 queries and outputs or not.)  Few rows: up to 24 to 64 of max_rows times the query
+ * heads of a KV head, by format, width and whether there are windows or one sequence.
  * Any format but FP8_ROW, head_dim 64, 128 or 256, num_q_heads / num_kv_heads up to 64.
  *   q, out: [rows][num_q_heads][head_dim], q unrotated, out rotated back and rounded once
  *       into its type; out must not overlap q, nor its rows each other.

@@ -17,13 +17,11 @@ def write(dst, src):
     torch.add(src, 0, out=dst)
 
 
-@pytest.mark.parametrize("fmt", ["FMT_Q4_HAD32", "FMT_Q4_0", "FMT_TQ4", "FMT_BF16"])
+@pytest.mark.parametrize("fmt,call", [(f, c) for f in ("FMT_Q4_HAD32", "FMT_Q4_0") for c in ("attn", "step", "merged", "window")]
+                         + [("FMT_TQ4", "attn"), ("FMT_BF16", "attn")])
 @pytest.mark.parametrize("lens", [[3000], [5000, 333], [9001] * 7 + [16]])  # grids of less and of more than one wave
-@pytest.mark.parametrize("call", ["attn", "step", "merged", "window"])
 @pytest.mark.parametrize("last", ["lens", "table"])
-def test_metadata_written_right_before(K, fmt, lens, call, last):
-    if (fmt == "FMT_BF16" and call != "attn") or (fmt == "FMT_TQ4" and call != "attn"):
-        pytest.skip("4-bit groups only")
+def test_metadata_written_right_before(K, fmt, call, lens, last):
     B, top = len(lens), max(lens)
     pages = -(-top // PS)
     signs = torch.arange(D // 32, dtype=torch.int32, device=DEV) * 77777
